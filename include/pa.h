@@ -200,6 +200,137 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
                   const pa_chunk *chunks, int32_t n_chunks, float softmax_scale, void *out, void *workspace,
                   size_t workspace_bytes, int32_t *status_dev, void *stream);
 
+/* Attention weight per cached key: what eviction by accumulated attention
+ * looks at.  For row r with sequence s and position p, kv head h and the G
+ * query heads that read it,
+ *     mass[s][h][t] += sum over those heads of softmax_t(scale * q[r][g] . K_s[t]),  t = 0..p
+ * so one row adds G to the sum of its (sequence, kv head).  K is read once, V
+ * not at all; append the step's rows first.
+ *   mass      f32 [num_seqs][Hkv][max_blocks_per_seq * page_size] in device memory,
+ *             16-byte aligned; the caller zeroes a sequence's rows when it admits it.
+ *             Entries past a row's position are not touched.
+ *   chunks    as for pa_attention: the rows of one prompt (its last rows as an
+ *             observation window, or all of them) are listed as a chunk.  A
+ *             chunk of at least 16 rows with bf16 queries over a bf16 pool runs on
+ *             the tensor-core tile path.
+ *   workspace device memory of at least pa_attention_mass_workspace_bytes(...) bytes,
+ *             256-byte aligned (may be NULL when 0 are needed); scratch that each call
+ *             writes before it reads it.  Calls that share one must not overlap on the GPU.
+ *   the other arguments: as pa_attention
+ * Precondition: a sequence has one row outside the chunks, or the rows of one
+ * chunk, in a call (a step's rows satisfy it): its sums then have one writer
+ * and the same bits in any batch.
+ * Sums and weights are FP32.  Errors as for pa_attention; a row with an
+ * invalid sequence, position or page, or a chunk with such a row or whose rows
+ * are not consecutive positions of one sequence, adds nothing and records
+ * PA_ERR_OUT_OF_RANGE.  Graph-capturable. */
+size_t pa_attention_mass_workspace_bytes(const pa_pool *pool, int32_t n_rows, int32_t num_q_heads,
+                                         int32_t max_blocks_per_seq, const pa_chunk *chunks, int32_t n_chunks);
+pa_status pa_attention_mass(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q_dtype,
+                            int32_t num_q_heads, const int32_t *seq_ids, const int32_t *positions,
+                            const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
+                            const pa_chunk *chunks, int32_t n_chunks, float softmax_scale, float *mass,
+                            void *workspace, size_t workspace_bytes, int32_t *status_dev, void *stream);
+
+/* Which tokens of a cache stay.  For each listed sequence i (slot seq_ids[i],
+ * lengths[i] tokens cached) and kv head h, keep[i][h][0..count) receives the
+ * tokens to keep in ascending order, count = min(lengths[i], budget), and -1
+ * behind them: the first keep_first and the last keep_last tokens, and of the
+ * others those with the most mass, ties to the lowest token.  NaN counts as
+ * less than any number.  A sequence no longer than the budget keeps
+ * everything.  Each kv head keeps its own tokens (a page holds each head's
+ * slots apart).
+ *   seq_ids, lengths  int32 [n] in device memory
+ *   mass              f32 [num_seqs][num_kv_heads][max_tokens], as pa_attention_mass
+ *                     fills it with max_tokens = max_blocks_per_seq * page_size
+ *   keep              int32 [n][num_kv_heads][budget], written whole
+ *   kept_lengths      int32 [n], receives count (may be NULL; may not be `lengths`)
+ * keep_first + keep_last <= budget.  One launch, no workspace; graph-capturable.
+ * A row whose sequence is outside [0, num_seqs) or whose length is outside
+ * [0, max_tokens] keeps nothing (all -1, count 0) and records
+ * PA_ERR_OUT_OF_RANGE. */
+pa_status pa_evict_select(int32_t n, const int32_t *seq_ids, const int32_t *lengths, const float *mass,
+                          int32_t num_seqs, int32_t num_kv_heads, int32_t max_tokens, int32_t budget,
+                          int32_t keep_first, int32_t keep_last, int32_t *keep, int32_t *kept_lengths,
+                          int32_t *status_dev, void *stream);
+
+/* Close the gaps: token keep[i][h][j] of slot seq_ids[i] becomes token j, for
+ * K, V and (mass not NULL) the weights, j < count = min(lengths[i], budget).
+ *   keep          int32 [n][Hkv][budget] in device memory, from pa_evict_select or a
+ *                 policy of the caller's: strictly ascending tokens below lengths[i]
+ *   dst_seq_ids   int32 [n]: slot dst_seq_ids[i] receives the tokens, through its own
+ *                 row of the same block tables (a cache whose pages other sequences
+ *                 share is compacted into a slot of its own).  NULL: in place.
+ *   mass          f32 [num_seqs][Hkv][max_blocks_per_seq * page_size]; the destination's
+ *                 entries count .. lengths[i] - 1 become zero.  NULL: left alone.
+ * The caller's next token goes to position count; pages behind it can be given
+ * back (pa_pages_trim).  Slots behind count keep their bytes.
+ * Precondition: no slot is listed twice, as a source of one row and a
+ * destination of another either, and a page that receives tokens belongs to
+ * that one sequence (in place: pages shared with another sequence would change
+ * under it).  One launch, no workspace; graph-capturable.
+ * Device-side, with PA_ERR_OUT_OF_RANGE: a row with an invalid slot or length
+ * moves nothing; a kept token out of order or range, or one whose page id is
+ * invalid, is not moved and its destination is unspecified. */
+pa_status pa_evict_compact(const pa_pool *pool, int32_t n, const int32_t *seq_ids, const int32_t *dst_seq_ids,
+                           const int32_t *lengths, const int32_t *keep, int32_t budget, const int32_t *block_tables,
+                           int32_t num_seqs, int32_t max_blocks_per_seq, float *mass, int32_t *status_dev,
+                           void *stream);
+
+/* Beam search's choice.  For each group of `beams` hypotheses, the n_out best
+ * continuations over beams x vocabulary by
+ *     score[b][v] = scores[b] + logits[b][v] - log(sum_u exp(logits[b][u]))
+ * best first; equal scores go to the lower beam, then the lower token.  A
+ * finished beam has one continuation: itself, with its score unchanged and
+ * token end_token.
+ *   logits      f32 or bf16 [n_groups * beams] rows of `vocab`, row_stride elements
+ *               apart (>= vocab), aligned to their element
+ *   scores      f32 [n_groups * beams], the hypotheses' log-probabilities so far
+ *   finished    int32 [n_groups * beams], non-zero: finished (may be NULL: none)
+ *   parents, tokens   int32 [n_groups][n_out]: the beam (0..beams-1) a continuation
+ *               extends, and its token;  out_scores  f32 [n_groups][n_out]
+ * beams <= 32, n_out <= 64.  A logit of -infinity is no continuation; a beam
+ * whose log-sum-exp is not finite (NaN or +infinity among its logits, or
+ * nothing but -infinity) or whose score is not finite has none.  Where fewer
+ * than n_out exist the rest is parent -1, token -1, score -infinity.
+ * Sums of exponentials are FP32 per thread and FP64 across threads; scores are
+ * compared in FP64 and rounded once.
+ *   workspace   device memory of at least pa_beam_workspace_bytes(...), 256-byte
+ *               aligned, ZERO-FILLED BEFORE ITS FIRST USE; every call leaves its
+ *               counters at zero again.  Calls that share one must not overlap on
+ *               the GPU.
+ * Graph-capturable. */
+size_t pa_beam_workspace_bytes(int32_t n_groups, int32_t beams, int32_t vocab, int32_t n_out);
+pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const void *logits, pa_dtype logits_dtype,
+                         int64_t row_stride, const float *scores, const int32_t *finished, int32_t end_token,
+                         int32_t n_out, int32_t *parents, int32_t *tokens, float *out_scores, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* Give every beam its parent's cache.  Beam b of group i sits in slot
+ * seq_ids[i][b] and becomes a copy of beam parents[i][b] (-1: of itself), all
+ * beams at once.  The beams of a group hold lengths[i] tokens each:
+ *   - whole pages (columns 0 .. lengths[i] / page_size - 1 of the block tables)
+ *     are shared: the beam's table row takes the parent's page ids;
+ *   - the unfinished page (column lengths[i] / page_size, when lengths[i] is not a
+ *     multiple of page_size) stays each beam's own, and its slots in use are copied
+ *     from the parent's;
+ *   - later columns stay: they are the beam's own pages for the tokens to come.
+ * A parent of 0 for every beam fans a prompt out, its unfinished page included.
+ * Pages of beams that died stay referenced by the survivors' tables: the slots
+ * of a group are released together.
+ *   state      per-slot rows of the caller's (e.g. the attention weights), permuted the
+ *              same way: state_row_bytes (a multiple of 4) for each of num_seqs slots,
+ *              4-byte aligned.  NULL: none.
+ * Precondition: a slot is listed once in a call, and an unfinished page belongs
+ * to one beam.  beams <= 32, n_groups <= 65535.  One launch, no workspace;
+ * graph-capturable.  A group with an invalid slot, parent, length or unfinished
+ * page, a slot listed twice or an unfinished page shared by two of its beams is
+ * left as it was and records PA_ERR_OUT_OF_RANGE. */
+pa_status pa_beam_reorder(const pa_pool *pool, int32_t n_groups, int32_t beams, const int32_t *seq_ids,
+                          const int32_t *parents, const int32_t *lengths, int32_t *block_tables, int32_t num_seqs,
+                          int32_t max_blocks_per_seq, void *state, size_t state_row_bytes, int32_t *status_dev,
+                          void *stream);
+
 /* pa_attention without a workspace argument, for callers that cannot allocate
  * device memory: code handed only its input and output buffers by a host
  * runtime that owns and budgets all device memory (a plugin interface), or a
@@ -364,6 +495,13 @@ pa_status pa_pages_admit(pa_pages *pages, int32_t seq, int32_t prompt_tokens, in
  * list when no sequence holds it) and reset its block_tables row to -1
  * (block_tables may be NULL).  PA_ERR_INVALID_ARG if the slot holds nothing. */
 pa_status pa_pages_release(pa_pages *pages, int32_t seq, int32_t *block_tables);
+
+/* Give back the pages of slot seq behind its first `tokens` tokens (after an
+ * eviction): the slot keeps ceil(tokens / page_size) pages, the rest lose its
+ * hold, and their block_tables entries become -1 (block_tables may be NULL).
+ * A slot that holds no more pages than that is left as it is.
+ * PA_ERR_INVALID_ARG if the slot holds nothing or tokens < 0. */
+pa_status pa_pages_trim(pa_pages *pages, int32_t seq, int32_t tokens, int32_t *block_tables);
 
 int32_t pa_pages_free_count(const pa_pages *pages);            /* -1 if pages is NULL */
 int32_t pa_pages_refcount(const pa_pages *pages, int32_t page); /* sequences holding page; -1 if out of range */

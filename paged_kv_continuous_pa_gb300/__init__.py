@@ -1,6 +1,6 @@
 """Python binding of libpa_gb300 (include/pa.h): argument marshalling only.
 
-Every step of append and attention runs in the library's CUDA kernels; this
+Every step of append, attention, eviction and beam search runs in the library's CUDA kernels; this
 module passes tensor pointers, sizes and the current CUDA stream through
 ctypes.  PyTorch supplies device memory and streams.  There is no fallback:
 if the shared library is missing or a CUDA device is absent the calls raise.
@@ -86,6 +86,24 @@ def load(path: str = LIB_PATH):
         L.pa_step.argtypes = [vp, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp, i32, i32, ctypes.POINTER(Chunk), i32,
                               f32, vp, vp, sz, vp, vp]
         L.pa_step.restype = st
+        i64 = ctypes.c_int64
+        L.pa_attention_mass_workspace_bytes.argtypes = [vp, i32, i32, i32, ctypes.POINTER(Chunk), i32]
+        L.pa_attention_mass_workspace_bytes.restype = sz
+        L.pa_attention_mass.argtypes = [vp, i32, vp, i32, i32, vp, vp, vp, i32, i32, ctypes.POINTER(Chunk), i32, f32,
+                                        vp, vp, sz, vp, vp]
+        L.pa_attention_mass.restype = st
+        L.pa_evict_select.argtypes = [i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        L.pa_evict_select.restype = st
+        L.pa_evict_compact.argtypes = [vp, i32, vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, vp]
+        L.pa_evict_compact.restype = st
+        L.pa_beam_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.pa_beam_workspace_bytes.restype = sz
+        L.pa_beam_select.argtypes = [i32, i32, i32, vp, i32, i64, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.pa_beam_select.restype = st
+        L.pa_beam_reorder.argtypes = [vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, sz, vp, vp]
+        L.pa_beam_reorder.restype = st
+        L.pa_pages_trim.argtypes = [vp, i32, i32, vp]
+        L.pa_pages_trim.restype = st
         L.pa_pages_needed.argtypes = [i32, i32, i32]
         L.pa_pages_needed.restype = i32
         L.pa_pages_create.argtypes = [i32, i32, i32, i32, ctypes.POINTER(vp)]
@@ -280,6 +298,11 @@ class Pages:
     def release(self, seq: int):
         _check(load().pa_pages_release(self.handle, int(seq), self.block_tables.ctypes.data_as(ctypes.c_void_p)))
 
+    def trim(self, seq: int, tokens: int):
+        """Give back the slot's pages behind its first `tokens` tokens."""
+        _check(load().pa_pages_trim(self.handle, int(seq), int(tokens),
+                                    self.block_tables.ctypes.data_as(ctypes.c_void_p)))
+
     def free_count(self) -> int:
         return int(load().pa_pages_free_count(self.handle))
 
@@ -360,6 +383,180 @@ def attention_noalloc(pool: Pool, q, seq_ids, positions, block_tables, out,
                                        _ptr(positions), _ptr(block_tables), num_seqs, max_blocks,
                                        arr if chunks else None, len(chunks), float(softmax_scale), _ptr(out),
                                        _ptr(status), _stream(stream)))
+
+
+def _check_f32(t, name: str, shape):
+    """A float32 tensor of this shape."""
+    import torch
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {list(shape)}")
+
+
+def _check_int_shape(t, name: str, shape):
+    """An int32 tensor of this shape."""
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {list(shape)}")
+
+
+class _launch_on:
+    """The device of a call's tensors made current (they must share one), with
+    the stream the call runs on: the caller's, or that device's current one."""
+
+    def __init__(self, stream, *tensors):
+        import torch
+        devices = {t.device for t in tensors if t is not None}
+        if any(d.type != "cuda" for d in devices):
+            raise ValueError("tensor must live on a CUDA device")
+        if len(devices) != 1:
+            raise ValueError(f"tensors live on different devices: {sorted(map(str, devices))}")
+        self.guard = torch.cuda.device(devices.pop())
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _chunk_array(chunks):
+    return (Chunk * max(1, len(chunks)))(*[Chunk(int(b), int(c)) for b, c in chunks])
+
+
+def mass_workspace_bytes(pool: Pool, n_rows: int, num_q_heads: int, max_blocks: int,
+                         chunks: Sequence[Tuple[int, int]] = ()) -> int:
+    """Workspace bytes attention_mass() needs for these rows and chunks."""
+    return int(load().pa_attention_mass_workspace_bytes(pool.handle, int(n_rows), int(num_q_heads), int(max_blocks),
+                                                        _chunk_array(chunks) if chunks else None, len(chunks)))
+
+
+def attention_mass(pool: Pool, q, seq_ids, positions, block_tables, mass, chunks: Sequence[Tuple[int, int]] = (),
+                   softmax_scale: float = 0.0, workspace=None, status=None, stream=None):
+    """Add every row's attention weights (q [n, Hq, D] f32|bf16) to mass, f32
+    [num_seqs, Hkv, max_blocks * P], summed over the query heads of a kv head."""
+    n = _check_rows(pool, q, seq_ids, positions, block_tables, q, status)
+    num_seqs, max_blocks = (int(x) for x in block_tables.shape)
+    _check_f32(mass, "mass", (num_seqs, pool.num_kv_heads, max_blocks * pool.page_size))
+    ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    with _launch_on(stream, pool.k_pool, q, seq_ids, positions, block_tables, mass, workspace, status) as s:
+        _check(load().pa_attention_mass(pool.handle, n, _ptr(q), _dtype_code(q), int(q.shape[1]), _ptr(seq_ids),
+                                        _ptr(positions), _ptr(block_tables), num_seqs, max_blocks,
+                                        _chunk_array(chunks) if chunks else None, len(chunks), float(softmax_scale),
+                                        _ptr(mass), _ptr(workspace), ws_len, _ptr(status), s))
+
+
+def evict_select(mass, seq_ids, lengths, keep, kept_lengths=None, keep_first: int = 0, keep_last: int = 0, status=None,
+                 stream=None):
+    """The tokens each (sequence, kv head) keeps, ascending, into keep int32
+    [n, Hkv, budget] (-1 behind them): the first and last ones asked for, and
+    those with the most mass (f32 [num_seqs, Hkv, max_tokens])."""
+    _check_index(seq_ids, "seq_ids")
+    n = int(seq_ids.shape[0])
+    _check_index(lengths, "lengths", n)
+    if mass.dim() != 3 or keep.dim() != 3:
+        raise ValueError("mass must be [num_seqs, Hkv, max_tokens] and keep [n, Hkv, budget]")
+    _check_f32(mass, "mass", mass.shape)
+    num_seqs, heads, max_tokens = (int(x) for x in mass.shape)
+    budget = int(keep.shape[2])
+    _check_int_shape(keep, "keep", (n, heads, budget))
+    if kept_lengths is not None:
+        _check_index(kept_lengths, "kept_lengths", n)
+        if n and kept_lengths.data_ptr() == lengths.data_ptr():
+            raise ValueError("kept_lengths may not be lengths")
+    if status is not None:
+        _check_index(status, "status")
+    with _launch_on(stream, mass, seq_ids, lengths, keep, kept_lengths, status) as s:
+        _check(load().pa_evict_select(n, _ptr(seq_ids), _ptr(lengths), _ptr(mass), num_seqs, heads, max_tokens, budget,
+                                      int(keep_first), int(keep_last), _ptr(keep), _ptr(kept_lengths), _ptr(status),
+                                      s))
+
+
+def evict_compact(pool: Pool, keep, seq_ids, lengths, block_tables, mass=None, dst_seq_ids=None, status=None,
+                  stream=None):
+    """Move the kept tokens (keep int32 [n, Hkv, budget], ascending) to the front
+    of their sequence, or of the slots dst_seq_ids: K, V and, if given, mass."""
+    _check_index(seq_ids, "seq_ids")
+    n = int(seq_ids.shape[0])
+    _check_index(lengths, "lengths", n)
+    _check_index(block_tables, "block_tables", dims=2)
+    if dst_seq_ids is not None:
+        _check_index(dst_seq_ids, "dst_seq_ids", n)
+    if status is not None:
+        _check_index(status, "status")
+    if keep.dim() != 3:
+        raise ValueError(f"keep has shape {tuple(keep.shape)}; expected [{n}, {pool.num_kv_heads}, budget]")
+    budget = int(keep.shape[2])
+    _check_int_shape(keep, "keep", (n, pool.num_kv_heads, budget))
+    num_seqs, max_blocks = (int(x) for x in block_tables.shape)
+    if mass is not None:
+        _check_f32(mass, "mass", (num_seqs, pool.num_kv_heads, max_blocks * pool.page_size))
+    with _launch_on(stream, pool.k_pool, keep, seq_ids, lengths, block_tables, mass, dst_seq_ids, status) as s:
+        _check(load().pa_evict_compact(pool.handle, n, _ptr(seq_ids), _ptr(dst_seq_ids), _ptr(lengths), _ptr(keep),
+                                       budget, _ptr(block_tables), num_seqs, max_blocks, _ptr(mass), _ptr(status), s))
+
+
+def beam_workspace_bytes(n_groups: int, beams: int, vocab: int, n_out: int) -> int:
+    """Workspace bytes beam_select() needs."""
+    return int(load().pa_beam_workspace_bytes(int(n_groups), int(beams), int(vocab), int(n_out)))
+
+
+def beam_select(logits, scores, parents, tokens, out_scores, finished=None, end_token: int = 0, workspace=None,
+                stream=None):
+    """The best continuations of each group over beams x vocabulary: logits
+    [groups, beams, vocab] f32|bf16 (rows may be padded), scores f32 and finished
+    int32 [groups, beams] into parents, tokens int32 and out_scores f32 [groups, n_out]."""
+    if logits.dim() != 3:
+        raise ValueError(f"logits have shape {tuple(logits.shape)}; expected [groups, beams, vocab]")
+    groups, beams, vocab = (int(x) for x in logits.shape)
+    if parents.dim() != 2:
+        raise ValueError(f"parents has shape {tuple(parents.shape)}; expected [{groups}, n_out]")
+    n_out = int(parents.shape[1])
+    _check_f32(scores, "scores", (groups, beams))
+    _check_int_shape(parents, "parents", (groups, n_out))
+    _check_int_shape(tokens, "tokens", (groups, n_out))
+    _check_f32(out_scores, "out_scores", (groups, n_out))
+    if finished is not None:
+        _check_int_shape(finished, "finished", (groups, beams))
+    # rows: contiguous, and evenly spaced over groups and beams (a stride of a size-1 axis says nothing)
+    row = int(logits.stride(1)) if beams > 1 else int(logits.stride(0)) if groups > 1 else vocab
+    if (vocab > 1 and logits.stride(2) != 1) or (groups > 1 and logits.stride(0) != beams * row):
+        raise ValueError("logits must have contiguous rows, evenly spaced over groups and beams")
+    with _launch_on(stream, logits, scores, parents, tokens, out_scores, finished, workspace) as s:
+        ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check(load().pa_beam_select(groups, beams, vocab, logits.data_ptr(), _dtype_code(logits), row, _ptr(scores),
+                                     _ptr(finished), int(end_token), n_out, _ptr(parents), _ptr(tokens),
+                                     _ptr(out_scores), _ptr(workspace), ws_len, s))
+
+
+def beam_reorder(pool: Pool, parents, seq_ids, lengths, block_tables, state=None, status=None, stream=None):
+    """Give the beam in slot seq_ids[i, b] the cache of beam parents[i, b] of its
+    group (int32 [groups, beams]; -1: its own): block tables and unfinished pages,
+    and the rows of state [num_seqs, ...] (any 4-byte aligned rows), in place."""
+    if parents.dim() != 2:
+        raise ValueError(f"parents has shape {tuple(parents.shape)}; expected [groups, beams]")
+    groups, beams = (int(x) for x in parents.shape)
+    _check_int_shape(parents, "parents", (groups, beams))
+    _check_int_shape(seq_ids, "seq_ids", (groups, beams))
+    _check_index(lengths, "lengths", groups)
+    _check_index(block_tables, "block_tables", dims=2)
+    if status is not None:
+        _check_index(status, "status")
+    num_seqs, max_blocks = (int(x) for x in block_tables.shape)
+    row_bytes = 0
+    if state is not None:
+        if state.dim() < 1 or int(state.shape[0]) != num_seqs:
+            raise ValueError(f"state has shape {tuple(state.shape)}; expected {num_seqs} rows")
+        row_bytes = state.numel() // num_seqs * state.element_size()
+    with _launch_on(stream, pool.k_pool, parents, seq_ids, lengths, block_tables, state, status) as s:
+        _check(load().pa_beam_reorder(pool.handle, groups, beams, _ptr(seq_ids), _ptr(parents), _ptr(lengths),
+                                      _ptr(block_tables), num_seqs, max_blocks, _ptr(state), row_bytes, _ptr(status),
+                                      s))
 
 
 def set_split_tokens(tokens: int):

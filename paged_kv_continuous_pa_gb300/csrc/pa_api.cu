@@ -13,21 +13,7 @@
 #include <mutex>
 
 #include "../../include/pa.h"
-#include "pa_kernels.h"
-
-struct pa_pool {
-  pa_pool_desc desc;
-  bool head_scales;  // fp8 scales per kv head (pa_pool_set_head_scales)
-  float k_scale_h[pa::kMaxHeadScales], v_scale_h[pa::kMaxHeadScales];
-  void* k;
-  void* v;
-  bool tile_maps_ready;  // kmap / vmap encoded (on first use by the prefill tile path)
-  bool dec_maps_ready;   // kmap_dec / vmap_dec encoded (on first use by tensor-core decode units)
-  CUtensorMap kmap;      // 2-D views of the pools for tensor-map copies
-  CUtensorMap vmap;
-  CUtensorMap kmap_dec;
-  CUtensorMap vmap_dec;
-};
+#include "pa_host.h"
 
 namespace {
 std::atomic<unsigned long long> g_launches{0};
@@ -45,7 +31,9 @@ std::atomic<int32_t> g_unit_order{PA_ORDER_AUTO};
 std::atomic<uint32_t> g_wait_limit{pa::kDefaultWaitLimit};
 std::atomic<int32_t> g_debug_stall{0};
 
-pa_status fail(pa_status st, const char* fmt, ...) {
+}  // namespace
+
+pa_status pa::fail(pa_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
@@ -53,13 +41,16 @@ pa_status fail(pa_status st, const char* fmt, ...) {
   return st;
 }
 
-pa_status cuda_fail(cudaError_t e, const char* what) {
+pa_status pa::cuda_fail(cudaError_t e, const char* what) {
   return fail(PA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-size_t elt_bytes(pa_dtype t) { return t == PA_F32 ? 4 : t == PA_BF16 ? 2 : 1; }
+namespace {
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using pa::aligned;
+using pa::cuda_fail;
+using pa::elt_bytes;
+using pa::fail;
 
 int max_splits_for(const pa_pool_desc& d, int32_t max_blocks, int32_t split_tokens) {
   const long long cap = static_cast<long long>(max_blocks) * d.page_size;
@@ -234,6 +225,34 @@ pa_status check_desc(const pa_pool_desc* d) {
 
 }  // namespace
 
+// The checks of a call's rows that pa_attention, pa_step and pa_attention_mass share.
+pa_status pa::check_rows(const pa_pool_desc& d, int32_t n_rows, pa_dtype q_dtype, int32_t num_q_heads, int32_t num_seqs,
+                         int32_t max_blocks_per_seq, const pa_chunk* chunks, int32_t n_chunks) {
+  if (n_rows < 0) return fail(PA_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
+  if (q_dtype != PA_F32 && q_dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "q dtype must be f32 or bf16");
+  if (num_q_heads <= 0 || num_q_heads % d.num_kv_heads != 0)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of num_kv_heads %d", num_q_heads,
+                d.num_kv_heads);
+  const int G = num_q_heads / d.num_kv_heads;
+  if (G > 8) return fail(PA_ERR_UNSUPPORTED, "query heads per kv head %d > 8", G);
+  if (num_seqs <= 0 || max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG, "num_seqs and max_blocks_per_seq must be positive");
+  if (n_chunks < 0 || n_chunks > pa::kMaxChunks)
+    return fail(PA_ERR_INVALID_ARG, "n_chunks %d outside [0, %d]", n_chunks, pa::kMaxChunks);
+  if (n_chunks > 0 && chunks == nullptr) return fail(PA_ERR_INVALID_ARG, "chunks is NULL");
+  for (int c = 0; c < n_chunks; ++c) {
+    if (chunks[c].n_rows <= 0 || chunks[c].row_begin < 0 ||
+        static_cast<long long>(chunks[c].row_begin) + chunks[c].n_rows > n_rows)
+      return fail(PA_ERR_INVALID_ARG, "chunk %d rows [%d, +%d) outside [0, %d)", c, chunks[c].row_begin,
+                  chunks[c].n_rows, n_rows);
+    for (int c2 = 0; c2 < c; ++c2)
+      if (chunks[c].row_begin < chunks[c2].row_begin + chunks[c2].n_rows &&
+          chunks[c2].row_begin < chunks[c].row_begin + chunks[c].n_rows)
+        return fail(PA_ERR_INVALID_ARG, "chunks %d and %d overlap", c2, c);
+  }
+  return PA_OK;
+}
+
 void pa::set_last_error(const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -303,28 +322,9 @@ pa_status attention_impl(const pa_pool* pool, int32_t n_rows, const void* q, pa_
                          const pa::FixedScratch* scratch = nullptr) {
   if (pool == nullptr) return fail(PA_ERR_INVALID_ARG, "pool is NULL");
   const pa_pool_desc& d = pool->desc;
-  if (n_rows < 0) return fail(PA_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
-  if (q_dtype != PA_F32 && q_dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "q dtype must be f32 or bf16");
-  if (num_q_heads <= 0 || num_q_heads % d.num_kv_heads != 0)
-    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of num_kv_heads %d", num_q_heads,
-                d.num_kv_heads);
+  const pa_status row_st = pa::check_rows(d, n_rows, q_dtype, num_q_heads, num_seqs, max_blocks_per_seq, chunks, n_chunks);
+  if (row_st != PA_OK) return row_st;
   const int G = num_q_heads / d.num_kv_heads;
-  if (G > 8) return fail(PA_ERR_UNSUPPORTED, "query heads per kv head %d > 8", G);
-  if (num_seqs <= 0 || max_blocks_per_seq <= 0)
-    return fail(PA_ERR_INVALID_ARG, "num_seqs and max_blocks_per_seq must be positive");
-  if (n_chunks < 0 || n_chunks > pa::kMaxChunks)
-    return fail(PA_ERR_INVALID_ARG, "n_chunks %d outside [0, %d]", n_chunks, pa::kMaxChunks);
-  if (n_chunks > 0 && chunks == nullptr) return fail(PA_ERR_INVALID_ARG, "chunks is NULL");
-  for (int c = 0; c < n_chunks; ++c) {
-    if (chunks[c].n_rows <= 0 || chunks[c].row_begin < 0 ||
-        static_cast<long long>(chunks[c].row_begin) + chunks[c].n_rows > n_rows)
-      return fail(PA_ERR_INVALID_ARG, "chunk %d rows [%d, +%d) outside [0, %d)", c, chunks[c].row_begin,
-                  chunks[c].n_rows, n_rows);
-    for (int c2 = 0; c2 < c; ++c2)
-      if (chunks[c].row_begin < chunks[c2].row_begin + chunks[c2].n_rows &&
-          chunks[c2].row_begin < chunks[c].row_begin + chunks[c].n_rows)
-        return fail(PA_ERR_INVALID_ARG, "chunks %d and %d overlap", c2, c);
-  }
   if (n_rows == 0) {
     if (pre == nullptr) return PA_OK;
     const cudaError_t e = pa::launch_append(*pre, static_cast<cudaStream_t>(stream));

@@ -185,4 +185,28 @@ pa_status pa_pages_release(pa_pages* a, int32_t seq, int32_t* block_tables) {
   return PA_OK;
 }
 
+pa_status pa_pages_trim(pa_pages* a, int32_t seq, int32_t tokens, int32_t* block_tables) {
+  if (a == nullptr) {
+    pa::set_last_error("pa_pages_trim: allocator is NULL");
+    return PA_ERR_INVALID_ARG;
+  }
+  if (seq < 0 || seq >= a->num_seqs || !a->in_use[seq]) {
+    pa::set_last_error("pa_pages_trim: sequence %d holds no pages", seq);
+    return PA_ERR_INVALID_ARG;
+  }
+  if (tokens < 0) {
+    pa::set_last_error("pa_pages_trim: negative token count %d", tokens);
+    return PA_ERR_INVALID_ARG;
+  }
+  std::vector<int32_t>& mine = a->seq_pages[seq];
+  const size_t stay = static_cast<size_t>(ceil_div(tokens, a->page_size));
+  while (mine.size() > stay) {  // last page first, as a release hands them back
+    const int32_t pg = mine.back();
+    mine.pop_back();
+    if (--a->refs[pg] == 0) a->free_stack.push_back(pg);
+    if (block_tables != nullptr) block_tables[static_cast<size_t>(seq) * a->max_blocks + mine.size()] = -1;
+  }
+  return PA_OK;
+}
+
 }  // extern "C"

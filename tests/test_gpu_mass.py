@@ -1,0 +1,260 @@
+"""pa_attention_mass against a 64-bit reference: types, head groups, page and
+sequence lengths, chunks (observation windows and whole prompts), strangers'
+memory, refused rows, streams and graphs."""
+import pytest
+import torch
+
+import cache_ref as R
+import paged_kv_continuous_pa_gb300 as pa
+
+pytestmark = pytest.mark.gpu
+
+
+def run(c, q, seq_ids, positions, mass, chunks=(), **kw):
+    ids = torch.tensor(seq_ids, dtype=torch.int32, device="cuda")
+    pos = torch.tensor(positions, dtype=torch.int32, device="cuda")
+    size = pa.mass_workspace_bytes(c.pool, len(seq_ids), q.shape[1], c.max_blocks, chunks)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xA5) if size else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.attention_mass(c.pool, q, ids, pos, kw.pop("tables", c.tables), mass, chunks=chunks, workspace=ws, status=status,
+                      **kw)
+    torch.cuda.synchronize()
+    return int(status.item())
+
+
+def check(c, q, seq_ids, positions, chunks=(), seed=0, **kw):
+    g = torch.Generator().manual_seed(100 + seed)
+    before = (torch.rand(c.num_seqs, c.Hkv, c.max_tokens, generator=g) * 3).cuda()
+    mass = before.clone()
+    assert run(c, q, seq_ids, positions, mass, chunks, **kw) == 0
+    added, big = R.mass_of_rows(c, q, seq_ids, positions, kw.get("softmax_scale"))
+    rows = max([1] + [n for _, n in chunks])
+    bound = R.mass_bound(c, added, before.double(), big, rows, q.shape[1] // c.Hkv)
+    err = (mass.double() - before.double() - added).abs()
+    assert torch.isfinite(mass).all()
+    assert (err <= bound).all(), f"worst {float((err / bound).max()):.3g} of the bound"
+    touched = torch.zeros_like(mass, dtype=torch.bool)
+    for s, p in zip(seq_ids, positions):
+        touched[s, :, :p + 1] = True
+    assert torch.equal(mass[~touched], before[~touched])
+    return mass
+
+
+def queries(n, hq, d, dtype, seed=0, scale=1.0):
+    g = torch.Generator().manual_seed(7 + seed)
+    return (torch.randn(n, hq, d, generator=g) * scale).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("q_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_types(kv, q_dtype, D):
+    c = R.make_cache([1, 15, 16, 17, 300, 1029], Hkv=2, D=D, P=16, kv=kv, seed=1)
+    q = queries(6, 6, D, q_dtype)
+    check(c, q, c.slots, [n - 1 for n in c.lengths])
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("kv,q_dtype", [("bf16", torch.bfloat16), ("e4m3", torch.float32)])
+def test_groups(G, kv, q_dtype):
+    c = R.make_cache([33, 700], Hkv=3, D=128, P=32, kv=kv, seed=G)
+    q = queries(2, 3 * G, 128, q_dtype, seed=G)
+    check(c, q, c.slots, [n - 1 for n in c.lengths])
+
+
+@pytest.mark.parametrize("P", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("window", [1, 40])
+def test_page_sizes(P, window):
+    c = R.make_cache([P - 1 + window, P + window, 5 * P + 3 + window], Hkv=2, D=64, P=P, seed=P)
+    n = len(c.lengths)
+    q = queries(n * window, 4, 64, torch.bfloat16, seed=P)
+    seq = [s for s in c.slots for _ in range(window)]
+    pos = [x - window + i for x in c.lengths for i in range(window)]
+    check(c, q, seq, pos, [(i * window, window) for i in range(n)] if window > 1 else ())
+
+
+@pytest.mark.parametrize("length", [4095, 4097, 9001, 33000])
+@pytest.mark.parametrize("G", [2, 8])
+def test_long_rows(length, G):
+    c = R.make_cache([length, 5], Hkv=1, D=128, P=64, seed=length)
+    q = queries(2, G, 128, torch.bfloat16, seed=length)
+    check(c, q, c.slots, [length - 1, 4])
+
+
+def test_very_long_row():
+    """More keys than one cluster keeps scores for."""
+    c = R.make_cache([150001], Hkv=1, D=64, P=256, seed=3)
+    q = queries(1, 8, 64, torch.bfloat16)
+    check(c, q, c.slots, [150000])
+
+
+def test_rows_that_look_back():
+    """A row may sit before the end of its cache: later keys stay untouched."""
+    c = R.make_cache([200, 300], Hkv=2, D=64, P=32, seed=5)
+    q = queries(2, 4, 64, torch.bfloat16)
+    check(c, q, c.slots, [0, 31])
+
+
+@pytest.mark.parametrize("softmax_scale", [0.02, 1.0])
+def test_scales(softmax_scale):
+    c = R.make_cache([257], Hkv=2, D=64, P=16, seed=6)
+    check(c, queries(1, 4, 64, torch.bfloat16), c.slots, [256], softmax_scale=softmax_scale)
+
+
+@pytest.mark.parametrize("rows", [2, 15, 16, 17, 40, 129, 300])
+@pytest.mark.parametrize("G", [1, 3, 4, 8])
+def test_chunks(rows, G):
+    """Windows at the end of a prompt, whole prompts (start 0), and decode rows beside them."""
+    c = R.make_cache([rows, rows + 77, 50, 4000], Hkv=2, D=128, P=32, seed=rows + G)
+    seq = [c.slots[0]] * rows + [c.slots[2]] + [c.slots[1]] * rows + [c.slots[3]]
+    pos = list(range(rows)) + [49] + [77 + i for i in range(rows)] + [3999]
+    q = queries(len(seq), 2 * G, 128, torch.bfloat16, seed=rows)
+    check(c, q, seq, pos, [(0, rows), (rows + 1, rows)])
+
+
+@pytest.mark.parametrize("D,P,length", [(64, 16, 5000), (128, 256, 4600), (128, 16, 9000)])
+def test_long_windows(D, P, length):
+    rows = 64
+    c = R.make_cache([length], Hkv=2, D=D, P=P, seed=length)
+    q = queries(rows, 8, D, torch.bfloat16)
+    check(c, q, c.slots * rows, [length - rows + i for i in range(rows)], [(0, rows)])
+
+
+@pytest.mark.parametrize("kv,q_dtype", [("e4m3", torch.bfloat16), ("f32", torch.bfloat16), ("bf16", torch.float32)])
+def test_chunks_of_other_types(kv, q_dtype):
+    rows = 21
+    c = R.make_cache([90, 30], Hkv=2, D=64, P=16, kv=kv, seed=8)
+    seq = [c.slots[0]] * rows + [c.slots[1]]
+    pos = [90 - rows + i for i in range(rows)] + [29]
+    check(c, queries(rows + 1, 6, 64, q_dtype), seq, pos, [(0, rows)])
+
+
+def test_large_scores():
+    """Scores far apart: one key takes all the weight, the others vanish."""
+    c = R.make_cache([500], Hkv=1, D=64, P=16, seed=9)
+    q = queries(1, 2, 64, torch.bfloat16, scale=30.0)
+    check(c, q, c.slots, [499])
+
+
+def test_bits_do_not_depend_on_the_batch():
+    c = R.make_cache([900, 64, 2000, 333, 2001, 17], Hkv=2, D=128, P=32, seed=10)
+    q = queries(6, 8, 128, torch.bfloat16)
+    pos = [n - 1 for n in c.lengths]
+    whole = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    assert run(c, q, c.slots, pos, whole) == 0
+    for i in range(6):
+        one = torch.zeros_like(whole)
+        assert run(c, q[i:i + 1].contiguous(), c.slots[i:i + 1], pos[i:i + 1], one) == 0
+        assert torch.equal(one[c.slots[i]], whole[c.slots[i]])
+    again = torch.zeros_like(whole)
+    assert run(c, q, c.slots, pos, again) == 0
+    assert torch.equal(again, whole)
+
+
+def test_chunk_bits_do_not_depend_on_the_batch():
+    rows = 40
+    c = R.make_cache([900, 700], Hkv=2, D=128, P=32, seed=11)
+    q = queries(2 * rows, 4, 128, torch.bfloat16)
+    seq = [c.slots[0]] * rows + [c.slots[1]] * rows
+    pos = [900 - rows + i for i in range(rows)] + [700 - rows + i for i in range(rows)]
+    whole = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    assert run(c, q, seq, pos, whole, [(0, rows), (rows, rows)]) == 0
+    one = torch.zeros_like(whole)
+    assert run(c, q[rows:].contiguous(), seq[rows:], pos[rows:], one, [(0, rows)]) == 0
+    assert torch.equal(one[c.slots[1]], whole[c.slots[1]])
+
+
+@pytest.mark.parametrize("what", ["sequence", "negative", "position", "page"])
+@pytest.mark.parametrize("rows", [1, 20])
+def test_bad_rows_add_nothing(what, rows):
+    """A bad row (or a tile-path chunk with one) is reported; the others are as without it."""
+    c = R.make_cache([100, 120], Hkv=2, D=64, P=16, seed=12)
+    seq = [c.slots[0]] * rows + [c.slots[1]]
+    pos = [100 - rows + i for i in range(rows)] + [119]
+    q = queries(rows + 1, 4, 64, torch.bfloat16)
+    chunks = [(0, rows)] if rows > 1 else ()
+    tables = c.tables
+    good = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    assert run(c, q[rows:].contiguous(), seq[rows:], pos[rows:], good) == 0
+    if what == "sequence":
+        seq = [c.num_seqs] * rows + seq[rows:]
+    elif what == "negative":
+        seq = [-1] * rows + seq[rows:]
+    elif what == "position":
+        pos = [c.max_tokens - rows + 1 + i for i in range(rows)] + pos[rows:]
+    else:
+        tables = tables.clone()
+        tables[c.slots[0], 2] = c.k.shape[0]
+    mass = torch.zeros_like(good)
+    assert run(c, q, seq, pos, mass, chunks, tables=tables) == pa.PA_ERR_OUT_OF_RANGE
+    assert torch.equal(mass, good)
+
+
+def test_poison_beside_the_queries():
+    """Rows behind a chunk and other chunks' rows never leak in (NaN queries beside it)."""
+    rows = 50
+    c = R.make_cache([400, 300], Hkv=2, D=128, P=32, seed=13)
+    q = queries(rows + 1, 6, 128, torch.bfloat16)
+    q[rows:] = float("nan")
+    seq, pos = [c.slots[0]] * rows + [c.slots[1]], [400 - rows + i for i in range(rows)] + [299]
+    mass = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    assert run(c, q, seq, pos, mass, [(0, rows)]) == 0
+    clean = torch.zeros_like(mass)
+    assert run(c, q[:rows].contiguous(), seq[:rows], pos[:rows], clean, [(0, rows)]) == 0
+    assert torch.isfinite(mass[c.slots[0]]).all()
+    assert torch.equal(mass[c.slots[0]], clean[c.slots[0]])
+
+
+def test_no_rows():
+    c = R.make_cache([10], Hkv=2, D=64, P=16)
+    mass = torch.ones(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    pa.attention_mass(c.pool, torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"),
+                      torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda"),
+                      c.tables, mass)
+    assert torch.equal(mass, torch.ones_like(mass))
+
+
+def test_stream_and_graph():
+    """On a stream of its own, captured and replayed: each replay adds the same weights."""
+    rows = 32
+    c = R.make_cache([600, 500], Hkv=2, D=128, P=32, seed=14)
+    seq, pos = [c.slots[0]] * rows + [c.slots[1]], [600 - rows + i for i in range(rows)] + [499]
+    q = queries(rows + 1, 4, 128, torch.bfloat16)
+    ids = torch.tensor(seq, dtype=torch.int32, device="cuda")
+    positions = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    chunks = [(0, rows)]
+    size = pa.mass_workspace_bytes(c.pool, rows + 1, 4, c.max_blocks, chunks)
+    ws = torch.zeros(max(size, 1), dtype=torch.uint8, device="cuda")
+    mass = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    want = torch.zeros_like(mass)
+    assert run(c, q, seq, pos, want, chunks) == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        pa.attention_mass(c.pool, q, ids, positions, c.tables, mass, chunks=chunks, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(mass, want)
+    graph.replay()
+    torch.cuda.synchronize()
+    # the buffer is rounded at most once for each row that adds to it: on the second replay a
+    # half step (2^-24) of a sum no larger than the final one, and as much on the first
+    assert ((mass - 2 * want).abs() <= 2 * rows * 2.0 ** -24 * 2 * want).all()
+
+
+def test_matches_the_attention_step():
+    """With V the unit vectors of each key, the attention's output is the weights."""
+    c = R.make_cache([60], Hkv=1, D=64, P=64, kv="f32", seed=15, spare_blocks=0)
+    page = int(c.tables[c.slots[0], 0])
+    c.v.zero_()
+    c.v[page, 0] = torch.eye(64, device="cuda")
+    q = queries(1, 4, 64, torch.float32)
+    ids = torch.tensor(c.slots, dtype=torch.int32, device="cuda")
+    pos = torch.tensor([59], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    pa.attention(c.pool, q, ids, pos, c.tables, out)
+    mass = torch.zeros(c.num_seqs, 1, 64, device="cuda")
+    pa.attention_mass(c.pool, q, ids, pos, c.tables, mass)
+    # two FP32 evaluations of the same weights, each within (64 + 8) roundings of scores below 8
+    assert torch.allclose(mass[c.slots[0], 0, :60], out[0].sum(dim=0)[:60], rtol=2 * 72 * 2.0 ** -23 * 8 * 2, atol=1e-7)
