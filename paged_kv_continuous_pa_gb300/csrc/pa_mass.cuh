@@ -1,0 +1,652 @@
+// pa_mass.cuh -- the kernels of pa_attention_mass: the attention weight that
+// every cached key receives from a step's queries, accumulated per sequence and
+// kv head.  For row r (sequence s, position p), kv head h and its G query heads,
+//     mass[s][h][t] += sum_g exp(scale q[r][g] . K_s[t] - lse[r][g]),  t = 0..p
+// with lse the log-sum-exp of the row's own scores.  Scores live in the log2
+// domain; a row's weights need its maximum and sum over all keys first.
+//
+// Rows outside the chunks (`mass_row_kernel`): one cluster of CTAs per (row, kv
+// head).  K is read from memory once, straight into tensor-core fragments; the
+// scores wait in shared memory while the cluster's CTAs exchange their (max,
+// sum) pairs, then become weights.
+// Chunks (`chunk_stats_kernel`, then `chunk_weights_kernel`): the (row, head)
+// pairs of a kv head are columns that share the keys.  The first launch finds
+// every column's (max, sum) over ranges of keys, the second recomputes the
+// scores key block by key block, merges the ranges of each column and sums the
+// weights over the columns: each key has one owner, which adds once.
+// No atomic decides an order: the same rows give the same bits in any batch.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "pa_decode_mma.cuh"
+
+namespace pa {
+
+constexpr int kMassThreads = 256;
+constexpr int kMassWarps = kMassThreads / 32;
+constexpr int kMassSplitKeys = 4096;  // keys per range of the chunks' first launch
+constexpr int kMassBlockKeys = 128;   // keys per CTA of their second launch
+constexpr int kMassClusterKeys = 2048;             // keys per CTA that a row's cluster aims at
+constexpr int kMassMaxCluster = 8;
+constexpr size_t kMassScoreBytes = 104 * 1024;     // shared memory for a CTA's scores (two CTAs to an SM)
+
+struct MassParams {
+  const void* k_pool;
+  const void* q;
+  const int32_t* seq_ids;
+  const int32_t* positions;
+  const int32_t* block_tables;
+  float* mass;  // [num_seqs][Hkv][max_blocks * P]
+  int32_t* status;
+  int32_t n_rows, num_seqs, max_blocks, num_pages, P, Hq, Hkv, D;
+  int32_t q_is_bf16, kv_type, head_scales;
+  float qk_scale_log2_h[kMaxHeadScales];  // softmax scale * log2(e) * k scale
+  int32_t cluster;      // CTAs per (row, kv head) of the rows' launch
+  int32_t score_keys;   // keys per CTA whose scores fit in shared memory (a multiple of 16)
+  int32_t n_chunks;
+  int32_t chunk_begin[kMaxChunks];
+  int32_t chunk_end[kMaxChunks];
+  int32_t chunk_cta[kMaxChunks + 1];   // first launch: prefix sums of CTAs per chunk
+  int32_t n_splits;                    // key ranges of the longest row
+  int32_t n_blocks;                    // second launch: key blocks of the longest row
+  int64_t chunk_stats[kMaxChunks];     // offset of a chunk's (max, sum) pairs, in pairs
+  float2* ws_stats;                    // per chunk [Hkv][n_splits][rows * G]
+};
+
+// ------------------------------------------------------------- fragments --
+//
+// A warp scores 16 keys x 8 columns with mma.m16n8k16: A = K, lane (g4, t4)
+// holding pieces of key rows g4 and g4 + 8, B = the queries.  The order of the
+// D products of a dot product is free, so a lane takes whole 16-byte pieces of
+// its rows (piece t4 + 4 i) and feeds them to the MMAs as they are; the query
+// fragments follow the same order.
+//   bf16 K  as it is; an f32 query enters as three bf16 parts (24 bits), a bf16 one as one
+//   e4m3 K  exactly as f16; the query as f16 after a power-of-two scaling per column that puts
+//           its largest element in [2^14, 2^15): one part for bf16, two (22 bits) for f32
+//   f32 K   as three bf16 parts, with the query's parts; products below 2^-24 are left out
+
+template <int KVT, int D, bool QB>
+struct MassGeom {
+  static constexpr int ELT = KvElt<KVT>::bytes;
+  static constexpr int RB = D * ELT;        // bytes of a K row
+  static constexpr int EP = 16 / ELT;       // elements of a piece
+  static constexpr int NPT = RB / 64;       // pieces a lane holds of a row
+  static constexpr int STEPS = D / 16;      // MMA k-steps
+  static constexpr int KP = KVT == KV_F32 ? 3 : 1;
+  static constexpr int QP = QB ? 1 : (KVT == KV_E4M3 ? 2 : 3);
+};
+
+__device__ __forceinline__ void mass_mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two floats as bf16 pairs: the leading part, and what it leaves (in place).
+__device__ __forceinline__ uint32_t take_bf16(float& x, float& y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  x = __fsub_rn(x, __low2float(h));
+  y = __fsub_rn(y, __high2float(h));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t take_f16(float& x, float& y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  x = __fsub_rn(x, __low2float(h));
+  y = __fsub_rn(y, __high2float(h));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A column's query as B fragments, and the factor that turns its dot products
+// into log2-domain scores.  `row` < 0: an empty column (zeros).
+template <int KVT, int D, bool QB>
+struct QueryFrag {
+  using Geo = MassGeom<KVT, D, QB>;
+  uint32_t b[Geo::QP][Geo::STEPS][2];
+
+  // The column of lane group g4 (head `head` of row `row`); returns its factor.
+  __device__ __forceinline__ float load(const MassParams& p, int row, int head, float scale, int t4) {
+    float x[Geo::STEPS][4];
+    const size_t base = row < 0 ? 0 : (static_cast<size_t>(row) * p.Hq + head) * D;
+#pragma unroll
+    for (int i = 0; i < Geo::NPT; ++i)
+#pragma unroll
+      for (int j = 0; j < Geo::EP / 4; ++j) {
+        float(&e)[4] = x[i * (Geo::EP / 4) + j];
+        const size_t at = base + (t4 + 4 * i) * Geo::EP + 4 * j;
+        if (row < 0) {
+          e[0] = e[1] = e[2] = e[3] = 0.0f;
+        } else if constexpr (QB) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at));
+          e[0] = bf16lo(w.x), e[1] = bf16hi(w.x), e[2] = bf16lo(w.y), e[3] = bf16hi(w.y);
+        } else {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at));
+          e[0] = w.x, e[1] = w.y, e[2] = w.z, e[3] = w.w;
+        }
+      }
+    if constexpr (KVT == KV_E4M3) {
+      float top = 0.0f;
+#pragma unroll
+      for (int s = 0; s < Geo::STEPS; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(x[s][k]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the power of two that puts `top` in [2^14, 2^15); none for a column of zeros or one that is not finite
+      const int e = (top > 0.0f && top < INFINITY) ? 14 - ilogbf(top) : 0;
+#pragma unroll
+      for (int s = 0; s < Geo::STEPS; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[s][k] = scalbnf(x[s][k], e);
+      scale = scalbnf(scale, -e);
+    }
+#pragma unroll
+    for (int part = 0; part < Geo::QP; ++part)
+#pragma unroll
+      for (int s = 0; s < Geo::STEPS; ++s)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          b[part][s][k] = KVT == KV_E4M3 ? take_f16(x[s][2 * k], x[s][2 * k + 1]) : take_bf16(x[s][2 * k], x[s][2 * k + 1]);
+    return scale;
+  }
+};
+
+// A lane's pieces of the two key rows it holds of a 16-key tile.
+template <int KVT, int D, bool QB>
+struct KeyFrag {
+  using Geo = MassGeom<KVT, D, QB>;
+  uint4 lo[Geo::NPT], hi[Geo::NPT];  // rows g4 and g4 + 8
+
+  // rows: the tile's first key row (16 consecutive slots of one page)
+  __device__ __forceinline__ void load(const unsigned char* rows, int g4, int t4) {
+    const unsigned char* r = rows + static_cast<size_t>(g4) * Geo::RB + t4 * 16;
+#pragma unroll
+    for (int i = 0; i < Geo::NPT; ++i) {
+      lo[i] = ldg_stream(r + 64 * i);
+      hi[i] = ldg_stream(r + 8 * Geo::RB + 64 * i);
+    }
+  }
+  __device__ __forceinline__ static uint4 ldg_stream(const unsigned char* a) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(a));
+    return v;
+  }
+
+  // c[n] += K . Q of NT column groups
+  template <int NT>
+  __device__ __forceinline__ void score(const QueryFrag<KVT, D, QB> (&q)[NT], float (&c)[NT][4]) const {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Geo::NPT; ++i) {
+      const uint32_t lw[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w}, hw[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+      if constexpr (KVT == KV_BF16) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t a[4] = {lw[2 * j], hw[2 * j], lw[2 * j + 1], hw[2 * j + 1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int part = 0; part < Geo::QP; ++part)
+              mass_mma_bf16(c[n], a, q[n].b[part][2 * i + j][0], q[n].b[part][2 * i + j][1]);
+        }
+      } else if constexpr (KVT == KV_E4M3) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a[4] = {e4m3x2_to_f16x2(lw[j], true), e4m3x2_to_f16x2(hw[j], true),
+                                 e4m3x2_to_f16x2(lw[j], false), e4m3x2_to_f16x2(hw[j], false)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int part = 0; part < Geo::QP; ++part)
+              mma_f16_16816(c[n], a, q[n].b[part][4 * i + j][0], q[n].b[part][4 * i + j][1]);
+        }
+      } else {
+        float l[4], h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l[k] = __uint_as_float(lw[k]), h[k] = __uint_as_float(hw[k]);
+#pragma unroll
+        for (int kp = 0; kp < Geo::KP; ++kp) {
+          const uint32_t a[4] = {take_bf16(l[0], l[1]), take_bf16(h[0], h[1]), take_bf16(l[2], l[3]),
+                                 take_bf16(h[2], h[3])};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int part = 0; part < Geo::QP; ++part)
+              if (kp + part < 3) mass_mma_bf16(c[n], a, q[n].b[part][i][0], q[n].b[part][i][1]);
+        }
+      }
+    }
+  }
+};
+
+// A lane's running (maximum, sum) of one column, over the keys that it sees.
+struct ColumnStat {
+  float m, l;
+  __device__ __forceinline__ void add2(float s0, float s1) {
+    const float top = fmaxf(m, fmaxf(s0, s1));
+    if (top > m) {
+      l = __fmul_rn(l, ex2(__fsub_rn(m, top)));
+      m = top;
+    }
+    if (m > -INFINITY) l = __fadd_rn(l, __fadd_rn(ex2(__fsub_rn(s0, m)), ex2(__fsub_rn(s1, m))));
+    if (s0 != s0 || s1 != s1) l = NAN;
+  }
+  __device__ __forceinline__ void merge(float om, float ol) {
+    const float top = fmaxf(m, om);
+    const float a = m == top ? 1.0f : ex2(__fsub_rn(m, top)), b = om == top ? 1.0f : ex2(__fsub_rn(om, top));
+    l = __fadd_rn(__fmul_rn(l, a), __fmul_rn(ol, b));
+    m = top;
+  }
+};
+
+// The tensor-map-free address of token t's K row of kv head h (t % 16 == 0), or
+// of page 0 where the page id is out of range (`bad` is set then).
+template <int RB>
+__device__ __forceinline__ const unsigned char* key_rows(const MassParams& p, int page, int h, int t, int lg_p, bool& bad) {
+  if (page < 0 || page >= p.num_pages) {
+    bad = true;
+    page = 0;
+  }
+  return static_cast<const unsigned char*>(p.k_pool) +
+         (((static_cast<size_t>(page) * p.Hkv + h) << lg_p) + (t & ((1 << lg_p) - 1))) * RB;
+}
+
+__device__ __forceinline__ bool mass_row_in_chunk(const MassParams& p, int row) {
+  for (int c = 0; c < p.n_chunks; ++c)
+    if (row >= p.chunk_begin[c] && row < p.chunk_end[c]) return true;
+  return false;
+}
+
+// ------------------------------------------------------------------ rows --
+
+// Stride between the heads' score rows: 4 banks apart, so that the four lanes
+// that hold a key's columns write to different banks.
+__host__ __device__ constexpr int score_stride(int keys) { return (keys + 31) / 32 * 32 + 4; }
+
+// One cluster per (row, kv head).  The row's 16-key tiles are dealt to the CTAs
+// in contiguous shares of its own length, and within a CTA to the warps in
+// turn; the loads of a warp's next tile are in flight while it scores one.
+template <int KVT, int D, bool QB>
+__global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ? 1 : 2) mass_row_kernel(const __grid_constant__ MassParams p) {
+  using Geo = MassGeom<KVT, D, QB>;
+  extern __shared__ float scores[];  // [G][score_stride(score_keys)]
+  __shared__ float2 warp_stat[kMassWarps][8];
+  __shared__ float2 cta_stat[8];
+  __shared__ int cta_bad;
+  __shared__ float2 row_stat[8];  // (maximum, 1 / sum) of the whole row
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = blockIdx.x % p.cluster, unit = blockIdx.x / p.cluster;
+  const int h = unit % p.Hkv, row = unit / p.Hkv;
+  if (mass_row_in_chunk(p, row)) return;  // the whole cluster leaves
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
+  const int G = p.Hq / p.Hkv, lg_p = 31 - __clz(p.P);
+  const int seq = __ldg(p.seq_ids + row), pos = __ldg(p.positions + row);
+  if (seq < 0 || seq >= p.num_seqs || pos < 0 || pos >= p.max_blocks * p.P) {
+    if (rank == 0 && tid == 0) record_error(p.status, ST_OUT_OF_RANGE);
+    return;
+  }
+  const int tiles = (pos + 16) / 16, share = (tiles + p.cluster - 1) / p.cluster;
+  const int tile0 = min(tiles, rank * share), mine = min(tiles, tile0 + share) - tile0;  // this CTA's tiles
+  const int stride = score_stride(p.score_keys);
+  const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
+  if (tid == 0) cta_bad = 0;
+
+  QueryFrag<KVT, D, QB> q[1];
+  const float factor = q[0].load(p, g4 < G ? row : -1, h * G + g4, p.qk_scale_log2_h[PA_HEAD(p, h)], t4);
+  // this lane's columns are 2 t4 and 2 t4 + 1: their factors sit in the lanes of those groups
+  const float f0 = __shfl_sync(0xffffffffu, factor, 8 * t4), f1 = __shfl_sync(0xffffffffu, factor, 8 * t4 + 4);
+  __syncthreads();
+
+  bool bad = false;
+  // page ids of the warp's next 32 tiles, one to a lane
+  int pages = 0;
+  auto page_of_tile = [&](int k) {  // the warp's k-th tile
+    if (k % 32 == 0) {
+      const int t = (tile0 + warp + (k + lane) * kMassWarps) * 16;
+      pages = t <= pos ? __ldg(table + (t >> lg_p)) : 0;
+    }
+    return __shfl_sync(0xffffffffu, pages, k % 32);
+  };
+  auto scores_of = [&](KeyFrag<KVT, D, QB>& f, int t0, float (&c)[1][4]) {
+    f.score(q, c);
+    const bool in0 = t0 + g4 <= pos, in1 = t0 + g4 + 8 <= pos;
+    c[0][0] = in0 ? __fmul_rn(c[0][0], f0) : -INFINITY;
+    c[0][1] = in0 ? __fmul_rn(c[0][1], f1) : -INFINITY;
+    c[0][2] = in1 ? __fmul_rn(c[0][2], f0) : -INFINITY;
+    c[0][3] = in1 ? __fmul_rn(c[0][3], f1) : -INFINITY;
+  };
+  ColumnStat st0{-INFINITY, 0.0f}, st1{-INFINITY, 0.0f};
+  const int count = mine > warp ? (mine - warp + kMassWarps - 1) / kMassWarps : 0;  // this warp's tiles
+  KeyFrag<KVT, D, QB> next;
+  if (count > 0) next.load(key_rows<Geo::RB>(p, page_of_tile(0), h, (tile0 + warp) * 16, lg_p, bad), g4, t4);
+  for (int k = 0; k < count; ++k) {
+    KeyFrag<KVT, D, QB> now = next;
+    const int local = warp + k * kMassWarps, t0 = (tile0 + local) * 16;
+    if (k + 1 < count)
+      next.load(key_rows<Geo::RB>(p, page_of_tile(k + 1), h, t0 + 16 * kMassWarps, lg_p, bad), g4, t4);
+    float c[1][4];
+    scores_of(now, t0, c);
+    st0.add2(c[0][0], c[0][2]);
+    st1.add2(c[0][1], c[0][3]);
+    if (local * 16 < p.score_keys) {
+      float* s = scores + 2 * t4 * stride + local * 16 + g4;
+      if (2 * t4 < G) s[0] = c[0][0], s[8] = c[0][2];
+      if (2 * t4 + 1 < G) s[stride] = c[0][1], s[stride + 8] = c[0][3];
+    }
+  }
+  // (max, sum) of each column: over the lanes of a warp, the warps, the CTAs
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    st0.merge(__shfl_xor_sync(0xffffffffu, st0.m, off), __shfl_xor_sync(0xffffffffu, st0.l, off));
+    st1.merge(__shfl_xor_sync(0xffffffffu, st1.m, off), __shfl_xor_sync(0xffffffffu, st1.l, off));
+  }
+  if (g4 == 0) {
+    warp_stat[warp][2 * t4] = make_float2(st0.m, st0.l);
+    warp_stat[warp][2 * t4 + 1] = make_float2(st1.m, st1.l);
+  }
+  if (bad) cta_bad = 1;
+  __syncthreads();
+  if (tid < 8) {
+    ColumnStat s{-INFINITY, 0.0f};
+    for (int w = 0; w < kMassWarps; ++w) s.merge(warp_stat[w][tid].x, warp_stat[w][tid].y);
+    cta_stat[tid] = make_float2(s.m, s.l);
+  }
+  cluster.sync();
+  int any_bad = 0;
+  if (tid < 8) {
+    ColumnStat s{-INFINITY, 0.0f};
+    for (int r = 0; r < p.cluster; ++r) {
+      const float2 o = cluster.map_shared_rank(cta_stat, r)[tid];
+      any_bad |= *cluster.map_shared_rank(&cta_bad, r);
+      s.merge(o.x, o.y);
+    }
+    row_stat[tid] = make_float2(s.m, __fdiv_rn(1.0f, s.l));
+  }
+  __syncwarp();
+  cluster.barrier_arrive();  // this CTA has read the others'
+  if (__syncthreads_or(any_bad)) {  // a page out of range: the row adds nothing
+    if (rank == 0 && tid == 0) record_error(p.status, ST_OUT_OF_RANGE);
+  } else {
+    float* sums = p.mass + (static_cast<size_t>(seq) * p.Hkv + h) * (static_cast<size_t>(p.max_blocks) << lg_p);
+    const int first = tile0 * 16, stored = min(min(mine * 16, p.score_keys), pos + 1 - first);
+    float2 rs[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) rs[g] = row_stat[g];
+    for (int t = tid; t < stored; t += kMassThreads) {
+      float w = 0.0f;
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        if (g < G) w = fmaf(ex2(__fsub_rn(scores[g * stride + t], rs[g].x)), rs[g].y, w);
+      atomicAdd(sums + first + t, w);  // one writer a key: the order of additions is the calls'
+    }
+    // keys whose scores found no room: scored again
+    const float2 r0 = row_stat[2 * t4], r1 = row_stat[2 * t4 + 1];
+    for (int local = p.score_keys / 16 + warp; local < mine; local += kMassWarps) {
+      const int t0 = (tile0 + local) * 16;
+      KeyFrag<KVT, D, QB> f;
+      f.load(key_rows<Geo::RB>(p, __ldg(table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
+      float c[1][4];
+      scores_of(f, t0, c);
+      float w0 = 0.0f, w1 = 0.0f;
+      if (2 * t4 < G) {
+        w0 = __fmul_rn(ex2(__fsub_rn(c[0][0], r0.x)), r0.y);
+        w1 = __fmul_rn(ex2(__fsub_rn(c[0][2], r0.x)), r0.y);
+      }
+      if (2 * t4 + 1 < G) {
+        w0 = fmaf(ex2(__fsub_rn(c[0][1], r1.x)), r1.y, w0);
+        w1 = fmaf(ex2(__fsub_rn(c[0][3], r1.x)), r1.y, w1);
+      }
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        w0 = __fadd_rn(w0, __shfl_xor_sync(0xffffffffu, w0, off));
+        w1 = __fadd_rn(w1, __shfl_xor_sync(0xffffffffu, w1, off));
+      }
+      if (t4 == 0 && t0 + g4 <= pos) atomicAdd(sums + t0 + g4, w0);
+      if (t4 == 0 && t0 + g4 + 8 <= pos) atomicAdd(sums + t0 + g4 + 8, w1);
+    }
+  }
+  __syncwarp();
+  cluster.barrier_wait();  // no CTA leaves while another may read its (max, sum)
+}
+
+// ---------------------------------------------------------------- chunks --
+
+// A chunk as both launches see it: its rows (consecutive positions of one
+// sequence, checked by every CTA) and its columns, column c being head c % G of
+// row c / G.
+struct ChunkView {
+  int rows, row0, seq, pos0, last;  // last: the last row's position
+  const int32_t* table;
+  bool ok;
+
+  // The whole CTA: false for a chunk that adds nothing (the error is recorded).
+  __device__ __forceinline__ bool open(const MassParams& p, int c) {
+    row0 = p.chunk_begin[c];
+    rows = p.chunk_end[c] - row0;
+    seq = __ldg(p.seq_ids + row0);
+    pos0 = __ldg(p.positions + row0);
+    last = pos0 + rows - 1;
+    bool bad = seq < 0 || seq >= p.num_seqs || pos0 < 0 || pos0 > p.max_blocks * p.P - rows;
+    table = p.block_tables + static_cast<size_t>(bad ? 0 : seq) * p.max_blocks;
+    if (!bad) {
+      for (int r = threadIdx.x; r < rows; r += blockDim.x)
+        bad |= __ldg(p.seq_ids + row0 + r) != seq || __ldg(p.positions + row0 + r) != pos0 + r;
+      for (int j = threadIdx.x; j <= last / p.P; j += blockDim.x) {
+        const int page = __ldg(table + j);
+        bad |= page < 0 || page >= p.num_pages;
+      }
+    }
+    ok = !__syncthreads_or(bad);
+    if (!ok && threadIdx.x == 0) record_error(p.status, ST_OUT_OF_RANGE);
+    return ok;
+  }
+};
+
+// A column's (maximum, 1 / sum) over its key ranges, merged in ascending order.
+__device__ __forceinline__ float2 column_stat(const MassParams& p, const ChunkView& v, int c, int h, int col, int G) {
+  const size_t cols = static_cast<size_t>(v.rows) * G;
+  const float2* s = p.ws_stats + p.chunk_stats[c] + static_cast<size_t>(h) * p.n_splits * cols + col;
+  const int n = (v.pos0 + col / G) / kMassSplitKeys + 1;
+  ColumnStat st{-INFINITY, 0.0f};
+  for (int k = 0; k < n; ++k) {
+    const float2 o = __ldcg(s + k * cols);
+    st.merge(o.x, o.y);
+  }
+  return make_float2(st.m, __fdiv_rn(1.0f, st.l));
+}
+
+// Columns a warp scores at once (8 to a group), held to about 64 registers of query fragments.
+template <int KVT, int D, bool QB>
+struct ChunkGeom {
+  static constexpr int NT = MassGeom<KVT, D, QB>::QP == 1 ? 4 : MassGeom<KVT, D, QB>::QP == 2 ? 2 : 1;
+  static constexpr int COLS = 8 * NT;
+};
+
+// First launch: one CTA per (chunk, kv head, key range, column block).  The
+// CTA's warps take the range's 16-key tiles in turn.
+template <int KVT, int D, bool QB>
+__global__ void __launch_bounds__(kMassThreads) chunk_stats_kernel(const __grid_constant__ MassParams p) {
+  using Geo = MassGeom<KVT, D, QB>;
+  constexpr int NT = ChunkGeom<KVT, D, QB>::NT, COLS = ChunkGeom<KVT, D, QB>::COLS;
+  __shared__ float2 warp_stat[kMassWarps][COLS];
+  int c = 0;
+  while (c + 1 < p.n_chunks && static_cast<int>(blockIdx.x) >= p.chunk_cta[c + 1]) ++c;
+  const int local = blockIdx.x - p.chunk_cta[c];
+  const int h = local % p.Hkv, split = (local / p.Hkv) % p.n_splits, block = local / p.Hkv / p.n_splits;
+  const int G = p.Hq / p.Hkv, lg_p = 31 - __clz(p.P);
+  ChunkView v;
+  if (!v.open(p, c)) return;
+  const int cols = v.rows * G, col0 = block * COLS, col_end = min(cols, col0 + COLS);
+  const int key0 = split * kMassSplitKeys;
+  const int top = v.pos0 + (col_end - 1) / G;  // the last key any of the columns sees
+  const int key_end = min(top + 1, key0 + kMassSplitKeys);
+  if (key0 >= key_end) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
+  QueryFrag<KVT, D, QB> q[NT];
+  float f[NT][2];
+  int lim[NT][2];  // last key of the lane's columns
+  ColumnStat st[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int col = col0 + 8 * n + g4;
+    const float factor = q[n].load(p, col < cols ? v.row0 + col / G : -1, h * G + col % G, p.qk_scale_log2_h[PA_HEAD(p, h)], t4);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      f[n][k] = __shfl_sync(0xffffffffu, factor, 8 * t4 + 4 * k);
+      lim[n][k] = v.pos0 + (col0 + 8 * n + 2 * t4 + k) / G;
+      st[n][k] = ColumnStat{-INFINITY, 0.0f};
+    }
+  }
+  bool bad = false;
+  for (int t0 = key0 + warp * 16; t0 < key_end; t0 += kMassWarps * 16) {
+    KeyFrag<KVT, D, QB> a;
+    a.load(key_rows<Geo::RB>(p, __ldg(v.table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
+    float s[NT][4];
+    a.score(q, s);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        st[n][k].add2(t0 + g4 <= lim[n][k] ? __fmul_rn(s[n][k], f[n][k]) : -INFINITY,
+                      t0 + g4 + 8 <= lim[n][k] ? __fmul_rn(s[n][2 + k], f[n][k]) : -INFINITY);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1)
+        st[n][k].merge(__shfl_xor_sync(0xffffffffu, st[n][k].m, off), __shfl_xor_sync(0xffffffffu, st[n][k].l, off));
+      if (g4 == 0) warp_stat[warp][8 * n + 2 * t4 + k] = make_float2(st[n][k].m, st[n][k].l);
+    }
+  __syncthreads();
+  if (tid < COLS && col0 + tid < cols) {
+    ColumnStat s{-INFINITY, 0.0f};
+    for (int w = 0; w < kMassWarps; ++w) s.merge(warp_stat[w][tid].x, warp_stat[w][tid].y);
+    p.ws_stats[p.chunk_stats[c] + (static_cast<size_t>(h) * p.n_splits + split) * cols + col0 + tid] = make_float2(s.m, s.l);
+  }
+}
+
+// Second launch: one CTA per (chunk, kv head, block of 128 keys).  A warp keeps
+// its 16 keys' fragments and goes over the columns that see them.
+template <int KVT, int D, bool QB>
+__global__ void __launch_bounds__(kMassThreads) chunk_weights_kernel(const __grid_constant__ MassParams p) {
+  using Geo = MassGeom<KVT, D, QB>;
+  constexpr int NT = ChunkGeom<KVT, D, QB>::NT, COLS = ChunkGeom<KVT, D, QB>::COLS;
+  __shared__ float2 stat[COLS];
+  const int h = blockIdx.x % p.Hkv, block = (blockIdx.x / p.Hkv) % p.n_blocks, c = blockIdx.x / p.Hkv / p.n_blocks;
+  const int G = p.Hq / p.Hkv, lg_p = 31 - __clz(p.P);
+  ChunkView v;
+  if (!v.open(p, c)) return;
+  const int key0 = block * kMassWarps * 16;
+  if (key0 > v.last) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
+  const int cols = v.rows * G, t0 = key0 + warp * 16;
+  bool bad = false;
+  KeyFrag<KVT, D, QB> a;
+  if (t0 <= v.last) a.load(key_rows<Geo::RB>(p, __ldg(v.table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
+  float w0 = 0.0f, w1 = 0.0f;
+  // columns before the first row that sees key0 see none of the block
+  for (int col0 = max(0, key0 - v.pos0) * G / COLS * COLS; col0 < cols; col0 += COLS) {
+    __syncthreads();
+    if (tid < COLS && col0 + tid < cols) stat[tid] = column_stat(p, v, c, h, col0 + tid, G);
+    __syncthreads();
+    if (t0 > v.last) continue;
+    QueryFrag<KVT, D, QB> q[NT];
+    float factor[NT], s[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = col0 + 8 * n + g4;
+      factor[n] = q[n].load(p, col < cols ? v.row0 + col / G : -1, h * G + col % G, p.qk_scale_log2_h[PA_HEAD(p, h)], t4);
+    }
+    a.score(q, s);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float f = __shfl_sync(0xffffffffu, factor[n], 8 * t4 + 4 * k);
+        const int col = col0 + 8 * n + 2 * t4 + k;
+        if (col < cols) {
+          const int lim = v.pos0 + col / G;
+          const float2 z = stat[8 * n + 2 * t4 + k];
+          if (t0 + g4 <= lim) w0 = fmaf(ex2(__fsub_rn(__fmul_rn(s[n][k], f), z.x)), z.y, w0);
+          if (t0 + g4 + 8 <= lim) w1 = fmaf(ex2(__fsub_rn(__fmul_rn(s[n][2 + k], f), z.x)), z.y, w1);
+        }
+      }
+  }
+#pragma unroll
+  for (int off = 1; off < 4; off <<= 1) {
+    w0 = __fadd_rn(w0, __shfl_xor_sync(0xffffffffu, w0, off));
+    w1 = __fadd_rn(w1, __shfl_xor_sync(0xffffffffu, w1, off));
+  }
+  float* sums = p.mass + (static_cast<size_t>(v.seq) * p.Hkv + h) * (static_cast<size_t>(p.max_blocks) << lg_p);
+  if (t4 == 0 && t0 + g4 <= v.last) atomicAdd(sums + t0 + g4, w0);
+  if (t4 == 0 && t0 + g4 + 8 <= v.last) atomicAdd(sums + t0 + g4 + 8, w1);
+}
+
+// -------------------------------------------------------------- launches --
+
+template <int KVT, int D, bool QB>
+cudaError_t launch_mass_inst(const MassParams& p0, bool rows, cudaStream_t stream) {
+  MassParams p = p0;
+  cudaError_t e = cudaSuccess;
+  if (rows) {
+    const int G = p.Hq / p.Hkv;
+    const size_t smem = static_cast<size_t>(G) * score_stride(p.score_keys) * sizeof(float);
+    static std::atomic<unsigned long long> smem_done{0};
+    e = allow_dynamic_smem(mass_row_kernel<KVT, D, QB>, smem_done, kMassScoreBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.n_rows) * p.Hkv * p.cluster);
+    cfg.blockDim = dim3(kMassThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(p.cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, mass_row_kernel<KVT, D, QB>, p);
+    count_launch();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.n_chunks > 0) {
+    constexpr int COLS = ChunkGeom<KVT, D, QB>::COLS;
+    const int G = p.Hq / p.Hkv;
+    long long ctas = 0;
+    for (int c = 0; c < p.n_chunks; ++c) {
+      p.chunk_cta[c] = static_cast<int32_t>(ctas);
+      const long long cols = static_cast<long long>(p.chunk_end[c] - p.chunk_begin[c]) * G;
+      ctas += (cols + COLS - 1) / COLS * p.Hkv * p.n_splits;
+      if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    }
+    p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);
+    const long long blocks = static_cast<long long>(p.n_chunks) * p.Hkv * p.n_blocks;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    chunk_stats_kernel<KVT, D, QB><<<static_cast<unsigned>(ctas), kMassThreads, 0, stream>>>(p);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    chunk_weights_kernel<KVT, D, QB><<<static_cast<unsigned>(blocks), kMassThreads, 0, stream>>>(p);
+    count_launch();
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+template <int KVT>
+cudaError_t launch_mass_dispatch(const MassParams& p, bool rows, cudaStream_t stream) {
+  if (p.D == 64) return p.q_is_bf16 ? launch_mass_inst<KVT, 64, true>(p, rows, stream) : launch_mass_inst<KVT, 64, false>(p, rows, stream);
+  return p.q_is_bf16 ? launch_mass_inst<KVT, 128, true>(p, rows, stream) : launch_mass_inst<KVT, 128, false>(p, rows, stream);
+}
+
+// One translation unit per K dtype.  rows: some row is outside every chunk.
+cudaError_t launch_mass_f32(const MassParams& p, bool rows, cudaStream_t stream);
+cudaError_t launch_mass_bf16(const MassParams& p, bool rows, cudaStream_t stream);
+cudaError_t launch_mass_e4m3(const MassParams& p, bool rows, cudaStream_t stream);
+
+}  // namespace pa
