@@ -403,26 +403,40 @@ def _check_int_shape(t, name: str, shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {list(shape)}")
 
 
-class _launch_on:
-    """The device of a call's tensors made current (they must share one), with
-    the stream the call runs on: the caller's, or that device's current one."""
+def _cptr(t, name: str) -> Optional[int]:
+    """The address of a contiguous tensor (its device is _call's to check)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def __init__(self, stream, *tensors):
-        import torch
-        devices = {t.device for t in tensors if t is not None}
-        if any(d.type != "cuda" for d in devices):
+
+def _call(fn, stream, tensors, *args):
+    """fn(*args, stream) on the device of a call's tensors, which they must
+    share: on the caller's stream, or that device's current one."""
+    import torch
+    device = -1
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
             raise ValueError("tensor must live on a CUDA device")
-        if len(devices) != 1:
-            raise ValueError(f"tensors live on different devices: {sorted(map(str, devices))}")
-        self.guard = torch.cuda.device(devices.pop())
-        self.stream = stream
-
-    def __enter__(self):
-        self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        if device >= 0 and d != device:
+            raise ValueError(f"tensors live on different devices: cuda:{device} and cuda:{d}")
+        device = d
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != PA_OK:
+        raise PaError(status, last_error())
 
 
 def _chunk_array(chunks):
@@ -444,11 +458,12 @@ def attention_mass(pool: Pool, q, seq_ids, positions, block_tables, mass, chunks
     num_seqs, max_blocks = (int(x) for x in block_tables.shape)
     _check_f32(mass, "mass", (num_seqs, pool.num_kv_heads, max_blocks * pool.page_size))
     ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    with _launch_on(stream, pool.k_pool, q, seq_ids, positions, block_tables, mass, workspace, status) as s:
-        _check(load().pa_attention_mass(pool.handle, n, _ptr(q), _dtype_code(q), int(q.shape[1]), _ptr(seq_ids),
-                                        _ptr(positions), _ptr(block_tables), num_seqs, max_blocks,
-                                        _chunk_array(chunks) if chunks else None, len(chunks), float(softmax_scale),
-                                        _ptr(mass), _ptr(workspace), ws_len, _ptr(status), s))
+    _call(load().pa_attention_mass, stream,
+          (pool.k_pool, q, seq_ids, positions, block_tables, mass, workspace, status), pool.handle, n, _cptr(q, "q"),
+          _dtype_code(q), int(q.shape[1]), _cptr(seq_ids, "seq_ids"), _cptr(positions, "positions"),
+          _cptr(block_tables, "block_tables"), num_seqs, max_blocks, _chunk_array(chunks) if chunks else None,
+          len(chunks), float(softmax_scale), _cptr(mass, "mass"), _cptr(workspace, "workspace"), ws_len,
+          _cptr(status, "status"))
 
 
 def evict_select(mass, seq_ids, lengths, keep, kept_lengths=None, keep_first: int = 0, keep_last: int = 0, status=None,
@@ -471,10 +486,10 @@ def evict_select(mass, seq_ids, lengths, keep, kept_lengths=None, keep_first: in
             raise ValueError("kept_lengths may not be lengths")
     if status is not None:
         _check_index(status, "status")
-    with _launch_on(stream, mass, seq_ids, lengths, keep, kept_lengths, status) as s:
-        _check(load().pa_evict_select(n, _ptr(seq_ids), _ptr(lengths), _ptr(mass), num_seqs, heads, max_tokens, budget,
-                                      int(keep_first), int(keep_last), _ptr(keep), _ptr(kept_lengths), _ptr(status),
-                                      s))
+    _call(load().pa_evict_select, stream, (mass, seq_ids, lengths, keep, kept_lengths, status), n,
+          _cptr(seq_ids, "seq_ids"), _cptr(lengths, "lengths"), _cptr(mass, "mass"), num_seqs, heads, max_tokens, budget,
+          int(keep_first), int(keep_last), _cptr(keep, "keep"), _cptr(kept_lengths, "kept_lengths"),
+          _cptr(status, "status"))
 
 
 def evict_compact(pool: Pool, keep, seq_ids, lengths, block_tables, mass=None, dst_seq_ids=None, status=None,
@@ -496,9 +511,11 @@ def evict_compact(pool: Pool, keep, seq_ids, lengths, block_tables, mass=None, d
     num_seqs, max_blocks = (int(x) for x in block_tables.shape)
     if mass is not None:
         _check_f32(mass, "mass", (num_seqs, pool.num_kv_heads, max_blocks * pool.page_size))
-    with _launch_on(stream, pool.k_pool, keep, seq_ids, lengths, block_tables, mass, dst_seq_ids, status) as s:
-        _check(load().pa_evict_compact(pool.handle, n, _ptr(seq_ids), _ptr(dst_seq_ids), _ptr(lengths), _ptr(keep),
-                                       budget, _ptr(block_tables), num_seqs, max_blocks, _ptr(mass), _ptr(status), s))
+    _call(load().pa_evict_compact, stream,
+          (pool.k_pool, keep, seq_ids, lengths, block_tables, mass, dst_seq_ids, status), pool.handle, n,
+          _cptr(seq_ids, "seq_ids"), _cptr(dst_seq_ids, "dst_seq_ids"), _cptr(lengths, "lengths"), _cptr(keep, "keep"),
+          budget, _cptr(block_tables, "block_tables"), num_seqs, max_blocks, _cptr(mass, "mass"),
+          _cptr(status, "status"))
 
 
 def beam_workspace_bytes(n_groups: int, beams: int, vocab: int, n_out: int) -> int:
@@ -527,11 +544,11 @@ def beam_select(logits, scores, parents, tokens, out_scores, finished=None, end_
     row = int(logits.stride(1)) if beams > 1 else int(logits.stride(0)) if groups > 1 else vocab
     if (vocab > 1 and logits.stride(2) != 1) or (groups > 1 and logits.stride(0) != beams * row):
         raise ValueError("logits must have contiguous rows, evenly spaced over groups and beams")
-    with _launch_on(stream, logits, scores, parents, tokens, out_scores, finished, workspace) as s:
-        ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(load().pa_beam_select(groups, beams, vocab, logits.data_ptr(), _dtype_code(logits), row, _ptr(scores),
-                                     _ptr(finished), int(end_token), n_out, _ptr(parents), _ptr(tokens),
-                                     _ptr(out_scores), _ptr(workspace), ws_len, s))
+    ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _call(load().pa_beam_select, stream, (logits, scores, parents, tokens, out_scores, finished, workspace), groups,
+          beams, vocab, logits.data_ptr(), _dtype_code(logits), row, _cptr(scores, "scores"),
+          _cptr(finished, "finished"), int(end_token), n_out, _cptr(parents, "parents"), _cptr(tokens, "tokens"),
+          _cptr(out_scores, "out_scores"), _cptr(workspace, "workspace"), ws_len)
 
 
 def beam_reorder(pool: Pool, parents, seq_ids, lengths, block_tables, state=None, status=None, stream=None):
@@ -553,10 +570,10 @@ def beam_reorder(pool: Pool, parents, seq_ids, lengths, block_tables, state=None
         if state.dim() < 1 or int(state.shape[0]) != num_seqs:
             raise ValueError(f"state has shape {tuple(state.shape)}; expected {num_seqs} rows")
         row_bytes = state.numel() // num_seqs * state.element_size()
-    with _launch_on(stream, pool.k_pool, parents, seq_ids, lengths, block_tables, state, status) as s:
-        _check(load().pa_beam_reorder(pool.handle, groups, beams, _ptr(seq_ids), _ptr(parents), _ptr(lengths),
-                                      _ptr(block_tables), num_seqs, max_blocks, _ptr(state), row_bytes, _ptr(status),
-                                      s))
+    _call(load().pa_beam_reorder, stream, (pool.k_pool, parents, seq_ids, lengths, block_tables, state, status),
+          pool.handle, groups, beams, _cptr(seq_ids, "seq_ids"), _cptr(parents, "parents"), _cptr(lengths, "lengths"),
+          _cptr(block_tables, "block_tables"), num_seqs, max_blocks, _cptr(state, "state"), row_bytes,
+          _cptr(status, "status"))
 
 
 def set_split_tokens(tokens: int):
