@@ -289,17 +289,17 @@ pa_status pa_evict_compact(const pa_pool *pool, int32_t n, const int32_t *seq_id
  *   finished    int32 [n_groups * beams], non-zero: finished (may be NULL: none)
  *   parents, tokens   int32 [n_groups][n_out]: the beam (0..beams-1) a continuation
  *               extends, and its token;  out_scores  f32 [n_groups][n_out]
- * beams <= 32, n_out <= 64.  A logit of -infinity is no continuation; a beam
+ * beams <= 32, n_out <= 64, vocab <= 2^20.  A logit of -infinity is no continuation; a beam
  * whose log-sum-exp is not finite (NaN or +infinity among its logits, or
  * nothing but -infinity) or whose score is not finite has none.  Where fewer
  * than n_out exist the rest is parent -1, token -1, score -infinity.
- * Sums of exponentials are FP32 per thread and FP64 across threads; scores are
- * compared in FP64 and rounded once.
+ * Sums of exponentials are FP32 within 32 KB of a row and FP64 across them;
+ * scores are compared in FP64 and rounded once.  A group's results do not depend on the
+ * other groups, nor on the alignment of its rows.
  *   workspace   device memory of at least pa_beam_workspace_bytes(...), 256-byte
- *               aligned, ZERO-FILLED BEFORE ITS FIRST USE; every call leaves its
- *               counters at zero again.  Calls that share one must not overlap on
- *               the GPU.
- * Graph-capturable. */
+ *               aligned; scratch that each call writes before it reads it.  Calls
+ *               that share one must not overlap on the GPU.
+ * Two launches, the second a programmatic dependent of the first; graph-capturable. */
 size_t pa_beam_workspace_bytes(int32_t n_groups, int32_t beams, int32_t vocab, int32_t n_out);
 pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const void *logits, pa_dtype logits_dtype,
                          int64_t row_stride, const float *scores, const int32_t *finished, int32_t end_token,

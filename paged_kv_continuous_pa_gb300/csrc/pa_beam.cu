@@ -21,20 +21,34 @@ struct BeamParams {
   int32_t* parents;
   int32_t* tokens;
   float* out_scores;
-  uint64_t* cand;   // [rows][n_out] best (logit, token) of each row, best first; 0: none
-  double* norm;     // [rows] log-sum-exp; NaN: the row has no candidates
-  int32_t groups, beams, vocab, n_out, end_token;
+  // workspace, per chunk of a row: its best (logit, token) keys, best first (0: none), its sum of
+  // exponentials and the maximum they are relative to
+  uint64_t* chunk_keys;  // [rows][chunks][n_out]
+  float* chunk_sum;      // [rows][chunks]
+  float* chunk_max;      // [rows][chunks]
+  int32_t groups, beams, vocab, chunks, n_out, end_token;
+  int32_t merge_warps;  // warps of the merge that have room for a row's keys
 };
 
-constexpr int kBeamThreads = 512;
+constexpr int kBeamThreads = 256;
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kBeamVecs = 8;                                        // 16-byte vectors a thread holds
+constexpr int kBeamChunkBytes = kBeamThreads * kBeamVecs * 16;      // of a row, per CTA
+constexpr int kMaxVocab = 1 << 20;
+constexpr size_t kBeamListBytes = 68 * 1024;  // keys the merge holds at once (at least a row: 128 chunks, n_out 64)
+constexpr size_t kBeamMaxSmem = 96 * 1024;
+
+__host__ __device__ constexpr int beam_chunk(bool bf16) { return kBeamChunkBytes / (bf16 ? 2 : 4); }
 
 // A logit and its token as one integer: larger logits first, then lower
 // tokens; -0 and +0 are one value.  NaN and -infinity are never asked for (0).
-__device__ __forceinline__ uint64_t cand_key(float x, int token) {
-  if (!(x > -INFINITY)) return 0ull;
+__device__ __forceinline__ uint32_t logit_order(float x) {
+  if (!(x > -INFINITY)) return 0u;
   const uint32_t u = x == 0.0f ? 0u : __float_as_uint(x);
-  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return (static_cast<uint64_t>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(token));
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t cand_key(uint32_t order, int token) {
+  return (static_cast<uint64_t>(order) << 32) | (0xffffffffu - static_cast<uint32_t>(token));
 }
 __device__ __forceinline__ float cand_logit(uint64_t key) {
   const uint32_t o = static_cast<uint32_t>(key >> 32);
@@ -42,103 +56,370 @@ __device__ __forceinline__ float cand_logit(uint64_t key) {
 }
 __device__ __forceinline__ int cand_token(uint64_t key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
 
-__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
-
-template <bool BF16>
-__device__ __forceinline__ float logit_at(const BeamParams& p, size_t i) {
-  if constexpr (BF16)
-    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.logits)[i]) << 16);
-  else
-    return static_cast<const float*>(p.logits)[i];
+// 16 bytes of a row from any element-aligned address.  A misaligned vector is
+// shifted together from the two aligned ones that hold it, the second read only
+// where it holds an element of the row (left: the row's bytes from here on), so
+// that no aligned 16 bytes without one is touched.
+__device__ __forceinline__ uint4 load_row_vec(const unsigned char* src, int64_t left) {
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+  const uint4* at = reinterpret_cast<const uint4*>(src - off);
+  const uint4 a = __ldcs(at);
+  if (off == 0) return a;
+  uint4 b = make_uint4(0u, 0u, 0u, 0u);
+  if (left > 16 - off) b = __ldcs(at + 1);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int sh = 8 * (off & 3);
+  uint32_t r[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)  // the same word offset for the whole row: a uniform choice
+    if (off / 4 == s) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = __funnelshift_r(w[s + k], s + k + 1 < 8 ? w[s + k + 1] : 0u, sh);
+    }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// One CTA per beam: the row's log-sum-exp, then its n_out best logits, one
-// scan of the row for each.
+// Element e of a held vector.
 template <bool BF16>
-__global__ void __launch_bounds__(kBeamThreads) beam_row_kernel(const __grid_constant__ BeamParams p) {
-  __shared__ double red_sum[kBeamThreads / 32];
-  __shared__ float red_max[kBeamThreads / 32];
-  __shared__ uint64_t red_key[kBeamThreads / 32];
-  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (p.finished != nullptr && __ldg(p.finished + row) != 0) return;
-  const size_t base = static_cast<size_t>(row) * p.row_stride;
-  float top = -INFINITY;
-  bool nan = false;
-  for (int v = tid; v < p.vocab; v += kBeamThreads) {
-    const float x = logit_at<BF16>(p, base + v);
-    nan |= x != x;
-    top = fmaxf(top, x);
+__device__ __forceinline__ float vec_logit(const uint4& v, int e) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (BF16) return (e & 1) ? bf16hi(w[e / 2]) : bf16lo(w[e / 2]);
+  return __uint_as_float(w[e]);
+}
+
+// A held vector whose elements from `left` on are behind the row: those become -infinity.
+template <bool BF16>
+__device__ __forceinline__ uint4 cut_vec(uint4 v, int left) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF16) {
+      if (2 * k >= left) w[k] = (w[k] & 0xffff0000u) | 0xff80u;
+      if (2 * k + 1 >= left) w[k] = (w[k] & 0x0000ffffu) | 0xff800000u;
+    } else {
+      if (k >= left) w[k] = 0xff800000u;
+    }
   }
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (lane == 0) red_max[warp] = top;
-  nan = __syncthreads_or(nan);
-  top = red_max[0];
-  for (int w = 1; w < kBeamThreads / 32; ++w) top = fmaxf(top, red_max[w]);
-  const bool dead = nan || !(fabsf(top) < INFINITY);
-  float part = 0.0f;
-  for (int v = tid; v < p.vocab && !dead; v += kBeamThreads) part += expf(logit_at<BF16>(p, base + v) - top);
-  double sum = part;
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// The largest element of a vector (NaN only if nothing else is there).
+template <bool BF16>
+__device__ __forceinline__ float vec_max(const uint4& v) {
+  if constexpr (BF16) {
+    const uint32_t m = max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
+    return fmaxf(bf16lo(m), bf16hi(m));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+}
+
+// One warp: a bound that at least `want` of the (distinct, or zero) keys list[0, n)
+// reach, and no more than 2 * want; 1 where fewer than `want` reach lo.
+__device__ __forceinline__ uint64_t bound_keys(const uint64_t* list, int n, int want, uint64_t lo, uint64_t hi, int lane) {
+  auto reach = [&](uint64_t bound) {
+    int c = 0;
+    for (int i = lane; i < n; i += 32) c += list[i] >= bound;
+    return static_cast<int>(__reduce_add_sync(0xffffffffu, c));
+  };
+  int at_lo = reach(lo);
+  if (at_lo < want) return 1ull;
+  while (at_lo > 2 * want && hi - lo > 1ull) {  // reach(lo) >= want > reach(hi)
+    const uint64_t mid = lo + (hi - lo) / 2;
+    const int c = reach(mid);
+    if (c >= want) lo = mid, at_lo = c;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// One CTA per 32 KB of a row, held in registers from one read: its maximum and
+// sum of exponentials, and its n_out best.  The n_out-th best of the CTA is at
+// least the n_out-th best of the threads' bests; a value that n_out of those
+// reach (and at most twice as many) is found by bisection, only threads whose
+// best reaches it look for candidates again, and what they find is ranked by
+// counting.  Where more threads' bests are equal, the lowest tokens among them
+// set the bound.
+//
+// Bound by the one read of the logits: about eight instructions an element
+// (maximum, subtraction, multiplication, ex2, addition; packed in pairs).
+template <bool BF16>
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const __grid_constant__ BeamParams p) {
+  constexpr int V = BF16 ? 8 : 4;  // elements of a vector
+  constexpr int ELT = BF16 ? 2 : 4;
+  constexpr int CHUNK = beam_chunk(BF16);
+  constexpr int PER = kBeamThreads / 32;
+  extern __shared__ uint64_t list[];
+  __shared__ float red_sum[kBeamWarps], red_max[kBeamWarps];
+  __shared__ uint32_t best_order[kBeamThreads];
+  __shared__ int best_token[kBeamThreads];
+  __shared__ uint32_t bound_order;
+  __shared__ int bound_need, bound_token, found;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  const int K = p.n_out;
+  if (p.finished != nullptr && __ldg(p.finished + row) != 0) return;  // its logits do not matter
+  const int base = chunk * CHUNK;  // the CTA's first token
+  const unsigned char* src =
+      static_cast<const unsigned char*>(p.logits) + (static_cast<size_t>(row) * p.row_stride + base) * ELT;
+  const int n = min(CHUNK, p.vocab - base);
+  uint4 v[kBeamVecs];
+  if (n == CHUNK) {
+#pragma unroll
+    for (int i = 0; i < kBeamVecs; ++i) {
+      const int e0 = (i * kBeamThreads + tid) * V;
+      v[i] = load_row_vec(src + static_cast<size_t>(e0) * ELT, static_cast<int64_t>(n - e0) * ELT);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBeamVecs; ++i) {
+      const int e0 = (i * kBeamThreads + tid) * V;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (e0 < n) v[i] = load_row_vec(src + static_cast<size_t>(e0) * ELT, static_cast<int64_t>(n - e0) * ELT);
+      if (e0 + V > n) v[i] = cut_vec<BF16>(v[i], n - e0);
+    }
+  }
+  griddep_launch_dependents();  // the merge may be launched; it waits for all of this
+  if (tid == 0) found = 0;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kBeamVecs; ++i) top = fmaxf(top, vec_max<BF16>(v[i]));
+  best_order[tid] = logit_order(top);
+  float m = top;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane == 0) red_max[warp] = m;
+  __syncthreads();
+  m = red_max[0];
+#pragma unroll
+  for (int w = 1; w < kBeamWarps; ++w) m = fmaxf(m, red_max[w]);
+  if (warp == 0) {
+    uint32_t o[PER], most = 0u;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      o[i] = best_order[i * 32 + lane];
+      most = max(most, o[i]);
+    }
+    auto reach = [&](uint32_t bound) {
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c += o[i] >= bound;
+      return static_cast<int>(__reduce_add_sync(0xffffffffu, c));
+    };
+    // every lane has a best that reaches the smallest of the lanes' largest: a first bound for K <= 32
+    uint32_t lo = max(1u, K <= 32 ? __reduce_min_sync(0xffffffffu, most) : 1u), hi = logit_order(m) + 1u;
+    int at_lo = reach(lo), need = 0;
+    if (at_lo < K) at_lo = reach(lo = 1u);
+    if (at_lo >= K) {
+      while (at_lo > 2 * K && hi - lo > 1u) {  // reach(lo) >= K > reach(hi)
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int c = reach(mid);
+        if (c >= K) lo = mid, at_lo = c;
+        else hi = mid;
+      }
+      if (at_lo > 2 * K) need = K - reach(lo + 1u);  // equal bests: so many of them, those with the lowest tokens
+    }
+    if (lane == 0) {
+      bound_order = lo;
+      bound_need = need;
+      bound_token = 0x7fffffff;
+    }
+  }
+  // the exponentials against the chunk's maximum (0 where it holds none, so that a NaN still shows)
+  const float ref = m == -INFINITY ? 0.0f : m;
+  constexpr float kLog2e = 1.4426950408889634f;
+  float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < kBeamVecs; ++i)
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float2 d = __fadd2_rn(make_float2(vec_logit<BF16>(v[i], e), vec_logit<BF16>(v[i], e + 1)), make_float2(-ref, -ref));
+      const float2 t = __fmul2_rn(d, make_float2(kLog2e, kLog2e));
+      part = __fadd2_rn(part, make_float2(ex2(t.x), ex2(t.y)));
+    }
+  float sum = __fadd_rn(part.x, part.y);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));
   if (lane == 0) red_sum[warp] = sum;
   __syncthreads();
-  if (tid == 0) {
-    double s = 0.0;
-    for (int w = 0; w < kBeamThreads / 32; ++w) s += red_sum[w];
-    p.norm[row] = dead ? static_cast<double>(NAN) : static_cast<double>(top) + log(s);
-  }
-  uint64_t last = ~0ull;
-  for (int k = 0; k < p.n_out; ++k) {
-    uint64_t best = 0ull;
-    for (int v = tid; v < p.vocab && !dead; v += kBeamThreads) {
-      const uint64_t key = cand_key(logit_at<BF16>(p, base + v), v);
-      if (key < last) best = max_u64(best, key);
+  const uint32_t bo = bound_order;
+  const float bv = bo <= 0x00800000u ? -3.402823466e38f : cand_logit(static_cast<uint64_t>(bo) << 32);  // as a logit
+  if (bound_need > 0) {
+    // the whole CTA: each thread's first token of exactly the bound, then the bound_need-th lowest of them
+    int first = 0x7fffffff;
+    if (logit_order(top) == bo) {
+#pragma unroll
+      for (int i = kBeamVecs - 1; i >= 0; --i)
+#pragma unroll
+        for (int e = V - 1; e >= 0; --e)
+          if (vec_logit<BF16>(v[i], e) == bv) first = (i * kBeamThreads + tid) * V + e;
     }
-    for (int off = 16; off > 0; off >>= 1) best = max_u64(best, __shfl_xor_sync(0xffffffffu, best, off));
+    best_token[tid] = first;
     __syncthreads();
-    if (lane == 0) red_key[warp] = best;
+    if (warp == 0) {
+      int t[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) t[i] = best_token[i * 32 + lane];
+      int a = 0, b = CHUNK - 1;
+      while (a < b) {
+        const int mid = (a + b) / 2;
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) c += t[i] <= mid;
+        if (static_cast<int>(__reduce_add_sync(0xffffffffu, c)) >= bound_need) b = mid;
+        else a = mid + 1;
+      }
+      if (lane == 0) bound_token = a;
+    }
     __syncthreads();
-    for (int w = 0; w < kBeamThreads / 32; ++w) best = max_u64(best, red_key[w]);
-    last = best;
-    if (tid == 0) p.cand[static_cast<size_t>(row) * p.n_out + k] = best;
+  }
+  // at most 2 n_out threads get here: `list` has room for all that they hold
+  const int bt = bound_token;
+  if (top > bv || top == bv) {
+#pragma unroll
+    for (int i = 0; i < kBeamVecs; ++i) {
+      if (!(vec_max<BF16>(v[i]) >= bv)) continue;
+      const int e0 = (i * kBeamThreads + tid) * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float x = vec_logit<BF16>(v[i], e);
+        if (x > bv || (x == bv && e0 + e <= bt)) list[atomicAdd(&found, 1)] = cand_key(logit_order(x), base + e0 + e);
+      }
+    }
+  }
+  __syncthreads();
+  const int total = found;
+  uint64_t* out = p.chunk_keys + (static_cast<size_t>(row) * p.chunks + chunk) * K;
+  for (int c = tid; c < total; c += kBeamThreads) {
+    const uint64_t key = list[c];
+    int rank = 0;
+    for (int o = 0; o < total; ++o) rank += list[o] > key;
+    if (rank < K) out[rank] = key;
+  }
+  for (int c = total + tid; c < K; c += kBeamThreads) out[c] = 0ull;
+  if (tid == 0) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBeamWarps; w += 2) s = __fadd_rn(s, __fadd_rn(red_sum[w], red_sum[w + 1]));
+    p.chunk_sum[static_cast<size_t>(row) * p.chunks + chunk] = s;
+    p.chunk_max[static_cast<size_t>(row) * p.chunks + chunk] = ref;
   }
 }
 
-// One CTA per group: scores of the beams' candidates in 64 bits, each
-// candidate's rank by counting the better ones, the n_out best written.
-__global__ void __launch_bounds__(256) beam_merge_kernel(const __grid_constant__ BeamParams p) {
-  extern __shared__ double score[];  // [beams * n_out]
-  const int g = blockIdx.x, tid = threadIdx.x;
-  const int total = p.beams * p.n_out;
-  for (int c = tid; c < total; c += 256) {
-    const int row = g * p.beams + c / p.n_out, k = c % p.n_out;
+// One CTA per group.  A warp takes a row: the log-sum-exp over its chunks, and
+// its n_out best out of the chunks' lists (a bound, then ranks by counting what
+// reaches it).  Then the beams' candidates by score in 64 bits: each beam's
+// descend, so a candidate's rank is a sum of binary searches.
+__global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_constant__ BeamParams p) {
+  extern __shared__ uint64_t list[];  // a warp each: [chunks][n_out] keys, [2 n_out] candidates; then the scores
+  __shared__ int found;
+  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int K = p.n_out, per_row = p.chunks * K, total = p.beams * K;
+  uint64_t* keys = list + static_cast<size_t>(warp) * (per_row + 2 * K);
+  uint64_t* cand = keys + per_row;
+  double* score = reinterpret_cast<double*>(list + static_cast<size_t>(p.merge_warps) * (per_row + 2 * K));  // [beams][n_out]
+  int* token = reinterpret_cast<int*>(score + total);
+  if (tid == 0) found = 0;
+  griddep_wait();  // the chunks' results
+  for (int b = warp; b < p.beams && warp < p.merge_warps; b += p.merge_warps) {
+    const size_t row = static_cast<size_t>(g) * p.beams + b;
     const double cum = __ldg(p.scores + row);
-    double s = -INFINITY;
+    for (int k = lane; k < K; k += 32) score[b * K + k] = -INFINITY;
+    __syncwarp();
     if (p.finished != nullptr && __ldg(p.finished + row) != 0) {
-      if (k == 0) s = cum;
-    } else {
-      const uint64_t key = p.cand[static_cast<size_t>(row) * p.n_out + k];
-      if (key != 0ull) s = cum + (static_cast<double>(cand_logit(key)) - p.norm[row]);
+      if (lane == 0) {
+        if (isfinite(cum)) score[b * K] = cum;
+        token[b * K] = p.end_token;
+      }
+      continue;
     }
-    score[c] = isfinite(s) ? s : static_cast<double>(-INFINITY);
-  }
-  for (int k = tid; k < p.n_out; k += 256) {
-    p.parents[static_cast<size_t>(g) * p.n_out + k] = -1;
-    p.tokens[static_cast<size_t>(g) * p.n_out + k] = -1;
-    p.out_scores[static_cast<size_t>(g) * p.n_out + k] = -INFINITY;
+    const uint64_t* from = p.chunk_keys + row * per_row;
+    uint64_t most = 0ull, least = 0ull;  // the largest key, and the largest n_out-th of a chunk
+    for (int c = lane; c < per_row; c += 32) {
+      const uint64_t key = __ldcg(from + c);
+      keys[c] = key;
+      most = key > most ? key : most;
+      if (c % K == K - 1 && key > least) least = key;
+    }
+    const float* cs = p.chunk_sum + row * p.chunks;
+    const float* cm = p.chunk_max + row * p.chunks;
+    float m = -INFINITY;
+    for (int j = lane; j < p.chunks; j += 32)
+      if (__ldcg(cs + j) != 0.0f) m = fmaxf(m, __ldcg(cm + j));  // NaN sums among them
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      const uint64_t a = __shfl_xor_sync(0xffffffffu, most, off), z = __shfl_xor_sync(0xffffffffu, least, off);
+      most = a > most ? a : most;
+      least = z > least ? z : least;
+    }
+    double s = 0.0;
+    for (int j = lane; j < p.chunks; j += 32) {
+      const float c = __ldcg(cs + j);
+      if (c != 0.0f) s += static_cast<double>(c) * static_cast<double>(expf(__fsub_rn(__ldcg(cm + j), m)));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const double log_s = log(s);
+    __syncwarp();
+    if (!isfinite(m) || !isfinite(log_s) || !isfinite(cum) || most == 0ull) continue;
+    const uint64_t bound = bound_keys(keys, per_row, K, least > 0ull ? least : 1ull, most + 1ull, lane);
+    int n = 0;
+    for (int c0 = 0; c0 < per_row; c0 += 32) {
+      const uint64_t key = c0 + lane < per_row ? keys[c0 + lane] : 0ull;
+      const unsigned in = __ballot_sync(0xffffffffu, key >= bound);
+      if (key >= bound) cand[n + __popc(in & ((1u << lane) - 1u))] = key;
+      n += __popc(in);
+    }
+    __syncwarp();
+    for (int c = lane; c < n; c += 32) {
+      const uint64_t key = cand[c];
+      int rank = 0;
+      for (int o = 0; o < n; ++o) rank += cand[o] > key;
+      if (rank < K) {
+        // the logit below the maximum first: exact where both are large
+        score[b * K + rank] = cum + ((static_cast<double>(cand_logit(key)) - static_cast<double>(m)) - log_s);
+        token[b * K + rank] = cand_token(key);
+      }
+    }
+    __syncwarp();
   }
   __syncthreads();
-  for (int c = tid; c < total; c += 256) {
+  int valid = 0;
+  for (int c = tid; c < total; c += kBeamThreads) {
     const double s = score[c];
     if (!(s > -INFINITY)) continue;
-    int rank = 0;
-    for (int o = 0; o < total; ++o) rank += score[o] > s || (score[o] == s && o < c);
-    if (rank >= p.n_out) continue;
-    const int row = g * p.beams + c / p.n_out;
-    const bool ended = p.finished != nullptr && __ldg(p.finished + row) != 0;
-    const size_t at = static_cast<size_t>(g) * p.n_out + rank;
-    p.parents[at] = c / p.n_out;
-    p.tokens[at] = ended ? p.end_token : cand_token(p.cand[static_cast<size_t>(row) * p.n_out + c % p.n_out]);
+    ++valid;
+    const int b = c / K;
+    int rank = c % K;  // the better ones of its own beam
+    for (int o = 0; o < p.beams && rank < K; ++o) {
+      if (o == b) continue;
+      int lo = 0, hi = K;  // those of beam o that come first: better, or as good in a lower beam
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        const double x = score[o * K + mid];
+        if (x > s || (x == s && o < b)) lo = mid + 1;
+        else hi = mid;
+      }
+      rank += lo;
+    }
+    if (rank >= K) continue;
+    const size_t at = static_cast<size_t>(g) * K + rank;
+    p.parents[at] = b;
+    p.tokens[at] = token[c];
     p.out_scores[at] = static_cast<float>(s);
+  }
+  if (valid > 0) atomicAdd(&found, valid);
+  __syncthreads();
+  for (int c = found + tid; c < K; c += kBeamThreads) {
+    p.parents[static_cast<size_t>(g) * K + c] = -1;
+    p.tokens[static_cast<size_t>(g) * K + c] = -1;
+    p.out_scores[static_cast<size_t>(g) * K + c] = -INFINITY;
   }
 }
 
@@ -237,7 +518,25 @@ using pa::fail;
 namespace {
 
 bool beam_sizes_ok(int32_t beams, int32_t vocab, int32_t n_out) {
-  return beams >= 1 && beams <= pa::kMaxBeams && vocab >= 1 && n_out >= 1 && n_out <= pa::kMaxBeamOut;
+  return beams >= 1 && beams <= pa::kMaxBeams && vocab >= 1 && vocab <= pa::kMaxVocab && n_out >= 1 &&
+         n_out <= pa::kMaxBeamOut;
+}
+
+int32_t beam_chunks(int32_t vocab, bool bf16) { return (vocab + pa::beam_chunk(bf16) - 1) / pa::beam_chunk(bf16); }
+
+// The workspace's parts.
+size_t beam_layout(int32_t n_groups, int32_t beams, int32_t n_out, int32_t chunks, void* base, pa::BeamParams* p) {
+  const size_t rows = static_cast<size_t>(n_groups) * beams;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return static_cast<unsigned char*>(base) + at;
+  };
+  p->chunk_keys = reinterpret_cast<uint64_t*>(take(rows * chunks * n_out * sizeof(uint64_t)));
+  p->chunk_sum = reinterpret_cast<float*>(take(rows * chunks * sizeof(float)));
+  p->chunk_max = reinterpret_cast<float*>(take(rows * chunks * sizeof(float)));
+  return off;
 }
 
 }  // namespace
@@ -246,9 +545,8 @@ extern "C" {
 
 size_t pa_beam_workspace_bytes(int32_t n_groups, int32_t beams, int32_t vocab, int32_t n_out) {
   if (n_groups <= 0 || !beam_sizes_ok(beams, vocab, n_out)) return 0;
-  const size_t rows = static_cast<size_t>(n_groups) * beams;
-  const size_t need = rows * n_out * sizeof(uint64_t) + rows * sizeof(double);
-  return (need + 255) / 256 * 256;
+  pa::BeamParams p{};
+  return beam_layout(n_groups, beams, n_out, beam_chunks(vocab, false), nullptr, &p);  // f32 rows have the most chunks
 }
 
 pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const void* logits, pa_dtype logits_dtype,
@@ -258,12 +556,15 @@ pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const v
   if (n_groups < 0) return fail(PA_ERR_INVALID_ARG, "n_groups %d < 0", n_groups);
   if (beams < 1 || vocab < 1 || n_out < 1)
     return fail(PA_ERR_INVALID_ARG, "beams %d, vocab %d and n_out %d must be positive", beams, vocab, n_out);
-  if (beams > pa::kMaxBeams || n_out > pa::kMaxBeamOut)
-    return fail(PA_ERR_UNSUPPORTED, "beams %d > %d or n_out %d > %d", beams, pa::kMaxBeams, n_out, pa::kMaxBeamOut);
+  if (!beam_sizes_ok(beams, vocab, n_out))
+    return fail(PA_ERR_UNSUPPORTED, "beams %d > %d, n_out %d > %d or vocab %d > %d", beams, pa::kMaxBeams, n_out,
+                pa::kMaxBeamOut, vocab, pa::kMaxVocab);
   if (logits_dtype != PA_F32 && logits_dtype != PA_BF16)
     return fail(PA_ERR_INVALID_ARG, "logits dtype must be f32 or bf16");
   if (row_stride < vocab) return fail(PA_ERR_INVALID_ARG, "row stride %lld < vocab %d", (long long)row_stride, vocab);
-  if (static_cast<int64_t>(n_groups) * beams > 0x7fffffff)
+  const bool bf16 = logits_dtype == PA_BF16;
+  const int32_t chunks = beam_chunks(vocab, bf16);
+  if (static_cast<int64_t>(n_groups) * beams * chunks > 0x7fffffff)
     return fail(PA_ERR_UNSUPPORTED, "%d groups of %d beams in one call", n_groups, beams);
   if (n_groups == 0) return PA_OK;
   if (!logits || !scores || !parents || !tokens || !out_scores)
@@ -275,7 +576,7 @@ pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const v
                 workspace == nullptr ? static_cast<size_t>(0) : workspace_bytes);
   if (!aligned(workspace, 256)) return fail(PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   pa::BeamParams p{};
-  const size_t rows = static_cast<size_t>(n_groups) * beams;
+  beam_layout(n_groups, beams, n_out, chunks, workspace, &p);
   p.logits = logits;
   p.row_stride = row_stride;
   p.scores = scores;
@@ -283,24 +584,31 @@ pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const v
   p.parents = parents;
   p.tokens = tokens;
   p.out_scores = out_scores;
-  p.cand = static_cast<uint64_t*>(workspace);
-  p.norm = reinterpret_cast<double*>(p.cand + rows * n_out);
   p.groups = n_groups;
   p.beams = beams;
   p.vocab = vocab;
+  p.chunks = chunks;
   p.n_out = n_out;
   p.end_token = end_token;
+  // candidates of one CTA: 2 n_out threads at most, all their elements
+  const size_t smem = sizeof(uint64_t) * 2 * n_out * (pa::beam_chunk(bf16) / pa::kBeamThreads);
+  const size_t row_bytes = sizeof(uint64_t) * (static_cast<size_t>(chunks) + 2) * n_out;
+  p.merge_warps = static_cast<int32_t>(
+      std::min<size_t>({static_cast<size_t>(pa::kBeamWarps), static_cast<size_t>(beams), pa::kBeamListBytes / row_bytes}));
+  const size_t merge_smem = p.merge_warps * row_bytes + static_cast<size_t>(beams) * n_out * (sizeof(double) + sizeof(int));
+  static std::atomic<unsigned long long> done_f32{0}, done_bf16{0}, done_merge{0};
+  cudaError_t e = bf16 ? pa::allow_dynamic_smem(pa::beam_select_kernel<true>, done_bf16, pa::kBeamMaxSmem)
+                       : pa::allow_dynamic_smem(pa::beam_select_kernel<false>, done_f32, pa::kBeamMaxSmem);
+  if (e == cudaSuccess) e = pa::allow_dynamic_smem(pa::beam_merge_kernel, done_merge, pa::kBeamMaxSmem);
+  if (e != cudaSuccess) return cuda_fail(e, "beam select shared memory");
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(n_groups) * beams * chunks));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (logits_dtype == PA_BF16)
-    pa::beam_row_kernel<true><<<static_cast<unsigned>(rows), pa::kBeamThreads, 0, s>>>(p);
-  else
-    pa::beam_row_kernel<false><<<static_cast<unsigned>(rows), pa::kBeamThreads, 0, s>>>(p);
+  e = bf16 ? pa::launch_kernel(pa::beam_select_kernel<true>, grid, dim3(pa::kBeamThreads), smem, s, false, p)
+           : pa::launch_kernel(pa::beam_select_kernel<false>, grid, dim3(pa::kBeamThreads), smem, s, false, p);
   pa::count_launch();
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "beam select launch");
-  pa::beam_merge_kernel<<<n_groups, 256, sizeof(double) * beams * n_out, s>>>(p);
+  e = pa::launch_kernel(pa::beam_merge_kernel, dim3(n_groups), dim3(pa::kBeamThreads), merge_smem, s, true, p);
   pa::count_launch();
-  e = cudaGetLastError();
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "beam merge launch");
 }
 

@@ -103,7 +103,7 @@ def test_beam_select_refusals(lib):
     for name in ("logits", "scores", "parents", "ws"):
         assert call(**{name: None}) == bad
     assert call(b=0) == bad and call(v=0) == bad and call(out=0) == bad
-    assert call(b=33) == unsupported and call(out=65) == unsupported
+    assert call(b=33) == unsupported and call(out=65) == unsupported and call(v=(1 << 20) + 1, stride=1 << 21) == unsupported
     assert call(dt=pa.PA_FP8_E4M3) == bad
     assert call(stride=99) == bad
     assert call(logits=ctypes.c_void_p(0x100002)) == bad

@@ -16,7 +16,7 @@ def ints(x):
 def select(logits, scores, n_out, finished=None, end_token=0):
     n, b, v = logits.shape
     size = pa.beam_workspace_bytes(n, b, v, n_out)
-    ws = torch.zeros(max(size, 1), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda").fill_(0xA5)  # scratch: any contents
     out = (torch.full((n, n_out), 99, dtype=torch.int32, device="cuda"),
            torch.full((n, n_out), 99, dtype=torch.int32, device="cuda"), torch.full((n, n_out), 99.0, device="cuda"))
     for _ in range(2):  # the workspace serves call after call
@@ -32,7 +32,7 @@ def reference(logits, scores, n_out, finished=None, end_token=0):
     tokens, best = parents.clone(), torch.full((n, n_out), float("-inf"), dtype=torch.float64)
     x, cum = logits.cpu().double(), scores.cpu().double()
     for i in range(n):
-        total = cum[i].view(b, 1) + (x[i] - torch.logsumexp(x[i], dim=1, keepdim=True))
+        total = cum[i].view(b, 1) + torch.log_softmax(x[i], dim=1)
         total[torch.isinf(torch.logsumexp(x[i], dim=1)) | torch.isnan(torch.logsumexp(x[i], dim=1))] = float("-inf")
         total = torch.where(torch.isfinite(total), total, float("-inf"))
         if finished is not None:
@@ -57,7 +57,7 @@ def check(logits, scores, n_out, finished=None, end_token=0):
     assert torch.equal(parents, want_p) and torch.equal(tokens, want_t)
     none = torch.isinf(want_s)
     assert torch.equal(none, torch.isinf(got))
-    # log-sum-exp: FP32 exponentials (a few 2^-22) and partial sums of at most vocab / 256 additions
+    # log-sum-exp: FP32 exponentials (a few 2^-22) and FP32 sums of at most vocab / 256 + 16 additions
     # (2^-24 each); the score is rounded to FP32 once
     bound = (16 + logits.shape[2] / 256) * 2.0 ** -24 * 4 + 2.0 ** -24 * want_s.abs()
     assert ((got.double() - want_s).abs() <= bound)[~none].all()
