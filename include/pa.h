@@ -293,7 +293,7 @@ pa_status pa_evict_compact(const pa_pool *pool, int32_t n, const int32_t *seq_id
  * whose log-sum-exp is not finite (NaN or +infinity among its logits, or
  * nothing but -infinity) or whose score is not finite has none.  Where fewer
  * than n_out exist the rest is parent -1, token -1, score -infinity.
- * Sums of exponentials are FP32 within 32 KB of a row and FP64 across them;
+ * Sums of exponentials are FP32 within 128 KB of a row and FP64 across them;
  * scores are compared in FP64 and rounded once.  A group's results do not depend on the
  * other groups, nor on the alignment of its rows.
  *   workspace   device memory of at least pa_beam_workspace_bytes(...), 256-byte

@@ -21,21 +21,22 @@ struct BeamParams {
   int32_t* parents;
   int32_t* tokens;
   float* out_scores;
-  // workspace, per chunk of a row: its best (logit, token) keys, best first (0: none), its sum of
+  // workspace, per segment of a row: its best (logit, token) keys, best first (0: none), its sum of
   // exponentials and the maximum they are relative to
-  uint64_t* chunk_keys;  // [rows][chunks][n_out]
-  float* chunk_sum;      // [rows][chunks]
-  float* chunk_max;      // [rows][chunks]
-  int32_t groups, beams, vocab, chunks, n_out, end_token;
+  uint64_t* segment_keys;  // [rows][segments][n_out]
+  float* segment_sum;      // [rows][segments]
+  float* segment_max;      // [rows][segments]
+  int32_t groups, beams, vocab, segments, n_out, end_token;
   int32_t merge_warps;  // warps of the merge that have room for a row's keys
 };
 
 constexpr int kBeamThreads = 256;
 constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamVecs = 8;                                        // 16-byte vectors a thread holds
-constexpr int kBeamChunkBytes = kBeamThreads * kBeamVecs * 16;      // of a row, per CTA
+constexpr int kBeamChunkBytes = kBeamThreads * kBeamVecs * 16;      // of a row, held at once
+constexpr int kBeamSegment = 4;                                     // chunks of a CTA's part of a row
 constexpr int kMaxVocab = 1 << 20;
-constexpr size_t kBeamListBytes = 68 * 1024;  // keys the merge holds at once (at least a row: 128 chunks, n_out 64)
+constexpr size_t kBeamListBytes = 32 * 1024;  // keys the merge holds at once (a row has 34 segments at most, n_out 64 of each)
 constexpr size_t kBeamMaxSmem = 96 * 1024;
 
 __host__ __device__ constexpr int beam_chunk(bool bf16) { return kBeamChunkBytes / (bf16 ? 2 : 4); }
@@ -56,20 +57,18 @@ __device__ __forceinline__ float cand_logit(uint64_t key) {
 }
 __device__ __forceinline__ int cand_token(uint64_t key) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)); }
 
-// 16 bytes of a row from any element-aligned address.  A misaligned vector is
-// shifted together from the two aligned ones that hold it, the second read only
+// 16 bytes of a row from an address `off` bytes behind a 16-byte boundary, shifted
+// together from the two aligned vectors that hold them, the second read only
 // where it holds an element of the row (left: the row's bytes from here on), so
 // that no aligned 16 bytes without one is touched.
-__device__ __forceinline__ uint4 load_row_vec(const unsigned char* src, int64_t left) {
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+__device__ __forceinline__ uint4 load_row_vec(const unsigned char* src, int off, int64_t left) {
   const uint4* at = reinterpret_cast<const uint4*>(src - off);
   const uint4 a = __ldcs(at);
-  if (off == 0) return a;
   uint4 b = make_uint4(0u, 0u, 0u, 0u);
   if (left > 16 - off) b = __ldcs(at + 1);
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   const int sh = 8 * (off & 3);
-  uint32_t r[4];
+  uint32_t r[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int s = 0; s < 4; ++s)  // the same word offset for the whole row: a uniform choice
     if (off / 4 == s) {
@@ -138,59 +137,195 @@ __device__ __forceinline__ uint64_t bound_keys(const uint64_t* list, int n, int 
   return lo;
 }
 
-// One CTA per 32 KB of a row, held in registers from one read: its maximum and
-// sum of exponentials, and its n_out best.  The n_out-th best of the CTA is at
-// least the n_out-th best of the threads' bests; a value that n_out of those
-// reach (and at most twice as many) is found by bisection, only threads whose
-// best reaches it look for candidates again, and what they find is ranked by
-// counting.  Where more threads' bests are equal, the lowest tokens among them
-// set the bound.
+// One CTA per segment of a row (four chunks of 32 KB).  A chunk is held in
+// registers from one read, while the next one's loads are in flight.
+//   * log-sum-exp: every thread keeps its own maximum and sum; they meet once, at
+//     the segment's end.
+//   * the n_out best: only threads whose largest logit of the chunk beats the
+//     n_out-th best so far look for candidates.  Where those are more than
+//     2 n_out (the first chunk, or an ascending row), a value that n_out of the
+//     threads' bests reach, and at most twice as many, bounds them first: the n_out-th
+//     best of the chunk is at least that.  It is found by bisection; among equal
+//     bests the lowest tokens set it.  Candidates are ranked by counting.
 //
-// Bound by the one read of the logits: about eight instructions an element
+// Bound by the one read of the logits: about six instructions an element
 // (maximum, subtraction, multiplication, ex2, addition; packed in pairs).
 template <bool BF16>
-__global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const __grid_constant__ BeamParams p) {
+__global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const __grid_constant__ BeamParams p) {
   constexpr int V = BF16 ? 8 : 4;  // elements of a vector
   constexpr int ELT = BF16 ? 2 : 4;
   constexpr int CHUNK = beam_chunk(BF16);
   constexpr int PER = kBeamThreads / 32;
-  extern __shared__ uint64_t list[];
+  constexpr float kLog2e = 1.4426950408889634f;
+  extern __shared__ uint64_t list[];  // the best so far and a chunk's candidates, then [n_out] for their ranking
   __shared__ float red_sum[kBeamWarps], red_max[kBeamWarps];
   __shared__ uint32_t best_order[kBeamThreads];
   __shared__ int best_token[kBeamThreads];
   __shared__ uint32_t bound_order;
   __shared__ int bound_need, bound_token, found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  const int row = blockIdx.x / p.segments, segment = blockIdx.x % p.segments;
   const int K = p.n_out;
   if (p.finished != nullptr && __ldg(p.finished + row) != 0) return;  // its logits do not matter
-  const int base = chunk * CHUNK;  // the CTA's first token
-  const unsigned char* src =
-      static_cast<const unsigned char*>(p.logits) + (static_cast<size_t>(row) * p.row_stride + base) * ELT;
-  const int n = min(CHUNK, p.vocab - base);
-  uint4 v[kBeamVecs];
-  if (n == CHUNK) {
+  uint64_t* ranked = list + K + 2 * K * (CHUNK / kBeamThreads);
+  const unsigned char* src = static_cast<const unsigned char*>(p.logits) + static_cast<size_t>(row) * p.row_stride * ELT;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+  // A whole chunk of an aligned row (the common case) as eight plain loads: one uniform branch for all of
+  // them, so that none waits for another.
+  auto load = [&](int base, uint4(&v)[kBeamVecs]) {
+    const int n = p.vocab - base;
+    const unsigned char* at = src + static_cast<size_t>(base + tid * V) * ELT;
+    if (off == 0 && n >= CHUNK) {
 #pragma unroll
-    for (int i = 0; i < kBeamVecs; ++i) {
-      const int e0 = (i * kBeamThreads + tid) * V;
-      v[i] = load_row_vec(src + static_cast<size_t>(e0) * ELT, static_cast<int64_t>(n - e0) * ELT);
-    }
-  } else {
+      for (int i = 0; i < kBeamVecs; ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(at + i * kBeamThreads * 16));
+    } else {
 #pragma unroll
-    for (int i = 0; i < kBeamVecs; ++i) {
-      const int e0 = (i * kBeamThreads + tid) * V;
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (e0 < n) v[i] = load_row_vec(src + static_cast<size_t>(e0) * ELT, static_cast<int64_t>(n - e0) * ELT);
-      if (e0 + V > n) v[i] = cut_vec<BF16>(v[i], n - e0);
+      for (int i = 0; i < kBeamVecs; ++i) {
+        const int e0 = (i * kBeamThreads + tid) * V;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (e0 < n) v[i] = load_row_vec(at + i * kBeamThreads * 16, off, static_cast<int64_t>(n - e0) * ELT);
+        if (e0 + V > n) v[i] = cut_vec<BF16>(v[i], n - e0);
+      }
     }
-  }
-  griddep_launch_dependents();  // the merge may be launched; it waits for all of this
+  };
+  const int begin = segment * kBeamSegment * CHUNK, end = min(p.vocab, begin + kBeamSegment * CHUNK);
+  uint4 v[kBeamVecs], next[kBeamVecs];
+  load(begin, v);
   if (tid == 0) found = 0;
-  float top = -INFINITY;
+  float run_max = -INFINITY, run_sum = 0.0f;  // this thread's, over the segment
+  int held = 0;                               // entries of the list, sorted: the best so far
+  float least = -INFINITY;                    // the n_out-th of them, once there are as many
+  for (int base = begin; base < end; base += CHUNK) {
+    if (base + CHUNK < end) load(base + CHUNK, next);
+    else griddep_launch_dependents();  // the merge may be launched; it waits for all of this
+    float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kBeamVecs; ++i) top = fmaxf(top, vec_max<BF16>(v[i]));
-  best_order[tid] = logit_order(top);
-  float m = top;
+    for (int i = 0; i < kBeamVecs; ++i) top = fmaxf(top, vec_max<BF16>(v[i]));
+    best_order[tid] = logit_order(top);
+    const int many = __syncthreads_count(top > least);
+    // a candidate is above `bv`, or equal to it with a token of at most `bt` in the chunk
+    float bv = least;
+    int bt = -1;
+    if (many > 2 * K) {
+      if (warp == 0) {
+        uint32_t o[PER], most = 0u;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          o[i] = best_order[i * 32 + lane];
+          most = max(most, o[i]);
+        }
+        auto reach = [&](uint32_t bound) {
+          int c = 0;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) c += o[i] >= bound;
+          return static_cast<int>(__reduce_add_sync(0xffffffffu, c));
+        };
+        uint32_t lo = logit_order(least) + 1u, hi = __reduce_max_sync(0xffffffffu, most) + 1u;
+        int at_lo = many;  // reach(lo) >= K > reach(hi) all along
+        if (K <= 32) {
+          // every lane has a best that reaches the smallest of the lanes' largest
+          const uint32_t first = __reduce_min_sync(0xffffffffu, most);
+          if (first > lo) at_lo = reach(lo = first);
+        }
+        while (at_lo > 2 * K && hi - lo > 1u) {
+          const uint32_t mid = lo + (hi - lo) / 2;
+          const int c = reach(mid);
+          if (c >= K) lo = mid, at_lo = c;
+          else hi = mid;
+        }
+        const int above = at_lo > 2 * K ? reach(lo + 1u) : K;
+        if (lane == 0) {
+          bound_order = lo;
+          bound_need = K - above;  // of the equal bests: so many, those with the lowest tokens (0: all)
+        }
+      }
+      __syncthreads();
+      const uint32_t bo = bound_order;
+      bv = cand_logit(static_cast<uint64_t>(bo) << 32);
+      bt = CHUNK;
+      if (bo <= 0x00800000u) bv = -3.402823466e38f;  // below every finite logit's key: all of them
+      if (bound_need > 0) {
+        int first = CHUNK;  // this thread's first token of exactly the bound
+        if (logit_order(top) == bo) {
+#pragma unroll
+          for (int i = kBeamVecs - 1; i >= 0; --i)
+#pragma unroll
+            for (int e = V - 1; e >= 0; --e)
+              if (vec_logit<BF16>(v[i], e) == bv) first = (i * kBeamThreads + tid) * V + e;
+        }
+        best_token[tid] = first;
+        __syncthreads();
+        if (warp == 0) {
+          int t[PER];
+#pragma unroll
+          for (int i = 0; i < PER; ++i) t[i] = best_token[i * 32 + lane];
+          int a = 0, b = CHUNK - 1;
+          while (a < b) {
+            const int mid = (a + b) / 2;
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) c += t[i] <= mid;
+            if (static_cast<int>(__reduce_add_sync(0xffffffffu, c)) >= bound_need) b = mid;
+            else a = mid + 1;
+          }
+          if (lane == 0) bound_token = a;
+        }
+        __syncthreads();
+        bt = bound_token;
+      }
+    }
+    // at most 2 n_out threads find anything: the list has room for all that they hold
+    if (many > 0 && (top > bv || (top == bv && bt >= 0))) {
+#pragma unroll
+      for (int i = 0; i < kBeamVecs; ++i) {
+        if (!(vec_max<BF16>(v[i]) >= bv)) continue;
+        const int e0 = (i * kBeamThreads + tid) * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float x = vec_logit<BF16>(v[i], e);
+          if (x > bv || (x == bv && e0 + e <= bt)) list[atomicAdd(&found, 1)] = cand_key(logit_order(x), base + e0 + e);
+        }
+      }
+    }
+    // the exponentials against the thread's maximum (0 where it holds none, so that a NaN still shows)
+    {
+      const float m = fmaxf(run_max, top), ref = m == -INFINITY ? 0.0f : m;
+      if (m > run_max) {
+        run_sum = __fmul_rn(run_sum, ex2(__fmul_rn(__fsub_rn(run_max, m), kLog2e)));
+        run_max = m;
+      }
+      float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < kBeamVecs; ++i)
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float2 d = __fadd2_rn(make_float2(vec_logit<BF16>(v[i], e), vec_logit<BF16>(v[i], e + 1)), make_float2(-ref, -ref));
+          const float2 t = __fmul2_rn(d, make_float2(kLog2e, kLog2e));
+          part = __fadd2_rn(part, make_float2(ex2(t.x), ex2(t.y)));
+        }
+      run_sum = __fadd_rn(run_sum, __fadd_rn(part.x, part.y));
+    }
+    if (many > 0) {
+      __syncthreads();
+      const int total = found;
+      for (int c = tid; c < total; c += kBeamThreads) {
+        const uint64_t key = list[c];
+        int rank = 0;
+        for (int o = 0; o < total; ++o) rank += list[o] > key;
+        if (rank < K) ranked[rank] = key;
+      }
+      __syncthreads();
+      held = min(total, K);
+      for (int c = tid; c < held; c += kBeamThreads) list[c] = ranked[c];
+      if (tid == 0) found = held;
+      if (held == K) least = cand_logit(ranked[K - 1]);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kBeamVecs; ++i) v[i] = next[i];
+  }
+  // the segment's maximum and sum
+  float m = run_max;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   if (lane == 0) red_max[warp] = m;
@@ -198,134 +333,37 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const __gr
   m = red_max[0];
 #pragma unroll
   for (int w = 1; w < kBeamWarps; ++w) m = fmaxf(m, red_max[w]);
-  if (warp == 0) {
-    uint32_t o[PER], most = 0u;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      o[i] = best_order[i * 32 + lane];
-      most = max(most, o[i]);
-    }
-    auto reach = [&](uint32_t bound) {
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) c += o[i] >= bound;
-      return static_cast<int>(__reduce_add_sync(0xffffffffu, c));
-    };
-    // every lane has a best that reaches the smallest of the lanes' largest: a first bound for K <= 32
-    uint32_t lo = max(1u, K <= 32 ? __reduce_min_sync(0xffffffffu, most) : 1u), hi = logit_order(m) + 1u;
-    int at_lo = reach(lo), need = 0;
-    if (at_lo < K) at_lo = reach(lo = 1u);
-    if (at_lo >= K) {
-      while (at_lo > 2 * K && hi - lo > 1u) {  // reach(lo) >= K > reach(hi)
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const int c = reach(mid);
-        if (c >= K) lo = mid, at_lo = c;
-        else hi = mid;
-      }
-      if (at_lo > 2 * K) need = K - reach(lo + 1u);  // equal bests: so many of them, those with the lowest tokens
-    }
-    if (lane == 0) {
-      bound_order = lo;
-      bound_need = need;
-      bound_token = 0x7fffffff;
-    }
-  }
-  // the exponentials against the chunk's maximum (0 where it holds none, so that a NaN still shows)
-  const float ref = m == -INFINITY ? 0.0f : m;
-  constexpr float kLog2e = 1.4426950408889634f;
-  float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int i = 0; i < kBeamVecs; ++i)
-#pragma unroll
-    for (int e = 0; e < V; e += 2) {
-      const float2 d = __fadd2_rn(make_float2(vec_logit<BF16>(v[i], e), vec_logit<BF16>(v[i], e + 1)), make_float2(-ref, -ref));
-      const float2 t = __fmul2_rn(d, make_float2(kLog2e, kLog2e));
-      part = __fadd2_rn(part, make_float2(ex2(t.x), ex2(t.y)));
-    }
-  float sum = __fadd_rn(part.x, part.y);
+  float sum = run_max == m ? run_sum : __fmul_rn(run_sum, ex2(__fmul_rn(__fsub_rn(run_max, m), kLog2e)));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));
   if (lane == 0) red_sum[warp] = sum;
   __syncthreads();
-  const uint32_t bo = bound_order;
-  const float bv = bo <= 0x00800000u ? -3.402823466e38f : cand_logit(static_cast<uint64_t>(bo) << 32);  // as a logit
-  if (bound_need > 0) {
-    // the whole CTA: each thread's first token of exactly the bound, then the bound_need-th lowest of them
-    int first = 0x7fffffff;
-    if (logit_order(top) == bo) {
-#pragma unroll
-      for (int i = kBeamVecs - 1; i >= 0; --i)
-#pragma unroll
-        for (int e = V - 1; e >= 0; --e)
-          if (vec_logit<BF16>(v[i], e) == bv) first = (i * kBeamThreads + tid) * V + e;
-    }
-    best_token[tid] = first;
-    __syncthreads();
-    if (warp == 0) {
-      int t[PER];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) t[i] = best_token[i * 32 + lane];
-      int a = 0, b = CHUNK - 1;
-      while (a < b) {
-        const int mid = (a + b) / 2;
-        int c = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) c += t[i] <= mid;
-        if (static_cast<int>(__reduce_add_sync(0xffffffffu, c)) >= bound_need) b = mid;
-        else a = mid + 1;
-      }
-      if (lane == 0) bound_token = a;
-    }
-    __syncthreads();
-  }
-  // at most 2 n_out threads get here: `list` has room for all that they hold
-  const int bt = bound_token;
-  if (top > bv || top == bv) {
-#pragma unroll
-    for (int i = 0; i < kBeamVecs; ++i) {
-      if (!(vec_max<BF16>(v[i]) >= bv)) continue;
-      const int e0 = (i * kBeamThreads + tid) * V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float x = vec_logit<BF16>(v[i], e);
-        if (x > bv || (x == bv && e0 + e <= bt)) list[atomicAdd(&found, 1)] = cand_key(logit_order(x), base + e0 + e);
-      }
-    }
-  }
-  __syncthreads();
-  const int total = found;
-  uint64_t* out = p.chunk_keys + (static_cast<size_t>(row) * p.chunks + chunk) * K;
-  for (int c = tid; c < total; c += kBeamThreads) {
-    const uint64_t key = list[c];
-    int rank = 0;
-    for (int o = 0; o < total; ++o) rank += list[o] > key;
-    if (rank < K) out[rank] = key;
-  }
-  for (int c = total + tid; c < K; c += kBeamThreads) out[c] = 0ull;
+  const size_t at = static_cast<size_t>(row) * p.segments + segment;
   if (tid == 0) {
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kBeamWarps; w += 2) s = __fadd_rn(s, __fadd_rn(red_sum[w], red_sum[w + 1]));
-    p.chunk_sum[static_cast<size_t>(row) * p.chunks + chunk] = s;
-    p.chunk_max[static_cast<size_t>(row) * p.chunks + chunk] = ref;
+    p.segment_sum[at] = s;
+    p.segment_max[at] = m == -INFINITY ? 0.0f : m;
   }
+  for (int c = tid; c < K; c += kBeamThreads) p.segment_keys[at * K + c] = c < held ? list[c] : 0ull;
 }
 
-// One CTA per group.  A warp takes a row: the log-sum-exp over its chunks, and
-// its n_out best out of the chunks' lists (a bound, then ranks by counting what
+// One CTA per group.  A warp takes a row: the log-sum-exp over its segments,
+// and its n_out best out of their lists (a bound, then ranks by counting what
 // reaches it).  Then the beams' candidates by score in 64 bits: each beam's
 // descend, so a candidate's rank is a sum of binary searches.
 __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_constant__ BeamParams p) {
-  extern __shared__ uint64_t list[];  // a warp each: [chunks][n_out] keys, [2 n_out] candidates; then the scores
+  extern __shared__ uint64_t list[];  // a warp each: [segments][n_out] keys, [2 n_out] candidates; then the scores
   __shared__ int found;
   const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int K = p.n_out, per_row = p.chunks * K, total = p.beams * K;
+  const int K = p.n_out, per_row = p.segments * K, total = p.beams * K;
   uint64_t* keys = list + static_cast<size_t>(warp) * (per_row + 2 * K);
   uint64_t* cand = keys + per_row;
   double* score = reinterpret_cast<double*>(list + static_cast<size_t>(p.merge_warps) * (per_row + 2 * K));  // [beams][n_out]
   int* token = reinterpret_cast<int*>(score + total);
   if (tid == 0) found = 0;
-  griddep_wait();  // the chunks' results
+  griddep_wait();  // the segments' results
   for (int b = warp; b < p.beams && warp < p.merge_warps; b += p.merge_warps) {
     const size_t row = static_cast<size_t>(g) * p.beams + b;
     const double cum = __ldg(p.scores + row);
@@ -338,18 +376,18 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_c
       }
       continue;
     }
-    const uint64_t* from = p.chunk_keys + row * per_row;
-    uint64_t most = 0ull, least = 0ull;  // the largest key, and the largest n_out-th of a chunk
+    const uint64_t* from = p.segment_keys + row * per_row;
+    uint64_t most = 0ull, least = 0ull;  // the largest key, and the largest n_out-th of a segment
     for (int c = lane; c < per_row; c += 32) {
       const uint64_t key = __ldcg(from + c);
       keys[c] = key;
       most = key > most ? key : most;
       if (c % K == K - 1 && key > least) least = key;
     }
-    const float* cs = p.chunk_sum + row * p.chunks;
-    const float* cm = p.chunk_max + row * p.chunks;
+    const float* cs = p.segment_sum + row * p.segments;
+    const float* cm = p.segment_max + row * p.segments;
     float m = -INFINITY;
-    for (int j = lane; j < p.chunks; j += 32)
+    for (int j = lane; j < p.segments; j += 32)
       if (__ldcg(cs + j) != 0.0f) m = fmaxf(m, __ldcg(cm + j));  // NaN sums among them
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -359,7 +397,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_c
       least = z > least ? z : least;
     }
     double s = 0.0;
-    for (int j = lane; j < p.chunks; j += 32) {
+    for (int j = lane; j < p.segments; j += 32) {
       const float c = __ldcg(cs + j);
       if (c != 0.0f) s += static_cast<double>(c) * static_cast<double>(expf(__fsub_rn(__ldcg(cm + j), m)));
     }
@@ -522,10 +560,13 @@ bool beam_sizes_ok(int32_t beams, int32_t vocab, int32_t n_out) {
          n_out <= pa::kMaxBeamOut;
 }
 
-int32_t beam_chunks(int32_t vocab, bool bf16) { return (vocab + pa::beam_chunk(bf16) - 1) / pa::beam_chunk(bf16); }
+int32_t beam_segments(int32_t vocab, bool bf16) {
+  const int segment = pa::kBeamSegment * pa::beam_chunk(bf16);
+  return (vocab + segment - 1) / segment;
+}
 
 // The workspace's parts.
-size_t beam_layout(int32_t n_groups, int32_t beams, int32_t n_out, int32_t chunks, void* base, pa::BeamParams* p) {
+size_t beam_layout(int32_t n_groups, int32_t beams, int32_t n_out, int32_t segments, void* base, pa::BeamParams* p) {
   const size_t rows = static_cast<size_t>(n_groups) * beams;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -533,9 +574,9 @@ size_t beam_layout(int32_t n_groups, int32_t beams, int32_t n_out, int32_t chunk
     off += (bytes + 255) / 256 * 256;
     return static_cast<unsigned char*>(base) + at;
   };
-  p->chunk_keys = reinterpret_cast<uint64_t*>(take(rows * chunks * n_out * sizeof(uint64_t)));
-  p->chunk_sum = reinterpret_cast<float*>(take(rows * chunks * sizeof(float)));
-  p->chunk_max = reinterpret_cast<float*>(take(rows * chunks * sizeof(float)));
+  p->segment_keys = reinterpret_cast<uint64_t*>(take(rows * segments * n_out * sizeof(uint64_t)));
+  p->segment_sum = reinterpret_cast<float*>(take(rows * segments * sizeof(float)));
+  p->segment_max = reinterpret_cast<float*>(take(rows * segments * sizeof(float)));
   return off;
 }
 
@@ -546,7 +587,7 @@ extern "C" {
 size_t pa_beam_workspace_bytes(int32_t n_groups, int32_t beams, int32_t vocab, int32_t n_out) {
   if (n_groups <= 0 || !beam_sizes_ok(beams, vocab, n_out)) return 0;
   pa::BeamParams p{};
-  return beam_layout(n_groups, beams, n_out, beam_chunks(vocab, false), nullptr, &p);  // f32 rows have the most chunks
+  return beam_layout(n_groups, beams, n_out, beam_segments(vocab, false), nullptr, &p);  // f32 rows have the most segments
 }
 
 pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const void* logits, pa_dtype logits_dtype,
@@ -563,8 +604,8 @@ pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const v
     return fail(PA_ERR_INVALID_ARG, "logits dtype must be f32 or bf16");
   if (row_stride < vocab) return fail(PA_ERR_INVALID_ARG, "row stride %lld < vocab %d", (long long)row_stride, vocab);
   const bool bf16 = logits_dtype == PA_BF16;
-  const int32_t chunks = beam_chunks(vocab, bf16);
-  if (static_cast<int64_t>(n_groups) * beams * chunks > 0x7fffffff)
+  const int32_t segments = beam_segments(vocab, bf16);
+  if (static_cast<int64_t>(n_groups) * beams * segments > 0x7fffffff)
     return fail(PA_ERR_UNSUPPORTED, "%d groups of %d beams in one call", n_groups, beams);
   if (n_groups == 0) return PA_OK;
   if (!logits || !scores || !parents || !tokens || !out_scores)
@@ -576,7 +617,7 @@ pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const v
                 workspace == nullptr ? static_cast<size_t>(0) : workspace_bytes);
   if (!aligned(workspace, 256)) return fail(PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   pa::BeamParams p{};
-  beam_layout(n_groups, beams, n_out, chunks, workspace, &p);
+  beam_layout(n_groups, beams, n_out, segments, workspace, &p);
   p.logits = logits;
   p.row_stride = row_stride;
   p.scores = scores;
@@ -587,12 +628,12 @@ pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const v
   p.groups = n_groups;
   p.beams = beams;
   p.vocab = vocab;
-  p.chunks = chunks;
+  p.segments = segments;
   p.n_out = n_out;
   p.end_token = end_token;
-  // candidates of one CTA: 2 n_out threads at most, all their elements
-  const size_t smem = sizeof(uint64_t) * 2 * n_out * (pa::beam_chunk(bf16) / pa::kBeamThreads);
-  const size_t row_bytes = sizeof(uint64_t) * (static_cast<size_t>(chunks) + 2) * n_out;
+  // the best so far (twice) and a chunk's candidates: 2 n_out threads at most, all their elements
+  const size_t smem = sizeof(uint64_t) * n_out * (2 + 2 * (pa::beam_chunk(bf16) / pa::kBeamThreads));
+  const size_t row_bytes = sizeof(uint64_t) * (static_cast<size_t>(segments) + 2) * n_out;
   p.merge_warps = static_cast<int32_t>(
       std::min<size_t>({static_cast<size_t>(pa::kBeamWarps), static_cast<size_t>(beams), pa::kBeamListBytes / row_bytes}));
   const size_t merge_smem = p.merge_warps * row_bytes + static_cast<size_t>(beams) * n_out * (sizeof(double) + sizeof(int));
@@ -601,7 +642,7 @@ pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const v
                        : pa::allow_dynamic_smem(pa::beam_select_kernel<false>, done_f32, pa::kBeamMaxSmem);
   if (e == cudaSuccess) e = pa::allow_dynamic_smem(pa::beam_merge_kernel, done_merge, pa::kBeamMaxSmem);
   if (e != cudaSuccess) return cuda_fail(e, "beam select shared memory");
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(n_groups) * beams * chunks));
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(n_groups) * beams * segments));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   e = bf16 ? pa::launch_kernel(pa::beam_select_kernel<true>, grid, dim3(pa::kBeamThreads), smem, s, false, p)
            : pa::launch_kernel(pa::beam_select_kernel<false>, grid, dim3(pa::kBeamThreads), smem, s, false, p);
