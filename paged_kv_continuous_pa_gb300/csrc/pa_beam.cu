@@ -36,7 +36,8 @@ constexpr int kBeamVecs = 8;                                        // 16-byte v
 constexpr int kBeamChunkBytes = kBeamThreads * kBeamVecs * 16;      // of a row, held at once
 constexpr int kBeamSegment = 4;                                     // chunks of a CTA's part of a row
 constexpr int kMaxVocab = 1 << 20;
-constexpr size_t kBeamListBytes = 32 * 1024;  // keys the merge holds at once (a row has 34 segments at most, n_out 64 of each)
+static_assert(kMaxVocab <= 32 * kBeamSegment * kBeamChunkBytes / 4, "a row has at most 32 segments");
+constexpr size_t kBeamListBytes = 32 * 1024;  // keys the merge holds at once (a row has 32 segments at most, n_out 64 of each)
 constexpr size_t kBeamMaxSmem = 96 * 1024;
 
 __host__ __device__ constexpr int beam_chunk(bool bf16) { return kBeamChunkBytes / (bf16 ? 2 : 4); }
@@ -138,7 +139,7 @@ __device__ __forceinline__ uint64_t bound_keys(const uint64_t* list, int n, int 
 }
 
 // One CTA per segment of a row (four chunks of 32 KB).  A chunk is held in
-// registers from one read, while the next one's loads are in flight.
+// registers from one read; the SM's other CTAs compute while it arrives.
 //   * log-sum-exp: every thread keeps its own maximum and sum; they meet once, at
 //     the segment's end.
 //   * the n_out best: only threads whose largest logit of the chunk beats the
@@ -151,7 +152,7 @@ __device__ __forceinline__ uint64_t bound_keys(const uint64_t* list, int n, int 
 // Bound by the one read of the logits: about six instructions an element
 // (maximum, subtraction, multiplication, ex2, addition; packed in pairs).
 template <bool BF16>
-__global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const __grid_constant__ BeamParams p) {
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const __grid_constant__ BeamParams p) {
   constexpr int V = BF16 ? 8 : 4;  // elements of a vector
   constexpr int ELT = BF16 ? 2 : 4;
   constexpr int CHUNK = beam_chunk(BF16);
@@ -189,15 +190,14 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const __gr
     }
   };
   const int begin = segment * kBeamSegment * CHUNK, end = min(p.vocab, begin + kBeamSegment * CHUNK);
-  uint4 v[kBeamVecs], next[kBeamVecs];
-  load(begin, v);
+  uint4 v[kBeamVecs];
   if (tid == 0) found = 0;
   float run_max = -INFINITY, run_sum = 0.0f;  // this thread's, over the segment
   int held = 0;                               // entries of the list, sorted: the best so far
   float least = -INFINITY;                    // the n_out-th of them, once there are as many
   for (int base = begin; base < end; base += CHUNK) {
-    if (base + CHUNK < end) load(base + CHUNK, next);
-    else griddep_launch_dependents();  // the merge may be launched; it waits for all of this
+    load(base, v);
+    if (base + CHUNK >= end) griddep_launch_dependents();  // the merge may be launched; it waits for all of this
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kBeamVecs; ++i) top = fmaxf(top, vec_max<BF16>(v[i]));
@@ -321,8 +321,6 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const __gr
       if (held == K) least = cand_logit(ranked[K - 1]);
       __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < kBeamVecs; ++i) v[i] = next[i];
   }
   // the segment's maximum and sum
   float m = run_max;
@@ -349,6 +347,15 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const __gr
   for (int c = tid; c < K; c += kBeamThreads) p.segment_keys[at * K + c] = c < held ? list[c] : 0ull;
 }
 
+// A score (finite) as an integer of the same order, above 0.
+__device__ __forceinline__ uint64_t score_key(double s) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(s == 0.0 ? 0.0 : s));
+  return (u >> 63) ? ~u : (u | (1ull << 63));
+}
+__device__ __forceinline__ double score_of(uint64_t key) {
+  return __longlong_as_double(static_cast<long long>((key >> 63) ? (key & ~(1ull << 63)) : ~key));
+}
+
 // One CTA per group.  A warp takes a row: the log-sum-exp over its segments,
 // and its n_out best out of their lists (a bound, then ranks by counting what
 // reaches it).  Then the beams' candidates by score in 64 bits: each beam's
@@ -360,35 +367,36 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_c
   const int K = p.n_out, per_row = p.segments * K, total = p.beams * K;
   uint64_t* keys = list + static_cast<size_t>(warp) * (per_row + 2 * K);
   uint64_t* cand = keys + per_row;
-  double* score = reinterpret_cast<double*>(list + static_cast<size_t>(p.merge_warps) * (per_row + 2 * K));  // [beams][n_out]
+  uint64_t* score = list + static_cast<size_t>(p.merge_warps) * (per_row + 2 * K);  // [beams][n_out] score keys, 0: none
   int* token = reinterpret_cast<int*>(score + total);
   if (tid == 0) found = 0;
-  griddep_wait();  // the segments' results
+  bool waited = false;
   for (int b = warp; b < p.beams && warp < p.merge_warps; b += p.merge_warps) {
     const size_t row = static_cast<size_t>(g) * p.beams + b;
     const double cum = __ldg(p.scores + row);
-    for (int k = lane; k < K; k += 32) score[b * K + k] = -INFINITY;
+    const bool ended = p.finished != nullptr && __ldg(p.finished + row) != 0;
+    for (int k = lane; k < K; k += 32) score[b * K + k] = 0ull;
     __syncwarp();
-    if (p.finished != nullptr && __ldg(p.finished + row) != 0) {
+    if (!waited) griddep_wait();  // the segments' results
+    waited = true;
+    if (ended) {
       if (lane == 0) {
-        if (isfinite(cum)) score[b * K] = cum;
+        if (isfinite(cum)) score[b * K] = score_key(cum);
         token[b * K] = p.end_token;
       }
       continue;
     }
     const uint64_t* from = p.segment_keys + row * per_row;
-    uint64_t most = 0ull, least = 0ull;  // the largest key, and the largest n_out-th of a segment
-    for (int c = lane; c < per_row; c += 32) {
-      const uint64_t key = __ldcg(from + c);
-      keys[c] = key;
-      most = key > most ? key : most;
-      if (c % K == K - 1 && key > least) least = key;
-    }
     const float* cs = p.segment_sum + row * p.segments;
     const float* cm = p.segment_max + row * p.segments;
-    float m = -INFINITY;
-    for (int j = lane; j < p.segments; j += 32)
-      if (__ldcg(cs + j) != 0.0f) m = fmaxf(m, __ldcg(cm + j));  // NaN sums among them
+    // a row has at most 32 segments: one to a lane
+    const float part = lane < p.segments ? __ldcg(cs + lane) : 0.0f;
+    const float ref = lane < p.segments ? __ldcg(cm + lane) : 0.0f;
+    for (int c = lane; c < per_row; c += 32) keys[c] = __ldcg(from + c);
+    __syncwarp();
+    uint64_t most = lane < p.segments ? keys[lane * K] : 0ull;           // the best of all
+    uint64_t least = lane < p.segments ? keys[lane * K + K - 1] : 0ull;  // the largest n_out-th of a segment
+    float m = part != 0.0f ? ref : -INFINITY;                            // NaN sums among them
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -396,15 +404,10 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_c
       most = a > most ? a : most;
       least = z > least ? z : least;
     }
-    double s = 0.0;
-    for (int j = lane; j < p.segments; j += 32) {
-      const float c = __ldcg(cs + j);
-      if (c != 0.0f) s += static_cast<double>(c) * static_cast<double>(expf(__fsub_rn(__ldcg(cm + j), m)));
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    double s = part != 0.0f ? static_cast<double>(part) * static_cast<double>(expf(__fsub_rn(ref, m))) : 0.0;
+    for (int off = 1; off < p.segments; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    s = __shfl_sync(0xffffffffu, s, 0);
     const double log_s = log(s);
-    __syncwarp();
     if (!isfinite(m) || !isfinite(log_s) || !isfinite(cum) || most == 0ull) continue;
     const uint64_t bound = bound_keys(keys, per_row, K, least > 0ull ? least : 1ull, most + 1ull, lane);
     int n = 0;
@@ -418,40 +421,41 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_c
     for (int c = lane; c < n; c += 32) {
       const uint64_t key = cand[c];
       int rank = 0;
+#pragma unroll 4
       for (int o = 0; o < n; ++o) rank += cand[o] > key;
       if (rank < K) {
         // the logit below the maximum first: exact where both are large
-        score[b * K + rank] = cum + ((static_cast<double>(cand_logit(key)) - static_cast<double>(m)) - log_s);
+        score[b * K + rank] = score_key(cum + ((static_cast<double>(cand_logit(key)) - static_cast<double>(m)) - log_s));
         token[b * K + rank] = cand_token(key);
       }
     }
     __syncwarp();
   }
   __syncthreads();
-  int valid = 0;
-  for (int c = tid; c < total; c += kBeamThreads) {
-    const double s = score[c];
-    if (!(s > -INFINITY)) continue;
-    ++valid;
-    const int b = c / K;
-    int rank = c % K;  // the better ones of its own beam
-    for (int o = 0; o < p.beams && rank < K; ++o) {
-      if (o == b) continue;
-      int lo = 0, hi = K;  // those of beam o that come first: better, or as good in a lower beam
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        const double x = score[o * K + mid];
-        if (x > s || (x == s && o < b)) lo = mid + 1;
-        else hi = mid;
+  int valid = 0, top_step = 1;
+  while (2 * top_step <= K) top_step *= 2;
+  for (int b = warp; b < p.beams; b += kBeamWarps)
+    for (int k = lane; k < K; k += 32) {
+      const uint64_t s = score[b * K + k];
+      if (s == 0ull) continue;
+      ++valid;
+      int rank = k;  // the better ones of its own beam
+#pragma unroll 4
+      for (int o = 0; o < p.beams; ++o) {
+        // those of beam o that come first: better, or as good in a lower beam
+        const uint64_t* other = score + o * K;
+        const uint64_t edge = s + (o < b ? 0ull : 1ull);
+        int at = 0;
+        for (int step = top_step; step > 0; step >>= 1)
+          if (at + step <= K && other[at + step - 1] >= edge) at += step;
+        rank += o == b ? 0 : at;
       }
-      rank += lo;
+      if (rank >= K) continue;
+      const size_t at = static_cast<size_t>(g) * K + rank;
+      p.parents[at] = b;
+      p.tokens[at] = token[b * K + k];
+      p.out_scores[at] = static_cast<float>(score_of(s));
     }
-    if (rank >= K) continue;
-    const size_t at = static_cast<size_t>(g) * K + rank;
-    p.parents[at] = b;
-    p.tokens[at] = token[c];
-    p.out_scores[at] = static_cast<float>(s);
-  }
   if (valid > 0) atomicAdd(&found, valid);
   __syncthreads();
   for (int c = found + tid; c < K; c += kBeamThreads) {
