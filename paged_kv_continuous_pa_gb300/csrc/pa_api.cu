@@ -50,6 +50,7 @@ namespace {
 using pa::aligned;
 using pa::cuda_fail;
 using pa::elt_bytes;
+using pa::encode_tile_maps;
 using pa::fail;
 
 int max_splits_for(const pa_pool_desc& d, int32_t max_blocks, int32_t split_tokens) {
@@ -182,16 +183,6 @@ pa_status encode_map_pair(pa_pool* pool, CUtensorMap* km, CUtensorMap* vm, uint3
   return PA_OK;
 }
 
-// bf16 pools, prefill tiles: 64 elements x min(P, 64) rows (half or all of the head dim).
-pa_status encode_tile_maps(pa_pool* pool) {
-  if (pool->tile_maps_ready) return PA_OK;
-  if (pool->desc.kv_dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "the tile path reads bf16 pools");
-  const int P = pool->desc.page_size;
-  const pa_status st = encode_map_pair(pool, &pool->kmap, &pool->vmap, 64u, static_cast<uint32_t>(P > 64 ? 64 : P));
-  if (st == PA_OK) pool->tile_maps_ready = true;
-  return st;
-}
-
 // D = 128 pools, tensor-core decode units: bf16 boxes of 64 elements x min(P, 32)
 // rows (one head-dim half), e4m3 boxes of 128 bytes x min(P, 32) rows.
 pa_status encode_decode_maps(pa_pool* pool) {
@@ -224,6 +215,33 @@ pa_status check_desc(const pa_pool_desc* d) {
 }
 
 }  // namespace
+
+// bf16 pools, prefill tiles: 64 elements x min(P, 64) rows (half or all of the head dim).
+pa_status pa::encode_tile_maps(pa_pool* pool) {
+  if (pool->tile_maps_ready) return PA_OK;
+  if (pool->desc.kv_dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "the tile path reads bf16 pools");
+  const int P = pool->desc.page_size;
+  const pa_status st = encode_map_pair(pool, &pool->kmap, &pool->vmap, 64u, static_cast<uint32_t>(P > 64 ? 64 : P));
+  if (st == PA_OK) pool->tile_maps_ready = true;
+  return st;
+}
+
+pa_status pa::encode_query_map(CUtensorMap* map, const void* q, int32_t n_rows, int32_t hq, int32_t head_dim, int32_t group) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(hq), static_cast<cuuint64_t>(n_rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(hq) * head_dim * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(kTileRowsTotal / group)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return PA_OK;
+}
+
+uint32_t pa::wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+int32_t pa::debug_stall() { return g_debug_stall.load(std::memory_order_relaxed); }
 
 // The checks of a call's rows that pa_attention, pa_step and pa_attention_mass share.
 pa_status pa::check_rows(const pa_pool_desc& d, int32_t n_rows, pa_dtype q_dtype, int32_t num_q_heads, int32_t num_seqs,

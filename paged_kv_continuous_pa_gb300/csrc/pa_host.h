@@ -32,6 +32,16 @@ pa_status cuda_fail(cudaError_t e, const char* what);
 pa_status check_rows(const pa_pool_desc& d, int32_t n_rows, pa_dtype q_dtype, int32_t num_q_heads, int32_t num_seqs,
                      int32_t max_blocks_per_seq, const pa_chunk* chunks, int32_t n_chunks);
 
+// The pool's tensor maps for the tile paths (bf16), encoded on first use.
+pa_status encode_tile_maps(pa_pool* pool);
+// bf16 queries [n_rows][hq][head_dim] as a 3-D tensor, 128-byte swizzle, boxes of
+// 64 elements x `group` heads x 128 / group rows.
+pa_status encode_query_map(CUtensorMap* map, const void* q, int32_t n_rows, int32_t hq, int32_t head_dim, int32_t group);
+
+// Process-wide settings, each read once per call.
+uint32_t wait_limit();
+int32_t debug_stall();
+
 inline size_t elt_bytes(pa_dtype t) { return t == PA_F32 ? 4 : t == PA_BF16 ? 2 : 1; }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

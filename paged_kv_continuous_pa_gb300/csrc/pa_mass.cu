@@ -6,6 +6,35 @@
 #include "pa_host.h"
 #include "pa_mass.cuh"
 
+namespace pa {
+
+// Second launch: every column's (maximum, 1 / sum) over its key ranges, merged
+// in ascending order.  One CTA per (tile, kv head) of a chunk.
+__global__ void __launch_bounds__(kMassSlots) chunk_merge_kernel(const __grid_constant__ MassParams p) {
+  int c = 0;
+  while (c + 1 < p.n_chunks && static_cast<int>(blockIdx.x) >= p.chunk_cta[c + 1]) ++c;
+  const int local = blockIdx.x - p.chunk_cta[c], tiles = p.chunk_tiles[c];
+  const int h = local % p.Hkv, tile = local / p.Hkv, m = threadIdx.x;
+  const int G = p.Hq / p.Hkv, R = kMassSlots / G, row = tile * R + m / G;
+  float2 out = make_float2(0.0f, 0.0f);
+  if (m < R * G && row < p.chunk_end[c] - p.chunk_begin[c]) {
+    const int pos = __ldg(p.positions + p.chunk_begin[c]) + row;
+    // a chunk that adds nothing may have any positions: its statistics are not read
+    const int n = min(pos < 0 ? 0 : pos / kMassSplitKeys + 1, p.n_splits);
+    ColumnStat st{-INFINITY, 0.0f};
+    for (int k = 0; k < n; ++k) {
+      const float2 o = __ldcg(p.ws_part + p.chunk_part[c] + ((static_cast<size_t>(h) * p.n_splits + k) * tiles + tile) * kMassSlots + m);
+      st.merge(o.x, o.y);
+    }
+    out = make_float2(st.m, __fdiv_rn(1.0f, st.l));
+  }
+  float* stat = p.ws_stat + p.chunk_stat[c] + (static_cast<size_t>(h) * tiles + tile) * 2 * kMassSlots;
+  stat[m] = out.x;
+  stat[kMassSlots + m] = out.y;
+}
+
+}  // namespace pa
+
 using pa::aligned;
 using pa::cuda_fail;
 using pa::fail;
@@ -14,19 +43,72 @@ namespace {
 
 // Key ranges, key blocks and the chunks' places in the workspace, from sizes alone.
 size_t plan_chunks(const pa_pool_desc& d, int32_t hq, int32_t max_blocks, const pa_chunk* chunks, int32_t n_chunks,
-                   pa::MassParams* p) {
+                   void* workspace, pa::MassParams* p) {
   const int64_t keys = static_cast<int64_t>(max_blocks) * d.page_size;
-  p->n_splits = static_cast<int32_t>((keys + pa::kMassSplitKeys - 1) / pa::kMassSplitKeys);
-  p->n_blocks = static_cast<int32_t>((keys + pa::kMassBlockKeys - 1) / pa::kMassBlockKeys);
-  int64_t pairs = 0;
+  auto cut = [&](int64_t n) { return static_cast<int32_t>((keys + n - 1) / n); };
+  p->n_splits = cut(pa::kMassSplitKeys);
+  p->n_blocks = cut(pa::kMassBlockKeys);
+  p->n_ranges = cut(pa::kMassRangeKeys);
+  const int R = pa::kMassSlots / (hq / d.num_kv_heads);
+  int64_t pairs = 0, floats = 0;
   for (int c = 0; c < n_chunks; ++c) {
     p->chunk_begin[c] = chunks[c].row_begin;
     p->chunk_end[c] = chunks[c].row_begin + chunks[c].n_rows;
-    p->chunk_stats[c] = pairs;
-    pairs += static_cast<int64_t>(chunks[c].n_rows) * hq * p->n_splits;
+    p->chunk_tiles[c] = (chunks[c].n_rows + R - 1) / R;
+    const int64_t slots = static_cast<int64_t>(p->chunk_tiles[c]) * pa::kMassSlots * d.num_kv_heads;
+    p->chunk_part[c] = pairs;
+    p->chunk_stat[c] = floats;
+    pairs += slots * p->n_splits;
+    floats += slots * 2;
   }
   p->n_chunks = n_chunks;
-  return (static_cast<size_t>(pairs) * sizeof(float2) + 255) / 256 * 256;
+  // the merged statistics first: 1 KB blocks, which the tile path copies whole
+  p->ws_stat = static_cast<float*>(workspace);
+  p->ws_part = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + static_cast<size_t>(floats) * sizeof(float));
+  return static_cast<size_t>(floats) * sizeof(float) + static_cast<size_t>(pairs) * sizeof(float2);
+}
+
+// The chunks of `all` for which `take` holds.
+template <typename Take>
+pa::MassParams some_chunks(const pa::MassParams& all, Take take) {
+  pa::MassParams p = all;
+  p.n_chunks = 0;
+  for (int c = 0; c < all.n_chunks; ++c) {
+    if (!take(c)) continue;
+    const int k = p.n_chunks++;
+    p.chunk_begin[k] = all.chunk_begin[c];
+    p.chunk_end[k] = all.chunk_end[c];
+    p.chunk_tiles[k] = all.chunk_tiles[c];
+    p.chunk_part[k] = all.chunk_part[c];
+    p.chunk_stat[k] = all.chunk_stat[c];
+  }
+  return p;
+}
+
+// The chunks' columns: statistics over key ranges, merged, then the weights,
+// on the tile path for bf16 chunks of kMinTileRows rows and more.
+template <typename Launch>
+cudaError_t launch_chunks(const pa::MassParams& all, bool tile_types, Launch launch, cudaStream_t s) {
+  auto tiled = [&](int c) { return tile_types && all.chunk_end[c] - all.chunk_begin[c] >= pa::kMinTileRows; };
+  const pa::MassParams tiles = some_chunks(all, tiled), others = some_chunks(all, [&](int c) { return !tiled(c); });
+  cudaError_t e = cudaSuccess;
+  if (tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, false, s);
+  if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_STATS, s);
+  if (e != cudaSuccess) return e;
+  pa::MassParams p = all;
+  long long ctas = 0;
+  for (int c = 0; c < p.n_chunks; ++c) {
+    p.chunk_cta[c] = static_cast<int32_t>(ctas);
+    ctas += static_cast<long long>(p.chunk_tiles[c]) * p.Hkv;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  }
+  p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);
+  pa::chunk_merge_kernel<<<static_cast<unsigned>(ctas), pa::kMassSlots, 0, s>>>(p);
+  pa::count_launch();
+  e = cudaGetLastError();
+  if (e == cudaSuccess && tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, true, s);
+  if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_WEIGHTS, s);
+  return e;
 }
 
 }  // namespace
@@ -39,7 +121,7 @@ size_t pa_attention_mass_workspace_bytes(const pa_pool* pool, int32_t n_rows, in
                                         n_chunks) != PA_OK)
     return 0;
   pa::MassParams p{};
-  return plan_chunks(pool->desc, num_q_heads, max_blocks_per_seq, chunks, n_chunks, &p);
+  return plan_chunks(pool->desc, num_q_heads, max_blocks_per_seq, chunks, n_chunks, nullptr, &p);
 }
 
 pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, pa_dtype q_dtype, int32_t num_q_heads,
@@ -81,13 +163,12 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
     const double ks = d.kv_dtype == PA_FP8_E4M3 ? static_cast<double>(pool->head_scales ? pool->k_scale_h[h] : d.k_scale) : 1.0;
     p.qk_scale_log2_h[h] = static_cast<float>(sm * ks * 1.4426950408889634073599246810018921);  // log2(e)
   }
-  const size_t need = plan_chunks(d, num_q_heads, max_blocks_per_seq, chunks, n_chunks, &p);
+  const size_t need = plan_chunks(d, num_q_heads, max_blocks_per_seq, chunks, n_chunks, workspace, &p);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need)
       return fail(PA_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", need,
                   workspace == nullptr ? static_cast<size_t>(0) : workspace_bytes);
     if (!aligned(workspace, 256)) return fail(PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-    p.ws_stats = static_cast<float2*>(workspace);
   }
   int64_t in_chunks = 0;
   for (int c = 0; c < n_chunks; ++c) in_chunks += chunks[c].n_rows;
@@ -102,14 +183,22 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
   p.score_keys = static_cast<int32_t>(std::min(room, share));
   if (static_cast<int64_t>(n_rows) * d.num_kv_heads * p.cluster > 0x7fffffff)
     return fail(PA_ERR_UNSUPPORTED, "%d rows of %d kv heads in one call", n_rows, d.num_kv_heads);
-  const bool rows = in_chunks < n_rows;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  switch (d.kv_dtype) {
-    case PA_F32: e = pa::launch_mass_f32(p, rows, s); break;
-    case PA_BF16: e = pa::launch_mass_bf16(p, rows, s); break;
-    default: e = pa::launch_mass_e4m3(p, rows, s); break;
+  p.wait_limit = pa::wait_limit();
+  p.debug_stall = pa::debug_stall();
+  const bool tile_types = d.kv_dtype == PA_BF16 && q_dtype == PA_BF16;
+  bool tiles = false;
+  for (int c = 0; c < n_chunks; ++c) tiles = tiles || (tile_types && chunks[c].n_rows >= pa::kMinTileRows);
+  if (tiles) {
+    st = pa::encode_tile_maps(const_cast<pa_pool*>(pool));
+    if (st == PA_OK) st = pa::encode_query_map(&p.qmap, q, n_rows, num_q_heads, d.head_dim, G);
+    if (st != PA_OK) return st;
+    p.kmap = pool->kmap;
   }
+  auto launch = d.kv_dtype == PA_F32 ? pa::launch_mass_f32 : d.kv_dtype == PA_BF16 ? pa::launch_mass_bf16 : pa::launch_mass_e4m3;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (in_chunks < n_rows) e = launch(p, pa::MASS_ROWS, s);
+  if (e == cudaSuccess && n_chunks > 0) e = launch_chunks(p, tile_types, launch, s);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "attention mass launch");
 }
 

@@ -9,11 +9,12 @@
 // head).  K is read from memory once, straight into tensor-core fragments; the
 // scores wait in shared memory while the cluster's CTAs exchange their (max,
 // sum) pairs, then become weights.
-// Chunks (`chunk_stats_kernel`, then `chunk_weights_kernel`): the (row, head)
-// pairs of a kv head are columns that share the keys.  The first launch finds
-// every column's (max, sum) over ranges of keys, the second recomputes the
-// scores key block by key block, merges the ranges of each column and sums the
-// weights over the columns: each key has one owner, which adds once.
+// Chunks: the (row, head) pairs of a kv head are columns that share the keys.
+// `chunk_stats_kernel` finds every column's (max, sum) over ranges of keys,
+// `chunk_merge_kernel` joins the ranges, `chunk_weights_kernel` recomputes the
+// scores key block by key block and sums the weights over the columns: each key
+// has one owner, which adds once.  (bf16 chunks of 16 rows and more: the same
+// three steps on the tile path, pa_mass_tiles.cuh.)
 // No atomic decides an order: the same rows give the same bits in any batch.
 #pragma once
 
@@ -25,8 +26,10 @@ namespace pa {
 
 constexpr int kMassThreads = 256;
 constexpr int kMassWarps = kMassThreads / 32;
-constexpr int kMassSplitKeys = 4096;  // keys per range of the chunks' first launch
-constexpr int kMassBlockKeys = 128;   // keys per CTA of their second launch
+constexpr int kMassSplitKeys = 2048;  // keys per range of the chunks' first launch
+constexpr int kMassBlockKeys = 128;   // keys per CTA of their last launch
+constexpr int kMassRangeKeys = 1024;  // ... on the tile path
+constexpr int kMassSlots = 128;       // columns of a chunk come in tiles of 128 / G rows, 128 slots each
 constexpr int kMassClusterKeys = 2048;             // keys per CTA that a row's cluster aims at
 constexpr int kMassMaxCluster = 8;
 constexpr size_t kMassScoreBytes = 104 * 1024;     // shared memory for a CTA's scores (two CTAs to an SM)
@@ -44,15 +47,27 @@ struct MassParams {
   float qk_scale_log2_h[kMaxHeadScales];  // softmax scale * log2(e) * k scale
   int32_t cluster;      // CTAs per (row, kv head) of the rows' launch
   int32_t score_keys;   // keys per CTA whose scores fit in shared memory (a multiple of 16)
+  uint32_t wait_limit;  // microseconds (tile path)
+  int32_t debug_stall;  // tile path: also wait on a barrier nothing completes
   int32_t n_chunks;
   int32_t chunk_begin[kMaxChunks];
   int32_t chunk_end[kMaxChunks];
-  int32_t chunk_cta[kMaxChunks + 1];   // first launch: prefix sums of CTAs per chunk
-  int32_t n_splits;                    // key ranges of the longest row
-  int32_t n_blocks;                    // second launch: key blocks of the longest row
-  int64_t chunk_stats[kMaxChunks];     // offset of a chunk's (max, sum) pairs, in pairs
-  float2* ws_stats;                    // per chunk [Hkv][n_splits][rows * G]
+  int32_t chunk_cta[kMaxChunks + 1];   // prefix sums of CTAs per chunk (set per launch)
+  int32_t chunk_tiles[kMaxChunks];     // tiles of 128 / G rows
+  int32_t n_splits, n_blocks, n_ranges;  // of the longest row: key ranges, key blocks, tile-path ranges
+  int64_t chunk_part[kMaxChunks];      // offset of a chunk in ws_part, in pairs
+  int64_t chunk_stat[kMaxChunks];      // ... in ws_stat, in floats
+  float2* ws_part;                     // (max, sum) per chunk [Hkv][n_splits][tiles][128]
+  float* ws_stat;                      // merged, per chunk [Hkv][tiles] x (max x 128, then 1 / sum x 128)
+  CUtensorMap kmap;                    // tile path: the pool as [num_pages * Hkv * P][D], boxes of 64 x min(P, 64)
+  CUtensorMap qmap;                    // tile path: q as [n_rows][Hq][D], boxes of 128 / G rows x G heads x 64
 };
+
+// The slot of a column (head col % G of row col / G) among its chunk's tiles.
+__device__ __forceinline__ int column_slot(int col, int G) {
+  const int r = col / G, R = kMassSlots / G;
+  return r / R * kMassSlots + r % R * G + col % G;
+}
 
 // ------------------------------------------------------------- fragments --
 //
@@ -447,19 +462,6 @@ struct ChunkView {
   }
 };
 
-// A column's (maximum, 1 / sum) over its key ranges, merged in ascending order.
-__device__ __forceinline__ float2 column_stat(const MassParams& p, const ChunkView& v, int c, int h, int col, int G) {
-  const size_t cols = static_cast<size_t>(v.rows) * G;
-  const float2* s = p.ws_stats + p.chunk_stats[c] + static_cast<size_t>(h) * p.n_splits * cols + col;
-  const int n = (v.pos0 + col / G) / kMassSplitKeys + 1;
-  ColumnStat st{-INFINITY, 0.0f};
-  for (int k = 0; k < n; ++k) {
-    const float2 o = __ldcg(s + k * cols);
-    st.merge(o.x, o.y);
-  }
-  return make_float2(st.m, __fdiv_rn(1.0f, st.l));
-}
-
 // Columns a warp scores at once (8 to a group), held to about 64 registers of query fragments.
 template <int KVT, int D, bool QB>
 struct ChunkGeom {
@@ -528,11 +530,12 @@ __global__ void __launch_bounds__(kMassThreads) chunk_stats_kernel(const __grid_
   if (tid < COLS && col0 + tid < cols) {
     ColumnStat s{-INFINITY, 0.0f};
     for (int w = 0; w < kMassWarps; ++w) s.merge(warp_stat[w][tid].x, warp_stat[w][tid].y);
-    p.ws_stats[p.chunk_stats[c] + (static_cast<size_t>(h) * p.n_splits + split) * cols + col0 + tid] = make_float2(s.m, s.l);
+    p.ws_part[p.chunk_part[c] + (static_cast<size_t>(h) * p.n_splits + split) * p.chunk_tiles[c] * kMassSlots +
+              column_slot(col0 + tid, G)] = make_float2(s.m, s.l);
   }
 }
 
-// Second launch: one CTA per (chunk, kv head, block of 128 keys).  A warp keeps
+// Last launch: one CTA per (chunk, kv head, block of 128 keys).  A warp keeps
 // its 16 keys' fragments and goes over the columns that see them.
 template <int KVT, int D, bool QB>
 __global__ void __launch_bounds__(kMassThreads) chunk_weights_kernel(const __grid_constant__ MassParams p) {
@@ -554,7 +557,12 @@ __global__ void __launch_bounds__(kMassThreads) chunk_weights_kernel(const __gri
   // columns before the first row that sees key0 see none of the block
   for (int col0 = max(0, key0 - v.pos0) * G / COLS * COLS; col0 < cols; col0 += COLS) {
     __syncthreads();
-    if (tid < COLS && col0 + tid < cols) stat[tid] = column_stat(p, v, c, h, col0 + tid, G);
+    if (tid < COLS && col0 + tid < cols) {
+      const int slot = column_slot(col0 + tid, G);
+      const float* z = p.ws_stat + p.chunk_stat[c] +
+                       (static_cast<size_t>(h) * p.chunk_tiles[c] + slot / kMassSlots) * 2 * kMassSlots + slot % kMassSlots;
+      stat[tid] = make_float2(__ldcg(z), __ldcg(z + kMassSlots));
+    }
     __syncthreads();
     if (t0 > v.last) continue;
     QueryFrag<KVT, D, QB> q[NT];
@@ -591,15 +599,17 @@ __global__ void __launch_bounds__(kMassThreads) chunk_weights_kernel(const __gri
 
 // -------------------------------------------------------------- launches --
 
+// What one call to a launcher runs, in this order.
+enum MassLaunch { MASS_ROWS, MASS_CHUNK_STATS, MASS_CHUNK_WEIGHTS };
+
 template <int KVT, int D, bool QB>
-cudaError_t launch_mass_inst(const MassParams& p0, bool rows, cudaStream_t stream) {
+cudaError_t launch_mass_inst(const MassParams& p0, MassLaunch what, cudaStream_t stream) {
   MassParams p = p0;
-  cudaError_t e = cudaSuccess;
-  if (rows) {
-    const int G = p.Hq / p.Hkv;
+  const int G = p.Hq / p.Hkv;
+  if (what == MASS_ROWS) {
     const size_t smem = static_cast<size_t>(G) * score_stride(p.score_keys) * sizeof(float);
     static std::atomic<unsigned long long> smem_done{0};
-    e = allow_dynamic_smem(mass_row_kernel<KVT, D, QB>, smem_done, kMassScoreBytes);
+    const cudaError_t e = allow_dynamic_smem(mass_row_kernel<KVT, D, QB>, smem_done, kMassScoreBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.n_rows) * p.Hkv * p.cluster);
@@ -611,42 +621,41 @@ cudaError_t launch_mass_inst(const MassParams& p0, bool rows, cudaStream_t strea
     attr[0].val.clusterDim = {static_cast<unsigned>(p.cluster), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mass_row_kernel<KVT, D, QB>, p);
     count_launch();
-    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, mass_row_kernel<KVT, D, QB>, p);
   }
-  if (p.n_chunks > 0) {
-    constexpr int COLS = ChunkGeom<KVT, D, QB>::COLS;
-    const int G = p.Hq / p.Hkv;
-    long long ctas = 0;
-    for (int c = 0; c < p.n_chunks; ++c) {
-      p.chunk_cta[c] = static_cast<int32_t>(ctas);
-      const long long cols = static_cast<long long>(p.chunk_end[c] - p.chunk_begin[c]) * G;
-      ctas += (cols + COLS - 1) / COLS * p.Hkv * p.n_splits;
-      if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    }
-    p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);
-    const long long blocks = static_cast<long long>(p.n_chunks) * p.Hkv * p.n_blocks;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  constexpr int COLS = ChunkGeom<KVT, D, QB>::COLS;
+  long long ctas = 0;
+  for (int c = 0; c < p.n_chunks; ++c) {
+    p.chunk_cta[c] = static_cast<int32_t>(ctas);
+    const long long cols = static_cast<long long>(p.chunk_end[c] - p.chunk_begin[c]) * G;
+    ctas += (cols + COLS - 1) / COLS * p.Hkv * p.n_splits;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  }
+  p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);
+  const long long blocks = static_cast<long long>(p.n_chunks) * p.Hkv * p.n_blocks;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (what == MASS_CHUNK_STATS)
     chunk_stats_kernel<KVT, D, QB><<<static_cast<unsigned>(ctas), kMassThreads, 0, stream>>>(p);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  else
     chunk_weights_kernel<KVT, D, QB><<<static_cast<unsigned>(blocks), kMassThreads, 0, stream>>>(p);
-    count_launch();
-    e = cudaGetLastError();
-  }
-  return e;
+  count_launch();
+  return cudaGetLastError();
 }
 
 template <int KVT>
-cudaError_t launch_mass_dispatch(const MassParams& p, bool rows, cudaStream_t stream) {
-  if (p.D == 64) return p.q_is_bf16 ? launch_mass_inst<KVT, 64, true>(p, rows, stream) : launch_mass_inst<KVT, 64, false>(p, rows, stream);
-  return p.q_is_bf16 ? launch_mass_inst<KVT, 128, true>(p, rows, stream) : launch_mass_inst<KVT, 128, false>(p, rows, stream);
+cudaError_t launch_mass_dispatch(const MassParams& p, MassLaunch what, cudaStream_t stream) {
+  if (p.D == 64) return p.q_is_bf16 ? launch_mass_inst<KVT, 64, true>(p, what, stream) : launch_mass_inst<KVT, 64, false>(p, what, stream);
+  return p.q_is_bf16 ? launch_mass_inst<KVT, 128, true>(p, what, stream) : launch_mass_inst<KVT, 128, false>(p, what, stream);
 }
 
-// One translation unit per K dtype.  rows: some row is outside every chunk.
-cudaError_t launch_mass_f32(const MassParams& p, bool rows, cudaStream_t stream);
-cudaError_t launch_mass_bf16(const MassParams& p, bool rows, cudaStream_t stream);
-cudaError_t launch_mass_e4m3(const MassParams& p, bool rows, cudaStream_t stream);
+// One translation unit per K dtype.
+cudaError_t launch_mass_f32(const MassParams& p, MassLaunch what, cudaStream_t stream);
+cudaError_t launch_mass_bf16(const MassParams& p, MassLaunch what, cudaStream_t stream);
+cudaError_t launch_mass_e4m3(const MassParams& p, MassLaunch what, cudaStream_t stream);
+
+// The tensor-core tile launches (bf16 queries and pool): the columns'
+// statistics, or with `weights` the weights.
+cudaError_t launch_mass_tiles(const MassParams& p, bool weights, cudaStream_t stream);
 
 }  // namespace pa

@@ -3,8 +3,8 @@
 
 namespace pa {
 
-cudaError_t launch_mass_bf16(const MassParams& p, bool rows, cudaStream_t stream) {
-  return launch_mass_dispatch<KV_BF16>(p, rows, stream);
+cudaError_t launch_mass_bf16(const MassParams& p, MassLaunch what, cudaStream_t stream) {
+  return launch_mass_dispatch<KV_BF16>(p, what, stream);
 }
 
 }  // namespace pa

@@ -3,8 +3,8 @@
 
 namespace pa {
 
-cudaError_t launch_mass_f32(const MassParams& p, bool rows, cudaStream_t stream) {
-  return launch_mass_dispatch<KV_F32>(p, rows, stream);
+cudaError_t launch_mass_f32(const MassParams& p, MassLaunch what, cudaStream_t stream) {
+  return launch_mass_dispatch<KV_F32>(p, what, stream);
 }
 
 }  // namespace pa

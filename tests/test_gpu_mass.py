@@ -258,3 +258,40 @@ def test_matches_the_attention_step():
     pa.attention_mass(c.pool, q, ids, pos, c.tables, mass)
     # two FP32 evaluations of the same weights, each within (64 + 8) roundings of scores below 8
     assert torch.allclose(mass[c.slots[0], 0, :60], out[0].sum(dim=0)[:60], rtol=2 * 72 * 2.0 ** -23 * 8 * 2, atol=1e-7)
+
+
+@pytest.mark.parametrize("rows", [20, 130])
+def test_nan_query_stays_with_the_keys_it_sees(rows):
+    """One row of a chunk has a NaN query: the keys behind its position are as if it were not there."""
+    c = R.make_cache([700], Hkv=2, D=128, P=32, seed=16)
+    q = queries(rows, 6, 128, torch.bfloat16)
+    clean = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    pos = [700 - rows + i for i in range(rows)]
+    assert run(c, q, c.slots * rows, pos, clean, [(0, rows)]) == 0
+    bad = 7
+    q[bad] = float("nan")
+    mass = torch.zeros_like(clean)
+    assert run(c, q, c.slots * rows, pos, mass, [(0, rows)]) == 0
+    s = c.slots[0]
+    assert torch.isnan(mass[s, :, :pos[bad] + 1]).all()
+    # the rows that see the keys behind it are the same ones: the same weights
+    assert torch.equal(mass[s, :, pos[bad] + 1:700], clean[s, :, pos[bad] + 1:700])
+
+
+def test_wait_limit_runs_out_cleanly():
+    """The tile path's bounded waits: with the injected stall the call reports PA_ERR_TIMEOUT, adds nothing,
+    and the next call is right."""
+    rows = 32
+    c = R.make_cache([600], Hkv=2, D=128, P=32, seed=17)
+    q = queries(rows, 4, 128, torch.bfloat16)
+    seq, pos = c.slots * rows, [600 - rows + i for i in range(rows)]
+    mass = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    pa.set_wait_limit(1000)
+    pa.debug_stall_waits(True)
+    try:
+        assert run(c, q, seq, pos, mass, [(0, rows)]) == pa.PA_ERR_TIMEOUT
+    finally:
+        pa.debug_stall_waits(False)
+        pa.set_wait_limit(0)
+    assert torch.equal(mass, torch.zeros_like(mass))
+    check(c, q, seq, pos, [(0, rows)])
