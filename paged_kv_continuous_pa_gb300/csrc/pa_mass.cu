@@ -6,35 +6,6 @@
 #include "pa_host.h"
 #include "pa_mass.cuh"
 
-namespace pa {
-
-// Second launch: every column's (maximum, 1 / sum) over its key ranges, merged
-// in ascending order.  One CTA per (tile, kv head) of a chunk.
-__global__ void __launch_bounds__(kMassSlots) chunk_merge_kernel(const __grid_constant__ MassParams p) {
-  int c = 0;
-  while (c + 1 < p.n_chunks && static_cast<int>(blockIdx.x) >= p.chunk_cta[c + 1]) ++c;
-  const int local = blockIdx.x - p.chunk_cta[c], tiles = p.chunk_tiles[c];
-  const int h = local % p.Hkv, tile = local / p.Hkv, m = threadIdx.x;
-  const int G = p.Hq / p.Hkv, R = kMassSlots / G, row = tile * R + m / G;
-  float2 out = make_float2(0.0f, 0.0f);
-  if (m < R * G && row < p.chunk_end[c] - p.chunk_begin[c]) {
-    const int pos = __ldg(p.positions + p.chunk_begin[c]) + row;
-    // a chunk that adds nothing may have any positions: its statistics are not read
-    const int n = min(pos < 0 ? 0 : pos / kMassSplitKeys + 1, p.n_splits);
-    ColumnStat st{-INFINITY, 0.0f};
-    for (int k = 0; k < n; ++k) {
-      const float2 o = __ldcg(p.ws_part + p.chunk_part[c] + ((static_cast<size_t>(h) * p.n_splits + k) * tiles + tile) * kMassSlots + m);
-      st.merge(o.x, o.y);
-    }
-    out = make_float2(st.m, __fdiv_rn(1.0f, st.l));
-  }
-  float* stat = p.ws_stat + p.chunk_stat[c] + (static_cast<size_t>(h) * tiles + tile) * 2 * kMassSlots;
-  stat[m] = out.x;
-  stat[kMassSlots + m] = out.y;
-}
-
-}  // namespace pa
-
 using pa::aligned;
 using pa::cuda_fail;
 using pa::fail;
@@ -50,22 +21,18 @@ size_t plan_chunks(const pa_pool_desc& d, int32_t hq, int32_t max_blocks, const 
   p->n_blocks = cut(pa::kMassBlockKeys);
   p->n_ranges = cut(pa::kMassRangeKeys);
   const int R = pa::kMassSlots / (hq / d.num_kv_heads);
-  int64_t pairs = 0, floats = 0;
+  int64_t pairs = 0;
   for (int c = 0; c < n_chunks; ++c) {
     p->chunk_begin[c] = chunks[c].row_begin;
     p->chunk_end[c] = chunks[c].row_begin + chunks[c].n_rows;
     p->chunk_tiles[c] = (chunks[c].n_rows + R - 1) / R;
     const int64_t slots = static_cast<int64_t>(p->chunk_tiles[c]) * pa::kMassSlots * d.num_kv_heads;
     p->chunk_part[c] = pairs;
-    p->chunk_stat[c] = floats;
     pairs += slots * p->n_splits;
-    floats += slots * 2;
   }
   p->n_chunks = n_chunks;
-  // the merged statistics first: 1 KB blocks, which the tile path copies whole
-  p->ws_stat = static_cast<float*>(workspace);
-  p->ws_part = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + static_cast<size_t>(floats) * sizeof(float));
-  return static_cast<size_t>(floats) * sizeof(float) + static_cast<size_t>(pairs) * sizeof(float2);
+  p->ws_part = static_cast<float2*>(workspace);
+  return static_cast<size_t>(pairs) * sizeof(float2);
 }
 
 // The chunks of `all` for which `take` holds.
@@ -80,33 +47,20 @@ pa::MassParams some_chunks(const pa::MassParams& all, Take take) {
     p.chunk_end[k] = all.chunk_end[c];
     p.chunk_tiles[k] = all.chunk_tiles[c];
     p.chunk_part[k] = all.chunk_part[c];
-    p.chunk_stat[k] = all.chunk_stat[c];
   }
   return p;
 }
 
-// The chunks' columns: statistics over key ranges, merged, then the weights,
-// on the tile path for bf16 chunks of kMinTileRows rows and more.
+// The chunks' columns: statistics over key ranges, then the weights, on the
+// tile path for bf16 chunks of kMinTileRows rows and more.
 template <typename Launch>
 cudaError_t launch_chunks(const pa::MassParams& all, bool tile_types, Launch launch, cudaStream_t s) {
   auto tiled = [&](int c) { return tile_types && all.chunk_end[c] - all.chunk_begin[c] >= pa::kMinTileRows; };
   const pa::MassParams tiles = some_chunks(all, tiled), others = some_chunks(all, [&](int c) { return !tiled(c); });
   cudaError_t e = cudaSuccess;
   if (tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, false, s);
-  if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_STATS, s);
-  if (e != cudaSuccess) return e;
-  pa::MassParams p = all;
-  long long ctas = 0;
-  for (int c = 0; c < p.n_chunks; ++c) {
-    p.chunk_cta[c] = static_cast<int32_t>(ctas);
-    ctas += static_cast<long long>(p.chunk_tiles[c]) * p.Hkv;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  }
-  p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);
-  pa::chunk_merge_kernel<<<static_cast<unsigned>(ctas), pa::kMassSlots, 0, s>>>(p);
-  pa::count_launch();
-  e = cudaGetLastError();
   if (e == cudaSuccess && tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, true, s);
+  if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_STATS, s);
   if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_WEIGHTS, s);
   return e;
 }

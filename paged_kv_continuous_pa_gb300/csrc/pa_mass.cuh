@@ -11,10 +11,10 @@
 // sum) pairs, then become weights.
 // Chunks: the (row, head) pairs of a kv head are columns that share the keys.
 // `chunk_stats_kernel` finds every column's (max, sum) over ranges of keys,
-// `chunk_merge_kernel` joins the ranges, `chunk_weights_kernel` recomputes the
-// scores key block by key block and sums the weights over the columns: each key
-// has one owner, which adds once.  (bf16 chunks of 16 rows and more: the same
-// three steps on the tile path, pa_mass_tiles.cuh.)
+// `chunk_weights_kernel` merges the ranges, recomputes the scores key block by
+// key block and sums the weights over the columns: each key has one owner, which
+// adds once.  (bf16 chunks of 16 rows and more: the same two steps on the tile
+// path, pa_mass_tiles.cuh.)
 // No atomic decides an order: the same rows give the same bits in any batch.
 #pragma once
 
@@ -56,9 +56,7 @@ struct MassParams {
   int32_t chunk_tiles[kMaxChunks];     // tiles of 128 / G rows
   int32_t n_splits, n_blocks, n_ranges;  // of the longest row: key ranges, key blocks, tile-path ranges
   int64_t chunk_part[kMaxChunks];      // offset of a chunk in ws_part, in pairs
-  int64_t chunk_stat[kMaxChunks];      // ... in ws_stat, in floats
   float2* ws_part;                     // (max, sum) per chunk [Hkv][n_splits][tiles][128]
-  float* ws_stat;                      // merged, per chunk [Hkv][tiles] x (max x 128, then 1 / sum x 128)
   CUtensorMap kmap;                    // tile path: the pool as [num_pages * Hkv * P][D], boxes of 64 x min(P, 64)
   CUtensorMap qmap;                    // tile path: q as [n_rows][Hq][D], boxes of 128 / G rows x G heads x 64
 };
@@ -462,6 +460,23 @@ struct ChunkView {
   }
 };
 
+// A column's (maximum, 1 / sum) over the key ranges that a row at `pos` sees,
+// merged in ascending order: slot `slot` of the chunk's tile `tile`.
+__device__ __forceinline__ float2 column_stat(const MassParams& p, int c, int h, int tile, int slot,
+                                              int pos) {
+  const size_t stride = static_cast<size_t>(p.chunk_tiles[c]) * kMassSlots;
+  const float2* s = p.ws_part + p.chunk_part[c] + static_cast<size_t>(h) * p.n_splits * stride +
+                    static_cast<size_t>(tile) * kMassSlots + slot;
+  const int n = pos / kMassSplitKeys + 1;
+  ColumnStat st{-INFINITY, 0.0f};
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float2 o = __ldcg(s + k * stride);
+    st.merge(o.x, o.y);
+  }
+  return make_float2(st.m, __fdiv_rn(1.0f, st.l));
+}
+
 // Columns a warp scores at once (8 to a group), held to about 64 registers of query fragments.
 template <int KVT, int D, bool QB>
 struct ChunkGeom {
@@ -559,9 +574,7 @@ __global__ void __launch_bounds__(kMassThreads) chunk_weights_kernel(const __gri
     __syncthreads();
     if (tid < COLS && col0 + tid < cols) {
       const int slot = column_slot(col0 + tid, G);
-      const float* z = p.ws_stat + p.chunk_stat[c] +
-                       (static_cast<size_t>(h) * p.chunk_tiles[c] + slot / kMassSlots) * 2 * kMassSlots + slot % kMassSlots;
-      stat[tid] = make_float2(__ldcg(z), __ldcg(z + kMassSlots));
+      stat[tid] = column_stat(p, c, h, slot / kMassSlots, slot % kMassSlots, v.pos0 + (col0 + tid) / G);
     }
     __syncthreads();
     if (t0 > v.last) continue;

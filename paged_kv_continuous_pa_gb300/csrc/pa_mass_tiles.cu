@@ -9,8 +9,8 @@ cudaError_t launch_mass_tiles(const MassParams& p0, bool weights, cudaStream_t s
   long long ctas = 0;
   for (int c = 0; c < p.n_chunks; ++c) {
     p.chunk_cta[c] = static_cast<int32_t>(ctas);
-    const long long tiles = (p.chunk_end[c] - p.chunk_begin[c] + R - 1) / R;
-    ctas += weights ? static_cast<long long>(p.Hkv) * p.n_ranges : tiles * p.Hkv * p.n_splits;
+    const long long pairs = (p.chunk_end[c] - p.chunk_begin[c] + 2 * R - 1) / (2 * R);  // of column tiles
+    ctas += weights ? static_cast<long long>(p.Hkv) * p.n_ranges : pairs * p.Hkv * p.n_splits;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   }
   p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);

@@ -295,3 +295,11 @@ def test_wait_limit_runs_out_cleanly():
         pa.set_wait_limit(0)
     assert torch.equal(mass, torch.zeros_like(mass))
     check(c, q, seq, pos, [(0, rows)])
+
+
+@pytest.mark.parametrize("rows,start,G", [(2500, 0, 1), (1300, 900, 2), (700, 5000, 3), (513, 1, 8)])
+def test_long_chunks(rows, start, G):
+    """Many column tiles over several key ranges: every pair of tiles, with ranges and tiles that see only part."""
+    c = R.make_cache([start + rows], Hkv=1, D=64, P=32, seed=rows)
+    q = queries(rows, G, 64, torch.bfloat16, seed=rows)
+    check(c, q, c.slots * rows, list(range(start, start + rows)), [(0, rows)])
