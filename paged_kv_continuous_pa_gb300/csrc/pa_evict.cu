@@ -24,7 +24,12 @@ struct SelectParams {
   int32_t n, num_seqs, Hkv, max_tokens, budget, keep_first, keep_last;
 };
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 256;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectSamples = 512;
+constexpr int kSelectList = 512;             // keys a warp's list holds
+constexpr int kSelectAll = kSelectList * kSelectWarps;  // that many competing tokens need no sample
+constexpr int kSelectWords = 2048;           // 32-token words marked at once
 
 // The weights in an integer order: a larger weight has a larger key, -0 and +0
 // share one, and NaN comes last (below -infinity).
@@ -34,14 +39,54 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, kv head).  The tokens between the protected first and
-// last ones are searched by radix: four passes over 8 bits of the key fix the
-// key of the last token kept and how many tokens of exactly that key stay (the
-// lowest indices); one more pass writes the kept indices in ascending order.
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t warp_eq[32], warp_sel[32];
-  __shared__ uint32_t sh_prefix, sh_need;
+struct SelectSmem {
+  uint32_t list[kSelectAll];   // per warp: keys between the two pivots
+  uint32_t marks[kSelectWords][2];  // per word: tokens above the last key, of exactly the last key; then kept tokens, first place
+  uint32_t count[2][kSelectWarps][2];
+  uint32_t warp_sum[kSelectWarps][2];
+  uint32_t pivot[2];
+  int overflow;
+};
+
+// One warp: a key that `want` of the samples reach, or a few more.
+__device__ __forceinline__ uint32_t sample_pivot(const uint32_t* samples, int want, int lane) {
+  constexpr int PER = kSelectSamples / 32;
+  uint32_t k[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) k[i] = samples[i * 32 + lane];
+  uint32_t lo = 0u, hi = 0xffffffffu;  // as many reach lo, fewer reach hi
+  while (hi - lo > 1u) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c += k[i] >= mid;
+    c = static_cast<int>(__reduce_add_sync(0xffffffffu, c));
+    if (c >= want) {
+      lo = mid;
+      if (c <= want + 2) break;
+    } else {
+      hi = mid;
+    }
+  }
+  return lo;
+}
+
+// One CTA per (sequence, kv head).  Of the N tokens between the protected ones
+// the m with the largest keys stay; what has to be known is the last key kept
+// and how many tokens of exactly that key stay (the lowest indices).
+//   1. 512 samples, evenly spaced, give two pivots that enclose the m-th key
+//      (3.5 standard deviations of a sample rank to either side).
+//   2. One pass over the weights counts the keys from the upper pivot on and those of
+//      exactly the lower one, and lists the keys between the two (a few in a
+//      hundred; no sample is taken where all fit).
+//   3. Bisection over the list, three pivots a step, finds the last key.
+//   4. A second pass (from L2) marks kept tokens as bits, 32 to a word; counts
+//      over the words place them, in ascending order.
+// Where the pivots miss (the m-th key outside, or a warp's list too short, as a
+// hostile order can bring about) step 3 bisects over the weights themselves.
+// Bound by the read of the weights and the latency of the steps.
+__global__ void __launch_bounds__(kSelectThreads, 5) select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ SelectSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int i = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   const int seq = __ldg(p.seq_ids + i), len = __ldg(p.lengths + i);
@@ -56,66 +101,223 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     return;
   }
   const float* w = p.mass + (static_cast<size_t>(seq) * p.Hkv + h) * p.max_tokens;
-  const int a = p.keep_first, b = len - p.keep_last;  // tokens [a, b) compete
-  const uint32_t m = p.budget - p.keep_first - p.keep_last;
-  uint32_t prefix = 0u, mask = 0u, need = m;
+  const int a = p.keep_first, b = len - p.keep_last, N = b - a;  // tokens [a, b) compete
+  const int m = p.budget - p.keep_first - p.keep_last;           // 0 <= m < N
+  // sums over the CTA of two counts; alternating buffers, so one barrier a sum
+  int turn = 0;
+  auto sum2 = [&](uint32_t x, uint32_t y) {
+    x = __reduce_add_sync(0xffffffffu, x);
+    y = __reduce_add_sync(0xffffffffu, y);
+    turn ^= 1;
+    if (lane == 0) {
+      sm.count[turn][warp][0] = x;
+      sm.count[turn][warp][1] = y;
+    }
+    __syncthreads();
+    x = y = 0u;
+#pragma unroll
+    for (int k = 0; k < kSelectWarps; ++k) {
+      x += sm.count[turn][k][0];
+      y += sm.count[turn][k][1];
+    }
+    return make_uint2(x, y);
+  };
+  uint32_t last = 0xffffffffu, ties = 0u;  // kept: keys above `last`, and the first `ties` tokens of exactly it
   if (m > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0u;
+    uint32_t low = 0u, high = 0xffffffffu;  // no key is that high
+    if (N > kSelectAll) {
+      for (int k = tid; k < kSelectSamples; k += kSelectThreads)
+        sm.list[k] = weight_key(__ldg(w + a + static_cast<int>((static_cast<long long>(2 * k + 1) * N) / (2 * kSelectSamples))));
       __syncthreads();
-      for (int t = a + tid; t < b; t += kSelectThreads) {
-        const uint32_t k = weight_key(w[t]);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      if (warp < 2) {
+        const float rank = static_cast<float>(m) * kSelectSamples / N;
+        const float off = 3.5f * sqrtf(rank * (1.0f - rank / kSelectSamples)) + 2.0f;
+        const int want = static_cast<int>(warp == 0 ? rank - off : rank + off + 1.0f);
+        uint32_t pivot = warp == 0 ? 0xffffffffu : 0u;
+        if (want >= 1 && want <= kSelectSamples) pivot = sample_pivot(sm.list, want, lane);
+        if (lane == 0) sm.pivot[warp] = pivot;
       }
       __syncthreads();
-      if (tid == 0) {
-        uint32_t above = 0u;
-        int bin = 255;
-        while (bin > 0 && above + hist[bin] < need) above += hist[bin--];
-        sh_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-        sh_need = need - above;
+      high = sm.pivot[0];
+      low = sm.pivot[1];
+    }
+    if (tid == 0) sm.overflow = 0;
+    __syncthreads();
+    uint32_t above = 0u, equal = 0u;
+    int listed = 0;  // of this warp
+    const uint32_t below = (1u << lane) - 1u;
+    uint32_t* mine = sm.list + warp * kSelectList;
+    constexpr int UNROLL = 8;
+    for (int t0 = a + tid; t0 - tid < b; t0 += UNROLL * kSelectThreads) {
+      float x[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int t = t0 + u * kSelectThreads;
+        x[u] = t < b ? __ldg(w + t) : 0.0f;
       }
-      __syncthreads();
-      prefix = sh_prefix;
-      need = sh_need;
-      mask |= 255u << shift;
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const bool in = t0 + u * kSelectThreads < b;
+        const uint32_t k = weight_key(x[u]);
+        above += in && k >= high;
+        equal += in && k == low && k < high;
+        const bool between = in && k > low && k < high;
+        const uint32_t who = __ballot_sync(0xffffffffu, between);
+        if (who != 0u) {
+          const int at = listed + __popc(who & below);
+          if (between && at < kSelectList) mine[at] = k;
+          listed += __popc(who);
+        }
+      }
+    }
+    if (lane == 0 && listed > kSelectList) sm.overflow = 1;
+    const uint2 s = sum2(above, equal);
+    const int between = static_cast<int>(sum2(lane == 0 ? listed : 0, 0u).x);
+    const int need = m - static_cast<int>(s.x);  // of the keys below `high`
+    const bool found = !sm.overflow && need > 0 && need <= between + static_cast<int>(s.y);
+    if (found && need > between) {
+      last = low;
+      ties = need - between;
+    } else {
+      // the last key lies between two keys, fewer than `want` tokens reach hi, as many or more reach lo: over the
+      // listed keys, or (the pivots missed) over all
+      uint32_t lo = found ? low : 0u, hi = found ? high : 0xffffffffu;
+      const int want = found ? need : m;
+      uint32_t k[kSelectAll / kSelectThreads];
+#pragma unroll
+      for (int e = 0; e < kSelectAll / kSelectThreads; ++e) k[e] = 0u;
+      if (found) {
+#pragma unroll
+        for (int e = 0; e < kSelectAll / kSelectThreads; ++e) {
+          const int at = e * 32 + lane;
+          if (at < listed) k[e] = mine[at];
+        }
+      }
+      int reach_hi = 0;
+      bool done = false;
+      while (hi - lo > 1u && !done) {
+        const uint32_t step = (hi - lo) / 4;
+        uint32_t q[3] = {lo + step, lo + 2 * step, lo + 3 * step};
+        if (step == 0u) q[0] = q[1] = q[2] = lo + 1u;
+        uint32_t c[3] = {0u, 0u, 0u};
+        if (found) {
+#pragma unroll
+          for (int e = 0; e < kSelectAll / kSelectThreads; ++e)
+#pragma unroll
+            for (int z = 0; z < 3; ++z) c[z] += k[e] >= q[z];
+        } else {
+          for (int t = a + tid; t < b; t += kSelectThreads) {
+            const uint32_t key = weight_key(__ldg(w + t));
+#pragma unroll
+            for (int z = 0; z < 3; ++z) c[z] += key >= q[z];
+          }
+        }
+        // listed keys: sums below 2^16, two to a word
+        uint2 r;
+        int n[3];
+        if (found) {
+          r = sum2(c[0] | (c[1] << 16), c[2]);
+          n[0] = r.x & 0xffffu, n[1] = r.x >> 16, n[2] = r.y;
+        } else {
+          r = sum2(c[0], c[1]);
+          n[0] = r.x, n[1] = r.y;
+          n[2] = sum2(c[2], 0u).x;
+        }
+#pragma unroll
+        for (int z = 2; z >= 0; --z) {
+          if (n[z] < want) {
+            if (q[z] < hi) hi = q[z], reach_hi = n[z];
+          } else if (q[z] > lo) {
+            lo = q[z];
+            if (n[z] == want) done = true;
+          }
+        }
+      }
+      if (done) {
+        last = lo - 1u;  // exactly those from lo on
+      } else {
+        last = lo;
+        ties = want - reach_hi;
+      }
     }
   }
-  // ascending output: per block of tokens, ranks among the tokens of the last key and among the kept
-  uint32_t eq_base = 0u, sel_base = 0u;
-  const uint32_t below = (1u << lane) - 1u;
-  for (int t0 = 0; t0 < len; t0 += kSelectThreads) {
-    const int t = t0 + tid;
-    bool sel = false, eq = false;
-    if (t < len) {
-      if (t < a || t >= b) {
-        sel = true;
-      } else if (m > 0) {
-        const uint32_t k = weight_key(w[t]);
-        sel = k > prefix;
-        eq = k == prefix;
+  // ---- marks and places, kSelectWords words of 32 tokens at a time
+  uint32_t sel_base = 0u, eq_base = 0u;
+  for (int t0 = 0; t0 < len; t0 += kSelectWords * 32) {
+    const int words = min(kSelectWords, (len - t0 + 31) / 32);
+    __syncthreads();
+    for (int w0 = warp; w0 < words; w0 += 4 * kSelectWarps) {
+      float x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = t0 + (w0 + u * kSelectWarps) * 32 + lane;
+        x[u] = t < len ? __ldg(w + t) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int word = w0 + u * kSelectWarps, t = t0 + word * 32 + lane;
+        const uint32_t k = weight_key(x[u]);
+        const bool competes = t >= a && t < b;
+        const uint32_t gt = __ballot_sync(0xffffffffu, t < len && (!competes || k > last));
+        const uint32_t eq = __ballot_sync(0xffffffffu, t < len && competes && k == last && ties > 0u);
+        if (lane == 0 && word < words) {
+          sm.marks[word][0] = gt;
+          sm.marks[word][1] = eq;
+        }
       }
     }
-    const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) warp_eq[warp] = __popc(eqs);
     __syncthreads();
-    uint32_t rank = eq_base, eq_all = 0u;
-    for (int i2 = 0; i2 < 32; ++i2) {
-      if (i2 < warp) rank += warp_eq[i2];
-      eq_all += warp_eq[i2];
+    constexpr int PER = kSelectWords / kSelectThreads;
+    uint32_t gt[PER], eq[PER], ng = 0u, ne = 0u;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int word = tid * PER + e;
+      gt[e] = word < words ? sm.marks[word][0] : 0u;
+      eq[e] = word < words ? sm.marks[word][1] : 0u;
+      ng += __popc(gt[e]);
+      ne += __popc(eq[e]);
     }
-    if (eq) sel = rank + __popc(eqs & below) < need;
-    const uint32_t sels = __ballot_sync(0xffffffffu, sel);
-    if (lane == 0) warp_sel[warp] = __popc(sels);
+    uint32_t ig = ng, ie = ne;  // inclusive over the warp, then the warps before
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, ig, off), y = __shfl_up_sync(0xffffffffu, ie, off);
+      if (lane >= off) ig += x, ie += y;
+    }
+    if (lane == 31) {
+      sm.warp_sum[warp][0] = ig;
+      sm.warp_sum[warp][1] = ie;
+    }
     __syncthreads();
-    uint32_t at = sel_base, sel_all = 0u;
-    for (int i2 = 0; i2 < 32; ++i2) {
-      if (i2 < warp) at += warp_sel[i2];
-      sel_all += warp_sel[i2];
+    uint32_t all_g = 0u, all_e = 0u;
+    uint32_t pg = ig - ng, pe = ie - ne;
+#pragma unroll
+    for (int k = 0; k < kSelectWarps; ++k) {
+      const uint32_t x = sm.warp_sum[k][0], y = sm.warp_sum[k][1];
+      if (k < warp) pg += x, pe += y;
+      all_g += x;
+      all_e += y;
     }
-    if (sel) keep[at + __popc(sels & below)] = t;
-    eq_base += eq_all;
-    sel_base += sel_all;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int word = tid * PER + e;
+      // of the ties before this word `ties` at most were kept; of its own, the first of what is left
+      const uint32_t before = min(eq_base + pe, ties), left = ties - before;
+      uint32_t take = eq[e];
+      if (__popc(take) > left) take = left == 0u ? 0u : take & (0xffffffffu >> (31 - __fns(take, 0, left)));
+      if (word < words) {
+        sm.marks[word][0] = gt[e] | take;
+        sm.marks[word][1] = sel_base + pg + before - min(eq_base, ties);
+      }
+      pg += __popc(gt[e]);
+      pe += __popc(eq[e]);
+    }
+    sel_base += all_g + min(eq_base + all_e, ties) - min(eq_base, ties);
+    eq_base += all_e;
+    __syncthreads();
+    for (int word = warp; word < words; word += kSelectWarps) {
+      const uint32_t sel = sm.marks[word][0];
+      if ((sel >> lane) & 1u) keep[sm.marks[word][1] + __popc(sel & ((1u << lane) - 1u))] = t0 + word * 32 + lane;
+    }
   }
 }
 
@@ -238,6 +440,7 @@ pa_status pa_evict_select(int32_t n, const int32_t* seq_ids, const int32_t* leng
   if (n < 0) return fail(PA_ERR_INVALID_ARG, "n %d < 0", n);
   if (num_seqs <= 0 || num_kv_heads <= 0 || max_tokens <= 0)
     return fail(PA_ERR_INVALID_ARG, "num_seqs, num_kv_heads and max_tokens must be positive");
+  if (max_tokens > (1 << 30)) return fail(PA_ERR_UNSUPPORTED, "max_tokens %d > 2^30", max_tokens);
   if (budget <= 0) return fail(PA_ERR_INVALID_ARG, "budget %d must be positive", budget);
   if (keep_first < 0 || keep_last < 0 || static_cast<int64_t>(keep_first) + keep_last > budget)
     return fail(PA_ERR_INVALID_ARG, "keep_first %d and keep_last %d must be non-negative and fit in the budget %d",

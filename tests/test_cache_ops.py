@@ -73,7 +73,7 @@ def test_select_refusals(lib):
     assert call(first=-1) == bad and call(last=-1) == bad
     assert call(first=6, last=5) == bad and "budget" in pa.last_error()
     assert call(first=0x7fffffff, last=0x7fffffff) == bad
-    assert call(n=0x7fffffff) == pa.PA_ERR_UNSUPPORTED
+    assert call(n=0x7fffffff) == pa.PA_ERR_UNSUPPORTED and call(tokens=(1 << 30) + 1) == pa.PA_ERR_UNSUPPORTED
 
 
 def test_compact_refusals(lib, pool):

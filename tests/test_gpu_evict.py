@@ -74,6 +74,17 @@ def test_select_long(kind, length, budget):
     check_select(mass, [1, 0], [length, length // 2 + 1], budget, 4, 64)
 
 
+@pytest.mark.parametrize("kind", ["ascending", "descending", "steps", "last block", "stripes", "zeros"])
+@pytest.mark.parametrize("budget", [10, 700, 8000])
+def test_select_orders(kind, budget):
+    """Orders that evenly spaced samples misjudge, and large groups of equal weights."""
+    n = 20011
+    t = torch.arange(n, dtype=torch.float32)
+    w = {"ascending": t, "descending": -t, "steps": (t / 1000).floor(), "last block": (t >= n - 6000) * (t + 1),
+         "stripes": (t % 40 < 2) * (t + 1), "zeros": (t % 7 == 0) * (t + 1)}[kind]
+    check_select(torch.stack([w, w.flip(0)]).view(1, 2, n), [0], [n], budget, 3, 5)
+
+
 def test_select_many_rows():
     mass = weights((300, 2, 130), "ties", 1)
     lengths = [(i * 37) % 131 for i in range(300)]
