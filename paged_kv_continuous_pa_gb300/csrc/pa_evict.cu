@@ -27,33 +27,39 @@ struct SelectParams {
 constexpr int kSelectThreads = 256;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectSamples = 512;
-constexpr int kSelectList = 512;             // keys a warp's list holds
-constexpr int kSelectAll = kSelectList * kSelectWarps;  // that many competing tokens need no sample
-constexpr int kSelectWords = 2048;           // 32-token words marked at once
+constexpr int kSelectSlots = 32;                            // weights a thread can list
+constexpr int kSelectAll = kSelectSlots * kSelectThreads;   // that many competing tokens need no sample
+constexpr int kSelectGroups = 512;                          // groups of 128 tokens marked at once
+constexpr int kSelectBatch = 4;                             // groups a warp loads at once
 
 // The weights in an integer order: a larger weight has a larger key, -0 and +0
-// share one, and NaN comes last (below -infinity).
+// share one, and NaN comes last (0, below -infinity).
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
   const uint32_t u = w == 0.0f ? 0u : __float_as_uint(w);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float key_weight(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
 
 struct SelectSmem {
-  uint32_t list[kSelectAll];   // per warp: keys between the two pivots
-  uint32_t marks[kSelectWords][2];  // per word: tokens above the last key, of exactly the last key; then kept tokens, first place
+  float list[kSelectSlots][kSelectThreads];  // weights between the two pivots, a column to a thread
+  // a group's tokens by lane (four consecutive ones each): above the last weight kept, equal to it; then
+  // kept tokens and ties before the group
+  uint32_t above[kSelectGroups][4], equal[kSelectGroups][4], before[kSelectGroups][2];
   uint32_t count[2][kSelectWarps][2];
   uint32_t warp_sum[kSelectWarps][2];
-  uint32_t pivot[2];
+  float pivot[2];
   int overflow;
 };
 
 // One warp: a key that `want` of the samples reach, or a few more.
-__device__ __forceinline__ uint32_t sample_pivot(const uint32_t* samples, int want, int lane) {
+__device__ __forceinline__ uint32_t sample_pivot(const float* samples, int want, int lane) {
   constexpr int PER = kSelectSamples / 32;
   uint32_t k[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) k[i] = samples[i * 32 + lane];
+  for (int i = 0; i < PER; ++i) k[i] = weight_key(samples[i * 32 + lane]);
   uint32_t lo = 0u, hi = 0xffffffffu;  // as many reach lo, fewer reach hi
   while (hi - lo > 1u) {
     const uint32_t mid = lo + (hi - lo) / 2;
@@ -71,22 +77,43 @@ __device__ __forceinline__ uint32_t sample_pivot(const uint32_t* samples, int wa
   return lo;
 }
 
+// kSelectBatch groups of 128 tokens for a warp, `stride` tokens apart, four tokens
+// to a lane: x[u][e] is token t0 + u * stride + e (0 behind `len`).  One uniform
+// branch around all loads, so that none waits for another.
+__device__ __forceinline__ void load_groups(const float* w, bool vec, int t0, int stride, int len, float (&x)[kSelectBatch][4]) {
+  if (vec && t0 + (kSelectBatch - 1) * stride + 4 <= len) {
+#pragma unroll
+    for (int u = 0; u < kSelectBatch; ++u) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(w + t0 + u * stride));
+      x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kSelectBatch; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = t0 + u * stride + e;
+        x[u][e] = t < len ? __ldg(w + t) : 0.0f;
+      }
+  }
+}
+
 // One CTA per (sequence, kv head).  Of the N tokens between the protected ones
-// the m with the largest keys stay; what has to be known is the last key kept
-// and how many tokens of exactly that key stay (the lowest indices).
-//   1. 512 samples, evenly spaced, give two pivots that enclose the m-th key
+// the m with the largest weights stay; what has to be known is the last weight
+// kept and how many tokens of exactly that weight stay (the lowest indices).
+//   1. 512 samples, evenly spaced, give two pivots that enclose the m-th weight
 //      (3.5 standard deviations of a sample rank to either side).
-//   2. One pass over the weights counts the keys from the upper pivot on and those of
-//      exactly the lower one, and lists the keys between the two (a few in a
-//      hundred; no sample is taken where all fit).
-//   3. Bisection over the list, three pivots a step, finds the last key.
-//   4. A second pass (from L2) marks kept tokens as bits, 32 to a word; counts
-//      over the words place them, in ascending order.
-// Where the pivots miss (the m-th key outside, or a warp's list too short, as a
-// hostile order can bring about) step 3 bisects over the weights themselves.
-// Bound by the read of the weights and the latency of the steps.
-__global__ void __launch_bounds__(kSelectThreads, 5) select_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ SelectSmem sm;
+//   2. One pass counts the weights from the upper pivot on and lists those between
+//      the two (a few in a hundred; no sample is taken where all fit).
+//   3. Bisection over the lists, three pivots a step, finds the last weight.
+//   4. A second pass (from L2) marks the kept tokens as bits; counts over groups of
+//      128 tokens place them, in ascending order.
+// Where the pivots miss (the m-th weight outside, or a thread's list too short,
+// as a hostile order can bring about) step 3 bisects over the weights themselves.
+// Bound by the latency of the steps at the first read's rate: one wave of CTAs.
+__global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ __align__(16) unsigned char select_smem[];
+  SelectSmem& sm = *reinterpret_cast<SelectSmem*>(select_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int i = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   const int seq = __ldg(p.seq_ids + i), len = __ldg(p.lengths + i);
@@ -101,6 +128,7 @@ __global__ void __launch_bounds__(kSelectThreads, 5) select_kernel(const __grid_
     return;
   }
   const float* w = p.mass + (static_cast<size_t>(seq) * p.Hkv + h) * p.max_tokens;
+  const bool vec = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
   const int a = p.keep_first, b = len - p.keep_last, N = b - a;  // tokens [a, b) compete
   const int m = p.budget - p.keep_first - p.keep_last;           // 0 <= m < N
   // sums over the CTA of two counts; alternating buffers, so one barrier a sum
@@ -124,18 +152,20 @@ __global__ void __launch_bounds__(kSelectThreads, 5) select_kernel(const __grid_
   };
   uint32_t last = 0xffffffffu, ties = 0u;  // kept: keys above `last`, and the first `ties` tokens of exactly it
   if (m > 0) {
-    uint32_t low = 0u, high = 0xffffffffu;  // no key is that high
+    float low = -INFINITY, high = INFINITY;
     if (N > kSelectAll) {
+      float* samples = sm.list[0];
       for (int k = tid; k < kSelectSamples; k += kSelectThreads)
-        sm.list[k] = weight_key(__ldg(w + a + static_cast<int>((static_cast<long long>(2 * k + 1) * N) / (2 * kSelectSamples))));
+        samples[k] = __ldg(w + a + static_cast<int>((static_cast<long long>(2 * k + 1) * N) / (2 * kSelectSamples)));
       __syncthreads();
       if (warp < 2) {
         const float rank = static_cast<float>(m) * kSelectSamples / N;
         const float off = 3.5f * sqrtf(rank * (1.0f - rank / kSelectSamples)) + 2.0f;
         const int want = static_cast<int>(warp == 0 ? rank - off : rank + off + 1.0f);
-        uint32_t pivot = warp == 0 ? 0xffffffffu : 0u;
-        if (want >= 1 && want <= kSelectSamples) pivot = sample_pivot(sm.list, want, lane);
-        if (lane == 0) sm.pivot[warp] = pivot;
+        uint32_t pivot = 0u;
+        if (want >= 1 && want <= kSelectSamples) pivot = sample_pivot(samples, want, lane);
+        // no pivot, or a NaN: every number
+        if (lane == 0) sm.pivot[warp] = pivot == 0u ? (warp == 0 ? INFINITY : -INFINITY) : key_weight(pivot);
       }
       __syncthreads();
       high = sm.pivot[0];
@@ -143,68 +173,73 @@ __global__ void __launch_bounds__(kSelectThreads, 5) select_kernel(const __grid_
     }
     if (tid == 0) sm.overflow = 0;
     __syncthreads();
-    uint32_t above = 0u, equal = 0u;
-    int listed = 0;  // of this warp
-    const uint32_t below = (1u << lane) - 1u;
-    uint32_t* mine = sm.list + warp * kSelectList;
-    constexpr int UNROLL = 8;
-    for (int t0 = a + tid; t0 - tid < b; t0 += UNROLL * kSelectThreads) {
-      float x[UNROLL];
+    uint32_t from_high = 0u;
+    int listed = 0;  // of this thread
+    constexpr int STRIDE = kSelectWarps * 128;
+    // four comparisons and a store in predicates, no branch: a weight between the pivots goes to the next
+    // slot, or the last one over and over (which `overflow` reports)
+    auto list4 = [&](const float(&x)[4]) {
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int t = t0 + u * kSelectThreads;
-        x[u] = t < b ? __ldg(w + t) : 0.0f;
+      for (int e = 0; e < 4; ++e) {
+        from_high += x[e] >= high;
+        const bool in = x[e] > low && x[e] < high;
+        if (in) sm.list[min(listed, kSelectSlots - 1)][tid] = x[e];
+        listed += in;
+      }
+    };
+    for (int g0 = a / 128 * 128; g0 < b; g0 += kSelectBatch * STRIDE) {
+      const int t0 = g0 + warp * 128 + lane * 4;
+      float x[kSelectBatch][4];
+      load_groups(w, vec, t0, STRIDE, b, x);
+      if (g0 < a || g0 + kSelectBatch * STRIDE > b) {
+#pragma unroll
+        for (int u = 0; u < kSelectBatch; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = t0 + u * STRIDE + e;
+            if (t < a || t >= b) x[u][e] = NAN;  // in no comparison
+          }
       }
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const bool in = t0 + u * kSelectThreads < b;
-        const uint32_t k = weight_key(x[u]);
-        above += in && k >= high;
-        equal += in && k == low && k < high;
-        const bool between = in && k > low && k < high;
-        const uint32_t who = __ballot_sync(0xffffffffu, between);
-        if (who != 0u) {
-          const int at = listed + __popc(who & below);
-          if (between && at < kSelectList) mine[at] = k;
-          listed += __popc(who);
-        }
+      for (int u = 0; u < kSelectBatch; ++u) list4(x[u]);
+    }
+    if (listed > kSelectSlots) sm.overflow = 1;
+    const uint2 s = sum2(from_high, listed);
+    const int between = static_cast<int>(s.y), need = m - static_cast<int>(s.x);  // of the weights below `high`
+    bool found = !sm.overflow && need > 0 && low < high;
+    bool at_low = false;
+    if (found && need > between) {
+      // weights equal to `low` come next (many equal ones, or -infinity), then, behind -infinity, NaNs
+      uint32_t same = 0u;
+      for (int t = a + tid; t < b; t += kSelectThreads) same += __ldg(w + t) == low;
+      const int n = static_cast<int>(sum2(same, 0u).x);
+      at_low = need <= between + n || low == -INFINITY;
+      if (at_low) {
+        last = need <= between + n ? weight_key(low) : 0u;
+        ties = need <= between + n ? need - between : need - between - n;
+      } else {
+        found = false;
       }
     }
-    if (lane == 0 && listed > kSelectList) sm.overflow = 1;
-    const uint2 s = sum2(above, equal);
-    const int between = static_cast<int>(sum2(lane == 0 ? listed : 0, 0u).x);
-    const int need = m - static_cast<int>(s.x);  // of the keys below `high`
-    const bool found = !sm.overflow && need > 0 && need <= between + static_cast<int>(s.y);
-    if (found && need > between) {
-      last = low;
-      ties = need - between;
-    } else {
-      // the last key lies between two keys, fewer than `want` tokens reach hi, as many or more reach lo: over the
-      // listed keys, or (the pivots missed) over all
-      uint32_t lo = found ? low : 0u, hi = found ? high : 0xffffffffu;
+    if (!at_low) {
+      if (found)
+        for (int e = 0; e < listed; ++e) sm.list[e][tid] = __uint_as_float(weight_key(sm.list[e][tid]));  // keys from here on
+      // the last key lies in [lo, hi): fewer than `want` reach hi, as many or more reach lo: of the listed
+      // weights, or (the pivots missed) of all
+      uint32_t lo = found ? weight_key(low) : 0u, hi = found ? weight_key(high) : 0xffffffffu;
       const int want = found ? need : m;
-      uint32_t k[kSelectAll / kSelectThreads];
-#pragma unroll
-      for (int e = 0; e < kSelectAll / kSelectThreads; ++e) k[e] = 0u;
-      if (found) {
-#pragma unroll
-        for (int e = 0; e < kSelectAll / kSelectThreads; ++e) {
-          const int at = e * 32 + lane;
-          if (at < listed) k[e] = mine[at];
-        }
-      }
       int reach_hi = 0;
-      bool done = false;
-      while (hi - lo > 1u && !done) {
+      while (hi - lo > 1u) {
         const uint32_t step = (hi - lo) / 4;
         uint32_t q[3] = {lo + step, lo + 2 * step, lo + 3 * step};
         if (step == 0u) q[0] = q[1] = q[2] = lo + 1u;
         uint32_t c[3] = {0u, 0u, 0u};
         if (found) {
+          for (int e = 0; e < listed; ++e) {
+            const uint32_t key = __float_as_uint(sm.list[e][tid]);
 #pragma unroll
-          for (int e = 0; e < kSelectAll / kSelectThreads; ++e)
-#pragma unroll
-            for (int z = 0; z < 3; ++z) c[z] += k[e] >= q[z];
+            for (int z = 0; z < 3; ++z) c[z] += key >= q[z];
+          }
         } else {
           for (int t = a + tid; t < b; t += kSelectThreads) {
             const uint32_t key = weight_key(__ldg(w + t));
@@ -212,72 +247,93 @@ __global__ void __launch_bounds__(kSelectThreads, 5) select_kernel(const __grid_
             for (int z = 0; z < 3; ++z) c[z] += key >= q[z];
           }
         }
-        // listed keys: sums below 2^16, two to a word
-        uint2 r;
         int n[3];
-        if (found) {
-          r = sum2(c[0] | (c[1] << 16), c[2]);
+        if (found) {  // sums below 2^16, two to a word
+          const uint2 r = sum2(c[0] | (c[1] << 16), c[2]);
           n[0] = r.x & 0xffffu, n[1] = r.x >> 16, n[2] = r.y;
         } else {
-          r = sum2(c[0], c[1]);
+          const uint2 r = sum2(c[0], c[1]);
           n[0] = r.x, n[1] = r.y;
           n[2] = sum2(c[2], 0u).x;
         }
+        bool done = false;
 #pragma unroll
         for (int z = 2; z >= 0; --z) {
           if (n[z] < want) {
             if (q[z] < hi) hi = q[z], reach_hi = n[z];
           } else if (q[z] > lo) {
             lo = q[z];
-            if (n[z] == want) done = true;
+            done = n[z] == want;
           }
         }
+        if (done) {  // exactly those from lo on: above the key before it, without ties
+          lo = lo - 1u;
+          if (lo == 0x7fffffffu) lo -= 1u;  // the pattern of -0, which as a number equals the 0 behind it
+          reach_hi = want;
+          break;
+        }
       }
-      if (done) {
-        last = lo - 1u;  // exactly those from lo on
-      } else {
-        last = lo;
-        ties = want - reach_hi;
-      }
+      last = lo;
+      ties = want - reach_hi;
     }
   }
-  // ---- marks and places, kSelectWords words of 32 tokens at a time
-  uint32_t sel_base = 0u, eq_base = 0u;
-  for (int t0 = 0; t0 < len; t0 += kSelectWords * 32) {
-    const int words = min(kSelectWords, (len - t0 + 31) / 32);
+  // ---- marks and places, kSelectGroups groups of 128 tokens at a time.  Kept: weights above `edge`, and the
+  // first `ties` equal to it.  Keys below -infinity's: every number stays, and `ties` NaNs; no weight has the
+  // key 0xffffffff: none stays.
+  const bool numbers = last < weight_key(-INFINITY);
+  const float edge = numbers || last == 0xffffffffu ? NAN : key_weight(last);
+  uint32_t kept_base = 0u, tie_base = 0u;
+  for (int c0 = 0; c0 < len; c0 += kSelectGroups * 128) {
+    const int groups = min(kSelectGroups, (len - c0 + 127) / 128);
     __syncthreads();
-    for (int w0 = warp; w0 < words; w0 += 4 * kSelectWarps) {
-      float x[4];
+    for (int g0 = warp; g0 < groups; g0 += kSelectBatch * kSelectWarps) {
+      const int t0 = c0 + g0 * 128 + lane * 4;
+      float x[kSelectBatch][4];
+      load_groups(w, vec, t0, kSelectWarps * 128, len, x);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int t = t0 + (w0 + u * kSelectWarps) * 32 + lane;
-        x[u] = t < len ? __ldg(w + t) : 0.0f;
-      }
+      for (int u = 0; u < kSelectBatch; ++u) {
+        const int g = g0 + u * kSelectWarps, t = t0 + u * kSelectWarps * 128;
+        uint32_t gt[4], eq[4] = {0u, 0u, 0u, 0u};
+        if (c0 + g * 128 >= a && c0 + g * 128 + 128 <= b && !numbers) {  // the whole group competes
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int word = w0 + u * kSelectWarps, t = t0 + word * 32 + lane;
-        const uint32_t k = weight_key(x[u]);
-        const bool competes = t >= a && t < b;
-        const uint32_t gt = __ballot_sync(0xffffffffu, t < len && (!competes || k > last));
-        const uint32_t eq = __ballot_sync(0xffffffffu, t < len && competes && k == last && ties > 0u);
-        if (lane == 0 && word < words) {
-          sm.marks[word][0] = gt;
-          sm.marks[word][1] = eq;
+          for (int e = 0; e < 4; ++e) gt[e] = __ballot_sync(0xffffffffu, x[u][e] > edge);
+          if (ties > 0u) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) eq[e] = __ballot_sync(0xffffffffu, x[u][e] == edge);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool competes = t + e >= a && t + e < b;
+            const bool more = numbers ? x[u][e] == x[u][e] : x[u][e] > edge;
+            const bool same = numbers ? x[u][e] != x[u][e] : x[u][e] == edge;
+            gt[e] = __ballot_sync(0xffffffffu, t + e < len && (!competes || more));
+            eq[e] = __ballot_sync(0xffffffffu, competes && same && ties > 0u);
+          }
+        }
+        if (lane == 0 && g < groups) {
+          *reinterpret_cast<uint4*>(sm.above[g]) = make_uint4(gt[0], gt[1], gt[2], gt[3]);
+          *reinterpret_cast<uint4*>(sm.equal[g]) = make_uint4(eq[0], eq[1], eq[2], eq[3]);
         }
       }
     }
     __syncthreads();
-    constexpr int PER = kSelectWords / kSelectThreads;
-    uint32_t gt[PER], eq[PER], ng = 0u, ne = 0u;
+    // kept tokens and ties before each group: kSelectGroups / kSelectThreads groups to a thread
+    constexpr int PER = kSelectGroups / kSelectThreads;
+    uint32_t ng[PER], ne[PER], sg = 0u, se = 0u;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const int word = tid * PER + e;
-      gt[e] = word < words ? sm.marks[word][0] : 0u;
-      eq[e] = word < words ? sm.marks[word][1] : 0u;
-      ng += __popc(gt[e]);
-      ne += __popc(eq[e]);
+    for (int k = 0; k < PER; ++k) {
+      const int g = tid * PER + k;
+      ng[k] = ne[k] = 0u;
+      if (g < groups) {
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.above[g]), y = *reinterpret_cast<const uint4*>(sm.equal[g]);
+        ng[k] = __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w);
+        ne[k] = __popc(y.x) + __popc(y.y) + __popc(y.z) + __popc(y.w);
+      }
+      sg += ng[k];
+      se += ne[k];
     }
-    uint32_t ig = ng, ie = ne;  // inclusive over the warp, then the warps before
+    uint32_t ig = sg, ie = se;  // inclusive over the warp, then the warps before
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, ig, off), y = __shfl_up_sync(0xffffffffu, ie, off);
@@ -288,8 +344,7 @@ __global__ void __launch_bounds__(kSelectThreads, 5) select_kernel(const __grid_
       sm.warp_sum[warp][1] = ie;
     }
     __syncthreads();
-    uint32_t all_g = 0u, all_e = 0u;
-    uint32_t pg = ig - ng, pe = ie - ne;
+    uint32_t all_g = 0u, all_e = 0u, pg = ig - sg, pe = ie - se;
 #pragma unroll
     for (int k = 0; k < kSelectWarps; ++k) {
       const uint32_t x = sm.warp_sum[k][0], y = sm.warp_sum[k][1];
@@ -298,25 +353,40 @@ __global__ void __launch_bounds__(kSelectThreads, 5) select_kernel(const __grid_
       all_e += y;
     }
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const int word = tid * PER + e;
-      // of the ties before this word `ties` at most were kept; of its own, the first of what is left
-      const uint32_t before = min(eq_base + pe, ties), left = ties - before;
-      uint32_t take = eq[e];
-      if (__popc(take) > left) take = left == 0u ? 0u : take & (0xffffffffu >> (31 - __fns(take, 0, left)));
-      if (word < words) {
-        sm.marks[word][0] = gt[e] | take;
-        sm.marks[word][1] = sel_base + pg + before - min(eq_base, ties);
+    for (int k = 0; k < PER; ++k) {
+      const int g = tid * PER + k;
+      if (g < groups) {
+        sm.before[g][0] = kept_base + pg + min(tie_base + pe, ties) - min(tie_base, ties);
+        sm.before[g][1] = tie_base + pe;
       }
-      pg += __popc(gt[e]);
-      pe += __popc(eq[e]);
+      pg += ng[k];
+      pe += ne[k];
     }
-    sel_base += all_g + min(eq_base + all_e, ties) - min(eq_base, ties);
-    eq_base += all_e;
+    kept_base += all_g + min(tie_base + all_e, ties) - min(tie_base, ties);
+    tie_base += all_e;
     __syncthreads();
-    for (int word = warp; word < words; word += kSelectWarps) {
-      const uint32_t sel = sm.marks[word][0];
-      if ((sel >> lane) & 1u) keep[sm.marks[word][1] + __popc(sel & ((1u << lane) - 1u))] = t0 + word * 32 + lane;
+    const uint32_t below = (1u << lane) - 1u;
+    for (int g = warp; g < groups; g += kSelectWarps) {
+      const uint4 x = *reinterpret_cast<const uint4*>(sm.above[g]);
+      uint32_t keep_bits = ((x.x >> lane) & 1u) | ((x.y >> lane) & 1u) << 1 | ((x.z >> lane) & 1u) << 2 | ((x.w >> lane) & 1u) << 3;
+      uint32_t at = sm.before[g][0] + __popc(x.x & below) + __popc(x.y & below) + __popc(x.z & below) + __popc(x.w & below);
+      if (ties > 0u) {
+        const uint4 y = *reinterpret_cast<const uint4*>(sm.equal[g]);
+        const uint32_t tie0 = sm.before[g][1];
+        uint32_t tie = tie0 + __popc(y.x & below) + __popc(y.y & below) + __popc(y.z & below) + __popc(y.w & below);
+        at += min(tie, ties) - min(tie0, ties);  // ties of the lanes before that stayed
+        const uint32_t eq[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t same = (eq[e] >> lane) & 1u;
+          if (same && tie < ties) keep_bits |= 1u << e;
+          tie += same;
+        }
+      }
+      const int t = c0 + g * 128 + lane * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((keep_bits >> e) & 1u) keep[at++] = t + e;
     }
   }
 }
@@ -463,9 +533,12 @@ pa_status pa_evict_select(int32_t n, const int32_t* seq_ids, const int32_t* leng
   p.budget = budget;
   p.keep_first = keep_first;
   p.keep_last = keep_last;
-  pa::select_kernel<<<static_cast<unsigned>(units), pa::kSelectThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  static std::atomic<unsigned long long> smem_done{0};
+  cudaError_t e = pa::allow_dynamic_smem(pa::select_kernel, smem_done, sizeof(pa::SelectSmem));
+  if (e != cudaSuccess) return cuda_fail(e, "select shared memory");
+  e = pa::launch_kernel(pa::select_kernel, dim3(static_cast<unsigned>(units)), dim3(pa::kSelectThreads),
+                        sizeof(pa::SelectSmem), static_cast<cudaStream_t>(stream), false, p);
   pa::count_launch();
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "select launch");
 }
 

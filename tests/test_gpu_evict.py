@@ -85,6 +85,17 @@ def test_select_orders(kind, budget):
     check_select(torch.stack([w, w.flip(0)]).view(1, 2, n), [0], [n], budget, 3, 5)
 
 
+@pytest.mark.parametrize("n", [90, 12000])
+def test_select_between_kinds(n):
+    """The last kept weight on every border: positive, zeros of both signs, negative, lowest, -infinity, NaN."""
+    g = torch.Generator().manual_seed(n)
+    parts = [torch.tensor([2.0, 1e-45, 0.0, -0.0, -1e-45, -3.0, torch.finfo(torch.float32).min, float("-inf"), float("nan")])]
+    w = parts[0].repeat(n // 9 + 1)[:n][torch.randperm(n, generator=g)]
+    mass = w.view(1, 1, n)
+    for budget in sorted({1, n - 1} | {n * k // 9 + d for k in range(1, 9) for d in (-1, 0, 1)}):
+        check_select(mass, [0], [n], budget)
+
+
 def test_select_many_rows():
     mass = weights((300, 2, 130), "ties", 1)
     lengths = [(i * 37) % 131 for i in range(300)]
