@@ -403,18 +403,13 @@ struct CompactParams {
   const int32_t* block_tables;
   int32_t* status;
   int32_t n, num_seqs, max_blocks, num_pages, P, Hkv, row_bytes, budget;
+  int32_t stripes;  // CTAs that share a (sequence, kv head, K | V), a column of 16-byte pieces each
 };
 
 constexpr int kCompactThreads = 256;
 constexpr int kCompactUnroll = 4;
-
-// The physical page of token t of a sequence, or -1 after recording an error.
-__device__ __forceinline__ int page_of(const CompactParams& p, const int32_t* table, int t) {
-  const int page = __ldg(table + t / p.P);
-  if (page >= 0 && page < p.num_pages) return page;
-  record_error(p.status, ST_OUT_OF_RANGE);
-  return -1;
-}
+constexpr int kCompactCtas = 608;
+constexpr int kCompactBlock = 2048;  // kept tokens looked up at once
 
 // keep[j] if it is a token of the sequence above the one before it (the order
 // that moving in place relies on), else -1 after recording an error.
@@ -425,73 +420,108 @@ __device__ __forceinline__ int kept_token(const CompactParams& p, const int32_t*
   return -1;
 }
 
-// One CTA per (sequence, kv head, K | V | weights).  The kept tokens move in
-// order, a tile at a time: every thread loads its pieces of the tile, the CTA
-// meets, and the tile is stored.  Kept tokens ascend, so the j-th comes from a
-// token t >= j: a tile's stores reach only slots that earlier tiles and this
-// one read, never a later tile's, and the move is safe in place.
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_constant__ CompactParams p) {
-  const int operands = p.mass != nullptr ? 3 : 2;
-  const int op = blockIdx.x % operands;
-  const int unit = blockIdx.x / operands;
-  const int i = unit / p.Hkv, h = unit % p.Hkv, tid = threadIdx.x;
+// 16 bytes that another thread of the CTA may overwrite later: an ordinary load
+// (never through the read-only path), not kept in L1.
+__device__ __forceinline__ uint4 load_piece(const unsigned char* a) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(a)
+               : "memory");
+  return v;
+}
+
+// One CTA per (sequence, kv head, K | V, stripe), and one per (sequence, kv head)
+// for the weights.  The kept tokens move in order, a tile at a time: every thread
+// loads its pieces of the tile, the CTA meets, and the tile is stored.  Kept
+// tokens ascend, so the j-th comes from a token t >= j: a tile's stores reach only
+// slots that earlier tiles and this one read, never a later tile's, and the move
+// is safe in place -- also with the next tile's loads on their way before the
+// stores.  Stripes of a row are independent of one another; they fill the GPU
+// where the sequences alone would not.
+// Bound by the read and the write of the kept rows.
+__global__ void __launch_bounds__(kCompactThreads, 6) compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ int2 from[kCompactBlock];  // page (-1: not moved) and token of a kept token
+  const int per_head = 2 * p.stripes;
+  const int rows_ctas = p.n * p.Hkv * per_head, tid = threadIdx.x;
+  const bool weights = static_cast<int>(blockIdx.x) >= rows_ctas;
+  const int unit = weights ? blockIdx.x - rows_ctas : blockIdx.x / per_head;
+  const int op = blockIdx.x / p.stripes % 2, stripe = blockIdx.x % p.stripes;  // of K and V
+  const int i = unit / p.Hkv, h = unit % p.Hkv;
   const int src = __ldg(p.seq_ids + i), dst = p.dst_seq_ids != nullptr ? __ldg(p.dst_seq_ids + i) : src;
   const int len = __ldg(p.lengths + i);
   if (src < 0 || src >= p.num_seqs || dst < 0 || dst >= p.num_seqs || len < 0 || len > p.max_blocks * p.P) {
-    if (h == 0 && op == 0 && tid == 0) record_error(p.status, ST_OUT_OF_RANGE);
+    if (tid == 0) record_error(p.status, ST_OUT_OF_RANGE);
     return;
   }
   const int count = min(len, p.budget);
   const int32_t* keep = p.keep + static_cast<size_t>(unit) * p.budget;
-  if (op == 2) {
+  if (weights) {
     const size_t T = static_cast<size_t>(p.max_blocks) * p.P;
-    const float* from = p.mass + (static_cast<size_t>(src) * p.Hkv + h) * T;
-    float* to = p.mass + (static_cast<size_t>(dst) * p.Hkv + h) * T;
+    const float* from_w = p.mass + (static_cast<size_t>(src) * p.Hkv + h) * T;
+    float* to_w = p.mass + (static_cast<size_t>(dst) * p.Hkv + h) * T;
     for (int j0 = 0; j0 < count; j0 += kCompactThreads * kCompactUnroll) {
       float v[kCompactUnroll];
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) {
         const int j = j0 + u * kCompactThreads + tid;
         const int t = j < count ? kept_token(p, keep, j, len) : -1;
-        v[u] = t >= 0 ? from[t] : 0.0f;
+        v[u] = t >= 0 ? from_w[t] : 0.0f;
       }
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) {
         const int j = j0 + u * kCompactThreads + tid;
-        if (j < count) to[j] = v[u];
+        if (j < count) to_w[j] = v[u];
       }
     }
-    for (int j = count + tid; j < len; j += kCompactThreads) to[j] = 0.0f;
+    for (int j = count + tid; j < len; j += kCompactThreads) to_w[j] = 0.0f;
     return;
   }
   const int32_t* from_table = p.block_tables + static_cast<size_t>(src) * p.max_blocks;
   const int32_t* to_table = p.block_tables + static_cast<size_t>(dst) * p.max_blocks;
   unsigned char* pool = p.pool[op];
-  const int pieces = p.row_bytes / 16, rows = kCompactThreads / pieces;  // rows moved side by side
-  const int piece = tid % pieces, r = tid / pieces;
+  const int lg_p = 31 - __clz(p.P);
+  const int pieces = p.row_bytes / 16 / p.stripes, rows = kCompactThreads / pieces;  // rows moved side by side
+  const int r = tid / pieces, offset = (stripe * pieces + tid % pieces) * 16;
   auto address = [&](int page, int t) {
-    return pool + ((static_cast<size_t>(page) * p.Hkv + h) * p.P + t % p.P) * p.row_bytes + piece * 16;
+    return pool + (((static_cast<size_t>(page) * p.Hkv + h) << lg_p) + (t & (p.P - 1))) * p.row_bytes + offset;
   };
-  for (int j0 = 0; j0 < count; j0 += rows * kCompactUnroll) {
-    uint4 v[kCompactUnroll];
-    unsigned char* to[kCompactUnroll];
-#pragma unroll
-    for (int u = 0; u < kCompactUnroll; ++u) {
-      const int j = j0 + u * rows + r;
-      to[u] = nullptr;
-      if (j >= count) continue;
+  for (int b0 = 0; b0 < count; b0 += kCompactBlock) {
+    const int end = min(count, b0 + kCompactBlock);
+    __syncthreads();
+    for (int j = b0 + tid; j < end; j += kCompactThreads) {
       const int t = kept_token(p, keep, j, len);
-      const int page = t >= 0 ? page_of(p, from_table, t) : -1;
-      const int to_page = page_of(p, to_table, j);
-      if (page < 0 || to_page < 0) continue;
-      v[u] = *reinterpret_cast<const uint4*>(address(page, t));
-      to[u] = address(to_page, j);
+      int page = t >= 0 ? __ldg(from_table + (t >> lg_p)) : -1;
+      const int to_page = __ldg(to_table + (j >> lg_p));
+      if (t >= 0 && (page < 0 || page >= p.num_pages || to_page < 0 || to_page >= p.num_pages)) {
+        record_error(p.status, ST_OUT_OF_RANGE);
+        page = -1;
+      }
+      from[j - b0] = make_int2(t == j && src == dst ? -1 : page, t);  // a token in its place already stays
     }
     __syncthreads();
+    uint4 now[kCompactUnroll], next[kCompactUnroll];
+    auto load = [&](int j0, uint4(&v)[kCompactUnroll]) {
 #pragma unroll
-    for (int u = 0; u < kCompactUnroll; ++u)
-      if (to[u] != nullptr) *reinterpret_cast<uint4*>(to[u]) = v[u];
+      for (int u = 0; u < kCompactUnroll; ++u) {
+        const int j = j0 + u * rows + r;
+        const int2 f = j < end ? from[j - b0] : make_int2(-1, 0);
+        v[u] = load_piece(f.x >= 0 ? address(f.x, f.y) : pool);  // (a piece that is not moved: any valid address)
+      }
+    };
+    load(b0, now);
+    for (int j0 = b0; j0 < end; j0 += rows * kCompactUnroll) {
+      if (j0 + rows * kCompactUnroll < end) load(j0 + rows * kCompactUnroll, next);
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kCompactUnroll; ++u) {
+        const int j = j0 + u * rows + r;
+        if (j < end && from[j - b0].x >= 0) *reinterpret_cast<uint4*>(address(__ldg(to_table + (j >> lg_p)), j)) = now[u];
+      }
+#pragma unroll
+      for (int u = 0; u < kCompactUnroll; ++u) now[u] = next[u];
+    }
   }
 }
 
@@ -556,7 +586,12 @@ pa_status pa_evict_compact(const pa_pool* pool, int32_t n, const int32_t* seq_id
   if (budget <= 0) return fail(PA_ERR_INVALID_ARG, "budget %d must be positive", budget);
   if (n == 0) return PA_OK;
   if (!seq_ids || !lengths || !keep || !block_tables) return fail(PA_ERR_INVALID_ARG, "compact: a device pointer is NULL");
-  const int64_t units = static_cast<int64_t>(n) * d.num_kv_heads * (mass != nullptr ? 3 : 2);
+  const int row_bytes = d.head_dim * static_cast<int>(pa::elt_bytes(d.kv_dtype));
+  const int64_t heads = static_cast<int64_t>(n) * d.num_kv_heads;
+  // stripes of 64 bytes and more until there are about four CTAs to an SM
+  int stripes = 1;
+  while (heads * 2 * stripes < pa::kCompactCtas && row_bytes / stripes > 64) stripes *= 2;
+  const int64_t units = heads * (2 * stripes + (mass != nullptr ? 1 : 0));
   if (units > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "%lld units of work in one call", (long long)units);
   pa::CompactParams p{};
   p.pool[0] = static_cast<unsigned char*>(pool->k);
@@ -574,7 +609,8 @@ pa_status pa_evict_compact(const pa_pool* pool, int32_t n, const int32_t* seq_id
   p.num_pages = d.num_pages;
   p.P = d.page_size;
   p.Hkv = d.num_kv_heads;
-  p.row_bytes = d.head_dim * static_cast<int>(pa::elt_bytes(d.kv_dtype));
+  p.row_bytes = row_bytes;
+  p.stripes = stripes;
   p.budget = budget;
   pa::compact_kernel<<<static_cast<unsigned>(units), pa::kCompactThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   pa::count_launch();
