@@ -409,7 +409,7 @@ struct CompactParams {
 constexpr int kCompactThreads = 256;
 constexpr int kCompactUnroll = 4;
 constexpr int kCompactCtas = 608;
-constexpr int kCompactBlock = 2048;  // kept tokens looked up at once
+constexpr int kCompactBlock = 1024;  // kept tokens looked up at once
 
 // keep[j] if it is a token of the sequence above the one before it (the order
 // that moving in place relies on), else -1 after recording an error.
@@ -440,8 +440,8 @@ __device__ __forceinline__ uint4 load_piece(const unsigned char* a) {
 // stores.  Stripes of a row are independent of one another; they fill the GPU
 // where the sequences alone would not.
 // Bound by the read and the write of the kept rows.
-__global__ void __launch_bounds__(kCompactThreads, 6) compact_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ int2 from[kCompactBlock];  // page (-1: not moved) and token of a kept token
+__global__ void __launch_bounds__(kCompactThreads, 4) compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ long long from[kCompactBlock], to[kCompactBlock];  // byte offsets of a kept token's row (from -1: not moved)
   const int per_head = 2 * p.stripes;
   const int rows_ctas = p.n * p.Hkv * per_head, tid = threadIdx.x;
   const bool weights = static_cast<int>(blockIdx.x) >= rows_ctas;
@@ -484,40 +484,41 @@ __global__ void __launch_bounds__(kCompactThreads, 6) compact_kernel(const __gri
   const int lg_p = 31 - __clz(p.P);
   const int pieces = p.row_bytes / 16 / p.stripes, rows = kCompactThreads / pieces;  // rows moved side by side
   const int r = tid / pieces, offset = (stripe * pieces + tid % pieces) * 16;
-  auto address = [&](int page, int t) {
-    return pool + (((static_cast<size_t>(page) * p.Hkv + h) << lg_p) + (t & (p.P - 1))) * p.row_bytes + offset;
+  const unsigned char* base = pool + offset;
+  auto row_offset = [&](int page, int t) {
+    return static_cast<long long>((((static_cast<size_t>(page) * p.Hkv + h) << lg_p) + (t & (p.P - 1))) * p.row_bytes);
   };
   for (int b0 = 0; b0 < count; b0 += kCompactBlock) {
-    const int end = min(count, b0 + kCompactBlock);
+    const int n = min(count - b0, kCompactBlock);
     __syncthreads();
-    for (int j = b0 + tid; j < end; j += kCompactThreads) {
-      const int t = kept_token(p, keep, j, len);
-      int page = t >= 0 ? __ldg(from_table + (t >> lg_p)) : -1;
+    for (int k = tid; k < n; k += kCompactThreads) {
+      const int j = b0 + k, t = kept_token(p, keep, j, len);
+      const int page = t >= 0 ? __ldg(from_table + (t >> lg_p)) : -1;
       const int to_page = __ldg(to_table + (j >> lg_p));
-      if (t >= 0 && (page < 0 || page >= p.num_pages || to_page < 0 || to_page >= p.num_pages)) {
-        record_error(p.status, ST_OUT_OF_RANGE);
-        page = -1;
-      }
-      from[j - b0] = make_int2(t == j && src == dst ? -1 : page, t);  // a token in its place already stays
+      bool moves = page >= 0 && page < p.num_pages && to_page >= 0 && to_page < p.num_pages;
+      if (t >= 0 && !moves) record_error(p.status, ST_OUT_OF_RANGE);
+      if (t == j && src == dst) moves = false;  // in its place already
+      from[k] = moves ? row_offset(page, t) : -1;
+      to[k] = moves ? row_offset(to_page, j) : 0;
     }
     __syncthreads();
+    const int step = rows * kCompactUnroll;
     uint4 now[kCompactUnroll], next[kCompactUnroll];
-    auto load = [&](int j0, uint4(&v)[kCompactUnroll]) {
+    auto load = [&](int k0, uint4(&v)[kCompactUnroll]) {
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) {
-        const int j = j0 + u * rows + r;
-        const int2 f = j < end ? from[j - b0] : make_int2(-1, 0);
-        v[u] = load_piece(f.x >= 0 ? address(f.x, f.y) : pool);  // (a piece that is not moved: any valid address)
+        const int k = k0 + u * rows;
+        v[u] = load_piece(base + (k < n ? max(from[k], 0ll) : 0ll));  // (a row that is not moved: any valid address)
       }
     };
-    load(b0, now);
-    for (int j0 = b0; j0 < end; j0 += rows * kCompactUnroll) {
-      if (j0 + rows * kCompactUnroll < end) load(j0 + rows * kCompactUnroll, next);
+    load(r, now);
+    for (int k0 = r; k0 - r < n; k0 += step) {
+      if (k0 - r + step < n) load(k0 + step, next);
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) {
-        const int j = j0 + u * rows + r;
-        if (j < end && from[j - b0].x >= 0) *reinterpret_cast<uint4*>(address(__ldg(to_table + (j >> lg_p)), j)) = now[u];
+        const int k = k0 + u * rows;
+        if (k < n && from[k] >= 0) *reinterpret_cast<uint4*>(const_cast<unsigned char*>(base) + to[k]) = now[u];
       }
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) now[u] = next[u];
