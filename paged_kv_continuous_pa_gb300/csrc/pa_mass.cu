@@ -133,7 +133,8 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
   while (p.cluster < pa::kMassMaxCluster && keys > static_cast<int64_t>(p.cluster) * pa::kMassClusterKeys) p.cluster *= 2;
   const int G = num_q_heads / d.num_kv_heads;
   const int64_t room = (static_cast<int64_t>(pa::kMassScoreBytes) / (G * 4) - 36) / 32 * 32;  // keys whose scores fit
-  const int64_t share = ((keys + 15) / 16 + p.cluster - 1) / p.cluster * 16;
+  // a CTA's share of the longest row, in the kernel's steps (at most four 16-key tiles)
+  const int64_t share = ((keys + 15) / 16 + p.cluster * 4 - 1) / (p.cluster * 4) * 64;
   p.score_keys = static_cast<int32_t>(std::min(room, share));
   if (static_cast<int64_t>(n_rows) * d.num_kv_heads * p.cluster > 0x7fffffff)
     return fail(PA_ERR_UNSUPPORTED, "%d rows of %d kv heads in one call", n_rows, d.num_kv_heads);

@@ -30,7 +30,7 @@ constexpr int kMassSplitKeys = 2048;  // keys per range of the chunks' first lau
 constexpr int kMassBlockKeys = 128;   // keys per CTA of their last launch
 constexpr int kMassRangeKeys = 1024;  // ... on the tile path
 constexpr int kMassSlots = 128;       // columns of a chunk come in tiles of 128 / G rows, 128 slots each
-constexpr int kMassClusterKeys = 2048;             // keys per CTA that a row's cluster aims at
+constexpr int kMassClusterKeys = 4096;             // keys per CTA that a row's cluster aims at
 constexpr int kMassMaxCluster = 8;
 constexpr size_t kMassScoreBytes = 104 * 1024;     // shared memory for a CTA's scores (two CTAs to an SM)
 
@@ -86,6 +86,7 @@ struct MassGeom {
   static constexpr int EP = 16 / ELT;       // elements of a piece
   static constexpr int NPT = RB / 64;       // pieces a lane holds of a row
   static constexpr int STEPS = D / 16;      // MMA k-steps
+  static constexpr int MT = RB < 256 ? 256 / RB : 1;  // 16-key tiles a warp of a row's cluster loads at once (4 KB)
   static constexpr int KP = KVT == KV_F32 ? 3 : 1;
   static constexpr int QP = QB ? 1 : (KVT == KV_E4M3 ? 2 : 3);
 };
@@ -282,7 +283,8 @@ __host__ __device__ constexpr int score_stride(int keys) { return (keys + 31) / 
 
 // One cluster per (row, kv head).  The row's 16-key tiles are dealt to the CTAs
 // in contiguous shares of its own length, and within a CTA to the warps in
-// turn; the loads of a warp's next tile are in flight while it scores one.
+// turn, MT at a time (4 KB of K, 8 KB with f32); the loads of a warp's next tiles
+// are in flight while it scores one's.
 template <int KVT, int D, bool QB>
 __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ? 1 : 2) mass_row_kernel(const __grid_constant__ MassParams p) {
   using Geo = MassGeom<KVT, D, QB>;
@@ -303,7 +305,8 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
     if (rank == 0 && tid == 0) record_error(p.status, ST_OUT_OF_RANGE);
     return;
   }
-  const int tiles = (pos + 16) / 16, share = (tiles + p.cluster - 1) / p.cluster;
+  constexpr int MT = Geo::MT;
+  const int tiles = (pos + 16) / 16, share = (tiles + p.cluster * MT - 1) / (p.cluster * MT) * MT;
   const int tile0 = min(tiles, rank * share), mine = min(tiles, tile0 + share) - tile0;  // this CTA's tiles
   const int stride = score_stride(p.score_keys);
   const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
@@ -316,14 +319,18 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
   __syncthreads();
 
   bool bad = false;
-  // page ids of the warp's next 32 tiles, one to a lane
+  // the warp's k-th MT tiles start at the CTA's tile (warp + 8 k) MT; page ids of the next 32 tiles, one to a lane
   int pages = 0;
-  auto page_of_tile = [&](int k) {  // the warp's k-th tile
-    if (k % 32 == 0) {
-      const int t = (tile0 + warp + (k + lane) * kMassWarps) * 16;
+  auto load = [&](int k, KeyFrag<KVT, D, QB>(&f)[MT]) {
+    if (k % (32 / MT) == 0) {
+      const int t = (tile0 + (warp + (k + lane / MT) * kMassWarps) * MT + lane % MT) * 16;
       pages = t <= pos ? __ldg(table + (t >> lg_p)) : 0;
     }
-    return __shfl_sync(0xffffffffu, pages, k % 32);
+#pragma unroll
+    for (int s = 0; s < MT; ++s) {
+      const int page = __shfl_sync(0xffffffffu, pages, k % (32 / MT) * MT + s);
+      f[s].load(key_rows<Geo::RB>(p, page, h, (tile0 + (warp + k * kMassWarps) * MT + s) * 16, lg_p, bad), g4, t4);
+    }
   };
   auto scores_of = [&](KeyFrag<KVT, D, QB>& f, int t0, float (&c)[1][4]) {
     f.score(q, c);
@@ -334,22 +341,26 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
     c[0][3] = in1 ? __fmul_rn(c[0][3], f1) : -INFINITY;
   };
   ColumnStat st0{-INFINITY, 0.0f}, st1{-INFINITY, 0.0f};
-  const int count = mine > warp ? (mine - warp + kMassWarps - 1) / kMassWarps : 0;  // this warp's tiles
-  KeyFrag<KVT, D, QB> next;
-  if (count > 0) next.load(key_rows<Geo::RB>(p, page_of_tile(0), h, (tile0 + warp) * 16, lg_p, bad), g4, t4);
+  const int count = mine > warp * MT ? (mine - warp * MT + kMassWarps * MT - 1) / (kMassWarps * MT) : 0;  // of this warp
+  KeyFrag<KVT, D, QB> next[MT];
+  if (count > 0) load(0, next);
   for (int k = 0; k < count; ++k) {
-    KeyFrag<KVT, D, QB> now = next;
-    const int local = warp + k * kMassWarps, t0 = (tile0 + local) * 16;
-    if (k + 1 < count)
-      next.load(key_rows<Geo::RB>(p, page_of_tile(k + 1), h, t0 + 16 * kMassWarps, lg_p, bad), g4, t4);
-    float c[1][4];
-    scores_of(now, t0, c);
-    st0.add2(c[0][0], c[0][2]);
-    st1.add2(c[0][1], c[0][3]);
-    if (local * 16 < p.score_keys) {
-      float* s = scores + 2 * t4 * stride + local * 16 + g4;
-      if (2 * t4 < G) s[0] = c[0][0], s[8] = c[0][2];
-      if (2 * t4 + 1 < G) s[stride] = c[0][1], s[stride + 8] = c[0][3];
+    KeyFrag<KVT, D, QB> now[MT];
+#pragma unroll
+    for (int s = 0; s < MT; ++s) now[s] = next[s];
+    if (k + 1 < count) load(k + 1, next);
+#pragma unroll
+    for (int s = 0; s < MT; ++s) {
+      const int local = (warp + k * kMassWarps) * MT + s;
+      float c[1][4];
+      scores_of(now[s], (tile0 + local) * 16, c);
+      st0.add2(c[0][0], c[0][2]);
+      st1.add2(c[0][1], c[0][3]);
+      if (local * 16 < p.score_keys) {
+        float* z = scores + 2 * t4 * stride + local * 16 + g4;
+        if (2 * t4 < G) z[0] = c[0][0], z[8] = c[0][2];
+        if (2 * t4 + 1 < G) z[stride] = c[0][1], z[stride + 8] = c[0][3];
+      }
     }
   }
   // (max, sum) of each column: over the lanes of a warp, the warps, the CTAs
