@@ -57,6 +57,8 @@ def header_functions():
 def load(path: str = LIB_PATH):
     """Load the shared library and declare the C signatures.  Raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -385,58 +387,60 @@ def attention_noalloc(pool: Pool, q, seq_ids, positions, block_tables, out,
                                        _ptr(status), _stream(stream)))
 
 
-def _check_f32(t, name: str, shape):
-    """A float32 tensor of this shape."""
-    import torch
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be float32, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {list(shape)}")
+# The calls below run in a serving loop beside small kernels: one pass over a
+# call's tensors checks and unpacks them all.
 
-
-def _check_int_shape(t, name: str, shape):
-    """An int32 tensor of this shape."""
-    import torch
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {list(shape)}")
-
-
-def _cptr(t, name: str) -> Optional[int]:
-    """The address of a contiguous tensor (its device is _call's to check)."""
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _call(fn, stream, tensors, *args):
-    """fn(*args, stream) on the device of a call's tensors, which they must
-    share: on the caller's stream, or that device's current one."""
-    import torch
-    device = -1
-    for t in tensors:
+def _tensors(spec):
+    """Device index and addresses of a call's tensors, in order.  spec: (tensor
+    or None, name, dtype or None, shape or None) each; they must be contiguous
+    CUDA tensors of one device."""
+    for t, name, dtype, shape in spec:
         if t is None:
+            continue
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"{name} must be {str(dtype).split('.')[-1]}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {list(shape)}")
+    device, pointers = -1, []
+    for t, name, _, _ in spec:
+        if t is None:
+            pointers.append(None)
             continue
         d = t.get_device()
         if d < 0:
-            raise ValueError("tensor must live on a CUDA device")
-        if device >= 0 and d != device:
-            raise ValueError(f"tensors live on different devices: cuda:{device} and cuda:{d}")
-        device = d
+            raise ValueError(f"{name} must live on a CUDA device")
+        if d != device:
+            if device >= 0:
+                raise ValueError(f"{name} lives on cuda:{d}, other tensors of the call on cuda:{device}")
+            device = d
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        pointers.append(t.data_ptr())
+    return device, pointers
+
+
+def _call(fn, device: int, stream, *args):
+    """fn(*args, stream) on `device`: on the caller's stream, or that device's current one."""
+    import torch
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(device)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
             status = fn(*args, stream)
     if status != PA_OK:
         raise PaError(status, last_error())
+
+
+def _dims(t, name: str, dims: str):
+    """The shape of a tensor with as many dimensions as `dims` names."""
+    shape = t.shape
+    if len(shape) != dims.count(",") + 1:
+        raise ValueError(f"{name} has shape {tuple(shape)}; expected [{dims}]")
+    return shape
 
 
 def _chunk_array(chunks):
@@ -454,16 +458,19 @@ def attention_mass(pool: Pool, q, seq_ids, positions, block_tables, mass, chunks
                    softmax_scale: float = 0.0, workspace=None, status=None, stream=None):
     """Add every row's attention weights (q [n, Hq, D] f32|bf16) to mass, f32
     [num_seqs, Hkv, max_blocks * P], summed over the query heads of a kv head."""
-    n = _check_rows(pool, q, seq_ids, positions, block_tables, q, status)
-    num_seqs, max_blocks = (int(x) for x in block_tables.shape)
-    _check_f32(mass, "mass", (num_seqs, pool.num_kv_heads, max_blocks * pool.page_size))
-    ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _call(load().pa_attention_mass, stream,
-          (pool.k_pool, q, seq_ids, positions, block_tables, mass, workspace, status), pool.handle, n, _cptr(q, "q"),
-          _dtype_code(q), int(q.shape[1]), _cptr(seq_ids, "seq_ids"), _cptr(positions, "positions"),
-          _cptr(block_tables, "block_tables"), num_seqs, max_blocks, _chunk_array(chunks) if chunks else None,
-          len(chunks), float(softmax_scale), _cptr(mass, "mass"), _cptr(workspace, "workspace"), ws_len,
-          _cptr(status, "status"))
+    import torch
+    n, hq, d = _dims(q, "q", "n, Hq, D")
+    num_seqs, max_blocks = _dims(block_tables, "block_tables", "num_seqs, max_blocks")
+    if d != pool.head_dim:
+        raise ValueError(f"q has shape {tuple(q.shape)}; expected [n, Hq, {pool.head_dim}]")
+    device, (k, qp, sp, pp, tp, mp, wp, stp) = _tensors((
+        (pool.k_pool, "pool", None, None), (q, "q", None, None), (seq_ids, "seq_ids", torch.int32, (n,)),
+        (positions, "positions", torch.int32, (n,)), (block_tables, "block_tables", torch.int32, None),
+        (mass, "mass", torch.float32, (num_seqs, pool.num_kv_heads, max_blocks * pool.page_size)),
+        (workspace, "workspace", None, None), (status, "status", torch.int32, None)))
+    _call(load().pa_attention_mass, device, stream, pool.handle, n, qp, _dtype_code(q), hq, sp, pp, tp, num_seqs,
+          max_blocks, _chunk_array(chunks) if chunks else None, len(chunks), softmax_scale, mp, wp,
+          workspace.nbytes if workspace is not None else 0, stp)
 
 
 def evict_select(mass, seq_ids, lengths, keep, kept_lengths=None, keep_first: int = 0, keep_last: int = 0, status=None,
@@ -471,51 +478,34 @@ def evict_select(mass, seq_ids, lengths, keep, kept_lengths=None, keep_first: in
     """The tokens each (sequence, kv head) keeps, ascending, into keep int32
     [n, Hkv, budget] (-1 behind them): the first and last ones asked for, and
     those with the most mass (f32 [num_seqs, Hkv, max_tokens])."""
-    _check_index(seq_ids, "seq_ids")
-    n = int(seq_ids.shape[0])
-    _check_index(lengths, "lengths", n)
-    if mass.dim() != 3 or keep.dim() != 3:
-        raise ValueError("mass must be [num_seqs, Hkv, max_tokens] and keep [n, Hkv, budget]")
-    _check_f32(mass, "mass", mass.shape)
-    num_seqs, heads, max_tokens = (int(x) for x in mass.shape)
-    budget = int(keep.shape[2])
-    _check_int_shape(keep, "keep", (n, heads, budget))
-    if kept_lengths is not None:
-        _check_index(kept_lengths, "kept_lengths", n)
-        if n and kept_lengths.data_ptr() == lengths.data_ptr():
-            raise ValueError("kept_lengths may not be lengths")
-    if status is not None:
-        _check_index(status, "status")
-    _call(load().pa_evict_select, stream, (mass, seq_ids, lengths, keep, kept_lengths, status), n,
-          _cptr(seq_ids, "seq_ids"), _cptr(lengths, "lengths"), _cptr(mass, "mass"), num_seqs, heads, max_tokens, budget,
-          int(keep_first), int(keep_last), _cptr(keep, "keep"), _cptr(kept_lengths, "kept_lengths"),
-          _cptr(status, "status"))
+    import torch
+    num_seqs, heads, max_tokens = _dims(mass, "mass", "num_seqs, Hkv, max_tokens")
+    n, _, budget = _dims(keep, "keep", "n, Hkv, budget")
+    if kept_lengths is not None and n and kept_lengths.data_ptr() == lengths.data_ptr():
+        raise ValueError("kept_lengths may not be lengths")
+    device, (mp, sp, lp, kp, np_, stp) = _tensors((
+        (mass, "mass", torch.float32, None), (seq_ids, "seq_ids", torch.int32, (n,)),
+        (lengths, "lengths", torch.int32, (n,)), (keep, "keep", torch.int32, (n, heads, budget)),
+        (kept_lengths, "kept_lengths", torch.int32, (n,)), (status, "status", torch.int32, None)))
+    _call(load().pa_evict_select, device, stream, n, sp, lp, mp, num_seqs, heads, max_tokens, budget, keep_first,
+          keep_last, kp, np_, stp)
 
 
 def evict_compact(pool: Pool, keep, seq_ids, lengths, block_tables, mass=None, dst_seq_ids=None, status=None,
                   stream=None):
     """Move the kept tokens (keep int32 [n, Hkv, budget], ascending) to the front
     of their sequence, or of the slots dst_seq_ids: K, V and, if given, mass."""
-    _check_index(seq_ids, "seq_ids")
-    n = int(seq_ids.shape[0])
-    _check_index(lengths, "lengths", n)
-    _check_index(block_tables, "block_tables", dims=2)
-    if dst_seq_ids is not None:
-        _check_index(dst_seq_ids, "dst_seq_ids", n)
-    if status is not None:
-        _check_index(status, "status")
-    if keep.dim() != 3:
-        raise ValueError(f"keep has shape {tuple(keep.shape)}; expected [{n}, {pool.num_kv_heads}, budget]")
-    budget = int(keep.shape[2])
-    _check_int_shape(keep, "keep", (n, pool.num_kv_heads, budget))
-    num_seqs, max_blocks = (int(x) for x in block_tables.shape)
-    if mass is not None:
-        _check_f32(mass, "mass", (num_seqs, pool.num_kv_heads, max_blocks * pool.page_size))
-    _call(load().pa_evict_compact, stream,
-          (pool.k_pool, keep, seq_ids, lengths, block_tables, mass, dst_seq_ids, status), pool.handle, n,
-          _cptr(seq_ids, "seq_ids"), _cptr(dst_seq_ids, "dst_seq_ids"), _cptr(lengths, "lengths"), _cptr(keep, "keep"),
-          budget, _cptr(block_tables, "block_tables"), num_seqs, max_blocks, _cptr(mass, "mass"),
-          _cptr(status, "status"))
+    import torch
+    n, _, budget = _dims(keep, "keep", "n, Hkv, budget")
+    num_seqs, max_blocks = _dims(block_tables, "block_tables", "num_seqs, max_blocks")
+    device, (k, kp, sp, lp, tp, mp, dp, stp) = _tensors((
+        (pool.k_pool, "pool", None, None), (keep, "keep", torch.int32, (n, pool.num_kv_heads, budget)),
+        (seq_ids, "seq_ids", torch.int32, (n,)), (lengths, "lengths", torch.int32, (n,)),
+        (block_tables, "block_tables", torch.int32, None),
+        (mass, "mass", torch.float32, (num_seqs, pool.num_kv_heads, max_blocks * pool.page_size)),
+        (dst_seq_ids, "dst_seq_ids", torch.int32, (n,)), (status, "status", torch.int32, None)))
+    _call(load().pa_evict_compact, device, stream, pool.handle, n, sp, dp, lp, kp, budget, tp, num_seqs, max_blocks, mp,
+          stp)
 
 
 def beam_workspace_bytes(n_groups: int, beams: int, vocab: int, n_out: int) -> int:
@@ -528,52 +518,43 @@ def beam_select(logits, scores, parents, tokens, out_scores, finished=None, end_
     """The best continuations of each group over beams x vocabulary: logits
     [groups, beams, vocab] f32|bf16 (rows may be padded), scores f32 and finished
     int32 [groups, beams] into parents, tokens int32 and out_scores f32 [groups, n_out]."""
-    if logits.dim() != 3:
-        raise ValueError(f"logits have shape {tuple(logits.shape)}; expected [groups, beams, vocab]")
-    groups, beams, vocab = (int(x) for x in logits.shape)
-    if parents.dim() != 2:
-        raise ValueError(f"parents has shape {tuple(parents.shape)}; expected [{groups}, n_out]")
-    n_out = int(parents.shape[1])
-    _check_f32(scores, "scores", (groups, beams))
-    _check_int_shape(parents, "parents", (groups, n_out))
-    _check_int_shape(tokens, "tokens", (groups, n_out))
-    _check_f32(out_scores, "out_scores", (groups, n_out))
-    if finished is not None:
-        _check_int_shape(finished, "finished", (groups, beams))
+    import torch
+    groups, beams, vocab = _dims(logits, "logits", "groups, beams, vocab")
+    _, n_out = _dims(parents, "parents", "groups, n_out")
     # rows: contiguous, and evenly spaced over groups and beams (a stride of a size-1 axis says nothing)
-    row = int(logits.stride(1)) if beams > 1 else int(logits.stride(0)) if groups > 1 else vocab
-    if (vocab > 1 and logits.stride(2) != 1) or (groups > 1 and logits.stride(0) != beams * row):
+    across, down, along = logits.stride()
+    row = down if beams > 1 else across if groups > 1 else vocab
+    if (vocab > 1 and along != 1) or (groups > 1 and across != beams * row):
         raise ValueError("logits must have contiguous rows, evenly spaced over groups and beams")
-    ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _call(load().pa_beam_select, stream, (logits, scores, parents, tokens, out_scores, finished, workspace), groups,
-          beams, vocab, logits.data_ptr(), _dtype_code(logits), row, _cptr(scores, "scores"),
-          _cptr(finished, "finished"), int(end_token), n_out, _cptr(parents, "parents"), _cptr(tokens, "tokens"),
-          _cptr(out_scores, "out_scores"), _cptr(workspace, "workspace"), ws_len)
+    device, (sp, pp, tp, op, fp, wp) = _tensors((
+        (scores, "scores", torch.float32, (groups, beams)), (parents, "parents", torch.int32, (groups, n_out)),
+        (tokens, "tokens", torch.int32, (groups, n_out)), (out_scores, "out_scores", torch.float32, (groups, n_out)),
+        (finished, "finished", torch.int32, (groups, beams)), (workspace, "workspace", None, None)))
+    if logits.get_device() != device:
+        raise ValueError("logits and the other tensors of the call must live on one CUDA device")
+    _call(load().pa_beam_select, device, stream, groups, beams, vocab, logits.data_ptr(), _dtype_code(logits), row, sp,
+          fp, end_token, n_out, pp, tp, op, wp, workspace.nbytes if workspace is not None else 0)
 
 
 def beam_reorder(pool: Pool, parents, seq_ids, lengths, block_tables, state=None, status=None, stream=None):
     """Give the beam in slot seq_ids[i, b] the cache of beam parents[i, b] of its
     group (int32 [groups, beams]; -1: its own): block tables and unfinished pages,
     and the rows of state [num_seqs, ...] (any 4-byte aligned rows), in place."""
-    if parents.dim() != 2:
-        raise ValueError(f"parents has shape {tuple(parents.shape)}; expected [groups, beams]")
-    groups, beams = (int(x) for x in parents.shape)
-    _check_int_shape(parents, "parents", (groups, beams))
-    _check_int_shape(seq_ids, "seq_ids", (groups, beams))
-    _check_index(lengths, "lengths", groups)
-    _check_index(block_tables, "block_tables", dims=2)
-    if status is not None:
-        _check_index(status, "status")
-    num_seqs, max_blocks = (int(x) for x in block_tables.shape)
+    import torch
+    groups, beams = _dims(parents, "parents", "groups, beams")
+    num_seqs, max_blocks = _dims(block_tables, "block_tables", "num_seqs, max_blocks")
     row_bytes = 0
     if state is not None:
-        if state.dim() < 1 or int(state.shape[0]) != num_seqs:
+        if state.dim() < 1 or state.shape[0] != num_seqs:
             raise ValueError(f"state has shape {tuple(state.shape)}; expected {num_seqs} rows")
-        row_bytes = state.numel() // num_seqs * state.element_size()
-    _call(load().pa_beam_reorder, stream, (pool.k_pool, parents, seq_ids, lengths, block_tables, state, status),
-          pool.handle, groups, beams, _cptr(seq_ids, "seq_ids"), _cptr(parents, "parents"), _cptr(lengths, "lengths"),
-          _cptr(block_tables, "block_tables"), num_seqs, max_blocks, _cptr(state, "state"), row_bytes,
-          _cptr(status, "status"))
+        row_bytes = state.nbytes // num_seqs
+    device, (k, pp, sp, lp, tp, xp, stp) = _tensors((
+        (pool.k_pool, "pool", None, None), (parents, "parents", torch.int32, None),
+        (seq_ids, "seq_ids", torch.int32, (groups, beams)), (lengths, "lengths", torch.int32, (groups,)),
+        (block_tables, "block_tables", torch.int32, None), (state, "state", None, None),
+        (status, "status", torch.int32, None)))
+    _call(load().pa_beam_reorder, device, stream, pool.handle, groups, beams, sp, pp, lp, tp, num_seqs, max_blocks, xp,
+          row_bytes, stp)
 
 
 def set_split_tokens(tokens: int):

@@ -240,14 +240,21 @@ struct KeyFrag {
 // A lane's running (maximum, sum) of one column, over the keys that it sees.
 struct ColumnStat {
   float m, l;
-  __device__ __forceinline__ void add2(float s0, float s1) {
-    const float top = fmaxf(m, fmaxf(s0, s1));
+  // N scores more (log2 domain); a NaN among them makes the sum NaN
+  template <int N>
+  __device__ __forceinline__ void add(const float (&s)[N]) {
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, s[i]);
     if (top > m) {
       l = __fmul_rn(l, ex2(__fsub_rn(m, top)));
       m = top;
     }
-    if (m > -INFINITY) l = __fadd_rn(l, __fadd_rn(ex2(__fsub_rn(s0, m)), ex2(__fsub_rn(s1, m))));
-    if (s0 != s0 || s1 != s1) l = NAN;
+    const float ref = m == -INFINITY ? 0.0f : m;  // every score so far is -infinity: weights 0
+    float w = ex2(__fsub_rn(s[0], ref));
+#pragma unroll
+    for (int i = 1; i < N; ++i) w = __fadd_rn(w, ex2(__fsub_rn(s[i], ref)));
+    l = __fadd_rn(l, w);
   }
   __device__ __forceinline__ void merge(float om, float ol) {
     const float top = fmaxf(m, om);
@@ -332,36 +339,43 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
       f[s].load(key_rows<Geo::RB>(p, page, h, (tile0 + (warp + k * kMassWarps) * MT + s) * 16, lg_p, bad), g4, t4);
     }
   };
-  auto scores_of = [&](KeyFrag<KVT, D, QB>& f, int t0, float (&c)[1][4]) {
-    f.score(q, c);
-    const bool in0 = t0 + g4 <= pos, in1 = t0 + g4 + 8 <= pos;
-    c[0][0] = in0 ? __fmul_rn(c[0][0], f0) : -INFINITY;
-    c[0][1] = in0 ? __fmul_rn(c[0][1], f1) : -INFINITY;
-    c[0][2] = in1 ? __fmul_rn(c[0][2], f0) : -INFINITY;
-    c[0][3] = in1 ? __fmul_rn(c[0][3], f1) : -INFINITY;
+  // log2-domain scores of a 16-key tile (-infinity behind the row's position)
+  auto scores_of = [&](const KeyFrag<KVT, D, QB>& f, int t0, float (&c)[4]) {
+    float raw[1][4];
+    f.score(q, raw);
+    c[0] = __fmul_rn(raw[0][0], f0), c[1] = __fmul_rn(raw[0][1], f1);
+    c[2] = __fmul_rn(raw[0][2], f0), c[3] = __fmul_rn(raw[0][3], f1);
+    if (t0 + 15 > pos) {
+      if (t0 + g4 > pos) c[0] = c[1] = -INFINITY;
+      if (t0 + g4 + 8 > pos) c[2] = c[3] = -INFINITY;
+    }
   };
   ColumnStat st0{-INFINITY, 0.0f}, st1{-INFINITY, 0.0f};
   const int count = mine > warp * MT ? (mine - warp * MT + kMassWarps * MT - 1) / (kMassWarps * MT) : 0;  // of this warp
-  KeyFrag<KVT, D, QB> next[MT];
-  if (count > 0) load(0, next);
-  for (int k = 0; k < count; ++k) {
-    KeyFrag<KVT, D, QB> now[MT];
-#pragma unroll
-    for (int s = 0; s < MT; ++s) now[s] = next[s];
+  auto step = [&](int k, KeyFrag<KVT, D, QB>(&now)[MT], KeyFrag<KVT, D, QB>(&next)[MT]) {
     if (k + 1 < count) load(k + 1, next);
+    float even[2 * MT], odd[2 * MT];  // columns 2 t4 and 2 t4 + 1
 #pragma unroll
     for (int s = 0; s < MT; ++s) {
       const int local = (warp + k * kMassWarps) * MT + s;
-      float c[1][4];
+      float c[4];
       scores_of(now[s], (tile0 + local) * 16, c);
-      st0.add2(c[0][0], c[0][2]);
-      st1.add2(c[0][1], c[0][3]);
+      even[2 * s] = c[0], even[2 * s + 1] = c[2];
+      odd[2 * s] = c[1], odd[2 * s + 1] = c[3];
       if (local * 16 < p.score_keys) {
         float* z = scores + 2 * t4 * stride + local * 16 + g4;
-        if (2 * t4 < G) z[0] = c[0][0], z[8] = c[0][2];
-        if (2 * t4 + 1 < G) z[stride] = c[0][1], z[stride + 8] = c[0][3];
+        if (2 * t4 < G) z[0] = c[0], z[8] = c[2];
+        if (2 * t4 + 1 < G) z[stride] = c[1], z[stride + 8] = c[3];
       }
     }
+    st0.add(even);
+    st1.add(odd);
+  };
+  KeyFrag<KVT, D, QB> x[MT], y[MT];
+  if (count > 0) load(0, x);
+  for (int k = 0; k < count; k += 2) {
+    step(k, x, y);
+    if (k + 1 < count) step(k + 1, y, x);
   }
   // (max, sum) of each column: over the lanes of a warp, the warps, the CTAs
 #pragma unroll
@@ -414,16 +428,16 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
       const int t0 = (tile0 + local) * 16;
       KeyFrag<KVT, D, QB> f;
       f.load(key_rows<Geo::RB>(p, __ldg(table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
-      float c[1][4];
+      float c[4];
       scores_of(f, t0, c);
       float w0 = 0.0f, w1 = 0.0f;
       if (2 * t4 < G) {
-        w0 = __fmul_rn(ex2(__fsub_rn(c[0][0], r0.x)), r0.y);
-        w1 = __fmul_rn(ex2(__fsub_rn(c[0][2], r0.x)), r0.y);
+        w0 = __fmul_rn(ex2(__fsub_rn(c[0], r0.x)), r0.y);
+        w1 = __fmul_rn(ex2(__fsub_rn(c[2], r0.x)), r0.y);
       }
       if (2 * t4 + 1 < G) {
-        w0 = fmaf(ex2(__fsub_rn(c[0][1], r1.x)), r1.y, w0);
-        w1 = fmaf(ex2(__fsub_rn(c[0][3], r1.x)), r1.y, w1);
+        w0 = fmaf(ex2(__fsub_rn(c[1], r1.x)), r1.y, w0);
+        w1 = fmaf(ex2(__fsub_rn(c[3], r1.x)), r1.y, w1);
       }
 #pragma unroll
       for (int off = 1; off < 4; off <<= 1) {
@@ -539,9 +553,11 @@ __global__ void __launch_bounds__(kMassThreads) chunk_stats_kernel(const __grid_
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        st[n][k].add2(t0 + g4 <= lim[n][k] ? __fmul_rn(s[n][k], f[n][k]) : -INFINITY,
-                      t0 + g4 + 8 <= lim[n][k] ? __fmul_rn(s[n][2 + k], f[n][k]) : -INFINITY);
+      for (int k = 0; k < 2; ++k) {
+        const float z[2] = {t0 + g4 <= lim[n][k] ? __fmul_rn(s[n][k], f[n][k]) : -INFINITY,
+                            t0 + g4 + 8 <= lim[n][k] ? __fmul_rn(s[n][2 + k], f[n][k]) : -INFINITY};
+        st[n][k].add(z);
+      }
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n)
