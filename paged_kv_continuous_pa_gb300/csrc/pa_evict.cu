@@ -30,6 +30,8 @@ constexpr int kSelectSamples = 512;
 constexpr int kSelectSlots = 32;                            // weights a thread can list
 constexpr int kSelectAll = kSelectSlots * kSelectThreads;   // that many competing tokens need no sample
 constexpr int kSelectGroups = 512;                          // groups of 128 tokens marked at once
+constexpr int kSelectBinBits = 11;
+constexpr int kSelectBins = 1 << kSelectBinBits;
 constexpr int kSelectBatch = 4;                             // groups a warp loads at once
 
 // The weights in an integer order: a larger weight has a larger key, -0 and +0
@@ -45,9 +47,15 @@ __device__ __forceinline__ float key_weight(uint32_t key) {
 
 struct SelectSmem {
   float list[kSelectSlots][kSelectThreads];  // weights between the two pivots, a column to a thread
-  // a group's tokens by lane (four consecutive ones each): above the last weight kept, equal to it; then
-  // kept tokens and ties before the group
-  uint32_t above[kSelectGroups][4], equal[kSelectGroups][4], before[kSelectGroups][2];
+  union {
+    uint32_t bins[kSelectBins];
+    struct {
+      // a group's tokens by lane (four consecutive ones each): kept outright, equal to the last weight
+      uint32_t above[kSelectGroups][4], equal[kSelectGroups][4];
+    };
+  };
+  uint32_t before[kSelectGroups][2];  // kept tokens and ties before a group
+  int pick[3], gathered;
   uint32_t count[2][kSelectWarps][2];
   uint32_t warp_sum[kSelectWarps][2];
   float pivot[2];
@@ -105,11 +113,12 @@ __device__ __forceinline__ void load_groups(const float* w, bool vec, int t0, in
 //      (3.5 standard deviations of a sample rank to either side).
 //   2. One pass counts the weights from the upper pivot on and lists those between
 //      the two (a few in a hundred; no sample is taken where all fit).
-//   3. Bisection over the lists, three pivots a step, finds the last weight.
+//   3. A histogram of the listed keys, over their range, finds the bin of the last
+//      one; its few keys are ranked by counting (or it is the next range).
 //   4. A second pass (from L2) marks the kept tokens as bits; counts over groups of
 //      128 tokens place them, in ascending order.
 // Where the pivots miss (the m-th weight outside, or a thread's list too short,
-// as a hostile order can bring about) step 3 bisects over the weights themselves.
+// as a hostile order can bring about) step 3 goes over the weights themselves.
 // Bound by the latency of the steps at the first read's rate: one wave of CTAs.
 __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(16) unsigned char select_smem[];
@@ -150,7 +159,8 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     }
     return make_uint2(x, y);
   };
-  uint32_t last = 0xffffffffu, ties = 0u;  // kept: keys above `last`, and the first `ties` tokens of exactly it
+  // kept: keys above `last`, and of the `equals` tokens (0: not counted) of exactly it the first `ties`
+  uint32_t last = 0xffffffffu, ties = 0u, equals = 0u;
   if (m > 0) {
     float low = -INFINITY, high = INFINITY;
     if (N > kSelectAll) {
@@ -187,21 +197,32 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
         listed += in;
       }
     };
-    for (int g0 = a / 128 * 128; g0 < b; g0 += kSelectBatch * STRIDE) {
-      const int t0 = g0 + warp * 128 + lane * 4;
-      float x[kSelectBatch][4];
-      load_groups(w, vec, t0, STRIDE, b, x);
-      if (g0 < a || g0 + kSelectBatch * STRIDE > b) {
+    // a batch's loads are on their way while the one before is listed
+    auto batch = [&](int g0, const float(&x)[kSelectBatch][4], float(&next)[kSelectBatch][4]) {
+      const int t0 = g0 + warp * 128 + lane * 4, ahead = g0 + kSelectBatch * STRIDE;
+      if (ahead < b) load_groups(w, vec, t0 + kSelectBatch * STRIDE, STRIDE, b, next);
+      if (g0 >= a && ahead <= b) {
 #pragma unroll
-        for (int u = 0; u < kSelectBatch; ++u)
+        for (int u = 0; u < kSelectBatch; ++u) list4(x[u]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kSelectBatch; ++u) {
+          float y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int t = t0 + u * STRIDE + e;
-            if (t < a || t >= b) x[u][e] = NAN;  // in no comparison
+            y[e] = t >= a && t < b ? x[u][e] : NAN;  // NaN: in no comparison
           }
+          list4(y);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < kSelectBatch; ++u) list4(x[u]);
+    };
+    const int g_first = a / 128 * 128;
+    float x[kSelectBatch][4], y[kSelectBatch][4];
+    load_groups(w, vec, g_first + warp * 128 + lane * 4, STRIDE, b, x);
+    for (int g0 = g_first; g0 < b; g0 += 2 * kSelectBatch * STRIDE) {
+      batch(g0, x, y);
+      if (g0 + kSelectBatch * STRIDE < b) batch(g0 + kSelectBatch * STRIDE, y, x);
     }
     if (listed > kSelectSlots) sm.overflow = 1;
     const uint2 s = sum2(from_high, listed);
@@ -222,81 +243,115 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
       }
     }
     if (!at_low) {
-      if (found)
-        for (int e = 0; e < listed; ++e) sm.list[e][tid] = __uint_as_float(weight_key(sm.list[e][tid]));  // keys from here on
-      // the last key lies in [lo, hi): fewer than `want` reach hi, as many or more reach lo: of the listed
-      // weights, or (the pivots missed) of all
+      // the last key kept lies in [lo, hi): `ahead` keys (fewer than `want`) reach hi, `want` or more reach lo; of
+      // the listed weights, or (the pivots missed) of all
       uint32_t lo = found ? weight_key(low) : 0u, hi = found ? weight_key(high) : 0xffffffffu;
       const int want = found ? need : m;
-      int reach_hi = 0;
-      while (hi - lo > 1u) {
-        const uint32_t step = (hi - lo) / 4;
-        uint32_t q[3] = {lo + step, lo + 2 * step, lo + 3 * step};
-        if (step == 0u) q[0] = q[1] = q[2] = lo + 1u;
-        uint32_t c[3] = {0u, 0u, 0u};
-        if (found) {
-          for (int e = 0; e < listed; ++e) {
-            const uint32_t key = __float_as_uint(sm.list[e][tid]);
+      int ahead = 0;
+      auto each_key = [&](auto f) {
+        if (found)
+          for (int e = 0; e < listed; ++e) f(weight_key(sm.list[e][tid]));
+        else
+          for (int t = a + tid; t < b; t += kSelectThreads) f(weight_key(__ldg(w + t)));
+      };
+      for (bool more = true; more;) {
+        // a histogram of the range's keys, and the bin that holds the last one
+        const int shift = max(0, 32 - __clz(hi - 1u - lo) - kSelectBinBits);
+        __syncthreads();
+        for (int k = tid; k < kSelectBins; k += kSelectThreads) sm.bins[k] = 0u;
+        if (tid == 0) sm.gathered = 0;
+        __syncthreads();
+        each_key([&](uint32_t key) {
+          if (key >= lo && key < hi) atomicAdd(&sm.bins[(key - lo) >> shift], 1u);
+        });
+        __syncthreads();
+        constexpr int PER = kSelectBins / kSelectThreads;  // a thread's bins, from the top down
+        uint32_t n[PER], sum = 0u;
 #pragma unroll
-            for (int z = 0; z < 3; ++z) c[z] += key >= q[z];
-          }
-        } else {
-          for (int t = a + tid; t < b; t += kSelectThreads) {
-            const uint32_t key = weight_key(__ldg(w + t));
+        for (int k = 0; k < PER; ++k) {
+          n[k] = sm.bins[kSelectBins - 1 - (tid * PER + k)];
+          sum += n[k];
+        }
+        uint32_t upto = sum;
 #pragma unroll
-            for (int z = 0; z < 3; ++z) c[z] += key >= q[z];
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += y;
+        }
+        if (lane == 31) sm.warp_sum[warp][0] = upto;
+        __syncthreads();
+        int before = ahead + static_cast<int>(upto - sum);
+#pragma unroll
+        for (int k = 0; k < kSelectWarps; ++k)
+          if (k < warp) before += static_cast<int>(sm.warp_sum[k][0]);
+        if (before < want && before + static_cast<int>(sum) >= want) {
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            if (before < want && before + static_cast<int>(n[k]) >= want) {
+              sm.pick[0] = kSelectBins - 1 - (tid * PER + k);
+              sm.pick[1] = before;
+              sm.pick[2] = static_cast<int>(n[k]);
+              break;
+            }
+            before += static_cast<int>(n[k]);
           }
         }
-        int n[3];
-        if (found) {  // sums below 2^16, two to a word
-          const uint2 r = sum2(c[0] | (c[1] << 16), c[2]);
-          n[0] = r.x & 0xffffu, n[1] = r.x >> 16, n[2] = r.y;
-        } else {
-          const uint2 r = sum2(c[0], c[1]);
-          n[0] = r.x, n[1] = r.y;
-          n[2] = sum2(c[2], 0u).x;
-        }
-        bool done = false;
-#pragma unroll
-        for (int z = 2; z >= 0; --z) {
-          if (n[z] < want) {
-            if (q[z] < hi) hi = q[z], reach_hi = n[z];
-          } else if (q[z] > lo) {
-            lo = q[z];
-            done = n[z] == want;
+        __syncthreads();
+        lo += static_cast<uint32_t>(sm.pick[0]) << shift;
+        if (hi - lo > (1u << shift)) hi = lo + (1u << shift);
+        ahead = sm.pick[1];
+        const int held = sm.pick[2];  // keys in [lo, hi)
+        if (hi - lo == 1u) {
+          last = lo;
+          ties = want - ahead;
+          equals = held;
+          more = false;
+        } else if (held <= 32) {
+          // few enough to rank by counting, in every warp
+          each_key([&](uint32_t key) {
+            if (key >= lo && key < hi) sm.bins[atomicAdd(&sm.gathered, 1)] = key;  // (the bins are read: room for 32)
+          });
+          __syncthreads();
+          const uint32_t key = lane < held ? sm.bins[lane] : 0u;
+          int above = 0, same = 0;
+          for (int k = 0; k < held; ++k) {
+            const uint32_t other = __shfl_sync(0xffffffffu, key, k);
+            above += other > key;
+            same += other == key;
           }
-        }
-        if (done) {  // exactly those from lo on: above the key before it, without ties
-          lo = lo - 1u;
-          if (lo == 0x7fffffffu) lo -= 1u;  // the pattern of -0, which as a number equals the 0 behind it
-          reach_hi = want;
-          break;
+          const bool mine = lane < held && ahead + above < want && ahead + above + same >= want;
+          const int who = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+          last = __shfl_sync(0xffffffffu, key, who);
+          ties = want - ahead - __shfl_sync(0xffffffffu, above, who);
+          equals = __shfl_sync(0xffffffffu, same, who);
+          more = false;
         }
       }
-      last = lo;
-      ties = want - reach_hi;
     }
   }
-  // ---- marks and places, kSelectGroups groups of 128 tokens at a time.  Kept: weights above `edge`, and the
-  // first `ties` equal to it.  Keys below -infinity's: every number stays, and `ties` NaNs; no weight has the
-  // key 0xffffffff: none stays.
-  const bool numbers = last < weight_key(-INFINITY);
-  const float edge = numbers || last == 0xffffffffu ? NAN : key_weight(last);
+  // ---- marks and places, kSelectGroups groups of 128 tokens at a time.  Kept: weights from `from` on, and the
+  // first `ties` equal to `edge`.  The key 0 is the NaNs': every number stays, and `ties` of them; no weight has
+  // the key 0xffffffff: none stays.  (The number behind an edge has the next key; behind infinity comes a NaN,
+  // which nothing reaches.)
+  const bool numbers = last == 0u, none = last == 0xffffffffu;
+  const bool whole = !numbers && equals > 0u && ties == equals;  // every token of the last weight stays
+  if (whole) ties = 0u;
+  const float edge = numbers || none ? NAN : key_weight(last);
+  const float from = numbers || none ? NAN : key_weight(whole ? last : last + 1u);
   uint32_t kept_base = 0u, tie_base = 0u;
   for (int c0 = 0; c0 < len; c0 += kSelectGroups * 128) {
     const int groups = min(kSelectGroups, (len - c0 + 127) / 128);
     __syncthreads();
-    for (int g0 = warp; g0 < groups; g0 += kSelectBatch * kSelectWarps) {
-      const int t0 = c0 + g0 * 128 + lane * 4;
-      float x[kSelectBatch][4];
-      load_groups(w, vec, t0, kSelectWarps * 128, len, x);
+    auto mark = [&](int g0, const float(&x)[kSelectBatch][4], float(&next)[kSelectBatch][4]) {
+      const int t0 = c0 + g0 * 128 + lane * 4, ahead = g0 + kSelectBatch * kSelectWarps;
+      if (ahead < groups) load_groups(w, vec, c0 + ahead * 128 + lane * 4, kSelectWarps * 128, len, next);
 #pragma unroll
       for (int u = 0; u < kSelectBatch; ++u) {
         const int g = g0 + u * kSelectWarps, t = t0 + u * kSelectWarps * 128;
         uint32_t gt[4], eq[4] = {0u, 0u, 0u, 0u};
         if (c0 + g * 128 >= a && c0 + g * 128 + 128 <= b && !numbers) {  // the whole group competes
 #pragma unroll
-          for (int e = 0; e < 4; ++e) gt[e] = __ballot_sync(0xffffffffu, x[u][e] > edge);
+          for (int e = 0; e < 4; ++e) gt[e] = __ballot_sync(0xffffffffu, x[u][e] >= from);
           if (ties > 0u) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) eq[e] = __ballot_sync(0xffffffffu, x[u][e] == edge);
@@ -305,7 +360,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool competes = t + e >= a && t + e < b;
-            const bool more = numbers ? x[u][e] == x[u][e] : x[u][e] > edge;
+            const bool more = numbers ? x[u][e] == x[u][e] : x[u][e] >= from;
             const bool same = numbers ? x[u][e] != x[u][e] : x[u][e] == edge;
             gt[e] = __ballot_sync(0xffffffffu, t + e < len && (!competes || more));
             eq[e] = __ballot_sync(0xffffffffu, competes && same && ties > 0u);
@@ -316,6 +371,12 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
           *reinterpret_cast<uint4*>(sm.equal[g]) = make_uint4(eq[0], eq[1], eq[2], eq[3]);
         }
       }
+    };
+    float x[kSelectBatch][4], y[kSelectBatch][4];
+    if (warp < groups) load_groups(w, vec, c0 + warp * 128 + lane * 4, kSelectWarps * 128, len, x);
+    for (int g0 = warp; g0 < groups; g0 += 2 * kSelectBatch * kSelectWarps) {
+      mark(g0, x, y);
+      if (g0 + kSelectBatch * kSelectWarps < groups) mark(g0 + kSelectBatch * kSelectWarps, y, x);
     }
     __syncthreads();
     // kept tokens and ties before each group: kSelectGroups / kSelectThreads groups to a thread
@@ -366,6 +427,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     tie_base += all_e;
     __syncthreads();
     const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int g = warp; g < groups; g += kSelectWarps) {
       const uint4 x = *reinterpret_cast<const uint4*>(sm.above[g]);
       uint32_t keep_bits = ((x.x >> lane) & 1u) | ((x.y >> lane) & 1u) << 1 | ((x.z >> lane) & 1u) << 2 | ((x.w >> lane) & 1u) << 3;
