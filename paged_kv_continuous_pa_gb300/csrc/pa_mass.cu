@@ -6,6 +6,34 @@
 #include "pa_host.h"
 #include "pa_mass.cuh"
 
+namespace pa {
+
+// A CTA per chunk: whether its rows are consecutive positions of one sequence
+// within the table, and every page that they reach a page of the pool.
+__global__ void __launch_bounds__(256) chunk_check_kernel(const __grid_constant__ MassParams p) {
+  griddep_launch_dependents();  // the statistics may be launched; they wait for this
+  const int c = blockIdx.x, tid = threadIdx.x;
+  const int row0 = p.chunk_begin[c], rows = p.chunk_end[c] - row0;
+  const int seq = __ldg(p.seq_ids + row0), pos0 = __ldg(p.positions + row0);
+  bool bad = seq < 0 || seq >= p.num_seqs || pos0 < 0 || pos0 > p.max_blocks * p.P - rows;
+  if (!bad) {
+    const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
+    for (int r = tid; r < rows; r += 256)
+      bad |= __ldg(p.seq_ids + row0 + r) != seq || __ldg(p.positions + row0 + r) != pos0 + r;
+    for (int j = tid; j <= (pos0 + rows - 1) / p.P; j += 256) {
+      const int page = __ldg(table + j);
+      bad |= page < 0 || page >= p.num_pages;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) {
+    if (bad) record_error(p.status, ST_OUT_OF_RANGE);
+    p.ws_head[c] = make_int2(bad ? -1 : seq, pos0);
+  }
+}
+
+}  // namespace pa
+
 using pa::aligned;
 using pa::cuda_fail;
 using pa::fail;
@@ -19,7 +47,6 @@ size_t plan_chunks(const pa_pool_desc& d, int32_t hq, int32_t max_blocks, const 
   auto cut = [&](int64_t n) { return static_cast<int32_t>((keys + n - 1) / n); };
   p->n_splits = cut(pa::kMassSplitKeys);
   p->n_blocks = cut(pa::kMassBlockKeys);
-  p->n_ranges = cut(pa::kMassRangeKeys);
   const int R = pa::kMassSlots / (hq / d.num_kv_heads);
   int64_t pairs = 0;
   for (int c = 0; c < n_chunks; ++c) {
@@ -27,12 +54,15 @@ size_t plan_chunks(const pa_pool_desc& d, int32_t hq, int32_t max_blocks, const 
     p->chunk_end[c] = chunks[c].row_begin + chunks[c].n_rows;
     p->chunk_tiles[c] = (chunks[c].n_rows + R - 1) / R;
     const int64_t slots = static_cast<int64_t>(p->chunk_tiles[c]) * pa::kMassSlots * d.num_kv_heads;
+    p->chunk_index[c] = c;
     p->chunk_part[c] = pairs;
     pairs += slots * p->n_splits;
   }
   p->n_chunks = n_chunks;
-  p->ws_part = static_cast<float2*>(workspace);
-  return static_cast<size_t>(pairs) * sizeof(float2);
+  if (n_chunks == 0) return 0;
+  p->ws_head = static_cast<int2*>(workspace);
+  p->ws_part = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + 256);
+  return 256 + static_cast<size_t>(pairs) * sizeof(float2);
 }
 
 // The chunks of `all` for which `take` holds.
@@ -46,19 +76,22 @@ pa::MassParams some_chunks(const pa::MassParams& all, Take take) {
     p.chunk_begin[k] = all.chunk_begin[c];
     p.chunk_end[k] = all.chunk_end[c];
     p.chunk_tiles[k] = all.chunk_tiles[c];
+    p.chunk_index[k] = all.chunk_index[c];
     p.chunk_part[k] = all.chunk_part[c];
   }
   return p;
 }
 
-// The chunks' columns: statistics over key ranges, then the weights, on the
-// tile path for bf16 chunks of kMinTileRows rows and more.
+// The chunks' columns: a look at the chunks, statistics over key ranges, then the
+// weights, on the tile path for bf16 chunks of kMinTileRows rows and more.
 template <typename Launch>
 cudaError_t launch_chunks(const pa::MassParams& all, bool tile_types, Launch launch, cudaStream_t s) {
   auto tiled = [&](int c) { return tile_types && all.chunk_end[c] - all.chunk_begin[c] >= pa::kMinTileRows; };
   const pa::MassParams tiles = some_chunks(all, tiled), others = some_chunks(all, [&](int c) { return !tiled(c); });
-  cudaError_t e = cudaSuccess;
-  if (tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, false, s);
+  pa::chunk_check_kernel<<<all.n_chunks, 256, 0, s>>>(all);
+  pa::count_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, false, s);
   if (e == cudaSuccess && tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, true, s);
   if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_STATS, s);
   if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_WEIGHTS, s);

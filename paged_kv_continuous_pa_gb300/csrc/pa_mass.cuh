@@ -10,11 +10,11 @@
 // scores wait in shared memory while the cluster's CTAs exchange their (max,
 // sum) pairs, then become weights.
 // Chunks: the (row, head) pairs of a kv head are columns that share the keys.
-// `chunk_stats_kernel` finds every column's (max, sum) over ranges of keys,
-// `chunk_weights_kernel` merges the ranges, recomputes the scores key block by
+// `chunk_check_kernel` looks the chunks over, `chunk_stats_kernel` finds every
+// column's (max, sum) over ranges of keys, `chunk_weights_kernel` merges the ranges, recomputes the scores key block by
 // key block and sums the weights over the columns: each key has one owner, which
-// adds once.  (bf16 chunks of 16 rows and more: the same two steps on the tile
-// path, pa_mass_tiles.cuh.)
+// adds once.  (bf16 chunks of 16 rows and more: the same steps on the tile path,
+// pa_mass_tiles.cuh.)
 // No atomic decides an order: the same rows give the same bits in any batch.
 #pragma once
 
@@ -26,9 +26,8 @@ namespace pa {
 
 constexpr int kMassThreads = 256;
 constexpr int kMassWarps = kMassThreads / 32;
-constexpr int kMassSplitKeys = 2048;  // keys per range of the chunks' first launch
+constexpr int kMassSplitKeys = 1024;  // keys per range of the chunks' first launch (and of the tile path's last)
 constexpr int kMassBlockKeys = 128;   // keys per CTA of their last launch
-constexpr int kMassRangeKeys = 1024;  // ... on the tile path
 constexpr int kMassSlots = 128;       // columns of a chunk come in tiles of 128 / G rows, 128 slots each
 constexpr int kMassClusterKeys = 4096;             // keys per CTA that a row's cluster aims at
 constexpr int kMassMaxCluster = 8;
@@ -54,8 +53,10 @@ struct MassParams {
   int32_t chunk_end[kMaxChunks];
   int32_t chunk_cta[kMaxChunks + 1];   // prefix sums of CTAs per chunk (set per launch)
   int32_t chunk_tiles[kMaxChunks];     // tiles of 128 / G rows
-  int32_t n_splits, n_blocks, n_ranges;  // of the longest row: key ranges, key blocks, tile-path ranges
+  int32_t chunk_index[kMaxChunks];     // place in ws_head
+  int32_t n_splits, n_blocks;          // of the longest row: key ranges, key blocks
   int64_t chunk_part[kMaxChunks];      // offset of a chunk in ws_part, in pairs
+  int2* ws_head;                       // per chunk its sequence (-1: the chunk adds nothing) and first position
   float2* ws_part;                     // (max, sum) per chunk [Hkv][n_splits][tiles][128]
   CUtensorMap kmap;                    // tile path: the pool as [num_pages * Hkv * P][D], boxes of 64 x min(P, 64)
   CUtensorMap qmap;                    // tile path: q as [n_rows][Hq][D], boxes of 128 / G rows x G heads x 64
@@ -454,34 +455,23 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
 
 // ---------------------------------------------------------------- chunks --
 
-// A chunk as both launches see it: its rows (consecutive positions of one
-// sequence, checked by every CTA) and its columns, column c being head c % G of
-// row c / G.
+// A chunk as the launches see it: its rows (consecutive positions of one
+// sequence, checked by the launch before) and its columns, column c being head
+// c % G of row c / G.
 struct ChunkView {
   int rows, row0, seq, pos0, last;  // last: the last row's position
   const int32_t* table;
-  bool ok;
 
-  // The whole CTA: false for a chunk that adds nothing (the error is recorded).
+  // false for a chunk that adds nothing
   __device__ __forceinline__ bool open(const MassParams& p, int c) {
+    const int2 head = __ldcg(p.ws_head + p.chunk_index[c]);
     row0 = p.chunk_begin[c];
     rows = p.chunk_end[c] - row0;
-    seq = __ldg(p.seq_ids + row0);
-    pos0 = __ldg(p.positions + row0);
+    seq = head.x;
+    pos0 = head.y;
     last = pos0 + rows - 1;
-    bool bad = seq < 0 || seq >= p.num_seqs || pos0 < 0 || pos0 > p.max_blocks * p.P - rows;
-    table = p.block_tables + static_cast<size_t>(bad ? 0 : seq) * p.max_blocks;
-    if (!bad) {
-      for (int r = threadIdx.x; r < rows; r += blockDim.x)
-        bad |= __ldg(p.seq_ids + row0 + r) != seq || __ldg(p.positions + row0 + r) != pos0 + r;
-      for (int j = threadIdx.x; j <= last / p.P; j += blockDim.x) {
-        const int page = __ldg(table + j);
-        bad |= page < 0 || page >= p.num_pages;
-      }
-    }
-    ok = !__syncthreads_or(bad);
-    if (!ok && threadIdx.x == 0) record_error(p.status, ST_OUT_OF_RANGE);
-    return ok;
+    table = p.block_tables + static_cast<size_t>(max(seq, 0)) * p.max_blocks;
+    return seq >= 0;
   }
 };
 
@@ -494,7 +484,7 @@ __device__ __forceinline__ float2 column_stat(const MassParams& p, int c, int h,
                     static_cast<size_t>(tile) * kMassSlots + slot;
   const int n = pos / kMassSplitKeys + 1;
   ColumnStat st{-INFINITY, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 0; k < n; ++k) {
     const float2 o = __ldcg(s + k * stride);
     st.merge(o.x, o.y);

@@ -3,19 +3,14 @@
 
 namespace pa {
 
-cudaError_t launch_mass_tiles(const MassParams& p0, bool weights, cudaStream_t stream) {
-  MassParams p = p0;
-  const int R = kMtKeys / (p.Hq / p.Hkv);
-  long long ctas = 0;
-  for (int c = 0; c < p.n_chunks; ++c) {
-    p.chunk_cta[c] = static_cast<int32_t>(ctas);
-    const long long pairs = (p.chunk_end[c] - p.chunk_begin[c] + 2 * R - 1) / (2 * R);  // of column tiles
-    ctas += weights ? static_cast<long long>(p.Hkv) * p.n_ranges : pairs * p.Hkv * p.n_splits;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  }
-  p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);
-  if (p.D == 64) return weights ? launch_mass_tile_inst<64, true>(p, ctas, stream) : launch_mass_tile_inst<64, false>(p, ctas, stream);
-  return weights ? launch_mass_tile_inst<128, true>(p, ctas, stream) : launch_mass_tile_inst<128, false>(p, ctas, stream);
+cudaError_t launch_mass_tiles(const MassParams& p, bool weights, cudaStream_t stream) {
+  // no more CTAs than there can be units (the kernel counts them from the positions)
+  long long units = 0;
+  for (int c = 0; c < p.n_chunks; ++c)
+    units += static_cast<long long>(p.Hkv) * (static_cast<long long>(p.n_splits) * (weights ? 1 : (p.chunk_tiles[c] + 1) / 2));
+  if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (p.D == 64) return weights ? launch_mass_tile_inst<64, true>(p, units, stream) : launch_mass_tile_inst<64, false>(p, units, stream);
+  return weights ? launch_mass_tile_inst<128, true>(p, units, stream) : launch_mass_tile_inst<128, false>(p, units, stream);
 }
 
 }  // namespace pa

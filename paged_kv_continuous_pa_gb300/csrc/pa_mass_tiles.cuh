@@ -5,15 +5,18 @@
 // A chunk's columns for kv head h are its (row, query head) pairs, 128 / G rows
 // to a tile of 128 columns; a CTA works on two tiles at a time, so that a key
 // tile brought to shared memory serves 256 columns.
-//   mass_tile_kernel<D, false>: per (two tiles, key range) every column's maximum
-//     and sum.  S = Q K^T with the tiles' queries in tensor memory and key tiles of
-//     128 streamed; a thread owns a column (one lane of S) and goes over the keys.
-//   mass_tile_kernel<D, true>: per range of kMassRangeKeys keys the weights.
-//     S^T = K Q^T with two tiles' queries and their statistics resident and the key
-//     tiles streamed; a thread owns a key (one lane of S^T) and sums the weights of
-//     the columns.  Each group of warps has accumulators of its own; they are
+//   mass_tile_kernel<D, false>: per (two tiles, kMassSplitKeys keys) every column's maximum
+//     and sum.  S = Q K^T with the tiles' queries resident in shared memory and key
+//     tiles of 128 streamed; a thread owns a column (one lane of S) and goes over
+//     the keys.
+//   mass_tile_kernel<D, true>: per range of as many keys the weights.
+//     S^T = K Q^T, queries and key tiles alike, the columns' log2-sum-exps beside the
+//     queries; a thread owns a key (one lane of S^T) and sums the weights of the
+//     columns.  Each group of warps has accumulators of its own; they are
 //     joined in order at the end.  One addition to the buffer per key.
-// Both run 14 warps: twelve turn scores into sums (three groups of four, each with
+// Both run one CTA per SM that goes through its share of the units, so that the
+// copies of the next unit run while the scores of this one are summed, with 14
+// warps: twelve turn scores into sums (three groups of four, each with
 // its S buffer in tensor memory), one issues the copies, one the MMAs; they meet
 // at mbarriers only.
 //
@@ -22,6 +25,7 @@
 // Every wait is bounded; a call that gives up adds nothing and reports it.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "pa_mass.cuh"
@@ -42,7 +46,7 @@ enum {
   MT_SD0 = MT_KE0 + kMtKeyBufs,        // S buffer b computed
   MT_SE0 = MT_SD0 + kMtBuffers,        // ... read by its four warps
   MT_QF0 = MT_SE0 + kMtBuffers,        // queries of column tile 0 / 1 landed
-  MT_QE0 = MT_QF0 + 2,                 // ... done with by the score warps
+  MT_QE0 = MT_QF0 + 2,                 // ... read by their MMAs
   MT_STALL = MT_QE0 + 2,
   MT_COUNT
 };
@@ -52,16 +56,15 @@ struct MassTileSmem {  // byte offsets from a 1024-byte aligned base
   static constexpr int NH = D / 64;            // 64-element halves of the head dim
   static constexpr int HALF = kMtKeys * 128;   // one half of a tile of 128 rows
   static constexpr int TILE = NH * HALF;
-  static constexpr int Q_OFF = kMtKeyBufs * TILE;                // W: two query tiles
-  static constexpr int STAT_OFF = Q_OFF + (W ? 2 * TILE : 0);    // W: their statistics, [max x 128][1 / sum x 128]
-  static constexpr int ACC_OFF = STAT_OFF + (W ? 2 * 1024 : 0);  // per group: W a sum per key; else (max, sum) of two tiles
-  static constexpr int ACC = W ? kMassRangeKeys : 4 * kMtKeys;   // floats of a group
+  static constexpr int Q_OFF = kMtKeyBufs * TILE;                // two query tiles
+  static constexpr int STAT_OFF = Q_OFF + 2 * TILE;              // W: minus the log2-sum-exp of their columns
+  static constexpr int ACC_OFF = STAT_OFF + (W ? 2 * kMtKeys * 4 : 0);  // per group: W a sum per key; else (max, sum) of two tiles
+  static constexpr int ACC = W ? kMassSplitKeys : 4 * kMtKeys;   // floats of a group
   static constexpr int BAR_OFF = ACC_OFF + kMtBuffers * ACC * 4;
   static constexpr int TMEM_OFF = BAR_OFF + MT_COUNT * 8;
-  static constexpr int PID_OFF = BAR_OFF + 256;
-  static constexpr int PIDS = (W ? kMassRangeKeys : kMassSplitKeys) / 16;
-  static constexpr int BYTES = PID_OFF + PIDS * 4 + 1024;        // slack for aligning the base
-  static_assert(MT_COUNT * 8 + 4 <= 256 && BYTES <= 227 * 1024, "shared memory");
+  static constexpr int HEAD_OFF = BAR_OFF + 256;                 // the chunks
+  static constexpr int BYTES = HEAD_OFF + kMaxChunks * 16 + 1024;  // slack for aligning the base
+  static_assert(MT_COUNT * 8 + 8 <= 256 && BYTES <= 227 * 1024, "shared memory");
 };
 
 // 32 columns of this warp's lanes from tensor memory, without waiting ...
@@ -117,145 +120,150 @@ __device__ __forceinline__ void tma_load_3d(void* dst_smem, const CUtensorMap* m
       : "memory");
 }
 
-// Key tile `tile` (keys key0 + 128 tile ..) by the lanes of one warp: a box of
-// min(P, 64) keys x 64 elements per page piece and head-dim half.
-template <int D>
-__device__ __forceinline__ void mass_load_keys(const CUtensorMap* map, unsigned char* dst, uint64_t* bar,
-                                               const int32_t* ybase, int jp0, int t0, int lg_p, int lane) {
-  constexpr int NH = D / 64;
-  const int lg_br = lg_p < 6 ? lg_p : 6;
-  if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kMtKeys * D * 2));
-  __syncwarp();
-  if (lane < (kMtKeys >> lg_br) * NH) {
-    const int k = lane / NH, half = lane % NH;
-    const int t = t0 + (k << lg_br);
-    tc::tma_load_2d(dst + half * (kMtKeys * 128) + (k << lg_br) * 128, map, half * 64,
-                    ybase[(t >> lg_p) - jp0] + (t & ((1 << lg_p) - 1)), bar);
-  }
-}
+// A piece of work: for a kv head of a chunk two column tiles and a range of
+// keys (W false), or a range of keys and every column tile that sees it (W).
+struct MassUnit {
+  int chunk, h, row0, rows, seq, pos0, last;  // last: the last key that a row of the unit sees
+  int key0, nk;                               // first key, key tiles (0: nothing to do)
+  int t_first, t_end, split;                  // column tiles
+  const int32_t* table;
+};
 
 template <int D, bool W>
 __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_constant__ MassParams p) {
   using S = MassTileSmem<D, W>;
-  constexpr uint32_t kTmemQ = kMtBuffers * kMtKeys;  // W false: the two query tiles, behind the S buffers
-  constexpr uint32_t kTmemCols = 512;
-  static_assert(kTmemQ + D <= kTmemCols, "tensor memory");
+  constexpr uint32_t kTmemCols = 512;  // the S buffers (384; a power of two)
+  constexpr int kRange = kMassSplitKeys;
+  static_assert(kMtBuffers * kMtKeys <= kTmemCols, "tensor memory");
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR_OFF);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::TMEM_OFF);
-  int32_t* pids = reinterpret_cast<int32_t*>(sm + S::PID_OFF);  // tensor-map rows of the pages
+  int32_t* failed = reinterpret_cast<int32_t*>(sm + S::TMEM_OFF + 4);
+  int4* heads = reinterpret_cast<int4*>(sm + S::HEAD_OFF);  // per chunk: sequence, first position, units before and of it
   float* acc = reinterpret_cast<float*>(sm + S::ACC_OFF);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.Hq / p.Hkv, R = kMtKeys / G, lg_p = 31 - __clz(p.P);
 
-  int c = 0;
-  while (c + 1 < p.n_chunks && static_cast<int>(blockIdx.x) >= p.chunk_cta[c + 1]) ++c;
-  if (!W) griddep_launch_dependents();  // the weights' CTAs may be launched; what they read of this launch they wait for
-  const int local = blockIdx.x - p.chunk_cta[c];
-  const int h = local % p.Hkv, part = local / p.Hkv;
-  const int split = W ? 0 : part % p.n_splits, first_tile = W ? 0 : part / p.n_splits * 2;
-  ChunkView v;
-  const bool ok_chunk = v.open(p, c);
-  const int key0 = W ? part * kMassRangeKeys : split * kMassSplitKeys;  // the CTA's first key
-  const int row_end = W ? v.rows : min(v.rows, (first_tile + 2) * R);
-  const int last = v.pos0 + row_end - 1;  // the last key that a row of the CTA sees
-  if (!ok_chunk || key0 > last) {
-    if (warp == 0) tc::tmem_relinquish();
-    if (W) griddep_wait();  // no CTA of a dependent launch ends before the launch it depends on
-    return;
-  }
-  const int nk = min((W ? kMassRangeKeys : kMassSplitKeys) / kMtKeys, (last - key0) / kMtKeys + 1);  // key tiles
-  // The CTA's column tiles [t_first, t_end), two at a time, and how many of its key tiles a column tile sees.
-  // All roles go through the same steps: per two tiles the key tiles, per key tile the column tiles that see it.
-  const int t_end = (row_end + R - 1) / R, t_first = W ? max(0, key0 - v.pos0) / R : first_tile;
-  auto tiles_seen = [&](int t) {
-    const int end = v.pos0 + min(v.rows, (t + 1) * R) - 1;  // the last key that the column tile sees
-    return t < t_end && end >= key0 ? min(nk, (end - key0) / kMtKeys + 1) : 0;
-  };
-
   if (warp == 0) tc::tmem_alloc(tslot, kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < MT_COUNT; ++i)
-      mbar_init(&bar[i], i >= MT_SE0 && i < MT_SE0 + kMtBuffers ? 4u                // a group's warps
-                         : i >= MT_QE0 && i < MT_QE0 + 2        ? kMtScoreWarps : 1u);
+      mbar_init(&bar[i], i >= MT_SE0 && i < MT_SE0 + kMtBuffers ? 4u : 1u);  // (a group's warps)
+    *failed = 0;
     fence_barrier_init();
     tc::prefetch_tensormap(&p.kmap);
-    if (W) tc::prefetch_tensormap(&p.qmap);
-  }
-  const int jp0 = key0 / p.P, jp_last = (key0 + nk * kMtKeys - 1) / p.P;
-  for (int jp = jp0 + tid; jp <= jp_last; jp += kMtThreads) {
-    int pid = jp <= v.last / p.P ? __ldg(v.table + jp) : __ldg(v.table + jp0);  // past the chunk: any valid page (masked)
-    pids[jp - jp0] = (pid * p.Hkv + h) << lg_p;
+    tc::prefetch_tensormap(&p.qmap);
   }
   if (W)
     for (int i = tid; i < kMtBuffers * S::ACC; i += kMtThreads) acc[i] = 0.0f;
+  griddep_wait();  // the chunks' heads, and (W) their columns' statistics, from the launches before
+  if (!W) griddep_launch_dependents();
+  if (tid == 0) {
+    int before = 0;
+    for (int c = 0; c < p.n_chunks; ++c) {
+      const int2 hd = __ldcg(p.ws_head + p.chunk_index[c]);
+      const int rows = p.chunk_end[c] - p.chunk_begin[c];
+      int units = 0;  // a chunk that adds nothing has none
+      if (hd.x >= 0) units = p.Hkv * ((hd.y + rows - 1) / kRange + 1) * (W ? 1 : (p.chunk_tiles[c] + 1) / 2);
+      heads[c] = make_int4(hd.x, hd.y, before, units);
+      before += units;
+    }
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tb = *tslot;
   const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const int m = (warp & 3) * 32 + lane;  // this thread's lane of S
-  if constexpr (!W) {
-    // the queries into tensor memory: lane m holds column m of a tile (row m / G, head m % G)
-    if (warp < 8) {
-      uint32_t w[D / 2];
-      const int half = warp >> 2, r = (first_tile + half) * R + m / G;
-      if (m < R * G && r < v.rows) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                          (static_cast<size_t>(v.row0 + r) * p.Hq + h * G + m % G) * D);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = __ldg(src + i);
-          w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i) w[i] = 0u;
-      }
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        tc::tmem_st16(tb + lane_base + kTmemQ + half * (D / 2) + i * 16, *reinterpret_cast<uint32_t(*)[16]>(&w[16 * i]));
-      tc::tmem_wait_st();
-    }
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-  }
+  const int4 end_head = heads[p.n_chunks - 1];
+  const int total = end_head.z + end_head.w;
+
+  // unit i; every role goes through the same units, and in each through the same steps: per two column tiles
+  // the key tiles, per key tile the column tiles that see it
+  auto unit_at = [&](int i) {
+    MassUnit x;
+    int c = 0;
+    while (c + 1 < p.n_chunks && i >= heads[c + 1].z) ++c;
+    const int4 hd = heads[c];
+    const int local = i - hd.z;
+    x.chunk = c;
+    x.h = local % p.Hkv;
+    x.row0 = p.chunk_begin[c];
+    x.rows = p.chunk_end[c] - x.row0;
+    x.seq = hd.x;
+    x.pos0 = hd.y;
+    x.table = p.block_tables + static_cast<size_t>(x.seq) * p.max_blocks;
+    const int ranges = (x.pos0 + x.rows - 1) / kRange + 1, part = local / p.Hkv;
+    x.split = part % ranges;
+    x.key0 = x.split * kRange;
+    const int pair = part / ranges;
+    const int row_end = W ? x.rows : min(x.rows, (2 * pair + 2) * R);
+    x.last = x.pos0 + row_end - 1;
+    x.nk = x.key0 > x.last ? 0 : min(kRange / kMtKeys, (x.last - x.key0) / kMtKeys + 1);
+    x.t_first = W ? max(0, x.key0 - x.pos0) / R : 2 * pair;
+    x.t_end = (row_end + R - 1) / R;
+    return x;
+  };
+  // how many of a unit's key tiles column tile t sees
+  auto tiles_seen = [&](const MassUnit& x, int t) {
+    const int end = x.pos0 + min(x.rows, (t + 1) * R) - 1;  // the last key that the column tile sees
+    return t < x.t_end && end >= x.key0 ? min(x.nk, (end - x.key0) / kMtKeys + 1) : 0;
+  };
 
   PrefillIssueLog log;
   bool wok = !p.debug_stall || mbar_wait(&bar[MT_STALL], 0, p.wait_limit);  // the stall runs out
   wok = __all_sync(0xffffffffu, wok);
-  const float scale = p.qk_scale_log2_h[PA_HEAD(p, h)];
   // A barrier's use-th phase.  Every waiter of a phase has seen the one before it, or the phase cannot
   // begin without it: none mistakes an older phase of the same parity for its own.
   auto wait = [&](int b, int use) { return __all_sync(0xffffffffu, mbar_wait(&bar[b], use & 1, p.wait_limit)); };
 
   if (warp == kMtCopyWarp) {
     // ---- copies: key tile k into buffer k % 4 once the MMAs of key tile k - 4 are done
-    int k = 0;
-    for (int t = t_first, pair = 0; t < t_end && wok; t += 2, ++pair) {
-      const int n0 = tiles_seen(t), n1 = tiles_seen(t + 1), n = max(n0, n1);
-      if (W) {
-        for (int half = 0; half < 2 && t + half < t_end && wok; ++half) {
-          if (pair > 0) wok = wait(MT_QE0 + half, pair - 1);
-          if (!wok) break;
+    int k = 0, q_use[2] = {0, 0};
+    const int lg_br = lg_p < 6 ? lg_p : 6;  // rows of a box: a page, or a 64-key part of a larger page
+    const bool copies = lane < (kMtKeys >> lg_br) * S::NH;
+    for (int i = blockIdx.x; i < total && wok; i += gridDim.x) {
+      const MassUnit x = unit_at(i);
+      // the tensor-map row of this lane's box of key tile kt (keys past the chunk: its last page's, masked later)
+      auto box_row = [&](int kt) {
+        const int t = x.key0 + kt * kMtKeys + (lane / S::NH << lg_br);
+        const int page = copies ? __ldg(x.table + (min(t, x.pos0 + x.rows - 1) >> lg_p)) : 0;
+        return ((page * p.Hkv + x.h) << lg_p) + (t & (p.P - 1));
+      };
+      int row = x.nk > 0 ? box_row(0) : 0;
+      for (int t = x.t_first; t < x.t_end && x.nk > 0 && wok; t += 2) {
+        const int n = max(tiles_seen(x, t), tiles_seen(x, t + 1));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (t + half >= x.t_end || !wok) continue;
+          if (q_use[half] > 0) wok = wait(MT_QE0 + half, q_use[half] - 1);
+          if (!wok) continue;
+          ++q_use[half];
           if (lane == 0) {
             log.issue(MT_QF0 + half);
             mbar_arrive_expect_tx(&bar[MT_QF0 + half], static_cast<uint32_t>(S::NH * R * G * 128));
-            for (int i = 0; i < S::NH; ++i)
-              tma_load_3d(sm + S::Q_OFF + half * S::TILE + i * S::HALF, &p.qmap, i * 64, h * G, v.row0 + (t + half) * R,
-                          &bar[MT_QF0 + half]);
+            for (int j = 0; j < S::NH; ++j)
+              tma_load_3d(sm + S::Q_OFF + half * S::TILE + j * S::HALF, &p.qmap, j * 64, x.h * G,
+                          x.row0 + (t + half) * R, &bar[MT_QF0 + half]);
           }
           __syncwarp();
         }
-      }
-      for (int kt = 0; kt < n && wok; ++kt, ++k) {
-        const int b = k % kMtKeyBufs;
-        if (k >= kMtKeyBufs) wok = wait(MT_KE0 + b, k / kMtKeyBufs - 1);
-        if (!wok) break;
-        if (lane == 0) log.issue(MT_KF0 + b);
-        mass_load_keys<D>(&p.kmap, sm + b * S::TILE, &bar[MT_KF0 + b], pids, jp0, key0 + kt * kMtKeys, lg_p, lane);
+        for (int kt = 0; kt < n && wok; ++kt, ++k) {
+          const int b = k % kMtKeyBufs;
+          if (k >= kMtKeyBufs) wok = wait(MT_KE0 + b, k / kMtKeyBufs - 1);
+          if (!wok) break;
+          if (lane == 0) {
+            log.issue(MT_KF0 + b);
+            mbar_arrive_expect_tx(&bar[MT_KF0 + b], static_cast<uint32_t>(kMtKeys * D * 2));
+          }
+          __syncwarp();
+          if (copies) {
+            const int piece = lane / S::NH, half = lane % S::NH;
+            tc::tma_load_2d(sm + b * S::TILE + half * S::HALF + (piece << lg_br) * 128, &p.kmap, half * 64, row,
+                            &bar[MT_KF0 + b]);
+          }
+          row = box_row(kt + 1 < n ? kt + 1 : 0);  // the next key tile's, looked up while this one's buffer fills
+        }
       }
     }
   } else if (warp == kMtMmaWarp) {
@@ -263,175 +271,203 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
     constexpr uint32_t idesc = tc::idesc_bf16_f32(kMtKeys, kMtKeys, false);
     // descriptors of the first key and query tiles: others lie a constant number of 16-byte units away
     const uint64_t k_desc = tc::smem_desc(sm, 16, 1024), q_desc = tc::smem_desc(sm + S::Q_OFF, 16, 1024);
-    int k = 0, u = 0;
-    for (int t = t_first, pair = 0; t < t_end && wok; t += 2, ++pair) {
-      const int n0 = tiles_seen(t), n1 = tiles_seen(t + 1), n = max(n0, n1);
-      if (W) wok = wait(MT_QF0, pair) && (t + 1 >= t_end || wait(MT_QF0 + 1, pair));
-      for (int kt = 0; kt < n && wok; ++kt, ++k) {
-        const int kb = k % kMtKeyBufs;
-        wok = wait(MT_KF0 + kb, k / kMtKeyBufs);
-        for (int half = 0; half < 2 && wok; ++half) {
-          if (kt >= (half ? n1 : n0)) continue;
-          const int b = u % kMtBuffers;
-          if (u >= kMtBuffers) wok = wait(MT_SE0 + b, u / kMtBuffers - 1);
-          if (!wok) break;
-          if (lane == 0) {
-            tc::fence_after_sync();
-            const uint64_t kd = k_desc + kb * (S::TILE / 16), qd = q_desc + half * (S::TILE / 16);
+    int k = 0, u = 0, q_use[2] = {0, 0};
+    for (int i = blockIdx.x; i < total && wok; i += gridDim.x) {
+      const MassUnit x = unit_at(i);
+      for (int t = x.t_first; t < x.t_end && x.nk > 0 && wok; t += 2) {
+        const int n0 = tiles_seen(x, t), n1 = tiles_seen(x, t + 1), n = max(n0, n1);
+        wok = wait(MT_QF0, q_use[0]++);
+        if (t + 1 < x.t_end) wok = wok && wait(MT_QF0 + 1, q_use[1]++);
+        for (int kt = 0; kt < n && wok; ++kt, ++k) {
+          const int kb = k % kMtKeyBufs;
+          wok = wait(MT_KF0 + kb, k / kMtKeyBufs);
+          for (int half = 0; half < 2 && wok; ++half) {
+            if (kt >= (half ? n1 : n0)) continue;
+            const int b = u % kMtBuffers;
+            if (u >= kMtBuffers) wok = wait(MT_SE0 + b, u / kMtBuffers - 1);
+            if (!wok) break;
+            if (lane == 0) {
+              tc::fence_after_sync();
+              const uint64_t kd = k_desc + kb * (S::TILE / 16), qd = q_desc + half * (S::TILE / 16);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const int off = ((kk / 4) * S::HALF + (kk % 4) * 32) / 16;
-              if constexpr (W)
-                tc::mma_bf16(tb + b * kMtKeys, kd + off, qd + off, idesc, kk > 0);
-              else
-                tc::mma_bf16_ts(tb + b * kMtKeys, tb + kTmemQ + half * (D / 2) + kk * 8, kd + off, idesc, kk > 0);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const int off = ((kk / 4) * S::HALF + (kk % 4) * 32) / 16;
+                // W: lanes are keys and columns columns; else the other way round
+                tc::mma_bf16(tb + b * kMtKeys, (W ? kd : qd) + off, (W ? qd : kd) + off, idesc, kk > 0);
+              }
+              tc::mma_commit(&bar[MT_SD0 + b]);
+              log.issue(MT_SD0 + b);
             }
-            tc::mma_commit(&bar[MT_SD0 + b]);
-            log.issue(MT_SD0 + b);
+            __syncwarp();
+            ++u;
+          }
+          if (wok && lane == 0) {
+            tc::mma_commit(&bar[MT_KE0 + kb]);
+            log.issue(MT_KE0 + kb);
+            if (kt == n - 1) {
+              for (int half = 0; half < 2 && t + half < x.t_end; ++half) {
+                tc::mma_commit(&bar[MT_QE0 + half]);
+                log.issue(MT_QE0 + half);
+              }
+            }
           }
           __syncwarp();
-          ++u;
         }
-        if (wok && lane == 0) {
-          tc::mma_commit(&bar[MT_KE0 + kb]);
-          log.issue(MT_KE0 + kb);
-        }
-        __syncwarp();
       }
     }
   } else {
     const int group = warp >> 2;  // takes the steps u with u % 3 == group, and S buffer `group`
-    float* mine = acc + group * S::ACC;
-    float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};  // W false: this thread's columns
-    if (W) griddep_wait();  // the first launch's results
+    const float scale = p.qk_scale_log2_h[0];  // bf16 pools have no head scales
+    float* const mine = acc + group * S::ACC;
     int u = 0;
-    for (int t = t_first, pair = 0; t < t_end; t += 2, ++pair) {
-      const int n0 = tiles_seen(t), n1 = tiles_seen(t + 1), n = max(n0, n1);
-      if constexpr (W) {
-        // every column's (maximum, 1 / sum) of the two tiles, its key ranges merged in ascending order, a
-        // column to a thread (the score warps meet: the tiles before are done with)
-        if (pair > 0) asm volatile("bar.sync 1, %0;" ::"n"(kMtScoreWarps * 32) : "memory");
-        if (tid < 2 * kMtKeys) {
-          const int col = tid % kMtKeys, r = (t + tid / kMtKeys) * R + col / G;
-          float2 z = make_float2(0.0f, 0.0f);
-          if (col < R * G && r < v.rows) z = column_stat(p, c, h, t + tid / kMtKeys, col, v.pos0 + r);
-          float* stat = reinterpret_cast<float*>(sm + S::STAT_OFF + tid / kMtKeys * 1024);
-          stat[col] = z.x;
-          stat[kMtKeys + col] = z.y;
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kMtScoreWarps * 32) : "memory");
-      }
-      for (int kt = 0; kt < n && wok; ++kt) {
-        for (int half = 0; half < 2 && wok; ++half) {
-          if (kt >= (half ? n1 : n0)) continue;
-          const int use = u++;
-          if (use % kMtBuffers != group) continue;
-          const int t0 = key0 + kt * kMtKeys;
-          wok = wait(MT_SD0 + group, use / kMtBuffers);
-          if (!wok) break;
-          tc::fence_after_sync();
-          const uint32_t col = tb + lane_base + group * kMtKeys;
-          if constexpr (!W) {
-            // keys of the tile that the column sees: the first `seen`
-            const int seen = v.pos0 + min((t + half) * R + m / G, v.rows - 1) - t0 + 1;
-            const bool edge = v.pos0 + (t + half) * R - t0 + 1 < kMtKeys;  // some column of the tile sees less than all
-            float mr = half ? m_ref[1] : m_ref[0], lr = half ? l_run[1] : l_run[0];
-            over_columns(col, kMtKeys, [&](int i0, uint32_t(&x)[32]) {
-              float s[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(x[i]);
-              if (edge) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i0 + i >= seen) s[i] = -INFINITY;
-              }
-              float mx4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-              for (int i = 4; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[i]);
-              const float mx = __fmul_rn(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), scale);
-              if (mx > __fadd_rn(mr, kRescaleSlack)) {
-                lr = __fmul_rn(lr, ex2(__fsub_rn(mr, mx)));
-                mr = mx;
-              }
-              const float neg = mr == -INFINITY ? 0.0f : -mr;
-              float2 ls[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) ls[i] = make_float2(0.0f, 0.0f);
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 z = __ffma2_rn(make_float2(s[i], s[i + 1]), make_float2(scale, scale), make_float2(neg, neg));
-                ls[(i / 2) & 3] = __fadd2_rn(ls[(i / 2) & 3], make_float2(ex2(z.x), ex2(z.y)));
-              }
-              const float2 z = __fadd2_rn(__fadd2_rn(ls[0], ls[1]), __fadd2_rn(ls[2], ls[3]));
-              lr = __fadd_rn(lr, __fadd_rn(z.x, z.y));
-            });
-            if (half) m_ref[1] = mr, l_run[1] = lr;
-            else m_ref[0] = mr, l_run[0] = lr;
-          } else {
-            const float* stat = reinterpret_cast<const float*>(sm + S::STAT_OFF + half * 1024);
-            const int row0 = (t + half) * R, cols = min(R, v.rows - row0) * G;
-            // columns that see this thread's key: from `from` on (rows at or behind the key's position)
-            const int from = max(0, t0 + m - (v.pos0 + row0)) * G;
-            float2 w2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            // four columns' weights; in an edge tile those that do not see the key (or are none) are left
-            // out whole, so that nothing of theirs reaches it
-            auto add4 = [&](auto edge, const uint32_t(&x)[32], int i0, int i) {
-              const float4 M = *reinterpret_cast<const float4*>(stat + i0 + i);
-              float4 I = *reinterpret_cast<const float4*>(stat + kMtKeys + i0 + i);
-              const float2 sc = make_float2(scale, scale);
-              const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc, make_float2(-M.x, -M.y));
-              const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), sc, make_float2(-M.z, -M.w));
-              float2 e0 = make_float2(ex2(z0.x), ex2(z0.y)), e1 = make_float2(ex2(z1.x), ex2(z1.y));
-              if constexpr (decltype(edge)::value) {
-                const int j = i0 + i;
-                if (j < from || j >= cols) e0.x = I.x = 0.0f;
-                if (j + 1 < from || j + 1 >= cols) e0.y = I.y = 0.0f;
-                if (j + 2 < from || j + 2 >= cols) e1.x = I.z = 0.0f;
-                if (j + 3 < from || j + 3 >= cols) e1.y = I.w = 0.0f;
-              }
-              w2[0] = __ffma2_rn(e0, make_float2(I.x, I.y), w2[0]);
-              w2[1] = __ffma2_rn(e1, make_float2(I.z, I.w), w2[1]);
-            };
-            if (t0 + kMtKeys - 1 > v.pos0 + row0 || cols < kMtKeys)
-              over_columns(col, cols, [&](int i0, uint32_t(&x)[32]) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) add4(std::true_type(), x, i0, i);
-              });
-            else
-              over_columns(col, kMtKeys, [&](int i0, uint32_t(&x)[32]) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) add4(std::false_type(), x, i0, i);
-              });
-            const float2 w = __fadd2_rn(w2[0], w2[1]);
-            mine[kt * kMtKeys + m] = __fadd_rn(mine[kt * kMtKeys + m], __fadd_rn(w.x, w.y));
+    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kMtScoreWarps * 32) : "memory"); };
+    // The score warps meet the same number of times whatever a wait of theirs does (`wok` guards the waits).
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+      const MassUnit x = unit_at(i);
+      if (x.nk == 0) continue;
+      float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};  // W false: this thread's columns
+      for (int t = x.t_first; t < x.t_end; t += 2) {
+        const int n0 = tiles_seen(x, t), n1 = tiles_seen(x, t + 1), n = max(n0, n1);
+        if constexpr (W) {
+          // minus every column's log2-sum-exp, of the two tiles, a column to a thread
+          if (t > x.t_first) meet();  // the tiles before are done with
+          if (tid < 2 * kMtKeys) {
+            const int col = tid % kMtKeys, r = (t + tid / kMtKeys) * R + col / G;
+            float z = 0.0f;
+            if (col < R * G && r < x.rows) {
+              const float2 st = column_stat(p, x.chunk, x.h, t + tid / kMtKeys, col, x.pos0 + r);
+              z = __fsub_rn(log2f(st.y), st.x);  // (y is one over the sum)
+            }
+            reinterpret_cast<float*>(sm + S::STAT_OFF)[tid] = z;
           }
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[MT_SE0 + group]);
+          meet();
+        }
+        for (int kt = 0; kt < n && wok; ++kt) {
+          for (int half = 0; half < 2 && wok; ++half) {
+            if (kt >= (half ? n1 : n0)) continue;
+            const int use = u++;
+            if (use % kMtBuffers != group) continue;
+            const int t0 = x.key0 + kt * kMtKeys;
+            wok = wait(MT_SD0 + group, use / kMtBuffers);
+            if (!wok) break;
+            tc::fence_after_sync();
+            const uint32_t col = tb + lane_base + group * kMtKeys;
+            if constexpr (!W) {
+              // keys of the tile that the column sees: the first `seen`
+              const int seen = x.pos0 + min((t + half) * R + m / G, x.rows - 1) - t0 + 1;
+              const bool edge = x.pos0 + (t + half) * R - t0 + 1 < kMtKeys;  // some column of the tile sees less than all
+              float mr = half ? m_ref[1] : m_ref[0], lr = half ? l_run[1] : l_run[0];
+              over_columns(col, kMtKeys, [&](int i0, uint32_t(&y)[32]) {
+                float s[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(y[j]);
+                if (edge) {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (i0 + j >= seen) s[j] = -INFINITY;
+                }
+                float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int j = 4; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
+                const float mx = __fmul_rn(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), scale);
+                if (mx > __fadd_rn(mr, kRescaleSlack)) {
+                  lr = __fmul_rn(lr, ex2(__fsub_rn(mr, mx)));
+                  mr = mx;
+                }
+                const float neg = mr == -INFINITY ? 0.0f : -mr;
+                float2 ls[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ls[j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                  const float2 z = __ffma2_rn(make_float2(s[j], s[j + 1]), make_float2(scale, scale), make_float2(neg, neg));
+                  ls[(j / 2) & 3] = __fadd2_rn(ls[(j / 2) & 3], make_float2(ex2(z.x), ex2(z.y)));
+                }
+                const float2 z = __fadd2_rn(__fadd2_rn(ls[0], ls[1]), __fadd2_rn(ls[2], ls[3]));
+                lr = __fadd_rn(lr, __fadd_rn(z.x, z.y));
+              });
+              if (half) m_ref[1] = mr, l_run[1] = lr;
+              else m_ref[0] = mr, l_run[0] = lr;
+            } else {
+              const float* stat = reinterpret_cast<const float*>(sm + S::STAT_OFF) + half * kMtKeys;
+              const int first_row = (t + half) * R, cols = min(R, x.rows - first_row) * G;
+              // columns that see this thread's key: from `from` on (rows at or behind the key's position)
+              const int from = max(0, t0 + m - (x.pos0 + first_row)) * G;
+              float2 w2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+              // four columns' weights 2^(score - log2-sum-exp); in an edge tile those that do not see the key
+              // (or are none) are left out whole, so that nothing of theirs reaches it
+              auto add4 = [&](auto edge, const uint32_t(&y)[32], int i0, int j) {
+                const float4 z = *reinterpret_cast<const float4*>(stat + i0 + j);
+                const float2 sc = make_float2(scale, scale);
+                const float2 z0 = __ffma2_rn(make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), sc, make_float2(z.x, z.y));
+                const float2 z1 = __ffma2_rn(make_float2(__uint_as_float(y[j + 2]), __uint_as_float(y[j + 3])), sc, make_float2(z.z, z.w));
+                float2 e0 = make_float2(ex2(z0.x), ex2(z0.y)), e1 = make_float2(ex2(z1.x), ex2(z1.y));
+                if constexpr (decltype(edge)::value) {
+                  const int k = i0 + j;
+                  if (k < from || k >= cols) e0.x = 0.0f;
+                  if (k + 1 < from || k + 1 >= cols) e0.y = 0.0f;
+                  if (k + 2 < from || k + 2 >= cols) e1.x = 0.0f;
+                  if (k + 3 < from || k + 3 >= cols) e1.y = 0.0f;
+                }
+                w2[0] = __fadd2_rn(w2[0], e0);
+                w2[1] = __fadd2_rn(w2[1], e1);
+              };
+              if (t0 + kMtKeys - 1 > x.pos0 + first_row || cols < kMtKeys)
+                over_columns(col, cols, [&](int i0, uint32_t(&y)[32]) {
+#pragma unroll
+                  for (int j = 0; j < 32; j += 4) add4(std::true_type(), y, i0, j);
+                });
+              else
+                over_columns(col, kMtKeys, [&](int i0, uint32_t(&y)[32]) {
+#pragma unroll
+                  for (int j = 0; j < 32; j += 4) add4(std::false_type(), y, i0, j);
+                });
+              const float2 w = __fadd2_rn(w2[0], w2[1]);
+              mine[kt * kMtKeys + m] = __fadd_rn(mine[kt * kMtKeys + m], __fadd_rn(w.x, w.y));
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[MT_SE0 + group]);
+          }
         }
       }
-      if (W && wok && lane == 0) {
-        mbar_arrive(&bar[MT_QE0]);
-        if (t + 1 < t_end) mbar_arrive(&bar[MT_QE0 + 1]);
-      }
-    }
-    if constexpr (!W) {
-      // the groups' shares of the keys, merged in order (the score warps meet)
+      if (!wok) *failed = 1;
+      if constexpr (!W) {
+        meet();  // the unit before is merged (a group without a step of this one gets here early)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        mine[half * 2 * kMtKeys + m] = m_ref[half];
-        mine[half * 2 * kMtKeys + kMtKeys + m] = l_run[half];
+        for (int half = 0; half < 2; ++half) {
+          mine[half * 2 * kMtKeys + m] = m_ref[half];
+          mine[half * 2 * kMtKeys + kMtKeys + m] = l_run[half];
+        }
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(kMtScoreWarps * 32) : "memory");
-      const int half = group, row = (first_tile + half) * R + m / G;
-      if (group < 2 && wok && m < R * G && row < v.rows) {
-        ColumnStat s{-INFINITY, 0.0f};
+      meet();
+      if (*failed) continue;  // adds nothing
+      if constexpr (!W) {
+        // the groups' shares of the keys, merged in order
+        const int half = group, row = (x.t_first + half) * R + m / G;
+        if (group < 2 && m < R * G && row < x.rows) {
+          ColumnStat s{-INFINITY, 0.0f};
 #pragma unroll
-        for (int k = 0; k < kMtBuffers; ++k)
-          s.merge(acc[k * S::ACC + half * 2 * kMtKeys + m], acc[k * S::ACC + half * 2 * kMtKeys + kMtKeys + m]);
-        p.ws_part[p.chunk_part[c] +
-                  ((static_cast<size_t>(h) * p.n_splits + split) * p.chunk_tiles[c] + first_tile + half) * kMtKeys + m] =
-            make_float2(s.m, s.l);
+          for (int k = 0; k < kMtBuffers; ++k)
+            s.merge(acc[k * S::ACC + half * 2 * kMtKeys + m], acc[k * S::ACC + half * 2 * kMtKeys + kMtKeys + m]);
+          p.ws_part[p.chunk_part[x.chunk] +
+                    ((static_cast<size_t>(x.h) * p.n_splits + x.split) * p.chunk_tiles[x.chunk] + x.t_first + half) * kMtKeys + m] =
+              make_float2(s.m, s.l);
+        }
+      } else {
+        // the groups' sums of each key, in order; the accumulators are empty again for the next unit (whose
+        // score warps meet before they add)
+        float* sums = p.mass + (static_cast<size_t>(x.seq) * p.Hkv + x.h) * (static_cast<size_t>(p.max_blocks) << lg_p) + x.key0;
+        for (int j = tid; j < x.nk * kMtKeys; j += kMtScoreWarps * 32) {
+          float w = acc[j];
+          acc[j] = 0.0f;
+#pragma unroll
+          for (int k = 1; k < kMtBuffers; ++k) {
+            w = __fadd_rn(w, acc[k * S::ACC + j]);
+            acc[k * S::ACC + j] = 0.0f;
+          }
+          if (x.key0 + j <= x.last) atomicAdd(sums + j, w);
+        }
       }
     }
   }
@@ -443,14 +479,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
         if ((log.pending >> b) & 1u) mbar_wait(&bar[b], ((log.parity >> b) & 1u) ^ 1u, kDrainWaitLimit);
     }
     if (tid == 0) record_error(p.status, ST_TIMEOUT);
-  } else if (W) {
-    float* sums = p.mass + (static_cast<size_t>(v.seq) * p.Hkv + h) * (static_cast<size_t>(p.max_blocks) << lg_p) + key0;
-    for (int i = tid; i < nk * kMtKeys && key0 + i <= last; i += kMtThreads) {
-      float w = acc[i];
-#pragma unroll
-      for (int k = 1; k < kMtBuffers; ++k) w = __fadd_rn(w, acc[k * S::ACC + i]);
-      atomicAdd(sums + i, w);
-    }
+    if (!W && tid < p.n_chunks) p.ws_head[p.chunk_index[tid]].x = -1;  // no weights without the statistics
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -461,13 +490,14 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
 }
 
 template <int D, bool W>
-cudaError_t launch_mass_tile_inst(const MassParams& p, long long ctas, cudaStream_t stream) {
+cudaError_t launch_mass_tile_inst(const MassParams& p, long long units, cudaStream_t stream) {
   static std::atomic<unsigned long long> smem_done{0};
-  const cudaError_t e = allow_dynamic_smem(mass_tile_kernel<D, W>, smem_done, MassTileSmem<D, W>::BYTES);
-  if (e != cudaSuccess) return e;
+  static std::atomic<long long> resident[64];
+  const long long ctas = resident_ctas(mass_tile_kernel<D, W>, resident, smem_done, kMtThreads, MassTileSmem<D, W>::BYTES);
+  if (ctas <= 0) return cudaErrorInvalidConfiguration;
   count_launch();
-  return launch_kernel(mass_tile_kernel<D, W>, dim3(static_cast<unsigned>(ctas)), dim3(kMtThreads),
-                       MassTileSmem<D, W>::BYTES, stream, W, p);
+  return launch_kernel(mass_tile_kernel<D, W>, dim3(static_cast<unsigned>(std::min(units, ctas))), dim3(kMtThreads),
+                       MassTileSmem<D, W>::BYTES, stream, true, p);
 }
 
 }  // namespace pa

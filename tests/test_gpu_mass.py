@@ -303,3 +303,17 @@ def test_long_chunks(rows, start, G):
     c = R.make_cache([start + rows], Hkv=1, D=64, P=32, seed=rows)
     q = queries(rows, G, 64, torch.bfloat16, seed=rows)
     check(c, q, c.slots * rows, list(range(start, start + rows)), [(0, rows)])
+
+
+def test_many_short_units():
+    """More pieces of work than CTAs, some of one key tile, so that a CTA's warps reach its next piece at
+    different times: right, and the same bits each time."""
+    lengths = [1030 + 37 * i for i in range(12)]
+    c = R.make_cache(lengths, Hkv=32, D=64, P=16, seed=41)
+    q = queries(16 * 12, 32, 64, torch.bfloat16, seed=41)
+    seq = [s for s in c.slots for _ in range(16)]
+    pos = [n - 16 + i for n in c.lengths for i in range(16)]
+    chunks = [(16 * i, 16) for i in range(12)]
+    first = check(c, q, seq, pos, chunks, seed=41)
+    for _ in range(5):
+        assert torch.equal(check(c, q, seq, pos, chunks, seed=41), first)
