@@ -220,7 +220,8 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
  * Precondition: a sequence has one row outside the chunks, or the rows of one
  * chunk, in a call (a step's rows satisfy it): its sums then have one writer
  * and the same bits in any batch.
- * Sums and weights are FP32.  Errors as for pa_attention; a row with an
+ * Sums and weights are FP32.  max_blocks_per_seq * page_size <= 2^30.  Errors as
+ * for pa_attention; a row with an
  * invalid sequence, position or page, or a chunk with such a row or whose rows
  * are not consecutive positions of one sequence, adds nothing and records
  * PA_ERR_OUT_OF_RANGE.  Graph-capturable. */
@@ -245,7 +246,7 @@ pa_status pa_attention_mass(const pa_pool *pool, int32_t n_rows, const void *q, 
  *                     fills it with max_tokens = max_blocks_per_seq * page_size
  *   keep              int32 [n][num_kv_heads][budget], written whole
  *   kept_lengths      int32 [n], receives count (may be NULL; may not be `lengths`)
- * keep_first + keep_last <= budget.  One launch, no workspace; graph-capturable.
+ * keep_first + keep_last <= budget; max_tokens <= 2^30.  One launch, no workspace; graph-capturable.
  * A row whose sequence is outside [0, num_seqs) or whose length is outside
  * [0, max_tokens] keeps nothing (all -1, count 0) and records
  * PA_ERR_OUT_OF_RANGE. */
@@ -268,7 +269,8 @@ pa_status pa_evict_select(int32_t n, const int32_t *seq_ids, const int32_t *leng
  * Precondition: no slot is listed twice, as a source of one row and a
  * destination of another either, and a page that receives tokens belongs to
  * that one sequence (in place: pages shared with another sequence would change
- * under it).  One launch, no workspace; graph-capturable.
+ * under it).  max_blocks_per_seq * page_size <= 2^30.  One launch, no workspace;
+ * graph-capturable.
  * Device-side, with PA_ERR_OUT_OF_RANGE: a row with an invalid slot or length
  * moves nothing; a kept token out of order or range, or one whose page id is
  * invalid, is not moved and its destination is unspecified. */

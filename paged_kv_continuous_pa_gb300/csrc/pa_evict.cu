@@ -644,7 +644,7 @@ pa_status pa_evict_compact(const pa_pool* pool, int32_t n, const int32_t* seq_id
   if (num_seqs <= 0 || max_blocks_per_seq <= 0)
     return fail(PA_ERR_INVALID_ARG, "num_seqs and max_blocks_per_seq must be positive");
   const pa_pool_desc& d = pool->desc;
-  if (static_cast<int64_t>(max_blocks_per_seq) * d.page_size > 0x7fffffff)
+  if (static_cast<int64_t>(max_blocks_per_seq) * d.page_size > (1 << 30))  // (tokens and steps beyond stay int32)
     return fail(PA_ERR_UNSUPPORTED, "a block-table row of %d pages of %d tokens", max_blocks_per_seq, d.page_size);
   if (budget <= 0) return fail(PA_ERR_INVALID_ARG, "budget %d must be positive", budget);
   if (n == 0) return PA_OK;

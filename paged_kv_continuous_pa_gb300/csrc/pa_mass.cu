@@ -120,7 +120,7 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
   const pa_pool_desc& d = pool->desc;
   pa_status st = pa::check_rows(d, n_rows, q_dtype, num_q_heads, num_seqs, max_blocks_per_seq, chunks, n_chunks);
   if (st != PA_OK) return st;
-  if (static_cast<int64_t>(max_blocks_per_seq) * d.page_size > 0x7fffffff)
+  if (static_cast<int64_t>(max_blocks_per_seq) * d.page_size > (1 << 30))  // (positions and steps beyond stay int32)
     return fail(PA_ERR_UNSUPPORTED, "a block-table row of %d pages of %d tokens", max_blocks_per_seq, d.page_size);
   if (n_rows == 0) return PA_OK;
   if (!q || !seq_ids || !positions || !block_tables || !mass)

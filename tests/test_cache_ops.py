@@ -262,3 +262,20 @@ def test_trim_refusals(lib):
         p.trim(0, -1)
     assert lib.pa_pages_trim(None, 0, 0, None) == pa.PA_ERR_INVALID_ARG
     assert lib.pa_pages_trim(p.handle, 0, 16, None) == pa.PA_OK and p.free_count() == 7
+
+
+def test_longest_block_table(lib, pool):
+    """Tables of more than 2^30 tokens are refused (positions and steps beyond them stay 32-bit)."""
+    longest = (1 << 30) // 32
+
+    def mass(blocks):
+        return lib.pa_attention_mass(pool, 4, None, pa.PA_BF16, 8, None, None, None, 4, blocks, None, 0, 0.0, None, None,
+                                     0, None, None)
+
+    def compact(blocks):
+        return lib.pa_evict_compact(pool, 0, None, None, None, None, 8, None, 4, blocks, None, None, None)
+
+    assert mass(longest) == pa.PA_ERR_INVALID_ARG and "NULL" in pa.last_error()  # as far as its pointers
+    assert mass(longest + 1) == pa.PA_ERR_UNSUPPORTED
+    assert compact(longest) == pa.PA_OK
+    assert compact(longest + 1) == pa.PA_ERR_UNSUPPORTED
