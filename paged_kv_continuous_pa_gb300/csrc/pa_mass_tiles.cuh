@@ -15,10 +15,10 @@
 //     columns.  Each group of warps has accumulators of its own; they are
 //     joined in order at the end.  One addition to the buffer per key.
 // Both run one CTA per SM that goes through its share of the units, so that the
-// copies of the next unit run while the scores of this one are summed, with 14
-// warps: twelve turn scores into sums (three groups of four, each with
-// its S buffer in tensor memory), one issues the copies, one the MMAs; they meet
-// at mbarriers only.
+// copies of the next unit run while the scores of this one are summed, with 15
+// warps: twelve turn scores into sums (three groups of four, each with its S
+// buffer in tensor memory), one issues the copies, two the MMAs; they meet at
+// mbarriers only.
 //
 // The scores are computed twice (a weight needs its column's sum over all
 // keys first): 4 D operations and two exponentials per visible (row, head, key).
@@ -37,8 +37,8 @@ constexpr int kMtKeys = 128;      // keys of a key tile, columns of a column til
 constexpr int kMtBuffers = 3;     // S buffers, each with a group of four score warps
 constexpr int kMtKeyBufs = 4;     // key tiles in shared memory
 constexpr int kMtScoreWarps = 4 * kMtBuffers;
-constexpr int kMtCopyWarp = kMtScoreWarps, kMtMmaWarp = kMtCopyWarp + 1;
-constexpr int kMtThreads = 32 * (kMtMmaWarp + 1);
+constexpr int kMtCopyWarp = kMtScoreWarps, kMtMmaWarp = kMtCopyWarp + 1;  // ... two MMA warps
+constexpr int kMtThreads = 32 * (kMtMmaWarp + 2);
 
 enum {
   MT_KF0 = 0,                          // key tile in buffer b landed
@@ -47,7 +47,8 @@ enum {
   MT_SE0 = MT_SD0 + kMtBuffers,        // ... read by its four warps
   MT_QF0 = MT_SE0 + kMtBuffers,        // queries of column tile 0 / 1 landed
   MT_QE0 = MT_QF0 + 2,                 // ... read by their MMAs
-  MT_STALL = MT_QE0 + 2,
+  MT_DRAIN0 = MT_QE0 + 2,              // after a failure: all of MMA warp 0's / 1's MMAs done
+  MT_STALL = MT_DRAIN0 + 2,
   MT_COUNT
 };
 
@@ -148,7 +149,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
   if (warp == 0) tc::tmem_alloc(tslot, kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < MT_COUNT; ++i)
-      mbar_init(&bar[i], i >= MT_SE0 && i < MT_SE0 + kMtBuffers ? 4u : 1u);  // (a group's warps)
+      mbar_init(&bar[i], i >= MT_SE0 && i < MT_SE0 + kMtBuffers   ? 5u  // a group's warps, and the other MMA warp
+                         : i >= MT_KE0 && i < MT_KE0 + kMtKeyBufs ? 2u  // the MMA warps
+                                                                  : 1u);
     *failed = 0;
     fence_barrier_init();
     tc::prefetch_tensormap(&p.kmap);
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
     return t < x.t_end && end >= x.key0 ? min(x.nk, (end - x.key0) / kMtKeys + 1) : 0;
   };
 
-  PrefillIssueLog log;
+  PrefillIssueLog log;  // of the copies
   bool wok = !p.debug_stall || mbar_wait(&bar[MT_STALL], 0, p.wait_limit);  // the stall runs out
   wok = __all_sync(0xffffffffu, wok);
   // A barrier's use-th phase.  Every waiter of a phase has seen the one before it, or the phase cannot
@@ -266,18 +269,21 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
         }
       }
     }
-  } else if (warp == kMtMmaWarp) {
-    // ---- MMAs: step u into S buffer u % 3 once its four warps have read step u - 3
+  } else if (warp >= kMtMmaWarp) {
+    // ---- MMAs: step u into S buffer u % 3 once its four warps have read step u - 3.  One MMA warp has the first
+    // column tile of two, one the second (issuing a tile's MMAs holds a warp about as long as they run, so one's
+    // waits go beside the other's MMAs).  Both go through all steps: at the other's step a warp only adds its
+    // arrival to the buffer's barrier, so that no phase of it passes that one of the two has not seen.
+    const int my_half = warp - kMtMmaWarp;
     constexpr uint32_t idesc = tc::idesc_bf16_f32(kMtKeys, kMtKeys, false);
     // descriptors of the first key and query tiles: others lie a constant number of 16-byte units away
     const uint64_t k_desc = tc::smem_desc(sm, 16, 1024), q_desc = tc::smem_desc(sm + S::Q_OFF, 16, 1024);
-    int k = 0, u = 0, q_use[2] = {0, 0};
+    int k = 0, u = 0, q_use = 0;
     for (int i = blockIdx.x; i < total && wok; i += gridDim.x) {
       const MassUnit x = unit_at(i);
       for (int t = x.t_first; t < x.t_end && x.nk > 0 && wok; t += 2) {
         const int n0 = tiles_seen(x, t), n1 = tiles_seen(x, t + 1), n = max(n0, n1);
-        wok = wait(MT_QF0, q_use[0]++);
-        if (t + 1 < x.t_end) wok = wok && wait(MT_QF0 + 1, q_use[1]++);
+        if (t + my_half < x.t_end) wok = wait(MT_QF0 + my_half, q_use++);
         for (int kt = 0; kt < n && wok; ++kt, ++k) {
           const int kb = k % kMtKeyBufs;
           wok = wait(MT_KF0 + kb, k / kMtKeyBufs);
@@ -286,7 +292,8 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
             const int b = u % kMtBuffers;
             if (u >= kMtBuffers) wok = wait(MT_SE0 + b, u / kMtBuffers - 1);
             if (!wok) break;
-            if (lane == 0) {
+            if (lane == 0 && half != my_half) mbar_arrive(&bar[MT_SE0 + b]);
+            if (lane == 0 && half == my_half) {
               tc::fence_after_sync();
               const uint64_t kd = k_desc + kb * (S::TILE / 16), qd = q_desc + half * (S::TILE / 16);
 #pragma unroll
@@ -296,20 +303,13 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
                 tc::mma_bf16(tb + b * kMtKeys, (W ? kd : qd) + off, (W ? qd : kd) + off, idesc, kk > 0);
               }
               tc::mma_commit(&bar[MT_SD0 + b]);
-              log.issue(MT_SD0 + b);
             }
             __syncwarp();
             ++u;
           }
           if (wok && lane == 0) {
             tc::mma_commit(&bar[MT_KE0 + kb]);
-            log.issue(MT_KE0 + kb);
-            if (kt == n - 1) {
-              for (int half = 0; half < 2 && t + half < x.t_end; ++half) {
-                tc::mma_commit(&bar[MT_QE0 + half]);
-                log.issue(MT_QE0 + half);
-              }
-            }
+            if (kt == n - 1 && t + my_half < x.t_end) tc::mma_commit(&bar[MT_QE0 + my_half]);
           }
           __syncwarp();
         }
@@ -474,9 +474,10 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
   const bool ok = __syncthreads_and(wok);
   if (!ok) {
     // every copy and MMA in flight finishes before its memory is given back
-    if (lane == 0 && (warp == kMtCopyWarp || warp == kMtMmaWarp)) {
-      for (int b = 0; b < MT_COUNT; ++b)
-        if ((log.pending >> b) & 1u) mbar_wait(&bar[b], ((log.parity >> b) & 1u) ^ 1u, kDrainWaitLimit);
+    if (lane == 0 && warp == kMtCopyWarp) log.drain(bar, MT_COUNT);
+    if (lane == 0 && warp >= kMtMmaWarp) {
+      tc::mma_commit(&bar[MT_DRAIN0 + warp - kMtMmaWarp]);
+      mbar_wait(&bar[MT_DRAIN0 + warp - kMtMmaWarp], 0, kDrainWaitLimit);
     }
     if (tid == 0) record_error(p.status, ST_TIMEOUT);
     if (!W && tid < p.n_chunks) p.ws_head[p.chunk_index[tid]].x = -1;  // no weights without the statistics
