@@ -109,8 +109,10 @@ __device__ __forceinline__ void load_groups(const float* w, bool vec, int t0, in
 // One CTA per (sequence, kv head).  Of the N tokens between the protected ones
 // the m with the largest weights stay; what has to be known is the last weight
 // kept and how many tokens of exactly that weight stay (the lowest indices).
-//   1. 512 samples, evenly spaced, give two pivots that enclose the m-th weight
-//      (3.5 standard deviations of a sample rank to either side).
+//   1. 512 samples, four to each of 128 evenly spaced places (44 us at 64 x 32768
+//      tokens; 512 places, each a memory access of its own, 47.5), give two pivots
+//      that enclose the m-th weight (3.5 standard deviations of a sample rank to
+//      either side).
 //   2. One pass counts the weights from the upper pivot on and lists those between
 //      the two (a few in a hundred; no sample is taken where all fit).
 //   3. A histogram of the listed keys, over their range, finds the bin of the last
@@ -165,8 +167,11 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     float low = -INFINITY, high = INFINITY;
     if (N > kSelectAll) {
       float* samples = sm.list[0];
-      for (int k = tid; k < kSelectSamples; k += kSelectThreads)
-        samples[k] = __ldg(w + a + static_cast<int>((static_cast<long long>(2 * k + 1) * N) / (2 * kSelectSamples)));
+      for (int k = tid; k < kSelectSamples; k += kSelectThreads) {
+        // four samples, four tokens apart, to a place: N > 2^13, so the last place is more than 16 tokens from b
+        const int at = static_cast<int>((static_cast<long long>(2 * (k / 4) + 1) * N) / (kSelectSamples / 2));
+        samples[k] = __ldg(w + a + at + k % 4 * 4);
+      }
       __syncthreads();
       if (warp < 2) {
         const float rank = static_cast<float>(m) * kSelectSamples / N;
@@ -426,29 +431,29 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     kept_base += all_g + min(tie_base + all_e, ties) - min(tie_base, ties);
     tie_base += all_e;
     __syncthreads();
-    const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 4
-    for (int g = warp; g < groups; g += kSelectWarps) {
+    // a group to a thread, which goes over the lanes that marked something (a lane a step: four tokens)
+    for (int g = tid; g < groups; g += kSelectThreads) {
       const uint4 x = *reinterpret_cast<const uint4*>(sm.above[g]);
-      uint32_t keep_bits = ((x.x >> lane) & 1u) | ((x.y >> lane) & 1u) << 1 | ((x.z >> lane) & 1u) << 2 | ((x.w >> lane) & 1u) << 3;
-      uint32_t at = sm.before[g][0] + __popc(x.x & below) + __popc(x.y & below) + __popc(x.z & below) + __popc(x.w & below);
-      if (ties > 0u) {
-        const uint4 y = *reinterpret_cast<const uint4*>(sm.equal[g]);
-        const uint32_t tie0 = sm.before[g][1];
-        uint32_t tie = tie0 + __popc(y.x & below) + __popc(y.y & below) + __popc(y.z & below) + __popc(y.w & below);
-        at += min(tie, ties) - min(tie0, ties);  // ties of the lanes before that stayed
-        const uint32_t eq[4] = {y.x, y.y, y.z, y.w};
+      uint4 y = make_uint4(0u, 0u, 0u, 0u);
+      int32_t* out = keep + sm.before[g][0];
+      uint32_t left = 0u;  // ties that may still stay
+      if (ties > sm.before[g][1]) {
+        left = ties - sm.before[g][1];
+        y = *reinterpret_cast<const uint4*>(sm.equal[g]);
+      }
+      for (uint32_t any = x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w; any != 0u; any &= any - 1u) {
+        const int l = __ffs(any) - 1, t = c0 + g * 128 + l * 4;
+        const uint32_t kept[4] = {x.x, x.y, x.z, x.w}, tied[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t same = (eq[e] >> lane) & 1u;
-          if (same && tie < ties) keep_bits |= 1u << e;
-          tie += same;
+          bool stays = (kept[e] >> l) & 1u;
+          if (left > 0u && ((tied[e] >> l) & 1u)) {
+            stays = true;
+            --left;
+          }
+          if (stays) *out++ = t + e;
         }
       }
-      const int t = c0 + g * 128 + lane * 4;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if ((keep_bits >> e) & 1u) keep[at++] = t + e;
     }
   }
 }
