@@ -24,11 +24,9 @@ struct SelectParams {
   int32_t n, num_seqs, Hkv, max_tokens, budget, keep_first, keep_last;
 };
 
-constexpr int kSelectThreads = 256;
-constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectSamples = 512;
+constexpr int kSelectNarrow = 256, kSelectWide = 1024;         // threads of a CTA
+constexpr int kSelectSamples = 512;                         // or twice as many
 constexpr int kSelectSlots = 32;                            // weights a thread can list
-constexpr int kSelectAll = kSelectSlots * kSelectThreads;   // that many competing tokens need no sample
 constexpr int kSelectGroups = 512;                          // groups of 128 tokens marked at once
 constexpr int kSelectBinBits = 11;
 constexpr int kSelectBins = 1 << kSelectBinBits;
@@ -45,8 +43,9 @@ __device__ __forceinline__ float key_weight(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 
+template <int THREADS>
 struct SelectSmem {
-  float list[kSelectSlots][kSelectThreads];  // weights between the two pivots, a column to a thread
+  float list[kSelectSlots][THREADS];  // weights between the two pivots, a column to a thread
   union {
     uint32_t bins[kSelectBins];
     struct {
@@ -56,15 +55,15 @@ struct SelectSmem {
   };
   uint32_t before[kSelectGroups][2];  // kept tokens and ties before a group
   int pick[3], gathered;
-  uint32_t count[2][kSelectWarps][2];
-  uint32_t warp_sum[kSelectWarps][2];
+  uint32_t count[2][THREADS / 32][2];
+  uint32_t warp_sum[THREADS / 32][2];
   float pivot[2];
   int overflow;
 };
 
-// One warp: a key that `want` of the samples reach, or a few more.
+// One warp: a key that `want` of the 32 PER samples reach, or a few more.
+template <int PER>
 __device__ __forceinline__ uint32_t sample_pivot(const float* samples, int want, int lane) {
-  constexpr int PER = kSelectSamples / 32;
   uint32_t k[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) k[i] = weight_key(samples[i * 32 + lane]);
@@ -118,13 +117,21 @@ __device__ __forceinline__ void load_groups(const float* w, bool vec, int t0, in
 //   3. A histogram of the listed keys, over their range, finds the bin of the last
 //      one; its few keys are ranked by counting (or it is the next range).
 //   4. A second pass (from L2) marks the kept tokens as bits; counts over groups of
-//      128 tokens place them, in ascending order.
+//      128 tokens place them, in ascending order, a group to a thread where few
+//      stay (2048 of 32768: 45 us, a group to a warp 47), else to a warp (28000 of
+//      32768: 65 us against 145).
 // Where the pivots miss (the m-th weight outside, or a thread's list too short,
 // as a hostile order can bring about) step 3 goes over the weights themselves.
-// Bound by the latency of the steps at the first read's rate: one wave of CTAs.
-__global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_constant__ SelectParams p) {
+// Bound by the latency of the steps, of which a CTA's are in a row: 64 x 8 rows of
+// 32768 take 45 us (67 MB read from memory and again from L2: 1.5 TB/s), a third of
+// it the first pass, a quarter the second, a fifth the samples; 1024 threads to a
+// CTA bring long rows' passes down (16 x 8 rows of 131072: 166 to 43 us).
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int WARPS = THREADS / 32;
+  constexpr int ALL = kSelectSlots * THREADS;  // that many competing tokens need no sample
   extern __shared__ __align__(16) unsigned char select_smem[];
-  SelectSmem& sm = *reinterpret_cast<SelectSmem*>(select_smem);
+  SelectSmem<THREADS>& sm = *reinterpret_cast<SelectSmem<THREADS>*>(select_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int i = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   const int seq = __ldg(p.seq_ids + i), len = __ldg(p.lengths + i);
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     if (p.kept_lengths != nullptr) p.kept_lengths[i] = bad ? 0 : min(len, p.budget);
   }
   if (bad || len <= p.budget) {  // everything stays (or nothing, of a bad row)
-    for (int j = tid; j < p.budget; j += kSelectThreads) keep[j] = (!bad && j < len) ? j : -1;
+    for (int j = tid; j < p.budget; j += THREADS) keep[j] = (!bad && j < len) ? j : -1;
     return;
   }
   const float* w = p.mass + (static_cast<size_t>(seq) * p.Hkv + h) * p.max_tokens;
@@ -155,7 +162,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     __syncthreads();
     x = y = 0u;
 #pragma unroll
-    for (int k = 0; k < kSelectWarps; ++k) {
+    for (int k = 0; k < WARPS; ++k) {
       x += sm.count[turn][k][0];
       y += sm.count[turn][k][1];
     }
@@ -165,20 +172,29 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
   uint32_t last = 0xffffffffu, ties = 0u, equals = 0u;
   if (m > 0) {
     float low = -INFINITY, high = INFINITY;
-    if (N > kSelectAll) {
+    if (N > ALL) {
       float* samples = sm.list[0];
-      for (int k = tid; k < kSelectSamples; k += kSelectThreads) {
-        // four samples, four tokens apart, to a place: N > 2^13, so the last place is more than 16 tokens from b
-        const int at = static_cast<int>((static_cast<long long>(2 * (k / 4) + 1) * N) / (kSelectSamples / 2));
+      // ranks to either side of the m-th weight's among s samples
+      auto margin = [&](int s) {
+        const float share = static_cast<float>(m) / N;
+        return 3.5f * sqrtf(s * share * (1.0f - share)) + 2.0f;
+      };
+      // a thread lists 2 margin / samples of its N / THREADS weights: twice the samples where that would come near the
+      // room it has (budgets in the middle, long rows)
+      const bool twice = 2.0f * margin(kSelectSamples) * N > 0.375f * kSelectSlots * kSelectSamples * THREADS;
+      const int count = twice ? 2 * kSelectSamples : kSelectSamples;
+      for (int k = tid; k < count; k += THREADS) {
+        // four samples, four tokens apart, to a place: N > 2^13, so the last place is at least 16 tokens from b
+        const int at = static_cast<int>((static_cast<long long>(2 * (k / 4) + 1) * N) / (count / 2));
         samples[k] = __ldg(w + a + at + k % 4 * 4);
       }
       __syncthreads();
       if (warp < 2) {
-        const float rank = static_cast<float>(m) * kSelectSamples / N;
-        const float off = 3.5f * sqrtf(rank * (1.0f - rank / kSelectSamples)) + 2.0f;
+        const float rank = static_cast<float>(m) * count / N, off = margin(count);
         const int want = static_cast<int>(warp == 0 ? rank - off : rank + off + 1.0f);
         uint32_t pivot = 0u;
-        if (want >= 1 && want <= kSelectSamples) pivot = sample_pivot(samples, want, lane);
+        if (want >= 1 && want <= count)
+          pivot = twice ? sample_pivot<2 * kSelectSamples / 32>(samples, want, lane) : sample_pivot<kSelectSamples / 32>(samples, want, lane);
         // no pivot, or a NaN: every number
         if (lane == 0) sm.pivot[warp] = pivot == 0u ? (warp == 0 ? INFINITY : -INFINITY) : key_weight(pivot);
       }
@@ -190,7 +206,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     __syncthreads();
     uint32_t from_high = 0u;
     int listed = 0;  // of this thread
-    constexpr int STRIDE = kSelectWarps * 128;
+    constexpr int STRIDE = WARPS * 128;
     // four comparisons and a store in predicates, no branch: a weight between the pivots goes to the next
     // slot, or the last one over and over (which `overflow` reports)
     auto list4 = [&](const float(&x)[4]) {
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     if (found && need > between) {
       // weights equal to `low` come next (many equal ones, or -infinity), then, behind -infinity, NaNs
       uint32_t same = 0u;
-      for (int t = a + tid; t < b; t += kSelectThreads) same += __ldg(w + t) == low;
+      for (int t = a + tid; t < b; t += THREADS) same += __ldg(w + t) == low;
       const int n = static_cast<int>(sum2(same, 0u).x);
       at_low = need <= between + n || low == -INFINITY;
       if (at_low) {
@@ -257,20 +273,20 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
         if (found)
           for (int e = 0; e < listed; ++e) f(weight_key(sm.list[e][tid]));
         else
-          for (int t = a + tid; t < b; t += kSelectThreads) f(weight_key(__ldg(w + t)));
+          for (int t = a + tid; t < b; t += THREADS) f(weight_key(__ldg(w + t)));
       };
       for (bool more = true; more;) {
         // a histogram of the range's keys, and the bin that holds the last one
         const int shift = max(0, 32 - __clz(hi - 1u - lo) - kSelectBinBits);
         __syncthreads();
-        for (int k = tid; k < kSelectBins; k += kSelectThreads) sm.bins[k] = 0u;
+        for (int k = tid; k < kSelectBins; k += THREADS) sm.bins[k] = 0u;
         if (tid == 0) sm.gathered = 0;
         __syncthreads();
         each_key([&](uint32_t key) {
           if (key >= lo && key < hi) atomicAdd(&sm.bins[(key - lo) >> shift], 1u);
         });
         __syncthreads();
-        constexpr int PER = kSelectBins / kSelectThreads;  // a thread's bins, from the top down
+        constexpr int PER = kSelectBins / THREADS;  // a thread's bins, from the top down
         uint32_t n[PER], sum = 0u;
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
@@ -287,7 +303,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
         __syncthreads();
         int before = ahead + static_cast<int>(upto - sum);
 #pragma unroll
-        for (int k = 0; k < kSelectWarps; ++k)
+        for (int k = 0; k < WARPS; ++k)
           if (k < warp) before += static_cast<int>(sm.warp_sum[k][0]);
         if (before < want && before + static_cast<int>(sum) >= want) {
 #pragma unroll
@@ -348,11 +364,11 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     const int groups = min(kSelectGroups, (len - c0 + 127) / 128);
     __syncthreads();
     auto mark = [&](int g0, const float(&x)[kSelectBatch][4], float(&next)[kSelectBatch][4]) {
-      const int t0 = c0 + g0 * 128 + lane * 4, ahead = g0 + kSelectBatch * kSelectWarps;
-      if (ahead < groups) load_groups(w, vec, c0 + ahead * 128 + lane * 4, kSelectWarps * 128, len, next);
+      const int t0 = c0 + g0 * 128 + lane * 4, ahead = g0 + kSelectBatch * WARPS;
+      if (ahead < groups) load_groups(w, vec, c0 + ahead * 128 + lane * 4, WARPS * 128, len, next);
 #pragma unroll
       for (int u = 0; u < kSelectBatch; ++u) {
-        const int g = g0 + u * kSelectWarps, t = t0 + u * kSelectWarps * 128;
+        const int g = g0 + u * WARPS, t = t0 + u * WARPS * 128;
         uint32_t gt[4], eq[4] = {0u, 0u, 0u, 0u};
         if (c0 + g * 128 >= a && c0 + g * 128 + 128 <= b && !numbers) {  // the whole group competes
 #pragma unroll
@@ -378,14 +394,14 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
       }
     };
     float x[kSelectBatch][4], y[kSelectBatch][4];
-    if (warp < groups) load_groups(w, vec, c0 + warp * 128 + lane * 4, kSelectWarps * 128, len, x);
-    for (int g0 = warp; g0 < groups; g0 += 2 * kSelectBatch * kSelectWarps) {
+    if (warp < groups) load_groups(w, vec, c0 + warp * 128 + lane * 4, WARPS * 128, len, x);
+    for (int g0 = warp; g0 < groups; g0 += 2 * kSelectBatch * WARPS) {
       mark(g0, x, y);
-      if (g0 + kSelectBatch * kSelectWarps < groups) mark(g0 + kSelectBatch * kSelectWarps, y, x);
+      if (g0 + kSelectBatch * WARPS < groups) mark(g0 + kSelectBatch * WARPS, y, x);
     }
     __syncthreads();
-    // kept tokens and ties before each group: kSelectGroups / kSelectThreads groups to a thread
-    constexpr int PER = kSelectGroups / kSelectThreads;
+    // kept tokens and ties before each group: PER groups to a thread
+    constexpr int PER = (kSelectGroups + THREADS - 1) / THREADS;
     uint32_t ng[PER], ne[PER], sg = 0u, se = 0u;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -412,7 +428,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
     __syncthreads();
     uint32_t all_g = 0u, all_e = 0u, pg = ig - sg, pe = ie - se;
 #pragma unroll
-    for (int k = 0; k < kSelectWarps; ++k) {
+    for (int k = 0; k < WARPS; ++k) {
       const uint32_t x = sm.warp_sum[k][0], y = sm.warp_sum[k][1];
       if (k < warp) pg += x, pe += y;
       all_g += x;
@@ -428,11 +444,40 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_
       pg += ng[k];
       pe += ne[k];
     }
-    kept_base += all_g + min(tie_base + all_e, ties) - min(tie_base, ties);
+    const uint32_t kept_now = all_g + min(tie_base + all_e, ties) - min(tie_base, ties);
+    kept_base += kept_now;
     tie_base += all_e;
     __syncthreads();
-    // a group to a thread, which goes over the lanes that marked something (a lane a step: four tokens)
-    for (int g = tid; g < groups; g += kSelectThreads) {
+    if (kept_now > static_cast<uint32_t>(groups) * 16) {
+      // many stay: a group to a warp, four tokens to a lane, whose stores lie together
+      const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
+      for (int g = warp; g < groups; g += WARPS) {
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.above[g]);
+        uint32_t keep_bits = ((x.x >> lane) & 1u) | ((x.y >> lane) & 1u) << 1 | ((x.z >> lane) & 1u) << 2 | ((x.w >> lane) & 1u) << 3;
+        uint32_t at = sm.before[g][0] + __popc(x.x & below) + __popc(x.y & below) + __popc(x.z & below) + __popc(x.w & below);
+        if (ties > 0u) {
+          const uint4 y = *reinterpret_cast<const uint4*>(sm.equal[g]);
+          const uint32_t tie0 = sm.before[g][1];
+          uint32_t tie = tie0 + __popc(y.x & below) + __popc(y.y & below) + __popc(y.z & below) + __popc(y.w & below);
+          at += min(tie, ties) - min(tie0, ties);  // ties of the lanes before that stayed
+          const uint32_t eq[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t same = (eq[e] >> lane) & 1u;
+            if (same && tie < ties) keep_bits |= 1u << e;
+            tie += same;
+          }
+        }
+        const int t = c0 + g * 128 + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((keep_bits >> e) & 1u) keep[at++] = t + e;
+      }
+      continue;
+    }
+    // few stay: a group to a thread, which goes over the lanes that marked something (four tokens a step)
+    for (int g = tid; g < groups; g += THREADS) {
       const uint4 x = *reinterpret_cast<const uint4*>(sm.above[g]);
       uint4 y = make_uint4(0u, 0u, 0u, 0u);
       int32_t* out = keep + sm.before[g][0];
@@ -631,11 +676,18 @@ pa_status pa_evict_select(int32_t n, const int32_t* seq_ids, const int32_t* leng
   p.budget = budget;
   p.keep_first = keep_first;
   p.keep_last = keep_last;
-  static std::atomic<unsigned long long> smem_done{0};
-  cudaError_t e = pa::allow_dynamic_smem(pa::select_kernel, smem_done, sizeof(pa::SelectSmem));
+  // Long rows take CTAs of 1024 threads, shorter ones where there is at most one to an SM.  Measured, us narrow / wide
+  // (8 kv heads, 2048 kept): 16 x 32768 22.8 / 27.0, 16 x 49152 28.2 / 24.9, 64 x 65536 74 / 108, 64 x 131072 275 / 156.
+  const bool wide = max_tokens > (units <= 152 ? 1 << 15 : 1 << 16);
+  static std::atomic<unsigned long long> done_wide{0}, done{0};
+  constexpr size_t wide_smem = sizeof(pa::SelectSmem<pa::kSelectWide>), smem = sizeof(pa::SelectSmem<pa::kSelectNarrow>);
+  cudaError_t e = wide ? pa::allow_dynamic_smem(pa::select_kernel<pa::kSelectWide>, done_wide, wide_smem)
+                       : pa::allow_dynamic_smem(pa::select_kernel<pa::kSelectNarrow>, done, smem);
   if (e != cudaSuccess) return cuda_fail(e, "select shared memory");
-  e = pa::launch_kernel(pa::select_kernel, dim3(static_cast<unsigned>(units)), dim3(pa::kSelectThreads),
-                        sizeof(pa::SelectSmem), static_cast<cudaStream_t>(stream), false, p);
+  const dim3 grid(static_cast<unsigned>(units));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  e = wide ? pa::launch_kernel(pa::select_kernel<pa::kSelectWide>, grid, dim3(pa::kSelectWide), wide_smem, s, false, p)
+           : pa::launch_kernel(pa::select_kernel<pa::kSelectNarrow>, grid, dim3(pa::kSelectNarrow), smem, s, false, p);
   pa::count_launch();
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "select launch");
 }

@@ -96,6 +96,29 @@ def test_select_between_kinds(n):
         check_select(mass, [0], [n], budget)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal", "signs", "special"])
+@pytest.mark.parametrize("budget,first,last", [(1, 0, 0), (64, 10, 54), (3000, 4, 32), (20000, 0, 256)])
+def test_select_wide_table(kind, budget, first, last):
+    """Long tables: rows of every length in them, in few units and in many."""
+    mass = weights((6, 2, 70003), kind, budget)
+    check_select(mass, [4, 0, 2, 5, 1, 3], [70003, 33000, 0, 20001, 1, 20300], budget, first, last)
+
+
+@pytest.mark.parametrize("kind", ["ascending", "stripes", "zeros"])
+@pytest.mark.parametrize("budget", [700, 60000])
+def test_select_wide_orders(kind, budget):
+    n = 131101
+    t = torch.arange(n, dtype=torch.float32)
+    w = {"ascending": t, "stripes": (t % 40 < 2) * (t + 1), "zeros": (t % 7 == 0) * (t + 1)}[kind]
+    check_select(torch.stack([w, w.flip(0)]).view(1, 2, n), [0], [n], budget, 3, 5)
+
+
+def test_select_many_long_rows():
+    mass = weights((160, 1, 33001), "spread", 3)
+    lengths = [33001 - 7 * i for i in range(160)]
+    check_select(mass, list(range(160)), lengths, 16000, 4, 64)
+
+
 def test_select_many_rows():
     mass = weights((300, 2, 130), "ties", 1)
     lengths = [(i * 37) % 131 for i in range(300)]
