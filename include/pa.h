@@ -210,9 +210,8 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
  *             16-byte aligned; the caller zeroes a sequence's rows when it admits it.
  *             Entries past a row's position are not touched.
  *   chunks    as for pa_attention: the rows of one prompt (its last rows as an
- *             observation window, or all of them) are listed as a chunk.  A
- *             chunk of at least 16 rows with bf16 queries over a bf16 pool runs on
- *             the tensor-core tile path.
+ *             observation window, or all of them) are listed as a chunk.  Chunks
+ *             with bf16 queries over a bf16 pool run on the tensor-core tile path.
  *   workspace device memory of at least pa_attention_mass_workspace_bytes(...) bytes,
  *             256-byte aligned (may be NULL when 0 are needed); scratch that each call
  *             writes before it reads it.  Calls that share one must not overlap on the GPU.

@@ -54,7 +54,6 @@ size_t plan_chunks(const pa_pool_desc& d, int32_t hq, int32_t max_blocks, const 
     p->chunk_end[c] = chunks[c].row_begin + chunks[c].n_rows;
     p->chunk_tiles[c] = (chunks[c].n_rows + R - 1) / R;
     const int64_t slots = static_cast<int64_t>(p->chunk_tiles[c]) * pa::kMassSlots * d.num_kv_heads;
-    p->chunk_index[c] = c;
     p->chunk_part[c] = pairs;
     pairs += slots * p->n_splits;
   }
@@ -65,36 +64,14 @@ size_t plan_chunks(const pa_pool_desc& d, int32_t hq, int32_t max_blocks, const 
   return 256 + static_cast<size_t>(pairs) * sizeof(float2);
 }
 
-// The chunks of `all` for which `take` holds.
-template <typename Take>
-pa::MassParams some_chunks(const pa::MassParams& all, Take take) {
-  pa::MassParams p = all;
-  p.n_chunks = 0;
-  for (int c = 0; c < all.n_chunks; ++c) {
-    if (!take(c)) continue;
-    const int k = p.n_chunks++;
-    p.chunk_begin[k] = all.chunk_begin[c];
-    p.chunk_end[k] = all.chunk_end[c];
-    p.chunk_tiles[k] = all.chunk_tiles[c];
-    p.chunk_index[k] = all.chunk_index[c];
-    p.chunk_part[k] = all.chunk_part[c];
-  }
-  return p;
-}
-
-// The chunks' columns: a look at the chunks, statistics over key ranges, then the
-// weights, on the tile path for bf16 chunks of kMinTileRows rows and more.
+// The chunks' columns: a look at the chunks, statistics over key ranges, then the weights.
 template <typename Launch>
-cudaError_t launch_chunks(const pa::MassParams& all, bool tile_types, Launch launch, cudaStream_t s) {
-  auto tiled = [&](int c) { return tile_types && all.chunk_end[c] - all.chunk_begin[c] >= pa::kMinTileRows; };
-  const pa::MassParams tiles = some_chunks(all, tiled), others = some_chunks(all, [&](int c) { return !tiled(c); });
-  pa::chunk_check_kernel<<<all.n_chunks, 256, 0, s>>>(all);
+cudaError_t launch_chunks(const pa::MassParams& p, Launch launch, cudaStream_t s) {
+  pa::chunk_check_kernel<<<p.n_chunks, 256, 0, s>>>(p);
   pa::count_launch();
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, false, s);
-  if (e == cudaSuccess && tiles.n_chunks > 0) e = pa::launch_mass_tiles(tiles, true, s);
-  if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_STATS, s);
-  if (e == cudaSuccess && others.n_chunks > 0) e = launch(others, pa::MASS_CHUNK_WEIGHTS, s);
+  if (e == cudaSuccess) e = launch(p, pa::MASS_CHUNK_STATS, s);
+  if (e == cudaSuccess) e = launch(p, pa::MASS_CHUNK_WEIGHTS, s);
   return e;
 }
 
@@ -160,10 +137,15 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
   int64_t in_chunks = 0;
   for (int c = 0; c < n_chunks; ++c) in_chunks += chunks[c].n_rows;
   // A row's cluster: by the block table's width, never by the batch, so that a
-  // row's sums are taken in the same order whatever else the call holds.
+  // row's sums are taken in the same order whatever else the call holds.  4096
+  // keys to a CTA (512 ragged rows of up to 2662 keys in one CTA each: 225 us, in
+  // CTAs of 2048 keys 255, of 1024 358), so 8 CTAs from 16385 keys on; 16 from 65537
+  // on (one row of 131072 keys: 59 us with 16, 160 with 8; at 16 rows of 65536,
+  // 364 with 16 and 335 with 8).
   const int64_t keys = static_cast<int64_t>(max_blocks_per_seq) * d.page_size;
   p.cluster = 1;
-  while (p.cluster < pa::kMassMaxCluster && keys > static_cast<int64_t>(p.cluster) * pa::kMassClusterKeys) p.cluster *= 2;
+  while (p.cluster < 8 && keys > static_cast<int64_t>(p.cluster) * pa::kMassClusterKeys) p.cluster *= 2;
+  if (keys > static_cast<int64_t>(pa::kMassMaxCluster) * pa::kMassClusterKeys) p.cluster = pa::kMassMaxCluster;
   const int G = num_q_heads / d.num_kv_heads;
   const int64_t room = (static_cast<int64_t>(pa::kMassScoreBytes) / (G * 4) - 36) / 32 * 32;  // keys whose scores fit
   // a CTA's share of the longest row, in the kernel's steps (at most four 16-key tiles)
@@ -173,10 +155,7 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
     return fail(PA_ERR_UNSUPPORTED, "%d rows of %d kv heads in one call", n_rows, d.num_kv_heads);
   p.wait_limit = pa::wait_limit();
   p.debug_stall = pa::debug_stall();
-  const bool tile_types = d.kv_dtype == PA_BF16 && q_dtype == PA_BF16;
-  bool tiles = false;
-  for (int c = 0; c < n_chunks; ++c) tiles = tiles || (tile_types && chunks[c].n_rows >= pa::kMinTileRows);
-  if (tiles) {
+  if (n_chunks > 0 && d.kv_dtype == PA_BF16 && q_dtype == PA_BF16) {  // the tile path
     st = pa::encode_tile_maps(const_cast<pa_pool*>(pool));
     if (st == PA_OK) st = pa::encode_query_map(&p.qmap, q, n_rows, num_q_heads, d.head_dim, G);
     if (st != PA_OK) return st;
@@ -186,7 +165,7 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (in_chunks < n_rows) e = launch(p, pa::MASS_ROWS, s);
-  if (e == cudaSuccess && n_chunks > 0) e = launch_chunks(p, tile_types, launch, s);
+  if (e == cudaSuccess && n_chunks > 0) e = launch_chunks(p, launch, s);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "attention mass launch");
 }
 

@@ -13,7 +13,7 @@
 // `chunk_check_kernel` looks the chunks over, `chunk_stats_kernel` finds every
 // column's (max, sum) over ranges of keys, `chunk_weights_kernel` merges the ranges, recomputes the scores key block by
 // key block and sums the weights over the columns: each key has one owner, which
-// adds once.  (bf16 chunks of 16 rows and more: the same steps on the tile path,
+// adds once.  (bf16 queries over a bf16 pool: the same steps on the tile path,
 // pa_mass_tiles.cuh.)
 // No atomic decides an order: the same rows give the same bits in any batch.
 #pragma once
@@ -30,7 +30,7 @@ constexpr int kMassSplitKeys = 1024;  // keys per range of the chunks' first lau
 constexpr int kMassBlockKeys = 128;   // keys per CTA of their last launch
 constexpr int kMassSlots = 128;       // columns of a chunk come in tiles of 128 / G rows, 128 slots each
 constexpr int kMassClusterKeys = 4096;             // keys per CTA that a row's cluster aims at
-constexpr int kMassMaxCluster = 8;
+constexpr int kMassMaxCluster = 16;
 constexpr size_t kMassScoreBytes = 104 * 1024;     // shared memory for a CTA's scores (two CTAs to an SM)
 
 struct MassParams {
@@ -53,7 +53,6 @@ struct MassParams {
   int32_t chunk_end[kMaxChunks];
   int32_t chunk_cta[kMaxChunks + 1];   // prefix sums of CTAs per chunk (set per launch)
   int32_t chunk_tiles[kMaxChunks];     // tiles of 128 / G rows
-  int32_t chunk_index[kMaxChunks];     // place in ws_head
   int32_t n_splits, n_blocks;          // of the longest row: key ranges, key blocks
   int64_t chunk_part[kMaxChunks];      // offset of a chunk in ws_part, in pairs
   int2* ws_head;                       // per chunk its sequence (-1: the chunk adds nothing) and first position
@@ -464,7 +463,7 @@ struct ChunkView {
 
   // false for a chunk that adds nothing
   __device__ __forceinline__ bool open(const MassParams& p, int c) {
-    const int2 head = __ldcg(p.ws_head + p.chunk_index[c]);
+    const int2 head = __ldcg(p.ws_head + c);
     row0 = p.chunk_begin[c];
     rows = p.chunk_end[c] - row0;
     seq = head.x;
@@ -629,6 +628,23 @@ __global__ void __launch_bounds__(kMassThreads) chunk_weights_kernel(const __gri
 
 // -------------------------------------------------------------- launches --
 
+// More than 8 CTAs to a cluster have to be allowed, once per device.
+template <typename Kernel>
+cudaError_t allow_wide_clusters(Kernel kernel, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+// The tensor-core tile launches (bf16 queries and pool): the columns'
+// statistics, or with `weights` the weights.
+cudaError_t launch_mass_tiles(const MassParams& p, bool weights, cudaStream_t stream);
+
 // What one call to a launcher runs, in this order.
 enum MassLaunch { MASS_ROWS, MASS_CHUNK_STATS, MASS_CHUNK_WEIGHTS };
 
@@ -641,6 +657,11 @@ cudaError_t launch_mass_inst(const MassParams& p0, MassLaunch what, cudaStream_t
     static std::atomic<unsigned long long> smem_done{0};
     const cudaError_t e = allow_dynamic_smem(mass_row_kernel<KVT, D, QB>, smem_done, kMassScoreBytes);
     if (e != cudaSuccess) return e;
+    if (p.cluster > 8) {
+      static std::atomic<unsigned long long> wide_done{0};
+      const cudaError_t w = allow_wide_clusters(mass_row_kernel<KVT, D, QB>, wide_done);
+      if (w != cudaSuccess) return w;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.n_rows) * p.Hkv * p.cluster);
     cfg.blockDim = dim3(kMassThreads);
@@ -654,23 +675,27 @@ cudaError_t launch_mass_inst(const MassParams& p0, MassLaunch what, cudaStream_t
     count_launch();
     return cudaLaunchKernelEx(&cfg, mass_row_kernel<KVT, D, QB>, p);
   }
-  constexpr int COLS = ChunkGeom<KVT, D, QB>::COLS;
-  long long ctas = 0;
-  for (int c = 0; c < p.n_chunks; ++c) {
-    p.chunk_cta[c] = static_cast<int32_t>(ctas);
-    const long long cols = static_cast<long long>(p.chunk_end[c] - p.chunk_begin[c]) * G;
-    ctas += (cols + COLS - 1) / COLS * p.Hkv * p.n_splits;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if constexpr (KVT == KV_BF16 && QB) {
+    return launch_mass_tiles(p, what == MASS_CHUNK_WEIGHTS, stream);
+  } else {
+    constexpr int COLS = ChunkGeom<KVT, D, QB>::COLS;
+    long long ctas = 0;
+    for (int c = 0; c < p.n_chunks; ++c) {
+      p.chunk_cta[c] = static_cast<int32_t>(ctas);
+      const long long cols = static_cast<long long>(p.chunk_end[c] - p.chunk_begin[c]) * G;
+      ctas += (cols + COLS - 1) / COLS * p.Hkv * p.n_splits;
+      if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    }
+    p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);
+    const long long blocks = static_cast<long long>(p.n_chunks) * p.Hkv * p.n_blocks;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (what == MASS_CHUNK_STATS)
+      chunk_stats_kernel<KVT, D, QB><<<static_cast<unsigned>(ctas), kMassThreads, 0, stream>>>(p);
+    else
+      chunk_weights_kernel<KVT, D, QB><<<static_cast<unsigned>(blocks), kMassThreads, 0, stream>>>(p);
+    count_launch();
+    return cudaGetLastError();
   }
-  p.chunk_cta[p.n_chunks] = static_cast<int32_t>(ctas);
-  const long long blocks = static_cast<long long>(p.n_chunks) * p.Hkv * p.n_blocks;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (what == MASS_CHUNK_STATS)
-    chunk_stats_kernel<KVT, D, QB><<<static_cast<unsigned>(ctas), kMassThreads, 0, stream>>>(p);
-  else
-    chunk_weights_kernel<KVT, D, QB><<<static_cast<unsigned>(blocks), kMassThreads, 0, stream>>>(p);
-  count_launch();
-  return cudaGetLastError();
 }
 
 template <int KVT>
@@ -683,9 +708,5 @@ cudaError_t launch_mass_dispatch(const MassParams& p, MassLaunch what, cudaStrea
 cudaError_t launch_mass_f32(const MassParams& p, MassLaunch what, cudaStream_t stream);
 cudaError_t launch_mass_bf16(const MassParams& p, MassLaunch what, cudaStream_t stream);
 cudaError_t launch_mass_e4m3(const MassParams& p, MassLaunch what, cudaStream_t stream);
-
-// The tensor-core tile launches (bf16 queries and pool): the columns'
-// statistics, or with `weights` the weights.
-cudaError_t launch_mass_tiles(const MassParams& p, bool weights, cudaStream_t stream);
 
 }  // namespace pa

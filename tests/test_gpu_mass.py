@@ -317,3 +317,37 @@ def test_many_short_units():
     first = check(c, q, seq, pos, chunks, seed=41)
     for _ in range(5):
         assert torch.equal(check(c, q, seq, pos, chunks, seed=41), first)
+
+
+@pytest.mark.parametrize("G", [1, 4])
+def test_long_chunk_bits_do_not_depend_on_the_batch(G):
+    """Several column tiles to a key, and more pieces of work than CTAs before the chunk's own."""
+    rows = 500
+    c = R.make_cache([2900, 2333, 700 + rows], Hkv=8, D=64, P=16, seed=13)
+    q = queries(3 * rows, 8 * G, 64, torch.bfloat16, seed=13)
+    seq = [s for s in c.slots for _ in range(rows)]
+    pos = [n - rows + i for n in c.lengths for i in range(rows)]
+    whole = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    assert run(c, q, seq, pos, whole, [(i * rows, rows) for i in range(3)]) == 0
+    for i, s in enumerate(c.slots):
+        one = torch.zeros_like(whole)
+        part = slice(i * rows, (i + 1) * rows)
+        assert run(c, q[part].contiguous(), seq[part], pos[part], one, [(0, rows)]) == 0
+        assert torch.equal(one[s], whole[s])
+
+
+@pytest.mark.parametrize("kv,q_dtype,D", [("f32", torch.float32, 128), ("e4m3", torch.bfloat16, 64), ("bf16", torch.float32, 128)])
+def test_wide_tables(kv, q_dtype, D):
+    """Tables of more than 2^16 tokens take the largest clusters, whatever the rows' own lengths."""
+    c = R.make_cache([66001, 1, 300], Hkv=1, D=D, P=256, kv=kv, seed=17)
+    check(c, queries(3, 8, D, q_dtype, seed=17), c.slots, [66000, 0, 299])
+
+
+@pytest.mark.parametrize("rows", [1, 2, 7])
+@pytest.mark.parametrize("G", [1, 5])
+def test_short_chunks(rows, G):
+    c = R.make_cache([rows, 1500 + rows, 4100], Hkv=2, D=128, P=16, seed=19)
+    q = queries(3 * rows, 2 * G, 128, torch.bfloat16, seed=19)
+    seq = [s for s in c.slots for _ in range(rows)]
+    pos = [n - rows + i for n in c.lengths for i in range(rows)]
+    check(c, q, seq, pos, [(i * rows, rows) for i in range(3)])
