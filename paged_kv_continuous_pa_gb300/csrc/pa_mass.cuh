@@ -11,9 +11,9 @@
 // sum) pairs, then become weights.
 // Chunks: the (row, head) pairs of a kv head are columns that share the keys.
 // `chunk_check_kernel` looks the chunks over, `chunk_stats_kernel` finds every
-// column's (max, sum) over ranges of keys, `chunk_weights_kernel` merges the ranges, recomputes the scores key block by
-// key block and sums the weights over the columns: each key has one owner, which
-// adds once.  (bf16 queries over a bf16 pool: the same steps on the tile path,
+// column's (max, sum) over ranges of keys, `chunk_weights_kernel` merges the
+// ranges, recomputes the scores key block by key block and sums the weights over
+// the columns: each key has one owner, which adds once.  (bf16 queries over a bf16 pool: the same steps on the tile path,
 // pa_mass_tiles.cuh.)
 // No atomic decides an order: the same rows give the same bits in any batch.
 #pragma once
@@ -27,7 +27,7 @@ namespace pa {
 constexpr int kMassThreads = 256;
 constexpr int kMassWarps = kMassThreads / 32;
 constexpr int kMassSplitKeys = 1024;  // keys per range of the chunks' first launch (and of the tile path's last)
-constexpr int kMassBlockKeys = 128;   // keys per CTA of their last launch
+constexpr int kMassBlockKeys = 512;   // keys per CTA of their last launch
 constexpr int kMassSlots = 128;       // columns of a chunk come in tiles of 128 / G rows, 128 slots each
 constexpr int kMassClusterKeys = 4096;             // keys per CTA that a row's cluster aims at
 constexpr int kMassMaxCluster = 16;
@@ -291,7 +291,15 @@ __host__ __device__ constexpr int score_stride(int keys) { return (keys + 31) / 
 // One cluster per (row, kv head).  The row's 16-key tiles are dealt to the CTAs
 // in contiguous shares of its own length, and within a CTA to the warps in
 // turn, MT at a time (4 KB of K, 8 KB with f32); the loads of a warp's next tiles
-// are in flight while it scores one's.
+// in flight while it scores one's.
+//
+// Bound by the one read of K: 512 ragged rows of up to 2662 keys (16 query heads
+// over 8, bf16) take 226 us, 6.5 TB/s; 32 rows of 32768 keys (32 heads over 8,
+// e4m3) 217 us, 5.0 TB/s, where four scores per 128-byte key row (two conversions
+// and an MMA each) share the SM with the loads.  A weight costs one exponential
+// per score twice (the running sum, the weight); the score itself is kept, not
+// recomputed.  4 KB of K to a warp's step, in one CTA: 225 us; 16-key tiles one by
+// one in CTAs of 2048 keys: 256.  Few short rows (4 of up to 900 keys) are latency: 6 us.
 template <int KVT, int D, bool QB>
 __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ? 1 : 2) mass_row_kernel(const __grid_constant__ MassParams p) {
   using Geo = MassGeom<KVT, D, QB>;
@@ -491,20 +499,59 @@ __device__ __forceinline__ float2 column_stat(const MassParams& p, int c, int h,
   return make_float2(st.m, __fdiv_rn(1.0f, st.l));
 }
 
-// Columns a warp scores at once (8 to a group), held to about 64 registers of query fragments.
+// A CTA's columns, in groups of 8: a warp prepares a group's query fragments for
+// all, in shared memory, and a key tile meets NT groups at a time (held to about
+// 64 registers of fragments).
 template <int KVT, int D, bool QB>
 struct ChunkGeom {
-  static constexpr int NT = MassGeom<KVT, D, QB>::QP == 1 ? 4 : MassGeom<KVT, D, QB>::QP == 2 ? 2 : 1;
-  static constexpr int COLS = 8 * NT;
+  using Geo = MassGeom<KVT, D, QB>;
+  static constexpr int NT = Geo::QP == 1 ? 4 : Geo::QP == 2 ? 2 : 1;
+  static constexpr int GROUPS = Geo::QP == 3 ? 4 : 8;
+  static constexpr int COLS = 8 * GROUPS;
+  static constexpr int VECS = Geo::QP * Geo::STEPS * 2 / 4;  // 16-byte vectors of a lane's fragments
+  static constexpr bool AHEAD = Geo::RB <= 256;              // room for the next key tile's fragments
+  static_assert(GROUPS <= kMassWarps && GROUPS % NT == 0, "a warp prepares a group");
 };
 
+template <int KVT, int D, bool QB>
+struct ChunkQueries {
+  using Cg = ChunkGeom<KVT, D, QB>;
+  uint4 frag[Cg::GROUPS][Cg::VECS][32];
+  float factor[Cg::COLS];
+
+  // Each of the first warps prepares its group of the columns from col0 on; the caller meets before and behind.
+  __device__ __forceinline__ void prepare(const MassParams& p, const ChunkView& v, int h, int col0, int cols, int G, int warp, int g4, int t4) {
+    if (warp >= Cg::GROUPS) return;
+    const int col = col0 + 8 * warp + g4;
+    QueryFrag<KVT, D, QB> q;
+    const float f = q.load(p, col < cols ? v.row0 + col / G : -1, h * G + col % G, p.qk_scale_log2_h[PA_HEAD(p, h)], t4);
+    if (t4 == 0) factor[8 * warp + g4] = f;
+    const uint32_t* b = &q.b[0][0][0];
+#pragma unroll
+    for (int i = 0; i < Cg::VECS; ++i) frag[warp][i][4 * g4 + t4] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+  }
+  __device__ __forceinline__ void get(int group, int lane, QueryFrag<KVT, D, QB>& q) const {
+    uint32_t* b = &q.b[0][0][0];
+#pragma unroll
+    for (int i = 0; i < Cg::VECS; ++i) {
+      const uint4 x = frag[group][i][lane];
+      b[4 * i] = x.x, b[4 * i + 1] = x.y, b[4 * i + 2] = x.z, b[4 * i + 3] = x.w;
+    }
+  }
+};
+
+// The warp-level launches serve f32 and e4m3 pools and f32 queries; bf16 queries
+// over bf16 pools have the tile path.  Bound by instruction issue (conversions, an
+// exponential and a comparison per score and launch): CHUNKFIG
+//
 // First launch: one CTA per (chunk, kv head, key range, column block).  The
 // CTA's warps take the range's 16-key tiles in turn.
 template <int KVT, int D, bool QB>
 __global__ void __launch_bounds__(kMassThreads) chunk_stats_kernel(const __grid_constant__ MassParams p) {
   using Geo = MassGeom<KVT, D, QB>;
-  constexpr int NT = ChunkGeom<KVT, D, QB>::NT, COLS = ChunkGeom<KVT, D, QB>::COLS;
-  __shared__ float2 warp_stat[kMassWarps][COLS];
+  using Cg = ChunkGeom<KVT, D, QB>;
+  __shared__ ChunkQueries<KVT, D, QB> sq;
+  __shared__ float2 warp_stat[kMassWarps][Cg::COLS];
   int c = 0;
   while (c + 1 < p.n_chunks && static_cast<int>(blockIdx.x) >= p.chunk_cta[c + 1]) ++c;
   const int local = blockIdx.x - p.chunk_cta[c];
@@ -512,44 +559,60 @@ __global__ void __launch_bounds__(kMassThreads) chunk_stats_kernel(const __grid_
   const int G = p.Hq / p.Hkv, lg_p = 31 - __clz(p.P);
   ChunkView v;
   if (!v.open(p, c)) return;
-  const int cols = v.rows * G, col0 = block * COLS, col_end = min(cols, col0 + COLS);
+  const int cols = v.rows * G, col0 = block * Cg::COLS, col_end = min(cols, col0 + Cg::COLS);
   const int key0 = split * kMassSplitKeys;
   const int top = v.pos0 + (col_end - 1) / G;  // the last key any of the columns sees
   const int key_end = min(top + 1, key0 + kMassSplitKeys);
   if (key0 >= key_end) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
-  QueryFrag<KVT, D, QB> q[NT];
-  float f[NT][2];
-  int lim[NT][2];  // last key of the lane's columns
-  ColumnStat st[NT][2];
+  sq.prepare(p, v, h, col0, cols, G, warp, g4, t4);
+  int lim[Cg::GROUPS][2];  // last key of the lane's columns
+  ColumnStat st[Cg::GROUPS][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int col = col0 + 8 * n + g4;
-    const float factor = q[n].load(p, col < cols ? v.row0 + col / G : -1, h * G + col % G, p.qk_scale_log2_h[PA_HEAD(p, h)], t4);
+  for (int n = 0; n < Cg::GROUPS; ++n)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      f[n][k] = __shfl_sync(0xffffffffu, factor, 8 * t4 + 4 * k);
       lim[n][k] = v.pos0 + (col0 + 8 * n + 2 * t4 + k) / G;
       st[n][k] = ColumnStat{-INFINITY, 0.0f};
     }
-  }
+  __syncthreads();
   bool bad = false;
-  for (int t0 = key0 + warp * 16; t0 < key_end; t0 += kMassWarps * 16) {
-    KeyFrag<KVT, D, QB> a;
-    a.load(key_rows<Geo::RB>(p, __ldg(v.table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
-    float s[NT][4];
-    a.score(q, s);
+  auto load = [&](int t0, KeyFrag<KVT, D, QB>& a) {
+    if (t0 < key_end) a.load(key_rows<Geo::RB>(p, __ldg(v.table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
+  };
+  auto step = [&](int t0, KeyFrag<KVT, D, QB>& now, KeyFrag<KVT, D, QB>& next) {
+    if (t0 >= key_end) return;
+    if (Cg::AHEAD) load(t0 + kMassWarps * 16, next);
+    else load(t0, now);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n0 = 0; n0 < Cg::GROUPS; n0 += Cg::NT) {
+      if (col0 + 8 * n0 >= cols) break;
+      QueryFrag<KVT, D, QB> q[Cg::NT];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float z[2] = {t0 + g4 <= lim[n][k] ? __fmul_rn(s[n][k], f[n][k]) : -INFINITY,
-                            t0 + g4 + 8 <= lim[n][k] ? __fmul_rn(s[n][2 + k], f[n][k]) : -INFINITY};
-        st[n][k].add(z);
+      for (int n = 0; n < Cg::NT; ++n) sq.get(n0 + n, lane, q[n]);
+      float s[Cg::NT][4];
+      now.score(q, s);
+#pragma unroll
+      for (int n = 0; n < Cg::NT; ++n) {
+        const float2 f = *reinterpret_cast<const float2*>(sq.factor + 8 * (n0 + n) + 2 * t4);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float fk = k == 0 ? f.x : f.y;
+          const float z[2] = {t0 + g4 <= lim[n0 + n][k] ? __fmul_rn(s[n][k], fk) : -INFINITY,
+                              t0 + g4 + 8 <= lim[n0 + n][k] ? __fmul_rn(s[n][2 + k], fk) : -INFINITY};
+          st[n0 + n][k].add(z);
+        }
       }
+    }
+  };
+  KeyFrag<KVT, D, QB> x, y;
+  if (Cg::AHEAD) load(key0 + warp * 16, x);
+  for (int t0 = key0 + warp * 16; t0 < key_end; t0 += 2 * kMassWarps * 16) {
+    step(t0, x, y);
+    step(t0 + kMassWarps * 16, y, x);
   }
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int n = 0; n < Cg::GROUPS; ++n)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -558,7 +621,7 @@ __global__ void __launch_bounds__(kMassThreads) chunk_stats_kernel(const __grid_
       if (g4 == 0) warp_stat[warp][8 * n + 2 * t4 + k] = make_float2(st[n][k].m, st[n][k].l);
     }
   __syncthreads();
-  if (tid < COLS && col0 + tid < cols) {
+  if (tid < Cg::COLS && col0 + tid < cols) {
     ColumnStat s{-INFINITY, 0.0f};
     for (int w = 0; w < kMassWarps; ++w) s.merge(warp_stat[w][tid].x, warp_stat[w][tid].y);
     p.ws_part[p.chunk_part[c] + (static_cast<size_t>(h) * p.n_splits + split) * p.chunk_tiles[c] * kMassSlots +
@@ -566,64 +629,88 @@ __global__ void __launch_bounds__(kMassThreads) chunk_stats_kernel(const __grid_
   }
 }
 
-// Last launch: one CTA per (chunk, kv head, block of 128 keys).  A warp keeps
-// its 16 keys' fragments and goes over the columns that see them.
+// Last launch: one CTA per (chunk, kv head, block of 512 keys).  A warp has four
+// 16-key tiles of them and goes over the columns that see the block, a CTA's
+// groups of columns at a time.
 template <int KVT, int D, bool QB>
 __global__ void __launch_bounds__(kMassThreads) chunk_weights_kernel(const __grid_constant__ MassParams p) {
   using Geo = MassGeom<KVT, D, QB>;
-  constexpr int NT = ChunkGeom<KVT, D, QB>::NT, COLS = ChunkGeom<KVT, D, QB>::COLS;
-  __shared__ float2 stat[COLS];
+  using Cg = ChunkGeom<KVT, D, QB>;
+  constexpr int TILES = kMassBlockKeys / (16 * kMassWarps);
+  __shared__ ChunkQueries<KVT, D, QB> sq;
+  __shared__ float2 stat[Cg::COLS];
   const int h = blockIdx.x % p.Hkv, block = (blockIdx.x / p.Hkv) % p.n_blocks, c = blockIdx.x / p.Hkv / p.n_blocks;
   const int G = p.Hq / p.Hkv, lg_p = 31 - __clz(p.P);
   ChunkView v;
   if (!v.open(p, c)) return;
-  const int key0 = block * kMassWarps * 16;
+  const int key0 = block * kMassBlockKeys;
   if (key0 > v.last) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
-  const int cols = v.rows * G, t0 = key0 + warp * 16;
+  const int cols = v.rows * G;
   bool bad = false;
-  KeyFrag<KVT, D, QB> a;
-  if (t0 <= v.last) a.load(key_rows<Geo::RB>(p, __ldg(v.table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
-  float w0 = 0.0f, w1 = 0.0f;
+  auto tile_at = [&](int i) { return key0 + (i * kMassWarps + warp) * 16; };
+  auto load = [&](int i, KeyFrag<KVT, D, QB>& a) {
+    const int t0 = tile_at(i);
+    if (t0 <= v.last) a.load(key_rows<Geo::RB>(p, __ldg(v.table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
+  };
+  float w0[TILES], w1[TILES];  // keys g4 and g4 + 8 of each tile
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) w0[i] = w1[i] = 0.0f;
   // columns before the first row that sees key0 see none of the block
-  for (int col0 = max(0, key0 - v.pos0) * G / COLS * COLS; col0 < cols; col0 += COLS) {
+  for (int col0 = max(0, key0 - v.pos0) * G / Cg::COLS * Cg::COLS; col0 < cols; col0 += Cg::COLS) {
     __syncthreads();
-    if (tid < COLS && col0 + tid < cols) {
-      const int slot = column_slot(col0 + tid, G);
-      stat[tid] = column_stat(p, c, h, slot / kMassSlots, slot % kMassSlots, v.pos0 + (col0 + tid) / G);
+    sq.prepare(p, v, h, col0, cols, G, warp, g4, t4);
+    const int mine = tid - (kMassThreads - Cg::COLS);  // the last warps look the statistics up
+    if (mine >= 0 && col0 + mine < cols) {
+      const int slot = column_slot(col0 + mine, G);
+      stat[mine] = column_stat(p, c, h, slot / kMassSlots, slot % kMassSlots, v.pos0 + (col0 + mine) / G);
     }
     __syncthreads();
-    if (t0 > v.last) continue;
-    QueryFrag<KVT, D, QB> q[NT];
-    float factor[NT], s[NT][4];
+    const int top = v.pos0 + (min(cols, col0 + Cg::COLS) - 1) / G;  // the last key that any of the columns sees
+    if (tile_at(0) > top) continue;
+    KeyFrag<KVT, D, QB> a[2];
+    if (Cg::AHEAD) load(0, a[0]);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = col0 + 8 * n + g4;
-      factor[n] = q[n].load(p, col < cols ? v.row0 + col / G : -1, h * G + col % G, p.qk_scale_log2_h[PA_HEAD(p, h)], t4);
-    }
-    a.score(q, s);
+    for (int i = 0; i < TILES; ++i) {
+      const int t0 = tile_at(i);
+      if (t0 > top) break;
+      if (!Cg::AHEAD) load(i, a[0]);
+      else if (i + 1 < TILES) load(i + 1, a[(i + 1) & 1]);
+#pragma unroll 1
+      for (int n0 = 0; n0 < Cg::GROUPS && col0 + 8 * n0 < cols; n0 += Cg::NT) {
+        QueryFrag<KVT, D, QB> q[Cg::NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < Cg::NT; ++n) sq.get(n0 + n, lane, q[n]);
+        float s[Cg::NT][4];
+        a[Cg::AHEAD ? i & 1 : 0].score(q, s);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float f = __shfl_sync(0xffffffffu, factor[n], 8 * t4 + 4 * k);
-        const int col = col0 + 8 * n + 2 * t4 + k;
-        if (col < cols) {
-          const int lim = v.pos0 + col / G;
-          const float2 z = stat[8 * n + 2 * t4 + k];
-          if (t0 + g4 <= lim) w0 = fmaf(ex2(__fsub_rn(__fmul_rn(s[n][k], f), z.x)), z.y, w0);
-          if (t0 + g4 + 8 <= lim) w1 = fmaf(ex2(__fsub_rn(__fmul_rn(s[n][2 + k], f), z.x)), z.y, w1);
-        }
+        for (int n = 0; n < Cg::NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int at = 8 * (n0 + n) + 2 * t4 + k, col = col0 + at;
+            if (col < cols) {
+              const int lim = v.pos0 + col / G;
+              const float f = sq.factor[at];
+              const float2 z = stat[at];
+              if (t0 + g4 <= lim) w0[i] = fmaf(ex2(__fsub_rn(__fmul_rn(s[n][k], f), z.x)), z.y, w0[i]);
+              if (t0 + g4 + 8 <= lim) w1[i] = fmaf(ex2(__fsub_rn(__fmul_rn(s[n][2 + k], f), z.x)), z.y, w1[i]);
+            }
+          }
       }
-  }
-#pragma unroll
-  for (int off = 1; off < 4; off <<= 1) {
-    w0 = __fadd_rn(w0, __shfl_xor_sync(0xffffffffu, w0, off));
-    w1 = __fadd_rn(w1, __shfl_xor_sync(0xffffffffu, w1, off));
+    }
   }
   float* sums = p.mass + (static_cast<size_t>(v.seq) * p.Hkv + h) * (static_cast<size_t>(p.max_blocks) << lg_p);
-  if (t4 == 0 && t0 + g4 <= v.last) atomicAdd(sums + t0 + g4, w0);
-  if (t4 == 0 && t0 + g4 + 8 <= v.last) atomicAdd(sums + t0 + g4 + 8, w1);
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) {
+    const int t0 = tile_at(i);
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      w0[i] = __fadd_rn(w0[i], __shfl_xor_sync(0xffffffffu, w0[i], off));
+      w1[i] = __fadd_rn(w1[i], __shfl_xor_sync(0xffffffffu, w1[i], off));
+    }
+    if (t4 == 0 && t0 + g4 <= v.last) atomicAdd(sums + t0 + g4, w0[i]);
+    if (t4 == 0 && t0 + g4 + 8 <= v.last) atomicAdd(sums + t0 + g4 + 8, w1[i]);
+  }
 }
 
 // -------------------------------------------------------------- launches --
