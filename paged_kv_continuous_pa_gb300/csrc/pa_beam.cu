@@ -361,34 +361,33 @@ __device__ __forceinline__ double score_of(uint64_t key) {
 // One CTA per group.  A warp takes a row: the log-sum-exp over its segments,
 // and its n_out best out of their lists (a bound, then ranks by counting what
 // reaches it).  Then the beams' candidates by score in 64 bits: each beam's
-// descend, so a candidate's rank is a sum of binary searches.  Latency: 8 us alone,
-// most of it hidden behind the segments' launch (its programmatic dependent).
+// descend, so a candidate's rank is a sum of binary searches.  Latency: about 8
+// us alone, part of it hidden behind the segments' launch (its programmatic
+// dependent); a logarithm per warp instead of one per lane cost 15 us at 47 groups of 14.
 __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_constant__ BeamParams p) {
   extern __shared__ uint64_t list[];  // a warp each: [segments][n_out] keys, [2 n_out] candidates; then the scores
   __shared__ int found;
+  __shared__ int row_kind[kMaxBeams];  // 0: no continuation, 1: by its logits, 2: finished
+  __shared__ float row_max[kMaxBeams];
+  __shared__ double row_log[kMaxBeams];  // the sum of exponentials, then its logarithm
   const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = p.n_out, per_row = p.segments * K, total = p.beams * K;
   uint64_t* keys = list + static_cast<size_t>(warp) * (per_row + 2 * K);
   uint64_t* cand = keys + per_row;
-  uint64_t* score = list + static_cast<size_t>(p.merge_warps) * (per_row + 2 * K);  // [beams][n_out] score keys, 0: none
+  uint64_t* score = list + static_cast<size_t>(p.merge_warps) * (per_row + 2 * K);  // [beams][n_out] logit keys, then score keys, 0: none
   int* token = reinterpret_cast<int*>(score + total);
   if (tid == 0) found = 0;
   bool waited = false;
   for (int b = warp; b < p.beams && warp < p.merge_warps; b += p.merge_warps) {
     const size_t row = static_cast<size_t>(g) * p.beams + b;
-    const double cum = __ldg(p.scores + row);
+    const float cum = __ldg(p.scores + row);
     const bool ended = p.finished != nullptr && __ldg(p.finished + row) != 0;
     for (int k = lane; k < K; k += 32) score[b * K + k] = 0ull;
+    if (lane == 0) row_kind[b] = ended && isfinite(cum) ? 2 : 0;
     __syncwarp();
     if (!waited) griddep_wait();  // the segments' results
     waited = true;
-    if (ended) {
-      if (lane == 0) {
-        if (isfinite(cum)) score[b * K] = score_key(cum);
-        token[b * K] = p.end_token;
-      }
-      continue;
-    }
+    if (ended) continue;
     const uint64_t* from = p.segment_keys + row * per_row;
     const float* cs = p.segment_sum + row * p.segments;
     const float* cm = p.segment_max + row * p.segments;
@@ -410,8 +409,12 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_c
     double s = part != 0.0f ? static_cast<double>(part) * static_cast<double>(expf(__fsub_rn(ref, m))) : 0.0;
     for (int off = 1; off < p.segments; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     s = __shfl_sync(0xffffffffu, s, 0);
-    const double log_s = log(s);
-    if (!isfinite(m) || !isfinite(log_s) || !isfinite(cum) || most == 0ull) continue;
+    if (!isfinite(m) || !(s > 0.0) || !isfinite(s) || !isfinite(cum) || most == 0ull) continue;
+    if (lane == 0) {
+      row_kind[b] = 1;
+      row_max[b] = m;
+      row_log[b] = s;
+    }
     const uint64_t bound = bound_keys(keys, per_row, K, least > 0ull ? least : 1ull, most + 1ull, lane);
     int n = 0;
     for (int c0 = 0; c0 < per_row; c0 += 32) {
@@ -426,13 +429,26 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_c
       int rank = 0;
 #pragma unroll 4
       for (int o = 0; o < n; ++o) rank += cand[o] > key;
-      if (rank < K) {
-        // the logit below the maximum first: exact where both are large
-        score[b * K + rank] = score_key(cum + ((static_cast<double>(cand_logit(key)) - static_cast<double>(m)) - log_s));
-        token[b * K + rank] = cand_token(key);
-      }
+      if (rank < K) score[b * K + rank] = key;
     }
     __syncwarp();
+  }
+  __syncthreads();
+  // FP64 goes through the SM a lane or two at a time: one warp takes the logarithms of all rows
+  if (tid < p.beams && row_kind[tid] == 1) row_log[tid] = log(row_log[tid]);
+  __syncthreads();
+  for (int c = tid; c < total; c += kBeamThreads) {
+    const int b = c / K;
+    const uint64_t key = score[c];
+    const double cum = __ldg(p.scores + static_cast<size_t>(g) * p.beams + b);
+    if (key != 0ull) {
+      // the logit below the maximum first: exact where both are large
+      score[c] = score_key(cum + ((static_cast<double>(cand_logit(key)) - static_cast<double>(row_max[b])) - row_log[b]));
+      token[c] = cand_token(key);
+    } else if (row_kind[b] == 2 && c == b * K) {
+      score[c] = score_key(cum);
+      token[c] = p.end_token;
+    }
   }
   __syncthreads();
   int valid = 0, top_step = 1;

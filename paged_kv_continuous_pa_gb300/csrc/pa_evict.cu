@@ -520,7 +520,7 @@ struct CompactParams {
 
 constexpr int kCompactThreads = 256;
 constexpr int kCompactUnroll = 4;
-constexpr int kCompactCtas = 608;
+constexpr int kCompactCtas = 304;
 constexpr int kCompactBlock = 1024;  // kept tokens looked up at once
 
 // keep[j] if it is a token of the sequence above the one before it (the order
@@ -554,8 +554,9 @@ __device__ __forceinline__ uint4 load_piece(const unsigned char* a) {
 // Bound by the read and the write of the kept rows: 1024 of up to 8192 tokens of 64
 // sequences x 8 heads (bf16, D 128: 556 MB) take 98 us, 5.7 TB/s of scattered
 // 256-byte rows.  Four CTAs to an SM with four pieces to a thread; more pieces or
-// fewer CTAs took 98 to 125.  One CTA per (sequence, head, K | V) without stripes:
-// 8 sequences of 256 kept tokens 19 us, with them 8.
+// fewer CTAs took 98 to 125.  Stripes, until there are two CTAs to an SM: one
+// sequence of 8192 kept tokens 39 us, without them 92; 16 of 2048 47 us, without
+// 55, until there are four CTAs 54.
 __global__ void __launch_bounds__(kCompactThreads, 4) compact_kernel(const __grid_constant__ CompactParams p) {
   __shared__ long long from[kCompactBlock], to[kCompactBlock];  // byte offsets of a kept token's row (from -1: not moved)
   const int per_head = 2 * p.stripes;
@@ -712,8 +713,7 @@ pa_status pa_evict_compact(const pa_pool* pool, int32_t n, const int32_t* seq_id
   if (!seq_ids || !lengths || !keep || !block_tables) return fail(PA_ERR_INVALID_ARG, "compact: a device pointer is NULL");
   const int row_bytes = d.head_dim * static_cast<int>(pa::elt_bytes(d.kv_dtype));
   const int64_t heads = static_cast<int64_t>(n) * d.num_kv_heads;
-  // stripes of 64 bytes and more until there are about four CTAs to an SM (narrower ones would halve the
-  // 64 bytes that a memory access moves)
+  // stripes of 64 bytes and more (what a memory access moves) until there are about two CTAs to an SM
   int stripes = 1;
   while (heads * 2 * stripes < pa::kCompactCtas && row_bytes / stripes > 64) stripes *= 2;
   const int64_t units = heads * (2 * stripes + (mass != nullptr ? 1 : 0));
