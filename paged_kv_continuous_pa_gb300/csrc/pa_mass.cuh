@@ -542,10 +542,10 @@ struct ChunkQueries {
 
 // The warp-level launches serve f32 and e4m3 pools and f32 queries; bf16 queries
 // over bf16 pools have the tile path.  Bound by instruction issue (conversions, an
-// exponential and a comparison per score and launch): eight
-// windows of 64 rows over 4k-16k keys (32 heads over 8) take 595 us with an e4m3
-// pool, 1466 with f32 queries over a bf16 one, 2981 with f32 both.  Fragments
-// prepared by every warp for itself took 1076, 2675 and 4556.
+// exponential and a comparison per score and launch): eight windows of 64 rows
+// over 4k-16k keys (32 heads over 8) take 595 us with an e4m3 pool, 1466 with f32
+// queries over a bf16 one, 2981 with f32 both.  Fragments prepared by every warp
+// for itself took 1076, 2675 and 4556.
 //
 // First launch: one CTA per (chunk, kv head, key range, column block).  The
 // CTA's warps take the range's 16-key tiles in turn.
