@@ -351,3 +351,28 @@ def test_short_chunks(rows, G):
     seq = [s for s in c.slots for _ in range(rows)]
     pos = [n - rows + i for n in c.lengths for i in range(rows)]
     check(c, q, seq, pos, [(i * rows, rows) for i in range(3)])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_two_calls_at_once(kv):
+    """Two streams, two workspaces, two sums: the bits of the calls one after the other."""
+    rows = 64
+    c = R.make_cache([3000, 2500, 1800], Hkv=4, D=128, P=32, kv=kv, seed=23)
+    seq = torch.tensor([s for s in c.slots for _ in range(rows)], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([n - rows + i for n in c.lengths for i in range(rows)], dtype=torch.int32, device="cuda")
+    chunks = [(i * rows, rows) for i in range(3)]
+    q = [queries(3 * rows, 16, 128, torch.bfloat16, seed=s) for s in (23, 24)]
+    size = pa.mass_workspace_bytes(c.pool, 3 * rows, 16, c.max_blocks, chunks)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    mass = torch.zeros(2, 2, c.num_seqs, c.Hkv, c.max_tokens, device="cuda")  # [one by one | at once][query]
+    for i in range(2):
+        pa.attention_mass(c.pool, q[i], seq, pos, c.tables, mass[0, i], chunks=chunks, workspace=ws[i])
+        torch.cuda.synchronize()
+    for _ in range(4):
+        mass[1].zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            pa.attention_mass(c.pool, q[i], seq, pos, c.tables, mass[1, i], chunks=chunks, workspace=ws[i], stream=streams[i])
+        torch.cuda.synchronize()
+        assert torch.equal(mass[0], mass[1])
