@@ -223,7 +223,8 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
  * for pa_attention; a row with an
  * invalid sequence, position or page, or a chunk with such a row or whose rows
  * are not consecutive positions of one sequence, adds nothing and records
- * PA_ERR_OUT_OF_RANGE.  Graph-capturable. */
+ * PA_ERR_OUT_OF_RANGE.  After PA_ERR_TIMEOUT (pa_set_wait_limit) the sums of the
+ * call's chunks are unspecified.  Graph-capturable. */
 size_t pa_attention_mass_workspace_bytes(const pa_pool *pool, int32_t n_rows, int32_t num_q_heads,
                                          int32_t max_blocks_per_seq, const pa_chunk *chunks, int32_t n_chunks);
 pa_status pa_attention_mass(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q_dtype,

@@ -31,7 +31,7 @@
 // the pipe's rate).  One MMA warp for both column tiles took 139 us instead of
 // 121; a CTA per unit 147; S buffers of 64 columns, two to a group, 212; key
 // ranges of 512 / 2048 keys instead of 1024: 133 / 127.
-// Every wait is bounded; a call that gives up adds nothing and reports it.
+// Every wait is bounded; a call that gives up reports it, and adds nothing more.
 #pragma once
 
 #include <algorithm>
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
         }
       }
       meet();
-      if (*failed) continue;  // adds nothing
+      if (*failed) continue;  // adds nothing more
       if constexpr (!W) {
         // the groups' shares of the keys, merged in order
         const int half = group, row = (x.t_first + half) * R + m / G;
