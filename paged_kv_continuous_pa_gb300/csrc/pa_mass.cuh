@@ -27,6 +27,8 @@ namespace pa {
 constexpr int kMassThreads = 256;
 constexpr int kMassWarps = kMassThreads / 32;
 constexpr int kMassSplitKeys = 1024;  // keys per range of the chunks' first launch (and of the tile path's last)
+constexpr int kMassLongKeys = 256;    // ... of that one for chunks of more than kMassLongTiles column tiles
+constexpr int kMassLongTiles = 8;
 constexpr int kMassBlockKeys = 512;   // keys per CTA of their last launch
 constexpr int kMassSlots = 128;       // columns of a chunk come in tiles of 128 / G rows, 128 slots each
 constexpr int kMassClusterKeys = 4096;             // keys per CTA that a row's cluster aims at

@@ -7,7 +7,8 @@ cudaError_t launch_mass_tiles(const MassParams& p, bool weights, cudaStream_t st
   // no more CTAs than there can be units (the kernel counts them from the positions)
   long long units = 0;
   for (int c = 0; c < p.n_chunks; ++c)
-    units += static_cast<long long>(p.Hkv) * (static_cast<long long>(p.n_splits) * (weights ? 1 : (p.chunk_tiles[c] + 1) / 2));
+    units += static_cast<long long>(p.Hkv) * p.n_splits *
+             (!weights ? (p.chunk_tiles[c] + 1) / 2 : p.chunk_tiles[c] > kMassLongTiles ? kMassSplitKeys / kMassLongKeys : 1);
   if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (p.D == 64) return weights ? launch_mass_tile_inst<64, true>(p, units, stream) : launch_mass_tile_inst<64, false>(p, units, stream);
   return weights ? launch_mass_tile_inst<128, true>(p, units, stream) : launch_mass_tile_inst<128, false>(p, units, stream);

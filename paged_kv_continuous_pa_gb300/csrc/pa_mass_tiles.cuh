@@ -10,7 +10,8 @@
 //     and sum.  S = Q K^T with the tiles' queries resident in shared memory and key
 //     tiles of 128 streamed; a thread owns a column (one lane of S) and goes over
 //     the keys.
-//   mass_tile_kernel<D, true>: per range of as many keys the weights.
+//   mass_tile_kernel<D, true>: per range of as many keys, or of 256 for a chunk of more
+//     than eight column tiles, the weights.
 //     S^T = K Q^T, queries and key tiles alike, the columns' log2-sum-exps beside the
 //     queries; a thread owns a key (one lane of S^T) and sums the weights of the
 //     columns.  Each group of warps has accumulators of its own; they are
@@ -143,7 +144,10 @@ template <int D, bool W>
 __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_constant__ MassParams p) {
   using S = MassTileSmem<D, W>;
   constexpr uint32_t kTmemCols = 512;  // the S buffers (384; a power of two)
-  constexpr int kRange = kMassSplitKeys;
+  // Keys of a unit: 1024, or, of the weights of a chunk with many column tiles to go through, 256.  By the chunk
+  // alone, so that its sums do not depend on the batch.  us with 1024 / 256: 13 chunks of 396 rows x 6 heads (19
+  // tiles) 190 / 98, one of 512 x 32 over 8 (16 tiles) 113 / 77, eight of 256 x 32 over 8 (8 tiles) 413 / 528.
+  auto range_of = [&](int c) { return W && p.chunk_tiles[c] > kMassLongTiles ? kMassLongKeys : kMassSplitKeys; };
   static_assert(kMtBuffers * kMtKeys <= kTmemCols, "tensor memory");
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
       const int2 hd = __ldcg(p.ws_head + c);
       const int rows = p.chunk_end[c] - p.chunk_begin[c];
       int units = 0;  // a chunk that adds nothing has none
-      if (hd.x >= 0) units = p.Hkv * ((hd.y + rows - 1) / kRange + 1) * (W ? 1 : (p.chunk_tiles[c] + 1) / 2);
+      if (hd.x >= 0) units = p.Hkv * ((hd.y + rows - 1) / range_of(c) + 1) * (W ? 1 : (p.chunk_tiles[c] + 1) / 2);
       heads[c] = make_int4(hd.x, hd.y, before, units);
       before += units;
     }
@@ -205,13 +209,13 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
     x.seq = hd.x;
     x.pos0 = hd.y;
     x.table = p.block_tables + static_cast<size_t>(x.seq) * p.max_blocks;
-    const int ranges = (x.pos0 + x.rows - 1) / kRange + 1, part = local / p.Hkv;
+    const int range = range_of(c), ranges = (x.pos0 + x.rows - 1) / range + 1, part = local / p.Hkv;
     x.split = part % ranges;
-    x.key0 = x.split * kRange;
+    x.key0 = x.split * range;
     const int pair = part / ranges;
     const int row_end = W ? x.rows : min(x.rows, (2 * pair + 2) * R);
     x.last = x.pos0 + row_end - 1;
-    x.nk = x.key0 > x.last ? 0 : min(kRange / kMtKeys, (x.last - x.key0) / kMtKeys + 1);
+    x.nk = x.key0 > x.last ? 0 : min(range / kMtKeys, (x.last - x.key0) / kMtKeys + 1);
     x.t_first = W ? max(0, x.key0 - x.pos0) / R : 2 * pair;
     x.t_end = (row_end + R - 1) / R;
     return x;
