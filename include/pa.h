@@ -272,8 +272,10 @@ pa_status pa_evict_select(int32_t n, const int32_t *seq_ids, const int32_t *leng
  * under it).  max_blocks_per_seq * page_size <= 2^30.  One launch, no workspace;
  * graph-capturable.
  * Device-side, with PA_ERR_OUT_OF_RANGE: a row with an invalid slot or length
- * moves nothing; a kept token out of order or range, or one whose page id is
- * invalid, is not moved and its destination is unspecified. */
+ * moves nothing; a kept token out of range or out of order (not above the one
+ * before it, or below its own place j, which no ascending list has) is not moved
+ * and leaves a weight of zero, one whose page id is invalid is not moved; the
+ * others move as listed. */
 pa_status pa_evict_compact(const pa_pool *pool, int32_t n, const int32_t *seq_ids, const int32_t *dst_seq_ids,
                            const int32_t *lengths, const int32_t *keep, int32_t budget, const int32_t *block_tables,
                            int32_t num_seqs, int32_t max_blocks_per_seq, float *mass, int32_t *status_dev,

@@ -523,11 +523,13 @@ constexpr int kCompactUnroll = 4;
 constexpr int kCompactCtas = 304;
 constexpr int kCompactBlock = 1024;  // kept tokens looked up at once
 
-// keep[j] if it is a token of the sequence above the one before it (the order
-// that moving in place relies on), else -1 after recording an error.
+// keep[j] if it is a token of the sequence above the one before it and not below
+// its own place, else -1 after recording an error.  Moving in place relies on both:
+// an ascending list has keep[j] >= j throughout, but behind a step back a neighbour's
+// comparison holds again while the tokens' slots may have been overwritten.
 __device__ __forceinline__ int kept_token(const CompactParams& p, const int32_t* keep, int j, int len) {
   const int t = __ldg(keep + j), before = j > 0 ? __ldg(keep + j - 1) : -1;
-  if (t >= 0 && t < len && t > before) return t;
+  if (t >= j && t < len && t > before) return t;
   record_error(p.status, ST_OUT_OF_RANGE);
   return -1;
 }
@@ -545,8 +547,8 @@ __device__ __forceinline__ uint4 load_piece(const unsigned char* a) {
 
 // One CTA per (sequence, kv head, K | V, stripe), and one per (sequence, kv head)
 // for the weights.  The kept tokens move in order, a tile at a time: every thread
-// loads its pieces of the tile, the CTA meets, and the tile is stored.  Kept
-// tokens ascend, so the j-th comes from a token t >= j: a tile's stores reach only
+// loads its pieces of the tile, the CTA meets, and the tile is stored.  The
+// j-th comes from a token t >= j (`kept_token`): a tile's stores reach only
 // slots that earlier tiles and this one read, never a later tile's, and the move
 // is safe in place -- also with the next tile's loads on their way before the
 // stores.  Stripes of a row are independent of one another; they fill the GPU

@@ -339,3 +339,35 @@ def test_graph():
                 want = R.select_ref(w[s, h].cpu(), n, 50, 0, 0)
                 assert keep[i, h, :len(want)].tolist() == want
                 assert torch.equal(R.bits(R.cached(c, c.k, s, len(want))[h]), R.bits(old[i][h, want]))
+
+
+@pytest.mark.parametrize("start", [0, 1999, 2001, 2500])
+@pytest.mark.parametrize("copy", [False, True])
+def test_compact_lists_out_of_order(start, copy):
+    """A list that begins anew far down: what is not in order, or lies below its own place, is not moved;
+    every other entry gets its own token's bytes and weight."""
+    n, budget, turn = 6000, 3001, 2000
+    c = R.make_cache([n, n] if copy else [n], Hkv=2, D=64, P=32, seed=6, slots=[0, 1] if copy else [0])
+    j = torch.arange(budget)
+    keep = torch.where(j < turn, 2999 + j, start + j - turn).to(torch.int32)
+    before = torch.cat([torch.tensor([-1], dtype=torch.int32), keep[:-1]])
+    moved = ((keep > before) & (keep >= j)).cuda()
+    assert bool(moved[:turn].all()) and not bool(moved[turn])
+    dst = 1 if copy else 0
+    mass = torch.rand(c.num_seqs, 2, c.max_tokens, generator=torch.Generator().manual_seed(7)).cuda()
+    old = [[R.cached(c, pool, s, n).clone() for s in (0, dst)] for pool in (c.k, c.v)]
+    old_mass = mass.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.evict_compact(c.pool, keep.view(1, 1, -1).repeat(1, 2, 1).cuda(), ints([0]), ints([n]), c.tables, mass=mass,
+                     dst_seq_ids=ints([dst]) if copy else None, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == pa.PA_ERR_OUT_OF_RANGE
+    at = keep.long().cuda()
+    for pool, (source, there) in zip((c.k, c.v), old):
+        now = R.cached(c, pool, dst, n)
+        want = there.clone()
+        want[:, :budget] = torch.where(moved.view(1, -1, 1), source[:, at], there[:, :budget])
+        assert torch.equal(R.bits(now), R.bits(want))
+    want = torch.zeros_like(old_mass[0, :, :n])
+    want[:, :budget] = torch.where(moved, old_mass[0][:, at], torch.zeros_like(old_mass[0][:, at]))
+    assert torch.equal(mass[dst, :, :n], want)
