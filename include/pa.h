@@ -219,8 +219,9 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
  * Precondition: a sequence has one row outside the chunks, or the rows of one
  * chunk, in a call (a step's rows satisfy it): its sums then have one writer
  * and the same bits in any batch.
- * Sums and weights are FP32.  max_blocks_per_seq * page_size <= 2^30.  Errors as
- * for pa_attention; a row with an
+ * Scores, sums and weights are FP32.  A score of -infinity (an infinite key) is a weight of zero; one of
+ * +infinity or NaN makes its row's weights NaN for that kv head.
+ * max_blocks_per_seq * page_size <= 2^30.  Errors as for pa_attention; a row with an
  * invalid sequence, position or page, or a chunk with such a row or whose rows
  * are not consecutive positions of one sequence, adds nothing and records
  * PA_ERR_OUT_OF_RANGE.  After PA_ERR_TIMEOUT (pa_set_wait_limit) the sums of the

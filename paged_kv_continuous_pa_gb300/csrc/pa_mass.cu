@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(256) chunk_check_kernel(const __grid_constant_
   if (tid == 0) {
     if (bad) record_error(p.status, ST_OUT_OF_RANGE);
     p.ws_head[c] = make_int2(bad ? -1 : seq, pos0);
+    p.ws_whole[c] = 0;
   }
 }
 
@@ -59,7 +60,9 @@ size_t plan_chunks(const pa_pool_desc& d, int32_t hq, int32_t max_blocks, const 
   }
   p->n_chunks = n_chunks;
   if (n_chunks == 0) return 0;
+  static_assert(pa::kMaxChunks * (sizeof(int2) + sizeof(int32_t)) <= 256, "the chunks' heads");
   p->ws_head = static_cast<int2*>(workspace);
+  p->ws_whole = reinterpret_cast<int32_t*>(p->ws_head + pa::kMaxChunks);
   p->ws_part = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + 256);
   return 256 + static_cast<size_t>(pairs) * sizeof(float2);
 }

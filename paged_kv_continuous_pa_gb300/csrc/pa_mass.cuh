@@ -58,6 +58,7 @@ struct MassParams {
   int32_t n_splits, n_blocks;          // of the longest row: key ranges, key blocks
   int64_t chunk_part[kMaxChunks];      // offset of a chunk in ws_part, in pairs
   int2* ws_head;                       // per chunk its sequence (-1: the chunk adds nothing) and first position
+  int32_t* ws_whole;                   // per chunk: whether whole operands gave a column its sum (`in_parts`)
   float2* ws_part;                     // (max, sum) per chunk [Hkv][n_splits][tiles][128]
   CUtensorMap kmap;                    // tile path: the pool as [num_pages * Hkv * P][D], boxes of 64 x min(P, 64)
   CUtensorMap qmap;                    // tile path: q as [n_rows][Hq][D], boxes of 128 / G rows x G heads x 64
@@ -266,6 +267,46 @@ struct ColumnStat {
   }
 };
 
+// ----------------------------------------------- operands outside their parts --
+//
+// Parts of a value cannot stand for an infinity (what is left of it is inf - inf, and a
+// zero part times infinity is NaN too), nor for an f32 above the largest bf16, which
+// rounds to one.  A dot product with such an operand comes out right or NaN, and its
+// column's sum then NaN: a lane that finds its share of one so takes the scores again
+// from the operands themselves, in FP32, until the sum is NaN once more.  Other
+// columns keep their bits, and where no sum is NaN nothing is added to the loops (a
+// test of every score took 1923 us instead of 1335 for the windows of f32 queries below).
+// Keys and queries of one bf16 part need none of this, nor e4m3 keys (no
+// infinities; a query that is not finite has no weights at all).
+template <int KVT, bool QB>
+__host__ __device__ constexpr bool in_parts() { return KVT == KV_F32 || (KVT == KV_BF16 && !QB); }
+
+template <int KVT, int D, bool QB>
+__device__ float whole_dot(const MassParams& p, const int32_t* table, int h, int t, int row, int head) {
+  const int lg_p = 31 - __clz(p.P), page = __ldg(table + (t >> lg_p));
+  if (page < 0 || page >= p.num_pages) return 0.0f;  // a row that adds nothing
+  const size_t k0 = (((static_cast<size_t>(page) * p.Hkv + h) << lg_p) + (t & (p.P - 1))) * D;
+  const size_t q0 = (static_cast<size_t>(row) * p.Hq + head) * D;
+  float s = 0.0f;
+#pragma unroll 4
+  for (int d = 0; d < D; ++d) {
+    const float k = KVT == KV_F32 ? __ldg(static_cast<const float*>(p.k_pool) + k0 + d)
+                                  : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.k_pool) + k0 + d)) << 16);
+    const float q = QB ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.q) + q0 + d)) << 16)
+                       : __ldg(static_cast<const float*>(p.q) + q0 + d);
+    s = fmaf(q, k, s);
+  }
+  return s;
+}
+
+// One column's log2-domain scores of keys t and t + 8 (-infinity where its row, at position pos, does not see them).
+template <int KVT, int D, bool QB>
+__device__ __noinline__ float2 whole_scores(const MassParams& p, const int32_t* table, int h, int t, int pos, int row, int head) {
+  const float f = p.qk_scale_log2_h[PA_HEAD(p, h)];
+  return make_float2(t <= pos ? __fmul_rn(whole_dot<KVT, D, QB>(p, table, h, t, row, head), f) : -INFINITY,
+                     t + 8 <= pos ? __fmul_rn(whole_dot<KVT, D, QB>(p, table, h, t + 8, row, head), f) : -INFINITY);
+}
+
 // The tensor-map-free address of token t's K row of kv head h (t % 16 == 0), or
 // of page 0 where the page id is out of range (`bad` is set then).
 template <int RB>
@@ -308,7 +349,7 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
   extern __shared__ float scores[];  // [G][score_stride(score_keys)]
   __shared__ float2 warp_stat[kMassWarps][8];
   __shared__ float2 cta_stat[8];
-  __shared__ int cta_bad;
+  __shared__ int cta_bad, cta_whole;
   __shared__ float2 row_stat[8];  // (maximum, 1 / sum) of the whole row
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -327,7 +368,7 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
   const int tile0 = min(tiles, rank * share), mine = min(tiles, tile0 + share) - tile0;  // this CTA's tiles
   const int stride = score_stride(p.score_keys);
   const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
-  if (tid == 0) cta_bad = 0;
+  if (tid == 0) cta_bad = cta_whole = 0;
 
   QueryFrag<KVT, D, QB> q[1];
   const float factor = q[0].load(p, g4 < G ? row : -1, h * G + g4, p.qk_scale_log2_h[PA_HEAD(p, h)], t4);
@@ -387,6 +428,27 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
     step(k, x, y);
     if (k + 1 < count) step(k + 1, y, x);
   }
+  if constexpr (in_parts<KVT, QB>()) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // this lane's share of a column
+      ColumnStat& st = k == 0 ? st0 : st1;
+      if (2 * t4 + k >= G || st.l == st.l) continue;
+      st = ColumnStat{-INFINITY, 0.0f};
+#pragma unroll 1
+      for (int i = 0; i < count * MT && st.l == st.l; ++i) {
+        const int local = (warp + i / MT * kMassWarps) * MT + i % MT;
+        const float2 c = whole_scores<KVT, D, QB>(p, table, h, (tile0 + local) * 16 + g4, pos, row, h * G + 2 * t4 + k);
+        if (local * 16 < p.score_keys) {
+          float* z = scores + (2 * t4 + k) * stride + local * 16 + g4;
+          z[0] = c.x, z[8] = c.y;
+        }
+        const float two[2] = {c.x, c.y};
+        st.add(two);
+      }
+      if (st.l == st.l) cta_whole = 1;
+    }
+    __syncwarp();
+  }
   // (max, sum) of each column: over the lanes of a warp, the warps, the CTAs
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
@@ -440,6 +502,16 @@ __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ?
       f.load(key_rows<Geo::RB>(p, __ldg(table + (t0 >> lg_p)), h, t0, lg_p, bad), g4, t4);
       float c[4];
       scores_of(f, t0, c);
+      if constexpr (in_parts<KVT, QB>()) {
+        if (cta_whole) {
+#pragma unroll 1
+          for (int k = 0; k < 2 && 2 * t4 + k < G; ++k) {
+            const float2 w = whole_scores<KVT, D, QB>(p, table, h, t0 + g4, pos, row, h * G + 2 * t4 + k);
+            if (k == 0) c[0] = w.x, c[2] = w.y;
+            else c[1] = w.x, c[3] = w.y;
+          }
+        }
+      }
       float w0 = 0.0f, w1 = 0.0f;
       if (2 * t4 < G) {
         w0 = __fmul_rn(ex2(__fsub_rn(c[0], r0.x)), r0.y);
@@ -499,6 +571,23 @@ __device__ __forceinline__ float2 column_stat(const MassParams& p, int c, int h,
     st.merge(o.x, o.y);
   }
   return make_float2(st.m, __fdiv_rn(1.0f, st.l));
+}
+
+// A lane's share of key t's weight (columns 2 t4 and 2 t4 + 1 of every 8) from whole operands.
+template <int KVT, int D, bool QB>
+__device__ __noinline__ float whole_weight(const MassParams& p, const ChunkView& v, int c, int h, int t, int t4) {
+  const int G = p.Hq / p.Hkv;
+  float w = 0.0f;
+#pragma unroll 1
+  for (int i = max(0, t - v.pos0) * G / 8 * 2; w == w; ++i) {  // no row before that one sees the key
+    const int col = i / 2 * 8 + 2 * t4 + i % 2, row = col / G, pos = v.pos0 + row;
+    if (i / 2 * 8 >= v.rows * G) break;
+    if (row >= v.rows || pos < t) continue;
+    const int slot = column_slot(col, G);
+    const float2 z = column_stat(p, c, h, slot / kMassSlots, slot % kMassSlots, pos);
+    w = fmaf(ex2(__fsub_rn(whole_scores<KVT, D, QB>(p, v.table, h, t, pos, v.row0 + row, h * G + col % G).x, z.x)), z.y, w);
+  }
+  return w;
 }
 
 // A CTA's columns, in groups of 8: a warp prepares a group's query fragments for
@@ -616,6 +705,25 @@ __global__ void __launch_bounds__(kMassThreads) chunk_stats_kernel(const __grid_
     step(t0, x, y);
     step(t0 + kMassWarps * 16, y, x);
   }
+  if constexpr (in_parts<KVT, QB>()) {
+#pragma unroll
+    for (int n = 0; n < Cg::GROUPS; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // this lane's share of a column
+        const int col = col0 + 8 * n + 2 * t4 + k;
+        if (col >= cols || st[n][k].l == st[n][k].l) continue;
+        ColumnStat again{-INFINITY, 0.0f};
+#pragma unroll 1
+        for (int t0 = key0 + warp * 16; t0 < key_end && again.l == again.l; t0 += kMassWarps * 16) {
+          const float2 z = whole_scores<KVT, D, QB>(p, v.table, h, t0 + g4, lim[n][k], v.row0 + col / G, h * G + col % G);
+          const float two[2] = {z.x, z.y};
+          again.add(two);
+        }
+        st[n][k] = again;
+        if (again.l == again.l) p.ws_whole[c] = 1;
+      }
+    __syncwarp();
+  }
 #pragma unroll
   for (int n = 0; n < Cg::GROUPS; ++n)
 #pragma unroll
@@ -702,6 +810,16 @@ __global__ void __launch_bounds__(kMassThreads) chunk_weights_kernel(const __gri
             }
           }
       }
+    }
+  }
+  if constexpr (in_parts<KVT, QB>()) {
+    if (__ldcg(p.ws_whole + c) != 0) {
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) {
+        if (w0[i] != w0[i]) w0[i] = whole_weight<KVT, D, QB>(p, v, c, h, tile_at(i) + g4, t4);
+        if (w1[i] != w1[i]) w1[i] = whole_weight<KVT, D, QB>(p, v, c, h, tile_at(i) + g4 + 8, t4);
+      }
+      __syncwarp();
     }
   }
   float* sums = p.mass + (static_cast<size_t>(v.seq) * p.Hkv + h) * (static_cast<size_t>(p.max_blocks) << lg_p);

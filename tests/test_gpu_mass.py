@@ -376,3 +376,99 @@ def test_two_calls_at_once(kv):
             pa.attention_mass(c.pool, q[i], seq, pos, c.tables, mass[1, i], chunks=chunks, workspace=ws[i], stream=streams[i])
         torch.cuda.synchronize()
         assert torch.equal(mass[0], mass[1])
+
+
+# ------------------------------------------- infinities, and values beside them --
+
+def set_key(c, t, h, d, value):
+    c.k[c.tables[c.slots[0], t // c.P].long(), h, t % c.P, d] = value
+
+
+def window(length, rows):
+    """Positions of the last rows of a sequence, and its chunks (none for one row)."""
+    return [length - rows + i for i in range(rows)], [(0, rows)] if rows > 1 else []
+
+
+def check_against(c, q, pos, chunks, big):
+    """The added weights against 64 bits, `big` as in mass_bound; NaN where the reference has it."""
+    rows = len(pos)
+    before = torch.rand(c.num_seqs, c.Hkv, c.max_tokens, generator=torch.Generator().manual_seed(3)).cuda()
+    mass = before.clone()
+    assert run(c, q, c.slots * rows, pos, mass, chunks) == 0
+    added, _ = R.mass_of_rows(c, q, c.slots * rows, pos)
+    assert torch.equal(torch.isnan(mass), torch.isnan(added))
+    bound = R.mass_bound(c, added, before.double(), big, rows, q.shape[1] // c.Hkv)
+    err = (mass.double() - before.double() - added).abs()
+    assert ((err <= bound) | torch.isnan(added)).all()
+    return mass, before
+
+
+TYPES = [("f32", torch.float32), ("f32", torch.bfloat16), ("bf16", torch.float32), ("bf16", torch.bfloat16)]
+
+
+@pytest.mark.parametrize("kv,q_dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_infinite_keys(kv, q_dtype, D, rows):
+    """A key whose score is -infinity gets no weight, and the others theirs."""
+    c = R.make_cache([1700], Hkv=2, D=D, P=16, kv=kv, seed=31)
+    q = queries(rows, 6, D, q_dtype, seed=31)
+    q[:, :, 5] = q[:, :, 5].abs() + 0.1
+    q[:, :, D - 3] = -q[:, :, D - 3].abs() - 0.1
+    q[0, :, 5] = 0.5  # nothing of it is left behind the leading bits
+    pos, chunks = window(1700, rows)
+    _, big = R.mass_of_rows(c, q, c.slots * rows, pos)
+    none = [(0, 0), (0, 3), (0, 8), (1, 17), (1, 1023), (0, 1024), (1, 1699)]
+    for i, (h, t) in enumerate(none):
+        set_key(c, t, h, 5, float("-inf")) if i % 2 else set_key(c, t, h, D - 3, float("inf"))
+    mass, before = check_against(c, q, pos, chunks, big)
+    assert torch.isfinite(mass).all()
+    for h, t in none:
+        assert float(mass[c.slots[0], h, t]) == float(before[c.slots[0], h, t])
+
+
+@pytest.mark.parametrize("kv,q_dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 40])
+def test_infinite_scores(kv, q_dtype, rows):
+    """A score of +infinity leaves no weights to the rows that see the key; other rows and heads keep theirs."""
+    c = R.make_cache([1700], Hkv=2, D=64, P=16, kv=kv, seed=32)
+    q = queries(rows, 4, 64, q_dtype, seed=32)
+    q[:, :, 5] = q[:, :, 5].abs() + 0.1
+    pos, chunks = window(1700, rows)
+    _, big = R.mass_of_rows(c, q, c.slots * rows, pos)
+    set_key(c, 1690, 1, 5, float("inf"))
+    mass, _ = check_against(c, q, pos, chunks, big)
+    s = c.slots[0]
+    assert torch.isnan(mass[s, 1, :1700]).all() and torch.isfinite(mass[s, 0]).all()
+
+
+@pytest.mark.parametrize("kv,q_dtype,large", [("f32", torch.float32, "key"), ("f32", torch.bfloat16, "key"),
+                                              ("f32", torch.float32, "query"), ("bf16", torch.float32, "query")])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_largest_values(kv, q_dtype, large, rows):
+    """f32 values above the largest bf16 one, against ones that bring the product back."""
+    c = R.make_cache([300], Hkv=2, D=64, P=16, kv=kv, seed=33)
+    q = queries(rows, 4, 64, q_dtype, seed=33)
+    most, least = 3.4e38, 2e-38
+    for h in range(2):
+        for t in range(300):
+            set_key(c, t, h, 5, (most if t % 3 else -most) if large == "key" else (least if t % 3 else -least))
+    q[:, :, 5] = least if large == "key" else most
+    pos, chunks = window(300, rows)
+    _, big = R.mass_of_rows(c, q, c.slots * rows, pos)
+    mass, _ = check_against(c, q, pos, chunks, big)
+    assert torch.isfinite(mass).all()
+
+
+@pytest.mark.parametrize("kv,q_dtype", TYPES)
+@pytest.mark.parametrize("length", [4000, 9001])
+def test_infinite_keys_in_long_rows(kv, q_dtype, length):
+    """More scores than a CTA keeps, or a cluster of CTAs."""
+    c = R.make_cache([length], Hkv=1, D=64, P=16, kv=kv, seed=34)
+    q = queries(1, 8, 64, q_dtype, seed=34)
+    q[:, :, 5] = q[:, :, 5].abs() + 0.1
+    _, big = R.mass_of_rows(c, q, c.slots, [length - 1])
+    for t in (1, 2500, 3500, 3999, length - 1):
+        set_key(c, t, 0, 5, float("-inf"))
+    mass, before = check_against(c, q, [length - 1], [], big)
+    assert torch.isfinite(mass).all() and float(mass[c.slots[0], 0, 3500]) == float(before[c.slots[0], 0, 3500])
