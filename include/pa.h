@@ -265,8 +265,10 @@ pa_status pa_evict_select(int32_t n, const int32_t *seq_ids, const int32_t *leng
  *                 share is compacted into a slot of its own).  NULL: in place.
  *   mass          f32 [num_seqs][Hkv][max_blocks_per_seq * page_size]; the destination's
  *                 entries count .. lengths[i] - 1 become zero.  NULL: left alone.
- * The caller's next token goes to position count; pages behind it can be given
- * back (pa_pages_trim).  Slots behind count keep their bytes.
+ * The caller's next token goes to position count; pages behind the last token
+ * still to come can be given back (pa_pages_trim).  Slots behind count keep their
+ * bytes.  A sequence compacted in place no longer holds its prompt (every kv head
+ * keeps tokens of its own): it is no prefix parent for pa_pages_admit.
  * Precondition: no slot is listed twice, as a source of one row and a
  * destination of another either, and a page that receives tokens belongs to
  * that one sequence (in place: pages shared with another sequence would change
@@ -322,7 +324,10 @@ pa_status pa_beam_select(int32_t n_groups, int32_t beams, int32_t vocab, const v
  *   - later columns stay: they are the beam's own pages for the tokens to come.
  * A parent of 0 for every beam fans a prompt out, its unfinished page included.
  * Pages of beams that died stay referenced by the survivors' tables: the slots
- * of a group are released together.
+ * of a group are released together, and none of them is trimmed (pa_pages_trim)
+ * or compacted in place (pa_evict_compact) before.  The tables are changed on the
+ * device alone: an allocator's host rows of these slots keep naming the pages that
+ * each slot holds, and are not copied to the device again while the group lives.
  *   state      per-slot rows of the caller's (e.g. the attention weights), permuted the
  *              same way: state_row_bytes (a multiple of 4) for each of num_seqs slots,
  *              4-byte aligned.  NULL: none.
@@ -489,7 +494,8 @@ void pa_pages_destroy(pa_pages *pages);
 /* Admit sequence slot seq for prompt_tokens + max_new_tokens tokens: reserve
  * every page up front and write the slot's row of block_tables (host, may be
  * NULL).  prefix_parent >= 0 shares the parent's first prefix_tokens / page_size
- * pages (prefix_tokens <= prompt_tokens); -1 for none.  *info (may be NULL)
+ * pages (prefix_tokens <= prompt_tokens), whose contents the caller vouches for
+ * (not after pa_evict_compact in place on the parent); -1 for none.  *info (may be NULL)
  * receives the reason and the numbers.  Returns PA_OK; PA_ERR_NO_PAGES when
  * too few pages are free; PA_ERR_INVALID_ARG for the other reasons.  A refused
  * admission changes nothing. */
@@ -504,6 +510,11 @@ pa_status pa_pages_release(pa_pages *pages, int32_t seq, int32_t *block_tables);
 /* Give back the pages of slot seq behind its first `tokens` tokens (after an
  * eviction): the slot keeps ceil(tokens / page_size) pages, the rest lose its
  * hold, and their block_tables entries become -1 (block_tables may be NULL).
+ * A slot cannot be given pages again: `tokens` counts those that it will still
+ * receive beside those that it holds.  Copy the slot's row to the device's block
+ * tables before the next call that writes through them: the old row names pages that the next
+ * admission may hand to another sequence, whose first append belongs behind the
+ * eviction on the GPU.
  * A slot that holds no more pages than that is left as it is.
  * PA_ERR_INVALID_ARG if the slot holds nothing or tokens < 0. */
 pa_status pa_pages_trim(pa_pages *pages, int32_t seq, int32_t tokens, int32_t *block_tables);

@@ -301,7 +301,8 @@ class Pages:
         _check(load().pa_pages_release(self.handle, int(seq), self.block_tables.ctypes.data_as(ctypes.c_void_p)))
 
     def trim(self, seq: int, tokens: int):
-        """Give back the slot's pages behind its first `tokens` tokens."""
+        """Give back the slot's pages behind its first `tokens` tokens, those still to come
+        counted in (a slot cannot grow again).  The device's copy of its row is the caller's to renew."""
         _check(load().pa_pages_trim(self.handle, int(seq), int(tokens),
                                     self.block_tables.ctypes.data_as(ctypes.c_void_p)))
 
