@@ -303,7 +303,7 @@ class Pages:
     def trim(self, seq: int, tokens: int):
         """Give back the slot's pages behind its first `tokens` tokens, those still to come
         counted in (a slot cannot grow again).  The device's copy of its row is the caller's to renew."""
-        _check(load().pa_pages_trim(self.handle, int(seq), int(tokens),
+        _check(load().pa_pages_trim(self.handle, _int32(seq, "seq"), _int32(tokens, "tokens"),
                                     self.block_tables.ctypes.data_as(ctypes.c_void_p)))
 
     def free_count(self) -> int:
@@ -436,6 +436,14 @@ def _call(fn, device: int, stream, *args):
         raise PaError(status, last_error())
 
 
+def _int32(value, name: str) -> int:
+    """A number that the C ABI takes as int32 (ctypes would drop its upper bits)."""
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} {value} does not fit in 32 bits")
+    return value
+
+
 def _dims(t, name: str, dims: str):
     """The shape of a tensor with as many dimensions as `dims` names."""
     shape = t.shape
@@ -484,6 +492,7 @@ def evict_select(mass, seq_ids, lengths, keep, kept_lengths=None, keep_first: in
     n, _, budget = _dims(keep, "keep", "n, Hkv, budget")
     if kept_lengths is not None and n and kept_lengths.data_ptr() == lengths.data_ptr():
         raise ValueError("kept_lengths may not be lengths")
+    keep_first, keep_last = _int32(keep_first, "keep_first"), _int32(keep_last, "keep_last")
     device, (mp, sp, lp, kp, np_, stp) = _tensors((
         (mass, "mass", torch.float32, None), (seq_ids, "seq_ids", torch.int32, (n,)),
         (lengths, "lengths", torch.int32, (n,)), (keep, "keep", torch.int32, (n, heads, budget)),
@@ -522,6 +531,7 @@ def beam_select(logits, scores, parents, tokens, out_scores, finished=None, end_
     import torch
     groups, beams, vocab = _dims(logits, "logits", "groups, beams, vocab")
     _, n_out = _dims(parents, "parents", "groups, n_out")
+    end_token = _int32(end_token, "end_token")
     # rows: contiguous, and evenly spaced over groups and beams (a stride of a size-1 axis says nothing)
     across, down, along = logits.stride()
     row = down if beams > 1 else across if groups > 1 else vocab

@@ -279,3 +279,20 @@ def test_longest_block_table(lib, pool):
     assert mass(longest + 1) == pa.PA_ERR_UNSUPPORTED
     assert compact(longest) == pa.PA_OK
     assert compact(longest + 1) == pa.PA_ERR_UNSUPPORTED
+
+
+def test_numbers_beyond_32_bits(lib):
+    """They are refused, not cut to their lower bits."""
+    mass, three = torch.zeros(2, 2, 80), i32(3)
+    for name in ("keep_first", "keep_last"):
+        for value in (1 << 32, (1 << 32) + 4, -(1 << 32)):
+            with pytest.raises(ValueError, match=name):
+                pa.evict_select(mass, three, i32(3), i32(3, 2, 8), **{name: value})
+    with pytest.raises(ValueError, match="end_token"):
+        pa.beam_select(torch.zeros(2, 4, 100), torch.zeros(2, 4), i32(2, 8), i32(2, 8), torch.zeros(2, 8), end_token=1 << 32)
+    p = pa.Pages(20, 16, 3, 10)
+    assert p.admit(0, 100, 20)[0] == pa.PA_OK
+    for args in ((0, 1 << 32), ((1 << 32), 0)):
+        with pytest.raises(ValueError, match="32 bits"):
+            p.trim(*args)
+    assert p.free_count() == 12
