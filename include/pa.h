@@ -246,7 +246,7 @@ pa_status pa_attention_mass(const pa_pool *pool, int32_t n_rows, const void *q, 
  *   mass              f32 [num_seqs][num_kv_heads][max_tokens], as pa_attention_mass
  *                     fills it with max_tokens = max_blocks_per_seq * page_size
  *   keep              int32 [n][num_kv_heads][budget], written whole
- *   kept_lengths      int32 [n], receives count (may be NULL; may not be `lengths`)
+ *   kept_lengths      int32 [n], receives count (may be NULL; may be neither `lengths` nor `seq_ids`)
  * keep_first + keep_last <= budget; max_tokens <= 2^30.  One launch, no workspace; graph-capturable.
  * A row whose sequence is outside [0, num_seqs) or whose length is outside
  * [0, max_tokens] keeps nothing (all -1, count 0) and records

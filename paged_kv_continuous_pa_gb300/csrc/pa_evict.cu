@@ -667,6 +667,9 @@ pa_status pa_evict_select(int32_t n, const int32_t* seq_ids, const int32_t* leng
                 keep_first, keep_last, budget);
   if (n == 0) return PA_OK;
   if (!seq_ids || !lengths || !mass || !keep) return fail(PA_ERR_INVALID_ARG, "select: a device pointer is NULL");
+  // (a row's CTAs read its slot and length at different times)
+  if (kept_lengths != nullptr && (kept_lengths == lengths || kept_lengths == seq_ids))
+    return fail(PA_ERR_INVALID_ARG, "kept_lengths may not be lengths or seq_ids");
   const int64_t units = static_cast<int64_t>(n) * num_kv_heads;
   if (units > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "%lld (sequence, kv head) pairs in one call", (long long)units);
   pa::SelectParams p{};

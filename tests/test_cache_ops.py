@@ -296,3 +296,13 @@ def test_numbers_beyond_32_bits(lib):
         with pytest.raises(ValueError, match="32 bits"):
             p.trim(*args)
     assert p.free_count() == 12
+
+
+def test_select_does_not_write_its_inputs(lib):
+    """The C entry refuses counts that would go over what other CTAs of the call still read."""
+    other = [ctypes.c_void_p(0x200000 + 0x1000 * i) for i in range(4)]
+
+    def call(kept):
+        return lib.pa_evict_select(2, other[0], other[1], other[2], 4, 2, 100, 10, 0, 0, other[3], kept, None, None)
+    assert call(other[0]) == pa.PA_ERR_INVALID_ARG and "kept_lengths" in pa.last_error()
+    assert call(other[1]) == pa.PA_ERR_INVALID_ARG and "kept_lengths" in pa.last_error()
