@@ -23,6 +23,8 @@
  *     allocated and owned by the caller.  The library owns only the small host
  *     pa_pool object.  No call allocates device memory or synchronises.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default).
+ *   - Any host thread may call, several at once on one pool where their workspaces
+ *     and outputs are their own (pa_pool_set_head_scales comes before).
  *   - Host-side argument errors return a status at once, launch nothing, and
  *     set a thread-local message readable with pa_last_error().  No C++
  *     exception crosses the ABI.

@@ -198,14 +198,16 @@ pa_status encode_map_pair(pa_pool* pool, CUtensorMap* km, CUtensorMap* vm, uint3
 // D = 128 pools, tensor-core decode units: bf16 boxes of 64 elements x min(P, 32)
 // rows (one head-dim half), e4m3 boxes of 128 bytes x min(P, 32) rows.
 pa_status encode_decode_maps(pa_pool* pool) {
-  if (pool->dec_maps_ready) return PA_OK;
+  if (pool->dec_maps_ready.load(std::memory_order_acquire)) return PA_OK;
   const pa_pool_desc& d = pool->desc;
   if (d.head_dim != 128 || (d.kv_dtype != PA_BF16 && d.kv_dtype != PA_FP8_E4M3))
     return fail(PA_ERR_UNSUPPORTED, "no tensor-core decode view for this pool's dtype / head_dim");
   const int P = d.page_size;
+  const std::lock_guard<std::mutex> lock(pool->maps);
+  if (pool->dec_maps_ready.load(std::memory_order_relaxed)) return PA_OK;
   const pa_status st = encode_map_pair(pool, &pool->kmap_dec, &pool->vmap_dec, d.kv_dtype == PA_BF16 ? 64u : 128u,
                                        static_cast<uint32_t>(P > 32 ? 32 : P));
-  if (st == PA_OK) pool->dec_maps_ready = true;
+  if (st == PA_OK) pool->dec_maps_ready.store(true, std::memory_order_release);
   return st;
 }
 
@@ -230,11 +232,13 @@ pa_status check_desc(const pa_pool_desc* d) {
 
 // bf16 pools, prefill tiles: 64 elements x min(P, 64) rows (half or all of the head dim).
 pa_status pa::encode_tile_maps(pa_pool* pool) {
-  if (pool->tile_maps_ready) return PA_OK;
+  if (pool->tile_maps_ready.load(std::memory_order_acquire)) return PA_OK;
   if (pool->desc.kv_dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "the tile path reads bf16 pools");
   const int P = pool->desc.page_size;
+  const std::lock_guard<std::mutex> lock(pool->maps);
+  if (pool->tile_maps_ready.load(std::memory_order_relaxed)) return PA_OK;
   const pa_status st = encode_map_pair(pool, &pool->kmap, &pool->vmap, 64u, static_cast<uint32_t>(P > 64 ? 64 : P));
-  if (st == PA_OK) pool->tile_maps_ready = true;
+  if (st == PA_OK) pool->tile_maps_ready.store(true, std::memory_order_release);
   return st;
 }
 

@@ -5,6 +5,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "../../include/pa.h"
 #include "pa_kernels.h"
 
@@ -14,8 +17,9 @@ struct pa_pool {
   float k_scale_h[pa::kMaxHeadScales], v_scale_h[pa::kMaxHeadScales];
   void* k;
   void* v;
-  bool tile_maps_ready;  // kmap / vmap encoded (on first use by the prefill tile path)
-  bool dec_maps_ready;   // kmap_dec / vmap_dec encoded (on first use by tensor-core decode units)
+  std::mutex maps;       // held while they are encoded: threads may make a pool's first calls at once
+  std::atomic<bool> tile_maps_ready;  // kmap / vmap encoded (on first use by the tile paths)
+  std::atomic<bool> dec_maps_ready;   // kmap_dec / vmap_dec encoded (on first use by tensor-core decode units)
   CUtensorMap kmap;      // 2-D views of the pools for tensor-map copies
   CUtensorMap vmap;
   CUtensorMap kmap_dec;

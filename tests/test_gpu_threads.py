@@ -84,3 +84,20 @@ def test_first_call_of_a_thread(kv, name, fresh):
     pool = s.pool() if fresh else s.c.pool
     in_threads([lambda: s.calls()[name](pool, got, stream)])
     assert torch.equal(got[name][0], s.want[name][0])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_first_calls_of_a_pool(kv):
+    """The pool's tensor maps are encoded by whichever call comes first, whole before any call reads them."""
+    s = Step(kv)
+    names = ["mass", "chunk", "rows"] * 2
+    for _ in range(8):
+        pool, gate = s.pool(), threading.Barrier(len(names))
+        got, streams = [s.buffers() for _ in names], [torch.cuda.Stream() for _ in names]
+
+        def work(i):
+            gate.wait()
+            s.calls()[names[i]](pool, got[i], streams[i])
+        in_threads([lambda i=i: work(i) for i in range(len(names))])
+        for name, to in zip(names, got):
+            assert torch.equal(to[name][0], s.want[name][0])
