@@ -297,7 +297,8 @@ pa_status pa_evict_compact(const pa_pool *pool, int32_t n, const int32_t *seq_id
  *   scores      f32 [n_groups * beams], the hypotheses' log-probabilities so far
  *   finished    int32 [n_groups * beams], non-zero: finished (may be NULL: none)
  *   parents, tokens   int32 [n_groups][n_out]: the beam (0..beams-1) a continuation
- *               extends, and its token;  out_scores  f32 [n_groups][n_out]
+ *               extends, and its token;  out_scores  f32 [n_groups][n_out] (may be
+ *               `scores` where n_out = beams; otherwise outputs overlap no input)
  * beams <= 32, n_out <= 64, vocab <= 2^20.  A logit of -infinity is no continuation; a beam
  * whose log-sum-exp is not finite (NaN or +infinity among its logits, or
  * nothing but -infinity) or whose score is not finite has none.  Where fewer

@@ -360,3 +360,17 @@ def test_beam_search_over_a_paged_cache():
                      tables, status=status)
         scores = new_scores
     assert int(status.item()) == 0 and moved > steps // 4
+
+
+@pytest.mark.parametrize("b", [1, 4, 32])
+def test_scores_in_place(b):
+    """As many continuations as beams: the new scores may take the old ones' place."""
+    logits, scores = make(5, b, 3001, seed=40 + b)
+    want = reference(logits, scores, b)
+    ws = torch.zeros(pa.beam_workspace_bytes(5, b, 3001, b), dtype=torch.uint8, device="cuda")
+    parents, tokens = (torch.empty(5, b, dtype=torch.int32, device="cuda") for _ in range(2))
+    apart = torch.empty_like(scores)
+    pa.beam_select(logits, scores, parents, tokens, apart, workspace=ws)
+    pa.beam_select(logits, scores, parents, tokens, scores, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(parents.cpu(), want[0]) and torch.equal(tokens.cpu(), want[1]) and torch.equal(scores, apart)
