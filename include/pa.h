@@ -206,8 +206,8 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
  * looks at.  For row r with sequence s and position p, kv head h and the G
  * query heads that read it,
  *     mass[s][h][t] += sum over those heads of softmax_t(scale * q[r][g] . K_s[t]),  t = 0..p
- * so one row adds G to the sum of its (sequence, kv head).  K is read once, V
- * not at all; append the step's rows first.
+ * so one row adds G to the sum of its (sequence, kv head).  V is not read;
+ * append the step's rows first.
  *   mass      f32 [num_seqs][Hkv][max_blocks_per_seq * page_size] in device memory,
  *             16-byte aligned; the caller zeroes a sequence's rows when it admits it.
  *             Entries past a row's position are not touched.
@@ -221,8 +221,11 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
  * Precondition: a sequence has one row outside the chunks, or the rows of one
  * chunk, in a call (a step's rows satisfy it): its sums then have one writer
  * and the same bits in any batch.
- * Scores, sums and weights are FP32.  A score of -infinity (an infinite key) is a weight of zero; one of
- * +infinity or NaN makes its row's weights NaN for that kv head.
+ * Scores, sums and weights are FP32.  The products behind a score take bf16 and
+ * e4m3 values as they are, f32 ones as three bf16 parts (24 bits, fewer below
+ * 2^-110), an f32 query over an e4m3 pool as two f16 parts (22 bits).  A score of
+ * -infinity (an infinite key) is a weight of zero; one of +infinity or NaN makes
+ * its row's weights NaN for that kv head.
  * max_blocks_per_seq * page_size <= 2^30.  Errors as for pa_attention; a row with an
  * invalid sequence, position or page, or a chunk with such a row or whose rows
  * are not consecutive positions of one sequence, adds nothing and records

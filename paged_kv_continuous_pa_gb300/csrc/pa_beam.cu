@@ -149,8 +149,9 @@ __device__ __forceinline__ uint64_t bound_keys(const uint64_t* list, int n, int 
 //     best of the chunk is at least that.  It is found by bisection; among equal
 //     bests the lowest tokens set it.  Candidates are ranked by counting.
 //
-// Bound by the one read of the logits: about six instructions an element
-// (maximum, subtraction, multiplication, ex2, addition; packed in pairs).  512 rows
+// Bound by the read of the logits and by the pauses in it: a CTA asks for its next
+// chunk when the one before is summed and ranked (DRAM 54% busy, issue slots 34%, special
+// functions 13%; warps wait for loads, then at barriers).  512 rows
 // of 131071 f32 logits (268 MB) take 56 us, 4.8 TB/s, the merge behind it 6 more.
 // Four CTAs to an SM: 64 us for the pair, three 71, five 79.
 template <bool BF16>

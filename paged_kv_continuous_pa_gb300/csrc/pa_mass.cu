@@ -144,7 +144,9 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
   // keys to a CTA (512 ragged rows of up to 2662 keys in one CTA each: 225 us, in
   // CTAs of 2048 keys 255, of 1024 358), so 8 CTAs from 16385 keys on; 16 from 65537
   // on (one row of 131072 keys: 59 us with 16, 160 with 8; at 16 rows of 65536,
-  // 364 with 16 and 335 with 8).
+  // 364 with 16 and 335 with 8).  The price is paid by short rows under wide tables: the
+  // 512 ragged rows take 236 us with a table of 2662 tokens, 270 with 8192, 627 with 32768,
+  // 1432 with 131072.
   const int64_t keys = static_cast<int64_t>(max_blocks_per_seq) * d.page_size;
   p.cluster = 1;
   while (p.cluster < 8 && keys > static_cast<int64_t>(p.cluster) * pa::kMassClusterKeys) p.cluster *= 2;

@@ -6,8 +6,8 @@
 // domain; a row's weights need its maximum and sum over all keys first.
 //
 // Rows outside the chunks (`mass_row_kernel`): one cluster of CTAs per (row, kv
-// head).  K is read from memory once, straight into tensor-core fragments; the
-// scores wait in shared memory while the cluster's CTAs exchange their (max,
+// head).  K is read from memory once, straight into tensor-core fragments (but for
+// keys whose scores find no room); the scores wait in shared memory while the cluster's CTAs exchange their (max,
 // sum) pairs, then become weights.
 // Chunks: the (row, head) pairs of a kv head are columns that share the keys.
 // `chunk_check_kernel` looks the chunks over, `chunk_stats_kernel` finds every
@@ -338,10 +338,14 @@ __host__ __device__ constexpr int score_stride(int keys) { return (keys + 31) / 
 //
 // Bound by the one read of K: 512 ragged rows of up to 2662 keys (16 query heads
 // over 8, bf16) take 226 us, 6.5 TB/s; 32 rows of 32768 keys (32 heads over 8,
-// e4m3) 217 us, 5.0 TB/s, where four scores per 128-byte key row (two conversions
-// and an MMA each) share the SM with the loads.  A weight costs one exponential
+// e4m3) 217 us, 5.0 TB/s: there the loads' latency shows (DRAM 62% busy, issue slots
+// 36%, most warps waiting for K), with 4 KB of K ahead for each of an SM's 16 warps and
+// more to do between two loads.  f32 queries over bf16 take 309 us for the ragged
+// rows, f32 pools 535 (bf16 queries) and 608.  A weight costs one exponential
 // per score twice (the running sum, the weight); the score itself is kept, not
-// recomputed.  4 KB of K to a warp's step, in one CTA: 225 us; 16-key tiles one by
+// recomputed, as far as the CTA's room goes: 104 KB, 3744 keys of 7 query heads and 3264
+// of 8.  Keys beyond are read and scored a second time (64 rows of 4000 to 4096
+// keys: 98 us with 4 query heads, 170 with 7, 188 with 8).  4 KB of K to a warp's step, in one CTA: 225 us; 16-key tiles one by
 // one in CTAs of 2048 keys: 256.  Few short rows (4 of up to 900 keys) are latency: 6 us.
 template <int KVT, int D, bool QB>
 __global__ void __launch_bounds__(kMassThreads, MassGeom<KVT, D, QB>::RB > 256 ? 1 : 2) mass_row_kernel(const __grid_constant__ MassParams p) {
@@ -632,11 +636,13 @@ struct ChunkQueries {
 };
 
 // The warp-level launches serve f32 and e4m3 pools and f32 queries; bf16 queries
-// over bf16 pools have the tile path.  Bound by instruction issue (conversions, an
-// exponential and a comparison per score and launch): eight windows of 64 rows
-// over 4k-16k keys (32 heads over 8) take 595 us with an e4m3 pool, 1466 with f32
-// queries over a bf16 one, 2981 with f32 both.  Fragments prepared by every warp
-// for itself took 1076, 2675 and 4556.
+// over bf16 pools have the tile path.  Eight windows of 64 rows over 4k-16k keys (32
+// heads over 8) take 545 us with an e4m3 pool (f32 queries 700), 1305 with f32
+// queries over a bf16 one, 1229 with bf16 queries over an f32 one, 2649 with f32
+// both.  Bound by latency, not by a unit (issue slots 30% to 48% busy, tensor pipe 23% to
+// 48%, DRAM 3% to 5%): 8 or 16 warps to an SM, for their fragments' registers, and in each a
+// chain of conversions, MMAs and exponentials.  Fragments prepared by every warp for
+// itself took twice the time.
 //
 // First launch: one CTA per (chunk, kv head, key range, column block).  The
 // CTA's warps take the range's 16-key tiles in turn.

@@ -24,14 +24,16 @@
 //
 // The scores are computed twice (a weight needs its column's sum over all
 // keys first): 4 D operations and two exponentials per visible (row, head, key).
-// Eight windows of 64 rows over 4k-16k keys (32 heads over 8): 61 us for the
-// statistics and 60 for the weights, 85 GFLOP: 700 TFLOP/s while the two run, the
-// tensor pipe active a quarter of the time.  Bound by the steps' turnaround: a
-// score group reads its S buffer in about 1600 cycles, of which every third step
-// is its own, and an MMA warp holds 720 for a tile's eight MMAs (512 of them at
-// the pipe's rate).  One MMA warp for both column tiles took 139 us instead of
-// 121; a CTA per unit 147; S buffers of 64 columns, two to a group, 212; key
-// ranges of 512 / 2048 keys instead of 1024: 133 / 127.
+// Eight windows of 64 rows over 4k-16k keys (32 heads over 8): 130 us, of which 60
+// are the statistics' and 68 the weights' (cold, each alone; 43 GFLOP each).  A CTA
+// takes 1740 and 1990 cycles to a step of 128 keys x 128 columns, which needs 512 of
+// the tensor pipe and, at 32 exponentials a cycle, 512 of the special functions'.
+// No unit is busy: tensor pipe 28% and 24%, special functions 30% and 26%, issue
+// slots 40% and 31%.  Bound by latency: three score warps to a scheduler, which
+// mostly wait for their own results, for S from tensor memory and (weights) at the
+// barriers around the columns' statistics.  One MMA warp for both column tiles took
+// 139 us where two took 121 (inputs in L2); a CTA per unit 147; S buffers of 64
+// columns, two to a group, 212; key ranges of 512 / 2048 keys instead of 1024: 133 / 127.
 // Every wait is bounded; a call that gives up reports it, and adds nothing more.
 #pragma once
 
