@@ -259,9 +259,10 @@ struct ColumnStat {
     for (int i = 1; i < N; ++i) w = __fadd_rn(w, ex2(__fsub_rn(s[i], ref)));
     l = __fadd_rn(l, w);
   }
-  __device__ __forceinline__ void merge(float om, float ol) {
+  // (scale: of maxima in another measure than log2)
+  __device__ __forceinline__ void merge(float om, float ol, float scale = 1.0f) {
     const float top = fmaxf(m, om);
-    const float a = m == top ? 1.0f : ex2(__fsub_rn(m, top)), b = om == top ? 1.0f : ex2(__fsub_rn(om, top));
+    const float a = m == top ? 1.0f : ex2(__fmul_rn(__fsub_rn(m, top), scale)), b = om == top ? 1.0f : ex2(__fmul_rn(__fsub_rn(om, top), scale));
     l = __fadd_rn(__fmul_rn(l, a), __fmul_rn(ol, b));
     m = top;
   }
@@ -561,9 +562,10 @@ struct ChunkView {
 };
 
 // A column's (maximum, 1 / sum) over the key ranges that a row at `pos` sees,
-// merged in ascending order: slot `slot` of the chunk's tile `tile`.
+// merged in ascending order: slot `slot` of the chunk's tile `tile`.  (The tile path's maxima are scores as the
+// MMAs give them, to be scaled.)
 __device__ __forceinline__ float2 column_stat(const MassParams& p, int c, int h, int tile, int slot,
-                                              int pos) {
+                                              int pos, float scale = 1.0f) {
   const size_t stride = static_cast<size_t>(p.chunk_tiles[c]) * kMassSlots;
   const float2* s = p.ws_part + p.chunk_part[c] + static_cast<size_t>(h) * p.n_splits * stride +
                     static_cast<size_t>(tile) * kMassSlots + slot;
@@ -572,7 +574,7 @@ __device__ __forceinline__ float2 column_stat(const MassParams& p, int c, int h,
 #pragma unroll 8
   for (int k = 0; k < n; ++k) {
     const float2 o = __ldcg(s + k * stride);
-    st.merge(o.x, o.y);
+    st.merge(o.x, o.y, scale);
   }
   return make_float2(st.m, __fdiv_rn(1.0f, st.l));
 }

@@ -1,7 +1,7 @@
 // pa_mass_tiles.cuh -- the chunks' launches of pa_attention_mass on the
 // 5th-generation tensor cores (bf16 queries and pool).  Eight windows of 2 rows
-// over 4k-16k keys take 98 us here and 250 with the warp-level MMAs of the other
-// types' launches, of 64 rows 130 us here.
+// over 4k-16k keys take 100 us here and 250 with the warp-level MMAs of the other
+// types' launches, of 64 rows 134 us here.
 //
 // A chunk's columns for kv head h are its (row, query head) pairs, 128 / G rows
 // to a tile of 128 columns; a CTA works on two tiles at a time, so that a key
@@ -24,9 +24,9 @@
 //
 // The scores are computed twice (a weight needs its column's sum over all
 // keys first): 4 D operations and two exponentials per visible (row, head, key).
-// Eight windows of 64 rows over 4k-16k keys (32 heads over 8): 130 us, of which 60
-// are the statistics' and 68 the weights' (cold, each alone; 43 GFLOP each).  A CTA
-// takes 1740 and 1990 cycles to a step of 128 keys x 128 columns, which needs 512 of
+// Eight windows of 64 rows over 4k-16k keys (32 heads over 8): 134 us, of which 62
+// are the statistics' and 70 the weights' (cold, each alone; 43 GFLOP each).  A CTA
+// takes 1800 and 2040 cycles to a step of 128 keys x 128 columns, which needs 512 of
 // the tensor pipe and, at 32 exponentials a cycle, 512 of the special functions'.
 // No unit is busy: tensor pipe 28% and 24%, special functions 30% and 26%, issue
 // slots 40% and 31%.  Bound by latency: three score warps to a scheduler, which
@@ -48,6 +48,10 @@ namespace pa {
 constexpr int kMtKeys = 128;      // keys of a key tile, columns of a column tile
 constexpr int kMtBuffers = 3;     // S buffers, each with a group of four score warps
 constexpr int kMtKeyBufs = 4;     // key tiles in shared memory
+// Scores (log2 domain) up to which the weights take a column's log2-sum-exp as one number, rounded twice by half a
+// step of at most 2^-14: a weight is then off by up to 2^-14 ln 2 = 4e-5 of itself.  (As one number for all, scores of
+// 1e6 gave columns whose weights summed to 1.01, of 1e8 to millions.)
+constexpr float kMtNear = 1024.0f;
 constexpr int kMtScoreWarps = 4 * kMtBuffers;
 constexpr int kMtCopyWarp = kMtScoreWarps, kMtMmaWarp = kMtCopyWarp + 1;  // ... two MMA warps
 constexpr int kMtThreads = 32 * (kMtMmaWarp + 2);
@@ -70,8 +74,9 @@ struct MassTileSmem {  // byte offsets from a 1024-byte aligned base
   static constexpr int HALF = kMtKeys * 128;   // one half of a tile of 128 rows
   static constexpr int TILE = NH * HALF;
   static constexpr int Q_OFF = kMtKeyBufs * TILE;                // two query tiles
-  static constexpr int STAT_OFF = Q_OFF + 2 * TILE;              // W: minus the log2-sum-exp of their columns
-  static constexpr int ACC_OFF = STAT_OFF + (W ? 2 * kMtKeys * 4 : 0);  // per group: W a sum per key; else (max, sum) of two tiles
+  static constexpr int STAT_OFF = Q_OFF + 2 * TILE;              // W: of their columns minus the log2-sum-exp, then (for
+                                                                 // far scores) the maximum and minus log2 of the sum
+  static constexpr int ACC_OFF = STAT_OFF + (W ? 6 * kMtKeys * 4 : 0);  // per group: W a sum per key; else (max, sum) of two tiles
   static constexpr int ACC = W ? kMassSplitKeys : 4 * kMtKeys;   // floats of a group
   static constexpr int BAR_OFF = ACC_OFF + kMtBuffers * ACC * 4;
   static constexpr int TMEM_OFF = BAR_OFF + MT_COUNT * 8;
@@ -121,6 +126,32 @@ __device__ __forceinline__ void over_columns(uint32_t taddr, int cols, F f) {
     if (i0 + 64 < cols) tmem_ld32_start(taddr + i0 + 64, a);
     f(i0 + 32, b);
   }
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A key's weights of a column tile whose scores are far from zero, summed over the columns from `from` on: 2^((score -
+// maximum) scale - log2 sum), the steps of the statistics, so that a column's weights sum to 1 whatever its scores.
+// (Rarely run, and small, so as to leave the registers of the loop around it alone.)
+__device__ __forceinline__ float far_weight(uint32_t taddr, int from, int cols, const float* maximum, const float* lg, float scale) {
+  float w = 0.0f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < cols; i0 += 8) {
+    float y[8];
+    tmem_ld8(taddr + i0, y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float z = fmaf(__fsub_rn(y[j], maximum[i0 + j]), scale, lg[i0 + j]);
+      if (i0 + j >= from && i0 + j < cols) w = __fadd_rn(w, ex2(z));
+    }
+  }
+  return w;
 }
 
 // 3-D tiled load of the box at (x, y, z); x * element size a multiple of 16 bytes.
@@ -335,28 +366,47 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
     const float scale = p.qk_scale_log2_h[0];  // bf16 pools have no head scales
     int u = 0;
     auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kMtScoreWarps * 32) : "memory"); };
+    auto meet_or = [](bool mine) {  // ... and whether it holds for any of them
+      uint32_t any;
+      asm volatile("{ .reg .pred p, q; setp.ne.u32 q, %1, 0; bar.red.or.pred p, 1, %2, q; selp.u32 %0, 1, 0, p; }"
+                   : "=r"(any)
+                   : "r"(static_cast<uint32_t>(mine)), "n"(kMtScoreWarps * 32)
+                   : "memory");
+      return any != 0;
+    };
     // The score warps meet the same number of times whatever a wait of theirs does (`wok` guards the waits).
     for (int i = blockIdx.x; i < total; i += gridDim.x) {
       const MassUnit x = unit_at(i);
       if (x.nk == 0) continue;
       // the group's place in this unit: by the unit's own steps, so that its sums do not depend on the units before
       float* const mine = acc + (group + kMtBuffers - u % kMtBuffers) % kMtBuffers * S::ACC;
-      float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};  // W false: this thread's columns
+      // W false: this thread's columns, the maximum of the scores as the MMAs give them.  A score enters as its
+      // distance from it, times the scale: a product from which the scaled maximum is taken in one step (unrounded
+      // against rounded) is off by half a step of that, which a large one makes any number.  (62 us for the windows
+      // above, in one step 59.)
+      float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
       for (int t = x.t_first; t < x.t_end; t += 2) {
         const int n0 = tiles_seen(x, t), n1 = tiles_seen(x, t + 1), n = max(n0, n1);
+        bool far = false;  // W: a column of the two tiles has scores beyond kMtNear
         if constexpr (W) {
-          // minus every column's log2-sum-exp, of the two tiles, a column to a thread
+          // every column's maximum and sum, of the two tiles, a column to a thread
           if (t > x.t_first) meet();  // the tiles before are done with
           if (tid < 2 * kMtKeys) {
             const int col = tid % kMtKeys, r = (t + tid / kMtKeys) * R + col / G;
-            float z = 0.0f;
+            float m = 0.0f, lg = 0.0f;
             if (col < R * G && r < x.rows) {
-              const float2 st = column_stat(p, x.chunk, x.h, t + tid / kMtKeys, col, x.pos0 + r);
-              z = __fsub_rn(log2f(st.y), st.x);  // (y is one over the sum)
+              const float2 st = column_stat(p, x.chunk, x.h, t + tid / kMtKeys, col, x.pos0 + r, scale);
+              m = st.x;
+              lg = log2f(st.y);  // (y is one over the sum)
             }
-            reinterpret_cast<float*>(sm + S::STAT_OFF)[tid] = z;
+            float* stat = reinterpret_cast<float*>(sm + S::STAT_OFF) + tid;
+            const float y = __fmul_rn(m, scale);
+            stat[0] = __fsub_rn(lg, y);
+            stat[2 * kMtKeys] = m;
+            stat[4 * kMtKeys] = lg;
+            far = fabsf(y) > kMtNear && fabsf(y) < INFINITY;  // (a column without a finite maximum has no weights)
           }
-          meet();
+          far = meet_or(far);
         }
         for (int kt = 0; kt < n && wok; ++kt) {
           for (int half = 0; half < 2 && wok; ++half) {
@@ -385,9 +435,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
                 float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int j = 4; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
-                const float mx = __fmul_rn(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), scale);
-                if (mx > __fadd_rn(mr, kRescaleSlack)) {
-                  lr = __fmul_rn(lr, ex2(__fsub_rn(mr, mx)));
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                if (__fmul_rn(__fsub_rn(mx, mr), scale) > kRescaleSlack) {
+                  lr = __fmul_rn(lr, ex2(__fmul_rn(__fsub_rn(mr, mx), scale)));
                   mr = mx;
                 }
                 const float neg = mr == -INFINITY ? 0.0f : -mr;
@@ -396,7 +446,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
                 for (int j = 0; j < 4; ++j) ls[j] = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
-                  const float2 z = __ffma2_rn(make_float2(s[j], s[j + 1]), make_float2(scale, scale), make_float2(neg, neg));
+                  const float2 z = __fmul2_rn(__fadd2_rn(make_float2(s[j], s[j + 1]), make_float2(neg, neg)), make_float2(scale, scale));
                   ls[(j / 2) & 3] = __fadd2_rn(ls[(j / 2) & 3], make_float2(ex2(z.x), ex2(z.y)));
                 }
                 const float2 z = __fadd2_rn(__fadd2_rn(ls[0], ls[1]), __fadd2_rn(ls[2], ls[3]));
@@ -428,7 +478,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
                 w2[0] = __fadd2_rn(w2[0], e0);
                 w2[1] = __fadd2_rn(w2[1], e1);
               };
-              if (t0 + kMtKeys - 1 > x.pos0 + first_row || cols < kMtKeys)
+              if (far)
+                w2[0].x = far_weight(col, from, cols, stat + 2 * kMtKeys, stat + 4 * kMtKeys, scale);
+              else if (t0 + kMtKeys - 1 > x.pos0 + first_row || cols < kMtKeys)
                 over_columns(col, cols, [&](int i0, uint32_t(&y)[32]) {
 #pragma unroll
                   for (int j = 0; j < 32; j += 4) add4(std::true_type(), y, i0, j);
@@ -465,7 +517,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mass_tile_kernel(const __grid_c
           ColumnStat s{-INFINITY, 0.0f};
 #pragma unroll
           for (int k = 0; k < kMtBuffers; ++k)
-            s.merge(acc[k * S::ACC + half * 2 * kMtKeys + m], acc[k * S::ACC + half * 2 * kMtKeys + kMtKeys + m]);
+            s.merge(acc[k * S::ACC + half * 2 * kMtKeys + m], acc[k * S::ACC + half * 2 * kMtKeys + kMtKeys + m], scale);
           p.ws_part[p.chunk_part[x.chunk] +
                     ((static_cast<size_t>(x.h) * p.n_splits + x.split) * p.chunk_tiles[x.chunk] + x.t_first + half) * kMtKeys + m] =
               make_float2(s.m, s.l);

@@ -472,3 +472,22 @@ def test_infinite_keys_in_long_rows(kv, q_dtype, length):
         set_key(c, t, 0, 5, float("-inf"))
     mass, before = check_against(c, q, [length - 1], [], big)
     assert torch.isfinite(mass).all() and float(mass[c.slots[0], 0, 3500]) == float(before[c.slots[0], 0, 3500])
+
+
+@pytest.mark.parametrize("kv,q_dtype", TYPES + [("e4m3", torch.bfloat16), ("e4m3", torch.float32)])
+@pytest.mark.parametrize("scale", [1e2, 1e4, 1e6, 1e9, 1e20, 1e34])
+@pytest.mark.parametrize("rows,length,start", [(1, 1700, None), (1, 1700, 0), (40, 40, 0), (40, 2500, 0), (300, 2500, 0)])
+def test_weights_sum_to_one_at_any_score(kv, q_dtype, scale, rows, length, start):
+    """A row's weights are a distribution however large its finite scores are (start None: outside the chunks)."""
+    c = R.make_cache([length], Hkv=2, D=128, P=16, kv=kv, seed=36)
+    q = queries(rows, 8, 128, q_dtype, seed=36, scale=scale)
+    pos, _ = window(length, rows)
+    mass = torch.zeros(c.num_seqs, c.Hkv, c.max_tokens, device="cuda")
+    assert run(c, q, c.slots * rows, pos, mass, [] if start is None else [(0, rows)]) == 0
+    # a column's statistics against its weights: 2^-14 ln 2 at most (twice half a step of scores up to 1024 in the
+    # log2 domain; larger ones are taken relative to their maximum), ex2.approx 2^-22 twice, FP32 sums of at most
+    # `length` weights and rows * 4 columns, half a step 2^-24 an addition
+    tol = 2.0 ** -14 * 0.6932 + 2.0 ** -21 + (length + rows * 4) * 2.0 ** -24
+    total = mass[c.slots[0]].double().sum(dim=1)
+    assert ((total - rows * 4).abs() <= tol * rows * 4).all(), (total / (rows * 4)).tolist()
+    assert float(mass.max()) <= rows * 4 * (1 + tol)
