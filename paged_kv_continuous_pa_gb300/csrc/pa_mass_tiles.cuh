@@ -24,12 +24,13 @@
 //
 // The scores are computed twice (a weight needs its column's sum over all
 // keys first): 4 D operations and two exponentials per visible (row, head, key).
-// Eight windows of 64 rows over 4k-16k keys (32 heads over 8): 134 us, of which 62
-// are the statistics' and 70 the weights' (cold, each alone; 43 GFLOP each).  A CTA
-// takes 1800 and 2040 cycles to a step of 128 keys x 128 columns, which needs 512 of
+// Eight windows of 64 rows over 4k-16k keys (32 heads over 8): 134 us with cold
+// caches (127 among other calls), of which 62 to 64 are the statistics' and 70 the
+// weights' (each alone; 43 GFLOP each).  A CTA takes 1850 and 2030 cycles to a step
+// of 128 keys x 128 columns, which needs 512 of
 // the tensor pipe and, at 32 exponentials a cycle, 512 of the special functions'.
-// No unit is busy: tensor pipe 28% and 24%, special functions 30% and 26%, issue
-// slots 40% and 31%.  Bound by latency: three score warps to a scheduler, which
+// No unit is busy: tensor pipe 26% and 24%, special functions 28% and 25%, issue
+// slots 41% and 32%.  Bound by latency: three score warps to a scheduler, which
 // mostly wait for their own results, for S from tensor memory and (weights) at the
 // barriers around the columns' statistics.  One MMA warp for both column tiles took
 // 139 us where two took 121 (inputs in L2); a CTA per unit 147; S buffers of 64
