@@ -249,7 +249,8 @@ pa_status pa_attention_mass(const pa_pool *pool, int32_t n_rows, const void *q, 
  * slots apart).
  *   seq_ids, lengths  int32 [n] in device memory
  *   mass              f32 [num_seqs][num_kv_heads][max_tokens], as pa_attention_mass
- *                     fills it with max_tokens = max_blocks_per_seq * page_size
+ *                     fills it with max_tokens = max_blocks_per_seq * page_size; weights that
+ *                     another stream changes during the call leave a row's choice unspecified
  *   keep              int32 [n][num_kv_heads][budget], written whole
  *   kept_lengths      int32 [n], receives count (may be NULL; may be neither `lengths` nor `seq_ids`)
  * keep_first + keep_last <= budget; max_tokens <= 2^30.  One launch, no workspace; graph-capturable.

@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
         } else if (held <= 32) {
           // few enough to rank by counting, in every warp
           each_key([&](uint32_t key) {
-            if (key >= lo && key < hi) sm.bins[atomicAdd(&sm.gathered, 1)] = key;  // (the bins are read: room for 32)
+            // (the bins are read: room for 32, which weights that change during the call could pass)
+            if (key >= lo && key < hi) sm.bins[min(atomicAdd(&sm.gathered, 1), 32)] = key;
           });
           __syncthreads();
           const uint32_t key = lane < held ? sm.bins[lane] : 0u;
@@ -447,6 +448,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_kernel(const _
     const uint32_t kept_now = all_g + min(tie_base + all_e, ties) - min(tie_base, ties);
     kept_base += kept_now;
     tie_base += all_e;
+    // no more than the budget is marked, unless the weights change between the passes: then nothing is written behind it
+    if (kept_base > static_cast<uint32_t>(p.budget)) return;
     __syncthreads();
     if (kept_now > static_cast<uint32_t>(groups) * 16) {
       // many stay: a group to a warp, four tokens to a lane, whose stores lie together

@@ -371,3 +371,25 @@ def test_compact_lists_out_of_order(start, copy):
     want = torch.zeros_like(old_mass[0, :, :n])
     want[:, :budget] = torch.where(moved, old_mass[0][:, at], torch.zeros_like(old_mass[0][:, at]))
     assert torch.equal(mass[dst, :, :n], want)
+
+
+def test_weights_that_change_during_the_call():
+    """Another stream rewrites the weights while they are chosen from: which tokens come out is unspecified, but
+    nothing is written outside the rows of the call."""
+    n, T, budget = 32, 40000, 3000
+    mass = weights((n, 4, T), "ties", 9).cuda()
+    other = weights((n, 4, T), "spread", 10).cuda()
+    room = torch.full((2 * n, 4, budget), -7, dtype=torch.int32, device="cuda")
+    keep, slots, lengths = room[::2], ints(list(range(n))), ints([T] * n)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(30):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                mass.copy_(other)
+                mass.mul_(0.5).round_()
+        for k in range(n):  # a row of `room` each, with untouched ones between
+            pa.evict_select(mass, slots[k:k + 1], lengths[k:k + 1], keep[k:k + 1], keep_first=4, keep_last=64)
+    torch.cuda.synchronize()
+    assert (room[1::2] == -7).all()
+    assert ((keep == -7) | ((keep >= 0) & (keep < T))).all()  # (or not written)
