@@ -421,8 +421,9 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const __grid_c
     for (int c0 = 0; c0 < per_row; c0 += 32) {
       const uint64_t key = c0 + lane < per_row ? keys[c0 + lane] : 0ull;
       const unsigned in = __ballot_sync(0xffffffffu, key >= bound);
-      if (key >= bound) cand[n + __popc(in & ((1u << lane) - 1u))] = key;
-      n += __popc(in);
+      const int at = n + __popc(in & ((1u << lane) - 1u));
+      if (key >= bound && at < 2 * K) cand[at] = key;
+      n = min(n + __popc(in), 2 * K);  // (2 n_out at most, unless another call writes this workspace)
     }
     __syncwarp();
     for (int c = lane; c < n; c += 32) {

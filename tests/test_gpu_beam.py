@@ -374,3 +374,25 @@ def test_scores_in_place(b):
     pa.beam_select(logits, scores, parents, tokens, scores, workspace=ws)
     torch.cuda.synchronize()
     assert torch.equal(parents.cpu(), want[0]) and torch.equal(tokens.cpu(), want[1]) and torch.equal(scores, apart)
+
+
+def test_calls_that_share_a_workspace():
+    """Ruled out where they overlap, and their results unspecified: but nothing else is touched, and the next call is right."""
+    n, b, out = 16, 6, 12
+    sizes, streams = (40001, 300, 9001), [torch.cuda.Stream() for _ in range(3)]
+    ws = torch.empty(max(pa.beam_workspace_bytes(n, b, v, out) for v in sizes), dtype=torch.uint8, device="cuda").fill_(0xA5)
+    jobs, room = [], torch.full((3, 3, 3, n, out), -7, dtype=torch.int32, device="cuda")
+    for i, v in enumerate(sizes):
+        logits, scores = make(n, b, v, seed=50 + i, std=0.0 if i == 1 else 2.0)
+        jobs.append((logits, scores, room[i, 1, 0], room[i, 1, 1], room[i, 1, 2].view(torch.float32)))
+    torch.cuda.synchronize()
+    for _ in range(60):
+        for s, job in zip(streams, jobs):
+            pa.beam_select(*job, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert (room[:, 0] == -7).all() and (room[:, 2] == -7).all()
+    for logits, scores, parents, tokens, got in jobs:
+        want = reference(logits, scores, out)
+        pa.beam_select(logits, scores, parents, tokens, got, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(parents.cpu(), want[0]) and torch.equal(tokens.cpu(), want[1])
