@@ -62,7 +62,7 @@ typedef enum {
     PA_ERR_NO_PAGES = 6     /* host-side: an admission needs more free pages than the pool has */
 } pa_status;
 
-typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
+typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
 
 /* Pool geometry.  page_size in {16, 32, 64, 128, 256}; head_dim in {64, 128};
  * kv_dtype PA_F32, PA_BF16 or PA_FP8_E4M3.  k_scale / v_scale are the fp8
@@ -103,6 +103,26 @@ size_t pa_pool_bytes(const pa_pool_desc *desc);
  * head_dim outside the supported sets). */
 pa_status pa_pool_create(const pa_pool_desc *desc, void *k_pool, void *v_pool, pa_pool **out);
 
+/* A pool of 4-bit codes.  Every token of a kv head has its own range, for K and for V:
+ *     value(c) = step * c + low,  c = 0..15,  one binary32 multiply-add
+ * and storing the head_dim elements x of one token and kv head takes, with x clamped to
+ * +-65504 and every step one rounding to nearest even,
+ *     low  = f16(min x)
+ *     step = f16(max((max x - low) / 15, 0))      (binary32 subtraction and division)
+ *     c    = clamp(rint((x - low) / step), 0, 15) (the same; 0 where step is 0)
+ * A row that holds a NaN gets low = step = NaN and reads as NaN.
+ *   desc      kv_dtype PA_INT4; k_scale and v_scale are ignored
+ *   k_codes, v_codes    [num_pages][Hkv][P][D / 2] bytes, pa_pool_bytes(desc) each, 16-byte
+ *                       aligned: element 2i in the low, 2i + 1 in the high four bits of byte i
+ *   k_ranges, v_ranges  [num_pages][Hkv][P][2] f16 (step, low), pa_pool_range_bytes(desc) each,
+ *                       16-byte aligned
+ * Such a pool is taken by pa_append_kv, pa_rope_append, pa_read_kv, pa_attention, pa_step and
+ * pa_attention_noalloc; pa_attention_mass, pa_evict_compact and pa_beam_reorder
+ * refuse it with PA_ERR_UNSUPPORTED.  Errors as for pa_pool_create. */
+size_t pa_pool_range_bytes(const pa_pool_desc *desc);
+pa_status pa_pool_create_int4(const pa_pool_desc *desc, void *k_codes, void *v_codes, void *k_ranges, void *v_ranges,
+                              pa_pool **out);
+
 /* Free the host object (not the device buffers).  NULL is allowed. */
 void pa_pool_destroy(pa_pool *pool);
 
@@ -133,6 +153,18 @@ pa_status pa_append_kv(const pa_pool *pool, int32_t n_rows, const void *k_new, c
                        pa_dtype in_dtype, const int32_t *seq_ids, const int32_t *positions,
                        const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
                        int32_t *status_dev, void *stream);
+
+/* The cached K and V of tokens, as dense rows: the counterpart of pa_append_kv, for every
+ * pool type.  Row r, kv head h and element d:
+ *     out[r][h][d] = value(pool[block_tables[s][p / P]][h][p % P][d]),  s = seq_ids[r], p = positions[r]
+ * the value that the stored element stands for (fp8 and 4-bit pools: scaled), computed in
+ * binary32 and rounded once to out_dtype, PA_F32 or PA_BF16.
+ *   k_out, v_out  [n_rows][Hkv][D], 16-byte aligned; either may be NULL
+ * A row may be listed more than once.  n_rows == 0 is a no-op.  One launch; graph-capturable.
+ * Device-side: a row that pa_append_kv would skip gets zeros and records PA_ERR_OUT_OF_RANGE. */
+pa_status pa_read_kv(const pa_pool *pool, int32_t n_rows, const int32_t *seq_ids, const int32_t *positions,
+                     const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq, void *k_out,
+                     void *v_out, pa_dtype out_dtype, int32_t *status_dev, void *stream);
 
 /* Workspace bytes pa_attention needs for these rows, this block-table width
  * and these prefill chunks (the split-KV partial triples of decode rows and of
@@ -201,6 +233,154 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
                   const int32_t *positions, const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
                   const pa_chunk *chunks, int32_t n_chunks, float softmax_scale, void *out, void *workspace,
                   size_t workspace_bytes, int32_t *status_dev, void *stream);
+
+/* Rotary positions.  The first rotary_dim elements of a head are pairs; pair i of a row at
+ * position p turns by the angle p * f_i and is scaled by `magnitude`:
+ *     (a, b) -> magnitude * (a cos - b sin, a sin + b cos)
+ * The elements behind rotary_dim stay.  PA_ROPE_HALF pairs elements i and i + rotary_dim / 2,
+ * PA_ROPE_INTERLEAVED elements 2i and 2i + 1.  f_i = base^(-2i / rotary_dim), changed for
+ * contexts longer than the `original_positions` that the weights know:
+ *   PA_ROPE_LINEAR  f_i / factor
+ *   PA_ROPE_BASE    with base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *   PA_ROPE_RAMP    f_i / factor for pairs that turn fewer than `low` times over the original
+ *                   positions, f_i for those that turn more than `high` times, and a linear ramp
+ *                   over the pair index between (the indices at which a pair turns t times,
+ *                   rotary_dim ln(original_positions / (2 pi t)) / (2 ln base), rounded outwards
+ *                   and kept within 0 .. rotary_dim - 1); magnitude 0 stands for 0.1 ln(factor) + 1
+ *   PA_ROPE_BANDS   the same ends, with t_i = original_positions f_i / (2 pi) turns and the weight
+ *                   (t_i - low) / (high - low), clamped to 0..1, on f_i
+ * Angles are exact for every int32 position: f_i / 2 pi is held as a 64-bit fraction of a turn,
+ * and p * f_i is taken modulo whole turns in integers.  Sines, cosines and products are FP32. */
+typedef enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
+typedef enum { PA_ROPE_NONE = 0, PA_ROPE_LINEAR = 1, PA_ROPE_BASE = 2, PA_ROPE_RAMP = 3, PA_ROPE_BANDS = 4 } pa_rope_scaling;
+typedef struct {
+    int32_t rotary_dim;          /* even, 2..128 */
+    pa_rope_layout layout;
+    double base;                 /* > 1 */
+    pa_rope_scaling scaling;
+    double factor;               /* > 0 (ignored by PA_ROPE_NONE) */
+    int32_t original_positions;  /* > 0 (PA_ROPE_RAMP and PA_ROPE_BANDS) */
+    double low, high;            /* 0 < low < high (the same two) */
+    double magnitude;            /* 0: 1, or PA_ROPE_RAMP's; otherwise > 0 */
+} pa_rope_desc;
+typedef struct pa_rope pa_rope; /* opaque host object, unchanged after its creation */
+
+/* Errors: PA_ERR_INVALID_ARG (a number outside the ranges above, PA_ROPE_BASE with
+ * rotary_dim 2).  pa_rope_frequencies copies f_i (rotary_dim / 2 numbers, radians per
+ * position) and the magnitude, either of which may be NULL. */
+pa_status pa_rope_create(const pa_rope_desc *desc, pa_rope **out);
+void pa_rope_destroy(pa_rope *rope);
+pa_status pa_rope_frequencies(const pa_rope *rope, double *frequencies, double *magnitude);
+
+/* Rotate rows: out[r][h] = rotated x[r][h] at positions[r].
+ *   x, out       [n_rows][n_heads][head_dim] of dtype (PA_F32 or PA_BF16), 16-byte aligned; a
+ *                row's heads are contiguous, rows x_stride / out_stride elements apart (a
+ *                multiple of 16 bytes, at least n_heads * head_dim).  out may be x (with its
+ *                stride); otherwise they do not overlap
+ *   head_dim     64 or 128, at least rotary_dim
+ *   positions    any int32: a negative one turns back
+ *   inverse      non-zero: the transposed map, magnitude * (a cos + b sin, b cos - a sin): the
+ *                gradient of x from the gradient of out
+ * One launch; graph-capturable. */
+pa_status pa_rope_rows(const pa_rope *rope, int32_t n_rows, const void *x, int64_t x_stride, void *out,
+                       int64_t out_stride, pa_dtype dtype, int32_t n_heads, int32_t head_dim, const int32_t *positions,
+                       int32_t inverse, void *stream);
+
+/* A step's projections taken in: queries rotated into q_out, keys rotated and stored in
+ * their page slots, values stored, in one launch (in place of pa_rope_rows for q and k and
+ * pa_append_kv).  Keys are stored from the FP32 result: an f32 or bf16 pool gets it rounded once, an
+ * fp8 or 4-bit pool its code.  Values are stored as pa_append_kv stores them.
+ *   q            [n_rows][num_q_heads][D], k, v [n_rows][Hkv][D] of dtype (PA_F32 or PA_BF16); rows
+ *                q_stride, k_stride, v_stride elements apart as for pa_rope_rows (the three may be
+ *                parts of one packed projection)
+ *   q_out        [n_rows][num_q_heads][D], contiguous; may be q where q_stride is num_q_heads * D
+ *   num_q_heads  any number >= 0 (0: q and q_out are not read)
+ *   rope         its rotary_dim at most the pool's head_dim; NULL: nothing is rotated
+ *   the other arguments and preconditions: as pa_append_kv
+ * Device-side: a row with an invalid sequence, position or page stores nothing, leaves its
+ * q_out as it was and records PA_ERR_OUT_OF_RANGE. */
+pa_status pa_rope_append(const pa_pool *pool, const pa_rope *rope, int32_t n_rows, const void *q, int64_t q_stride,
+                         int32_t num_q_heads, void *q_out, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, pa_dtype dtype, const int32_t *seq_ids, const int32_t *positions,
+                         const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t *status_dev,
+                         void *stream);
+
+/* Causal attention over whole prompts, packed one behind the other, before or beside their
+ * append: no cache is read.  For token i of sequence s (rows row_starts[s] .. row_starts[s + 1] - 1)
+ * and query head g,
+ *     out[i][g] = softmax_j(scale * q[i][g] . k[j][g / (Hq / Hkv)]) . v[j][g / (Hq / Hkv)],  j <= i of the same sequence
+ *   q            [n_rows][Hq][D], k, v [n_rows][Hkv][D], PA_BF16, rows q_stride, k_stride, v_stride
+ *                elements apart (multiples of 8, at least a row), heads contiguous, 16-byte aligned
+ *   out          [n_rows][Hq][D] contiguous, PA_BF16; rows behind the last sequence (and any
+ *                before the first) are left as they were.  It overlaps no input
+ *   lse          f32 [n_rows][Hq] or NULL: the natural logarithm of the sum of a row's exponentials
+ *                (to join the result with that over a cached prefix)
+ *   row_starts   int32 [n_seqs + 1] in device memory, ascending, within 0..n_rows; a sequence may
+ *                be empty
+ *   num_q_heads  a multiple of num_kv_heads, any group size; head_dim 64 or 128
+ *   softmax_scale <= 0 selects 1 / sqrt(head_dim)
+ *   workspace    pa_prompt_workspace_bytes(...) bytes, 256-byte aligned; scratch that each call
+ *                writes before it reads it.  Calls that share one must not overlap on the GPU
+ * Scores, sums and accumulators are FP32; a softmax weight enters its product with V as bf16.
+ * What masked keys and values hold (infinities and NaN too, other sequences' rows too) has no
+ * influence.  An infinite value that a row attends to gives that element +-infinity, or NaN.
+ * A row's bits depend on its own sequence alone.  Two launches, the second a programmatic
+ * dependent of the first; graph-capturable.
+ * Errors: PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED (dtype PA_F32, head_dim), PA_ERR_CUDA.
+ * Device-side: row_starts that descend or leave 0..n_rows compute nothing and record
+ * PA_ERR_OUT_OF_RANGE; a wait that ran out records PA_ERR_TIMEOUT and leaves out unspecified. */
+size_t pa_prompt_workspace_bytes(int32_t n_rows, int32_t n_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim);
+pa_status pa_prompt_attention(int32_t n_rows, int32_t n_seqs, const void *q, int64_t q_stride, const void *k,
+                              int64_t k_stride, const void *v, int64_t v_stride, pa_dtype dtype, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, const int32_t *row_starts, float softmax_scale,
+                              void *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *status_dev,
+                              void *stream);
+
+/* Block tables and the rows of a step, made on the GPU (no host copy of the tables, so a
+ * captured loop can run it).  The free pages of the pool are a stack in device memory:
+ * free_pages[0 .. *free_count - 1], taken from its end.  Request i has lengths[i] tokens
+ * cached in slot seq_ids[i] and takes new_tokens[i] more:
+ *   - its table row gets pages for columns ceil(lengths / P) .. ceil((lengths + new) / P) - 1, in
+ *     request order and then column order the next ones of the stack;
+ *   - its rows are row_starts[i] .. row_starts[i + 1] - 1, at positions lengths[i] .. + new - 1:
+ *     row_seqs, row_positions (the seq_ids and positions of the other calls) and row_slots, the
+ *     token's place page * P + position % P in a pool's [num_pages * P] tokens of a kv head
+ *     (-1: its page is not one of the pool).
+ * Requests are served in order as long as pages and rows suffice: the first that does not fit and
+ * every one behind it get nothing (row_starts stays where it is) and PA_ERR_NO_PAGES is recorded.
+ * A request with an invalid slot, count, length or new length (together more than
+ * max_blocks_per_seq * P), or a slot that is listed twice, takes nothing and PA_ERR_OUT_OF_RANGE is recorded.
+ *   free_pages    int32 [num_pages]; an entry outside [0, num_pages) enters the table as -1
+ *                 and records PA_ERR_OUT_OF_RANGE
+ *   free_count    int32 [1], within 0..num_pages;  free_left  int32 [1], receives what remains (may
+ *                 be free_count)
+ *   row_starts, page_starts  int32 [n + 1], receive the exclusive sums of rows and of pages taken
+ *   row_seqs, row_positions  int32 [max_rows], row_slots int64 [max_rows] (may be NULL); entries behind
+ *                 row_starts[n] are left as they were.  All three may be NULL where max_rows is 0
+ * Outputs overlap no input (but free_left).  The pages of a pool are handed out here or by
+ * pa_pages_*, not by both; pages are not shared between slots.
+ * num_seqs <= 2^19.  One launch for at most 4096 rows, else two, the second a programmatic
+ * dependent of the first; no workspace; graph-capturable. */
+pa_status pa_tables_grow(int32_t n, const int32_t *seq_ids, const int32_t *lengths, const int32_t *new_tokens,
+                         const int32_t *free_pages, const int32_t *free_count, int32_t *free_left, int32_t num_pages,
+                         int32_t page_size, int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
+                         int32_t *row_starts, int32_t *page_starts, int32_t max_rows, int32_t *row_seqs,
+                         int32_t *row_positions, int64_t *row_slots, int32_t *status_dev, void *stream);
+
+/* Give pages back to the stack: slot seq_ids[i] holds lengths[i] tokens and keeps the first
+ * keep_tokens[i] (NULL: none).  The pages of columns ceil(keep / P) .. ceil(lengths / P) - 1 go on
+ * the stack, the last request's last column first, so that a pa_tables_grow that asks for the
+ * same again gets the same pages, and their table entries become -1.  A request with an invalid
+ * slot or length, a slot that is listed twice, or an invalid page in those columns gives nothing back and
+ * records PA_ERR_OUT_OF_RANGE; so does the whole call where the stack would hold more than
+ * num_pages.  keep_tokens beyond lengths keeps everything.
+ *   free_count    int32 [1], the stack's height, changed in place
+ * num_seqs <= 2^19.  One launch of one CTA; no workspace; graph-capturable. */
+pa_status pa_tables_release(int32_t n, const int32_t *seq_ids, const int32_t *lengths, const int32_t *keep_tokens,
+                            int32_t *free_pages, int32_t *free_count, int32_t num_pages, int32_t page_size,
+                            int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t *status_dev,
+                            void *stream);
 
 /* Attention weight per cached key: what eviction by accumulated attention
  * looks at.  For row r with sequence s and position p, kv head h and the G

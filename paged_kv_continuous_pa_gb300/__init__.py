@@ -19,7 +19,9 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "pa.h")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_OUT_OF_RANGE, PA_ERR_TIMEOUT, PA_ERR_CUDA, PA_ERR_NO_PAGES = range(7)
 PA_ADMIT_OK, PA_ADMIT_NO_PAGES, PA_ADMIT_TOO_LONG, PA_ADMIT_SEQ_IN_USE, PA_ADMIT_BAD_ARG = range(5)
-PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
+PA_F32, PA_BF16, PA_FP8_E4M3, PA_INT4 = 0, 1, 2, 3
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 PA_ORDER_AUTO, PA_ORDER_CALL, PA_ORDER_LONGEST_FIRST = 0, 1, 2
 
 _lib = None
@@ -40,6 +42,12 @@ class PoolDesc(ctypes.Structure):
 
 class Chunk(ctypes.Structure):
     _fields_ = [("row_begin", ctypes.c_int32), ("n_rows", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int), ("base", ctypes.c_double),
+                ("scaling", ctypes.c_int), ("factor", ctypes.c_double), ("original_positions", ctypes.c_int32),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 
 class AdmitInfo(ctypes.Structure):
@@ -104,6 +112,31 @@ def load(path: str = LIB_PATH):
         L.pa_beam_select.restype = st
         L.pa_beam_reorder.argtypes = [vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, sz, vp, vp]
         L.pa_beam_reorder.restype = st
+        L.pa_pool_range_bytes.argtypes = [ctypes.POINTER(PoolDesc)]
+        L.pa_pool_range_bytes.restype = sz
+        L.pa_pool_create_int4.argtypes = [ctypes.POINTER(PoolDesc), vp, vp, vp, vp, ctypes.POINTER(vp)]
+        L.pa_pool_create_int4.restype = st
+        L.pa_read_kv.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, vp, i32, vp, vp]
+        L.pa_read_kv.restype = st
+        L.pa_rope_create.argtypes = [ctypes.POINTER(RopeDesc), ctypes.POINTER(vp)]
+        L.pa_rope_create.restype = st
+        L.pa_rope_destroy.argtypes = [vp]
+        L.pa_rope_destroy.restype = None
+        L.pa_rope_frequencies.argtypes = [vp, vp, vp]
+        L.pa_rope_frequencies.restype = st
+        L.pa_rope_rows.argtypes = [vp, i32, vp, i64, vp, i64, i32, i32, i32, vp, i32, vp]
+        L.pa_rope_rows.restype = st
+        L.pa_rope_append.argtypes = [vp, vp, i32, vp, i64, i32, vp, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, vp, vp]
+        L.pa_rope_append.restype = st
+        L.pa_prompt_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.pa_prompt_workspace_bytes.restype = sz
+        L.pa_prompt_attention.argtypes = [i32, i32, vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, vp, f32, vp, vp, vp,
+                                          sz, vp, vp]
+        L.pa_prompt_attention.restype = st
+        L.pa_tables_grow.argtypes = [i32, vp, vp, vp, vp, vp, vp, i32, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp]
+        L.pa_tables_grow.restype = st
+        L.pa_tables_release.argtypes = [i32, vp, vp, vp, vp, vp, i32, i32, vp, i32, i32, vp, vp]
+        L.pa_tables_release.restype = st
         L.pa_pages_trim.argtypes = [vp, i32, i32, vp]
         L.pa_pages_trim.restype = st
         L.pa_pages_needed.argtypes = [i32, i32, i32]
@@ -232,14 +265,23 @@ def pool_bytes(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
 class Pool:
     """A paged K/V pool over two caller-owned device tensors [num_pages, Hkv, P, D]."""
 
-    def __init__(self, k_pool, v_pool, k_scale=1.0, v_scale=1.0):
-        """k_scale / v_scale: fp8 scales, one float (per tensor) or one per kv head."""
+    def __init__(self, k_pool, v_pool, k_scale=1.0, v_scale=1.0, k_ranges=None, v_ranges=None):
+        """k_scale / v_scale: fp8 scales, one float (per tensor) or one per kv head.
+        k_ranges / v_ranges: a 4-bit pool, its codes uint8 [num_pages, Hkv, P, D / 2] and
+        the (step, low) pairs float16 [num_pages, Hkv, P, 2] of every token and kv head."""
         import numpy as np
+        import torch
         if k_pool.shape != v_pool.shape or k_pool.dim() != 4 or k_pool.dtype != v_pool.dtype:
             raise ValueError("k_pool and v_pool must be matching [num_pages, Hkv, P, D] tensors")
         self.k_pool, self.v_pool = k_pool, v_pool
+        self.k_ranges, self.v_ranges = k_ranges, v_ranges
         n, h, p, d = k_pool.shape
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = int(n), int(h), int(p), int(d)
+        if (k_ranges is None) != (v_ranges is None):
+            raise ValueError("give k_ranges and v_ranges, or neither")
+        if k_ranges is not None:
+            self._create_int4(torch)
+            return
         self.kv_dtype = _dtype_code(k_pool)
         per_head = np.ndim(k_scale) > 0 or np.ndim(v_scale) > 0
         self.k_scale = np.asarray(k_scale, np.float32) if per_head else float(k_scale)
@@ -254,6 +296,20 @@ class Pool:
             vs = np.ascontiguousarray(np.broadcast_to(self.v_scale, (self.num_kv_heads,)), np.float32)
             _check(load().pa_pool_set_head_scales(self._h, ks.ctypes.data_as(ctypes.c_void_p),
                                                   vs.ctypes.data_as(ctypes.c_void_p)))
+
+    def _create_int4(self, torch):
+        if self.k_pool.dtype != torch.uint8:
+            raise TypeError(f"4-bit codes must be uint8, got {self.k_pool.dtype}")
+        want = (self.num_pages, self.num_kv_heads, self.page_size, 2)
+        self.head_dim *= 2
+        self.kv_dtype, self.k_scale, self.v_scale = PA_INT4, 1.0, 1.0
+        _, (kp, vp, kr, vr) = _tensors((
+            (self.k_pool, "k_pool", None, None), (self.v_pool, "v_pool", None, None),
+            (self.k_ranges, "k_ranges", torch.float16, want), (self.v_ranges, "v_ranges", torch.float16, want)))
+        self.desc = PoolDesc(self.num_pages, self.page_size, self.num_kv_heads, self.head_dim, self.kv_dtype, 1.0, 1.0)
+        handle = ctypes.c_void_p()
+        _check(load().pa_pool_create_int4(ctypes.byref(self.desc), kp, vp, kr, vr, ctypes.byref(handle)))
+        self._h = handle
 
     @property
     def handle(self):
@@ -566,6 +622,195 @@ def beam_reorder(pool: Pool, parents, seq_ids, lengths, block_tables, state=None
         (status, "status", torch.int32, None)))
     _call(load().pa_beam_reorder, device, stream, pool.handle, groups, beams, sp, pp, lp, tp, num_seqs, max_blocks, xp,
           row_bytes, stp)
+
+
+def _row_view(t, name: str):
+    """(n, heads, D, elements from row to row) of rows whose heads are contiguous: a
+    [n, heads, D] tensor, or a part of the heads of a packed projection."""
+    n, heads, d = _dims(t, name, "n, heads, D")
+    across, down, along = t.stride()
+    if (d > 1 and along != 1) or (heads > 1 and down != d):
+        raise ValueError(f"{name} must have contiguous heads in each row")
+    return n, heads, d, across if n > 1 else heads * d
+
+
+def _same_device(device: int, *tensors):
+    for t, name in tensors:
+        if t.get_device() != device or device < 0:
+            raise ValueError(f"{name} and the other tensors of the call must live on one CUDA device")
+
+
+class Rope:
+    """Rotary positions: the frequencies of rotary_dim / 2 pairs of a head."""
+
+    def __init__(self, rotary_dim: int, layout: str = "half", base: float = 10000.0, scaling: Optional[str] = None,
+                 factor: float = 1.0, original_positions: int = 0, low: Optional[float] = None,
+                 high: Optional[float] = None, magnitude: float = 0.0):
+        """layout: "half" (elements i and i + rotary_dim / 2) or "interleaved" (2i and 2i + 1).
+        scaling: None, "linear", "base", "ramp" or "bands", with factor and, for the last
+        two, original_positions and the turns low < high between which a pair's frequency
+        changes over (1 and 32 for "ramp", 1 and 4 for "bands")."""
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout {layout!r} is not one of {sorted(ROPE_LAYOUTS)}")
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling {scaling!r} is not one of {list(ROPE_SCALINGS)}")
+        low = 1.0 if low is None else low
+        high = (32.0 if scaling == "ramp" else 4.0) if high is None else high
+        self.rotary_dim = _int32(rotary_dim, "rotary_dim")
+        desc = RopeDesc(self.rotary_dim, ROPE_LAYOUTS[layout], float(base), ROPE_SCALINGS[scaling], float(factor),
+                        _int32(original_positions, "original_positions"), float(low), float(high), float(magnitude))
+        handle = ctypes.c_void_p()
+        _check(load().pa_rope_create(ctypes.byref(desc), ctypes.byref(handle)))
+        self.handle = handle
+
+    def frequencies(self):
+        """(numpy float64 [rotary_dim / 2] radians per position, the magnitude)."""
+        import numpy as np
+        f, m = np.zeros(self.rotary_dim // 2), ctypes.c_double()
+        _check(load().pa_rope_frequencies(self.handle, f.ctypes.data_as(ctypes.c_void_p),
+                                          ctypes.cast(ctypes.byref(m), ctypes.c_void_p)))
+        return f, m.value
+
+    def __del__(self):
+        try:
+            if _lib is not None and getattr(self, "handle", None):
+                _lib.pa_rope_destroy(self.handle)
+        except Exception:
+            pass
+
+
+def rope_rows(rope: Rope, x, positions, out=None, inverse: bool = False, stream=None):
+    """Rotate rows x [n, heads, D] (f32|bf16, a packed projection's part allowed) at positions
+    int32 [n] into out (default: x itself); inverse: the transposed rotation."""
+    import torch
+    out = x if out is None else out
+    n, heads, d, x_stride = _row_view(x, "x")
+    if tuple(out.shape) != (n, heads, d) or out.dtype != x.dtype:
+        raise ValueError("out must match x's shape and dtype")
+    out_stride = _row_view(out, "out")[3]
+    device, (pp,) = _tensors(((positions, "positions", torch.int32, (n,)),))
+    _same_device(device, (x, "x"), (out, "out"))
+    _call(load().pa_rope_rows, device, stream, rope.handle, n, x.data_ptr(), x_stride, out.data_ptr(), out_stride,
+          _dtype_code(x), heads, d, pp, 1 if inverse else 0)
+
+
+def rope_append(pool: Pool, rope: Optional[Rope], q, k_new, v_new, seq_ids, positions, block_tables, q_out, status=None,
+                stream=None):
+    """Queries q [n, Hq, D] rotated into q_out, keys rotated and values stored in their page
+    slots (one launch).  q, k_new and v_new may be parts of one packed projection; rope
+    None rotates nothing, q and q_out None take in keys and values alone."""
+    import torch
+    n, heads, d, k_stride = _row_view(k_new, "k_new")
+    if (heads, d) != (pool.num_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new and v_new must be [n, {pool.num_kv_heads}, {pool.head_dim}]")
+    v_stride = _row_view(v_new, "v_new")[3]
+    if v_new.dtype != k_new.dtype or (q is not None and q.dtype != k_new.dtype):
+        raise ValueError("q, k_new and v_new must share a dtype")
+    hq = q_stride = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("give q and q_out, or neither")
+    if q is not None:
+        qn, hq, qd, q_stride = _row_view(q, "q")
+        if (qn, qd) != (n, d):
+            raise ValueError(f"q has shape {tuple(q.shape)}; expected [{n}, Hq, {d}]")
+    num_seqs, max_blocks = _dims(block_tables, "block_tables", "num_seqs, max_blocks")
+    device, (kp, sp, pp, tp, op, stp) = _tensors((
+        (pool.k_pool, "pool", None, None), (seq_ids, "seq_ids", torch.int32, (n,)),
+        (positions, "positions", torch.int32, (n,)), (block_tables, "block_tables", torch.int32, None),
+        (q_out, "q_out", k_new.dtype, (n, hq, d)), (status, "status", torch.int32, None)))
+    _same_device(device, (k_new, "k_new"), (v_new, "v_new"), *(((q, "q"),) if q is not None else ()))
+    _call(load().pa_rope_append, device, stream, pool.handle, rope.handle if rope is not None else None, n,
+          q.data_ptr() if q is not None else None, q_stride, hq, op, k_new.data_ptr(), k_stride, v_new.data_ptr(),
+          v_stride, _dtype_code(k_new), sp, pp, tp, num_seqs, max_blocks, stp)
+
+
+def read_kv(pool: Pool, seq_ids, positions, block_tables, k_out=None, v_out=None, status=None, stream=None):
+    """The cached K and V of tokens (seq_ids, positions int32 [n]) as dense rows
+    [n, Hkv, D], f32 or bf16: the values that the stored elements stand for."""
+    import torch
+    (n,) = _dims(seq_ids, "seq_ids", "n")
+    out = k_out if k_out is not None else v_out
+    if out is None:
+        raise ValueError("give k_out, v_out or both")
+    num_seqs, max_blocks = _dims(block_tables, "block_tables", "num_seqs, max_blocks")
+    rows = (n, pool.num_kv_heads, pool.head_dim)
+    device, (kp, sp, pp, tp, ko, vo, stp) = _tensors((
+        (pool.k_pool, "pool", None, None), (seq_ids, "seq_ids", torch.int32, (n,)),
+        (positions, "positions", torch.int32, (n,)), (block_tables, "block_tables", torch.int32, None),
+        (k_out, "k_out", out.dtype, rows), (v_out, "v_out", out.dtype, rows), (status, "status", torch.int32, None)))
+    _call(load().pa_read_kv, device, stream, pool.handle, n, sp, pp, tp, num_seqs, max_blocks, ko, vo, _dtype_code(out),
+          stp)
+
+
+def prompt_workspace_bytes(n_rows: int, n_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes prompt_attention() needs."""
+    return int(load().pa_prompt_workspace_bytes(_int32(n_rows, "n_rows"), _int32(n_seqs, "n_seqs"),
+                                                _int32(num_q_heads, "num_q_heads"), _int32(num_kv_heads, "num_kv_heads"),
+                                                _int32(head_dim, "head_dim")))
+
+
+def prompt_attention(q, k, v, row_starts, out, lse=None, softmax_scale: float = 0.0, workspace=None, status=None,
+                     stream=None):
+    """Causal attention of whole prompts packed one behind the other: q [n, Hq, D], k and v
+    [n, Hkv, D] bf16 (parts of a packed projection allowed), sequence s in rows
+    row_starts[s] .. row_starts[s + 1] - 1 (int32, on the device), into out [n, Hq, D] and,
+    if given, lse f32 [n, Hq]."""
+    import torch
+    n, hq, d, q_stride = _row_view(q, "q")
+    kn, hkv, kd, k_stride = _row_view(k, "k")
+    if (kn, kd) != (n, d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{n}, Hkv, {d}]")
+    v_stride = _row_view(v, "v")[3]
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must share a dtype")
+    (starts,) = _dims(row_starts, "row_starts", "n_seqs + 1")
+    if starts < 1:
+        raise ValueError("row_starts needs n_seqs + 1 entries")
+    device, (rp, op, lp, wp, stp) = _tensors((
+        (row_starts, "row_starts", torch.int32, None), (out, "out", q.dtype, (n, hq, d)),
+        (lse, "lse", torch.float32, (n, hq)), (workspace, "workspace", None, None), (status, "status", torch.int32, None)))
+    _same_device(device, (q, "q"), (k, "k"), (v, "v"))
+    _call(load().pa_prompt_attention, device, stream, n, starts - 1, q.data_ptr(), q_stride, k.data_ptr(), k_stride,
+          v.data_ptr(), v_stride, _dtype_code(q), hq, hkv, d, rp, softmax_scale, op, lp, wp,
+          workspace.nbytes if workspace is not None else 0, stp)
+
+
+def tables_grow(seq_ids, lengths, new_tokens, free_pages, free_count, free_left, page_size: int, block_tables,
+                row_starts, page_starts, row_seqs, row_positions, row_slots=None, status=None, stream=None):
+    """Pages from the stack free_pages[:free_count] into the block tables for new_tokens
+    more tokens of each request, and the rows of the step: seq ids, positions and
+    (optional, int64) token places in the pool.  All int32 on the device."""
+    import torch
+    i32 = torch.int32
+    (n,) = _dims(seq_ids, "seq_ids", "n")
+    (num_pages,) = _dims(free_pages, "free_pages", "num_pages")
+    (rows,) = _dims(row_seqs, "row_seqs", "max_rows")
+    num_seqs, max_blocks = _dims(block_tables, "block_tables", "num_seqs, max_blocks")
+    device, (sp, lp, np_, fp, cp, ep, tp, rsp, psp, qp, pp, op, stp) = _tensors((
+        (seq_ids, "seq_ids", i32, None), (lengths, "lengths", i32, (n,)), (new_tokens, "new_tokens", i32, (n,)),
+        (free_pages, "free_pages", i32, None), (free_count, "free_count", i32, (1,)), (free_left, "free_left", i32, (1,)),
+        (block_tables, "block_tables", i32, None), (row_starts, "row_starts", i32, (n + 1,)),
+        (page_starts, "page_starts", i32, (n + 1,)), (row_seqs, "row_seqs", i32, None),
+        (row_positions, "row_positions", i32, (rows,)), (row_slots, "row_slots", torch.int64, (rows,)),
+        (status, "status", i32, None)))
+    _call(load().pa_tables_grow, device, stream, n, sp, lp, np_, fp, cp, ep, num_pages, _int32(page_size, "page_size"), tp,
+          num_seqs, max_blocks, rsp, psp, rows, qp, pp, op, stp)
+
+
+def tables_release(seq_ids, lengths, free_pages, free_count, page_size: int, block_tables, keep_tokens=None, status=None,
+                   stream=None):
+    """Pages behind each request's first keep_tokens (default: all of them) back onto the stack."""
+    import torch
+    i32 = torch.int32
+    (n,) = _dims(seq_ids, "seq_ids", "n")
+    (num_pages,) = _dims(free_pages, "free_pages", "num_pages")
+    num_seqs, max_blocks = _dims(block_tables, "block_tables", "num_seqs, max_blocks")
+    device, (sp, lp, kp, fp, cp, tp, stp) = _tensors((
+        (seq_ids, "seq_ids", i32, None), (lengths, "lengths", i32, (n,)), (keep_tokens, "keep_tokens", i32, (n,)),
+        (free_pages, "free_pages", i32, None), (free_count, "free_count", i32, (1,)),
+        (block_tables, "block_tables", i32, None), (status, "status", i32, None)))
+    _call(load().pa_tables_release, device, stream, n, sp, lp, kp, fp, cp, num_pages, _int32(page_size, "page_size"), tp,
+          num_seqs, max_blocks, stp)
 
 
 def set_split_tokens(tokens: int):

@@ -216,7 +216,7 @@ pa_status check_desc(const pa_pool_desc* d) {
   if (d->num_pages <= 0 || d->num_kv_heads <= 0 || d->page_size <= 0 || d->head_dim <= 0)
     return fail(PA_ERR_INVALID_ARG, "pool sizes must be positive (pages %d, kv heads %d, page %d, head_dim %d)",
                 d->num_pages, d->num_kv_heads, d->page_size, d->head_dim);
-  if (d->kv_dtype != PA_F32 && d->kv_dtype != PA_BF16 && d->kv_dtype != PA_FP8_E4M3)
+  if (d->kv_dtype != PA_F32 && d->kv_dtype != PA_BF16 && d->kv_dtype != PA_FP8_E4M3 && d->kv_dtype != PA_INT4)
     return fail(PA_ERR_INVALID_ARG, "unknown kv dtype %d", static_cast<int>(d->kv_dtype));
   if (d->page_size < 16 || d->page_size > 256 || (d->page_size & (d->page_size - 1)) != 0)
     return fail(PA_ERR_UNSUPPORTED, "page_size %d not in {16, 32, 64, 128, 256}", d->page_size);
@@ -251,6 +251,27 @@ pa_status pa::encode_query_map(CUtensorMap* map, const void* q, int32_t n_rows, 
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = encode_with_context([&] {
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
+  if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return PA_OK;
+}
+
+pa_status pa::encode_map_16bit(CUtensorMap* map, const void* base, int rank, const int64_t* dims, const int64_t* strides,
+                               const uint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], one[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = box[i];
+    one[i] = 1;
+    if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i]) * 2;
+  }
+  const CUresult r = encode_with_context([&] {
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, b, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   });
@@ -318,6 +339,8 @@ pa_status build_append(const pa_pool* pool, int32_t n_rows, const void* k_new, c
   pa::AppendParams p{};
   p.k_pool = pool->k;
   p.v_pool = pool->v;
+  p.k_ranges = pool->k_ranges;
+  p.v_ranges = pool->v_ranges;
   p.k_new = k_new;
   p.v_new = v_new;
   p.seq_ids = seq_ids;
@@ -394,6 +417,8 @@ pa_status attention_impl(const pa_pool* pool, int32_t n_rows, const void* q, pa_
   pa::AttnParams p{};
   p.k_pool = pool->k;
   p.v_pool = pool->v;
+  p.k_ranges = pool->k_ranges;
+  p.v_ranges = pool->v_ranges;
   p.q = q;
   p.out = out;
   p.seq_ids = seq_ids;
@@ -514,7 +539,13 @@ pa_status attention_impl(const pa_pool* pool, int32_t n_rows, const void* q, pa_
       if (e != cudaSuccess) return cuda_fail(e, "pa_attention_noalloc: clearing the tile counters");
     }
   }
-  if (pre != nullptr) {
+  if (pre != nullptr && d.kv_dtype == PA_INT4) {
+    // a 4-bit token is stored with its range, found over the whole row: every row
+    // is appended first, and the attention depends on that launch
+    const cudaError_t ea = pa::launch_append(*pre, s);
+    if (ea != cudaSuccess) return cuda_fail(ea, "append launch");
+    p.dependent = 1;
+  } else if (pre != nullptr) {
     // pa_step: rows outside the chunks append their own K/V inside the
     // attention launch (each is its sequence's only row in the step); the
     // chunks' rows, which read one another's keys, are appended first by a
@@ -566,6 +597,7 @@ pa_status attention_impl(const pa_pool* pool, int32_t n_rows, const void* q, pa_
     switch (d.kv_dtype) {
       case PA_F32: e = pa::launch_decode_f32(p, s); break;
       case PA_BF16: e = pa::launch_decode_bf16(p, s); break;
+      case PA_INT4: e = pa::launch_decode_int4(p, s); break;
       default: e = pa::launch_decode_e4m3(p, s); break;
     }
   }
@@ -586,12 +618,52 @@ pa_status pa::attention_fixed_scratch(const pa_pool* pool, int32_t n_rows, const
                         nullptr, &scratch);
 }
 
+namespace {
+
+pa_status make_pool(const pa_pool_desc* desc, void* k, void* v, void* k_ranges, void* v_ranges, pa_pool** out) {
+  const bool int4 = desc->kv_dtype == PA_INT4;
+  if (k == nullptr || v == nullptr || (int4 && (k_ranges == nullptr || v_ranges == nullptr)))
+    return fail(PA_ERR_INVALID_ARG, "pool buffers must not be NULL");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_ranges, 16) || !aligned(v_ranges, 16))
+    return fail(PA_ERR_INVALID_ARG, "pool buffers must be 16-byte aligned");
+  pa_pool* p = new (std::nothrow) pa_pool;
+  if (p == nullptr) return fail(PA_ERR_INVALID_ARG, "out of host memory");
+  p->desc = *desc;
+  if (p->desc.kv_dtype != PA_FP8_E4M3) p->desc.k_scale = p->desc.v_scale = 1.0f;
+  p->head_scales = false;
+  p->k = k;
+  p->v = v;
+  p->k_ranges = k_ranges;
+  p->v_ranges = v_ranges;
+  p->tile_maps_ready = false;
+  p->dec_maps_ready = false;
+  *out = p;
+  return PA_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t pa_pool_bytes(const pa_pool_desc* desc) {
   if (check_desc(desc) != PA_OK) return 0;
-  return static_cast<size_t>(desc->num_pages) * desc->num_kv_heads * desc->page_size * desc->head_dim *
-         elt_bytes(desc->kv_dtype);
+  const size_t elements = static_cast<size_t>(desc->num_pages) * desc->num_kv_heads * desc->page_size * desc->head_dim;
+  return desc->kv_dtype == PA_INT4 ? elements / 2 : elements * elt_bytes(desc->kv_dtype);
+}
+
+size_t pa_pool_range_bytes(const pa_pool_desc* desc) {
+  if (check_desc(desc) != PA_OK || desc->kv_dtype != PA_INT4) return 0;
+  return static_cast<size_t>(desc->num_pages) * desc->num_kv_heads * desc->page_size * 4;
+}
+
+pa_status pa_pool_create_int4(const pa_pool_desc* desc, void* k_codes, void* v_codes, void* k_ranges, void* v_ranges,
+                              pa_pool** out) {
+  if (out == nullptr) return fail(PA_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  const pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (desc->kv_dtype != PA_INT4) return fail(PA_ERR_INVALID_ARG, "a 4-bit pool has kv_dtype PA_INT4");
+  return make_pool(desc, k_codes, v_codes, k_ranges, v_ranges, out);
 }
 
 pa_status pa_pool_create(const pa_pool_desc* desc, void* k_pool, void* v_pool, pa_pool** out) {
@@ -599,19 +671,8 @@ pa_status pa_pool_create(const pa_pool_desc* desc, void* k_pool, void* v_pool, p
   *out = nullptr;
   pa_status st = check_desc(desc);
   if (st != PA_OK) return st;
-  if (k_pool == nullptr || v_pool == nullptr) return fail(PA_ERR_INVALID_ARG, "pool buffers must not be NULL");
-  if (!aligned(k_pool, 16) || !aligned(v_pool, 16)) return fail(PA_ERR_INVALID_ARG, "pool buffers must be 16-byte aligned");
-  pa_pool* p = new (std::nothrow) pa_pool;
-  if (p == nullptr) return fail(PA_ERR_INVALID_ARG, "out of host memory");
-  p->desc = *desc;
-  if (p->desc.kv_dtype != PA_FP8_E4M3) p->desc.k_scale = p->desc.v_scale = 1.0f;
-  p->head_scales = false;
-  p->k = k_pool;
-  p->v = v_pool;
-  p->tile_maps_ready = false;
-  p->dec_maps_ready = false;
-  *out = p;
-  return PA_OK;
+  if (desc->kv_dtype == PA_INT4) return fail(PA_ERR_INVALID_ARG, "a 4-bit pool is created by pa_pool_create_int4");
+  return make_pool(desc, k_pool, v_pool, nullptr, nullptr, out);
 }
 
 void pa_pool_destroy(pa_pool* pool) { delete pool; }

@@ -99,6 +99,30 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
 }
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+  if (p.kv_dtype == KV_INT4) {  // a token's range is found over its whole row
+    RowsParams r{};
+    r.k = p.k_new;
+    r.v = p.v_new;
+    r.k_stride = r.v_stride = static_cast<int64_t>(p.Hkv) * p.D;
+    r.k_pool = p.k_pool;
+    r.v_pool = p.v_pool;
+    r.k_ranges = p.k_ranges;
+    r.v_ranges = p.v_ranges;
+    r.seq_ids = p.seq_ids;
+    r.positions = p.positions;
+    r.block_tables = p.block_tables;
+    r.n_rows = p.n_rows;
+    r.num_seqs = p.num_seqs;
+    r.max_blocks = p.max_blocks;
+    r.num_pages = p.num_pages;
+    r.P = p.P;
+    r.Hkv = p.Hkv;
+    r.D = p.D;
+    r.in_dtype = p.in_dtype;
+    r.kv_dtype = p.kv_dtype;
+    r.status = p.status;
+    return launch_rows(r, stream);
+  }
   const long long rows = p.n_ranges > 0 ? p.range_first[p.n_ranges] : p.n_rows;
   const long long total = rows * 2 * p.Hkv * p.D / 8;
   if (total <= 0 && !p.with_order) return cudaSuccess;

@@ -693,6 +693,7 @@ pa_status pa_beam_reorder(const pa_pool* pool, int32_t n_groups, int32_t beams, 
   if (num_seqs <= 0 || max_blocks_per_seq <= 0)
     return fail(PA_ERR_INVALID_ARG, "num_seqs and max_blocks_per_seq must be positive");
   const pa_pool_desc& d = pool->desc;
+  if (d.kv_dtype == PA_INT4) return fail(PA_ERR_UNSUPPORTED, "reorder: a 4-bit pool");
   if (static_cast<int64_t>(max_blocks_per_seq) * d.page_size > 0x7fffffff)
     return fail(PA_ERR_UNSUPPORTED, "a block-table row of %d pages of %d tokens", max_blocks_per_seq, d.page_size);
   if (state != nullptr && (state_row_bytes == 0 || state_row_bytes % 4 != 0 || !aligned(state, 4)))

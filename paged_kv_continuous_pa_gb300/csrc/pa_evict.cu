@@ -714,6 +714,7 @@ pa_status pa_evict_compact(const pa_pool* pool, int32_t n, const int32_t* seq_id
   if (num_seqs <= 0 || max_blocks_per_seq <= 0)
     return fail(PA_ERR_INVALID_ARG, "num_seqs and max_blocks_per_seq must be positive");
   const pa_pool_desc& d = pool->desc;
+  if (d.kv_dtype == PA_INT4) return fail(PA_ERR_UNSUPPORTED, "compact: a 4-bit pool");
   if (static_cast<int64_t>(max_blocks_per_seq) * d.page_size > (1 << 30))  // (tokens and steps beyond stay int32)
     return fail(PA_ERR_UNSUPPORTED, "a block-table row of %d pages of %d tokens", max_blocks_per_seq, d.page_size);
   if (budget <= 0) return fail(PA_ERR_INVALID_ARG, "budget %d must be positive", budget);

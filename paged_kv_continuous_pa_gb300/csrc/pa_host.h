@@ -17,6 +17,8 @@ struct pa_pool {
   float k_scale_h[pa::kMaxHeadScales], v_scale_h[pa::kMaxHeadScales];
   void* k;
   void* v;
+  void* k_ranges;  // 4-bit pools, else null
+  void* v_ranges;
   std::mutex maps;       // held while they are encoded: threads may make a pool's first calls at once
   std::atomic<bool> tile_maps_ready;  // kmap / vmap encoded (on first use by the tile paths)
   std::atomic<bool> dec_maps_ready;   // kmap_dec / vmap_dec encoded (on first use by tensor-core decode units)
@@ -41,6 +43,11 @@ pa_status encode_tile_maps(pa_pool* pool);
 // bf16 queries [n_rows][hq][head_dim] as a 3-D tensor, 128-byte swizzle, boxes of
 // 64 elements x `group` heads x 128 / group rows.
 pa_status encode_query_map(CUtensorMap* map, const void* q, int32_t n_rows, int32_t hq, int32_t head_dim, int32_t group);
+
+// A tensor map of a 16-bit tensor of `rank` dimensions (dims and strides in elements,
+// innermost first, its own stride 1), 128-byte swizzle, out-of-range elements zero.
+pa_status encode_map_16bit(CUtensorMap* map, const void* base, int rank, const int64_t* dims, const int64_t* strides,
+                           const uint32_t* box);
 
 // Process-wide settings, each read once per call.
 uint32_t wait_limit();

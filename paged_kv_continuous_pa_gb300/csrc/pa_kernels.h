@@ -40,7 +40,7 @@ constexpr int kDecodeMinCtas = PA_DECODE_MIN_CTAS;
 constexpr int kDecodeRingBytes = PA_DECODE_RING_KB * 1024;   // at four CTAs per SM
 constexpr int kDecodeRingBytes3 = 64 * 1024;                 // at three CTAs per SM
 
-enum KvType { KV_F32 = 0, KV_BF16 = 1, KV_E4M3 = 2 };
+enum KvType { KV_F32 = 0, KV_BF16 = 1, KV_E4M3 = 2, KV_INT4 = 3 };
 
 // Device status codes (same values as pa_status in include/pa.h).
 enum { ST_OK = 0, ST_OUT_OF_RANGE = 3, ST_TIMEOUT = 4, ST_LAUNCH = 5 };  // ST_LAUNCH: a kernel found its launch inconsistent
@@ -68,6 +68,8 @@ struct OrderParams {
 struct AppendParams {
   void* k_pool;
   void* v_pool;
+  void* k_ranges;  // 4-bit pools: (step, low) f16 pairs
+  void* v_ranges;
   const void* k_new;
   const void* v_new;
   const int32_t* seq_ids;
@@ -96,6 +98,8 @@ struct AppendParams {
 struct AttnParams {
   const void* k_pool;
   const void* v_pool;
+  const void* k_ranges;  // 4-bit pools: (step, low) f16 pairs
+  const void* v_ranges;
   const void* q;
   void* out;
   const int32_t* seq_ids;
@@ -157,6 +161,60 @@ struct AttnParams {
 };
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
+
+// A step's rows taken in: q rotated into q_out, k rotated and stored, v stored
+// (pa_rope_append), q alone (pa_rope_rows: Hkv = 0), or k and v stored as they are
+// (the append to a 4-bit pool: Hq = 0, rot = 0).
+struct RowsParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride, out_stride;  // elements from row to row
+  void* k_pool;
+  void* v_pool;
+  void* k_ranges;
+  void* v_ranges;
+  const int32_t* seq_ids;
+  const int32_t* positions;
+  const int32_t* block_tables;
+  int32_t n_rows, num_seqs, max_blocks, num_pages;
+  int32_t P, Hq, Hkv, D;
+  int32_t in_dtype;       // KV_F32 or KV_BF16
+  int32_t kv_dtype;       // KvType of the pool
+  int32_t head_scales;
+  float k_scale_h[kMaxHeadScales], v_scale_h[kMaxHeadScales];
+  int32_t* status;
+  int32_t rot;            // rotated elements of a head (0: none)
+  int32_t interleaved;    // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
+  float sign;             // -1: the transposed rotation
+  float magnitude;
+  uint64_t turns[64];     // per pair: turns per position, as a 64-bit fraction of one turn
+};
+cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream);
+
+struct ReadParams {
+  const void* k_pool;
+  const void* v_pool;
+  const void* k_ranges;
+  const void* v_ranges;
+  void* k_out;
+  void* v_out;
+  const int32_t* seq_ids;
+  const int32_t* positions;
+  const int32_t* block_tables;
+  int32_t n_rows, num_seqs, max_blocks, num_pages;
+  int32_t P, Hkv, D;
+  int32_t out_bf16;
+  int32_t kv_dtype;
+  int32_t head_scales;
+  float k_scale_h[kMaxHeadScales], v_scale_h[kMaxHeadScales];
+  int32_t* status;
+};
+cudaError_t launch_read(const ReadParams& p, cudaStream_t stream);
+
+// Decode units over 4-bit pools, every head group and query dtype.
+cudaError_t launch_decode_int4(const AttnParams& p, cudaStream_t stream);
 
 // One CTA that writes o.order (the rows longest first); the attention launched
 // after it as a programmatic dependent may start its setup at once.

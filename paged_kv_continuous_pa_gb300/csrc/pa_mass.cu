@@ -98,6 +98,7 @@ pa_status pa_attention_mass(const pa_pool* pool, int32_t n_rows, const void* q, 
                             int32_t* status_dev, void* stream) {
   if (pool == nullptr) return fail(PA_ERR_INVALID_ARG, "pool is NULL");
   const pa_pool_desc& d = pool->desc;
+  if (d.kv_dtype == PA_INT4) return fail(PA_ERR_UNSUPPORTED, "attention mass: a 4-bit pool");
   pa_status st = pa::check_rows(d, n_rows, q_dtype, num_q_heads, num_seqs, max_blocks_per_seq, chunks, n_chunks);
   if (st != PA_OK) return st;
   if (static_cast<int64_t>(max_blocks_per_seq) * d.page_size > (1 << 30))  // (positions and steps beyond stay int32)

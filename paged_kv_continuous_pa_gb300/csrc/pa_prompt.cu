@@ -1,0 +1,625 @@
+// pa_prompt.cu -- causal attention over whole prompts packed one behind the other
+// (pa_prompt_attention), on tcgen05 tiles.
+//
+//   out_i = sum_{j <= i} exp2(s_ij - m_i) v_j / sum_{j <= i} exp2(s_ij - m_i),   s_ij = scale log2(e) q_i . k_j
+//
+// One pass over the keys with a running reference m_i: it moves only when a score
+// passes it by 2^8, so the accumulator is seldom rescaled.
+//
+// What bounds it: the two matrix products, 4 D flops for each (query head, query, key).
+// One CTA per SM goes through units of work.  A unit is two query tiles of 128 rows that
+// read the same keys: two query heads of one kv head at the same positions where the
+// head group is even, else two neighbouring ranges of 128 positions of one head.  While
+// the softmax of one tile runs, the tensor core works for the other.
+//   warps 0-3, 4-7   softmax and output of tile A, B: one row to a thread
+//   warp 8           loads: queries and 128-key tiles of K and V through a ring (TMA)
+//   warp 9           issues the MMAs:  S = Q K^T (smem x smem), then O += P V (TMEM x smem)
+//   warps 10, 11     look over the values of the blocks that hold masked keys
+// Tensor memory: S of A and B (128 columns each), the weights P over their S as bf16, O of A and B.
+//
+// Masked keys.  Only the block on a tile's diagonal has any (keys behind the
+// sequence's end are behind every row's diagonal too).  A masked key's weight is 0,
+// but 0 times an infinite or NaN value is NaN, so warps 10 and 11 put 0 in the
+// place of such values in shared memory; a row that does attend to one gets it added at the end.
+//
+// Units are listed longest first by a launch of their own and dealt out to the CTAs in a
+// snake, so that the last ones are short.
+#include <algorithm>
+#include <cmath>
+
+#include "pa_device.cuh"
+#include "pa_host.h"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+constexpr int kPrTile = 128;     // rows of a query tile, keys of a block
+constexpr int kPrThreads = 384;
+constexpr int kPrBins = 2048;    // of the units' lengths, when they are ordered
+constexpr int kPrPlanThreads = 1024;
+// registers of a softmax thread and of the others; their sum over the CTA is what it is launched with
+constexpr int kPrRegs = 168, kPrSoftmaxRegs = 208, kPrOtherRegs = 88;
+static_assert(2 * 128 * kPrSoftmaxRegs + 128 * kPrOtherRegs <= kPrThreads * kPrRegs, "register split");
+
+struct PromptParams {
+  const int32_t* row_starts;
+  int32_t* n_tiles;      // workspace: number of tiles listed
+  int4* tiles;           // workspace: first row and end of the sequence, position of the tile
+  const uint16_t* v;
+  int64_t v_stride;
+  uint16_t* out;
+  float* lse;
+  int32_t* status;
+  int32_t n_rows, n_seqs, Hq, G, max_tiles, bin_shift;
+  int32_t tile_rows;     // positions of a unit: 128 (two heads) or 256
+  float scale_log2;
+  uint32_t wait_limit;
+  int32_t debug_stall;
+  CUtensorMap qmap, kmap, vmap;  // [rows][heads][D], boxes of 64 elements x 1 head x 128 rows
+};
+
+// The tiles of all sequences, longest first.
+__global__ void __launch_bounds__(kPrPlanThreads) prompt_plan_kernel(const __grid_constant__ PromptParams p) {
+  __shared__ int32_t hist[kPrBins];
+  __shared__ int32_t sums[32];
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kPrBins; i += kPrPlanThreads) hist[i] = 0;
+  bool bad = false;
+  for (int s = tid; s <= p.n_seqs; s += kPrPlanThreads) {
+    const int a = p.row_starts[s];
+    bad |= a < 0 || a > p.n_rows || (s > 0 && p.row_starts[s - 1] > a);
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      record_error(p.status, ST_OUT_OF_RANGE);
+      *p.n_tiles = 0;
+    }
+    return;
+  }
+  // bin 0 holds the longest units
+  auto bin_of = [&](int pos) { return kPrBins - 1 - min(kPrBins - 1, (pos / kPrTile) >> p.bin_shift); };
+  for (int s = warp; s < p.n_seqs; s += kPrPlanThreads / 32) {
+    const int len = p.row_starts[s + 1] - p.row_starts[s];
+    for (int64_t pos = static_cast<int64_t>(lane) * p.tile_rows; pos < len; pos += 32ll * p.tile_rows)
+      atomicAdd(&hist[bin_of(static_cast<int>(pos))], 1);
+  }
+  __syncthreads();
+  // exclusive sums over the bins, two to a thread
+  const int a = hist[2 * tid], b = hist[2 * tid + 1];
+  int x = a + b;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int y = sums[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int z = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) y += z;
+    }
+    sums[lane] = y;
+  }
+  __syncthreads();
+  const int before = x - a - b + (warp > 0 ? sums[warp - 1] : 0);
+  hist[2 * tid] = before;
+  hist[2 * tid + 1] = before + a;
+  if (tid == 0) *p.n_tiles = sums[31];
+  __syncthreads();
+  for (int s = warp; s < p.n_seqs; s += kPrPlanThreads / 32) {
+    const int begin = p.row_starts[s], end = p.row_starts[s + 1];
+    for (int64_t pos = static_cast<int64_t>(lane) * p.tile_rows; pos < end - begin; pos += 32ll * p.tile_rows)
+      p.tiles[atomicAdd(&hist[bin_of(static_cast<int>(pos))], 1)] = make_int4(begin, end, static_cast<int>(pos), 0);
+  }
+}
+
+__device__ __forceinline__ void pr_load_3d(void* dst_smem, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                           uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst_smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// 32 columns of this warp's lanes, without waiting; pr_ld_wait waits for every load started.
+__device__ __forceinline__ void pr_ld32(uint32_t taddr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void pr_ld_wait(float* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                 "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
+                 "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                 "+f"(r[30]), "+f"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pr_pack(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+template <int D>
+struct PromptSmem {  // byte offsets from a 1024-byte aligned base
+  static constexpr int NH = D / 64;
+  static constexpr int HALF = kPrTile * 128;       // 64 elements of 128 rows
+  static constexpr int TILE = NH * HALF;
+  static constexpr int STAGES = D == 128 ? 5 : 8;  // tiles of K and V in the ring
+  static constexpr int RING = 2 * TILE;            // behind the two query tiles
+  static constexpr int BAR = RING + STAGES * TILE;
+  static constexpr int BYTES = BAR + 512 + 1024;   // slack for aligning the base
+  static_assert(BYTES <= 227 * 1024, "shared memory");
+};
+
+// A unit: the tiles' positions, heads and numbers of key blocks.
+struct PromptUnit {
+  int begin, end;      // rows of the sequence
+  int pos[2], head[2], blocks[2];
+  int n;               // blocks of the longer tile
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+  using S = PromptSmem<D>;
+  enum {
+    FULL = 0,                    // K / V tile landed
+    EMPTY = FULL + S::STAGES,    // ... read by its MMAs
+    QF = EMPTY + S::STAGES,      // queries of tile A / B landed
+    QE = QF + 2,                 // ... read by the unit's MMAs
+    SF = QE + 2,                 // scores of tile A / B
+    PF = SF + 2,                 // weights of tile A / B (their scores are read, O may be added to)
+    PV = PF + 2,                 // O of tile A / B holds one more block
+    // the values of a block with masked keys are looked over: in turn, as the look may be a unit ahead of the
+    // MMAs, and a unit has at most two such blocks
+    VOK = PV + 2,
+    DRAIN = VOK + 4,
+    STALL,
+    COUNT
+  };
+  static_assert(COUNT * 8 + 32 <= 512, "barriers");
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::BAR + COUNT * 8);
+  volatile int32_t* odd_values = reinterpret_cast<volatile int32_t*>(tslot + 1);  // entry k % 4 is k + 1: values of unit k were put to 0
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (warp == 0) tc::tmem_alloc(tslot, 512);
+  if (tid == 0) {
+    for (int i = 0; i < COUNT; ++i) mbar_init(&bar[i], i == PF || i == PF + 1 ? 4u : i >= VOK && i < VOK + 4 ? 2u : 1u);
+    for (int i = 0; i < 4; ++i) odd_values[i] = 0;
+    fence_barrier_init();
+    tc::prefetch_tensormap(&p.qmap);
+    tc::prefetch_tensormap(&p.kmap);
+    tc::prefetch_tensormap(&p.vmap);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  griddep_wait();  // the list of tiles
+  const uint32_t tb = *tslot;
+  const bool two_heads = p.tile_rows == kPrTile;
+  const int per_tile = two_heads ? p.Hq / 2 : p.Hq;
+  const int units = *p.n_tiles * per_tile;
+
+  auto wait = [&](int b, uint32_t parity) {
+    if (mbar_wait(&bar[b], parity, p.wait_limit)) return true;
+    record_error(p.status, ST_TIMEOUT);
+    return false;
+  };
+  // the k-th unit of this CTA (every other round backwards); false behind the last
+  auto unit_at = [&](int k, PromptUnit& x) {
+    const int64_t u = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (static_cast<int64_t>(k) * gridDim.x >= units) return false;
+    x.n = x.blocks[0] = x.blocks[1] = 0;
+    if (u >= units) return true;  // (a round without work for this CTA)
+    const int4 t = __ldcg(p.tiles + u / per_tile);
+    const int h = static_cast<int>(u % per_tile);
+    x.begin = t.x;
+    x.end = t.y;
+    x.pos[0] = t.z;
+    x.blocks[0] = t.z / kPrTile + 1;
+    if (two_heads) {
+      x.head[0] = 2 * h;
+      x.head[1] = 2 * h + 1;
+      x.pos[1] = t.z;
+      x.blocks[1] = x.blocks[0];
+    } else {
+      x.head[0] = x.head[1] = h;
+      x.pos[1] = t.z + kPrTile;
+      x.blocks[1] = x.pos[1] < t.y - t.x ? x.blocks[0] + 1 : 0;
+    }
+    x.n = max(x.blocks[0], x.blocks[1]);
+    return true;
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrOtherRegs));
+    if (warp == 8 && lane == 0) {
+      // ---- loads
+      int item = 0, done[2] = {0, 0};  // tiles of K and V, query tiles issued so far
+      bool ok = !p.debug_stall || wait(STALL, 0);  // (runs out by construction)
+      PromptUnit x{};
+      for (int k = 0; ok && unit_at(k, x); ++k) {
+        for (int t = 0; ok && t < 2; ++t) {
+          if (x.blocks[t] == 0) continue;
+          if (done[t] > 0) ok = wait(QE + t, (done[t] - 1) & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bar[QF + t], S::TILE);
+          for (int hf = 0; hf < S::NH; ++hf)
+            pr_load_3d(sm + t * S::TILE + hf * S::HALF, &p.qmap, hf * 64, x.head[t], x.begin + x.pos[t], &bar[QF + t]);
+          ++done[t];
+        }
+        for (int j = 0; ok && j < 2 * x.n; ++j) {
+          const int s = item % S::STAGES;
+          if (item >= S::STAGES) ok = wait(EMPTY + s, (item / S::STAGES - 1) & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bar[FULL + s], S::TILE);
+          for (int hf = 0; hf < S::NH; ++hf)
+            pr_load_3d(sm + S::RING + s * S::TILE + hf * S::HALF, (j & 1) ? &p.vmap : &p.kmap, hf * 64, x.head[0] / p.G,
+                       x.begin + (j >> 1) * kPrTile, &bar[FULL + s]);
+          ++item;
+        }
+      }
+      if (!ok) {  // what is in flight lands before the shared memory is given up
+        for (int i = max(0, item - S::STAGES); i < item; ++i)
+          mbar_wait(&bar[FULL + i % S::STAGES], (i / S::STAGES) & 1, kDrainWaitLimit);
+        for (int t = 0; t < 2; ++t)
+          if (done[t] > 0) mbar_wait(&bar[QF + t], (done[t] - 1) & 1, kDrainWaitLimit);
+      }
+    } else if (warp == 9 && lane == 0) {
+      // ---- MMAs
+      constexpr uint32_t id_qk = tc::idesc_bf16_f32(kPrTile, kPrTile, false);
+      constexpr uint32_t id_pv = tc::idesc_bf16_f32(kPrTile, D, true);
+      int base = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0}, checked = 0;
+      bool ok = true;
+      PromptUnit x{};
+      auto full = [&](int item) { return wait(FULL + item % S::STAGES, (item / S::STAGES) & 1); };
+      auto qk = [&](int t, int j) {
+        const unsigned char* q = sm + t * S::TILE;
+        const unsigned char* kt = sm + S::RING + ((base + 2 * j) % S::STAGES) * S::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int off = (kk / 4) * S::HALF + (kk % 4) * 32;
+          tc::mma_bf16(tb + t * 128, tc::smem_desc(q + off, 16, 1024), tc::smem_desc(kt + off, 16, 1024), id_qk, kk > 0);
+        }
+        tc::mma_commit(&bar[SF + t]);
+        if (j == x.blocks[t] - 1) tc::mma_commit(&bar[QE + t]);
+      };
+      auto pv = [&](int t, int j) {
+        const unsigned char* vt = sm + S::RING + ((base + 2 * j + 1) % S::STAGES) * S::TILE;
+#pragma unroll
+        for (int kk = 0; kk < kPrTile / 16; ++kk)
+          tc::mma_bf16_ts(tb + 256 + t * 128, tb + t * 128 + kk * 8, tc::smem_desc(vt + kk * 2048, S::HALF, 1024), id_pv,
+                          j > 0 || kk > 0);
+        tc::mma_commit(&bar[PV + t]);
+      };
+      for (int k = 0; ok && unit_at(k, x); ++k) {
+        if (x.n == 0) continue;
+        ok = full(base);
+        for (int t = 0; ok && t < 2; ++t) {
+          if (x.blocks[t] == 0) continue;
+          ok = wait(QF + t, q_count[t]++ & 1);
+          if (ok) qk(t, 0);
+        }
+        if (ok) tc::mma_commit(&bar[EMPTY + base % S::STAGES]);
+        for (int j = 0; ok && j < x.n; ++j) {
+          ok = full(base + 2 * j + 1);
+          if (ok && j >= x.blocks[0] - 1) {
+            ok = wait(VOK + (checked & 3), (checked >> 2) & 1);
+            ++checked;
+          }
+          if (ok && j + 1 < x.n) ok = full(base + 2 * j + 2);
+          for (int t = 0; ok && t < 2; ++t) {
+            if (j >= x.blocks[t]) continue;
+            ok = wait(PF + t, p_count[t]++ & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            pv(t, j);
+            if (j + 1 < x.blocks[t]) qk(t, j + 1);
+          }
+          if (!ok) break;
+          tc::mma_commit(&bar[EMPTY + (base + 2 * j + 1) % S::STAGES]);
+          if (j + 1 < x.n) tc::mma_commit(&bar[EMPTY + (base + 2 * j + 2) % S::STAGES]);
+        }
+        base += 2 * x.n;
+      }
+      if (!ok) {  // every MMA issued is done before the tensor memory is given up
+        tc::mma_commit(&bar[DRAIN]);
+        mbar_wait(&bar[DRAIN], 0, kDrainWaitLimit);
+      }
+    } else if (warp >= 10) {
+      // ---- values of the blocks that hold masked keys: infinities and NaN become 0
+      int base = 0, checked = 0;
+      bool ok = true;
+      PromptUnit x{};
+      for (int k = 0; ok && unit_at(k, x); ++k) {
+        if (x.n == 0) continue;
+        for (int j = x.blocks[0] - 1; ok && j < x.n; ++j, ++checked) {
+          const int item = base + 2 * j + 1;
+          ok = __all_sync(0xffffffffu, wait(FULL + item % S::STAGES, (item / S::STAGES) & 1));
+          if (!ok) break;
+          uint4* tile = reinterpret_cast<uint4*>(sm + S::RING + (item % S::STAGES) * S::TILE);
+          bool found = false;
+          for (int i = (warp - 10) * 32 + lane; i < S::TILE / 16; i += 64) {
+            uint4 w = tile[i];
+            auto odd = [](uint32_t a) { return ((a & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };  // exponent of all ones
+            if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
+              auto clean = [&](uint32_t a) {
+                const uint32_t o = odd(a);
+                return a & ~((o & 0x8000u ? 0xffffu : 0u) | (o & 0x80000000u ? 0xffff0000u : 0u));
+              };
+              tile[i] = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+              found = true;
+            }
+          }
+          if (found) odd_values[k & 3] = k + 1;
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[VOK + (checked & 3)]);
+        }
+        base += 2 * x.n;
+      }
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrSoftmaxRegs));
+    // ---- softmax and output of tile t
+    const int t = warp >> 2, r = tid & 127;  // the thread's row of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tb + lanes + t * 128, to = tb + lanes + 256 + t * 128;
+    int count = 0;  // blocks of this tile so far
+    bool ok = true;
+    PromptUnit x{};
+    for (int k = 0; ok && unit_at(k, x); ++k) {
+      const int n = x.blocks[t];
+      if (n == 0) continue;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < n; ++j, ++count) {
+        ok = __all_sync(0xffffffffu, wait(SF + t, count & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
+        float s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pr_ld32(ts + 32 * i, s + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pr_ld_wait(s + 32 * i);
+        if (j == n - 1) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = i > r ? -INFINITY : s[i];
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], fmaxf(s[i + 2 * q], s[i + 2 * q + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool move = (top - m) * p.scale_log2 > kRescaleSlack;
+        if (__any_sync(0xffffffffu, move)) {
+          if (j > 0) {
+            ok = __all_sync(0xffffffffu, wait(PV + t, (count - 1) & 1));
+            if (!ok) break;
+            tc::fence_after_sync();
+            const float f = move ? ex2((m - top) * p.scale_log2) : 1.0f;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              pr_ld32(to + 32 * c, o);
+              pr_ld_wait(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              tc::tmem_st32(to + 32 * c, o);
+            }
+          }
+          if (move) m = top;
+        }
+        const float shift = m == -INFINITY ? 0.0f : m * p.scale_log2;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float a = ex2(fmaf(s[32 * i + 2 * q], p.scale_log2, -shift));
+            const float b = ex2(fmaf(s[32 * i + 2 * q + 1], p.scale_log2, -shift));
+            sum[2 * (q & 1)] += a;
+            sum[2 * (q & 1) + 1] += b;
+            w[q] = pr_pack(a, b);
+          }
+          tc::tmem_st16(ts + 16 * i, w);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[PF + t]);
+      }
+      if (!ok) break;
+      // ---- output
+      ok = __all_sync(0xffffffffu, wait(PV + t, (count - 1) & 1));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const int row = x.begin + x.pos[t] + r;
+      const bool live = row < x.end;
+      const bool odd = odd_values[k & 3] == k + 1;
+      const float inv = __fdiv_rn(1.0f, l);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        pr_ld32(to + 32 * c, o);
+        pr_ld_wait(o);
+        if (odd && live) {  // the values that were put to 0 and this row attends to
+          for (int key = x.begin + (x.blocks[0] - 1) * kPrTile; key <= row; ++key) {
+            const uint16_t* v = p.v + key * p.v_stride + (x.head[t] / p.G) * D + 32 * c;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float a = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
+              if (!(fabsf(a) < INFINITY)) o[i] += a;
+            }
+          }
+        }
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row) * p.Hq + x.head[t]) * D + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pr_pack(o[8 * i] * inv, o[8 * i + 1] * inv), pr_pack(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pr_pack(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pr_pack(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        }
+      }
+      if (p.lse != nullptr && live)
+        p.lse[static_cast<int64_t>(row) * p.Hq + x.head[t]] =
+            l > 0.0f ? 0.69314718055994531f * fmaf(m, p.scale_log2, log2f(l)) : l == 0.0f ? -INFINITY : l;
+      tc::fence_before_sync();  // O is read before the next unit's first weights are announced
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tb, 512);
+}
+
+template <int D>
+cudaError_t launch_prompt(const PromptParams& p, unsigned grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_dynamic_smem(prompt_kernel<D>, done, PromptSmem<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  // the register split waits for what the CTA was not launched with
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_acquire) == 0) {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, prompt_kernel<D>);
+    if (e != cudaSuccess) return e;
+    regs.store(a.numRegs, std::memory_order_release);
+  }
+  if (regs.load(std::memory_order_acquire) != kPrRegs) return cudaErrorInvalidKernelImage;
+  prompt_plan_kernel<<<1, kPrPlanThreads, 0, stream>>>(p);
+  count_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(prompt_kernel<D>, dim3(grid), dim3(kPrThreads), PromptSmem<D>::BYTES, stream, true, p);
+  count_launch();
+  return e;
+}
+
+}  // namespace pa
+
+using pa::aligned;
+using pa::cuda_fail;
+using pa::fail;
+
+namespace {
+
+// Whether a unit is two heads at the same positions (else two ranges of one head).
+bool two_heads(int32_t hq, int32_t hkv) { return hq / hkv % 2 == 0; }
+
+int64_t most_tiles(int32_t n_rows, int32_t n_seqs, int32_t hq, int32_t hkv) {
+  return n_rows / (two_heads(hq, hkv) ? pa::kPrTile : 2 * pa::kPrTile) + static_cast<int64_t>(n_seqs);
+}
+
+pa_status check_prompt(int32_t n_rows, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t head_dim) {
+  if (n_rows < 0 || n_seqs < 0) return fail(PA_ERR_INVALID_ARG, "n_rows %d or n_seqs %d < 0", n_rows, n_seqs);
+  if (hkv <= 0 || hq <= 0 || hq % hkv != 0)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of num_kv_heads %d", hq, hkv);
+  if (head_dim != 64 && head_dim != 128) return fail(PA_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", head_dim);
+  if (most_tiles(n_rows, n_seqs, hq, hkv) * hq > 0x7fffffff - 1024)
+    return fail(PA_ERR_UNSUPPORTED, "%d rows of %d query heads in one call", n_rows, hq);
+  return PA_OK;
+}
+
+pa_status check_rows16(const char* name, const void* base, int64_t stride, int64_t elements) {
+  if (base == nullptr) return fail(PA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(base, 16)) return fail(PA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride < elements || stride % 8 != 0 || stride >= (1ll << 38))
+    return fail(PA_ERR_INVALID_ARG, "%s rows of %lld elements, %lld apart: a multiple of 8, at least a row", name,
+                (long long)elements, (long long)stride);
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_prompt_workspace_bytes(int32_t n_rows, int32_t n_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim) {
+  if (check_prompt(n_rows, n_seqs, num_q_heads, num_kv_heads, head_dim) != PA_OK) return 0;
+  return 256 + static_cast<size_t>(most_tiles(n_rows, n_seqs, num_q_heads, num_kv_heads)) * sizeof(int4);
+}
+
+pa_status pa_prompt_attention(int32_t n_rows, int32_t n_seqs, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, pa_dtype dtype, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, const int32_t* row_starts, float softmax_scale,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                              void* stream) {
+  pa_status st = check_prompt(n_rows, n_seqs, num_q_heads, num_kv_heads, head_dim);
+  if (st != PA_OK) return st;
+  if (dtype != PA_F32 && dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "prompt attention takes bf16 rows");
+  if (dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "prompt attention takes bf16 rows");
+  if (n_rows == 0 || n_seqs == 0) return PA_OK;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim, kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  st = check_rows16("q", q, q_stride, q_row);
+  if (st == PA_OK) st = check_rows16("k", k, k_stride, kv_row);
+  if (st == PA_OK) st = check_rows16("v", v, v_stride, kv_row);
+  if (st == PA_OK) st = check_rows16("out", out, q_row, q_row);
+  if (st != PA_OK) return st;
+  if (row_starts == nullptr) return fail(PA_ERR_INVALID_ARG, "row_starts is NULL");
+  const size_t need = pa_prompt_workspace_bytes(n_rows, n_seqs, num_q_heads, num_kv_heads, head_dim);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(PA_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", need,
+                workspace == nullptr ? static_cast<size_t>(0) : workspace_bytes);
+  if (!aligned(workspace, 256)) return fail(PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const double scale = softmax_scale > 0.f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(static_cast<double>(head_dim));
+  pa::PromptParams p{};
+  p.row_starts = row_starts;
+  p.n_tiles = static_cast<int32_t*>(workspace);
+  p.tiles = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + 256);
+  p.v = static_cast<const uint16_t*>(v);
+  p.v_stride = v_stride;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.status = status_dev;
+  p.n_rows = n_rows;
+  p.n_seqs = n_seqs;
+  p.Hq = num_q_heads;
+  p.G = num_q_heads / num_kv_heads;
+  p.tile_rows = two_heads(num_q_heads, num_kv_heads) ? pa::kPrTile : 2 * pa::kPrTile;
+  while ((n_rows / pa::kPrTile) >> p.bin_shift >= pa::kPrBins) ++p.bin_shift;
+  p.scale_log2 = static_cast<float>(scale * 1.4426950408889634073599246810018921);
+  p.wait_limit = pa::wait_limit();
+  p.debug_stall = pa::debug_stall();
+  struct { CUtensorMap* map; const void* base; int64_t stride; int32_t heads; } maps[3] = {
+      {&p.qmap, q, q_stride, num_q_heads}, {&p.kmap, k, k_stride, num_kv_heads}, {&p.vmap, v, v_stride, num_kv_heads}};
+  for (auto& m : maps) {
+    const int64_t dims[3] = {head_dim, m.heads, n_rows}, strides[3] = {1, head_dim, m.stride};
+    const uint32_t box[3] = {64, 1, static_cast<uint32_t>(pa::kPrTile)};
+    st = pa::encode_map_16bit(m.map, m.base, 3, dims, strides, box);
+    if (st != PA_OK) return st;
+  }
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention");
+  const int64_t units = most_tiles(n_rows, n_seqs, num_q_heads, num_kv_heads) * (p.tile_rows == pa::kPrTile ? num_q_heads / 2 : num_q_heads);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(sms, units));
+  e = head_dim == 128 ? pa::launch_prompt<128>(p, grid, static_cast<cudaStream_t>(stream))
+                      : pa::launch_prompt<64>(p, grid, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "prompt attention launch");
+}
+
+}  // extern "C"

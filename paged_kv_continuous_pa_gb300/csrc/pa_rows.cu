@@ -1,0 +1,574 @@
+// pa_rows.cu -- a step's rows on their way into the cache and back: rotary positions
+// (pa_rope_rows, pa_rope_append), the append to 4-bit pools, and cached tokens as
+// dense rows (pa_read_kv).
+//
+// A pair (a, b) at position p turns by the angle p f_i:
+//   (a, b) -> m (a cos - b sin, a sin + b cos)
+// The angle is taken in turns: f_i / 2 pi is a 64-bit fraction of a turn, so p f_i modulo
+// whole turns is one wrapping integer product, exact at any position (an FP32 product
+// is off by 0.06 rad at position 10^6); sincospi gets its upper 32 bits.  A row's
+// sines and cosines are the same for all of its heads, so a CTA computes them once
+// for its rows into shared memory.
+//
+// What bounds it is memory: every element is read and written once.  D / 8 lanes share
+// one head of one row, 8 consecutive elements (one or two 16-byte accesses) to a lane; the
+// partner octet of the half layout sits in another lane of the same group and comes by
+// shuffle.  So a head is in one place when it is rotated, which a 4-bit pool needs: its
+// range is a reduction over the group.
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "pa_device.cuh"
+#include "pa_host.h"
+
+namespace pa {
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsPerCta = 8;  // at most
+
+// 8 consecutive elements of one head, as loaded (plain loads: queries may be rotated in place)
+template <bool BF16>
+struct Octet {
+  uint32_t w[BF16 ? 4 : 8];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Octet<BF16> load_octet(const void* base, int64_t element) {
+  Octet<BF16> o;
+  if constexpr (BF16) {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + element);
+    o.w[0] = a.x; o.w[1] = a.y; o.w[2] = a.z; o.w[3] = a.w;
+  } else {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + element);
+    const uint4 a = s[0], b = s[1];
+    o.w[0] = a.x; o.w[1] = a.y; o.w[2] = a.z; o.w[3] = a.w;
+    o.w[4] = b.x; o.w[5] = b.y; o.w[6] = b.z; o.w[7] = b.w;
+  }
+  return o;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen(const Octet<BF16>& o, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (BF16)
+      x[i] = (i & 1) ? bf16hi(o.w[i / 2]) : bf16lo(o.w[i / 2]);
+    else
+      x[i] = __uint_as_float(o.w[i]);
+  }
+}
+
+__device__ __forceinline__ void store_f32(void* base, int64_t element, const float (&x)[8]) {
+  float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + element);
+  d[0] = make_float4(x[0], x[1], x[2], x[3]);
+  d[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+__device__ __forceinline__ void store_bf16(void* base, int64_t element, const float (&x)[8]) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = encode_bf16(x[2 * i]) | (encode_bf16(x[2 * i + 1]) << 16);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + element) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One token of one kv head into a 4-bit pool: L lanes hold 8 elements each.  The range is
+// stored first and the codes are taken against what was stored, so that a code is off by
+// half a step at most (each conversion below rounds once, to nearest even).
+template <int L>
+__device__ __forceinline__ void store_int4(void* codes, void* ranges, int64_t token, int l, float (&x)[8]) {
+  bool nan = false;
+  float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    nan |= x[i] != x[i];
+    x[i] = fminf(fmaxf(x[i], -65504.0f), 65504.0f);  // the range is held in f16
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+  }
+#pragma unroll
+  for (int d = L / 2; d > 0; d /= 2) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+    nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), d) != 0;
+  }
+  __half low = __float2half_rn(lo);
+  const float lf = __half2float(low);
+  __half step = __float2half_rn(fmaxf(__fdiv_rn(__fsub_rn(hi, lf), 15.0f), 0.0f));
+  const float sf = __half2float(step);
+  uint32_t word = 0;
+  if (sf > 0.0f && !nan) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], lf), sf)), 0.0f), 15.0f);
+      word |= static_cast<uint32_t>(c) << (4 * i);
+    }
+  }
+  if (nan) low = step = __ushort_as_half(0x7fff);
+  if (token < 0) return;
+  static_cast<uint32_t*>(codes)[token * L + l] = word;
+  if (l == 0)
+    static_cast<uint32_t*>(ranges)[token] = static_cast<uint32_t>(__half_as_ushort(step)) |
+                                            static_cast<uint32_t>(__half_as_ushort(low)) << 16;
+}
+
+struct RowsSmem {
+  float2 turn[kRowsPerCta][64];  // (cos, sin) of the row's pairs
+  int32_t page[kRowsPerCta];     // of the row's token (-1: a row that is skipped)
+  int32_t slot[kRowsPerCta];
+  float x[kRowsThreads * 8];     // heads whose partners do not sit in one lane
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constant__ RowsParams p, int rows_per_cta) {
+  constexpr int L = D / 8, kGroups = kRowsThreads / L, kBatch = 2;
+  __shared__ __align__(16) RowsSmem sm;
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, l = tid % L, group = tid / L;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_per_cta;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(rows_per_cta), p.n_rows - row0));
+  const int H = p.Hq + 2 * p.Hkv, units = rows * H;
+
+  // the first heads of each group are on their way while the angles are computed
+  auto load = [&](int u) -> Octet<BF16> {
+    if (u >= units) return Octet<BF16>{};
+    const int64_t row = row0 + u / H;
+    const int h = u % H;
+    if (h < p.Hq) return load_octet<BF16>(p.q, row * p.q_stride + h * D + 8 * l);
+    if (h < p.Hq + p.Hkv) return load_octet<BF16>(p.k, row * p.k_stride + (h - p.Hq) * D + 8 * l);
+    return load_octet<BF16>(p.v, row * p.v_stride + (h - p.Hq - p.Hkv) * D + 8 * l);
+  };
+  Octet<BF16> raw[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) raw[b] = load(group + b * kGroups);
+
+  if (p.Hkv > 0 && tid < rows) {
+    const int seq = __ldg(p.seq_ids + row0 + tid), pos = __ldg(p.positions + row0 + tid);
+    int page = -1;
+    if (seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < static_cast<int64_t>(p.max_blocks) * p.P)
+      page = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + pos / p.P);
+    if (page < 0 || page >= p.num_pages) {
+      page = -1;
+      record_error(p.status, ST_OUT_OF_RANGE);
+    }
+    sm.page[tid] = page;
+    sm.slot[tid] = pos & (p.P - 1);
+  }
+  const int pairs = p.rot / 2;
+  for (int i = tid; i < rows * pairs; i += kRowsThreads) {
+    const int r = i / pairs, j = i % pairs;
+    const int64_t pos = __ldg(p.positions + row0 + r);
+    const uint64_t phase = p.turns[j] * static_cast<uint64_t>(pos) + (1ull << 31);
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &s, &c);
+    sm.turn[r][j] = make_float2(c * p.magnitude, s * p.magnitude * p.sign);
+  }
+  __syncthreads();
+
+  const bool half_octets = !p.interleaved && pairs % 8 == 0;
+  const int o8 = pairs / 8;
+  const int partner = lane - l + (l < o8 ? l + o8 : l < 2 * o8 ? l - o8 : l);
+  for (int u0 = 0; u0 < units; u0 += kBatch * kGroups) {  // the same rounds for every lane of a warp
+    Octet<BF16> next[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) next[b] = load(u0 + (kBatch + b) * kGroups + group);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (u0 + b * kGroups >= units) break;
+      const int u = u0 + b * kGroups + group;
+      const bool live = u < units;
+      const int r = live ? u / H : 0, h = live ? u % H : 0;
+      const bool turned = h < p.Hq + p.Hkv && p.rot > 0;
+      float x[8];
+      widen<BF16>(raw[b], x);
+      if (p.interleaved) {
+        if (turned) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (8 * l + 2 * i >= p.rot) break;
+            const float2 t = sm.turn[r][4 * l + i];
+            const float a = x[2 * i], c = x[2 * i + 1];
+            x[2 * i] = a * t.x - c * t.y;
+            x[2 * i + 1] = c * t.x + a * t.y;
+          }
+        }
+      } else if (half_octets) {
+        Octet<BF16> other;
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 4 : 8); ++i) other.w[i] = __shfl_sync(0xffffffffu, raw[b].w[i], partner);
+        if (turned && l < 2 * o8) {
+          float y[8];
+          widen<BF16>(other, y);
+          const float2* t = &sm.turn[r][l < o8 ? 8 * l : 8 * (l - o8)];
+          const float way = l < o8 ? -1.0f : 1.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = x[i] * t[i].x + way * (y[i] * t[i].y);
+        }
+      } else {  // partners across octets: the head through shared memory
+        float* head = sm.x + (tid - l) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) head[8 * l + i] = x[i];
+        __syncwarp();
+        if (turned) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = 8 * l + i;
+            if (e >= p.rot) break;
+            const float2 t = sm.turn[r][e < pairs ? e : e - pairs];
+            x[i] = e < pairs ? x[i] * t.x - head[e + pairs] * t.y : x[i] * t.x + head[e - pairs] * t.y;
+          }
+        }
+        __syncwarp();
+      }
+      const int page = p.Hkv > 0 ? sm.page[r] : 0;
+      if (h < p.Hq) {
+        if (live && page >= 0) {
+          const int64_t at = (row0 + r) * p.out_stride + h * D + 8 * l;
+          if constexpr (BF16)
+            store_bf16(p.q_out, at, x);
+          else
+            store_f32(p.q_out, at, x);
+        }
+        if (p.kv_dtype != KV_INT4 || p.Hkv == 0) continue;
+      }
+      const bool stored = live && page >= 0 && h >= p.Hq, is_v = h >= p.Hq + p.Hkv;
+      const int kvh = h - p.Hq - (is_v ? p.Hkv : 0);
+      const int64_t token = stored ? (static_cast<int64_t>(page) * p.Hkv + kvh) * p.P + sm.slot[r] : -1;
+      void* pool = is_v ? p.v_pool : p.k_pool;
+      if (p.kv_dtype == KV_INT4) {  // a reduction over the group: the warp's every lane takes part
+        store_int4<L>(pool, is_v ? p.v_ranges : p.k_ranges, token, l, x);
+      } else if (stored) {
+        const int64_t at = token * D + 8 * l;
+        if (p.kv_dtype == KV_F32) {
+          store_f32(pool, at, x);
+        } else if (p.kv_dtype == KV_BF16) {
+          if (BF16 && (is_v || p.rot == 0))  // a copy, whatever the bits
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at) =
+                make_uint4(raw[b].w[0], raw[b].w[1], raw[b].w[2], raw[b].w[3]);
+          else
+            store_bf16(pool, at, x);
+        } else {
+          const float scale = is_v ? p.v_scale_h[PA_HEAD(p, kvh)] : p.k_scale_h[PA_HEAD(p, kvh)];
+          uint32_t o[2] = {0u, 0u};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i / 4] |= encode_e4m3(x[i], scale) << (8 * (i % 4));
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at) = make_uint2(o[0], o[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) raw[b] = next[b];
+  }
+}
+
+// A thread per 8 elements of a (row, K or V, kv head).
+__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
+  const int octets = p.Hkv * p.D / 8;
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int sides = (p.k_out != nullptr) + (p.v_out != nullptr);
+  if (idx >= static_cast<int64_t>(p.n_rows) * sides * octets) return;
+  const int64_t row = idx / (sides * octets);
+  const int rem = static_cast<int>(idx % (sides * octets));
+  const bool is_v = p.k_out == nullptr || rem >= octets;
+  const int e = (rem >= octets ? rem - octets : rem) * 8, h = e / p.D, d = e % p.D;
+  const int seq = __ldg(p.seq_ids + row), pos = __ldg(p.positions + row);
+  int page = -1;
+  if (seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < static_cast<int64_t>(p.max_blocks) * p.P)
+    page = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + pos / p.P);
+  float x[8] = {};
+  if (page < 0 || page >= p.num_pages) {
+    if (rem == 0) record_error(p.status, ST_OUT_OF_RANGE);
+  } else {
+    const int64_t token = (static_cast<int64_t>(page) * p.Hkv + h) * p.P + (pos & (p.P - 1));
+    const int64_t at = token * p.D + d;
+    const void* pool = is_v ? p.v_pool : p.k_pool;
+    if (p.kv_dtype == KV_INT4) {
+      const uint32_t w = __ldg(static_cast<const uint32_t*>(pool) + at / 8);
+      const uint32_t range = __ldg(static_cast<const uint32_t*>(is_v ? p.v_ranges : p.k_ranges) + token);
+      const float step = __half2float(__ushort_as_half(static_cast<unsigned short>(range & 0xffffu)));
+      const float low = __half2float(__ushort_as_half(static_cast<unsigned short>(range >> 16)));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(static_cast<float>((w >> (4 * i)) & 15u), step, low);
+    } else if (p.kv_dtype == KV_E4M3) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + at));
+      const float scale = is_v ? p.v_scale_h[PA_HEAD(p, h)] : p.k_scale_h[PA_HEAD(p, h)];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 two = e4m3x2_to_float2((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
+        x[2 * i] = two.x * scale;
+        x[2 * i + 1] = two.y * scale;
+      }
+    } else if (p.kv_dtype == KV_BF16) {
+      widen<true>(load_octet<true>(pool, at), x);
+    } else {
+      widen<false>(load_octet<false>(pool, at), x);
+    }
+  }
+  void* out = is_v ? p.v_out : p.k_out;
+  const int64_t to = row * p.Hkv * p.D + e;
+  if (p.out_bf16)
+    store_bf16(out, to, x);
+  else
+    store_f32(out, to, x);
+}
+
+cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream) {
+  if (p.n_rows <= 0) return cudaSuccess;
+  const int per = p.n_rows <= 1024 ? 1 : p.n_rows <= 4096 ? 4 : kRowsPerCta;
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.n_rows) + per - 1) / per);
+  auto kernel = p.D == 128 ? (p.in_dtype == KV_BF16 ? rows_kernel<128, true> : rows_kernel<128, false>)
+                           : (p.in_dtype == KV_BF16 ? rows_kernel<64, true> : rows_kernel<64, false>);
+  kernel<<<grid, kRowsThreads, 0, stream>>>(p, per);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_read(const ReadParams& p, cudaStream_t stream) {
+  const int64_t sides = (p.k_out != nullptr) + (p.v_out != nullptr);
+  const int64_t blocks = (static_cast<int64_t>(p.n_rows) * sides * p.Hkv * p.D / 8 + 255) / 256;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  read_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace pa
+
+using pa::aligned;
+using pa::cuda_fail;
+using pa::elt_bytes;
+using pa::fail;
+
+struct pa_rope {
+  pa_rope_desc desc;
+  double frequencies[64];
+  double magnitude;
+  uint64_t turns[64];
+};
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+// rows of `elements` elements, `stride` apart, as the kernels read them
+pa_status check_stride(const char* name, const void* base, int64_t stride, int64_t elements, pa_dtype dtype) {
+  if (base == nullptr) return fail(PA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(base, 16)) return fail(PA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride < elements || stride * static_cast<int64_t>(elt_bytes(dtype)) % 16 != 0)
+    return fail(PA_ERR_INVALID_ARG, "%s rows of %lld elements, %lld apart: a multiple of 16 bytes, at least a row", name,
+                (long long)elements, (long long)stride);
+  if (stride > (1ll << 40)) return fail(PA_ERR_INVALID_ARG, "%s rows %lld elements apart", name, (long long)stride);
+  return PA_OK;
+}
+
+void set_rope(pa::RowsParams* p, const pa_rope* rope) {
+  p->sign = p->magnitude = 1.0f;
+  if (rope == nullptr) return;
+  p->rot = rope->desc.rotary_dim;
+  p->interleaved = rope->desc.layout == PA_ROPE_INTERLEAVED;
+  p->magnitude = static_cast<float>(rope->magnitude);
+  for (int i = 0; i < p->rot / 2; ++i) p->turns[i] = rope->turns[i];
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_rope_create(const pa_rope_desc* desc, pa_rope** out) {
+  if (out == nullptr) return fail(PA_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (desc == nullptr) return fail(PA_ERR_INVALID_ARG, "rope descriptor is NULL");
+  const pa_rope_desc& d = *desc;
+  const int r = d.rotary_dim;
+  if (r < 2 || r > 128 || r % 2 != 0) return fail(PA_ERR_INVALID_ARG, "rotary_dim %d is not an even number in [2, 128]", r);
+  if (d.layout != PA_ROPE_HALF && d.layout != PA_ROPE_INTERLEAVED) return fail(PA_ERR_INVALID_ARG, "unknown rope layout");
+  if (!(std::isfinite(d.base) && d.base > 1.0)) return fail(PA_ERR_INVALID_ARG, "rope base %g must be above 1", d.base);
+  if (d.scaling < PA_ROPE_NONE || d.scaling > PA_ROPE_BANDS) return fail(PA_ERR_INVALID_ARG, "unknown rope scaling");
+  if (d.scaling != PA_ROPE_NONE && !(std::isfinite(d.factor) && d.factor > 0.0))
+    return fail(PA_ERR_INVALID_ARG, "rope factor %g must be positive", d.factor);
+  const bool ranged = d.scaling == PA_ROPE_RAMP || d.scaling == PA_ROPE_BANDS;
+  if (ranged && (d.original_positions <= 0 || !(std::isfinite(d.high) && d.low > 0.0 && d.high > d.low)))
+    return fail(PA_ERR_INVALID_ARG, "rope ranges need original_positions > 0 and 0 < low < high");
+  if (d.scaling == PA_ROPE_BASE && r == 2) return fail(PA_ERR_INVALID_ARG, "a changed base needs rotary_dim > 2");
+  if (!(std::isfinite(d.magnitude) && d.magnitude >= 0.0))
+    return fail(PA_ERR_INVALID_ARG, "rope magnitude %g must not be negative", d.magnitude);
+  pa_rope* p = new (std::nothrow) pa_rope;
+  if (p == nullptr) return fail(PA_ERR_INVALID_ARG, "out of host memory");
+  p->desc = d;
+  p->magnitude = d.magnitude > 0.0 ? d.magnitude : d.scaling == PA_ROPE_RAMP ? 0.1 * std::log(d.factor) + 1.0 : 1.0;
+  const double base = d.scaling == PA_ROPE_BASE ? d.base * std::pow(d.factor, static_cast<double>(r) / (r - 2)) : d.base;
+  // PA_ROPE_RAMP: the pair index at which a pair turns t times over the original positions
+  auto index_of = [&](double t) { return r * std::log(d.original_positions / (kTwoPi * t)) / (2.0 * std::log(d.base)); };
+  double from = 0.0, to = 0.0;
+  if (d.scaling == PA_ROPE_RAMP) {
+    from = std::max(std::floor(index_of(d.high)), 0.0);
+    to = std::min(std::ceil(index_of(d.low)), r - 1.0);
+  }
+  for (int i = 0; i < r / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / r);
+    double keep = 1.0;  // the weight of the unchanged frequency
+    if (d.scaling == PA_ROPE_LINEAR) keep = 0.0;
+    if (d.scaling == PA_ROPE_RAMP) keep = 1.0 - std::min(std::max((i - from) / std::max(to - from, 0.001), 0.0), 1.0);
+    if (d.scaling == PA_ROPE_BANDS)
+      keep = std::min(std::max((d.original_positions * f / kTwoPi - d.low) / (d.high - d.low), 0.0), 1.0);
+    const double g = keep == 1.0 ? f : f / d.factor * (1.0 - keep) + f * keep;
+    p->frequencies[i] = g;
+    const double turn = std::fmod(g / kTwoPi, 1.0);
+    p->turns[i] = static_cast<uint64_t>(std::ldexp(turn, 63)) * 2;  // (2^64 itself would not fit)
+  }
+  *out = p;
+  return PA_OK;
+}
+
+void pa_rope_destroy(pa_rope* rope) { delete rope; }
+
+pa_status pa_rope_frequencies(const pa_rope* rope, double* frequencies, double* magnitude) {
+  if (rope == nullptr) return fail(PA_ERR_INVALID_ARG, "rope is NULL");
+  for (int i = 0; frequencies != nullptr && i < rope->desc.rotary_dim / 2; ++i) frequencies[i] = rope->frequencies[i];
+  if (magnitude != nullptr) *magnitude = rope->magnitude;
+  return PA_OK;
+}
+
+pa_status pa_rope_rows(const pa_rope* rope, int32_t n_rows, const void* x, int64_t x_stride, void* out,
+                       int64_t out_stride, pa_dtype dtype, int32_t n_heads, int32_t head_dim, const int32_t* positions,
+                       int32_t inverse, void* stream) {
+  if (rope == nullptr) return fail(PA_ERR_INVALID_ARG, "rope is NULL");
+  if (n_rows < 0) return fail(PA_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
+  if (dtype != PA_F32 && dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "rope rows are f32 or bf16");
+  if (head_dim != 64 && head_dim != 128) return fail(PA_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", head_dim);
+  if (rope->desc.rotary_dim > head_dim)
+    return fail(PA_ERR_INVALID_ARG, "rotary_dim %d of head_dim %d", rope->desc.rotary_dim, head_dim);
+  if (n_heads <= 0 || n_heads > (1 << 16)) return fail(PA_ERR_INVALID_ARG, "n_heads %d not in [1, 65536]", n_heads);
+  if (n_rows == 0) return PA_OK;
+  const int64_t row = static_cast<int64_t>(n_heads) * head_dim;
+  pa_status st = check_stride("x", x, x_stride, row, dtype);
+  if (st == PA_OK) st = check_stride("out", out, out_stride, row, dtype);
+  if (st != PA_OK) return st;
+  if (positions == nullptr) return fail(PA_ERR_INVALID_ARG, "positions is NULL");
+  if (out == x && out_stride != x_stride) return fail(PA_ERR_INVALID_ARG, "in place the two strides are the same");
+  pa::RowsParams p{};
+  p.q = x;
+  p.q_out = out;
+  p.q_stride = x_stride;
+  p.out_stride = out_stride;
+  p.positions = positions;
+  p.n_rows = n_rows;
+  p.Hq = n_heads;
+  p.D = head_dim;
+  p.P = 16;  // (no page is looked up)
+  p.in_dtype = dtype == PA_F32 ? pa::KV_F32 : pa::KV_BF16;
+  set_rope(&p, rope);
+  if (inverse != 0) p.sign = -1.0f;
+  const cudaError_t e = pa::launch_rows(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "rope launch");
+}
+
+pa_status pa_rope_append(const pa_pool* pool, const pa_rope* rope, int32_t n_rows, const void* q, int64_t q_stride,
+                         int32_t num_q_heads, void* q_out, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, pa_dtype dtype, const int32_t* seq_ids, const int32_t* positions,
+                         const int32_t* block_tables, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t* status_dev,
+                         void* stream) {
+  if (pool == nullptr) return fail(PA_ERR_INVALID_ARG, "pool is NULL");
+  const pa_pool_desc& d = pool->desc;
+  if (n_rows < 0) return fail(PA_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
+  if (dtype != PA_F32 && dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "rope rows are f32 or bf16");
+  if (num_q_heads < 0 || num_q_heads > (1 << 16))
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d not in [0, 65536]", num_q_heads);
+  if (rope != nullptr && rope->desc.rotary_dim > d.head_dim)
+    return fail(PA_ERR_INVALID_ARG, "rotary_dim %d of head_dim %d", rope->desc.rotary_dim, d.head_dim);
+  if (num_seqs <= 0 || max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG, "num_seqs and max_blocks_per_seq must be positive");
+  if (d.num_kv_heads > (1 << 16)) return fail(PA_ERR_UNSUPPORTED, "%d kv heads", d.num_kv_heads);
+  if (n_rows == 0) return PA_OK;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * d.head_dim, kv_row = static_cast<int64_t>(d.num_kv_heads) * d.head_dim;
+  pa_status st = PA_OK;
+  if (num_q_heads > 0) {
+    st = check_stride("q", q, q_stride, q_row, dtype);
+    if (st == PA_OK) st = check_stride("q_out", q_out, q_row, q_row, dtype);
+    if (st == PA_OK && q_out == q && q_stride != q_row)
+      return fail(PA_ERR_INVALID_ARG, "q_out is contiguous; in place q has to be, too");
+  }
+  if (st == PA_OK) st = check_stride("k", k, k_stride, kv_row, dtype);
+  if (st == PA_OK) st = check_stride("v", v, v_stride, kv_row, dtype);
+  if (st != PA_OK) return st;
+  if (!seq_ids || !positions || !block_tables) return fail(PA_ERR_INVALID_ARG, "rope append: a device pointer is NULL");
+  pa::RowsParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.out_stride = q_row;
+  p.k_pool = pool->k;
+  p.v_pool = pool->v;
+  p.k_ranges = pool->k_ranges;
+  p.v_ranges = pool->v_ranges;
+  p.seq_ids = seq_ids;
+  p.positions = positions;
+  p.block_tables = block_tables;
+  p.n_rows = n_rows;
+  p.num_seqs = num_seqs;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_pages = d.num_pages;
+  p.P = d.page_size;
+  p.Hq = num_q_heads;
+  p.Hkv = d.num_kv_heads;
+  p.D = d.head_dim;
+  p.in_dtype = dtype == PA_F32 ? pa::KV_F32 : pa::KV_BF16;
+  p.kv_dtype = static_cast<int32_t>(d.kv_dtype);
+  p.head_scales = pool->head_scales ? 1 : 0;
+  for (int h = 0; h < (pool->head_scales ? d.num_kv_heads : 1); ++h) {
+    p.k_scale_h[h] = pool->head_scales ? pool->k_scale_h[h] : d.k_scale;
+    p.v_scale_h[h] = pool->head_scales ? pool->v_scale_h[h] : d.v_scale;
+  }
+  p.status = status_dev;
+  set_rope(&p, rope);
+  const cudaError_t e = pa::launch_rows(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "rope append launch");
+}
+
+pa_status pa_read_kv(const pa_pool* pool, int32_t n_rows, const int32_t* seq_ids, const int32_t* positions,
+                     const int32_t* block_tables, int32_t num_seqs, int32_t max_blocks_per_seq, void* k_out,
+                     void* v_out, pa_dtype out_dtype, int32_t* status_dev, void* stream) {
+  if (pool == nullptr) return fail(PA_ERR_INVALID_ARG, "pool is NULL");
+  const pa_pool_desc& d = pool->desc;
+  if (n_rows < 0) return fail(PA_ERR_INVALID_ARG, "n_rows %d < 0", n_rows);
+  if (out_dtype != PA_F32 && out_dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "read output dtype must be f32 or bf16");
+  if (num_seqs <= 0 || max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG, "num_seqs and max_blocks_per_seq must be positive");
+  if (n_rows == 0 || (k_out == nullptr && v_out == nullptr)) return PA_OK;
+  if (!seq_ids || !positions || !block_tables) return fail(PA_ERR_INVALID_ARG, "read: a device pointer is NULL");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(PA_ERR_INVALID_ARG, "k_out / v_out must be 16-byte aligned");
+  if (static_cast<int64_t>(d.num_kv_heads) * d.head_dim > (1 << 28)) return fail(PA_ERR_UNSUPPORTED, "%d kv heads", d.num_kv_heads);
+  pa::ReadParams p{};
+  p.k_pool = pool->k;
+  p.v_pool = pool->v;
+  p.k_ranges = pool->k_ranges;
+  p.v_ranges = pool->v_ranges;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.seq_ids = seq_ids;
+  p.positions = positions;
+  p.block_tables = block_tables;
+  p.n_rows = n_rows;
+  p.num_seqs = num_seqs;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_pages = d.num_pages;
+  p.P = d.page_size;
+  p.Hkv = d.num_kv_heads;
+  p.D = d.head_dim;
+  p.out_bf16 = out_dtype == PA_BF16;
+  p.kv_dtype = static_cast<int32_t>(d.kv_dtype);
+  p.head_scales = pool->head_scales ? 1 : 0;
+  for (int h = 0; h < (pool->head_scales ? d.num_kv_heads : 1); ++h) {
+    p.k_scale_h[h] = pool->head_scales ? pool->k_scale_h[h] : d.k_scale;
+    p.v_scale_h[h] = pool->head_scales ? pool->v_scale_h[h] : d.v_scale;
+  }
+  p.status = status_dev;
+  const cudaError_t e = pa::launch_read(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "read launch");
+}
+
+}  // extern "C"
