@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     // the values of a block with masked keys are looked over: in turn, as the look may be a unit ahead of the
     // MMAs, and a unit has at most two such blocks
     VOK = PV + 2,
-    DRAIN = VOK + 4,
+    VIN = VOK + 4,               // its load is under way (the ring's slot has come to this tile)
+    DRAIN = VIN + 4,
     STALL,
     COUNT
   };
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrOtherRegs));
     if (warp == 8 && lane == 0) {
       // ---- loads
-      int item = 0, done[2] = {0, 0};  // tiles of K and V, query tiles issued so far
+      int item = 0, checked = 0, done[2] = {0, 0};  // tiles of K and V, those to be looked over, query tiles issued so far
       bool ok = !p.debug_stall || wait(STALL, 0);  // (runs out by construction)
       PromptUnit x{};
       for (int k = 0; ok && unit_at(k, x); ++k) {
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           for (int hf = 0; hf < S::NH; ++hf)
             pr_load_3d(sm + S::RING + s * S::TILE + hf * S::HALF, (j & 1) ? &p.vmap : &p.kmap, hf * 64, x.head[0] / p.G,
                        x.begin + (j >> 1) * kPrTile, &bar[FULL + s]);
+          if ((j & 1) && (j >> 1) >= x.blocks[0] - 1) mbar_arrive(&bar[VIN + (checked++ & 3)]);
           ++item;
         }
       }
@@ -353,7 +355,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         if (x.n == 0) continue;
         for (int j = x.blocks[0] - 1; ok && j < x.n; ++j, ++checked) {
           const int item = base + 2 * j + 1;
-          ok = __all_sync(0xffffffffu, wait(FULL + item % S::STAGES, (item / S::STAGES) & 1));
+          ok = __all_sync(0xffffffffu, wait(VIN + (checked & 3), (checked >> 2) & 1) &&
+                                           wait(FULL + item % S::STAGES, (item / S::STAGES) & 1));
           if (!ok) break;
           uint4* tile = reinterpret_cast<uint4*>(sm + S::RING + (item % S::STAGES) * S::TILE);
           bool found = false;
@@ -413,9 +416,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         const bool move = (top - m) * p.scale_log2 > kRescaleSlack;
         if (__any_sync(0xffffffffu, move)) {
           if (j > 0) {
-            ok = __all_sync(0xffffffffu, wait(PV + t, (count - 1) & 1));
-            if (!ok) break;
-            tc::fence_after_sync();
+            // (the scores' commit came behind the last block's product with V: O stands still)
             const float f = move ? ex2((m - top) * p.scale_log2) : 1.0f;
             l *= f;
 #pragma unroll
