@@ -5,25 +5,25 @@
 // 32-token stages in turn, each through a ring of its own of bulk copies, and are merged
 // at the end in a fixed order.  The ranges never touch the products' inner loops:
 //   q . K[t]  = step_t (q . c_t) + low_t sum(q)
-//   sum_t p_t V[t] = sum_t (p_t step_t) c_t + sum_t p_t low_t
-// so codes go into the tensor cores as they are.  A code becomes a bf16 number by placing its bits in
-// the mantissa of 16.0 (0x4180 | c << 3 is 16 + c): a shift and one logic operation for two
-// codes.  For K the 16 stays, and 16 step sum(q) is subtracted from the score; for V, whose
-// sums run over thousands of tokens and cancel, 24 is subtracted first (c - 8, exact), and
-// sum p (low + 8 step) is added: the accumulators then hold no offset larger than the result.
+//   sum_t p_t V[t] = sum_t (p_t step_t) (c_t - 8) + sum_t p_t (low_t + 8 step_t)
 //
-// m16n8k16 products, bf16 operands, FP32 sums.  The 16 rows are the kv head's G <= 8 query
-// heads twice: rows g + 8 carry what rows g lack.  Scores of f32 queries: rows g the upper, rows
-// g + 8 the middle eight bits, and a second product for the lower ones.  Weights: w = p step as
-// bf16 and, in rows g + 8, the bf16 of the rest (16 bits in all).
-//   B of scores (K): lane 4 n + c holds words 4c.. of token n's row, so the k index of an MMA is a
-//   permutation of head elements, the same one in A (the queries, prepared once).
-//   B of outputs (V): lane 4 n + c holds words of tokens 2c, 2c + 1, 2c + 8, 2c + 9; byte permutes pair
-//   two tokens' codes, and n is a permutation of head elements undone at the end.
+// A code needs no conversion: the f16 number with the bits 0x000c is c 2^-24, 0x00c0 is c 2^-20 (subnormal
+// numbers run on into the first normal ones), and the tensor cores take them at full rate.  So one shift and four
+// masks turn a word into the operands of eight codes; the powers of two go into the queries and the result.
+//   scores: S^T = K Q^T, m16n8k16, A = 16 tokens, B = the kv head's G <= 8 query heads.  Lane 4 g + c holds
+//     words 4c.. of tokens g and g + 8; the k index is a permutation of head elements, the same one in B.
+//   outputs: O^T += V^T P^T, A = 16 head elements x 16 tokens from words of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+//     (a byte permute pairs two tokens), B = the weights, moved into fragment order with movmatrix.
+// Queries are f16, a row scaled by a power of two below 2^15 (bf16 numbers are exact down to 2^-27 of the row's
+// largest); f32 queries in two parts (22 bits).  A weight w = p step is f16 relative to a running
+// reference, w = 2^(s - R) step <= 2^8, in one part for bf16 outputs (2^-11) and two for f32 ones (2^-22).  The
+// weights' sum as the products saw them comes out of a tile of ones, so that the 8 is subtracted exactly: the
+// result then holds no offset larger than itself.
+// (m16n8k32 on e4m3 bytes, where c is c 2^-9 as well, would need fewer operations, but is not native here: two f16
+// products and the conversions, 963 warp instructions for a stage.)
 //
-// What bounds it: the read of D + 8 bytes per token and kv head at HBM rate, with the
-// conversions close behind (about 270 warp instructions for 16 tokens at D = 128, where
-// HBM brings them in 90 clocks).
+// What bounds it: the read of D + 8 bytes per token and kv head at HBM rate; next are the logic
+// operations (about 200 of a warp for 32 tokens at D = 128, two to a clock, where HBM takes 186 clocks).
 #include "pa_decode_mma.cuh"
 
 namespace pa {
@@ -55,161 +55,175 @@ __host__ __device__ constexpr size_t i4_smem() {
   return (sizeof(I4Header) + 127) / 128 * 128 + I4Geom<D>::RING;
 }
 
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Codes s and s + 4 of a word (or code s of two tokens' halves) as bf16 16 + c.
-template <int S>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  const uint32_t moved = S == 0 ? w << 3 : w >> (4 * S - 3);
-  return (moved & 0x00780078u) | 0x41804180u;
-}
-
-__device__ __forceinline__ uint32_t minus24(uint32_t x) {  // 16 + c -> c - 8, exact
-  const uint32_t c = 0xc1c0c1c0u;  // bf16 -24, twice
-  const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 __device__ __forceinline__ float2 range_of(uint32_t w) {  // (step, low)
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-__device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
-
-// Stage n of a warp (tokens t0 .. of the unit's pages) into its ring slot: pieces of 32 tokens or
-// of one page; pages behind the unit's last are left out (their slots are masked).
+// A warp's copies.  A stage is eight of them at most, codes and ranges of K and V for each of one or two
+// pieces (32 tokens, or a page of 16): a lane each, so that their addresses are worked out together.
 template <int D>
-__device__ __forceinline__ void i4_issue(const AttnParams& p, const I4Header* hdr, unsigned char* st, uint64_t* bar, int t0,
-                                         int j0, int npg, int h, int lg_p) {
-  using Geo = I4Geom<D>;
-  const int P = 1 << lg_p, piece = min(P, kI4Tokens);
-  const uint64_t policy = l2_policy_evict_first();
-  int pieces = 0;
-  for (int i = 0; i < kI4Tokens / piece; ++i) pieces += ((t0 + i * piece) >> lg_p) - j0 < npg ? 1 : 0;
-  mbar_arrive_expect_tx(bar, static_cast<uint32_t>(pieces * piece * (2 * Geo::ROW + 8)));
-  for (int i = 0; i < pieces; ++i) {
-    const int t = t0 + i * piece;
-    const int64_t token = (static_cast<int64_t>(hdr->pid[(t >> lg_p) - j0]) * p.Hkv + h) * P + (t & (P - 1));
-    const int at = i * piece;
-    bulk_g2s(st + Geo::K + at * Geo::ROW, static_cast<const unsigned char*>(p.k_pool) + token * Geo::ROW, piece * Geo::ROW, bar, policy);
-    bulk_g2s(st + Geo::KR + at * 4, static_cast<const unsigned char*>(p.k_ranges) + token * 4, piece * 4, bar, policy);
-    bulk_g2s(st + Geo::V + at * Geo::ROW, static_cast<const unsigned char*>(p.v_pool) + token * Geo::ROW, piece * Geo::ROW, bar, policy);
-    bulk_g2s(st + Geo::VR + at * 4, static_cast<const unsigned char*>(p.v_ranges) + token * 4, piece * 4, bar, policy);
+struct I4Copies {
+  const unsigned char* base;  // of the lane's kind: K codes, K ranges, V codes, V ranges
+  uint64_t policy;
+  int token_bytes, to;        // bytes of a token, offset of the lane's piece in a stage
+  int lg_p, piece, first;     // tokens of a piece, the lane's first token in a stage
+
+  __device__ __forceinline__ I4Copies(const AttnParams& p, int lg_p_, int lane) : lg_p(lg_p_) {
+    using Geo = I4Geom<D>;
+    const int kind = lane & 3;
+    base = static_cast<const unsigned char*>(kind == 0 ? p.k_pool : kind == 1 ? p.k_ranges : kind == 2 ? p.v_pool : p.v_ranges);
+    policy = l2_policy_evict_first();
+    token_bytes = (kind & 1) ? 4 : Geo::ROW;
+    piece = min(1 << lg_p, kI4Tokens);
+    first = (lane >> 2) * piece;
+    to = (kind == 0 ? Geo::K : kind == 1 ? Geo::KR : kind == 2 ? Geo::V : Geo::VR) + first * token_bytes;
   }
+  // Tokens t0 .. of the unit's pages into the stage at `st`; pages behind the unit's last are left out (their
+  // slots are masked).
+  __device__ __forceinline__ void issue(const AttnParams& p, const I4Header* hdr, unsigned char* st, uint64_t* bar, int t0,
+                                        int j0, int npg, int h, int lane) const {
+    const int t = t0 + first, page = (t >> lg_p) - j0;
+    const bool mine = first < kI4Tokens && page < npg;
+    const int copies = __popc(__ballot_sync(0xffffffffu, mine));
+    if (lane == 0) {
+      fence_proxy_async();
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>((copies >> 2) * piece * (2 * I4Geom<D>::ROW + 8)));
+    }
+    __syncwarp();
+    if (mine) {
+      const int64_t token = ((static_cast<int64_t>(hdr->pid[page]) * p.Hkv + h) << lg_p) + (t & ((1 << lg_p) - 1));
+      bulk_g2s(st + to, base + token * token_bytes, piece * token_bytes, bar, policy);
+    }
+  }
+};
+
+// Codes 2 s and 2 s + 1 (s = 0, 1) of both halves of a word: c 2^-24 and c 2^-20 as f16.
+template <int S>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
+  const uint32_t x = S == 0 ? w : w >> 8;
+  even = x & 0x000f000fu;
+  odd = x & 0x00f000f0u;
 }
 
 template <int D, bool QF32>
 struct I4State {
-  uint32_t qa[D / 16][QF32 ? 4 : 2];  // A of scores: (row g, row g + 8) x k halves; bf16 queries leave rows g + 8 zero
-  uint32_t ql[QF32 ? D / 16 : 1][2];  // the lower part of f32 queries
-  float qsum;                         // sum of the row's query
-  float m, l;                         // running reference (log2 domain) and this lane's part of the sum
-  float fix;                          // this lane's part of sum p (low + 8 step)
-  float o[I4Geom<D>::NW][8][4];
+  static constexpr int PARTS = QF32 ? 2 : 1;
+  uint32_t q[PARTS][D / 16][2];       // B of scores: head g
+  float dot_scale[2], low_scale[2];   // of heads 2c, 2c + 1: a score is step (sum dot_scale) + low low_scale (log2 domain)
+  float r[2], l[2], fix[2];           // reference; this lane's parts of sum p and sum p (low + 8 step)
+  float o[I4Geom<D>::NW][4][4];       // head elements (2 to a lane's tile) x heads 2c, 2c + 1
+  float ones[4];                      // the weights' sums
 };
 
+constexpr float kI4Top = 8.0f, kI4Start = 6.0f;  // log2 of the largest weight: what it may reach, where the reference puts it
+
 // One stage: scores of 32 tokens, the softmax update, the outputs.
-template <int D, bool QF32>
-__device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned char* sm, int n_valid, float scale, int lane) {
+template <int D, bool QF32, bool WHOLE>
+__device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned char* sm, int n_valid, int lane) {
   using Geo = I4Geom<D>;
+  constexpr int PARTS = I4State<D, QF32>::PARTS;
   const int g = lane >> 2, c = lane & 3;
-  float s[4][4];
+  // e[i][k]: token 8 i + g, head 2c + k
+  float e[4][2];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.0f;
-    uint32_t w[D / 32];
-    const unsigned char* row = sm + Geo::K + (8 * u + g) * Geo::ROW;
-    if constexpr (D == 128) {
-      const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * c);
-      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * c);
-      w[0] = x.x; w[1] = x.y;
+  for (int u = 0; u < 2; ++u) {  // 16 tokens
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t w[2][D / 32];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const unsigned char* row = sm + Geo::K + (16 * u + 8 * h + g) * Geo::ROW;
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * c);
+        w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * c);
+        w[h][0] = x.x; w[h][1] = x.y;
+      }
     }
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const uint32_t b[4] = {codes_bf16<0>(w[i]), codes_bf16<1>(w[i]), codes_bf16<2>(w[i]), codes_bf16<3>(w[i])};
+      uint32_t a[4];
+      codes_f16<0>(w[0][i], a[0], a[2]);
+      codes_f16<0>(w[1][i], a[1], a[3]);
 #pragma unroll
-      for (int sp = 0; sp < 2; ++sp) {
-        const int k = 2 * i + sp;
-        if constexpr (QF32) {
-          mma_bf16_16816(s[u], st.qa[k], b[2 * sp], b[2 * sp + 1]);
-          const uint32_t lo[4] = {st.ql[k][0], 0u, st.ql[k][1], 0u};
-          mma_bf16_16816(s[u], lo, b[2 * sp], b[2 * sp + 1]);
-        } else {
-          const uint32_t a[4] = {st.qa[k][0], 0u, st.qa[k][1], 0u};
-          mma_bf16_16816(s[u], a, b[2 * sp], b[2 * sp + 1]);
-        }
-      }
+      for (int part = 0; part < PARTS; ++part) mma_f16_16816(s, a, st.q[part][2 * i][0], st.q[part][2 * i][1]);
+      codes_f16<1>(w[0][i], a[0], a[2]);
+      codes_f16<1>(w[1][i], a[1], a[3]);
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) mma_f16_16816(s, a, st.q[part][2 * i + 1][0], st.q[part][2 * i + 1][1]);
+    }
+    e[2 * u][0] = s[0];
+    e[2 * u][1] = s[1];
+    e[2 * u + 1][0] = s[2];
+    e[2 * u + 1][1] = s[3];
+  }
+  float2 v[4];
+  float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t kw = *reinterpret_cast<const uint32_t*>(sm + Geo::KR + (8 * i + g) * 4);
+    uint32_t vw = *reinterpret_cast<const uint32_t*>(sm + Geo::VR + (8 * i + g) * 4);
+    const bool valid = WHOLE || 8 * i + g < n_valid;
+    if (!valid) kw = vw = 0u;  // ranges of unused slots may be anything
+    const float2 k = range_of(kw);
+    v[i] = range_of(vw);
+    float lg;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(fabsf(v[i].x) + 0x1p-24f));  // (rows of one value have step 0)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      e[i][h] = fmaf(k.x, e[i][h] * st.dot_scale[h], k.y * st.low_scale[h]);
+      if (!valid) e[i][h] = -INFINITY;
+      top[h] = fmaxf(top[h], e[i][h] + lg);
     }
   }
-  // scores in the log2 domain, tokens 8u + 2c + i
-  float mx = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const uint2 rw = *reinterpret_cast<const uint2*>(sm + Geo::KR + (8 * u + 2 * c) * 4);
-    const float2 r0 = range_of(rw.x), r1 = range_of(rw.y);
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float step = i == 0 ? r0.x : r1.x, low = i == 0 ? r0.y : r1.y;
-      const float dot = QF32 ? s[u][i] + s[u][2 + i] : s[u][i];
-      const float x = fmaf(step, dot, fmaf(-16.0f, step, low) * st.qsum) * scale;
-      s[u][i] = 8 * u + 2 * c + i < n_valid ? x : -INFINITY;
-      mx = fmaxf(mx, s[u][i]);
+    for (int d = 4; d < 32; d *= 2) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], d));
+  if (__any_sync(0xffffffffu, top[0] - st.r[0] > kI4Top || top[1] - st.r[1] > kI4Top)) {
+    float f[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool move = top[h] - st.r[h] > kI4Top;
+      const float r = move ? top[h] - kI4Start : st.r[h];
+      f[h] = move ? ex2(st.r[h] - r) : 1.0f;  // (the first time: 2^-inf)
+      st.r[h] = r;
+      st.l[h] *= f[h];
+      st.fix[h] *= f[h];
+      st.ones[h] *= f[h];
     }
-  }
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  // the reference moves only when a score passes it by kRescaleSlack (weights stay below 2^8)
-  const bool move = mx - st.m > kRescaleSlack;
-  if (__any_sync(0xffffffffu, move)) {
-    const float f = move ? ex2(st.m - mx) : 1.0f;  // (the first time: 2^-inf)
-    if (move) st.m = mx;
-    st.l *= f;
-    st.fix *= f;
 #pragma unroll
     for (int i = 0; i < Geo::NW; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        st.o[i][j][0] *= f;
-        st.o[i][j][1] *= f;
-        st.o[i][j][2] *= f;
-        st.o[i][j][3] *= f;
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st.o[i][j][k] *= f[k & 1];
   }
-  const float m = st.m == -INFINITY ? 0.0f : st.m;
+  // weights of token 8 i + g as (head 2c, head 2c + 1), transposed into (tokens 8 i + 2c, + 1) of head g
+  uint32_t b[PARTS][4];
+  const float r0 = st.r[0] == -INFINITY ? 0.0f : st.r[0], r1 = st.r[1] == -INFINITY ? 0.0f : st.r[1];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {  // 16 tokens each
-    uint32_t a[4];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int u = 2 * half + v;
-      const uint2 rw = *reinterpret_cast<const uint2*>(sm + Geo::VR + (8 * u + 2 * c) * 4);
-      const float2 r0 = range_of(rw.x), r1 = range_of(rw.y);
-      float w[2], rest[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float step = i == 0 ? r0.x : r1.x, low = i == 0 ? r0.y : r1.y;
-        const bool valid = 8 * u + 2 * c + i < n_valid;
-        const float e = ex2(s[u][i] - m);
-        st.l += e;
-        st.fix = valid ? fmaf(e, fmaf(8.0f, step, low), st.fix) : st.fix;  // (ranges of unused slots may be anything)
-        const float x = valid ? e * step : 0.0f;
-        w[i] = x;
-        rest[i] = x - bf16_round(x);
-      }
-      a[2 * v] = pack_bf16x2(w[0], w[1]);
-      a[2 * v + 1] = pack_bf16x2(rest[0], rest[1]);
+  for (int i = 0; i < 4; ++i) {
+    const float p0 = ex2(e[i][0] - r0), p1 = ex2(e[i][1] - r1);
+    const float low8 = fmaf(8.0f, v[i].x, v[i].y);
+    st.l[0] += p0;
+    st.l[1] += p1;
+    st.fix[0] = fmaf(p0, low8, st.fix[0]);
+    st.fix[1] = fmaf(p1, low8, st.fix[1]);
+    const float w0 = p0 * v[i].x, w1 = p1 * v[i].x;
+    const uint32_t hi = pack_f16x2(w0, w1);
+    b[0][i] = movmatrix_trans(hi);
+    if constexpr (QF32) {
+      const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      b[PARTS - 1][i] = movmatrix_trans(pack_f16x2(w0 - back.x, w1 - back.y));
     }
-    uint32_t x[4][Geo::NW];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9 of the 16
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {  // 16 tokens
+    uint32_t x[4][Geo::NW];      // tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const unsigned char* row = sm + Geo::V + (16 * half + 2 * c + (t & 1) + 8 * (t >> 1)) * Geo::ROW;
+      const unsigned char* row = sm + Geo::V + (16 * u + 2 * c + (t & 1) + 8 * (t >> 1)) * Geo::ROW;
       if constexpr (D == 128) {
         const uint2 y = *reinterpret_cast<const uint2*>(row + 8 * g);
         x[t][0] = y.x;
@@ -218,19 +232,89 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
         x[t][0] = *reinterpret_cast<const uint32_t*>(row + 4 * g);
       }
     }
+    const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 #pragma unroll
-    for (int i = 0; i < Geo::NW; ++i) {
+    for (int part = 0; part < PARTS; ++part) mma_f16_16816(st.ones, one, b[part][2 * u], b[part][2 * u + 1]);
+#pragma unroll
+    for (int i = 0; i < Geo::NW; ++i)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {  // codes 4q .. 4q + 3 of the word
         const uint32_t z0 = __byte_perm(x[0][i], x[1][i], q == 0 ? 0x5410 : 0x7632);
         const uint32_t z1 = __byte_perm(x[2][i], x[3][i], q == 0 ? 0x5410 : 0x7632);
-        mma_bf16_16816(st.o[i][4 * q + 0], a, minus24(codes_bf16<0>(z0)), minus24(codes_bf16<0>(z1)));
-        mma_bf16_16816(st.o[i][4 * q + 1], a, minus24(codes_bf16<1>(z0)), minus24(codes_bf16<1>(z1)));
-        mma_bf16_16816(st.o[i][4 * q + 2], a, minus24(codes_bf16<2>(z0)), minus24(codes_bf16<2>(z1)));
-        mma_bf16_16816(st.o[i][4 * q + 3], a, minus24(codes_bf16<3>(z0)), minus24(codes_bf16<3>(z1)));
+        uint32_t a[4];
+        codes_f16<0>(z0, a[0], a[1]);
+        codes_f16<0>(z1, a[2], a[3]);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) mma_f16_16816(st.o[i][2 * q], a, b[part][2 * u], b[part][2 * u + 1]);
+        codes_f16<1>(z0, a[0], a[1]);
+        codes_f16<1>(z1, a[2], a[3]);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) mma_f16_16816(st.o[i][2 * q + 1], a, b[part][2 * u], b[part][2 * u + 1]);
       }
+  }
+}
+
+// The row's query (head g of the group; heads >= G are zero) as B operands, and the scores' factors.
+template <int D, bool QF32>
+__device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& st, size_t out_row, int G, int lane) {
+  using Geo = I4Geom<D>;
+  const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < Geo::NW; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) st.o[i][j][0] = st.o[i][j][1] = st.o[i][j][2] = st.o[i][j][3] = 0.0f;
+  st.ones[0] = st.ones[1] = st.ones[2] = st.ones[3] = 0.0f;
+  float q[D / 4], sum = 0.0f, big = 0.0f;
+  bool finite = true;
+  const size_t base = (out_row + (g < G ? g : 0)) * D + (D / 4) * c;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    float x[8];
+    load_q_vec<8>(p.q, !QF32, base + 8 * i, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      q[8 * i + j] = g < G ? x[j] : 0.0f;
+      sum += q[8 * i + j];
+      big = fmaxf(big, fabsf(q[8 * i + j]));
+      finite = finite && fabsf(q[8 * i + j]) < INFINITY;
     }
   }
+#pragma unroll
+  for (int d = 1; d < 4; d *= 2) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+    finite = __shfl_xor_sync(0xffffffffu, static_cast<int>(finite), d) != 0 && finite;
+  }
+  // the largest element into [2^14, 2^15): times 2^(14 - its exponent), a normal number either way
+  const int exponent = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 127);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - exponent) << 23);
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + exponent) << 23);
+  // codes count in 2^-24; a query with an infinity or NaN makes its scores NaN
+  const float dot = finite ? down * 0x1p24f * p.qk_scale_log2_h[0] : __uint_as_float(0x7fc00000u);
+  const float low = sum * p.qk_scale_log2_h[0];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // head h2 sits in lanes 4 h2 ..
+    st.dot_scale[h] = __shfl_sync(0xffffffffu, dot, 4 * (2 * c + h));
+    st.low_scale[h] = __shfl_sync(0xffffffffu, low, 4 * (2 * c + h));
+    st.r[h] = -INFINITY;
+    st.l[h] = st.fix[h] = 0.0f;
+  }
+  // k-step 2 i + s: elements 2 s, 2 s + 4 and, as codes there count in 2^-20, a sixteenth of 2 s + 1, 2 s + 5
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int odd = 0; odd < 2; ++odd) {
+        const float f = odd ? up * 0.0625f : up;
+        const float x = q[8 * i + 2 * s + odd] * f, y = q[8 * i + 2 * s + odd + 4] * f;
+        const uint32_t hi = pack_f16x2(x, y);
+        st.q[0][2 * i + s][odd] = hi;
+        if constexpr (QF32) {
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          st.q[1][2 * i + s][odd] = pack_f16x2(x - back.x, y - back.y);
+        }
+      }
 }
 
 template <int D, bool QF32>
@@ -287,50 +371,15 @@ __global__ void __launch_bounds__(32 * kI4Warps, 3) decode_int4_kernel(const __g
   // warp w takes stages w, w + kI4Warps, ..
   unsigned char* ring = rings + static_cast<size_t>(warp) * kI4Stages * Geo::STAGE;
   const int mine = bad || warp >= nstage ? 0 : (nstage - warp + kI4Warps - 1) / kI4Warps;
+  const I4Copies<D> copies(p, lg_p, lane);
   auto issue = [&](int n) {
-    i4_issue<D>(p, hdr, ring + (n % kI4Stages) * Geo::STAGE, &hdr->full[warp][n % kI4Stages],
-                t_begin + (warp + n * kI4Warps) * kI4Tokens, j0, npg, h, lg_p);
+    copies.issue(p, hdr, ring + (n % kI4Stages) * Geo::STAGE, &hdr->full[warp][n % kI4Stages],
+                 t_begin + (warp + n * kI4Warps) * kI4Tokens, j0, npg, h, lane);
   };
-  if (lane == 0)
-    for (int n = 0; n < min(mine, kI4Stages); ++n) issue(n);
+  for (int n = 0; n < min(mine, kI4Stages); ++n) issue(n);
 
   I4State<D, QF32> st;
-  st.m = -INFINITY;
-  st.l = st.fix = st.qsum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < Geo::NW; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) st.o[i][j][0] = st.o[i][j][1] = st.o[i][j][2] = st.o[i][j][3] = 0.0f;
-  {
-    // k-step (word i, sp) of lane c: elements e + 2 sp + {0, 4} and e + 2 sp + 1 + {0, 4}, e = (D / 4) c + 8 i
-    const size_t base = (out_row + (g < G ? g : 0)) * D + (D / 4) * c;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      float q[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        q[j] = g < G ? load_q(p.q, !QF32, base + 8 * i + j) : 0.0f;
-        st.qsum += q[j];
-      }
-#pragma unroll
-      for (int sp = 0; sp < 2; ++sp)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float x = q[2 * sp + hf], y = q[2 * sp + hf + 4];
-          if constexpr (QF32) {
-            const float x1 = x - bf16_round(x), y1 = y - bf16_round(y);
-            const float x2 = x1 - bf16_round(x1), y2 = y1 - bf16_round(y1);
-            st.qa[2 * i + sp][2 * hf] = pack_bf16x2(x, y);
-            st.qa[2 * i + sp][2 * hf + 1] = pack_bf16x2(x1, y1);
-            st.ql[2 * i + sp][hf] = pack_bf16x2(x2, y2);
-          } else {
-            st.qa[2 * i + sp][hf] = pack_bf16x2(x, y);
-          }
-        }
-    }
-    st.qsum += __shfl_xor_sync(0xffffffffu, st.qsum, 1);
-    st.qsum += __shfl_xor_sync(0xffffffffu, st.qsum, 2);
-  }
+  i4_prep<D, QF32>(p, st, out_row, G, lane);
 
   int gave_up = -1;
   for (int n = 0; n < mine; ++n) {
@@ -346,12 +395,12 @@ __global__ void __launch_bounds__(32 * kI4Warps, 3) decode_int4_kernel(const __g
       break;
     }
     const int t0 = t_begin + (warp + n * kI4Warps) * kI4Tokens;
-    i4_stage<D, QF32>(st, ring + s * Geo::STAGE, min(kI4Tokens, t_end - t0), p.qk_scale_log2_h[0], lane);
+    if (t_end - t0 >= kI4Tokens)
+      i4_stage<D, QF32, true>(st, ring + s * Geo::STAGE, kI4Tokens, lane);
+    else
+      i4_stage<D, QF32, false>(st, ring + s * Geo::STAGE, t_end - t0, lane);
     __syncwarp();
-    if (lane == 0 && n + kI4Stages < mine) {
-      fence_proxy_async();
-      issue(n + kI4Stages);
-    }
+    if (n + kI4Stages < mine) issue(n + kI4Stages);
   }
   if (gave_up >= 0 && lane == 0)  // copies in flight land before the ring is used again
     for (int n = gave_up; n < min(gave_up + kI4Stages, mine); ++n)
@@ -359,25 +408,32 @@ __global__ void __launch_bounds__(32 * kI4Warps, 3) decode_int4_kernel(const __g
 
   // the lanes' parts of a row's sums, then the warps' states in shared memory
 #pragma unroll
-  for (int d = 1; d < 4; d *= 2) {
-    st.l += __shfl_xor_sync(0xffffffffu, st.l, d);
-    st.fix += __shfl_xor_sync(0xffffffffu, st.fix, d);
-  }
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2) {
+      st.l[h] += __shfl_xor_sync(0xffffffffu, st.l[h], d);
+      st.fix[h] += __shfl_xor_sync(0xffffffffu, st.fix[h], d);
+    }
   __syncthreads();  // every ring is read
   bad = bad || hdr->bad != 0;
   float* acc = reinterpret_cast<float*>(rings);    // [warps][G][D]
   float* ml = acc + kI4Warps * G * D;              // [warps][G][2]
-  if (g < G) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int head = 2 * c + h;
+    if (head >= G) continue;
+    const float offset = fmaf(-8.0f, st.ones[h], st.fix[h]);
+    float* row = acc + (warp * G + head) * D + 8 * Geo::NW * g;
 #pragma unroll
     for (int i = 0; i < Geo::NW; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)  // accumulator column 2c + k: word (D / 64)(2c + k) + i of the row
-          acc[(warp * G + g) * D + 8 * (Geo::NW * (2 * c + k) + i) + j] = st.o[i][j][k] + st.o[i][j][2 + k] + st.fix;
-    if (c == 0) {
-      ml[(warp * G + g) * 2] = st.m;
-      ml[(warp * G + g) * 2 + 1] = st.l;
+      for (int j = 0; j < 4; ++j) {  // elements 2j (codes in 2^-24) and 2j + 1 (2^-20) of word i
+        const float2 two = make_float2(fmaf(0x1p24f, st.o[i][j][h], offset), fmaf(0x1p20f, st.o[i][j][2 + h], offset));
+        *reinterpret_cast<float2*>(row + 8 * i + 2 * j) = two;
+      }
+    if (g == 0) {
+      ml[(warp * G + head) * 2] = st.r[h];
+      ml[(warp * G + head) * 2 + 1] = st.l[h];
     }
   }
   __syncthreads();

@@ -89,9 +89,12 @@ def attend4(q, k, v, scale):
 
 
 def attend4_bound(q, out, p, k_ranges, v_ranges, scale):
-    """A score is step (q . (16 + c)) + (low - 16 step) sum(q): terms that add up to (47 step + |low|)
-    sum |q|.  A weight p step is held in two bf16 parts (2^-16) and multiplies c - 8, in -8..7; p (low +
-    8 step) is FP32.  Sums of T terms, truncated at 2^-23 a step.  The output's rounding."""
+    """A score is step (q . c) + low sum(q), terms that add up to (47 step + |low|) sum |q| and less.  A
+    row's query is f16 after scaling by a power of two: bf16 numbers are exact down to 2^-27 of its
+    largest element, f32 ones two parts (2^-22, one unit of score_error's).
+    A weight w = p step multiplies c - 8, in -8..7: f16 (2^-11) for bf16 rows, two parts (2^-22) for f32
+    ones; the f16 grid of 2^-24 is 2^-30 of the largest weight, below a unit of the sums' 2^-23.
+    p (low + 8 step) is FP32.  Sums of T terms, truncated at 2^-23 a step.  The output's rounding."""
     hkv, t = k_ranges.shape[:2]
     d = q.shape[-1]
     qd = q.double().view(hkv, -1, d)
@@ -99,7 +102,8 @@ def attend4_bound(q, out, p, k_ranges, v_ranges, scale):
     big = float(((47 * step + low.abs()).unsqueeze(1) * qd.abs().sum(dim=2, keepdim=True)).max()) * scale
     vs, vl = v_ranges[..., 0].double(), v_ranges[..., 1].double()
     size = (p @ (8 * vs + (vl + 8 * vs).abs()).unsqueeze(2)).expand(-1, -1, d).reshape(q.shape)
-    rel = 2.0 ** -16 + 2 * score_error(d, big) + 2.0 ** -21 + (t + 8) * 2.0 ** -23
+    rel = 2.0 ** -11 if q.dtype == torch.bfloat16 else 2.0 ** -22
+    rel += 2 * score_error(d, big) + 2.0 ** -21 + (t + 8) * 2.0 ** -23
     return rel * size + HALF_STEP[q.dtype] * (out.abs() + rel * size) + 1e-30
 
 
