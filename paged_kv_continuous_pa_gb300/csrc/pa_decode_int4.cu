@@ -2,8 +2,9 @@
 // (step, low) pair per token and kv head.
 //
 // One CTA per (row, split, kv head), as over the other pools; its warps take the split's
-// 32-token stages in turn, each through a ring of its own of bulk copies, and are merged
-// at the end in a fixed order.  The ranges never touch the products' inner loops:
+// 32-token stages in turn, each through a ring of its own of 16-byte asynchronous copies (bulk copies take
+// their addresses from uniform registers, so eight small ones cost a warp 80 instructions a stage, these 25), and
+// are merged at the end in a fixed order.  The ranges never touch the products' inner loops:
 //   q . K[t]  = step_t (q . c_t) + low_t sum(q)
 //   sum_t p_t V[t] = sum_t (p_t step_t) (c_t - 8) + sum_t p_t (low_t + 8 step_t)
 //
@@ -29,7 +30,7 @@
 namespace pa {
 
 constexpr int kI4Warps = 4;
-constexpr int kI4Stages = 4;   // ring slots of a warp
+constexpr int kI4Stages = 3;   // ring slots of a warp
 constexpr int kI4Tokens = 32;  // tokens of a stage
 
 template <int D>
@@ -43,11 +44,10 @@ struct I4Geom {
 };
 
 struct I4Header {
-  uint64_t full[kI4Warps][kI4Stages];
   uint64_t stall;              // never completed: the injected-stall test waits here
   int32_t bad;                 // a page id was out of range or a wait gave up
   int32_t last;                // this CTA merges the splits of its (row, kv head)
-  int32_t pid[kMaxUnitPages];
+  uint32_t place[kMaxUnitPages];  // of the unit's pages: (page Hkv + h) P / 16
 };
 
 template <int D>
@@ -59,43 +59,42 @@ __device__ __forceinline__ float2 range_of(uint32_t w) {  // (step, low)
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// A warp's copies.  A stage is eight of them at most, codes and ranges of K and V for each of one or two
-// pieces (32 tokens, or a page of 16): a lane each, so that their addresses are worked out together.
-template <int D>
-struct I4Copies {
-  const unsigned char* base;  // of the lane's kind: K codes, K ranges, V codes, V ranges
-  uint64_t policy;
-  int token_bytes, to;        // bytes of a token, offset of the lane's piece in a stage
-  int lg_p, piece, first;     // tokens of a piece, the lane's first token in a stage
+__device__ __forceinline__ void copy16(uint32_t dst_smem, const unsigned char* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
 
-  __device__ __forceinline__ I4Copies(const AttnParams& p, int lg_p_, int lane) : lg_p(lg_p_) {
-    using Geo = I4Geom<D>;
-    const int kind = lane & 3;
-    base = static_cast<const unsigned char*>(kind == 0 ? p.k_pool : kind == 1 ? p.k_ranges : kind == 2 ? p.v_pool : p.v_ranges);
-    policy = l2_policy_evict_first();
-    token_bytes = (kind & 1) ? 4 : Geo::ROW;
-    piece = min(1 << lg_p, kI4Tokens);
-    first = (lane >> 2) * piece;
-    to = (kind == 0 ? Geo::K : kind == 1 ? Geo::KR : kind == 2 ? Geo::V : Geo::VR) + first * token_bytes;
-  }
-  // Tokens t0 .. of the unit's pages into the stage at `st`; pages behind the unit's last are left out (their
-  // slots are masked).
-  __device__ __forceinline__ void issue(const AttnParams& p, const I4Header* hdr, unsigned char* st, uint64_t* bar, int t0,
-                                        int j0, int npg, int h, int lane) const {
-    const int t = t0 + first, page = (t >> lg_p) - j0;
-    const bool mine = first < kI4Tokens && page < npg;
-    const int copies = __popc(__ballot_sync(0xffffffffu, mine));
-    if (lane == 0) {
-      fence_proxy_async();
-      mbar_arrive_expect_tx(bar, static_cast<uint32_t>((copies >> 2) * piece * (2 * I4Geom<D>::ROW + 8)));
-    }
-    __syncwarp();
-    if (mine) {
-      const int64_t token = ((static_cast<int64_t>(hdr->pid[page]) * p.Hkv + h) << lg_p) + (t & ((1 << lg_p) - 1));
-      bulk_g2s(st + to, base + token * token_bytes, piece * token_bytes, bar, policy);
+// Tokens t0 .. t0 + 31 of a unit into the stage at `st`, in halves of 16 (which lie in one page); halves in pages
+// behind the unit's last are left out (their slots are masked).  One group of copies to a call.
+template <int D>
+__device__ __forceinline__ void i4_issue(const AttnParams& p, const I4Header* hdr, uint32_t st, int t0, int j0, int npg, int lg_p,
+                                         int lane) {
+  using Geo = I4Geom<D>;
+  constexpr int CHUNKS = Geo::ROW / 16, ROWS = 32 / CHUNKS;  // of a token; tokens that one instruction copies
+  const int mask = (1 << lg_p) - 1;
+  const uint32_t own = static_cast<uint32_t>(lane) * 16u;  // rows of a page follow one another
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = t0 + 16 * h, page = (t >> lg_p) - j0;
+    if (page < npg) {
+      const uint64_t at = static_cast<uint64_t>(hdr->place[page]) * (16u * Geo::ROW) + (static_cast<uint32_t>(t & mask) * Geo::ROW + own);
+      const unsigned char* k = static_cast<const unsigned char*>(p.k_pool) + at;
+      const unsigned char* v = static_cast<const unsigned char*>(p.v_pool) + at;
+#pragma unroll
+      for (int i = 0; i < 16 / ROWS; ++i) {
+        copy16(st + Geo::K + (16 * h + i * ROWS) * Geo::ROW + own, k + i * ROWS * Geo::ROW);
+        copy16(st + Geo::V + (16 * h + i * ROWS) * Geo::ROW + own, v + i * ROWS * Geo::ROW);
+      }
     }
   }
-};
+  // ranges: lanes 0-3, 4-7 those of K and V of the first half, 8-11, 12-15 of the second
+  const int t = t0 + 16 * ((lane >> 3) & 1), page = (t >> lg_p) - j0;
+  if (lane < 16 && page < npg) {
+    const unsigned char* base = static_cast<const unsigned char*>((lane & 4) ? p.v_ranges : p.k_ranges);
+    const uint64_t at = static_cast<uint64_t>(hdr->place[page]) * 64u + (static_cast<uint32_t>(t & mask) * 4u + (lane & 3) * 16u);
+    copy16(st + ((lane & 4) ? Geo::VR : Geo::KR) + (lane >> 3) * 64 + (lane & 3) * 16, base + at);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 
 // Codes 2 s and 2 s + 1 (s = 0, 1) of both halves of a word: c 2^-24 and c 2^-20 as f16.
 template <int S>
@@ -127,7 +126,7 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
   float e[4][2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {  // 16 tokens
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s[2][4] = {};  // two sums, so that each product waits for the one before the last
     uint32_t w[2][D / 32];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -146,16 +145,16 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
       codes_f16<0>(w[0][i], a[0], a[2]);
       codes_f16<0>(w[1][i], a[1], a[3]);
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) mma_f16_16816(s, a, st.q[part][2 * i][0], st.q[part][2 * i][1]);
+      for (int part = 0; part < PARTS; ++part) mma_f16_16816(s[0], a, st.q[part][2 * i][0], st.q[part][2 * i][1]);
       codes_f16<1>(w[0][i], a[0], a[2]);
       codes_f16<1>(w[1][i], a[1], a[3]);
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) mma_f16_16816(s, a, st.q[part][2 * i + 1][0], st.q[part][2 * i + 1][1]);
+      for (int part = 0; part < PARTS; ++part) mma_f16_16816(s[1], a, st.q[part][2 * i + 1][0], st.q[part][2 * i + 1][1]);
     }
-    e[2 * u][0] = s[0];
-    e[2 * u][1] = s[1];
-    e[2 * u + 1][0] = s[2];
-    e[2 * u + 1][1] = s[3];
+    e[2 * u][0] = s[0][0] + s[1][0];
+    e[2 * u][1] = s[0][1] + s[1][1];
+    e[2 * u + 1][0] = s[0][2] + s[1][2];
+    e[2 * u + 1][1] = s[0][3] + s[1][3];
   }
   float2 v[4];
   float top[2] = {-INFINITY, -INFINITY};
@@ -176,17 +175,18 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
       top[h] = fmaxf(top[h], e[i][h] + lg);
     }
   }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int d = 4; d < 32; d *= 2) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], d));
+  // the reference is the same in every lane of a head; it is looked at again only when a lane's weight passes the top
   if (__any_sync(0xffffffffu, top[0] - st.r[0] > kI4Top || top[1] - st.r[1] > kI4Top)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], d));
     float f[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const bool move = top[h] - st.r[h] > kI4Top;
       const float r = move ? top[h] - kI4Start : st.r[h];
-      f[h] = move ? ex2(st.r[h] - r) : 1.0f;  // (the first time: 2^-inf)
+      f[h] = move ? ex2(st.r[h] - r) : 1.0f;
       st.r[h] = r;
       st.l[h] *= f[h];
       st.fix[h] *= f[h];
@@ -201,10 +201,9 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
   }
   // weights of token 8 i + g as (head 2c, head 2c + 1), transposed into (tokens 8 i + 2c, + 1) of head g
   uint32_t b[PARTS][4];
-  const float r0 = st.r[0] == -INFINITY ? 0.0f : st.r[0], r1 = st.r[1] == -INFINITY ? 0.0f : st.r[1];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float p0 = ex2(e[i][0] - r0), p1 = ex2(e[i][1] - r1);
+    const float p0 = ex2(e[i][0] - st.r[0]), p1 = ex2(e[i][1] - st.r[1]);
     const float low8 = fmaf(8.0f, v[i].x, v[i].y);
     st.l[0] += p0;
     st.l[1] += p1;
@@ -296,7 +295,7 @@ __device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& s
   for (int h = 0; h < 2; ++h) {  // head h2 sits in lanes 4 h2 ..
     st.dot_scale[h] = __shfl_sync(0xffffffffu, dot, 4 * (2 * c + h));
     st.low_scale[h] = __shfl_sync(0xffffffffu, low, 4 * (2 * c + h));
-    st.r[h] = -INFINITY;
+    st.r[h] = -1e30f;  // (finite, so that differences to it are numbers)
     st.l[h] = st.fix[h] = 0.0f;
   }
   // k-step 2 i + s: elements 2 s, 2 s + 4 and, as codes there count in 2^-20, a sixteenth of 2 s + 1, 2 s + 5
@@ -318,7 +317,7 @@ __device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& s
 }
 
 template <int D, bool QF32>
-__global__ void __launch_bounds__(32 * kI4Warps, 3) decode_int4_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(32 * kI4Warps, QF32 ? 3 : 4) decode_int4_kernel(const __grid_constant__ AttnParams p) {
   using Geo = I4Geom<D>;
   constexpr int THREADS = 32 * kI4Warps;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -351,8 +350,6 @@ __global__ void __launch_bounds__(32 * kI4Warps, 3) decode_int4_kernel(const __g
   const int nstage = (t_end - t_begin + kI4Tokens - 1) / kI4Tokens;
 
   if (tid == 0) {
-    for (int w = 0; w < kI4Warps; ++w)
-      for (int s = 0; s < kI4Stages; ++s) mbar_init(&hdr->full[w][s], 1);
     mbar_init(&hdr->stall, 1);
     hdr->bad = 0;
     hdr->last = 0;
@@ -362,7 +359,7 @@ __global__ void __launch_bounds__(32 * kI4Warps, 3) decode_int4_kernel(const __g
   for (int i = tid; i < npg && i < kMaxUnitPages; i += THREADS) {
     const int pid = __ldg(p.block_tables + static_cast<size_t>(seq) * p.max_blocks + j0 + i);
     bad_page |= pid < 0 || pid >= p.num_pages;
-    hdr->pid[i] = pid;
+    hdr->place[i] = static_cast<uint32_t>((static_cast<uint64_t>(pid) * p.Hkv + h) << (lg_p - 4));  // (32 bits: checked by the host)
   }
   bool bad = __syncthreads_or(bad_page) != 0;
   if (bad && tid == 0) record_error(p.status, ST_OUT_OF_RANGE);
@@ -371,40 +368,37 @@ __global__ void __launch_bounds__(32 * kI4Warps, 3) decode_int4_kernel(const __g
   // warp w takes stages w, w + kI4Warps, ..
   unsigned char* ring = rings + static_cast<size_t>(warp) * kI4Stages * Geo::STAGE;
   const int mine = bad || warp >= nstage ? 0 : (nstage - warp + kI4Warps - 1) / kI4Warps;
-  const I4Copies<D> copies(p, lg_p, lane);
+  const uint32_t ring_at = smem_addr(ring);
   auto issue = [&](int n) {
-    copies.issue(p, hdr, ring + (n % kI4Stages) * Geo::STAGE, &hdr->full[warp][n % kI4Stages],
-                 t_begin + (warp + n * kI4Warps) * kI4Tokens, j0, npg, h, lane);
+    if (n < mine)
+      i4_issue<D>(p, hdr, ring_at + (n % kI4Stages) * Geo::STAGE, t_begin + (warp + n * kI4Warps) * kI4Tokens, j0, npg, lg_p, lane);
+    else
+      asm volatile("cp.async.commit_group;" ::: "memory");  // (an empty group, so that one more is always newer)
   };
-  for (int n = 0; n < min(mine, kI4Stages); ++n) issue(n);
+#pragma unroll 1
+  for (int n = 0; n < kI4Stages; ++n) issue(n);
 
   I4State<D, QF32> st;
   i4_prep<D, QF32>(p, st, out_row, G, lane);
 
-  int gave_up = -1;
-  for (int n = 0; n < mine; ++n) {
-    const int s = n % kI4Stages;
-    bool got = mbar_wait(&hdr->full[warp][s], (n / kI4Stages) & 1, p.wait_limit);
-    if (p.debug_stall) got = got && mbar_wait(&hdr->stall, 0, p.wait_limit);  // runs out by construction
-    if (!__all_sync(0xffffffffu, got)) {
-      gave_up = n;
-      if (lane == 0) {
-        record_error(p.status, ST_TIMEOUT);
-        hdr->bad = 1;
-      }
-      break;
-    }
-    const int t0 = t_begin + (warp + n * kI4Warps) * kI4Tokens;
-    if (t_end - t0 >= kI4Tokens)
-      i4_stage<D, QF32, true>(st, ring + s * Geo::STAGE, kI4Tokens, lane);
-    else
-      i4_stage<D, QF32, false>(st, ring + s * Geo::STAGE, t_end - t0, lane);
-    __syncwarp();
-    if (n + kI4Stages < mine) issue(n + kI4Stages);
+  if (p.debug_stall && !mbar_wait(&hdr->stall, 0, p.wait_limit)) {  // runs out by construction
+    record_error(p.status, ST_TIMEOUT);
+    hdr->bad = 1;
   }
-  if (gave_up >= 0 && lane == 0)  // copies in flight land before the ring is used again
-    for (int n = gave_up; n < min(gave_up + kI4Stages, mine); ++n)
-      mbar_wait(&hdr->full[warp][n % kI4Stages], (n / kI4Stages) & 1, kDrainWaitLimit);
+#pragma unroll 1
+  for (int n = 0; n < mine; ++n) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kI4Stages - 1) : "memory");
+    __syncwarp();
+    const unsigned char* stage = ring + (n % kI4Stages) * Geo::STAGE;
+    const int left = t_end - (t_begin + (warp + n * kI4Warps) * kI4Tokens);
+    if (left >= kI4Tokens)
+      i4_stage<D, QF32, true>(st, stage, kI4Tokens, lane);
+    else
+      i4_stage<D, QF32, false>(st, stage, left, lane);
+    __syncwarp();
+    issue(n + kI4Stages);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 
   // the lanes' parts of a row's sums, then the warps' states in shared memory
 #pragma unroll
@@ -463,7 +457,7 @@ cudaError_t launch_int4_inst(const AttnParams& p, cudaStream_t stream) {
   if (ea != cudaSuccess) return ea;
   const long long units = static_cast<long long>(p.n_unit_rows) * p.max_splits * p.Hkv;
   if (units <= 0) return cudaSuccess;
-  if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (units > 0x7fffffffLL || static_cast<long long>(p.num_pages) * p.Hkv * p.P / 16 > 0xffffffffLL) return cudaErrorInvalidConfiguration;
   const cudaError_t e = launch_kernel(decode_int4_kernel<D, QF32>, dim3(static_cast<unsigned>(units)),
                                       dim3(32 * kI4Warps), i4_smem<D>(), stream, p.dependent != 0, p);
   count_launch();
