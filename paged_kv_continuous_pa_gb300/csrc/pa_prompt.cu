@@ -4,22 +4,24 @@
 //   out_i = sum_{j <= i} exp2(s_ij - m_i) v_j / sum_{j <= i} exp2(s_ij - m_i),   s_ij = scale log2(e) q_i . k_j
 //
 // One pass over the keys with a running reference m_i: it moves only when a score
-// passes it by 2^8, so the accumulator is seldom rescaled.
+// passes it by 2^8, so the accumulator is seldom rescaled, and a row's maximum is
+// only taken over its four lanes then.
 //
 // What bounds it: the two matrix products, 4 D flops for each (query head, query, key).
 // One CTA per SM goes through units of work.  A unit is two query tiles of 128 rows that
 // read the same keys: two query heads of one kv head at the same positions where the
 // head group is even, else two neighbouring ranges of 128 positions of one head.  While
 // the softmax of one tile runs, the tensor core works for the other.
-//   warps 0-3, 4-7   softmax and output of tile A, B: one row to a thread
-//   warp 8           loads: queries and 128-key tiles of K and V through a ring (TMA)
-//   warp 9           issues the MMAs:  S = Q K^T (smem x smem), then O += P V (TMEM x smem)
-//   warps 10, 11     look over the values of the blocks that hold masked keys
+//   warps 0-7, 8-15  softmax of tile A, B: 16 rows to a warp, a row's scores in four lanes (so that a row is one
+//                    warp's, and four warps of a scheduler hide each other's latencies); output, a row to two threads
+//   warp 16          loads: queries and 128-key tiles of K and V through a ring (TMA)
+//   warp 17          issues the MMAs:  S = Q K^T (smem x smem), then O += P V (TMEM x smem)
+//   warps 18, 19     look over the values of the blocks that hold masked keys
 // Tensor memory: S of A and B (128 columns each), the weights P over their S as bf16, O of A and B.
 //
 // Masked keys.  Only the block on a tile's diagonal has any (keys behind the
 // sequence's end are behind every row's diagonal too).  A masked key's weight is 0,
-// but 0 times an infinite or NaN value is NaN, so warps 10 and 11 put 0 in the
+// but 0 times an infinite or NaN value is NaN, so warps 18 and 19 put 0 in the
 // place of such values in shared memory; a row that does attend to one gets it added at the end.
 //
 // Units are listed longest first by a launch of their own and dealt out to the CTAs in a
@@ -34,12 +36,13 @@
 namespace pa {
 
 constexpr int kPrTile = 128;     // rows of a query tile, keys of a block
-constexpr int kPrThreads = 384;
+constexpr int kPrSoftmaxThreads = 512;
+constexpr int kPrThreads = kPrSoftmaxThreads + 128;
 constexpr int kPrBins = 2048;    // of the units' lengths, when they are ordered
 constexpr int kPrPlanThreads = 1024;
 // registers of a softmax thread and of the others; their sum over the CTA is what it is launched with
-constexpr int kPrRegs = 168, kPrSoftmaxRegs = 208, kPrOtherRegs = 88;
-static_assert(2 * 128 * kPrSoftmaxRegs + 128 * kPrOtherRegs <= kPrThreads * kPrRegs, "register split");
+constexpr int kPrRegs = 96, kPrSoftmaxRegs = 104, kPrOtherRegs = 64;
+static_assert(kPrSoftmaxThreads * kPrSoftmaxRegs + 128 * kPrOtherRegs <= kPrThreads * kPrRegs, "register split");
 
 struct PromptParams {
   const int32_t* row_starts;
@@ -149,29 +152,117 @@ __device__ __forceinline__ void pr_ld_wait(float* r) {
                : "memory");
 }
 
+// 64 columns of 16 lanes: lane 4 g + c of the warp gets columns 8 i + 2c, + 1 of rows g (r[4i], r[4i + 1]) and g + 8.
+__device__ __forceinline__ void pr_ld16x64(uint32_t taddr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// 32 columns of two 16-bit numbers each, in the same places: w[2i] of row g, w[2i + 1] of row g + 8.
+__device__ __forceinline__ void pr_st16x32(uint32_t taddr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+      "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+      : "memory");
+}
+// 16 columns of 16 lanes, rows g and g + 8 multiplied in place (few registers: it is seldom done).
+__device__ __forceinline__ void pr_scale16x16(uint32_t taddr, float f0, float f1) {
+  float r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] *= (i & 2) ? f1 : f0;
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(r[0]), "f"(r[1]),
+               "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t pr_pack(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 
+// Two numbers at a time: a * b + c and a + b.
+__device__ __forceinline__ uint64_t pr_two(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void pr_split(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t pr_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pr_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float pr_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Barrier `id` of two warps; true where `x` holds for a thread of either.
+__device__ __forceinline__ bool pr_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 template <int D>
-struct PromptSmem {  // byte offsets from a 1024-byte aligned base
+struct PromptSmem {  // byte offsets from the base, which is 1024-byte aligned (no static shared memory lies before it)
   static constexpr int NH = D / 64;
   static constexpr int HALF = kPrTile * 128;       // 64 elements of 128 rows
   static constexpr int TILE = NH * HALF;
   static constexpr int STAGES = D == 128 ? 5 : 8;  // tiles of K and V in the ring
   static constexpr int RING = 2 * TILE;            // behind the two query tiles
   static constexpr int BAR = RING + STAGES * TILE;
-  static constexpr int BYTES = BAR + 512 + 1024;   // slack for aligning the base
+  static constexpr int ROWS = BAR + 384;           // a number of each softmax thread
+  static constexpr int BYTES = ROWS + kPrSoftmaxThreads * 4;
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
-// A unit: the tiles' positions, heads and numbers of key blocks.
+// A unit: the tiles' positions, heads and numbers of key blocks.  (No arrays: they would be indexed by a tile.)
 struct PromptUnit {
-  int begin, end;      // rows of the sequence
-  int pos[2], head[2], blocks[2];
-  int n;               // blocks of the longer tile
+  int begin, end;  // rows of the sequence
+  int pos_a, pos_b, head_a, head_b, blocks_a, blocks_b;
+  int n;           // blocks of the longer tile
+};
+
+// A place in the ring: its slot and the parity of its turn.
+template <int STAGES>
+struct PromptRing {
+  int slot = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == STAGES) {
+      slot = 0;
+      turn ^= 1u;
+    }
+  }
 };
 
 template <int D>
@@ -183,8 +274,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     QF = EMPTY + S::STAGES,      // queries of tile A / B landed
     QE = QF + 2,                 // ... read by the unit's MMAs
     SF = QE + 2,                 // scores of tile A / B
-    PF = SF + 2,                 // weights of tile A / B (their scores are read, O may be added to)
-    PV = PF + 2,                 // O of tile A / B holds one more block
+    PF = SF + 2,                 // weights of tile A / B, for either half of the keys (the scores are read, O may be added to)
+    PV = PF + 4,                 // O of tile A / B holds one more block
     // the values of a block with masked keys are looked over: in turn, as the look may be a unit ahead of the
     // MMAs, and a unit has at most two such blocks
     VOK = PV + 2,
@@ -193,9 +284,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     STALL,
     COUNT
   };
-  static_assert(COUNT * 8 + 32 <= 512, "barriers");
-  extern __shared__ __align__(128) unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  static_assert(COUNT * 8 + 32 <= S::ROWS - S::BAR, "barriers");
+  extern __shared__ __align__(1024) unsigned char sm[];
+  if ((smem_addr(sm) & 1023u) != 0) {  // (the swizzled tiles would be read at other places than they were written)
+    if (threadIdx.x == 0) record_error(p.status, ST_LAUNCH);
+    return;
+  }
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::BAR + COUNT * 8);
   volatile int32_t* odd_values = reinterpret_cast<volatile int32_t*>(tslot + 1);  // entry k % 4 is k + 1: values of unit k were put to 0
@@ -203,7 +297,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
   if (warp == 0) tc::tmem_alloc(tslot, 512);
   if (tid == 0) {
-    for (int i = 0; i < COUNT; ++i) mbar_init(&bar[i], i == PF || i == PF + 1 ? 4u : i >= VOK && i < VOK + 4 ? 2u : 1u);
+    for (int i = 0; i < COUNT; ++i) mbar_init(&bar[i], i >= PF && i < PF + 4 ? 8u : i >= VOK && i < VOK + 4 ? 2u : 1u);
     for (int i = 0; i < 4; ++i) odd_values[i] = 0;
     fence_barrier_init();
     tc::prefetch_tensormap(&p.qmap);
@@ -228,139 +322,170 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   auto unit_at = [&](int k, PromptUnit& x) {
     const int64_t u = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if (static_cast<int64_t>(k) * gridDim.x >= units) return false;
-    x.n = x.blocks[0] = x.blocks[1] = 0;
+    x.n = x.blocks_a = x.blocks_b = 0;
     if (u >= units) return true;  // (a round without work for this CTA)
     const int4 t = __ldcg(p.tiles + u / per_tile);
     const int h = static_cast<int>(u % per_tile);
     x.begin = t.x;
     x.end = t.y;
-    x.pos[0] = t.z;
-    x.blocks[0] = t.z / kPrTile + 1;
+    x.pos_a = t.z;
+    x.n = x.blocks_a = t.z / kPrTile + 1;
     if (two_heads) {
-      x.head[0] = 2 * h;
-      x.head[1] = 2 * h + 1;
-      x.pos[1] = t.z;
-      x.blocks[1] = x.blocks[0];
+      x.head_a = 2 * h;
+      x.head_b = 2 * h + 1;
+      x.pos_b = t.z;
+      x.blocks_b = x.n;
     } else {
-      x.head[0] = x.head[1] = h;
-      x.pos[1] = t.z + kPrTile;
-      x.blocks[1] = x.pos[1] < t.y - t.x ? x.blocks[0] + 1 : 0;
+      x.head_a = x.head_b = h;
+      x.pos_b = t.z + kPrTile;
+      if (x.pos_b < t.y - t.x) x.n = x.blocks_b = x.blocks_a + 1;
     }
-    x.n = max(x.blocks[0], x.blocks[1]);
     return true;
   };
 
-  if (warp >= 8) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrOtherRegs));
-    if (warp == 8 && lane == 0) {
+    if (warp == 16 && lane == 0) {
       // ---- loads
-      int item = 0, checked = 0, done[2] = {0, 0};  // tiles of K and V, those to be looked over, query tiles issued so far
+      PromptRing<S::STAGES> at;
+      int items = 0, checked = 0, done_a = 0, done_b = 0;  // tiles of K and V, those to be looked over, query tiles issued so far
       bool ok = !p.debug_stall || wait(STALL, 0);  // (runs out by construction)
       PromptUnit x{};
+      auto queries = [&](int t, int& done, int pos, int head) {
+        if (done > 0 && !wait(QE + t, (done - 1) & 1)) return false;
+        mbar_arrive_expect_tx(&bar[QF + t], S::TILE);
+        for (int hf = 0; hf < S::NH; ++hf)
+          pr_load_3d(sm + t * S::TILE + hf * S::HALF, &p.qmap, hf * 64, head, x.begin + pos, &bar[QF + t]);
+        ++done;
+        return true;
+      };
+      auto keys = [&](const CUtensorMap* map, int kv_head, int j) {
+        if (items >= S::STAGES && !wait(EMPTY + at.slot, at.turn ^ 1u)) return false;
+        mbar_arrive_expect_tx(&bar[FULL + at.slot], S::TILE);
+        for (int hf = 0; hf < S::NH; ++hf)
+          pr_load_3d(sm + S::RING + at.slot * S::TILE + hf * S::HALF, map, hf * 64, kv_head, x.begin + j * kPrTile,
+                     &bar[FULL + at.slot]);
+        ++items;
+        at.next();
+        return true;
+      };
       for (int k = 0; ok && unit_at(k, x); ++k) {
-        for (int t = 0; ok && t < 2; ++t) {
-          if (x.blocks[t] == 0) continue;
-          if (done[t] > 0) ok = wait(QE + t, (done[t] - 1) & 1);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bar[QF + t], S::TILE);
-          for (int hf = 0; hf < S::NH; ++hf)
-            pr_load_3d(sm + t * S::TILE + hf * S::HALF, &p.qmap, hf * 64, x.head[t], x.begin + x.pos[t], &bar[QF + t]);
-          ++done[t];
-        }
-        for (int j = 0; ok && j < 2 * x.n; ++j) {
-          const int s = item % S::STAGES;
-          if (item >= S::STAGES) ok = wait(EMPTY + s, (item / S::STAGES - 1) & 1);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bar[FULL + s], S::TILE);
-          for (int hf = 0; hf < S::NH; ++hf)
-            pr_load_3d(sm + S::RING + s * S::TILE + hf * S::HALF, (j & 1) ? &p.vmap : &p.kmap, hf * 64, x.head[0] / p.G,
-                       x.begin + (j >> 1) * kPrTile, &bar[FULL + s]);
-          if ((j & 1) && (j >> 1) >= x.blocks[0] - 1) mbar_arrive(&bar[VIN + (checked++ & 3)]);
-          ++item;
+        if (x.blocks_a > 0) ok = queries(0, done_a, x.pos_a, x.head_a);
+        if (ok && x.blocks_b > 0) ok = queries(1, done_b, x.pos_b, x.head_b);
+        const int kv_head = x.head_a / p.G;
+        for (int j = 0; ok && j < x.n; ++j) {
+          ok = keys(&p.kmap, kv_head, j) && keys(&p.vmap, kv_head, j);
+          if (ok && j >= x.blocks_a - 1) mbar_arrive(&bar[VIN + (checked++ & 3)]);
         }
       }
       if (!ok) {  // what is in flight lands before the shared memory is given up
-        for (int i = max(0, item - S::STAGES); i < item; ++i)
+        for (int i = max(0, items - S::STAGES); i < items; ++i)
           mbar_wait(&bar[FULL + i % S::STAGES], (i / S::STAGES) & 1, kDrainWaitLimit);
-        for (int t = 0; t < 2; ++t)
-          if (done[t] > 0) mbar_wait(&bar[QF + t], (done[t] - 1) & 1, kDrainWaitLimit);
+        if (done_a > 0) mbar_wait(&bar[QF], (done_a - 1) & 1, kDrainWaitLimit);
+        if (done_b > 0) mbar_wait(&bar[QF + 1], (done_b - 1) & 1, kDrainWaitLimit);
       }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 17 && lane == 0) {
       // ---- MMAs
       constexpr uint32_t id_qk = tc::idesc_bf16_f32(kPrTile, kPrTile, false);
       constexpr uint32_t id_pv = tc::idesc_bf16_f32(kPrTile, D, true);
-      int base = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0}, checked = 0;
+      PromptRing<S::STAGES> at;
+      uint32_t q_turn = 0, p_turn = 0;  // bit t: of tile t
+      int checked = 0;
       bool ok = true;
       PromptUnit x{};
-      auto full = [&](int item) { return wait(FULL + item % S::STAGES, (item / S::STAGES) & 1); };
-      auto qk = [&](int t, int j) {
-        const unsigned char* q = sm + t * S::TILE;
-        const unsigned char* kt = sm + S::RING + ((base + 2 * j) % S::STAGES) * S::TILE;
+      // Matrix descriptors differ in their address alone (the lower 14 bits, in 16 bytes).  The issue of 16 products
+      // takes as long as they do if each builds its own.
+      const uint64_t k_desc = tc::smem_desc(sm, 16, 1024), v_desc = tc::smem_desc(sm, S::HALF, 1024);
+      const uint32_t hi = static_cast<uint32_t>(k_desc >> 32), k_lo = static_cast<uint32_t>(k_desc), v_lo = static_cast<uint32_t>(v_desc);
+      auto desc = [&](uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; };
+      auto qk = [&](int t, int slot, bool last) {
+        const uint32_t q = k_lo + t * (S::TILE >> 4);
+        const uint32_t kt = k_lo + (S::RING >> 4) + slot * (S::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const int off = (kk / 4) * S::HALF + (kk % 4) * 32;
-          tc::mma_bf16(tb + t * 128, tc::smem_desc(q + off, 16, 1024), tc::smem_desc(kt + off, 16, 1024), id_qk, kk > 0);
+          const uint32_t off = ((kk / 4) * S::HALF + (kk % 4) * 32) >> 4;
+          tc::mma_bf16(tb + t * 128, desc(q + off), desc(kt + off), id_qk, kk > 0);
         }
         tc::mma_commit(&bar[SF + t]);
-        if (j == x.blocks[t] - 1) tc::mma_commit(&bar[QE + t]);
+        if (last) tc::mma_commit(&bar[QE + t]);
       };
-      auto pv = [&](int t, int j) {
-        const unsigned char* vt = sm + S::RING + ((base + 2 * j + 1) % S::STAGES) * S::TILE;
+      auto pv = [&](int t, int slot, bool first) {
+        const uint32_t vt = v_lo + (S::RING >> 4) + slot * (S::TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kPrTile / 16; ++kk)
-          tc::mma_bf16_ts(tb + 256 + t * 128, tb + t * 128 + kk * 8, tc::smem_desc(vt + kk * 2048, S::HALF, 1024), id_pv,
-                          j > 0 || kk > 0);
+        for (int kk = 0; kk < kPrTile / 16; ++kk) {
+          if (kk % 4 == 0) {
+            if (!wait(PF + 2 * t + kk / 4, (p_turn >> t) & 1u)) return false;
+            tc::fence_after_sync();
+          }
+          tc::mma_bf16_ts(tb + 256 + t * 128, tb + t * 128 + kk * 8, desc(vt + kk * (2048 >> 4)), id_pv, !first || kk > 0);
+        }
+        p_turn ^= 1u << t;
         tc::mma_commit(&bar[PV + t]);
+        return true;
       };
       for (int k = 0; ok && unit_at(k, x); ++k) {
         if (x.n == 0) continue;
-        ok = full(base);
-        for (int t = 0; ok && t < 2; ++t) {
-          if (x.blocks[t] == 0) continue;
-          ok = wait(QF + t, q_count[t]++ & 1);
-          if (ok) qk(t, 0);
+        const int k0 = at.slot;
+        ok = wait(FULL + at.slot, at.turn);
+        at.next();
+        if (ok) ok = wait(QF, q_turn & 1u);
+        if (!ok) break;
+        q_turn ^= 1u;
+        qk(0, k0, x.blocks_a == 1);
+        if (x.blocks_b > 0) {
+          ok = wait(QF + 1, (q_turn >> 1) & 1u);
+          if (!ok) break;
+          q_turn ^= 2u;
+          qk(1, k0, x.blocks_b == 1);
         }
-        if (ok) tc::mma_commit(&bar[EMPTY + base % S::STAGES]);
-        for (int j = 0; ok && j < x.n; ++j) {
-          ok = full(base + 2 * j + 1);
-          if (ok && j >= x.blocks[0] - 1) {
+        tc::mma_commit(&bar[EMPTY + k0]);
+        for (int j = 0; j < x.n; ++j) {
+          const int v = at.slot;
+          ok = wait(FULL + at.slot, at.turn);
+          at.next();
+          if (ok && j >= x.blocks_a - 1) {
             ok = wait(VOK + (checked & 3), (checked >> 2) & 1);
             ++checked;
           }
-          if (ok && j + 1 < x.n) ok = full(base + 2 * j + 2);
-          for (int t = 0; ok && t < 2; ++t) {
-            if (j >= x.blocks[t]) continue;
-            ok = wait(PF + t, p_count[t]++ & 1);
-            if (!ok) break;
-            tc::fence_after_sync();
-            pv(t, j);
-            if (j + 1 < x.blocks[t]) qk(t, j + 1);
+          const int kn = at.slot;
+          if (ok && j + 1 < x.n) {
+            ok = wait(FULL + at.slot, at.turn);
+            at.next();
           }
           if (!ok) break;
-          tc::mma_commit(&bar[EMPTY + (base + 2 * j + 1) % S::STAGES]);
-          if (j + 1 < x.n) tc::mma_commit(&bar[EMPTY + (base + 2 * j + 2) % S::STAGES]);
+          if (j < x.blocks_a) {
+            ok = pv(0, v, j == 0);
+            if (!ok) break;
+            if (j + 1 < x.blocks_a) qk(0, kn, j + 2 == x.blocks_a);
+          }
+          if (j < x.blocks_b) {
+            ok = pv(1, v, j == 0);
+            if (!ok) break;
+            if (j + 1 < x.blocks_b) qk(1, kn, j + 2 == x.blocks_b);
+          }
+          tc::mma_commit(&bar[EMPTY + v]);
+          if (j + 1 < x.n) tc::mma_commit(&bar[EMPTY + kn]);
         }
-        base += 2 * x.n;
       }
       if (!ok) {  // every MMA issued is done before the tensor memory is given up
         tc::mma_commit(&bar[DRAIN]);
         mbar_wait(&bar[DRAIN], 0, kDrainWaitLimit);
       }
-    } else if (warp >= 10) {
+    } else if (warp >= 18) {
       // ---- values of the blocks that hold masked keys: infinities and NaN become 0
       int base = 0, checked = 0;
       bool ok = true;
       PromptUnit x{};
       for (int k = 0; ok && unit_at(k, x); ++k) {
         if (x.n == 0) continue;
-        for (int j = x.blocks[0] - 1; ok && j < x.n; ++j, ++checked) {
+        for (int j = x.blocks_a - 1; ok && j < x.n; ++j, ++checked) {
           const int item = base + 2 * j + 1;
           ok = __all_sync(0xffffffffu, wait(VIN + (checked & 3), (checked >> 2) & 1) &&
                                            wait(FULL + item % S::STAGES, (item / S::STAGES) & 1));
           if (!ok) break;
           uint4* tile = reinterpret_cast<uint4*>(sm + S::RING + (item % S::STAGES) * S::TILE);
           bool found = false;
-          for (int i = (warp - 10) * 32 + lane; i < S::TILE / 16; i += 64) {
+          for (int i = (warp - 18) * 32 + lane; i < S::TILE / 16; i += 64) {
             uint4 w = tile[i];
             auto odd = [](uint32_t a) { return ((a & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };  // exponent of all ones
             if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
@@ -384,91 +509,128 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrSoftmaxRegs));
     // ---- softmax and output of tile t
-    const int t = warp >> 2, r = tid & 127;  // the thread's row of the tile
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tb + lanes + t * 128, to = tb + lanes + 256 + t * 128;
-    int count = 0;  // blocks of this tile so far
+    const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int pair = 1 + t * 4 + quarter;  // barrier of the two warps that share 32 rows
+    float* rows = reinterpret_cast<float*>(sm + S::ROWS) + t * 256;  // per row of the tile its sum and its reference
+    // softmax: rows r0 and r0 + 8, columns 8 i + 2 c, + 1
+    const int r0 = 32 * quarter + 16 * half + (lane >> 2), c2 = 2 * (lane & 3);
+    const uint32_t ts = tb + (static_cast<uint32_t>(32 * quarter + 16 * half) << 16) + t * 128, to = ts + 256;
+    const uint64_t scale2 = pr_two(p.scale_log2, p.scale_log2);
+    uint32_t s_turn = 0, o_turn = 0;
     bool ok = true;
     PromptUnit x{};
     for (int k = 0; ok && unit_at(k, x); ++k) {
-      const int n = x.blocks[t];
+      const int n = t == 0 ? x.blocks_a : x.blocks_b;
       if (n == 0) continue;
-      float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < n; ++j, ++count) {
-        ok = __all_sync(0xffffffffu, wait(SF + t, count & 1));
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      for (int j = 0; j < n; ++j, s_turn ^= 1u) {
+        ok = __all_sync(0xffffffffu, wait(SF + t, s_turn));
         if (!ok) break;
         tc::fence_after_sync();
-        float s[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pr_ld32(ts + 32 * i, s + 32 * i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pr_ld_wait(s + 32 * i);
+        float s[64];
+        pr_ld16x64(ts, s);
+        pr_ld16x64(ts + 64, s + 32);
+        pr_ld_wait(s);
+        pr_ld_wait(s + 32);
         if (j == n - 1) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) s[i] = i > r ? -INFINITY : s[i];
+          for (int i = 0; i < 64; ++i) {
+            const int column = 8 * (i >> 2) + c2 + (i & 1);
+            s[i] = column > r0 + ((i & 2) ? 8 : 0) ? -INFINITY : s[i];
+          }
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]), b0 = fmaxf(s[4], s[5]), b1 = fmaxf(s[6], s[7]);
 #pragma unroll
-        for (int i = 0; i < 128; i += 8)
+        for (int i = 8; i < 64; i += 8) {
+          a0 = pr_max3(a0, s[i], s[i + 1]);
+          a1 = pr_max3(a1, s[i + 2], s[i + 3]);
+          b0 = pr_max3(b0, s[i + 4], s[i + 5]);
+          b1 = pr_max3(b1, s[i + 6], s[i + 7]);
+        }
+        float top0 = fmaxf(a0, b0), top1 = fmaxf(a1, b1);
+        if (__any_sync(0xffffffffu, (top0 - m0) * p.scale_log2 > kRescaleSlack || (top1 - m1) * p.scale_log2 > kRescaleSlack)) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], fmaxf(s[i + 2 * q], s[i + 2 * q + 1]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const bool move = (top - m) * p.scale_log2 > kRescaleSlack;
-        if (__any_sync(0xffffffffu, move)) {
+          for (int d = 1; d < 4; d *= 2) {
+            top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
+            top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
+          }
+          const bool move0 = (top0 - m0) * p.scale_log2 > kRescaleSlack, move1 = (top1 - m1) * p.scale_log2 > kRescaleSlack;
           if (j > 0) {
             // (the scores' commit came behind the last block's product with V: O stands still)
-            const float f = move ? ex2((m - top) * p.scale_log2) : 1.0f;
-            l *= f;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              pr_ld32(to + 32 * c, o);
-              pr_ld_wait(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
-              tc::tmem_st32(to + 32 * c, o);
-            }
+            const float f0 = move0 ? ex2((m0 - top0) * p.scale_log2) : 1.0f, f1 = move1 ? ex2((m1 - top1) * p.scale_log2) : 1.0f;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) pr_scale16x16(to + c, f0, f1);
+            tc::tmem_wait_st();
           }
-          if (move) m = top;
+          if (move0) m0 = top0;
+          if (move1) m1 = top1;
         }
-        const float shift = m == -INFINITY ? 0.0f : m * p.scale_log2;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float shift0 = m0 == -INFINITY ? 0.0f : -m0 * p.scale_log2, shift1 = m1 == -INFINITY ? 0.0f : -m1 * p.scale_log2;
+        const uint64_t shifts[2] = {pr_two(shift0, shift0), pr_two(shift1, shift1)};
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {  // 64 keys
           uint32_t w[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
-            const float a = ex2(fmaf(s[32 * i + 2 * q], p.scale_log2, -shift));
-            const float b = ex2(fmaf(s[32 * i + 2 * q + 1], p.scale_log2, -shift));
-            sum[2 * (q & 1)] += a;
-            sum[2 * (q & 1) + 1] += b;
+            float a, b;
+            pr_split(pr_fma2(pr_two(s[32 * i + 2 * q], s[32 * i + 2 * q + 1]), scale2, shifts[q & 1]), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum[q & 1] = pr_add2(sum[q & 1], pr_two(a, b));
             w[q] = pr_pack(a, b);
           }
-          tc::tmem_st16(ts + 16 * i, w);
+          pr_st16x32(ts + 32 * i, w);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[PF + 2 * t + i]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[PF + t]);
+        float a, b;
+        pr_split(sum[0], a, b);
+        l0 += a + b;
+        pr_split(sum[1], a, b);
+        l1 += a + b;
       }
-      if (!ok) break;
-      // ---- output
-      ok = __all_sync(0xffffffffu, wait(PV + t, (count - 1) & 1));
-      if (!ok) break;
+      o_turn ^= n & 1;  // (once a block)
+      if (ok) {
+#pragma unroll
+        for (int d = 1; d < 4; d *= 2) {
+          l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+          l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+        }
+        if ((lane & 3) == 0) {
+          rows[r0] = l0;
+          rows[r0 + 8] = l1;
+          rows[128 + r0] = m0;
+          rows[128 + r0 + 8] = m1;
+        }
+        ok = __all_sync(0xffffffffu, wait(PV + t, o_turn ^ 1u));
+      }
+      // ---- output: row 32 quarter + lane, head elements D / 2 half ..  The two warps meet here whatever happened: a
+      // wait that ran out is told to the other.
+      if (pr_any(pair, !ok)) {
+        ok = false;
+        break;
+      }
       tc::fence_after_sync();
-      const int row = x.begin + x.pos[t] + r;
+      const int r = 32 * quarter + lane;
+      const float l = rows[r], m = rows[128 + r];
+      const int row = x.begin + (t == 0 ? x.pos_a : x.pos_b) + r, head = t == 0 ? x.head_a : x.head_b;
       const bool live = row < x.end;
       const bool odd = odd_values[k & 3] == k + 1;
       const float inv = __fdiv_rn(1.0f, l);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 64; ++c) {
         float o[32];
-        pr_ld32(to + 32 * c, o);
+        const int d0 = half * (D / 2) + 32 * c;
+        pr_ld32(tb + (static_cast<uint32_t>(32 * quarter) << 16) + 256 + t * 128 + d0, o);
         pr_ld_wait(o);
         if (odd && live) {  // the values that were put to 0 and this row attends to
-          for (int key = x.begin + (x.blocks[0] - 1) * kPrTile; key <= row; ++key) {
-            const uint16_t* v = p.v + key * p.v_stride + (x.head[t] / p.G) * D + 32 * c;
+          for (int key = x.begin + (x.blocks_a - 1) * kPrTile; key <= row; ++key) {
+            const uint16_t* v = p.v + key * p.v_stride + (head / p.G) * D + d0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float a = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
@@ -477,17 +639,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           }
         }
         if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row) * p.Hq + x.head[t]) * D + 32 * c);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row) * p.Hq + head) * D + d0);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             dst[i] = make_uint4(pr_pack(o[8 * i] * inv, o[8 * i + 1] * inv), pr_pack(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                 pr_pack(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pr_pack(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
         }
       }
-      if (p.lse != nullptr && live)
-        p.lse[static_cast<int64_t>(row) * p.Hq + x.head[t]] =
+      if (p.lse != nullptr && live && half == 0)
+        p.lse[static_cast<int64_t>(row) * p.Hq + head] =
             l > 0.0f ? 0.69314718055994531f * fmaf(m, p.scale_log2, log2f(l)) : l == 0.0f ? -INFINITY : l;
-      tc::fence_before_sync();  // O is read before the next unit's first weights are announced
+      tc::fence_before_sync();
+      // O is read by both warps before either announces the next unit's weights (and the rows' numbers before they change)
+      asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(pair) : "memory");
     }
   }
   tc::fence_before_sync();
