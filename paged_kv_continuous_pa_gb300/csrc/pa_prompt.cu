@@ -15,13 +15,15 @@
 //   warps 0-7, 8-15  softmax of tile A, B: 16 rows to a warp, a row's scores in four lanes (so that a row is one
 //                    warp's, and four warps of a scheduler hide each other's latencies); output, a row to two threads
 //   warp 16          loads: queries and 128-key tiles of K and V through a ring (TMA)
-//   warp 17          issues the MMAs:  S = Q K^T (smem x smem), then O += P V (TMEM x smem)
-//   warps 18, 19     look over the values of the blocks that hold masked keys
+//   warps 17, 18     issue the MMAs of tile A, B:  S = Q K^T (smem x smem), O += P V (TMEM x smem).  (One for both
+//                    was busy for all of the 3800 clocks that two tiles' blocks took: a wait costs it 100 to 200, 16 MMAs
+//                    1024, and neither can the queue of MMAs hide the waits.)
+//   warp 19          looks over the values of the blocks that hold masked keys
 // Tensor memory: S of A and B (128 columns each), the weights P over their S as bf16, O of A and B.
 //
 // Masked keys.  Only the block on a tile's diagonal has any (keys behind the
 // sequence's end are behind every row's diagonal too).  A masked key's weight is 0,
-// but 0 times an infinite or NaN value is NaN, so warps 18 and 19 put 0 in the
+// but 0 times an infinite or NaN value is NaN, so warp 19 puts 0 in the
 // place of such values in shared memory; a row that does attend to one gets it added at the end.
 //
 // Units are listed longest first by a launch of their own and dealt out to the CTAs in a
@@ -127,6 +129,13 @@ __device__ __forceinline__ void pr_load_3d(void* dst_smem, const CUtensorMap* ma
           smem_addr(dst_smem)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
+}
+
+// The wait of a barrier that is not passed yet.
+__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, uint32_t limit, int32_t* status) {
+  if (mbar_wait(bar, parity, limit)) return true;
+  record_error(status, ST_TIMEOUT);
+  return false;
 }
 
 // 32 columns of this warp's lanes, without waiting; pr_ld_wait waits for every load started.
@@ -275,13 +284,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     QE = QF + 2,                 // ... read by the unit's MMAs
     SF = QE + 2,                 // scores of tile A / B
     PF = SF + 2,                 // weights of tile A / B, for either half of the keys (the scores are read, O may be added to)
-    PV = PF + 4,                 // O of tile A / B holds one more block
+    PV = PF + 4,                 // O of tile A / B is complete
     // the values of a block with masked keys are looked over: in turn, as the look may be a unit ahead of the
     // MMAs, and a unit has at most two such blocks
     VOK = PV + 2,
     VIN = VOK + 4,               // its load is under way (the ring's slot has come to this tile)
     DRAIN = VIN + 4,
-    STALL,
+    STALL = DRAIN + 2,
     COUNT
   };
   static_assert(COUNT * 8 + 32 <= S::ROWS - S::BAR, "barriers");
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
   if (warp == 0) tc::tmem_alloc(tslot, 512);
   if (tid == 0) {
-    for (int i = 0; i < COUNT; ++i) mbar_init(&bar[i], i >= PF && i < PF + 4 ? 8u : i >= VOK && i < VOK + 4 ? 2u : 1u);
+    for (int i = 0; i < COUNT; ++i) mbar_init(&bar[i], i >= PF && i < PF + 4 ? 8u : i >= EMPTY && i < QF ? 2u : 1u);
     for (int i = 0; i < 4; ++i) odd_values[i] = 0;
     fence_barrier_init();
     tc::prefetch_tensormap(&p.qmap);
@@ -313,11 +322,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   const int per_tile = two_heads ? p.Hq / 2 : p.Hq;
   const int units = *p.n_tiles * per_tile;
 
-  auto wait = [&](int b, uint32_t parity) {
-    if (mbar_wait(&bar[b], parity, p.wait_limit)) return true;
-    record_error(p.status, ST_TIMEOUT);
-    return false;
-  };
+  auto wait = [&](int b, uint32_t parity) { return mbar_test(&bar[b], parity) || pr_wait(&bar[b], parity, p.wait_limit, p.status); };
   // the k-th unit of this CTA (every other round backwards); false behind the last
   auto unit_at = [&](int k, PromptUnit& x) {
     const int64_t u = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -384,94 +389,95 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         if (done_a > 0) mbar_wait(&bar[QF], (done_a - 1) & 1, kDrainWaitLimit);
         if (done_b > 0) mbar_wait(&bar[QF + 1], (done_b - 1) & 1, kDrainWaitLimit);
       }
-    } else if (warp == 17 && lane == 0) {
-      // ---- MMAs
+    } else if (warp <= 18 && warp >= 17 && lane == 0) {
+      // ---- MMAs of tile t
       constexpr uint32_t id_qk = tc::idesc_bf16_f32(kPrTile, kPrTile, false);
       constexpr uint32_t id_pv = tc::idesc_bf16_f32(kPrTile, D, true);
+      const int t = warp - 17;
+      const uint32_t ts = tb + t * 128, to = ts + 256;
       PromptRing<S::STAGES> at;
-      uint32_t q_turn = 0, p_turn = 0;  // bit t: of tile t
+      uint32_t q_turn = 0, p_turn = 0;
       int checked = 0;
       bool ok = true;
       PromptUnit x{};
-      // Matrix descriptors differ in their address alone (the lower 14 bits, in 16 bytes).  The issue of 16 products
-      // takes as long as they do if each builds its own.
+      // Matrix descriptors differ in their address alone (the lower 14 bits, in 16 bytes).
       const uint64_t k_desc = tc::smem_desc(sm, 16, 1024), v_desc = tc::smem_desc(sm, S::HALF, 1024);
-      const uint32_t hi = static_cast<uint32_t>(k_desc >> 32), k_lo = static_cast<uint32_t>(k_desc), v_lo = static_cast<uint32_t>(v_desc);
+      const uint32_t hi = static_cast<uint32_t>(k_desc >> 32);
+      const uint32_t q_lo = static_cast<uint32_t>(k_desc) + t * (S::TILE >> 4);
+      const uint32_t k_lo = static_cast<uint32_t>(k_desc) + (S::RING >> 4), v_lo = static_cast<uint32_t>(v_desc) + (S::RING >> 4);
       auto desc = [&](uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; };
-      auto qk = [&](int t, int slot, bool last) {
-        const uint32_t q = k_lo + t * (S::TILE >> 4);
-        const uint32_t kt = k_lo + (S::RING >> 4) + slot * (S::TILE >> 4);
+      // the next tile of the ring (a tile that is not used is waited for, too: a turn that is missed looks like the next but one)
+      auto take = [&](int& slot) {
+        slot = at.slot;
+        const bool got = wait(FULL + at.slot, at.turn);
+        at.next();
+        return got;
+      };
+      auto qk = [&](int slot, bool last) {
+        const uint32_t kt = k_lo + slot * (S::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * S::HALF + (kk % 4) * 32) >> 4;
-          tc::mma_bf16(tb + t * 128, desc(q + off), desc(kt + off), id_qk, kk > 0);
+          tc::mma_bf16(ts, desc(q_lo + off), desc(kt + off), id_qk, kk > 0);
         }
         tc::mma_commit(&bar[SF + t]);
+        tc::mma_commit(&bar[EMPTY + slot]);
         if (last) tc::mma_commit(&bar[QE + t]);
       };
-      auto pv = [&](int t, int slot, bool first) {
-        const uint32_t vt = v_lo + (S::RING >> 4) + slot * (S::TILE >> 4);
+      auto pv = [&](int slot, bool first, bool last) {
+        const uint32_t vt = v_lo + slot * (S::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < kPrTile / 16; ++kk) {
           if (kk % 4 == 0) {
-            if (!wait(PF + 2 * t + kk / 4, (p_turn >> t) & 1u)) return false;
+            if (!wait(PF + 2 * t + kk / 4, p_turn)) return false;
             tc::fence_after_sync();
           }
-          tc::mma_bf16_ts(tb + 256 + t * 128, tb + t * 128 + kk * 8, desc(vt + kk * (2048 >> 4)), id_pv, !first || kk > 0);
+          tc::mma_bf16_ts(to, ts + kk * 8, desc(vt + kk * (2048 >> 4)), id_pv, !first || kk > 0);
         }
-        p_turn ^= 1u << t;
-        tc::mma_commit(&bar[PV + t]);
+        p_turn ^= 1u;
+        tc::mma_commit(&bar[EMPTY + slot]);
+        if (last) tc::mma_commit(&bar[PV + t]);
         return true;
       };
       for (int k = 0; ok && unit_at(k, x); ++k) {
         if (x.n == 0) continue;
-        const int k0 = at.slot;
-        ok = wait(FULL + at.slot, at.turn);
-        at.next();
-        if (ok) ok = wait(QF, q_turn & 1u);
+        const int n = t == 0 ? x.blocks_a : x.blocks_b;
+        int slot;
+        ok = take(slot);
         if (!ok) break;
-        q_turn ^= 1u;
-        qk(0, k0, x.blocks_a == 1);
-        if (x.blocks_b > 0) {
-          ok = wait(QF + 1, (q_turn >> 1) & 1u);
+        if (n > 0) {
+          ok = wait(QF + t, q_turn);
           if (!ok) break;
-          q_turn ^= 2u;
-          qk(1, k0, x.blocks_b == 1);
+          q_turn ^= 1u;
+          qk(slot, n == 1);
+        } else {
+          mbar_arrive(&bar[EMPTY + slot]);
         }
-        tc::mma_commit(&bar[EMPTY + k0]);
         for (int j = 0; j < x.n; ++j) {
-          const int v = at.slot;
-          ok = wait(FULL + at.slot, at.turn);
-          at.next();
+          ok = take(slot);
           if (ok && j >= x.blocks_a - 1) {
             ok = wait(VOK + (checked & 3), (checked >> 2) & 1);
             ++checked;
           }
-          const int kn = at.slot;
-          if (ok && j + 1 < x.n) {
-            ok = wait(FULL + at.slot, at.turn);
-            at.next();
-          }
+          if (ok && j < n)
+            ok = pv(slot, j == 0, j == n - 1);
+          else if (ok)
+            mbar_arrive(&bar[EMPTY + slot]);
           if (!ok) break;
-          if (j < x.blocks_a) {
-            ok = pv(0, v, j == 0);
-            if (!ok) break;
-            if (j + 1 < x.blocks_a) qk(0, kn, j + 2 == x.blocks_a);
-          }
-          if (j < x.blocks_b) {
-            ok = pv(1, v, j == 0);
-            if (!ok) break;
-            if (j + 1 < x.blocks_b) qk(1, kn, j + 2 == x.blocks_b);
-          }
-          tc::mma_commit(&bar[EMPTY + v]);
-          if (j + 1 < x.n) tc::mma_commit(&bar[EMPTY + kn]);
+          if (j + 1 == x.n) break;
+          ok = take(slot);
+          if (!ok) break;
+          if (j + 1 < n)
+            qk(slot, j + 2 == n);
+          else
+            mbar_arrive(&bar[EMPTY + slot]);
         }
       }
       if (!ok) {  // every MMA issued is done before the tensor memory is given up
-        tc::mma_commit(&bar[DRAIN]);
-        mbar_wait(&bar[DRAIN], 0, kDrainWaitLimit);
+        tc::mma_commit(&bar[DRAIN + t]);
+        mbar_wait(&bar[DRAIN + t], 0, kDrainWaitLimit);
       }
-    } else if (warp >= 18) {
+    } else if (warp == 19) {
       // ---- values of the blocks that hold masked keys: infinities and NaN become 0
       int base = 0, checked = 0;
       bool ok = true;
@@ -485,7 +491,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           if (!ok) break;
           uint4* tile = reinterpret_cast<uint4*>(sm + S::RING + (item % S::STAGES) * S::TILE);
           bool found = false;
-          for (int i = (warp - 18) * 32 + lane; i < S::TILE / 16; i += 64) {
+#pragma unroll 8
+          for (int i = lane; i < S::TILE / 16; i += 32) {
             uint4 w = tile[i];
             auto odd = [](uint32_t a) { return ((a & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };  // exponent of all ones
             if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
@@ -594,8 +601,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         pr_split(sum[1], a, b);
         l1 += a + b;
       }
-      o_turn ^= n & 1;  // (once a block)
-      if (ok) {
+            if (ok) {
 #pragma unroll
         for (int d = 1; d < 4; d *= 2) {
           l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -607,7 +613,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           rows[128 + r0] = m0;
           rows[128 + r0 + 8] = m1;
         }
-        ok = __all_sync(0xffffffffu, wait(PV + t, o_turn ^ 1u));
+        ok = __all_sync(0xffffffffu, wait(PV + t, o_turn));
+        o_turn ^= 1u;
       }
       // ---- output: row 32 quarter + lane, head elements D / 2 half ..  The two warps meet here whatever happened: a
       // wait that ran out is told to the other.
