@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     // MMAs, and a unit has at most two such blocks
     VOK = PV + 2,
     VIN = VOK + 4,               // its load is under way (the ring's slot has come to this tile)
-    DRAIN = VIN + 4,
+    TURN = VIN + 4,              // tile A / B has issued the MMAs of one more block
+    DRAIN = TURN + 2,
     STALL = DRAIN + 2,
     COUNT
   };
@@ -413,64 +414,88 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         at.next();
         return got;
       };
-      auto qk = [&](int slot, bool last) {
+      int blocks = 0;  // of all units so far
+      // The tiles take turns, a block's products with V and with the next keys at a time: MMAs of the two that
+      // mix end at the same time, and then the softmax of both runs while the tensor core waits (3780 clocks a pair
+      // of blocks).  A's i-th block comes behind B's block i - 1, B's behind A's block i; the turn is passed on four
+      // MMAs before its end, which hide the way to the other warp, and the commits (100 clocks each) come behind.
+      auto my_turn = [&] {
+        if (t == 0) return blocks == 0 || wait(TURN + 1, (blocks - 1) & 1);
+        return wait(TURN, blocks & 1);
+      };
+      auto pass_on = [&] {
+        mbar_arrive(&bar[TURN + t]);
+        ++blocks;
+      };
+      auto qk = [&](int slot, int from, int to_step) {
         const uint32_t kt = k_lo + slot * (S::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * S::HALF + (kk % 4) * 32) >> 4;
-          tc::mma_bf16(ts, desc(q_lo + off), desc(kt + off), id_qk, kk > 0);
+          if (kk >= from && kk < to_step) tc::mma_bf16(ts, desc(q_lo + off), desc(kt + off), id_qk, kk > 0);
         }
+      };
+      auto qk_commit = [&](int slot, bool last) {
         tc::mma_commit(&bar[SF + t]);
         tc::mma_commit(&bar[EMPTY + slot]);
         if (last) tc::mma_commit(&bar[QE + t]);
       };
-      auto pv = [&](int slot, bool first, bool last) {
+      auto pv = [&](int slot, bool first) {
         const uint32_t vt = v_lo + slot * (S::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < kPrTile / 16; ++kk) {
-          if (kk % 4 == 0) {
-            if (!wait(PF + 2 * t + kk / 4, p_turn)) return false;
-            tc::fence_after_sync();
-          }
+          if (kk == 4 && !wait(PF + 2 * t + 1, p_turn)) return false;
+          if (kk % 4 == 0) tc::fence_after_sync();
           tc::mma_bf16_ts(to, ts + kk * 8, desc(vt + kk * (2048 >> 4)), id_pv, !first || kk > 0);
         }
         p_turn ^= 1u;
-        tc::mma_commit(&bar[EMPTY + slot]);
-        if (last) tc::mma_commit(&bar[PV + t]);
         return true;
       };
       for (int k = 0; ok && unit_at(k, x); ++k) {
         if (x.n == 0) continue;
         const int n = t == 0 ? x.blocks_a : x.blocks_b;
-        int slot;
+        int slot, next;
         ok = take(slot);
         if (!ok) break;
         if (n > 0) {
           ok = wait(QF + t, q_turn);
           if (!ok) break;
           q_turn ^= 1u;
-          qk(slot, n == 1);
+          qk(slot, 0, D / 16);
+          qk_commit(slot, n == 1);
         } else {
           mbar_arrive(&bar[EMPTY + slot]);
         }
         for (int j = 0; j < x.n; ++j) {
+          // everything that the turn needs, before it
           ok = take(slot);
           if (ok && j >= x.blocks_a - 1) {
             ok = wait(VOK + (checked & 3), (checked >> 2) & 1);
             ++checked;
           }
-          if (ok && j < n)
-            ok = pv(slot, j == 0, j == n - 1);
-          else if (ok)
-            mbar_arrive(&bar[EMPTY + slot]);
+          if (ok && j + 1 < x.n) ok = take(next);
+          if (ok && j < n) ok = wait(PF + 2 * t, p_turn);
+          ok = ok && my_turn();
           if (!ok) break;
-          if (j + 1 == x.n) break;
-          ok = take(slot);
-          if (!ok) break;
-          if (j + 1 < n)
-            qk(slot, j + 2 == n);
-          else
+          if (j >= n) {  // no block of this tile
+            pass_on();
             mbar_arrive(&bar[EMPTY + slot]);
+            if (j + 1 < x.n) mbar_arrive(&bar[EMPTY + next]);
+            continue;
+          }
+          ok = pv(slot, j == 0);
+          if (!ok) break;
+          if (j + 1 < n) {
+            qk(next, 0, D / 16 - 4);
+            pass_on();
+            qk(next, D / 16 - 4, D / 16);
+            qk_commit(next, j + 2 == n);
+          } else {
+            pass_on();
+            if (j + 1 < x.n) mbar_arrive(&bar[EMPTY + next]);
+          }
+          tc::mma_commit(&bar[EMPTY + slot]);
+          if (j == n - 1) tc::mma_commit(&bar[PV + t]);
         }
       }
       if (!ok) {  // every MMA issued is done before the tensor memory is given up
