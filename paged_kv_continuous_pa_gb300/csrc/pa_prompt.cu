@@ -4,26 +4,27 @@
 //   out_i = sum_{j <= i} exp2(s_ij - m_i) v_j / sum_{j <= i} exp2(s_ij - m_i),   s_ij = scale log2(e) q_i . k_j
 //
 // One pass over the keys with a running reference m_i: it moves only when a score
-// passes it by 2^8, so the accumulator is seldom rescaled, and a row's maximum is
-// only taken over its four lanes then.
+// passes it by 2^8, so the accumulator is seldom rescaled, a row's maximum is
+// only taken over its four lanes then, and the first half of a block's weights is
+// computed beside the maximum, before it is known whether they will do.
 //
 // What bounds it: the two matrix products, 4 D flops for each (query head, query, key).
 // One CTA per SM goes through units of work.  A unit is two query tiles of 128 rows that
 // read the same keys: two query heads of one kv head at the same positions where the
 // head group is even, else two neighbouring ranges of 128 positions of one head.  While
 // the softmax of one tile runs, the tensor core works for the other.
-//   warps 0-7, 8-15  softmax of tile A, B: 16 rows to a warp, a row's scores in four lanes (so that a row is one
-//                    warp's, and four warps of a scheduler hide each other's latencies); output, a row to two threads
+//   warps 0-7, 8-15  softmax and output of tile A, B: 16 rows to a warp, a row in four lanes (so that a row is one
+//                    warp's, and four warps of a scheduler hide each other's latencies); while they wait for the scores
+//                    of a block with masked keys they look over its values
 //   warp 16          loads: queries and 128-key tiles of K and V through a ring (TMA)
-//   warps 17, 18     issue the MMAs of tile A, B:  S = Q K^T (smem x smem), O += P V (TMEM x smem).  (One for both
+//   warps 18, 19     issue the MMAs of tile A, B:  S = Q K^T (smem x smem), O += P V (TMEM x smem).  (One for both
 //                    was busy for all of the 3800 clocks that two tiles' blocks took: a wait costs it 100 to 200, 16 MMAs
 //                    1024, and neither can the queue of MMAs hide the waits.)
-//   warp 19          looks over the values of the blocks that hold masked keys
 // Tensor memory: S of A and B (128 columns each), the weights P over their S as bf16, O of A and B.
 //
 // Masked keys.  Only the block on a tile's diagonal has any (keys behind the
 // sequence's end are behind every row's diagonal too).  A masked key's weight is 0,
-// but 0 times an infinite or NaN value is NaN, so warp 19 puts 0 in the
+// but 0 times an infinite or NaN value is NaN, so 0 is put in the
 // place of such values in shared memory; a row that does attend to one gets it added at the end.
 //
 // Units are listed longest first by a launch of their own and dealt out to the CTAs in a
@@ -138,18 +139,7 @@ __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, uint32_t
   return false;
 }
 
-// 32 columns of this warp's lanes, without waiting; pr_ld_wait waits for every load started.
-__device__ __forceinline__ void pr_ld32(uint32_t taddr, float* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
+// Waits for every load of tensor memory started; r is read only behind it.
 __device__ __forceinline__ void pr_ld_wait(float* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
@@ -161,7 +151,7 @@ __device__ __forceinline__ void pr_ld_wait(float* r) {
                : "memory");
 }
 
-// 64 columns of 16 lanes: lane 4 g + c of the warp gets columns 8 i + 2c, + 1 of rows g (r[4i], r[4i + 1]) and g + 8.
+// 64 columns of 16 lanes, without waiting: lane 4 g + c of the warp gets columns 8 i + 2c, + 1 of rows g (r[4i], r[4i + 1]) and g + 8.
 __device__ __forceinline__ void pr_ld16x64(uint32_t taddr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -227,18 +217,51 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
   return d;
 }
 
-// Barrier `id` of two warps; true where `x` holds for a thread of either.
-__device__ __forceinline__ bool pr_any(int id, bool x) {
-  uint32_t r;
+// Four words of each of a quad's lanes transposed: lane c gets word c of its lanes in order.
+__device__ __forceinline__ void pr_transpose4(uint32_t (&w)[4], int c) {
+#pragma unroll
+  for (int d = 1; d < 4; d *= 2) {
+    const bool up = (c & d) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + d], d);
+      if (up)
+        w[i] = got;
+      else
+        w[i + d] = got;
+    }
+  }
+}
+
+// One lane of a converged warp, the same one each time, as a number that is 0 elsewhere.
+__device__ __forceinline__ uint32_t pr_elect() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(one));
+  return one;
+}
+// D[tmem] (+)= A B and a commit, by the lane where `one` is not 0: the warp stays together, so that operands
+// are worked out once for all of it.
+__device__ __forceinline__ void pr_mma(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, %1, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(x ? 1u : 0u)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u), "r"(one)
       : "memory");
-  return r != 0;
+}
+__device__ __forceinline__ void pr_mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void pr_commit(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(one)
+      : "memory");
 }
 
 template <int D>
@@ -249,8 +272,7 @@ struct PromptSmem {  // byte offsets from the base, which is 1024-byte aligned (
   static constexpr int STAGES = D == 128 ? 5 : 8;  // tiles of K and V in the ring
   static constexpr int RING = 2 * TILE;            // behind the two query tiles
   static constexpr int BAR = RING + STAGES * TILE;
-  static constexpr int ROWS = BAR + 384;           // a number of each softmax thread
-  static constexpr int BYTES = ROWS + kPrSoftmaxThreads * 4;
+  static constexpr int BYTES = BAR + 384;
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -282,19 +304,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     EMPTY = FULL + S::STAGES,    // ... read by its MMAs
     QF = EMPTY + S::STAGES,      // queries of tile A / B landed
     QE = QF + 2,                 // ... read by the unit's MMAs
-    SF = QE + 2,                 // scores of tile A / B
-    PF = SF + 2,                 // weights of tile A / B, for either half of the keys (the scores are read, O may be added to)
+    SF = QE + 2,                 // scores of tile A / B for the first / second 64 keys of a block
+    PF = SF + 4,                 // ... their weights (the scores are read, O may be added to)
     PV = PF + 4,                 // O of tile A / B is complete
+    PL = PV + 2,                 // ... holds all but the unit's last 64 keys
     // the values of a block with masked keys are looked over: in turn, as the look may be a unit ahead of the
     // MMAs, and a unit has at most two such blocks
-    VOK = PV + 2,
+    VOK = PL + 2,
     VIN = VOK + 4,               // its load is under way (the ring's slot has come to this tile)
-    TURN = VIN + 4,              // tile A / B has issued the MMAs of one more block
-    DRAIN = TURN + 2,
+    DRAIN = VIN + 4,
     STALL = DRAIN + 2,
     COUNT
   };
-  static_assert(COUNT * 8 + 32 <= S::ROWS - S::BAR, "barriers");
+  static_assert(COUNT * 8 + 32 <= S::BYTES - S::BAR, "barriers");
   extern __shared__ __align__(1024) unsigned char sm[];
   if ((smem_addr(sm) & 1023u) != 0) {  // (the swizzled tiles would be read at other places than they were written)
     if (threadIdx.x == 0) record_error(p.status, ST_LAUNCH);
@@ -307,7 +329,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
 
   if (warp == 0) tc::tmem_alloc(tslot, 512);
   if (tid == 0) {
-    for (int i = 0; i < COUNT; ++i) mbar_init(&bar[i], i >= PF && i < PF + 4 ? 8u : i >= EMPTY && i < QF ? 2u : 1u);
+    for (int i = 0; i < COUNT; ++i) mbar_init(&bar[i], i >= PF && i < PF + 4 ? 8u : i >= EMPTY && i < QF ? 2u : i >= VOK && i < VOK + 4 ? 8u : 1u);
     for (int i = 0; i < 4; ++i) odd_values[i] = 0;
     fence_barrier_init();
     tc::prefetch_tensormap(&p.qmap);
@@ -324,13 +346,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   const int units = *p.n_tiles * per_tile;
 
   auto wait = [&](int b, uint32_t parity) { return mbar_test(&bar[b], parity) || pr_wait(&bar[b], parity, p.wait_limit, p.status); };
-  // the k-th unit of this CTA (every other round backwards); false behind the last
+  // the k-th unit of this CTA (every other round backwards); false behind the last.  The tile of the next one is
+  // on its way meanwhile.
+  auto index_of = [&](int k) {
+    return static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  };
+  int4 ahead = index_of(0) < units ? __ldcg(p.tiles + index_of(0) / per_tile) : make_int4(0, 0, 0, 0);
   auto unit_at = [&](int k, PromptUnit& x) {
-    const int64_t u = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    const int64_t u = index_of(k);
     if (static_cast<int64_t>(k) * gridDim.x >= units) return false;
+    const int4 t = ahead;
+    if (index_of(k + 1) < units) ahead = __ldcg(p.tiles + index_of(k + 1) / per_tile);
     x.n = x.blocks_a = x.blocks_b = 0;
     if (u >= units) return true;  // (a round without work for this CTA)
-    const int4 t = __ldcg(p.tiles + u / per_tile);
     const int h = static_cast<int>(u % per_tile);
     x.begin = t.x;
     x.end = t.y;
@@ -390,17 +418,26 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         if (done_a > 0) mbar_wait(&bar[QF], (done_a - 1) & 1, kDrainWaitLimit);
         if (done_b > 0) mbar_wait(&bar[QF + 1], (done_b - 1) & 1, kDrainWaitLimit);
       }
-    } else if (warp <= 18 && warp >= 17 && lane == 0) {
-      // ---- MMAs of tile t
-      constexpr uint32_t id_qk = tc::idesc_bf16_f32(kPrTile, kPrTile, false);
+    } else if (warp >= 18) {
+      // ---- MMAs of tile t.  A block's scores are two products of 64 keys with a place of their own each: while
+      // the weights of one are computed the tensor core has the other, and the same place's next scores come
+      // right behind its product with V.  (Products of 128 keys into one place take 2048 clocks a pair of tiles
+      // instead of 2560, as their operands come from shared memory at its full rate, but wait for the weights and the
+      // weights for them: 3500 clocks.)
+      constexpr uint32_t id_qk = tc::idesc_bf16_f32(kPrTile, 64, false);
       constexpr uint32_t id_pv = tc::idesc_bf16_f32(kPrTile, D, true);
-      const int t = warp - 17;
+      const int t = warp - 18;
       const uint32_t ts = tb + t * 128, to = ts + 256;
       PromptRing<S::STAGES> at;
       uint32_t q_turn = 0, p_turn = 0;
       int checked = 0;
       bool ok = true;
       PromptUnit x{};
+      const uint32_t one = pr_elect();
+      auto wait_all = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+      auto arrive = [&](int b) {
+        if (lane == 0) mbar_arrive(&bar[b]);
+      };
       // Matrix descriptors differ in their address alone (the lower 14 bits, in 16 bytes).
       const uint64_t k_desc = tc::smem_desc(sm, 16, 1024), v_desc = tc::smem_desc(sm, S::HALF, 1024);
       const uint32_t hi = static_cast<uint32_t>(k_desc >> 32);
@@ -410,280 +447,280 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       // the next tile of the ring (a tile that is not used is waited for, too: a turn that is missed looks like the next but one)
       auto take = [&](int& slot) {
         slot = at.slot;
-        const bool got = wait(FULL + at.slot, at.turn);
+        const bool got = wait_all(FULL + at.slot, at.turn);
         at.next();
         return got;
       };
-      int blocks = 0;  // of all units so far
-      // The tiles take turns, a block's products with V and with the next keys at a time: MMAs of the two that
-      // mix end at the same time, and then the softmax of both runs while the tensor core waits (3780 clocks a pair
-      // of blocks).  A's i-th block comes behind B's block i - 1, B's behind A's block i; the turn is passed on four
-      // MMAs before its end, which hide the way to the other warp, and the commits (100 clocks each) come behind.
-      auto my_turn = [&] {
-        if (t == 0) return blocks == 0 || wait(TURN + 1, (blocks - 1) & 1);
-        return wait(TURN, blocks & 1);
+      auto skip = [&](int& slot) {
+        slot = at.slot;
+        at.next();
       };
-      auto pass_on = [&] {
-        mbar_arrive(&bar[TURN + t]);
-        ++blocks;
-      };
-      auto qk = [&](int slot, int from, int to_step) {
-        const uint32_t kt = k_lo + slot * (S::TILE >> 4);
+      auto qk = [&](int slot, int half) {
+        const uint32_t kt = k_lo + slot * (S::TILE >> 4) + half * ((64 * 128) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * S::HALF + (kk % 4) * 32) >> 4;
-          if (kk >= from && kk < to_step) tc::mma_bf16(ts, desc(q_lo + off), desc(kt + off), id_qk, kk > 0);
+          pr_mma(one, ts + 64 * half, desc(q_lo + off), desc(kt + off), id_qk, kk > 0);
         }
+        pr_commit(one, &bar[SF + 2 * t + half]);
       };
-      auto qk_commit = [&](int slot, bool last) {
-        tc::mma_commit(&bar[SF + t]);
-        tc::mma_commit(&bar[EMPTY + slot]);
-        if (last) tc::mma_commit(&bar[QE + t]);
-      };
-      auto pv = [&](int slot, bool first) {
-        const uint32_t vt = v_lo + slot * (S::TILE >> 4);
+      auto pv = [&](int slot, int half, bool first) {
+        if (!wait_all(PF + 2 * t + half, p_turn)) return false;
+        tc::fence_after_sync();
+        const uint32_t vt = v_lo + slot * (S::TILE >> 4) + half * ((64 * 128) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kPrTile / 16; ++kk) {
-          if (kk == 4 && !wait(PF + 2 * t + 1, p_turn)) return false;
-          if (kk % 4 == 0) tc::fence_after_sync();
-          tc::mma_bf16_ts(to, ts + kk * 8, desc(vt + kk * (2048 >> 4)), id_pv, !first || kk > 0);
-        }
-        p_turn ^= 1u;
+        for (int kk = 0; kk < 4; ++kk)
+          pr_mma_ts(one, to, ts + 64 * half + kk * 8, desc(vt + kk * (2048 >> 4)), id_pv, !first || kk > 0);
         return true;
       };
       for (int k = 0; ok && unit_at(k, x); ++k) {
         if (x.n == 0) continue;
         const int n = t == 0 ? x.blocks_a : x.blocks_b;
-        int slot, next;
-        ok = take(slot);
+        int slot, next = 0;
+        ok = take(slot) && (n == 0 || wait_all(QF + t, q_turn));
         if (!ok) break;
         if (n > 0) {
-          ok = wait(QF + t, q_turn);
-          if (!ok) break;
           q_turn ^= 1u;
-          qk(slot, 0, D / 16);
-          qk_commit(slot, n == 1);
+          qk(slot, 0);
+          qk(slot, 1);
+          if (n == 1) pr_commit(one, &bar[QE + t]);
         } else {
-          mbar_arrive(&bar[EMPTY + slot]);
+          arrive(EMPTY + slot);
         }
         for (int j = 0; j < x.n; ++j) {
-          // everything that the turn needs, before it
-          ok = take(slot);
+          if (j < n) {
+            skip(slot);
+            if (j + 1 < n)
+              skip(next);
+            else if (j + 1 < x.n)
+              ok = take(next);
+          } else {
+            ok = take(slot) && (j + 1 == x.n || take(next));
+          }
           if (ok && j >= x.blocks_a - 1) {
-            ok = wait(VOK + (checked & 3), (checked >> 2) & 1);
+            ok = wait_all(VOK + (checked & 3), (checked >> 2) & 1);
             ++checked;
           }
-          if (ok && j + 1 < x.n) ok = take(next);
-          if (ok && j < n) ok = wait(PF + 2 * t, p_turn);
-          ok = ok && my_turn();
           if (!ok) break;
           if (j >= n) {  // no block of this tile
-            pass_on();
-            mbar_arrive(&bar[EMPTY + slot]);
-            if (j + 1 < x.n) mbar_arrive(&bar[EMPTY + next]);
+            arrive(EMPTY + slot);
+            if (j + 1 < x.n) arrive(EMPTY + next);
             continue;
           }
-          ok = pv(slot, j == 0);
+          ok = pv(slot, 0, j == 0);
           if (!ok) break;
-          if (j + 1 < n) {
-            qk(next, 0, D / 16 - 4);
-            pass_on();
-            qk(next, D / 16 - 4, D / 16);
-            qk_commit(next, j + 2 == n);
-          } else {
-            pass_on();
-            if (j + 1 < x.n) mbar_arrive(&bar[EMPTY + next]);
-          }
-          tc::mma_commit(&bar[EMPTY + slot]);
-          if (j == n - 1) tc::mma_commit(&bar[PV + t]);
+          if (j + 1 < n) qk(next, 0);
+          if (j + 1 == n) pr_commit(one, &bar[PL + t]);
+          ok = pv(slot, 1, false);
+          if (!ok) break;
+          p_turn ^= 1u;
+          if (j + 1 < n) qk(next, 1);
+          if (j + 1 == n && j + 1 < x.n) arrive(EMPTY + next);
+          if (j + 2 == n) pr_commit(one, &bar[QE + t]);
+          if (j + 1 == n) pr_commit(one, &bar[PV + t]);
         }
       }
       if (!ok) {  // every MMA issued is done before the tensor memory is given up
-        tc::mma_commit(&bar[DRAIN + t]);
+        pr_commit(one, &bar[DRAIN + t]);
         mbar_wait(&bar[DRAIN + t], 0, kDrainWaitLimit);
-      }
-    } else if (warp == 19) {
-      // ---- values of the blocks that hold masked keys: infinities and NaN become 0
-      int base = 0, checked = 0;
-      bool ok = true;
-      PromptUnit x{};
-      for (int k = 0; ok && unit_at(k, x); ++k) {
-        if (x.n == 0) continue;
-        for (int j = x.blocks_a - 1; ok && j < x.n; ++j, ++checked) {
-          const int item = base + 2 * j + 1;
-          ok = __all_sync(0xffffffffu, wait(VIN + (checked & 3), (checked >> 2) & 1) &&
-                                           wait(FULL + item % S::STAGES, (item / S::STAGES) & 1));
-          if (!ok) break;
-          uint4* tile = reinterpret_cast<uint4*>(sm + S::RING + (item % S::STAGES) * S::TILE);
-          bool found = false;
-#pragma unroll 8
-          for (int i = lane; i < S::TILE / 16; i += 32) {
-            uint4 w = tile[i];
-            auto odd = [](uint32_t a) { return ((a & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };  // exponent of all ones
-            if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
-              auto clean = [&](uint32_t a) {
-                const uint32_t o = odd(a);
-                return a & ~((o & 0x8000u ? 0xffffu : 0u) | (o & 0x80000000u ? 0xffff0000u : 0u));
-              };
-              tile[i] = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
-              found = true;
-            }
-          }
-          if (found) odd_values[k & 3] = k + 1;
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[VOK + (checked & 3)]);
-        }
-        base += 2 * x.n;
       }
     }
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrSoftmaxRegs));
-    // ---- softmax and output of tile t
-    const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-    const int pair = 1 + t * 4 + quarter;  // barrier of the two warps that share 32 rows
-    float* rows = reinterpret_cast<float*>(sm + S::ROWS) + t * 256;  // per row of the tile its sum and its reference
-    // softmax: rows r0 and r0 + 8, columns 8 i + 2 c, + 1
-    const int r0 = 32 * quarter + 16 * half + (lane >> 2), c2 = 2 * (lane & 3);
-    const uint32_t ts = tb + (static_cast<uint32_t>(32 * quarter + 16 * half) << 16) + t * 128, to = ts + 256;
+    // ---- softmax and output of tile t: rows r0 and r0 + 8, columns 8 i + 2 c, + 1
+    const int t = warp >> 3, c = lane & 3;
+    const int r0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1) + (lane >> 2);
+    const uint32_t ts = tb + (static_cast<uint32_t>(r0 - (lane >> 2)) << 16) + t * 128, to = ts + 256;
     const uint64_t scale2 = pr_two(p.scale_log2, p.scale_log2);
     uint32_t s_turn = 0, o_turn = 0;
+    int items = 0, checked = 0;  // tiles of K and V, and those looked over, of all units so far
+    const bool leader = (warp & 7) == 0;
+    auto landed = [&](int item) { return wait(FULL + item % S::STAGES, (item / S::STAGES) & 1); };
+    auto release = [&](int item) {
+      if (leader && lane == 0) mbar_arrive(&bar[EMPTY + item % S::STAGES]);
+    };
     bool ok = true;
     PromptUnit x{};
+    // Values of block `block` (the ring's tile `item`): infinities and NaN become 0.
+    auto look_over = [&](int item, int k) {
+      const int slot = item % S::STAGES;
+      if (!__all_sync(0xffffffffu, wait(VIN + (checked & 3), (checked >> 2) & 1) && wait(FULL + slot, (item / S::STAGES) & 1)))
+        return false;
+      uint4* tile = reinterpret_cast<uint4*>(sm + S::RING + slot * S::TILE);
+      bool found = false;
+#pragma unroll 4
+      for (int i = tid & 255; i < S::TILE / 16; i += 256) {
+        const uint4 w = tile[i];
+        auto odd = [](uint32_t a) { return ((a & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };  // exponent of all ones
+        if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
+          auto clean = [&](uint32_t a) {
+            const uint32_t o = odd(a);
+            return a & ~((o & 0x8000u ? 0xffffu : 0u) | (o & 0x80000000u ? 0xffff0000u : 0u));
+          };
+          tile[i] = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+          found = true;
+        }
+      }
+      if (found) odd_values[k & 3] = k + 1;
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[VOK + (checked & 3)]);
+      return true;
+    };
     for (int k = 0; ok && unit_at(k, x); ++k) {
       const int n = t == 0 ? x.blocks_a : x.blocks_b;
-      if (n == 0) continue;
+      const bool two_looks = x.blocks_b > x.blocks_a;  // each tile's warps look over the values of its own diagonal
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
       for (int j = 0; j < n; ++j, s_turn ^= 1u) {
-        ok = __all_sync(0xffffffffu, wait(SF + t, s_turn));
-        if (!ok) break;
-        tc::fence_after_sync();
-        float s[64];
-        pr_ld16x64(ts, s);
-        pr_ld16x64(ts + 64, s + 32);
-        pr_ld_wait(s);
-        pr_ld_wait(s + 32);
-        if (j == n - 1) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const int column = 8 * (i >> 2) + c2 + (i & 1);
-            s[i] = column > r0 + ((i & 2) ? 8 : 0) ? -INFINITY : s[i];
-          }
+        if (j == n - 1 && (t == 0 || two_looks)) {
+          checked += t;
+          ok = look_over(items + 2 * j + 1, k);
+          checked -= t;
+          if (!ok) break;
         }
-        float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]), b0 = fmaxf(s[4], s[5]), b1 = fmaxf(s[6], s[7]);
-#pragma unroll
-        for (int i = 8; i < 64; i += 8) {
-          a0 = pr_max3(a0, s[i], s[i + 1]);
-          a1 = pr_max3(a1, s[i + 2], s[i + 3]);
-          b0 = pr_max3(b0, s[i + 4], s[i + 5]);
-          b1 = pr_max3(b1, s[i + 6], s[i + 7]);
-        }
-        float top0 = fmaxf(a0, b0), top1 = fmaxf(a1, b1);
-        if (__any_sync(0xffffffffu, (top0 - m0) * p.scale_log2 > kRescaleSlack || (top1 - m1) * p.scale_log2 > kRescaleSlack)) {
-#pragma unroll
-          for (int d = 1; d < 4; d *= 2) {
-            top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
-            top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
+        for (int half = 0; half < 2; ++half) {  // 64 keys
+          ok = __all_sync(0xffffffffu, wait(SF + 2 * t + half, s_turn));
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (half == 0 && leader) {  // what the issuer needs behind these weights
+            ok = __all_sync(0xffffffffu, landed(items + 2 * j + 1) && (j + 1 == n || landed(items + 2 * j + 2)));
+            if (!ok) break;
           }
-          const bool move0 = (top0 - m0) * p.scale_log2 > kRescaleSlack, move1 = (top1 - m1) * p.scale_log2 > kRescaleSlack;
-          if (j > 0) {
-            // (the scores' commit came behind the last block's product with V: O stands still)
-            const float f0 = move0 ? ex2((m0 - top0) * p.scale_log2) : 1.0f, f1 = move1 ? ex2((m1 - top1) * p.scale_log2) : 1.0f;
-            l0 *= f0;
-            l1 *= f1;
+          if (half == 1) {  // the block's scores are complete, and with them the last block's product with V
+            release(items + 2 * j);
+            if (j > 0) release(items + 2 * j - 1);
+          }
+          const uint32_t at = ts + 64 * half;
+          float s[32];
+          pr_ld16x64(at, s);
+          pr_ld_wait(s);
+          if (j == n - 1) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int column = 64 * half + 8 * (i >> 2) + 2 * c + (i & 1);
+              s[i] = column > r0 + ((i & 2) ? 8 : 0) ? -INFINITY : s[i];
+            }
+          }
+          float top0 = fmaxf(s[0], s[1]), top1 = fmaxf(s[2], s[3]);
+#pragma unroll
+          for (int i = 4; i < 32; i += 4) {
+            top0 = pr_max3(top0, s[i], s[i + 1]);
+            top1 = pr_max3(top1, s[i + 2], s[i + 3]);
+          }
+          if (__any_sync(0xffffffffu, (top0 - m0) * p.scale_log2 > kRescaleSlack || (top1 - m1) * p.scale_log2 > kRescaleSlack)) {
+#pragma unroll
+            for (int d = 1; d < 4; d *= 2) {
+              top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
+              top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
+            }
+            const bool move0 = (top0 - m0) * p.scale_log2 > kRescaleSlack, move1 = (top1 - m1) * p.scale_log2 > kRescaleSlack;
+            if (j > 0 || half > 0) {
+              // The products with V so far come first.  The next scores were issued behind the last of them.
+              const bool got = half == 0    ? wait(SF + 2 * t + 1, s_turn)
+                               : j + 1 < n ? wait(SF + 2 * t, s_turn ^ 1u)
+                                           : wait(PL + t, o_turn);
+              ok = __all_sync(0xffffffffu, got);
+              if (!ok) break;
+              tc::fence_after_sync();
+              const float f0 = move0 ? ex2((m0 - top0) * p.scale_log2) : 1.0f, f1 = move1 ? ex2((m1 - top1) * p.scale_log2) : 1.0f;
+              l0 *= f0;
+              l1 *= f1;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) pr_scale16x16(to + c, f0, f1);
-            tc::tmem_wait_st();
+              for (int d = 0; d < D; d += 16) pr_scale16x16(to + d, f0, f1);
+              tc::tmem_wait_st();
+            }
+            if (move0) m0 = top0;
+            if (move1) m1 = top1;
           }
-          if (move0) m0 = top0;
-          if (move1) m1 = top1;
-        }
-        const float shift0 = m0 == -INFINITY ? 0.0f : -m0 * p.scale_log2, shift1 = m1 == -INFINITY ? 0.0f : -m1 * p.scale_log2;
-        const uint64_t shifts[2] = {pr_two(shift0, shift0), pr_two(shift1, shift1)};
-        uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {  // 64 keys
+          const float shift0 = m0 == -INFINITY ? 0.0f : -m0 * p.scale_log2, shift1 = m1 == -INFINITY ? 0.0f : -m1 * p.scale_log2;
+          const uint64_t shifts[2] = {pr_two(shift0, shift0), pr_two(shift1, shift1)};
+          uint64_t sum[2] = {0ull, 0ull};
           uint32_t w[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             float a, b;
-            pr_split(pr_fma2(pr_two(s[32 * i + 2 * q], s[32 * i + 2 * q + 1]), scale2, shifts[q & 1]), a, b);
+            pr_split(pr_fma2(pr_two(s[2 * q], s[2 * q + 1]), scale2, shifts[q & 1]), a, b);
             a = ex2(a);
             b = ex2(b);
             sum[q & 1] = pr_add2(sum[q & 1], pr_two(a, b));
             w[q] = pr_pack(a, b);
           }
-          pr_st16x32(ts + 32 * i, w);
+          pr_st16x32(at, w);
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[PF + 2 * t + i]);
+          if (lane == 0) mbar_arrive(&bar[PF + 2 * t + half]);
+          float a, b;
+          pr_split(sum[0], a, b);
+          l0 += a + b;
+          pr_split(sum[1], a, b);
+          l1 += a + b;
         }
-        float a, b;
-        pr_split(sum[0], a, b);
-        l0 += a + b;
-        pr_split(sum[1], a, b);
-        l1 += a + b;
+        if (!ok) break;
       }
-            if (ok) {
-#pragma unroll
-        for (int d = 1; d < 4; d *= 2) {
-          l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-          l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-        }
-        if ((lane & 3) == 0) {
-          rows[r0] = l0;
-          rows[r0 + 8] = l1;
-          rows[128 + r0] = m0;
-          rows[128 + r0 + 8] = m1;
-        }
-        ok = __all_sync(0xffffffffu, wait(PV + t, o_turn));
-        o_turn ^= 1u;
-      }
-      // ---- output: row 32 quarter + lane, head elements D / 2 half ..  The two warps meet here whatever happened: a
-      // wait that ran out is told to the other.
-      if (pr_any(pair, !ok)) {
-        ok = false;
-        break;
-      }
+      if (!ok) break;
+      items += 2 * x.n;
+      checked += x.n == 0 ? 0 : two_looks ? 2 : 1;
+      if (n == 0) continue;
+      // ---- output
+      ok = __all_sync(0xffffffffu, wait(PV + t, o_turn));
+      if (!ok) break;
+      o_turn ^= 1u;
+      release(items - 2 * x.n + 2 * n - 1);
       tc::fence_after_sync();
-      const int r = 32 * quarter + lane;
-      const float l = rows[r], m = rows[128 + r];
-      const int row = x.begin + (t == 0 ? x.pos_a : x.pos_b) + r, head = t == 0 ? x.head_a : x.head_b;
-      const bool live = row < x.end;
+#pragma unroll
+      for (int d = 1; d < 4; d *= 2) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      }
+      const int row0 = x.begin + (t == 0 ? x.pos_a : x.pos_b) + r0, row1 = row0 + 8, head = t == 0 ? x.head_a : x.head_b;
       const bool odd = odd_values[k & 3] == k + 1;
-      const float inv = __fdiv_rn(1.0f, l);
+      const float inv0 = __fdiv_rn(1.0f, l0), inv1 = __fdiv_rn(1.0f, l1);
+      uint16_t* out0 = p.out + (static_cast<int64_t>(row0) * p.Hq + head) * D;
+      uint16_t* out1 = out0 + static_cast<int64_t>(8) * p.Hq * D;
 #pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
+      for (int half = 0; half < D / 64; ++half) {
         float o[32];
-        const int d0 = half * (D / 2) + 32 * c;
-        pr_ld32(tb + (static_cast<uint32_t>(32 * quarter) << 16) + 256 + t * 128 + d0, o);
+        pr_ld16x64(to + 64 * half, o);
         pr_ld_wait(o);
-        if (odd && live) {  // the values that were put to 0 and this row attends to
-          for (int key = x.begin + (x.blocks_a - 1) * kPrTile; key <= row; ++key) {
-            const uint16_t* v = p.v + key * p.v_stride + (head / p.G) * D + d0;
+        if (odd) {  // the values that were put to 0 and a row attends to
+          for (int key = x.begin + (x.blocks_a - 1) * kPrTile; key <= min(row1, x.end - 1); ++key) {
+            const uint16_t* v = p.v + key * p.v_stride + (head / p.G) * D + 64 * half + 2 * c;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float a = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
-              if (!(fabsf(a) < INFINITY)) o[i] += a;
+              const float a = __uint_as_float(static_cast<uint32_t>(v[8 * (i >> 2) + (i & 1)]) << 16);
+              if (!(fabsf(a) < INFINITY) && key <= ((i & 2) ? row1 : row0)) o[i] += a;
             }
           }
         }
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row) * p.Hq + head) * D + d0);
+        // 8 elements to a lane: the quad's lanes hold two of each of four octets
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(pr_pack(o[8 * i] * inv, o[8 * i + 1] * inv), pr_pack(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                pr_pack(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pr_pack(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w0[4], w1[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* y = o + 4 * (4 * q + i);
+            w0[i] = pr_pack(y[0] * inv0, y[1] * inv0);
+            w1[i] = pr_pack(y[2] * inv1, y[3] * inv1);
+          }
+          pr_transpose4(w0, c);
+          pr_transpose4(w1, c);
+          const int d0 = 64 * half + 32 * q + 8 * c;
+          if (row0 < x.end) *reinterpret_cast<uint4*>(out0 + d0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+          if (row1 < x.end) *reinterpret_cast<uint4*>(out1 + d0) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
         }
       }
-      if (p.lse != nullptr && live && half == 0)
-        p.lse[static_cast<int64_t>(row) * p.Hq + head] =
-            l > 0.0f ? 0.69314718055994531f * fmaf(m, p.scale_log2, log2f(l)) : l == 0.0f ? -INFINITY : l;
-      tc::fence_before_sync();
-      // O is read by both warps before either announces the next unit's weights (and the rows' numbers before they change)
-      asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(pair) : "memory");
+      if (p.lse != nullptr && c == 0) {
+        auto store = [&](int row, float m, float l) {
+          if (row < x.end)
+            p.lse[static_cast<int64_t>(row) * p.Hq + head] =
+                l > 0.0f ? 0.69314718055994531f * fmaf(m, p.scale_log2, log2f(l)) : l == 0.0f ? -INFINITY : l;
+        };
+        store(row0, m0, l0);
+        store(row1, m1, l1);
+      }
+      tc::fence_before_sync();  // O is read before the next unit's weights are announced
     }
   }
   tc::fence_before_sync();
