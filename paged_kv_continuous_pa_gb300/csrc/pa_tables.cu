@@ -22,6 +22,7 @@ constexpr int kTablesMaxSlots = 1 << 19;  // two bits to a slot in shared memory
 constexpr int kTablesOneCtaRows = 4096;
 constexpr int kTablesRowThreads = 256;
 constexpr int kTablesRowsPerThread = 4;
+constexpr int kTablesStaged = 4096;  // requests whose row starts a CTA copies
 enum { ST_NO_PAGES = 6 };
 
 struct TablesParams {
@@ -39,6 +40,7 @@ struct TablesParams {
   int64_t* row_slots;
   int32_t* status;
   int32_t n, num_pages, lg_p, num_seqs, max_blocks, max_rows;
+  int32_t rows_aligned;  // the rows' arrays start on 16 bytes
 };
 
 struct ScanSmem {
@@ -127,24 +129,45 @@ __device__ __forceinline__ void write_pages(const TablesParams& p, int before, i
   }
 }
 
-// Rows r0 .. r0 + count - 1.
-__device__ __forceinline__ void write_rows(const TablesParams& p, int before, int total, int r0, int count) {
+// Rows r0 .. r0 + count - 1; starts and their requests may be a copy of p.row_starts in shared memory.
+__device__ __forceinline__ void write_rows(const TablesParams& p, const int32_t* starts, int before, int total, int r0, int count) {
   if (r0 >= total) return;
-  int i = find_start(p.row_starts, p.n, r0);
-  for (int r = r0; r < min(r0 + count, total); ++r) {
-    while (p.row_starts[i + 1] <= r) ++i;
+  int i = find_start(starts, p.n, r0);
+  const int mask = (1 << p.lg_p) - 1;
+  for (int r = r0, end = min(r0 + count, total); r < end;) {
+    while (starts[i + 1] <= r) ++i;
     const int seq = p.seq_ids[i], length = p.lengths[i];
-    const int pos = length + r - p.row_starts[i];
-    p.row_seqs[r] = seq;
-    p.row_positions[r] = pos;
-    if (p.row_slots == nullptr) continue;
-    const int column = pos >> p.lg_p, held = (length + (1 << p.lg_p) - 1) >> p.lg_p;
-    // a new page by its place on the stack: the table's entry may not be written yet
-    const int page = column < held ? p.block_tables[static_cast<int64_t>(seq) * p.max_blocks + column]
-                                   : p.free_pages[before - 1 - (p.page_starts[i] + column - held)];
-    const bool good = page >= 0 && page < p.num_pages;
-    if (!good) record_error(p.status, ST_OUT_OF_RANGE);
-    p.row_slots[r] = good ? (static_cast<int64_t>(page) << p.lg_p) + (pos & ((1 << p.lg_p) - 1)) : -1;
+    const int pos = length + r - starts[i];
+    // rows of one request in one page: one lookup for all of them
+    const int run = min(min(end, starts[i + 1]) - r, mask + 1 - (pos & mask));
+    int64_t slot = -1;
+    if (p.row_slots != nullptr) {
+      const int column = pos >> p.lg_p, held = (length + mask) >> p.lg_p;
+      // a new page by its place on the stack: the table's entry may not be written yet
+      const int page = column < held ? p.block_tables[static_cast<int64_t>(seq) * p.max_blocks + column]
+                                     : p.free_pages[before - 1 - (p.page_starts[i] + column - held)];
+      if (page >= 0 && page < p.num_pages)
+        slot = (static_cast<int64_t>(page) << p.lg_p) + (pos & mask);
+      else
+        record_error(p.status, ST_OUT_OF_RANGE);
+    }
+    if (run == 4 && (r & 3) == 0 && p.rows_aligned) {
+      *reinterpret_cast<int4*>(p.row_seqs + r) = make_int4(seq, seq, seq, seq);
+      *reinterpret_cast<int4*>(p.row_positions + r) = make_int4(pos, pos + 1, pos + 2, pos + 3);
+      if (p.row_slots != nullptr) {
+        const int64_t one = slot < 0 ? 0 : 1;
+        longlong2* s = reinterpret_cast<longlong2*>(p.row_slots + r);
+        s[0] = make_longlong2(slot, slot + one);
+        s[1] = make_longlong2(slot + 2 * one, slot + 3 * one);
+      }
+    } else {
+      for (int k = 0; k < run; ++k) {
+        p.row_seqs[r + k] = seq;
+        p.row_positions[r + k] = pos + k;
+        if (p.row_slots != nullptr) p.row_slots[r + k] = slot < 0 ? -1 : slot + k;
+      }
+    }
+    r += run;
   }
 }
 
@@ -205,19 +228,26 @@ __global__ void __launch_bounds__(kTablesThreads) tables_grow_kernel(const __gri
   if constexpr (ROWS) {
     __syncthreads();
     write_pages(p, count, total_pages, tid, kTablesThreads);
-    for (int r = tid; r < total_rows; r += kTablesThreads) write_rows(p, count, total_rows, r, 1);
+    for (int r = tid; r < total_rows; r += kTablesThreads) write_rows(p, p.row_starts, count, total_rows, r, 1);
   }
 }
 
 __global__ void __launch_bounds__(kTablesRowThreads) tables_rows_kernel(const __grid_constant__ TablesParams p) {
+  __shared__ int32_t staged[kTablesStaged + 1];
   griddep_wait();  // the sums are another launch's
   const int total_pages = p.page_starts[p.n], total_rows = p.row_starts[p.n];
   const int before = p.free_left[0] + total_pages;
   const int thread = blockIdx.x * kTablesRowThreads + threadIdx.x, threads = gridDim.x * kTablesRowThreads;
-  write_pages(p, before, total_pages, thread, threads);
+  const int32_t* starts = p.row_starts;
+  if (p.n <= kTablesStaged) {  // a search of dependent loads is short in shared memory
+    for (int i = threadIdx.x; i <= p.n; i += kTablesRowThreads) staged[i] = p.row_starts[i];
+    __syncthreads();
+    starts = staged;
+  }
   for (int64_t r = static_cast<int64_t>(thread) * kTablesRowsPerThread; r < total_rows;
        r += static_cast<int64_t>(threads) * kTablesRowsPerThread)
-    write_rows(p, before, total_rows, static_cast<int>(r), kTablesRowsPerThread);
+    write_rows(p, starts, before, total_rows, static_cast<int>(r), kTablesRowsPerThread);
+  write_pages(p, before, total_pages, thread, threads);
 }
 
 // One CTA: which requests are sound (a warp each looks over its pages), their place
@@ -343,6 +373,7 @@ pa_status pa_tables_grow(int32_t n, const int32_t* seq_ids, const int32_t* lengt
   p.num_seqs = num_seqs;
   p.max_blocks = max_blocks_per_seq;
   p.max_rows = max_rows;
+  p.rows_aligned = pa::aligned(row_seqs, 16) && pa::aligned(row_positions, 16) && pa::aligned(row_slots, 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool one = max_rows <= pa::kTablesOneCtaRows;
   static std::atomic<unsigned long long> done_one{0}, done_two{0};
