@@ -10,11 +10,13 @@
 // sines and cosines are the same for all of its heads, so a CTA computes them once
 // for its rows into shared memory.
 //
-// What bounds it is memory: every element is read and written once.  D / 8 lanes share
-// one head of one row, 8 consecutive elements (one or two 16-byte accesses) to a lane; the
-// partner octet of the half layout sits in another lane of the same group and comes by
-// shuffle.  So a head is in one place when it is rotated, which a 4-bit pool needs: its
-// range is a reduction over the group.
+// What bounds it is memory: every element is read and written once; and close behind it
+// the instructions, so that what can be is worked out once for several rows.  A warp takes
+// one head of a few neighbouring rows at a time: its kind (query, key, value) is the whole
+// warp's.  D / 8 lanes share one row, 8 consecutive elements (one or two 16-byte accesses) to
+// a lane; the partner octet of the half layout sits in another lane of the same group and comes
+// by shuffle.  So a row of a head is in one place when it is rotated, which a 4-bit pool
+// needs: its range is a reduction over the group.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -25,7 +27,7 @@
 namespace pa {
 
 constexpr int kRowsThreads = 256;
-constexpr int kRowsPerCta = 8;  // at most
+constexpr int kRowsPerCta = 16;  // at most
 
 // 8 consecutive elements of one head, as loaded (plain loads: queries may be rotated in place)
 template <bool BF16>
@@ -132,46 +134,34 @@ struct RowsSmem {
   float x[kRowsThreads * 8];     // heads whose partners do not sit in one lane
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constant__ RowsParams p, int rows_per_cta) {
-  constexpr int L = D / 8, kGroups = kRowsThreads / L, kBatch = 2;
+// Rows of a CTA: STEPS to each group of lanes; heads blockIdx.y, + gridDim.y, .. in turns of its warps.
+template <int D, bool BF16, int STEPS>
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int L = D / 8, G = 32 / L, kRows = G * STEPS, kWarps = kRowsThreads / 32;
+  static_assert(kRows <= kRowsPerCta, "rows of a CTA");
   __shared__ __align__(16) RowsSmem sm;
   griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, l = tid % L, group = tid / L;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_per_cta;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(rows_per_cta), p.n_rows - row0));
-  const int H = p.Hq + 2 * p.Hkv, units = rows * H;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane % L, g = lane / L;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), p.n_rows - row0));
+  const int H = p.Hq + 2 * p.Hkv, step = kWarps * gridDim.y;
+  int h = blockIdx.y * kWarps + warp;
 
-  // A group takes every kGroups-th head of the CTA's rows.
-  struct Place {
-    int r, h;
-    __device__ __forceinline__ void settle(int heads) {
-      while (h >= heads) {
-        h -= heads;
-        ++r;
-      }
-    }
-    __device__ __forceinline__ void next(int heads) {
-      h += kGroups;
-      settle(heads);
-    }
-  };
-  Place ahead{0, group}, at{0, group};
-  ahead.settle(H);
-  at.settle(H);
-  // the first heads of each group are on their way while the angles are computed
-  auto load = [&]() -> Octet<BF16> {
-    const int r = ahead.r, h = ahead.h;
-    ahead.next(H);
-    if (r >= rows) return Octet<BF16>{};
-    const int64_t row = row0 + r;
-    if (h < p.Hq) return load_octet<BF16>(p.q, row * p.q_stride + h * D + 8 * l);
-    if (h < p.Hq + p.Hkv) return load_octet<BF16>(p.k, row * p.k_stride + (h - p.Hq) * D + 8 * l);
-    return load_octet<BF16>(p.v, row * p.v_stride + (h - p.Hq - p.Hkv) * D + 8 * l);
-  };
-  Octet<BF16> raw[kBatch];
+  // the first head is on its way while the angles are computed
+  auto load = [&](int head, Octet<BF16> (&raw)[STEPS]) {
+    if (head >= H) return;
+    const bool is_q = head < p.Hq, is_k = head < p.Hq + p.Hkv;
+    const void* base = is_q ? p.q : is_k ? p.k : p.v;
+    const int64_t stride = is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride;
+    int64_t at = (row0 + g) * stride + (head - (is_q ? 0 : is_k ? p.Hq : p.Hq + p.Hkv)) * D + 8 * l;
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) raw[b] = load();
+    for (int s = 0; s < STEPS; ++s) {
+      if (s * G + g < rows) raw[s] = load_octet<BF16>(base, at);
+      at += G * stride;
+    }
+  };
+  Octet<BF16> raw[STEPS] = {};
+  load(h, raw);
 
   if (p.Hkv > 0 && tid < rows) {
     const int seq = __ldg(p.seq_ids + row0 + tid), pos = __ldg(p.positions + row0 + tid);
@@ -187,7 +177,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constan
   }
   const int pairs = p.rot / 2;
   for (int i = tid; i < rows * pairs; i += kRowsThreads) {
-    const int r = i / pairs, j = i % pairs;
+    const int r = i / pairs, j = i - r * pairs;
     const int64_t pos = __ldg(p.positions + row0 + r);
     const uint64_t phase = p.turns[j] * static_cast<uint64_t>(pos) + (1ull << 31);
     float s, c;
@@ -199,60 +189,59 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constan
   const bool half_octets = !p.interleaved && pairs % 8 == 0;
   const int o8 = pairs / 8;
   const int partner = lane - l + (l < o8 ? l + o8 : l < 2 * o8 ? l - o8 : l);
-  for (int u0 = 0; u0 < units; u0 += kBatch * kGroups) {  // the same rounds for every lane of a warp
-    Octet<BF16> next[kBatch];
+  for (; h < H; h += step) {  // the same head for every lane of a warp
+    Octet<BF16> next[STEPS] = {};
+    load(h + step, next);
+    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv, turned = !is_v && p.rot > 0;
+    const int kvh = h - p.Hq - (is_v ? p.Hkv : 0);
+    void* pool = is_v ? p.v_pool : p.k_pool;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) next[b] = load();
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (u0 + b * kGroups >= units) break;
-      const bool live = at.r < rows;
-      const int r = live ? at.r : 0, h = live ? at.h : 0;
-      at.next(H);
-      const bool turned = h < p.Hq + p.Hkv && p.rot > 0;
+    for (int s = 0; s < STEPS; ++s) {
+      const int r = s * G + g;
+      const bool live = r < rows;
       float x[8];
-      widen<BF16>(raw[b], x);
-      if (p.interleaved) {
-        if (turned) {
+      widen<BF16>(raw[s], x);
+      if (turned && p.interleaved) {
+        const float2* t = &sm.turn[r][4 * l];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (8 * l + 2 * i >= p.rot) break;
-            const float2 t = sm.turn[r][4 * l + i];
-            const float a = x[2 * i], c = x[2 * i + 1];
-            x[2 * i] = a * t.x - c * t.y;
-            x[2 * i + 1] = c * t.x + a * t.y;
-          }
+        for (int i = 0; i < 4; ++i) {
+          if (8 * l + 2 * i >= p.rot) break;
+          const float a = x[2 * i], c = x[2 * i + 1];
+          x[2 * i] = a * t[i].x - c * t[i].y;
+          x[2 * i + 1] = c * t[i].x + a * t[i].y;
         }
-      } else if (half_octets) {
+      } else if (turned && half_octets) {
         Octet<BF16> other;
 #pragma unroll
-        for (int i = 0; i < (BF16 ? 4 : 8); ++i) other.w[i] = __shfl_sync(0xffffffffu, raw[b].w[i], partner);
-        if (turned && l < 2 * o8) {
+        for (int i = 0; i < (BF16 ? 4 : 8); ++i) other.w[i] = __shfl_sync(0xffffffffu, raw[s].w[i], partner);
+        if (l < 2 * o8) {
           float y[8];
           widen<BF16>(other, y);
-          const float2* t = &sm.turn[r][l < o8 ? 8 * l : 8 * (l - o8)];
+          const float4* t = reinterpret_cast<const float4*>(&sm.turn[r][l < o8 ? 8 * l : 8 * (l - o8)]);
           const float way = l < o8 ? -1.0f : 1.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * t[i].x + way * (y[i] * t[i].y);
+          for (int i = 0; i < 4; ++i) {
+            const float4 two = t[i];  // (cos, sin) of two pairs
+            x[2 * i] = x[2 * i] * two.x + (way * y[2 * i]) * two.y;
+            x[2 * i + 1] = x[2 * i + 1] * two.z + (way * y[2 * i + 1]) * two.w;
+          }
         }
-      } else {  // partners across octets: the head through shared memory
+      } else if (turned) {  // partners across octets: the head through shared memory
         float* head = sm.x + (tid - l) * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) head[8 * l + i] = x[i];
         __syncwarp();
-        if (turned) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int e = 8 * l + i;
-            if (e >= p.rot) break;
-            const float2 t = sm.turn[r][e < pairs ? e : e - pairs];
-            x[i] = e < pairs ? x[i] * t.x - head[e + pairs] * t.y : x[i] * t.x + head[e - pairs] * t.y;
-          }
+        for (int i = 0; i < 8; ++i) {
+          const int e = 8 * l + i;
+          if (e >= p.rot) break;
+          const float2 t = sm.turn[r][e < pairs ? e : e - pairs];
+          x[i] = e < pairs ? x[i] * t.x - head[e + pairs] * t.y : x[i] * t.x + head[e - pairs] * t.y;
         }
         __syncwarp();
       }
       const int page = p.Hkv > 0 ? sm.page[r] : 0;
-      if (h < p.Hq) {
+      if (is_q) {
         if (live && page >= 0) {
           const int64_t at = (row0 + r) * p.out_stride + h * D + 8 * l;
           if constexpr (BF16)
@@ -260,12 +249,10 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constan
           else
             store_f32(p.q_out, at, x);
         }
-        if (p.kv_dtype != KV_INT4 || p.Hkv == 0) continue;
+        continue;
       }
-      const bool stored = live && page >= 0 && h >= p.Hq, is_v = h >= p.Hq + p.Hkv;
-      const int kvh = h - p.Hq - (is_v ? p.Hkv : 0);
+      const bool stored = live && page >= 0;
       const int64_t token = stored ? (static_cast<int64_t>(page) * p.Hkv + kvh) * p.P + sm.slot[r] : -1;
-      void* pool = is_v ? p.v_pool : p.k_pool;
       if (p.kv_dtype == KV_INT4) {  // a reduction over the group: the warp's every lane takes part
         store_int4<L>(pool, is_v ? p.v_ranges : p.k_ranges, token, l, x);
       } else if (stored) {
@@ -273,9 +260,9 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constan
         if (p.kv_dtype == KV_F32) {
           store_f32(pool, at, x);
         } else if (p.kv_dtype == KV_BF16) {
-          if (BF16 && (is_v || p.rot == 0))  // a copy, whatever the bits
+          if (BF16 && !turned)  // a copy, whatever the bits
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at) =
-                make_uint4(raw[b].w[0], raw[b].w[1], raw[b].w[2], raw[b].w[3]);
+                make_uint4(raw[s].w[0], raw[s].w[1], raw[s].w[2], raw[s].w[3]);
           else
             store_bf16(pool, at, x);
         } else {
@@ -288,52 +275,46 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constan
       }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) raw[b] = next[b];
+    for (int s = 0; s < STEPS; ++s) raw[s] = next[s];
   }
 }
 
-// A CTA per few rows, a thread per 8 elements of K or V.
-constexpr int kReadRows = 4;
-
+// A warp per row and a share of its octets (8 elements of K or V each) to a lane, gridDim.y shares of a row.
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
-  __shared__ int32_t pages[kReadRows], slots[kReadRows];
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kReadRows), p.n_rows - row0));
-  if (threadIdx.x < rows) {
-    const int seq = __ldg(p.seq_ids + row0 + threadIdx.x), pos = __ldg(p.positions + row0 + threadIdx.x);
-    int page = -1;
-    if (seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < static_cast<int64_t>(p.max_blocks) * p.P)
-      page = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + pos / p.P);
-    if (page < 0 || page >= p.num_pages) {
-      page = -1;
-      record_error(p.status, ST_OUT_OF_RANGE);
-    }
-    pages[threadIdx.x] = page;
-    slots[threadIdx.x] = pos & (p.P - 1);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= p.n_rows) return;
+  const int seq = __ldg(p.seq_ids + row), pos = __ldg(p.positions + row);
+  int page = -1;
+  if (seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < static_cast<int64_t>(p.max_blocks) * p.P)
+    page = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + pos / p.P);
+  if (page < 0 || page >= p.num_pages) {
+    page = -1;
+    if (lane == 0 && blockIdx.y == 0) record_error(p.status, ST_OUT_OF_RANGE);
   }
-  __syncthreads();
   const int lg_octets = p.D == 128 ? 4 : 3, octets = p.Hkv << lg_octets;  // of a row's K or V
-  const int sides = (p.k_out != nullptr) + (p.v_out != nullptr);
-  for (int r = 0; r < rows; ++r) {
-    const int page = pages[r], slot = slots[r];
-    for (int u = threadIdx.x; u < sides * octets; u += 256) {
-      const bool second = u >= octets, is_v = p.k_out == nullptr || second;
-      const int o = second ? u - octets : u, h = o >> lg_octets;
+  const int64_t token0 = static_cast<int64_t>(page) * p.Hkv * p.P + (pos & (p.P - 1));
+  for (int side = p.k_out == nullptr ? 1 : 0; side < (p.v_out == nullptr ? 1 : 2); ++side) {
+    const void* pool = side ? p.v_pool : p.k_pool;
+    const uint32_t* ranges = static_cast<const uint32_t*>(side ? p.v_ranges : p.k_ranges);
+    void* out = side ? p.v_out : p.k_out;
+#pragma unroll 4
+    for (int o = blockIdx.y * 32 + lane; o < octets; o += 32 * gridDim.y) {
+      const int h = o >> lg_octets;
       float x[8] = {};
       if (page >= 0) {
-        const int64_t token = (static_cast<int64_t>(page) * p.Hkv + h) * p.P + slot;
+        const int64_t token = token0 + h * p.P;
         const int64_t at = (token << lg_octets) + (o & ((1 << lg_octets) - 1));  // in octets
-        const void* pool = is_v ? p.v_pool : p.k_pool;
         if (p.kv_dtype == KV_INT4) {
           const uint32_t w = __ldg(static_cast<const uint32_t*>(pool) + at);
-          const uint32_t range = __ldg(static_cast<const uint32_t*>(is_v ? p.v_ranges : p.k_ranges) + token);
+          const uint32_t range = __ldg(ranges + token);
           const float step = __half2float(__ushort_as_half(static_cast<unsigned short>(range & 0xffffu)));
           const float low = __half2float(__ushort_as_half(static_cast<unsigned short>(range >> 16)));
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = fmaf(static_cast<float>((w >> (4 * i)) & 15u), step, low);
         } else if (p.kv_dtype == KV_E4M3) {
           const uint2 w = __ldg(static_cast<const uint2*>(pool) + at);
-          const float scale = is_v ? p.v_scale_h[PA_HEAD(p, h)] : p.k_scale_h[PA_HEAD(p, h)];
+          const float scale = side ? p.v_scale_h[PA_HEAD(p, h)] : p.k_scale_h[PA_HEAD(p, h)];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 two = e4m3x2_to_float2((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
@@ -346,8 +327,7 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
           widen<false>(load_octet<false>(pool, at * 8), x);
         }
       }
-      void* out = is_v ? p.v_out : p.k_out;
-      const int64_t to = ((row0 + r) * octets + o) * 8;
+      const int64_t to = (row * octets + o) * 8;
       if (p.out_bf16)
         store_bf16(out, to, x);
       else
@@ -356,20 +336,37 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
   }
 }
 
-cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream) {
-  if (p.n_rows <= 0) return cudaSuccess;
-  const int per = p.n_rows <= 1024 ? 1 : p.n_rows <= 4096 ? 4 : kRowsPerCta;
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.n_rows) + per - 1) / per);
-  auto kernel = p.D == 128 ? (p.in_dtype == KV_BF16 ? rows_kernel<128, true> : rows_kernel<128, false>)
-                           : (p.in_dtype == KV_BF16 ? rows_kernel<64, true> : rows_kernel<64, false>);
-  kernel<<<grid, kRowsThreads, 0, stream>>>(p, per);
+template <int D, bool BF16, int STEPS>
+cudaError_t launch_rows_inst(const RowsParams& p, cudaStream_t stream) {
+  constexpr int kRows = 256 / D * STEPS;
+  const int64_t grid = (static_cast<int64_t>(p.n_rows) + kRows - 1) / kRows;
+  // few rows: their heads are shared out to as many CTAs as the GPU holds at once (each computes the angles)
+  const int turns = (p.Hq + 2 * p.Hkv + 7) / 8;
+  const int64_t share = std::max<int64_t>(1, std::min<int64_t>(turns, 152 * 2 / grid));
+  rows_kernel<D, BF16, STEPS><<<dim3(static_cast<unsigned>(grid), static_cast<unsigned>(share)), kRowsThreads, 0, stream>>>(p);
   count_launch();
   return cudaGetLastError();
 }
 
+template <int D, bool BF16>
+cudaError_t launch_rows_steps(const RowsParams& p, cudaStream_t stream) {
+  // one step to a lane as long as that makes no more CTAs than the GPU holds at once
+  return p.n_rows <= 152 * 2 * (256 / D) ? launch_rows_inst<D, BF16, 1>(p, stream)
+                                         : launch_rows_inst<D, BF16, BF16 ? 4 : 2>(p, stream);
+}
+
+cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream) {
+  if (p.n_rows <= 0) return cudaSuccess;
+  const bool bf16 = p.in_dtype == KV_BF16;
+  if (p.D == 128) return bf16 ? launch_rows_steps<128, true>(p, stream) : launch_rows_steps<128, false>(p, stream);
+  return bf16 ? launch_rows_steps<64, true>(p, stream) : launch_rows_steps<64, false>(p, stream);
+}
+
 cudaError_t launch_read(const ReadParams& p, cudaStream_t stream) {
-  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.n_rows) + kReadRows - 1) / kReadRows);
-  read_kernel<<<blocks, 256, 0, stream>>>(p);
+  const int64_t blocks = (static_cast<int64_t>(p.n_rows) + 7) / 8;
+  const int64_t turns = (static_cast<int64_t>(p.Hkv) * p.D / 8 + 31) / 32;
+  const int64_t share = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(turns, 64), 152 * 4 / blocks));
+  read_kernel<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(share)), 256, 0, stream>>>(p);
   count_launch();
   return cudaGetLastError();
 }
