@@ -27,7 +27,8 @@
 namespace pa {
 
 constexpr int kRowsThreads = 256;
-constexpr int kRowsPerCta = 16;  // at most
+constexpr int kRowsPerCta = 16;  // at a time, at most
+constexpr int kRowsCtas = 3;     // to an SM
 
 // 8 consecutive elements of one head, as loaded (plain loads: queries may be rotated in place)
 template <bool BF16>
@@ -83,22 +84,33 @@ __device__ __forceinline__ void store_bf16(void* base, int64_t element, const fl
 // (with the integer divisions below gone as well, 75 -> 24 us for 16384 rows of 8 heads).
 template <int L>
 __device__ __forceinline__ void store_int4(void* codes, void* ranges, int64_t token, int l, float (&x)[8]) {
-  bool nan = false;
-  float lo = INFINITY, hi = -INFINITY;
+  float lo = x[0], hi = x[0], odd = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    nan |= x[i] != x[i];
-    x[i] = fminf(fmaxf(x[i], -65504.0f), 65504.0f);  // the range is held in f16
     lo = fminf(lo, x[i]);
     hi = fmaxf(hi, x[i]);
+    odd = fmaf(x[i], 0.0f, odd);  // NaN from an infinity or NaN on
   }
+  // maximum over the group of hi in its odd lanes, of -lo in the even ones
+  const bool upper = (l & 1) != 0;
+  float v = fmaxf(upper ? hi : -lo, __shfl_xor_sync(0xffffffffu, upper ? -lo : hi, 1));
 #pragma unroll
-  for (int d = L / 2; d > 0; d /= 2) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-  }
+  for (int d = 2; d < L; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  const float w = __shfl_xor_sync(0xffffffffu, v, 1);
+  lo = upper ? -w : -v;
+  hi = upper ? v : w;
   const uint32_t group = ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
-  nan = (__ballot_sync(0xffffffffu, nan) & group) != 0u;
+  bool nan = false;
+  if ((__ballot_sync(0xffffffffu, odd != odd || hi > 65504.0f || lo < -65504.0f) & group) != 0u) {  // the range is held in f16
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      nan |= x[i] != x[i];
+      x[i] = fminf(fmaxf(x[i], -65504.0f), 65504.0f);
+    }
+    nan = (__ballot_sync(group, nan) & group) != 0u;
+    lo = fminf(fmaxf(lo, -65504.0f), 65504.0f);
+    hi = fminf(fmaxf(hi, -65504.0f), 65504.0f);
+  }
   __half low = __float2half_rn(lo);
   const float lf = __half2float(low);
   __half step = __float2half_rn(fmaxf(__fdiv_rn(__fsub_rn(hi, lf), 15.0f), 0.0f));
@@ -106,17 +118,26 @@ __device__ __forceinline__ void store_int4(void* codes, void* ranges, int64_t to
   uint32_t word = 0;
   if (sf > 0.0f && !nan) {
     const float y = __frcp_rn(sf);
+    float c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = __fsub_rn(x[i], lf);
       const float q = __fmul_rn(d, y);
-      const float c = fminf(fmaxf(fmaf(fmaf(-q, sf, d), y, q), 0.0f), 15.0f);
-      // c + 1.5 2^23 rounds to the integer (ties to even) in the lowest bits; the rest goes below
-      word += __float_as_uint(__fadd_rn(c, 12582912.0f)) << (4 * i);
+      c[i] = fmaf(fmaf(-q, sf, d), y, q);
     }
+    // A step that is a normal f16 number is off by 2^-11 of it, and low by 2^-11 of low: quotients stay within -1/4
+    // and 15 + 1/4 unless low is large beside the step.
+    if (!(sf >= 0x1p-14f && fabsf(lf) <= 512.0f * sf)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(c[i], 0.0f), 15.0f);
+    }
+    // c + 1.5 2^23 rounds to the integer (ties to even) in the lowest bits; the rest goes below
     uint32_t rest = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rest += 0x4b400000u << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+      word += __float_as_uint(__fadd_rn(c[i], 12582912.0f)) << (4 * i);
+      rest += 0x4b400000u << (4 * i);
+    }
     word -= rest;
   }
   if (nan) low = step = __ushort_as_half(0x7fff);
@@ -127,160 +148,174 @@ __device__ __forceinline__ void store_int4(void* codes, void* ranges, int64_t to
                                             static_cast<uint32_t>(__half_as_ushort(low)) << 16;
 }
 
-struct RowsSmem {
-  float2 turn[kRowsPerCta][64];  // (cos, sin) of the row's pairs
-  int32_t page[kRowsPerCta];     // of the row's token (-1: a row that is skipped)
-  int32_t slot[kRowsPerCta];
-  float x[kRowsThreads * 8];     // heads whose partners do not sit in one lane
+struct RowsSmem {  // of the rows at hand and of the next ones
+  float2 turn[2][kRowsPerCta][64];  // (cos, sin) of the row's pairs
+  int32_t page[2][kRowsPerCta];     // of the row's token (-1: a row that is skipped)
+  int32_t slot[2][kRowsPerCta];
+  float x[kRowsThreads * 8];        // heads whose partners do not sit in one lane
 };
 
-// Rows of a CTA: STEPS to each group of lanes; heads blockIdx.y, + gridDim.y, .. in turns of its warps.
+// A CTA goes through sets of rows, STEPS to each group of lanes (every gridDim.x-th set), and of their heads takes
+// blockIdx.y, + gridDim.y, .. in turns of its warps.  The next set's angles and pages are looked up at the end of a set.
 template <int D, bool BF16, int STEPS>
-__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kRowsThreads, kRowsCtas) rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int L = D / 8, G = 32 / L, kRows = G * STEPS, kWarps = kRowsThreads / 32;
   static_assert(kRows <= kRowsPerCta, "rows of a CTA");
   __shared__ __align__(16) RowsSmem sm;
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane % L, g = lane / L;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), p.n_rows - row0));
-  const int H = p.Hq + 2 * p.Hkv, step = kWarps * gridDim.y;
-  int h = blockIdx.y * kWarps + warp;
+  const int64_t sets = (static_cast<int64_t>(p.n_rows) + kRows - 1) / kRows;
+  const int H = p.Hq + 2 * p.Hkv, step = kWarps * gridDim.y, first = blockIdx.y * kWarps + warp;
 
-  // the first head is on its way while the angles are computed
-  auto load = [&](int head, Octet<BF16> (&raw)[STEPS]) {
-    if (head >= H) return;
+  auto load = [&](int64_t set, int head, Octet<BF16> (&raw)[STEPS]) {
+    if (head >= H || set >= sets) return;
+    const int64_t row = set * kRows + g;
     const bool is_q = head < p.Hq, is_k = head < p.Hq + p.Hkv;
     const void* base = is_q ? p.q : is_k ? p.k : p.v;
     const int64_t stride = is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride;
-    int64_t at = (row0 + g) * stride + (head - (is_q ? 0 : is_k ? p.Hq : p.Hq + p.Hkv)) * D + 8 * l;
+    int64_t at = row * stride + (head - (is_q ? 0 : is_k ? p.Hq : p.Hq + p.Hkv)) * D + 8 * l;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      if (s * G + g < rows) raw[s] = load_octet<BF16>(base, at);
+      if (row + s * G < p.n_rows) raw[s] = load_octet<BF16>(base, at);
       at += G * stride;
     }
   };
-  Octet<BF16> raw[STEPS] = {};
-  load(h, raw);
-
-  if (p.Hkv > 0 && tid < rows) {
-    const int seq = __ldg(p.seq_ids + row0 + tid), pos = __ldg(p.positions + row0 + tid);
-    int page = -1;
-    if (seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < static_cast<int64_t>(p.max_blocks) * p.P)
-      page = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + pos / p.P);
-    if (page < 0 || page >= p.num_pages) {
-      page = -1;
-      record_error(p.status, ST_OUT_OF_RANGE);
-    }
-    sm.page[tid] = page;
-    sm.slot[tid] = pos & (p.P - 1);
-  }
   const int pairs = p.rot / 2;
-  for (int i = tid; i < rows * pairs; i += kRowsThreads) {
-    const int r = i / pairs, j = i - r * pairs;
-    const int64_t pos = __ldg(p.positions + row0 + r);
-    const uint64_t phase = p.turns[j] * static_cast<uint64_t>(pos) + (1ull << 31);
-    float s, c;
-    sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &s, &c);
-    sm.turn[r][j] = make_float2(c * p.magnitude, s * p.magnitude * p.sign);
-  }
+  auto look_up = [&](int64_t set, int buf) {
+    const int64_t row0 = set * kRows;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), p.n_rows - row0));
+    if (p.Hkv > 0 && tid < rows) {
+      const int seq = __ldg(p.seq_ids + row0 + tid), pos = __ldg(p.positions + row0 + tid);
+      int page = -1;
+      if (seq >= 0 && seq < p.num_seqs && pos >= 0 && pos < static_cast<int64_t>(p.max_blocks) * p.P)
+        page = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks + pos / p.P);
+      if (page < 0 || page >= p.num_pages) {
+        page = -1;
+        record_error(p.status, ST_OUT_OF_RANGE);
+      }
+      sm.page[buf][tid] = page;
+      sm.slot[buf][tid] = pos & (p.P - 1);
+    }
+    for (int i = tid; i < rows * pairs; i += kRowsThreads) {
+      const int r = i / pairs, j = i - r * pairs;
+      const int64_t pos = __ldg(p.positions + row0 + r);
+      const uint64_t phase = p.turns[j] * static_cast<uint64_t>(pos) + (1ull << 31);
+      float s, c;
+      sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &s, &c);
+      sm.turn[buf][r][j] = make_float2(c * p.magnitude, s * p.magnitude * p.sign);
+    }
+  };
+  // the first head is on its way while the angles are computed
+  Octet<BF16> raw[STEPS] = {};
+  load(blockIdx.x, first, raw);
+  look_up(blockIdx.x, 0);
   __syncthreads();
 
   const bool half_octets = !p.interleaved && pairs % 8 == 0;
   const int o8 = pairs / 8;
   const int partner = lane - l + (l < o8 ? l + o8 : l < 2 * o8 ? l - o8 : l);
-  for (; h < H; h += step) {  // the same head for every lane of a warp
-    Octet<BF16> next[STEPS] = {};
-    load(h + step, next);
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv, turned = !is_v && p.rot > 0;
-    const int kvh = h - p.Hq - (is_v ? p.Hkv : 0);
-    void* pool = is_v ? p.v_pool : p.k_pool;
+  int buf = 0;
+  for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, buf ^= 1) {
+    const int64_t row0 = set * kRows;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), p.n_rows - row0));
+    for (int h = first; h < H; h += step) {  // the same head for every lane of a warp
+      Octet<BF16> next[STEPS] = {};
+      const bool last = h + step >= H;
+      load(last ? set + gridDim.x : set, last ? first : h + step, next);
+      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv, turned = !is_v && p.rot > 0;
+      const int kvh = h - p.Hq - (is_v ? p.Hkv : 0);
+      void* pool = is_v ? p.v_pool : p.k_pool;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int r = s * G + g;
-      const bool live = r < rows;
-      float x[8];
-      widen<BF16>(raw[s], x);
-      if (turned && p.interleaved) {
-        const float2* t = &sm.turn[r][4 * l];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (8 * l + 2 * i >= p.rot) break;
-          const float a = x[2 * i], c = x[2 * i + 1];
-          x[2 * i] = a * t[i].x - c * t[i].y;
-          x[2 * i + 1] = c * t[i].x + a * t[i].y;
-        }
-      } else if (turned && half_octets) {
-        Octet<BF16> other;
-#pragma unroll
-        for (int i = 0; i < (BF16 ? 4 : 8); ++i) other.w[i] = __shfl_sync(0xffffffffu, raw[s].w[i], partner);
-        if (l < 2 * o8) {
-          float y[8];
-          widen<BF16>(other, y);
-          const float4* t = reinterpret_cast<const float4*>(&sm.turn[r][l < o8 ? 8 * l : 8 * (l - o8)]);
-          const float way = l < o8 ? -1.0f : 1.0f;
+      for (int s = 0; s < STEPS; ++s) {
+        const int r = s * G + g;
+        const bool live = r < rows;
+        float x[8];
+        widen<BF16>(raw[s], x);
+        if (turned && p.interleaved) {
+          const float2* t = &sm.turn[buf][r][4 * l];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 two = t[i];  // (cos, sin) of two pairs
-            x[2 * i] = x[2 * i] * two.x + (way * y[2 * i]) * two.y;
-            x[2 * i + 1] = x[2 * i + 1] * two.z + (way * y[2 * i + 1]) * two.w;
+            if (8 * l + 2 * i >= p.rot) break;
+            const float a = x[2 * i], c = x[2 * i + 1];
+            x[2 * i] = a * t[i].x - c * t[i].y;
+            x[2 * i + 1] = c * t[i].x + a * t[i].y;
+          }
+        } else if (turned && half_octets) {
+          Octet<BF16> other;
+#pragma unroll
+          for (int i = 0; i < (BF16 ? 4 : 8); ++i) other.w[i] = __shfl_sync(0xffffffffu, raw[s].w[i], partner);
+          if (l < 2 * o8) {
+            float y[8];
+            widen<BF16>(other, y);
+            const float4* t = reinterpret_cast<const float4*>(&sm.turn[buf][r][l < o8 ? 8 * l : 8 * (l - o8)]);
+            const float way = l < o8 ? -1.0f : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 two = t[i];  // (cos, sin) of two pairs
+              x[2 * i] = x[2 * i] * two.x + (way * y[2 * i]) * two.y;
+              x[2 * i + 1] = x[2 * i + 1] * two.z + (way * y[2 * i + 1]) * two.w;
+            }
+          }
+        } else if (turned) {  // partners across octets: the head through shared memory
+          float* head = sm.x + (tid - l) * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) head[8 * l + i] = x[i];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = 8 * l + i;
+            if (e >= p.rot) break;
+            const float2 t = sm.turn[buf][r][e < pairs ? e : e - pairs];
+            x[i] = e < pairs ? x[i] * t.x - head[e + pairs] * t.y : x[i] * t.x + head[e - pairs] * t.y;
+          }
+          __syncwarp();
+        }
+        const int page = p.Hkv > 0 ? sm.page[buf][r] : 0;
+        if (is_q) {
+          if (live && page >= 0) {
+            const int64_t at = (row0 + r) * p.out_stride + h * D + 8 * l;
+            if constexpr (BF16)
+              store_bf16(p.q_out, at, x);
+            else
+              store_f32(p.q_out, at, x);
+          }
+          continue;
+        }
+        const bool stored = live && page >= 0;
+        const int64_t token = stored ? (static_cast<int64_t>(page) * p.Hkv + kvh) * p.P + sm.slot[buf][r] : -1;
+        if (p.kv_dtype == KV_INT4) {  // a reduction over the group: the warp's every lane takes part
+          store_int4<L>(pool, is_v ? p.v_ranges : p.k_ranges, token, l, x);
+        } else if (stored) {
+          const int64_t at = token * D + 8 * l;
+          if (p.kv_dtype == KV_F32) {
+            store_f32(pool, at, x);
+          } else if (p.kv_dtype == KV_BF16) {
+            if (BF16 && !turned)  // a copy, whatever the bits
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at) =
+                  make_uint4(raw[s].w[0], raw[s].w[1], raw[s].w[2], raw[s].w[3]);
+            else
+              store_bf16(pool, at, x);
+          } else {
+            const float scale = is_v ? p.v_scale_h[PA_HEAD(p, kvh)] : p.k_scale_h[PA_HEAD(p, kvh)];
+            uint32_t o[2] = {0u, 0u};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i / 4] |= encode_e4m3(x[i], scale) << (8 * (i % 4));
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at) = make_uint2(o[0], o[1]);
           }
         }
-      } else if (turned) {  // partners across octets: the head through shared memory
-        float* head = sm.x + (tid - l) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) head[8 * l + i] = x[i];
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = 8 * l + i;
-          if (e >= p.rot) break;
-          const float2 t = sm.turn[r][e < pairs ? e : e - pairs];
-          x[i] = e < pairs ? x[i] * t.x - head[e + pairs] * t.y : x[i] * t.x + head[e - pairs] * t.y;
-        }
-        __syncwarp();
       }
-      const int page = p.Hkv > 0 ? sm.page[r] : 0;
-      if (is_q) {
-        if (live && page >= 0) {
-          const int64_t at = (row0 + r) * p.out_stride + h * D + 8 * l;
-          if constexpr (BF16)
-            store_bf16(p.q_out, at, x);
-          else
-            store_f32(p.q_out, at, x);
-        }
-        continue;
-      }
-      const bool stored = live && page >= 0;
-      const int64_t token = stored ? (static_cast<int64_t>(page) * p.Hkv + kvh) * p.P + sm.slot[r] : -1;
-      if (p.kv_dtype == KV_INT4) {  // a reduction over the group: the warp's every lane takes part
-        store_int4<L>(pool, is_v ? p.v_ranges : p.k_ranges, token, l, x);
-      } else if (stored) {
-        const int64_t at = token * D + 8 * l;
-        if (p.kv_dtype == KV_F32) {
-          store_f32(pool, at, x);
-        } else if (p.kv_dtype == KV_BF16) {
-          if (BF16 && !turned)  // a copy, whatever the bits
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at) =
-                make_uint4(raw[s].w[0], raw[s].w[1], raw[s].w[2], raw[s].w[3]);
-          else
-            store_bf16(pool, at, x);
-        } else {
-          const float scale = is_v ? p.v_scale_h[PA_HEAD(p, kvh)] : p.k_scale_h[PA_HEAD(p, kvh)];
-          uint32_t o[2] = {0u, 0u};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i / 4] |= encode_e4m3(x[i], scale) << (8 * (i % 4));
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at) = make_uint2(o[0], o[1]);
-        }
-      }
+      for (int s = 0; s < STEPS; ++s) raw[s] = next[s];
     }
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) raw[s] = next[s];
+    if (set + gridDim.x < sets) look_up(set + gridDim.x, buf ^ 1);
+    __syncthreads();
   }
 }
 
-// A warp per row and a share of its octets (8 elements of K or V each) to a lane, gridDim.y shares of a row.
+// A warp per row and 16 bytes of output at a time to a lane (E elements), gridDim.y shares of a row.
+template <bool BF16>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int E = BF16 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= p.n_rows) return;
@@ -292,46 +327,65 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
     page = -1;
     if (lane == 0 && blockIdx.y == 0) record_error(p.status, ST_OUT_OF_RANGE);
   }
-  const int lg_octets = p.D == 128 ? 4 : 3, octets = p.Hkv << lg_octets;  // of a row's K or V
+  const int lg_units = (p.D == 128 ? 7 : 6) - (BF16 ? 3 : 2), units = p.Hkv << lg_units;  // of a head; of a row's K or V
   const int64_t token0 = static_cast<int64_t>(page) * p.Hkv * p.P + (pos & (p.P - 1));
   for (int side = p.k_out == nullptr ? 1 : 0; side < (p.v_out == nullptr ? 1 : 2); ++side) {
     const void* pool = side ? p.v_pool : p.k_pool;
     const uint32_t* ranges = static_cast<const uint32_t*>(side ? p.v_ranges : p.k_ranges);
     void* out = side ? p.v_out : p.k_out;
 #pragma unroll 4
-    for (int o = blockIdx.y * 32 + lane; o < octets; o += 32 * gridDim.y) {
-      const int h = o >> lg_octets;
-      float x[8] = {};
+    for (int o = blockIdx.y * 32 + lane; o < units; o += 32 * gridDim.y) {
+      const int h = o >> lg_units;
+      float x[E] = {};
       if (page >= 0) {
-        const int64_t token = token0 + h * p.P;
-        const int64_t at = (token << lg_octets) + (o & ((1 << lg_octets) - 1));  // in octets
+        const int64_t token = token0 + static_cast<int64_t>(h) * p.P;
+        const int64_t at = (token << lg_units) + (o & ((1 << lg_units) - 1));  // in units
         if (p.kv_dtype == KV_INT4) {
-          const uint32_t w = __ldg(static_cast<const uint32_t*>(pool) + at);
+          const uint32_t w = BF16 ? __ldg(static_cast<const uint32_t*>(pool) + at) : __ldg(static_cast<const uint16_t*>(pool) + at);
           const uint32_t range = __ldg(ranges + token);
           const float step = __half2float(__ushort_as_half(static_cast<unsigned short>(range & 0xffffu)));
           const float low = __half2float(__ushort_as_half(static_cast<unsigned short>(range >> 16)));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = fmaf(static_cast<float>((w >> (4 * i)) & 15u), step, low);
+          for (int i = 0; i < E; ++i) x[i] = fmaf(static_cast<float>((w >> (4 * i)) & 15u), step, low);
         } else if (p.kv_dtype == KV_E4M3) {
-          const uint2 w = __ldg(static_cast<const uint2*>(pool) + at);
           const float scale = side ? p.v_scale_h[PA_HEAD(p, h)] : p.k_scale_h[PA_HEAD(p, h)];
+          const uint32_t* src = static_cast<const uint32_t*>(pool) + at * (E / 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 two = e4m3x2_to_float2((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
-            x[2 * i] = two.x * scale;
-            x[2 * i + 1] = two.y * scale;
+          for (int i = 0; i < E / 4; ++i) {
+            const uint32_t w = __ldg(src + i);
+            const float2 a = e4m3x2_to_float2(w), b = e4m3x2_to_float2(w >> 16);
+            x[4 * i] = a.x * scale;
+            x[4 * i + 1] = a.y * scale;
+            x[4 * i + 2] = b.x * scale;
+            x[4 * i + 3] = b.y * scale;
           }
         } else if (p.kv_dtype == KV_BF16) {
-          widen<true>(load_octet<true>(pool, at * 8), x);
+          const uint2* src = static_cast<const uint2*>(pool) + at * (E / 4);
+#pragma unroll
+          for (int i = 0; i < E / 4; ++i) {
+            const uint2 w = __ldg(src + i);
+            x[4 * i] = bf16lo(w.x);
+            x[4 * i + 1] = bf16hi(w.x);
+            x[4 * i + 2] = bf16lo(w.y);
+            x[4 * i + 3] = bf16hi(w.y);
+          }
         } else {
-          widen<false>(load_octet<false>(pool, at * 8), x);
+          const float4* src = static_cast<const float4*>(pool) + at * (E / 4);
+#pragma unroll
+          for (int i = 0; i < E / 4; ++i) {
+            const float4 w = __ldg(src + i);
+            x[4 * i] = w.x;
+            x[4 * i + 1] = w.y;
+            x[4 * i + 2] = w.z;
+            x[4 * i + 3] = w.w;
+          }
         }
       }
-      const int64_t to = (row * octets + o) * 8;
-      if (p.out_bf16)
-        store_bf16(out, to, x);
+      const int64_t to = row * units + o;
+      if constexpr (BF16)
+        store_bf16(out, to * 8, x);
       else
-        store_f32(out, to, x);
+        static_cast<float4*>(out)[to] = make_float4(x[0], x[1], x[2], x[3]);
     }
   }
 }
@@ -339,11 +393,12 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
 template <int D, bool BF16, int STEPS>
 cudaError_t launch_rows_inst(const RowsParams& p, cudaStream_t stream) {
   constexpr int kRows = 256 / D * STEPS;
-  const int64_t grid = (static_cast<int64_t>(p.n_rows) + kRows - 1) / kRows;
+  const int64_t sets = (static_cast<int64_t>(p.n_rows) + kRows - 1) / kRows, most = 152 * kRowsCtas;
   // few rows: their heads are shared out to as many CTAs as the GPU holds at once (each computes the angles)
-  const int turns = (p.Hq + 2 * p.Hkv + 7) / 8;
-  const int64_t share = std::max<int64_t>(1, std::min<int64_t>(turns, 152 * 2 / grid));
-  rows_kernel<D, BF16, STEPS><<<dim3(static_cast<unsigned>(grid), static_cast<unsigned>(share)), kRowsThreads, 0, stream>>>(p);
+  const int64_t turns = (p.Hq + 2 * p.Hkv + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
+  const int64_t share = std::max<int64_t>(1, std::min<int64_t>(turns, most / sets));
+  rows_kernel<D, BF16, STEPS><<<dim3(static_cast<unsigned>(std::min(sets, most)), static_cast<unsigned>(share)), kRowsThreads, 0,
+                                stream>>>(p);
   count_launch();
   return cudaGetLastError();
 }
@@ -351,8 +406,7 @@ cudaError_t launch_rows_inst(const RowsParams& p, cudaStream_t stream) {
 template <int D, bool BF16>
 cudaError_t launch_rows_steps(const RowsParams& p, cudaStream_t stream) {
   // one step to a lane as long as that makes no more CTAs than the GPU holds at once
-  return p.n_rows <= 152 * 2 * (256 / D) ? launch_rows_inst<D, BF16, 1>(p, stream)
-                                         : launch_rows_inst<D, BF16, BF16 ? 4 : 2>(p, stream);
+  return p.n_rows <= 152 * 2 * (256 / D) ? launch_rows_inst<D, BF16, 1>(p, stream) : launch_rows_inst<D, BF16, BF16 ? 4 : 2>(p, stream);
 }
 
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream) {
@@ -364,9 +418,13 @@ cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream) {
 
 cudaError_t launch_read(const ReadParams& p, cudaStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(p.n_rows) + 7) / 8;
-  const int64_t turns = (static_cast<int64_t>(p.Hkv) * p.D / 8 + 31) / 32;
+  const int64_t turns = (static_cast<int64_t>(p.Hkv) * p.D / (p.out_bf16 ? 8 : 4) + 31) / 32;
   const int64_t share = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(turns, 64), 152 * 4 / blocks));
-  read_kernel<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(share)), 256, 0, stream>>>(p);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(share));
+  if (p.out_bf16)
+    read_kernel<true><<<grid, 256, 0, stream>>>(p);
+  else
+    read_kernel<false><<<grid, 256, 0, stream>>>(p);
   count_launch();
   return cudaGetLastError();
 }
