@@ -4,6 +4,9 @@ Every step of append, attention, eviction and beam search runs in the library's 
 module passes tensor pointers, sizes and the current CUDA stream through
 ctypes.  PyTorch supplies device memory and streams.  There is no fallback:
 if the shared library is missing or a CUDA device is absent the calls raise.
+The calls of a serving step first try pa_bind, an extension module that looks at plain
+arguments and calls the library in one step; it answers None where an argument is of
+another kind, and the checks here then raise or make the call through ctypes.
 """
 from __future__ import annotations
 
@@ -25,6 +28,7 @@ ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 PA_ORDER_AUTO, PA_ORDER_CALL, PA_ORDER_LONGEST_FIRST = 0, 1, 2
 
 _lib = None
+_bind = None  # the module pa_bind, once the library is loaded
 _lock = threading.Lock()
 
 
@@ -177,8 +181,32 @@ def load(path: str = LIB_PATH):
         L.pa_kernel_launches.restype = ctypes.c_uint64
         L.pa_version.argtypes = []
         L.pa_version.restype = ctypes.c_char_p
+        _load_bind(L)
         _lib = L
         return L
+
+
+def _load_bind(L):
+    global _bind
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  (its libraries come first)
+    path = os.path.join(HERE, "_lib", "pa_bind.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"pa_bind.so not built at {path}; run paged_kv_continuous_pa_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("pa_bind", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_bind", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.pa_append_kv, L.pa_attention, L.pa_tables_grow, L.pa_rope_append, L.pa_prompt_attention, L.pa_read_kv)))
+    _bind = module
+
+
+def _status(status: int):
+    """A status other than PA_OK raises."""
+    if status:
+        raise PaError(status, last_error())
 
 
 def status_string(status: int) -> str:
@@ -251,8 +279,8 @@ def _check_kv_rows(pool: "Pool", k_new, v_new, n: int):
 
 def _stream(stream) -> Optional[int]:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # that of the current device
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -290,7 +318,7 @@ class Pool:
                              1.0 if per_head else self.k_scale, 1.0 if per_head else self.v_scale)
         handle = ctypes.c_void_p()
         _check(load().pa_pool_create(ctypes.byref(self.desc), _ptr(k_pool), _ptr(v_pool), ctypes.byref(handle)))
-        self._h = handle
+        self._h, self._address = handle, handle.value
         if per_head:
             ks = np.ascontiguousarray(np.broadcast_to(self.k_scale, (self.num_kv_heads,)), np.float32)
             vs = np.ascontiguousarray(np.broadcast_to(self.v_scale, (self.num_kv_heads,)), np.float32)
@@ -309,7 +337,7 @@ class Pool:
         self.desc = PoolDesc(self.num_pages, self.page_size, self.num_kv_heads, self.head_dim, self.kv_dtype, 1.0, 1.0)
         handle = ctypes.c_void_p()
         _check(load().pa_pool_create_int4(ctypes.byref(self.desc), kp, vp, kr, vr, ctypes.byref(handle)))
-        self._h = handle
+        self._h, self._address = handle, handle.value
 
     @property
     def handle(self):
@@ -318,7 +346,7 @@ class Pool:
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
             load().pa_pool_destroy(self._h)
-            self._h = None
+            self._h, self._address = None, 0
 
     def __del__(self):  # pragma: no cover
         try:
@@ -378,6 +406,11 @@ class Pages:
 
 def append_kv(pool: Pool, k_new, v_new, seq_ids, positions, block_tables, status=None, stream=None):
     """Scatter rows' new K/V ([n, Hkv, D], f32 or bf16) into their page slots (one launch)."""
+    if stream is None and pool.__class__ is Pool:
+        st = _bind.append_kv(pool._address, pool.num_kv_heads, pool.head_dim, pool.k_pool, k_new, v_new, seq_ids, positions,
+                             block_tables, status)
+        if st is not None:
+            return _status(st)
     _check_index(seq_ids, "seq_ids")
     n = int(seq_ids.shape[0])
     _check_index(positions, "positions", n)
@@ -402,6 +435,11 @@ def attention(pool: Pool, q, seq_ids, positions, block_tables, out,
               chunks: Sequence[Tuple[int, int]] = (), softmax_scale: float = 0.0, workspace=None, status=None,
               stream=None):
     """Paged attention of every row (q [n, Hq, D] f32|bf16) into out (same shape and dtype)."""
+    if stream is None and not chunks and pool.__class__ is Pool:
+        st = _bind.attention(pool._address, pool.head_dim, pool.k_pool, q, seq_ids, positions, block_tables, out, softmax_scale,
+                             workspace, status)
+        if st is not None:
+            return _status(st)
     n = _check_rows(pool, q, seq_ids, positions, block_tables, out, status)
     num_q_heads = int(q.shape[1])
     num_seqs, max_blocks = (int(x) for x in block_tables.shape)
@@ -661,7 +699,7 @@ class Rope:
                         _int32(original_positions, "original_positions"), float(low), float(high), float(magnitude))
         handle = ctypes.c_void_p()
         _check(load().pa_rope_create(ctypes.byref(desc), ctypes.byref(handle)))
-        self.handle = handle
+        self.handle, self._address = handle, handle.value
 
     def frequencies(self):
         """(numpy float64 [rotary_dim / 2] radians per position, the magnitude)."""
@@ -699,6 +737,12 @@ def rope_append(pool: Pool, rope: Optional[Rope], q, k_new, v_new, seq_ids, posi
     """Queries q [n, Hq, D] rotated into q_out, keys rotated and values stored in their page
     slots (one launch).  q, k_new and v_new may be parts of one packed projection; rope
     None rotates nothing, q and q_out None take in keys and values alone."""
+    if stream is None and pool.__class__ is Pool:
+        st = _bind.rope_append(pool._address, pool.num_kv_heads, pool.head_dim, pool.k_pool,
+                               rope._address if rope is not None else None, q, k_new, v_new, seq_ids, positions, block_tables,
+                               q_out, status)
+        if st is not None:
+            return _status(st)
     import torch
     n, heads, d, k_stride = _row_view(k_new, "k_new")
     if (heads, d) != (pool.num_kv_heads, pool.head_dim) or v_new.shape != k_new.shape:
@@ -727,6 +771,11 @@ def rope_append(pool: Pool, rope: Optional[Rope], q, k_new, v_new, seq_ids, posi
 def read_kv(pool: Pool, seq_ids, positions, block_tables, k_out=None, v_out=None, status=None, stream=None):
     """The cached K and V of tokens (seq_ids, positions int32 [n]) as dense rows
     [n, Hkv, D], f32 or bf16: the values that the stored elements stand for."""
+    if stream is None and pool.__class__ is Pool:
+        st = _bind.read_kv(pool._address, pool.num_kv_heads, pool.head_dim, pool.k_pool, seq_ids, positions, block_tables,
+                           k_out, v_out, status)
+        if st is not None:
+            return _status(st)
     import torch
     (n,) = _dims(seq_ids, "seq_ids", "n")
     out = k_out if k_out is not None else v_out
@@ -755,6 +804,10 @@ def prompt_attention(q, k, v, row_starts, out, lse=None, softmax_scale: float = 
     [n, Hkv, D] bf16 (parts of a packed projection allowed), sequence s in rows
     row_starts[s] .. row_starts[s + 1] - 1 (int32, on the device), into out [n, Hq, D] and,
     if given, lse f32 [n, Hq]."""
+    if stream is None and _bind is not None:
+        st = _bind.prompt_attention(q, k, v, row_starts, out, lse, softmax_scale, workspace, status)
+        if st is not None:
+            return _status(st)
     import torch
     n, hq, d, q_stride = _row_view(q, "q")
     kn, hkv, kd, k_stride = _row_view(k, "k")
@@ -780,6 +833,11 @@ def tables_grow(seq_ids, lengths, new_tokens, free_pages, free_count, free_left,
     """Pages from the stack free_pages[:free_count] into the block tables for new_tokens
     more tokens of each request, and the rows of the step: seq ids, positions and
     (optional, int64) token places in the pool.  All int32 on the device."""
+    if stream is None and _bind is not None:
+        st = _bind.tables_grow(seq_ids, lengths, new_tokens, free_pages, free_count, free_left, page_size, block_tables,
+                               row_starts, page_starts, row_seqs, row_positions, row_slots, status)
+        if st is not None:
+            return _status(st)
     import torch
     i32 = torch.int32
     (n,) = _dims(seq_ids, "seq_ids", "n")

@@ -2,7 +2,8 @@
 
 Each .cu under csrc/ compiles to an object in parallel, then one nvcc link
 produces ``_lib/libpa_gb300.so``.  Rebuilds only what changed (object newer
-than its source and every header).
+than its source and every header).  Beside it ``_lib/pa_bind.so``, the binding's
+short way into the library, is compiled with g++ against the installed torch.
 """
 from __future__ import annotations
 
@@ -19,6 +20,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpa_gb300.so")
+BIND_SOURCE = os.path.join(CSRC, "pa_bind.cpp")
+BIND_PATH = os.path.join(LIB_DIR, "pa_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -42,6 +45,29 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def build_bind(force: bool = False) -> str:
+    """Compile the extension module pa_bind (host code; g++, torch's headers and libraries)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    if not force and not _stale(BIND_PATH, [BIND_SOURCE, os.path.join(INCLUDE, "pa.h"), torch.__file__]):
+        return BIND_PATH
+    os.makedirs(LIB_DIR, exist_ok=True)
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{sysconfig.get_paths()['include']}",
+           f"-I{cuda}"] + [f"-I{p}" for p in cpp_extension.include_paths()] + \
+          [BIND_SOURCE, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on pa_bind.cpp:\n{r.stdout}\n{r.stderr[-4000:]}")
+    os.replace(tmp, BIND_PATH)
+    return BIND_PATH
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: str = "") -> str:
@@ -75,9 +101,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
             sys.stderr.write(r.stdout + r.stderr)
         os.replace(tmp, o)
 
-    if jobs:
-        with cf.ThreadPoolExecutor(max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
-            list(ex.map(compile_one, jobs))
+    with cf.ThreadPoolExecutor(max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        bind = ex.submit(build_bind, force) if not variant else None
+        list(ex.map(compile_one, jobs))
+        if bind is not None:
+            bind.result()
     if force or jobs or _stale(lib_path, objs):
         tmp = lib_path + f".tmp{os.getpid()}"
         cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xcompiler", "-fPIC"]
