@@ -266,7 +266,7 @@ typedef struct {
 typedef struct pa_rope pa_rope; /* opaque host object, unchanged after its creation */
 
 /* Errors: PA_ERR_INVALID_ARG (a number outside the ranges above, PA_ROPE_BASE with
- * rotary_dim 2).  pa_rope_frequencies copies f_i (rotary_dim / 2 numbers, radians per
+ * rotary_dim 2, a base and factor whose frequencies are not finite).  pa_rope_frequencies copies f_i (rotary_dim / 2 numbers, radians per
  * position) and the magnitude, either of which may be NULL. */
 pa_status pa_rope_create(const pa_rope_desc *desc, pa_rope **out);
 void pa_rope_destroy(pa_rope *rope);

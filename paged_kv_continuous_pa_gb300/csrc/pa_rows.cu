@@ -509,6 +509,10 @@ pa_status pa_rope_create(const pa_rope_desc* desc, pa_rope** out) {
     if (d.scaling == PA_ROPE_BANDS)
       keep = std::min(std::max((d.original_positions * f / kTwoPi - d.low) / (d.high - d.low), 0.0), 1.0);
     const double g = keep == 1.0 ? f : f / d.factor * (1.0 - keep) + f * keep;
+    if (!std::isfinite(base) || !std::isfinite(g)) {
+      delete p;
+      return fail(PA_ERR_INVALID_ARG, "rope base %g and factor %g give no finite frequencies", d.base, d.factor);
+    }
     p->frequencies[i] = g;
     const double turn = std::fmod(g / kTwoPi, 1.0);
     p->turns[i] = static_cast<uint64_t>(std::ldexp(turn, 63)) * 2;  // (2^64 itself would not fit)
