@@ -324,8 +324,9 @@ pa_status pa_rope_append(const pa_pool *pool, const pa_rope *rope, int32_t n_row
  * Scores, sums and accumulators are FP32; a softmax weight enters its product with V as bf16.
  * What masked keys and values hold (infinities and NaN too, other sequences' rows too) has no
  * influence.  An infinite value that a row attends to gives that element +-infinity, or NaN.
- * A row's bits depend on its own sequence alone.  Two launches, the second a programmatic
- * dependent of the first; graph-capturable.
+ * A row's bits depend on its own sequence alone.  One launch for few units of work (tiles of 128
+ * rows and two heads, or of 256 rows: at most one for each SM, of at most 32 sequences), else two, the
+ * second a programmatic dependent of the first; graph-capturable.
  * Errors: PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED (dtype PA_F32, head_dim), PA_ERR_CUDA.
  * Device-side: row_starts that descend or leave 0..n_rows compute nothing and record
  * PA_ERR_OUT_OF_RANGE; a wait that ran out records PA_ERR_TIMEOUT and leaves out unspecified. */

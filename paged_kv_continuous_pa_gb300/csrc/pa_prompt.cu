@@ -41,7 +41,9 @@ namespace pa {
 constexpr int kPrTile = 128;     // rows of a query tile, keys of a block
 constexpr int kPrSoftmaxThreads = 512;
 constexpr int kPrThreads = kPrSoftmaxThreads + 128;
-constexpr int kPrBins = 2048;    // of the units' lengths, when they are ordered
+constexpr int kPrGroups = 64, kPrBins = 64;  // of sequences, and of positions in a group, when the tiles are ordered
+constexpr int kPrLengths = 1024;             // of the sequences' lengths
+constexpr int64_t kPrGroupBytes = 16 << 20;
 constexpr int kPrPlanThreads = 1024;
 // registers of a softmax thread and of the others; their sum over the CTA is what it is launched with
 constexpr int kPrRegs = 96, kPrSoftmaxRegs = 104, kPrOtherRegs = 64;
@@ -49,14 +51,16 @@ static_assert(kPrSoftmaxThreads * kPrSoftmaxRegs + 128 * kPrOtherRegs <= kPrThre
 
 struct PromptParams {
   const int32_t* row_starts;
-  int32_t* n_tiles;      // workspace: number of tiles listed
+  int32_t* n_tiles;      // workspace: number of tiles listed, number of units taken from the list
   int4* tiles;           // workspace: first row and end of the sequence, position of the tile
+  int32_t* groups;       // workspace: each sequence's group
   const uint16_t* v;
   int64_t v_stride;
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int32_t n_rows, n_seqs, Hq, G, max_tiles, bin_shift;
+  int32_t n_rows, n_seqs, Hq, G, group_rows;
+  int32_t listed;        // the units are taken from the list (else unit i is CTA i's)
   int32_t tile_rows;     // positions of a unit: 128 (two heads) or 256
   float scale_log2;
   uint32_t wait_limit;
@@ -64,36 +68,9 @@ struct PromptParams {
   CUtensorMap qmap, kmap, vmap;  // [rows][heads][D], boxes of 64 elements x 1 head x 128 rows
 };
 
-// The tiles of all sequences, longest first.
-__global__ void __launch_bounds__(kPrPlanThreads) prompt_plan_kernel(const __grid_constant__ PromptParams p) {
-  __shared__ int32_t hist[kPrBins];
-  __shared__ int32_t sums[32];
-  griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kPrBins; i += kPrPlanThreads) hist[i] = 0;
-  bool bad = false;
-  for (int s = tid; s <= p.n_seqs; s += kPrPlanThreads) {
-    const int a = p.row_starts[s];
-    bad |= a < 0 || a > p.n_rows || (s > 0 && p.row_starts[s - 1] > a);
-  }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) {
-      record_error(p.status, ST_OUT_OF_RANGE);
-      *p.n_tiles = 0;
-    }
-    return;
-  }
-  // bin 0 holds the longest units
-  auto bin_of = [&](int pos) { return kPrBins - 1 - min(kPrBins - 1, (pos / kPrTile) >> p.bin_shift); };
-  for (int s = warp; s < p.n_seqs; s += kPrPlanThreads / 32) {
-    const int len = p.row_starts[s + 1] - p.row_starts[s];
-    for (int64_t pos = static_cast<int64_t>(lane) * p.tile_rows; pos < len; pos += 32ll * p.tile_rows)
-      atomicAdd(&hist[bin_of(static_cast<int>(pos))], 1);
-  }
-  __syncthreads();
-  // exclusive sums over the bins, two to a thread
-  const int a = hist[2 * tid], b = hist[2 * tid + 1];
-  int x = a + b;
+// Exclusive sums over the values of the CTA's threads, and (in sums[31]) their total.
+__device__ __forceinline__ int prompt_scan(int x, int32_t* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = x;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -111,15 +88,84 @@ __global__ void __launch_bounds__(kPrPlanThreads) prompt_plan_kernel(const __gri
     sums[lane] = y;
   }
   __syncthreads();
-  const int before = x - a - b + (warp > 0 ? sums[warp - 1] : 0);
-  hist[2 * tid] = before;
-  hist[2 * tid + 1] = before + a;
-  if (tid == 0) *p.n_tiles = sums[31];
+  return x - own + (warp > 0 ? sums[warp - 1] : 0);
+}
+
+// The tiles of all sequences in the order in which they are dealt out: by groups of sequences, the longest
+// sequences first, and in a group the longest tiles first (to within a 64th of the group's longest).
+__global__ void __launch_bounds__(kPrPlanThreads) prompt_plan_kernel(const __grid_constant__ PromptParams p) {
+  __shared__ int32_t hist[kPrGroups * kPrBins];
+  __shared__ int32_t rows[kPrLengths], longest[kPrGroups], sums[32];
+  static_assert(kPrGroups * kPrBins == 4 * kPrPlanThreads && kPrLengths == kPrPlanThreads, "bins of a thread");
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kPrGroups * kPrBins; i += kPrPlanThreads) hist[i] = 0;
+  rows[tid] = 0;
+  if (tid < kPrGroups) longest[tid] = 0;
+  bool bad = false;
+  for (int s = tid; s <= p.n_seqs; s += kPrPlanThreads) {
+    const int a = p.row_starts[s];
+    bad |= a < 0 || a > p.n_rows || (s > 0 && p.row_starts[s - 1] > a);
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      record_error(p.status, ST_OUT_OF_RANGE);
+      p.n_tiles[0] = 0;
+    }
+    return;
+  }
+  auto shift_of = [](int length, int bins) {
+    int shift = 0;
+    while ((length / kPrTile) >> shift >= bins) ++shift;
+    return shift;
+  };
+  const bool grouped = p.n_rows > p.group_rows;
+  if (grouped) {
+    // rows of longer sequences before a sequence's own say which group it is in
+    const int shift = shift_of(p.n_rows, kPrLengths);
+    auto bin_of = [&](int length) { return kPrLengths - 1 - ((length / kPrTile) >> shift); };
+    for (int s = tid; s < p.n_seqs; s += kPrPlanThreads) {
+      const int length = p.row_starts[s + 1] - p.row_starts[s];
+      atomicAdd(&rows[bin_of(length)], length);
+    }
+    __syncthreads();
+    rows[tid] = prompt_scan(rows[tid], sums);
+    __syncthreads();
+    for (int s = tid; s < p.n_seqs; s += kPrPlanThreads) {
+      const int length = p.row_starts[s + 1] - p.row_starts[s];
+      const int group = min(kPrGroups - 1, atomicAdd(&rows[bin_of(length)], length) / p.group_rows);  // (empty ones may lie behind the last)
+      p.groups[s] = group;
+      atomicMax(&longest[group], length);
+    }
+    __syncthreads();
+  }
+  auto place_of = [&](int s, int& shift) {  // the bin of a sequence's first tile
+    const int group = grouped ? p.groups[s] : 0;
+    shift = shift_of(grouped ? longest[group] : p.n_rows, kPrBins);
+    return group * kPrBins + kPrBins - 1;
+  };
+  for (int s = warp; s < p.n_seqs; s += kPrPlanThreads / 32) {
+    const int length = p.row_starts[s + 1] - p.row_starts[s];
+    int shift;
+    const int first = place_of(s, shift);
+    for (int64_t pos = static_cast<int64_t>(lane) * p.tile_rows; pos < length; pos += 32ll * p.tile_rows)
+      atomicAdd(&hist[first - ((static_cast<int>(pos) / kPrTile) >> shift)], 1);
+  }
+  __syncthreads();
+  int4 n = *reinterpret_cast<const int4*>(hist + 4 * tid);
+  const int before = prompt_scan(n.x + n.y + n.z + n.w, sums);
+  *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(before, before + n.x, before + n.x + n.y, before + n.x + n.y + n.z);
+  if (tid == 0) {
+    p.n_tiles[0] = sums[31];
+    p.n_tiles[1] = 0;  // units taken
+  }
   __syncthreads();
   for (int s = warp; s < p.n_seqs; s += kPrPlanThreads / 32) {
     const int begin = p.row_starts[s], end = p.row_starts[s + 1];
+    int shift;
+    const int first = place_of(s, shift);
     for (int64_t pos = static_cast<int64_t>(lane) * p.tile_rows; pos < end - begin; pos += 32ll * p.tile_rows)
-      p.tiles[atomicAdd(&hist[bin_of(static_cast<int>(pos))], 1)] = make_int4(begin, end, static_cast<int>(pos), 0);
+      p.tiles[atomicAdd(&hist[first - ((static_cast<int>(pos) / kPrTile) >> shift)], 1)] = make_int4(begin, end, static_cast<int>(pos), 0);
   }
 }
 
@@ -272,7 +318,7 @@ struct PromptSmem {  // byte offsets from the base, which is 1024-byte aligned (
   static constexpr int STAGES = D == 128 ? 5 : 8;  // tiles of K and V in the ring
   static constexpr int RING = 2 * TILE;            // behind the two query tiles
   static constexpr int BAR = RING + STAGES * TILE;
-  static constexpr int BYTES = BAR + 384;
+  static constexpr int BYTES = BAR + 512;
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -313,10 +359,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     VOK = PL + 2,
     VIN = VOK + 4,               // its load is under way (the ring's slot has come to this tile)
     DRAIN = VIN + 4,
-    STALL = DRAIN + 2,
+    UF = DRAIN + 2,              // a unit was taken, in turn
+    UE = UF + 4,                 // ... every warp knows it
+    STALL = UE + 4,
     COUNT
   };
-  static_assert(COUNT * 8 + 32 <= S::BYTES - S::BAR, "barriers");
+  constexpr int UNITS = (COUNT * 8 + 32 + 15) / 16 * 16;
+  static_assert(UNITS + 64 <= S::BYTES - S::BAR, "barriers");
   extern __shared__ __align__(1024) unsigned char sm[];
   if ((smem_addr(sm) & 1023u) != 0) {  // (the swizzled tiles would be read at other places than they were written)
     if (threadIdx.x == 0) record_error(p.status, ST_LAUNCH);
@@ -325,55 +374,83 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::BAR + COUNT * 8);
   volatile int32_t* odd_values = reinterpret_cast<volatile int32_t*>(tslot + 1);  // entry k % 4 is k + 1: values of unit k were put to 0
+  volatile int4* taken = reinterpret_cast<volatile int4*>(sm + S::BAR + UNITS);  // entry k % 4: unit k's tile and, in w, its head (-1: no unit)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (warp == 0) tc::tmem_alloc(tslot, 512);
-  if (tid == 0) {
-    for (int i = 0; i < COUNT; ++i) mbar_init(&bar[i], i >= PF && i < PF + 4 ? 8u : i >= EMPTY && i < QF ? 2u : i >= VOK && i < VOK + 4 ? 8u : 1u);
-    for (int i = 0; i < 4; ++i) odd_values[i] = 0;
+  if (tid >= 32 && tid < 32 + COUNT) {
+    const int i = tid - 32;
+    mbar_init(&bar[i], i >= UE && i < UE + 4 ? 18u : (i >= PF && i < PF + 4) || (i >= VOK && i < VOK + 4) ? 8u : i >= EMPTY && i < QF ? 2u : 1u);
+    if (i < 4) odd_values[i] = 0;
     fence_barrier_init();
+  }
+  if (tid == kPrSoftmaxThreads + 32) {
     tc::prefetch_tensormap(&p.qmap);
     tc::prefetch_tensormap(&p.kmap);
     tc::prefetch_tensormap(&p.vmap);
+  }
+  // The first unit is the CTA's own (the loading warp finds it; without a list, beside the set-up).
+  const bool two_heads = p.tile_rows == kPrTile;
+  const int per_tile = two_heads ? p.Hq / 2 : p.Hq;
+  int units = 0, u = blockIdx.x;
+  int4 tile = make_int4(0, 0, 0, 0);
+  if (warp == 16 && !p.listed) {
+    // a lane to a sequence; tiles in the sequences' order
+    const int begin = lane < p.n_seqs ? p.row_starts[lane] : 0, end = lane < p.n_seqs ? p.row_starts[lane + 1] : 0;
+    if (__any_sync(0xffffffffu, begin < 0 || end > p.n_rows || end < begin)) {
+      if (lane == 0) record_error(p.status, ST_OUT_OF_RANGE);
+    } else {
+      const int own = (end - begin + p.tile_rows - 1) / p.tile_rows;
+      int upto = own;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      units = __shfl_sync(0xffffffffu, upto, 31) * per_tile;
+      const int i = u / per_tile;
+      const int from = __popc(__ballot_sync(0xffffffffu, upto <= i)) & 31;  // (32: no unit for this CTA)
+      tile = make_int4(__shfl_sync(0xffffffffu, begin, from), __shfl_sync(0xffffffffu, end, from),
+                       (i - __shfl_sync(0xffffffffu, upto - own, from)) * p.tile_rows, 0);
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   griddep_wait();  // the list of tiles
   const uint32_t tb = *tslot;
-  const bool two_heads = p.tile_rows == kPrTile;
-  const int per_tile = two_heads ? p.Hq / 2 : p.Hq;
-  const int units = *p.n_tiles * per_tile;
+  if (warp == 16 && p.listed) {
+    units = p.n_tiles[0] * per_tile;
+    if (u < units) tile = __ldcg(p.tiles + u / per_tile);
+  }
 
   auto wait = [&](int b, uint32_t parity) { return mbar_test(&bar[b], parity) || pr_wait(&bar[b], parity, p.wait_limit, p.status); };
-  // the k-th unit of this CTA (every other round backwards); false behind the last.  The tile of the next one is
-  // on its way meanwhile.
-  auto index_of = [&](int k) {
-    return static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-  };
-  int4 ahead = index_of(0) < units ? __ldcg(p.tiles + index_of(0) / per_tile) : make_int4(0, 0, 0, 0);
-  auto unit_at = [&](int k, PromptUnit& x) {
-    const int64_t u = index_of(k);
-    if (static_cast<int64_t>(k) * gridDim.x >= units) return false;
-    const int4 t = ahead;
-    if (index_of(k + 1) < units) ahead = __ldcg(p.tiles + index_of(k + 1) / per_tile);
-    x.n = x.blocks_a = x.blocks_b = 0;
-    if (u >= units) return true;  // (a round without work for this CTA)
-    const int h = static_cast<int>(u % per_tile);
-    x.begin = t.x;
-    x.end = t.y;
-    x.pos_a = t.z;
-    x.n = x.blocks_a = t.z / kPrTile + 1;
+  auto describe = [&](PromptUnit& x, int begin, int end, int pos, int h) {
+    x.begin = begin;
+    x.end = end;
+    x.pos_a = pos;
+    x.n = x.blocks_a = pos / kPrTile + 1;
+    x.blocks_b = 0;
     if (two_heads) {
       x.head_a = 2 * h;
       x.head_b = 2 * h + 1;
-      x.pos_b = t.z;
+      x.pos_b = pos;
       x.blocks_b = x.n;
     } else {
       x.head_a = x.head_b = h;
-      x.pos_b = t.z + kPrTile;
-      if (x.pos_b < t.y - t.x) x.n = x.blocks_b = x.blocks_a + 1;
+      x.pos_b = pos + kPrTile;
+      if (x.pos_b < end - begin) x.n = x.blocks_b = x.blocks_a + 1;
     }
+  };
+  // The k-th unit of this CTA, for a whole warp; false behind the last, and where the wait for it ran out.
+  auto unit_at = [&](int k, PromptUnit& x, bool& ok) {
+    ok = __all_sync(0xffffffffu, wait(UF + (k & 3), (k >> 2) & 1));
+    if (!ok) return false;
+    const int begin = taken[k & 3].x, end = taken[k & 3].y, pos = taken[k & 3].z, h = taken[k & 3].w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[UE + (k & 3)]);
+    if (h < 0) return false;
+    describe(x, begin, end, pos, h);
     return true;
   };
 
@@ -403,14 +480,26 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         at.next();
         return true;
       };
-      for (int k = 0; ok && unit_at(k, x); ++k) {
-        if (x.blocks_a > 0) ok = queries(0, done_a, x.pos_a, x.head_a);
-        if (ok && x.blocks_b > 0) ok = queries(1, done_b, x.pos_b, x.head_b);
+      for (int k = 0; ok; ++k) {
+        if (k >= 4) ok = wait(UE + (k & 3), ((k >> 2) - 1) & 1);
+        if (!ok) break;
+        taken[k & 3].x = tile.x;
+        taken[k & 3].y = tile.y;
+        taken[k & 3].z = tile.z;
+        taken[k & 3].w = u < units ? u % per_tile : -1;
+        mbar_arrive(&bar[UF + (k & 3)]);
+        if (u >= units) break;
+        describe(x, tile.x, tile.y, tile.z, u % per_tile);
         const int kv_head = x.head_a / p.G;
         for (int j = 0; ok && j < x.n; ++j) {
-          ok = keys(&p.kmap, kv_head, j) && keys(&p.vmap, kv_head, j);
+          if (j == x.n - 1) u = p.listed ? static_cast<int>(gridDim.x) + atomicAdd(p.n_tiles + 1, 1) : units;  // the next one
+          ok = keys(&p.kmap, kv_head, j);
+          if (ok && j == 0)  // (these keys need not wait for the last unit's queries to be done with)
+            ok = queries(0, done_a, x.pos_a, x.head_a) && (x.blocks_b == 0 || queries(1, done_b, x.pos_b, x.head_b));
+          ok = ok && keys(&p.vmap, kv_head, j);
           if (ok && j >= x.blocks_a - 1) mbar_arrive(&bar[VIN + (checked++ & 3)]);
         }
+        if (u < units) tile = __ldcg(p.tiles + u / per_tile);
       }
       if (!ok) {  // what is in flight lands before the shared memory is given up
         for (int i = max(0, items - S::STAGES); i < items; ++i)
@@ -473,8 +562,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           pr_mma_ts(one, to, ts + 64 * half + kk * 8, desc(vt + kk * (2048 >> 4)), id_pv, !first || kk > 0);
         return true;
       };
-      for (int k = 0; ok && unit_at(k, x); ++k) {
-        if (x.n == 0) continue;
+      for (int k = 0; ok && unit_at(k, x, ok); ++k) {
         const int n = t == 0 ? x.blocks_a : x.blocks_b;
         int slot, next = 0;
         ok = take(slot) && (n == 0 || wait_all(QF + t, q_turn));
@@ -568,7 +656,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(&bar[VOK + (checked & 3)]);
       return true;
     };
-    for (int k = 0; ok && unit_at(k, x); ++k) {
+    for (int k = 0; ok && unit_at(k, x, ok); ++k) {
       const int n = t == 0 ? x.blocks_a : x.blocks_b;
       const bool two_looks = x.blocks_b > x.blocks_a;  // each tile's warps look over the values of its own diagonal
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
@@ -661,7 +749,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
       }
       if (!ok) break;
       items += 2 * x.n;
-      checked += x.n == 0 ? 0 : two_looks ? 2 : 1;
+      checked += two_looks ? 2 : 1;
       if (n == 0) continue;
       // ---- output
       ok = __all_sync(0xffffffffu, wait(PV + t, o_turn));
@@ -743,11 +831,13 @@ cudaError_t launch_prompt(const PromptParams& p, unsigned grid, cudaStream_t str
     regs.store(a.numRegs, std::memory_order_release);
   }
   if (regs.load(std::memory_order_acquire) != kPrRegs) return cudaErrorInvalidKernelImage;
-  prompt_plan_kernel<<<1, kPrPlanThreads, 0, stream>>>(p);
-  count_launch();
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  e = launch_kernel(prompt_kernel<D>, dim3(grid), dim3(kPrThreads), PromptSmem<D>::BYTES, stream, true, p);
+  if (p.listed) {
+    prompt_plan_kernel<<<1, kPrPlanThreads, 0, stream>>>(p);
+    count_launch();
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_kernel(prompt_kernel<D>, dim3(grid), dim3(kPrThreads), PromptSmem<D>::BYTES, stream, p.listed != 0, p);
   count_launch();
   return e;
 }
@@ -793,7 +883,8 @@ extern "C" {
 size_t pa_prompt_workspace_bytes(int32_t n_rows, int32_t n_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                  int32_t head_dim) {
   if (check_prompt(n_rows, n_seqs, num_q_heads, num_kv_heads, head_dim) != PA_OK) return 0;
-  return 256 + static_cast<size_t>(most_tiles(n_rows, n_seqs, num_q_heads, num_kv_heads)) * sizeof(int4);
+  return 256 + static_cast<size_t>(most_tiles(n_rows, n_seqs, num_q_heads, num_kv_heads)) * sizeof(int4) +
+         static_cast<size_t>(n_seqs) * sizeof(int32_t);
 }
 
 pa_status pa_prompt_attention(int32_t n_rows, int32_t n_seqs, const void* q, int64_t q_stride, const void* k,
@@ -823,6 +914,7 @@ pa_status pa_prompt_attention(int32_t n_rows, int32_t n_seqs, const void* q, int
   p.row_starts = row_starts;
   p.n_tiles = static_cast<int32_t*>(workspace);
   p.tiles = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + 256);
+  p.groups = reinterpret_cast<int32_t*>(p.tiles + most_tiles(n_rows, n_seqs, num_q_heads, num_kv_heads));
   p.v = static_cast<const uint16_t*>(v);
   p.v_stride = v_stride;
   p.out = static_cast<uint16_t*>(out);
@@ -833,7 +925,9 @@ pa_status pa_prompt_attention(int32_t n_rows, int32_t n_seqs, const void* q, int
   p.Hq = num_q_heads;
   p.G = num_q_heads / num_kv_heads;
   p.tile_rows = two_heads(num_q_heads, num_kv_heads) ? pa::kPrTile : 2 * pa::kPrTile;
-  while ((n_rows / pa::kPrTile) >> p.bin_shift >= pa::kPrBins) ++p.bin_shift;
+  // rows whose keys and values fill a group's share of L2, at most kPrGroups groups
+  const int64_t share = pa::kPrGroupBytes / (4 * kv_row);
+  p.group_rows = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>({share, (static_cast<int64_t>(n_rows) + pa::kPrGroups - 1) / pa::kPrGroups, 1}), 0x7fffffff));
   p.scale_log2 = static_cast<float>(scale * 1.4426950408889634073599246810018921);
   p.wait_limit = pa::wait_limit();
   p.debug_stall = pa::debug_stall();
@@ -851,6 +945,8 @@ pa_status pa_prompt_attention(int32_t n_rows, int32_t n_seqs, const void* q, int
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention");
   const int64_t units = most_tiles(n_rows, n_seqs, num_q_heads, num_kv_heads) * (p.tile_rows == pa::kPrTile ? num_q_heads / 2 : num_q_heads);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(sms, units));
+  // A CTA for each unit needs no list: its warp finds the unit among up to 32 sequences.
+  p.listed = units > sms || n_seqs > 32;
   e = head_dim == 128 ? pa::launch_prompt<128>(p, grid, static_cast<cudaStream_t>(stream))
                       : pa::launch_prompt<64>(p, grid, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "prompt attention launch");

@@ -206,3 +206,61 @@ def test_graph_and_stream():
         torch.cuda.synchronize()
         want, _ = run(q2, k2, v2, starts2)
         assert torch.equal(out[:sum(lengths)], want[:sum(lengths)])
+
+
+@pytest.mark.parametrize("seqs", [1, 31, 32, 33, 40])
+def test_few_units_and_a_list(seqs):
+    """A CTA for each unit finds its own among up to 32 sequences; beyond, they come from a list."""
+    lengths = [(37 * i) % 61 for i in range(seqs)]
+    check(*make(lengths, 4, 2, 64, seed=seqs), with_lse=True)
+
+
+def test_groups_of_sequences():
+    """Keys and values of more than one share of L2: sequences of all lengths, equal and empty ones among them."""
+    lengths = [0, 700, 1, 300, 300, 300, 129, 0, 2100, 5, 64, 300, 900, 1500, 128, 0]
+    check(*make(lengths, 16, 16, 128), with_lse=True)
+
+
+def test_as_many_groups_as_there_are():
+    """65536 rows in groups of 1024, with empty sequences behind the last row of the last group."""
+    lengths = [0, 0] + [128] * 510 + [256] + [0] * 3
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn(sum(lengths), 32, 128, generator=g, device="cuda", dtype=BF16) for _ in "qkv")
+    starts = torch.tensor([sum(lengths[:i]) for i in range(len(lengths) + 1)], dtype=torch.int32, device="cuda")
+    out, status = run(q, k, v, starts)
+    assert status == 0
+    half = torch.cat([starts[:257], starts[256:257]])
+    n = int(half[-1])
+    part, status = run(q[:n], k[:n], v[:n], half)
+    assert status == 0 and torch.equal(part, out[:n])
+    back = starts[257:] - starts[257]
+    m = int(starts[257])
+    part, status = run(q[m:].contiguous(), k[m:].contiguous(), v[m:].contiguous(), back)
+    assert status == 0 and torch.equal(part, out[m:])
+    for a, b in ((0, 128), (65280, 65536), (30080, 30208)):
+        want, size, _, big = R.causal(q[a:b], k[a:b], v[a:b], R.scale_of(128))
+        assert bool(((out[a:b].double() - want).abs() <= R.causal_bound(want, size, 128, b - a, big)).all())
+
+
+@pytest.mark.parametrize("bad", [(20, -1), (20, 10 ** 9), (39, 4000)])
+def test_bad_starts_of_a_list(bad):
+    q, k, v, starts = make([64] * 40, 2, 1, 64)
+    starts = starts.clone()
+    starts[bad[0]] = bad[1]
+    out, status = run(q, k, v, starts)
+    assert status == pa.PA_ERR_OUT_OF_RANGE and (out == 7.0).all()
+
+
+def test_a_list_that_is_waited_for_in_vain():
+    q, k, v, starts = make([200] * 40, 2, 1, 64)
+    want, status = run(q, k, v, starts)
+    assert status == 0
+    pa.set_wait_limit(2000)
+    pa.debug_stall_waits(True)
+    try:
+        assert run(q, k, v, starts)[1] == pa.PA_ERR_TIMEOUT
+    finally:
+        pa.debug_stall_waits(False)
+        pa.set_wait_limit(0)
+    out, status = run(q, k, v, starts)
+    assert status == 0 and torch.equal(out, want)
