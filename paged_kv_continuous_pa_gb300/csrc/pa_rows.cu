@@ -75,55 +75,95 @@ __device__ __forceinline__ void store_bf16(void* base, int64_t element, const fl
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + element) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Largest and smallest of two or three numbers; NaN where one is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Two binary32 numbers at a time, each operation rounded once.
+__device__ __forceinline__ uint64_t two_of(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void halves_of(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // One token of one kv head into a 4-bit pool: L lanes hold 8 elements each.  The range is
 // stored first and the codes are taken against what was stored, so that a code is off by
 // half a step at most (each conversion below rounds once, to nearest even).
 // The format divides in binary32.  With y the rounded reciprocal of the step, one per token, d y corrected once by the
 // exact remainder is the rounded quotient (Markstein's theorem: quotients here are below 32 and the
-// remainder is a multiple of what binary32 holds); two multiply-adds in place of a division for each element
-// (with the integer divisions below gone as well, 75 -> 24 us for 16384 rows of 8 heads).
+// remainder is a multiple of what binary32 holds): two multiply-adds in place of a division for each element.
 template <int L>
 __device__ __forceinline__ void store_int4(void* codes, void* ranges, int64_t token, int l, float (&x)[8]) {
-  float lo = x[0], hi = x[0], odd = 0.0f;
+  float lo = x[0], hi = x[0];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    odd = fmaf(x[i], 0.0f, odd);  // NaN from an infinity or NaN on
+  for (int i = 1; i < 7; i += 2) {
+    lo = min_nan(lo, x[i], x[i + 1]);
+    hi = max_nan(hi, x[i], x[i + 1]);
   }
-  // maximum over the group of hi in its odd lanes, of -lo in the even ones
+  lo = min_nan(lo, x[7], x[7]);
+  hi = max_nan(hi, x[7]);
+  // maximum over the group of hi in its odd lanes, of -lo in the even ones; NaN in both where there is one
   const bool upper = (l & 1) != 0;
-  float v = fmaxf(upper ? hi : -lo, __shfl_xor_sync(0xffffffffu, upper ? -lo : hi, 1));
+  float v = max_nan(upper ? hi : -lo, __shfl_xor_sync(0xffffffffu, upper ? -lo : hi, 1));
 #pragma unroll
-  for (int d = 2; d < L; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  for (int d = 2; d < L; d *= 2) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
   const float w = __shfl_xor_sync(0xffffffffu, v, 1);
   lo = upper ? -w : -v;
   hi = upper ? v : w;
-  const uint32_t group = ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
-  bool nan = false;
-  if ((__ballot_sync(0xffffffffu, odd != odd || hi > 65504.0f || lo < -65504.0f) & group) != 0u) {  // the range is held in f16
+  const bool nan = hi != hi;
+  if (!(hi <= 65504.0f && lo >= -65504.0f)) {  // the range is held in f16
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      nan |= x[i] != x[i];
-      x[i] = fminf(fmaxf(x[i], -65504.0f), 65504.0f);
-    }
-    nan = (__ballot_sync(group, nan) & group) != 0u;
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -65504.0f), 65504.0f);
     lo = fminf(fmaxf(lo, -65504.0f), 65504.0f);
     hi = fminf(fmaxf(hi, -65504.0f), 65504.0f);
   }
   __half low = __float2half_rn(lo);
   const float lf = __half2float(low);
-  __half step = __float2half_rn(fmaxf(__fdiv_rn(__fsub_rn(hi, lf), 15.0f), 0.0f));
+  // a fifteenth of the width, rounded once as below (what is too small for an exact remainder is 0 in f16)
+  constexpr float fifteenth = 1.0f / 15.0f;
+  const float width = __fsub_rn(hi, lf), part = __fmul_rn(width, fifteenth);
+  __half step = __float2half_rn(fmaxf(fmaf(fmaf(-part, 15.0f, width), fifteenth, part), 0.0f));
   const float sf = __half2float(step);
   uint32_t word = 0;
   if (sf > 0.0f && !nan) {
     const float y = __frcp_rn(sf);
     float c[8];
+    const uint64_t y2 = two_of(y, y), down2 = two_of(-lf, -lf), minus2 = two_of(-sf, -sf);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = __fsub_rn(x[i], lf);
-      const float q = __fmul_rn(d, y);
-      c[i] = fmaf(fmaf(-q, sf, d), y, q);
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t d = add2(two_of(x[i], x[i + 1]), down2), q = mul2(d, y2);
+      halves_of(fma2(fma2(q, minus2, d), y2, q), c[i], c[i + 1]);
     }
     // A step that is a normal f16 number is off by 2^-11 of it, and low by 2^-11 of low: quotients stay within -1/4
     // and 15 + 1/4 unless low is large beside the step.
@@ -134,9 +174,11 @@ __device__ __forceinline__ void store_int4(void* codes, void* ranges, int64_t to
     // c + 1.5 2^23 rounds to the integer (ties to even) in the lowest bits; the rest goes below
     uint32_t rest = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      word += __float_as_uint(__fadd_rn(c[i], 12582912.0f)) << (4 * i);
-      rest += 0x4b400000u << (4 * i);
+    for (int i = 0; i < 8; i += 2) {
+      float a, b;
+      halves_of(add2(two_of(c[i], c[i + 1]), two_of(12582912.0f, 12582912.0f)), a, b);
+      word += (__float_as_uint(a) << (4 * i)) + (__float_as_uint(b) << (4 * i + 4));
+      rest += (0x4b400000u << (4 * i)) + (0x4b400000u << (4 * i + 4));
     }
     word -= rest;
   }
@@ -313,7 +355,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsCtas) rows_kernel(const __g
 }
 
 // A warp per row and 16 bytes of output at a time to a lane (E elements), gridDim.y shares of a row.
-template <bool BF16>
+template <int KV, bool BF16>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
   constexpr int E = BF16 ? 8 : 4;
   const int lane = threadIdx.x & 31;
@@ -340,14 +382,14 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
       if (page >= 0) {
         const int64_t token = token0 + static_cast<int64_t>(h) * p.P;
         const int64_t at = (token << lg_units) + (o & ((1 << lg_units) - 1));  // in units
-        if (p.kv_dtype == KV_INT4) {
+        if constexpr (KV == KV_INT4) {
           const uint32_t w = BF16 ? __ldg(static_cast<const uint32_t*>(pool) + at) : __ldg(static_cast<const uint16_t*>(pool) + at);
           const uint32_t range = __ldg(ranges + token);
           const float step = __half2float(__ushort_as_half(static_cast<unsigned short>(range & 0xffffu)));
           const float low = __half2float(__ushort_as_half(static_cast<unsigned short>(range >> 16)));
 #pragma unroll
           for (int i = 0; i < E; ++i) x[i] = fmaf(static_cast<float>((w >> (4 * i)) & 15u), step, low);
-        } else if (p.kv_dtype == KV_E4M3) {
+        } else if constexpr (KV == KV_E4M3) {
           const float scale = side ? p.v_scale_h[PA_HEAD(p, h)] : p.k_scale_h[PA_HEAD(p, h)];
           const uint32_t* src = static_cast<const uint32_t*>(pool) + at * (E / 4);
 #pragma unroll
@@ -359,7 +401,7 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
             x[4 * i + 2] = b.x * scale;
             x[4 * i + 3] = b.y * scale;
           }
-        } else if (p.kv_dtype == KV_BF16) {
+        } else if constexpr (KV == KV_BF16) {
           const uint2* src = static_cast<const uint2*>(pool) + at * (E / 4);
 #pragma unroll
           for (int i = 0; i < E / 4; ++i) {
@@ -406,7 +448,8 @@ cudaError_t launch_rows_inst(const RowsParams& p, cudaStream_t stream) {
 template <int D, bool BF16>
 cudaError_t launch_rows_steps(const RowsParams& p, cudaStream_t stream) {
   // one step to a lane as long as that makes no more CTAs than the GPU holds at once
-  return p.n_rows <= 152 * 2 * (256 / D) ? launch_rows_inst<D, BF16, 1>(p, stream) : launch_rows_inst<D, BF16, BF16 ? 4 : 2>(p, stream);
+  return p.n_rows <= 152 * 2 * (256 / D) ? launch_rows_inst<D, BF16, 1>(p, stream)
+                                         : launch_rows_inst<D, BF16, BF16 ? 4 : 2>(p, stream);
 }
 
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream) {
@@ -421,10 +464,13 @@ cudaError_t launch_read(const ReadParams& p, cudaStream_t stream) {
   const int64_t turns = (static_cast<int64_t>(p.Hkv) * p.D / (p.out_bf16 ? 8 : 4) + 31) / 32;
   const int64_t share = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(turns, 64), 152 * 4 / blocks));
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(share));
-  if (p.out_bf16)
-    read_kernel<true><<<grid, 256, 0, stream>>>(p);
-  else
-    read_kernel<false><<<grid, 256, 0, stream>>>(p);
+  auto go = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(p); };
+  switch (p.kv_dtype) {
+    case KV_F32: p.out_bf16 ? go(read_kernel<KV_F32, true>) : go(read_kernel<KV_F32, false>); break;
+    case KV_BF16: p.out_bf16 ? go(read_kernel<KV_BF16, true>) : go(read_kernel<KV_BF16, false>); break;
+    case KV_E4M3: p.out_bf16 ? go(read_kernel<KV_E4M3, true>) : go(read_kernel<KV_E4M3, false>); break;
+    default: p.out_bf16 ? go(read_kernel<KV_INT4, true>) : go(read_kernel<KV_INT4, false>); break;
+  }
   count_launch();
   return cudaGetLastError();
 }
