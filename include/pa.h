@@ -21,7 +21,7 @@
  * Conventions for every entry point:
  *   - All device memory (pools, q, k/v, out, tables, workspace, status) is
  *     allocated and owned by the caller.  The library owns only the small host
- *     pa_pool object.  No call allocates device memory or synchronises.
+ *     pa_pool and pa_rope objects.  No call allocates device memory or synchronises.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default).
  *   - Any host thread may call, several at once on one pool where their workspaces
  *     and outputs are their own (pa_pool_set_head_scales comes before).
@@ -59,13 +59,13 @@ typedef enum {
     PA_ERR_OUT_OF_RANGE = 3, /* device-side: sequence id, position or page id out of range */
     PA_ERR_TIMEOUT = 4,     /* device-side: a bounded wait on a copy gave up */
     PA_ERR_CUDA = 5,        /* a CUDA runtime call failed (launch, attribute, driver entry point), or a kernel found its launch configuration inconsistent */
-    PA_ERR_NO_PAGES = 6     /* host-side: an admission needs more free pages than the pool has */
+    PA_ERR_NO_PAGES = 6     /* an admission (host-side) or a pa_tables_grow (device-side) needs more free pages or rows than there are */
 } pa_status;
 
 typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
 
 /* Pool geometry.  page_size in {16, 32, 64, 128, 256}; head_dim in {64, 128};
- * kv_dtype PA_F32, PA_BF16 or PA_FP8_E4M3.  k_scale / v_scale are the fp8
+ * kv_dtype PA_F32, PA_BF16 or PA_FP8_E4M3 (PA_INT4: pa_pool_create_int4).  k_scale / v_scale are the fp8
  * per-tensor scales ("Engines for the card you have", section "One checkpoint,
  * many engines": an FP8 key/value cache, calibrated): a stored code c means
  * value(c) * scale, and appending x stores e4m3_satfinite_rne(x / scale).
@@ -361,7 +361,7 @@ pa_status pa_prompt_attention(int32_t n_rows, int32_t n_seqs, const void *q, int
  *                 row_starts[n] are left as they were.  All three may be NULL where max_rows is 0
  * Outputs overlap no input (but free_left).  The pages of a pool are handed out here or by
  * pa_pages_*, not by both; pages are not shared between slots.
- * num_seqs <= 2^19.  One launch for at most 4096 rows, else two, the second a programmatic
+ * num_seqs <= 2^19.  One launch for at most 2048 rows, else two, the second a programmatic
  * dependent of the first; no workspace; graph-capturable. */
 pa_status pa_tables_grow(int32_t n, const int32_t *seq_ids, const int32_t *lengths, const int32_t *new_tokens,
                          const int32_t *free_pages, const int32_t *free_count, int32_t *free_left, int32_t num_pages,

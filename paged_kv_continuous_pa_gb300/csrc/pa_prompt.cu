@@ -3,10 +3,9 @@
 //
 //   out_i = sum_{j <= i} exp2(s_ij - m_i) v_j / sum_{j <= i} exp2(s_ij - m_i),   s_ij = scale log2(e) q_i . k_j
 //
-// One pass over the keys with a running reference m_i: it moves only when a score
-// passes it by 2^8, so the accumulator is seldom rescaled, a row's maximum is
-// only taken over its four lanes then, and the first half of a block's weights is
-// computed beside the maximum, before it is known whether they will do.
+// One pass over the keys with a running reference m_i: it moves only when a score passes it by
+// 2^8, so that the accumulator is seldom rescaled and a row's maximum is only joined over its four
+// lanes then.
 //
 // What bounds it: the two matrix products, 4 D flops for each (query head, query, key).
 // One CTA per SM goes through units of work.  A unit is two query tiles of 128 rows that
@@ -16,19 +15,31 @@
 //   warps 0-7, 8-15  softmax and output of tile A, B: 16 rows to a warp, a row in four lanes (so that a row is one
 //                    warp's, and four warps of a scheduler hide each other's latencies); while they wait for the scores
 //                    of a block with masked keys they look over its values
-//   warp 16          loads: queries and 128-key tiles of K and V through a ring (TMA)
-//   warps 18, 19     issue the MMAs of tile A, B:  S = Q K^T (smem x smem), O += P V (TMEM x smem).  (One for both
-//                    was busy for all of the 3800 clocks that two tiles' blocks took: a wait costs it 100 to 200, 16 MMAs
-//                    1024, and neither can the queue of MMAs hide the waits.)
-// Tensor memory: S of A and B (128 columns each), the weights P over their S as bf16, O of A and B.
+//   warp 16          takes the units and loads: queries and 128-key tiles of K and V through a ring (TMA)
+//   warps 18, 19     issue the MMAs of tile A, B:  S = Q K^T (smem x smem), O += P V (TMEM x smem).  A whole warp goes
+//                    through that code and one lane's instructions are predicated on: beside 16 busy warps an MMA
+//                    of 128 x 128 x 16 was issued every 44 clocks so, every 52 in a branch of an elected lane, every 84
+//                    in one of lane 0, and it takes the tensor core 64 (one prompt of 16384: 1532 -> 1308 us)
+// Tensor memory: S of A and B (128 columns each, the first and the second 64 keys of a block apart), the weights P over
+// their S as bf16, O of A and B.  A weight is rounded to bf16 (off by 2^-8 of itself at most) as the product with V takes it; the
+// sum l of a row's weights is taken before, in FP32.
 //
 // Masked keys.  Only the block on a tile's diagonal has any (keys behind the
 // sequence's end are behind every row's diagonal too).  A masked key's weight is 0,
 // but 0 times an infinite or NaN value is NaN, so 0 is put in the
 // place of such values in shared memory; a row that does attend to one gets it added at the end.
 //
-// Units are listed longest first by a launch of their own and dealt out to the CTAs in a
-// snake, so that the last ones are short.
+// Order.  A launch of one CTA lists the tiles, and the CTAs take units from the list as they get free.  Longest
+// first over all sequences ends with short units, but sends every sequence's keys through L2 once for each range of
+// positions: 64 prompts of 64 to 2662 tokens (356 MB of keys and values) read 2.96 GB from DRAM and took 631 us.  So
+// sequences come in groups whose keys and values are 16 MB, longest sequences first, and within a
+// group the longest tiles first: 523 us (526 with 32 MB, 538 with 64, 520 with 8, where one prompt of 16384 took 1395 instead
+// of 1280).  A unit that is taken before the last one's end is near goes to a CTA that is late already
+// (128 instead of 102 us for 8192 tokens of 8 heads).  Few units need no list (9.6 -> 8.2 us for 77 tokens).
+//
+// Measured: 1276 to 1400 us for one prompt of 16384 with 32 heads over 8 (the clock under the power
+// limit decides), 84 to 92% of what the products alone take at the measured matrix rate; 523 us for the 64 prompts (338 us of
+// products, 13% more on the diagonals' masked halves, and a unit's own start and end).
 #include <algorithm>
 #include <cmath>
 

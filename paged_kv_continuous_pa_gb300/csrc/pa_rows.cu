@@ -17,6 +17,11 @@
 // a lane; the partner octet of the half layout sits in another lane of the same group and comes
 // by shuffle.  So a row of a head is in one place when it is rotated, which a 4-bit pool
 // needs: its range is a reduction over the group.
+//
+// Measured: 128 us for 32768 rows of 32 query heads over 8, 64 of 128 elements rotated (806 MB: 119 us at the copy
+// rate); 44 us for 16384 rows of 8 heads into a 4-bit pool (85 MB: 13 us), which takes 230 warp instructions for
+// 256 elements, two thirds of the issue slots, and 31 us to read them back as f32 (151 MB: 22 us), whose warps wait for
+// their row's page and then its codes.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -447,7 +452,8 @@ cudaError_t launch_rows_inst(const RowsParams& p, cudaStream_t stream) {
 
 template <int D, bool BF16>
 cudaError_t launch_rows_steps(const RowsParams& p, cudaStream_t stream) {
-  // one step to a lane as long as that makes no more CTAs than the GPU holds at once
+  // One step to a lane as long as that makes no more CTAs than the GPU holds at once: rotated and appended rows of
+  // 16 heads over 8 take 3.1 us for 64 rows (4.7 with four steps), 5.5 for 608 (6.2); 1216 rows 9.7 (8.6), 8192 47.6 (38.8).
   return p.n_rows <= 152 * 2 * (256 / D) ? launch_rows_inst<D, BF16, 1>(p, stream)
                                          : launch_rows_inst<D, BF16, BF16 ? 4 : 2>(p, stream);
 }

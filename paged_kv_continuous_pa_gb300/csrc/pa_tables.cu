@@ -8,8 +8,9 @@
 // the rest as well); the rows of prompts are written by a dependent launch over all
 // SMs, four consecutive rows to a thread, found by binary search.
 //
-// What bounds it is latency: the chain of one load, two scans and a store for a decode step; the
-// 16 bytes a row for prompts (the sums take their few microseconds first).
+// What bounds it is latency: the chain of one load, two scans and a store for a decode step (4.2 us for 8
+// requests, 5.3 for 512; the launch alone takes 2 to 3), and the second launch's behind it for
+// prompts (10.4 us for 698000 rows of 512 requests, 11.5 MB, which HBM takes in 1.7).
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -19,7 +20,9 @@ namespace pa {
 
 constexpr int kTablesThreads = 1024;
 constexpr int kTablesMaxSlots = 1 << 19;  // two bits to a slot in shared memory
-constexpr int kTablesOneCtaRows = 4096;
+// Up to here one CTA writes the rows as well (1024 rows 4.5 us, with a second launch 5.3; 2048 rows 6.0 and 6.5; 4032
+// rows 8.2 and 7.6; 8192 rows 12.7 and 6.8).
+constexpr int kTablesOneCtaRows = 2048;
 constexpr int kTablesRowThreads = 256;
 constexpr int kTablesRowsPerThread = 4;
 constexpr int kTablesStaged = 4096;  // requests whose row starts a CTA copies

@@ -1,6 +1,9 @@
 """The serving operators as a server runs them: block tables grown on the GPU, projections
 rotated and appended, prompts attended to, single tokens decoded in a captured step, pages
 given back and handed out again."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -227,3 +230,31 @@ def test_plain_arguments_and_others_give_the_same(kind):
     pa.attention(s.pool, q, s.ids, rows, s.tables, again, workspace=s.ws, stream=stream)
     stream.synchronize()
     assert torch.equal(outs[0], again)
+
+
+def test_readme_serving_step():
+    """README's example of a serving step, run as it stands."""
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        block = next(b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "tables_release" in b)
+    n_rows, n_seqs, num_pages = sum(PROMPTS), len(PROMPTS), 100
+    bf16 = dict(dtype=torch.bfloat16)
+    a = dict(pa=pa, torch=torch, num_pages=num_pages, Hkv=HKV, Hq=HQ, D=D, P=PAGE, n_rows=n_rows, n_seqs=n_seqs,
+             slots=torch.arange(n_seqs, dtype=torch.int32, device="cuda"), lengths=zeros(n_seqs), new_tokens=ints(PROMPTS),
+             free_pages=torch.arange(num_pages, dtype=torch.int32, device="cuda"), free_count=ints([num_pages]),
+             block_tables=torch.full((n_seqs, BLOCKS), -1, dtype=torch.int32, device="cuda"), row_starts=zeros(n_seqs + 1),
+             page_starts=zeros(n_seqs + 1), row_seqs=zeros(n_rows), row_positions=zeros(n_rows), qkv=projections(n_rows, 2),
+             q_out=zeros(n_rows, HQ, D, **bf16), k_rows=zeros(n_rows, HKV, D, **bf16), v_rows=zeros(n_rows, HKV, D, **bf16),
+             out=zeros(n_rows, HQ, D, **bf16))
+    exec(block, a)
+    at = a["row_starts"].tolist()
+    for x, y in zip(at, at[1:]):
+        want, size, _, big = R.causal(a["q_out"][x:y], a["k_rows"][x:y], a["v_rows"][x:y], R.scale_of(D))
+        assert bool(((a["out"][x:y].double() - want).abs() <= R.causal_bound(want, size, D, y - x, big)).all())
+    # the keys that were read back lie within a step and a half of what was rotated (half a step, and the range's f16 roundings),
+    # and a rounding to bf16
+    f, m = a["rope"].frequencies()
+    want, _ = R.rotate(a["qkv"][:, HQ:HQ + HKV], a["row_positions"], f, m, D, False)
+    step = (want.amax(dim=2, keepdim=True) - want.amin(dim=2, keepdim=True)) / 15
+    assert bool(((a["k_rows"].double() - want).abs() <= 1.5 * step + want.abs() * 2.0 ** -7).all())
+    assert a["free_count"].item() == num_pages and (a["block_tables"] == -1).all()
+    assert sorted(a["free_pages"].tolist()) == list(range(num_pages))
