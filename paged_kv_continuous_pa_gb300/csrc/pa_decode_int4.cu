@@ -18,8 +18,10 @@
 // Queries are f16, a row scaled by a power of two below 2^15 (bf16 numbers are exact down to 2^-27 of the row's
 // largest); f32 queries in two parts (22 bits).  A weight w = p step is f16 relative to a running
 // reference, w = 2^(s - R) step <= 2^8, in one part for bf16 outputs (2^-11) and two for f32 ones (2^-22).  The
-// weights' sum as the products saw them comes out of a tile of ones, so that the 8 is subtracted exactly: the
-// result then holds no offset larger than itself.
+// weights' sum as the products saw them comes out of a tile of ones, so that the 8 is subtracted as it entered. The
+// products' sums are of c and larger than the results, 15 to 20 times for 53 keys, and the tensor cores truncate at 2^-23 of
+// them, which bf16 outputs do not show; for f32 rows, whose results were off by 1.5e-5 of their norm so, the codes are
+// taken as c - 8 from the start, one f16 subtraction for two, for K too (its offset is low + 8 step then).
 // (m16n8k32 on e4m3 bytes, where c is c 2^-9 as well, would need fewer operations, but ran as two f16
 // products and the conversions, 963 warp instructions for a stage.)
 //
@@ -99,12 +101,23 @@ __device__ __forceinline__ void i4_issue(const AttnParams& p, const I4Header* hd
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// Codes 2 s and 2 s + 1 (s = 0, 1) of both halves of a word: c 2^-24 and c 2^-20 as f16.
-template <int S>
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Codes 2 s and 2 s + 1 (s = 0, 1) of both halves of a word: c 2^-24 and c 2^-20 as f16; c - 8 in place of c where
+// CENTRED (exact: f16 holds both).
+template <int S, bool CENTRED>
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
   const uint32_t x = S == 0 ? w : w >> 8;
   even = x & 0x000f000fu;
   odd = x & 0x00f000f0u;
+  if constexpr (CENTRED) {
+    even = sub_f16x2(even, 0x00080008u);
+    odd = sub_f16x2(odd, 0x00800080u);
+  }
 }
 
 template <int D, bool QF32>
@@ -114,8 +127,23 @@ struct I4State {
   float dot_scale[2], low_scale[2];   // of heads 2c, 2c + 1: a score is step (sum dot_scale) + low low_scale (log2 domain)
   float r[2], l[2], fix[2];           // reference; this lane's parts of sum p and sum p (low + 8 step)
   float o[I4Geom<D>::NW][4][4];       // head elements (2 to a lane's tile) x heads 2c, 2c + 1
-  float ones[4];                      // the weights' sums
+  float ones[4];                      // the weights' sums (bf16 rows)
 };
+
+// Codes of 16 tokens times their weights into the results.  An MMA truncates each of its products to the sum that it
+// adds to; for f32 rows 16 tokens are summed apart and added with a rounding (7.9e-6 of the results' norm without, for 700 keys).
+template <bool QF32>
+__device__ __forceinline__ void i4_add(float (&o)[4], const uint32_t (&a)[4], const uint32_t (&b)[QF32 ? 2 : 1][4], int u) {
+  if constexpr (QF32) {
+    float t[4] = {};
+#pragma unroll
+    for (int part = 0; part < 2; ++part) mma_f16_16816(t, a, b[part][2 * u], b[part][2 * u + 1]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] += t[k];
+  } else {
+    mma_f16_16816(o, a, b[0][2 * u], b[0][2 * u + 1]);
+  }
+}
 
 constexpr float kI4Top = 8.0f, kI4Start = 6.0f;  // log2 of the largest weight: what it may reach, where the reference puts it
 
@@ -145,12 +173,12 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint32_t a[4];
-      codes_f16<0>(w[0][i], a[0], a[2]);
-      codes_f16<0>(w[1][i], a[1], a[3]);
+      codes_f16<0, QF32>(w[0][i], a[0], a[2]);
+      codes_f16<0, QF32>(w[1][i], a[1], a[3]);
 #pragma unroll
       for (int part = 0; part < PARTS; ++part) mma_f16_16816(s[0], a, st.q[part][2 * i][0], st.q[part][2 * i][1]);
-      codes_f16<1>(w[0][i], a[0], a[2]);
-      codes_f16<1>(w[1][i], a[1], a[3]);
+      codes_f16<1, QF32>(w[0][i], a[0], a[2]);
+      codes_f16<1, QF32>(w[1][i], a[1], a[3]);
 #pragma unroll
       for (int part = 0; part < PARTS; ++part) mma_f16_16816(s[1], a, st.q[part][2 * i + 1][0], st.q[part][2 * i + 1][1]);
     }
@@ -173,7 +201,7 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(fabsf(v[i].x) + 0x1p-24f));  // (rows of one value have step 0)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      e[i][h] = fmaf(k.x, e[i][h] * st.dot_scale[h], k.y * st.low_scale[h]);
+      e[i][h] = fmaf(k.x, e[i][h] * st.dot_scale[h], (QF32 ? fmaf(8.0f, k.x, k.y) : k.y) * st.low_scale[h]);
       if (!valid) e[i][h] = -INFINITY;
       top[h] = fmaxf(top[h], e[i][h] + lg);
     }
@@ -235,8 +263,7 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
       }
     }
     const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
-#pragma unroll
-    for (int part = 0; part < PARTS; ++part) mma_f16_16816(st.ones, one, b[part][2 * u], b[part][2 * u + 1]);
+    if constexpr (!QF32) mma_f16_16816(st.ones, one, b[0][2 * u], b[0][2 * u + 1]);
 #pragma unroll
     for (int i = 0; i < Geo::NW; ++i)
 #pragma unroll
@@ -244,14 +271,12 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
         const uint32_t z0 = __byte_perm(x[0][i], x[1][i], q == 0 ? 0x5410 : 0x7632);
         const uint32_t z1 = __byte_perm(x[2][i], x[3][i], q == 0 ? 0x5410 : 0x7632);
         uint32_t a[4];
-        codes_f16<0>(z0, a[0], a[1]);
-        codes_f16<0>(z1, a[2], a[3]);
-#pragma unroll
-        for (int part = 0; part < PARTS; ++part) mma_f16_16816(st.o[i][2 * q], a, b[part][2 * u], b[part][2 * u + 1]);
-        codes_f16<1>(z0, a[0], a[1]);
-        codes_f16<1>(z1, a[2], a[3]);
-#pragma unroll
-        for (int part = 0; part < PARTS; ++part) mma_f16_16816(st.o[i][2 * q + 1], a, b[part][2 * u], b[part][2 * u + 1]);
+        codes_f16<0, QF32>(z0, a[0], a[1]);
+        codes_f16<0, QF32>(z1, a[2], a[3]);
+        i4_add<QF32>(st.o[i][2 * q], a, b, u);
+        codes_f16<1, QF32>(z0, a[0], a[1]);
+        codes_f16<1, QF32>(z1, a[2], a[3]);
+        i4_add<QF32>(st.o[i][2 * q + 1], a, b, u);
       }
   }
 }
@@ -419,7 +444,7 @@ __global__ void __launch_bounds__(32 * kI4Warps, QF32 ? 3 : 4) decode_int4_kerne
   for (int h = 0; h < 2; ++h) {
     const int head = 2 * c + h;
     if (head >= G) continue;
-    const float offset = fmaf(-8.0f, st.ones[h], st.fix[h]);
+    const float offset = QF32 ? st.fix[h] : fmaf(-8.0f, st.ones[h], st.fix[h]);
     float* row = acc + (warp * G + head) * D + 8 * Geo::NW * g;
 #pragma unroll
     for (int i = 0; i < Geo::NW; ++i)

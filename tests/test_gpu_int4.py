@@ -356,3 +356,23 @@ def test_calls_that_do_not_take_it():
         with pytest.raises(pa.PaError) as e:
             call()
         assert e.value.status == pa.PA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("length", [8, 53, 700])
+@pytest.mark.parametrize("d", [64, 128])
+def test_f32_rows_lose_nothing_to_the_codes_offset(d, length):
+    """Norm of the error against the norm of the result.  With centred codes partial sums of scores stay below 4 (log2
+    domain, queries and values of size 1, scale 1 / sqrt(D)); their 16 or fewer truncations of 2^-23 and the weights' own
+    2^-21 make weights off by 2^-17 at most, most of it in common, which a softmax divides out; sums of weights times centred values are
+    of the result's own size.  2^-17 of the norm in all; sums over codes 0..15 are 8 sqrt(length) times as large
+    beside their result and truncated as often, 2^-16 and more at 53 keys."""
+    c = Cache4([length] * 16, hkv=4, d=d, page=32, seed=length)
+    q = queries(16, 16, d, torch.float32, seed=d)
+    out = attend(c, q, c.slots, [length - 1] * 16)
+    out = out[0] if isinstance(out, tuple) else out
+    want = torch.empty(q.shape, dtype=torch.float64, device="cuda")
+    for i, slot in enumerate(c.slots):
+        k, v = c.cached(0, slot, length)[0], c.cached(1, slot, length)[0]
+        want[i] = R.attend4(q[i], k, v, R.scale_of(d))[0]
+    err = float((out.double() - want).norm() / want.norm())
+    assert err <= 2.0 ** -17, err
