@@ -18,10 +18,11 @@
 // Queries are f16, a row scaled by a power of two below 2^15 (bf16 numbers are exact down to 2^-27 of the row's
 // largest); f32 queries in two parts (22 bits).  A weight w = p step is f16 relative to a running
 // reference, w = 2^(s - R) step <= 2^8, in one part for bf16 outputs (2^-11) and two for f32 ones (2^-22).  The
-// weights' sum as the products saw them comes out of a tile of ones, so that the 8 is subtracted as it entered. The
-// products' sums are of c and larger than the results, 15 to 20 times for 53 keys, and the tensor cores truncate at 2^-23 of
-// them, which bf16 outputs do not show; for f32 rows, whose results were off by 1.5e-5 of their norm so, the codes are
-// taken as c - 8 from the start, one f16 subtraction for two, for K too (its offset is low + 8 step then).
+// weights' sum as the products saw them comes out of a tile of ones, so that the 8 is subtracted as it entered.
+// f32 rows take c - 8 as a normal number, one operation more for two codes, for K too (its offset is low + 8 step
+// then): the tensor cores' sums were cut off at 2^-18 or so of their largest product with subnormal operands, and sums of c
+// are 15 to 20 times as large as the results of 53 keys: 1.5e-5 of the results' norm so, 5e-6 with c - 8 as a subnormal
+// number, 3e-7 now. bf16 rows' outputs are rounded at 2^-8.
 // (m16n8k32 on e4m3 bytes, where c is c 2^-9 as well, would need fewer operations, but ran as two f16
 // products and the conversions, 963 warp instructions for a stage.)
 //
@@ -107,16 +108,17 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Codes 2 s and 2 s + 1 (s = 0, 1) of both halves of a word: c 2^-24 and c 2^-20 as f16; c - 8 in place of c where
-// CENTRED (exact: f16 holds both).
+// Codes 2 s and 2 s + 1 (s = 0, 1) of both halves of a word as f16: c 2^-24 and c 2^-20, or, where CENTRED, the normal
+// numbers c - 8 and 16 (c - 8), from 1024 + c and 1024 + 16 c (all exact).
 template <int S, bool CENTRED>
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
   const uint32_t x = S == 0 ? w : w >> 8;
-  even = x & 0x000f000fu;
-  odd = x & 0x00f000f0u;
   if constexpr (CENTRED) {
-    even = sub_f16x2(even, 0x00080008u);
-    odd = sub_f16x2(odd, 0x00800080u);
+    even = sub_f16x2((x & 0x000f000fu) | 0x64006400u, 0x64086408u);
+    odd = sub_f16x2((x & 0x00f000f0u) | 0x64006400u, 0x64806480u);
+  } else {
+    even = x & 0x000f000fu;
+    odd = x & 0x00f000f0u;
   }
 }
 
@@ -130,8 +132,8 @@ struct I4State {
   float ones[4];                      // the weights' sums (bf16 rows)
 };
 
-// Codes of 16 tokens times their weights into the results.  An MMA truncates each of its products to the sum that it
-// adds to; for f32 rows 16 tokens are summed apart and added with a rounding (7.9e-6 of the results' norm without, for 700 keys).
+// Codes of 16 tokens times their weights into the results.  An MMA cuts its products off below the sum that it adds to;
+// for f32 rows 16 tokens are summed apart and added with a rounding.
 template <bool QF32>
 __device__ __forceinline__ void i4_add(float (&o)[4], const uint32_t (&a)[4], const uint32_t (&b)[QF32 ? 2 : 1][4], int u) {
   if constexpr (QF32) {
@@ -316,8 +318,8 @@ __device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& s
   const int exponent = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 127);
   const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - exponent) << 23);
   const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + exponent) << 23);
-  // codes count in 2^-24; a query with an infinity or NaN makes its scores NaN
-  const float dot = finite ? down * 0x1p24f * p.qk_scale_log2_h[0] : __uint_as_float(0x7fc00000u);
+  // codes count in 2^-24 (f32 rows: in 1); a query with an infinity or NaN makes its scores NaN
+  const float dot = finite ? down * (QF32 ? 1.0f : 0x1p24f) * p.qk_scale_log2_h[0] : __uint_as_float(0x7fc00000u);
   const float low = sum * p.qk_scale_log2_h[0];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {  // head h2 sits in lanes 4 h2 ..
@@ -326,7 +328,7 @@ __device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& s
     st.r[h] = -1e30f;  // (finite, so that differences to it are numbers)
     st.l[h] = st.fix[h] = 0.0f;
   }
-  // k-step 2 i + s: elements 2 s, 2 s + 4 and, as codes there count in 2^-20, a sixteenth of 2 s + 1, 2 s + 5
+  // k-step 2 i + s: elements 2 s, 2 s + 4 and, as codes there count 16 times as much, a sixteenth of 2 s + 1, 2 s + 5
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -449,8 +451,9 @@ __global__ void __launch_bounds__(32 * kI4Warps, QF32 ? 3 : 4) decode_int4_kerne
 #pragma unroll
     for (int i = 0; i < Geo::NW; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // elements 2j (codes in 2^-24) and 2j + 1 (2^-20) of word i
-        const float2 two = make_float2(fmaf(0x1p24f, st.o[i][j][h], offset), fmaf(0x1p20f, st.o[i][j][2 + h], offset));
+      for (int j = 0; j < 4; ++j) {  // elements 2j (codes in 2^-24, or 1) and 2j + 1 (16 times that) of word i
+        constexpr float even = QF32 ? 1.0f : 0x1p24f, odd = even * 0.0625f;
+        const float2 two = make_float2(fmaf(even, st.o[i][j][h], offset), fmaf(odd, st.o[i][j][2 + h], offset));
         *reinterpret_cast<float2*>(row + 8 * i + 2 * j) = two;
       }
     if (g == 0) {
