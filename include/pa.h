@@ -359,6 +359,10 @@ pa_status pa_prompt_attention(int32_t n_rows, int32_t n_seqs, const void *q, int
  *   row_starts, page_starts  int32 [n + 1], receive the exclusive sums of rows and of pages taken
  *   row_seqs, row_positions  int32 [max_rows], row_slots int64 [max_rows] (may be NULL); entries behind
  *                 row_starts[n] are left as they were.  All three may be NULL where max_rows is 0
+ * The calls that take the rows take all of them as real: a step of a fixed n_rows (a captured
+ * one) fills row_seqs with -1 before this call, in the step itself.  A row without a sequence stores
+ * nothing, gets zeros (pa_rope_append: its q_out stays) and records PA_ERR_OUT_OF_RANGE in that call's
+ * status word.  A request's tokens number row_starts[i + 1] - row_starts[i] from here on, not new_tokens[i].
  * Outputs overlap no input (but free_left).  The pages of a pool are handed out here or by
  * pa_pages_*, not by both; pages are not shared between slots.
  * num_seqs <= 2^19.  One launch for at most 2048 rows, else two, the second a programmatic

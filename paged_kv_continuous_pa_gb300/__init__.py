@@ -832,7 +832,8 @@ def tables_grow(seq_ids, lengths, new_tokens, free_pages, free_count, free_left,
                 row_starts, page_starts, row_seqs, row_positions, row_slots=None, status=None, stream=None):
     """Pages from the stack free_pages[:free_count] into the block tables for new_tokens
     more tokens of each request, and the rows of the step: seq ids, positions and
-    (optional, int64) token places in the pool.  All int32 on the device."""
+    (optional, int64) token places in the pool.  All int32 on the device.  Entries of rows that no
+    request gets stay as they were: fill row_seqs with -1 first where the step takes the whole array."""
     if stream is None and _bind is not None:
         st = _bind.tables_grow(seq_ids, lengths, new_tokens, free_pages, free_count, free_left, page_size, block_tables,
                                row_starts, page_starts, row_seqs, row_positions, row_slots, status)
