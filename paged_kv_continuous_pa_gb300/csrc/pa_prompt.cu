@@ -329,7 +329,7 @@ struct PromptSmem {  // byte offsets from the base, which is 1024-byte aligned (
   static constexpr int STAGES = D == 128 ? 5 : 8;  // tiles of K and V in the ring
   static constexpr int RING = 2 * TILE;            // behind the two query tiles
   static constexpr int BAR = RING + STAGES * TILE;
-  static constexpr int BYTES = BAR + 512;
+  static constexpr int BYTES = BAR + 640;
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -375,7 +375,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
     STALL = UE + 4,
     COUNT
   };
-  constexpr int UNITS = (COUNT * 8 + 32 + 15) / 16 * 16;
+  // A unit is announced when every warp knows the one four before it (UE), so a tile's warps may write the flag of unit
+  // k + 4 while one of the other tile's has yet to read that of unit k: five are in use, in a ring of eight.
+  constexpr int FLAGS = 8;
+  constexpr int UNITS = (COUNT * 8 + 4 + 4 * FLAGS + 15) / 16 * 16;  // behind the barriers, the tensor memory's address and the flags
   static_assert(UNITS + 64 <= S::BYTES - S::BAR, "barriers");
   extern __shared__ __align__(1024) unsigned char sm[];
   if ((smem_addr(sm) & 1023u) != 0) {  // (the swizzled tiles would be read at other places than they were written)
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::BAR);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + S::BAR + COUNT * 8);
-  volatile int32_t* odd_values = reinterpret_cast<volatile int32_t*>(tslot + 1);  // entry k % 4 is k + 1: values of unit k were put to 0
+  volatile int32_t* odd_values = reinterpret_cast<volatile int32_t*>(tslot + 1);  // entry k % FLAGS is k + 1: values of unit k were put to 0
   volatile int4* taken = reinterpret_cast<volatile int4*>(sm + S::BAR + UNITS);  // entry k % 4: unit k's tile and, in w, its head (-1: no unit)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
   if (tid >= 32 && tid < 32 + COUNT) {
     const int i = tid - 32;
     mbar_init(&bar[i], i >= UE && i < UE + 4 ? 18u : (i >= PF && i < PF + 4) || (i >= VOK && i < VOK + 4) ? 8u : i >= EMPTY && i < QF ? 2u : 1u);
-    if (i < 4) odd_values[i] = 0;
+    if (i < FLAGS) odd_values[i] = 0;
     fence_barrier_init();
   }
   if (tid == kPrSoftmaxThreads + 32) {
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
           found = true;
         }
       }
-      if (found) odd_values[k & 3] = k + 1;
+      if (found) odd_values[k & (FLAGS - 1)] = k + 1;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[VOK + (checked & 3)]);
@@ -774,7 +777,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) prompt_kernel(const __grid_cons
         l1 += __shfl_xor_sync(0xffffffffu, l1, d);
       }
       const int row0 = x.begin + (t == 0 ? x.pos_a : x.pos_b) + r0, row1 = row0 + 8, head = t == 0 ? x.head_a : x.head_b;
-      const bool odd = odd_values[k & 3] == k + 1;
+      const bool odd = odd_values[k & (FLAGS - 1)] == k + 1;
       const float inv0 = __fdiv_rn(1.0f, l0), inv1 = __fdiv_rn(1.0f, l1);
       uint16_t* out0 = p.out + (static_cast<int64_t>(row0) * p.Hq + head) * D;
       uint16_t* out1 = out0 + static_cast<int64_t>(8) * p.Hq * D;
