@@ -126,7 +126,9 @@ template <int D, bool QF32>
 struct I4State {
   static constexpr int PARTS = QF32 ? 2 : 1;
   uint32_t q[PARTS][D / 16][2];       // B of scores: head g
-  float dot_scale[2], low_scale[2];   // of heads 2c, 2c + 1: a score is step (sum dot_scale) + low low_scale (log2 domain)
+  // of heads 2c, 2c + 1: a score is (step sum + low q_sum) scale (log2 domain), where sum and q_sum are of the scaled
+  // query, so that nothing before the last product leaves the finite numbers
+  float q_sum[2], scale[2];
   float r[2], l[2], fix[2];           // reference; this lane's parts of sum p and sum p (low + 8 step)
   float o[I4Geom<D>::NW][4][4];       // head elements (2 to a lane's tile) x heads 2c, 2c + 1
   float ones[4];                      // the weights' sums (bf16 rows)
@@ -203,7 +205,10 @@ __device__ __forceinline__ void i4_stage(I4State<D, QF32>& st, const unsigned ch
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(fabsf(v[i].x) + 0x1p-24f));  // (rows of one value have step 0)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      e[i][h] = fmaf(k.x, e[i][h] * st.dot_scale[h], (QF32 ? fmaf(8.0f, k.x, k.y) : k.y) * st.low_scale[h]);
+      // (codes count in 2^-24, those of f32 rows in 1 and less 8)
+      const float x = QF32 ? fmaf(k.x, e[i][h], fmaf(8.0f, k.x, k.y) * st.q_sum[h])
+                           : fmaf(k.x * 0x1p24f, e[i][h], k.y * st.q_sum[h]);
+      e[i][h] = x * st.scale[h];
       if (!valid) e[i][h] = -INFINITY;
       top[h] = fmaxf(top[h], e[i][h] + lg);
     }
@@ -293,7 +298,7 @@ __device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& s
 #pragma unroll
     for (int j = 0; j < 4; ++j) st.o[i][j][0] = st.o[i][j][1] = st.o[i][j][2] = st.o[i][j][3] = 0.0f;
   st.ones[0] = st.ones[1] = st.ones[2] = st.ones[3] = 0.0f;
-  float q[D / 4], sum = 0.0f, big = 0.0f;
+  float q[D / 4], big = 0.0f;
   bool finite = true;
   const size_t base = (out_row + (g < G ? g : 0)) * D + (D / 4) * c;
 #pragma unroll
@@ -303,14 +308,12 @@ __device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& s
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       q[8 * i + j] = g < G ? x[j] : 0.0f;
-      sum += q[8 * i + j];
       big = fmaxf(big, fabsf(q[8 * i + j]));
       finite = finite && fabsf(q[8 * i + j]) < INFINITY;
     }
   }
 #pragma unroll
   for (int d = 1; d < 4; d *= 2) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, d);
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
     finite = __shfl_xor_sync(0xffffffffu, static_cast<int>(finite), d) != 0 && finite;
   }
@@ -318,13 +321,17 @@ __device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& s
   const int exponent = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 127);
   const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - exponent) << 23);
   const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + exponent) << 23);
-  // codes count in 2^-24 (f32 rows: in 1); a query with an infinity or NaN makes its scores NaN
-  const float dot = finite ? down * (QF32 ? 1.0f : 0x1p24f) * p.qk_scale_log2_h[0] : __uint_as_float(0x7fc00000u);
-  const float low = sum * p.qk_scale_log2_h[0];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < D / 4; ++i) sum = fmaf(q[i], up, sum);
+#pragma unroll
+  for (int d = 1; d < 4; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  // a query with an infinity or NaN makes its scores NaN
+  const float scale = finite ? down * p.qk_scale_log2_h[0] : __uint_as_float(0x7fc00000u);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {  // head h2 sits in lanes 4 h2 ..
-    st.dot_scale[h] = __shfl_sync(0xffffffffu, dot, 4 * (2 * c + h));
-    st.low_scale[h] = __shfl_sync(0xffffffffu, low, 4 * (2 * c + h));
+    st.q_sum[h] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c + h));
+    st.scale[h] = __shfl_sync(0xffffffffu, scale, 4 * (2 * c + h));
     st.r[h] = -1e30f;  // (finite, so that differences to it are numbers)
     st.l[h] = st.fix[h] = 0.0f;
   }
