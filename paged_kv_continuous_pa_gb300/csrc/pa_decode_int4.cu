@@ -332,7 +332,7 @@ __device__ __forceinline__ void i4_prep(const AttnParams& p, I4State<D, QF32>& s
   for (int h = 0; h < 2; ++h) {  // head h2 sits in lanes 4 h2 ..
     st.q_sum[h] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c + h));
     st.scale[h] = __shfl_sync(0xffffffffu, scale, 4 * (2 * c + h));
-    st.r[h] = -1e30f;  // (finite, so that differences to it are numbers)
+    st.r[h] = -0x1.fffffep127f;  // (below every finite score, and finite itself, so that differences to it are numbers)
     st.l[h] = st.fix[h] = 0.0f;
   }
   // k-step 2 i + s: elements 2 s, 2 s + 4 and, as codes there count 16 times as much, a sixteenth of 2 s + 1, 2 s + 5
