@@ -246,7 +246,8 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
  *                   positions, f_i for those that turn more than `high` times, and a linear ramp
  *                   over the pair index between (the indices at which a pair turns t times,
  *                   rotary_dim ln(original_positions / (2 pi t)) / (2 ln base), rounded outwards
- *                   and kept within 0 .. rotary_dim - 1); magnitude 0 stands for 0.1 ln(factor) + 1
+ *                   and kept within 0 .. rotary_dim - 1); magnitude 0 stands for 0.1 ln(factor) + 1,
+ *                   and for 1 where factor is 1 or less
  *   PA_ROPE_BANDS   the same ends, with t_i = original_positions f_i / (2 pi) turns and the weight
  *                   (t_i - low) / (high - low), clamped to 0..1, on f_i
  * Angles are exact for every int32 position: f_i / 2 pi is held as a 64-bit fraction of a turn,

@@ -585,7 +585,9 @@ pa_status pa_rope_create(const pa_rope_desc* desc, pa_rope** out) {
   pa_rope* p = new (std::nothrow) pa_rope;
   if (p == nullptr) return fail(PA_ERR_INVALID_ARG, "out of host memory");
   p->desc = d;
-  p->magnitude = d.magnitude > 0.0 ? d.magnitude : d.scaling == PA_ROPE_RAMP ? 0.1 * std::log(d.factor) + 1.0 : 1.0;
+  // (a factor of 1 or less stretches nothing: the logarithm is negative there, and the sum with it from e^-10 on)
+  const double own = d.scaling == PA_ROPE_RAMP && d.factor > 1.0 ? 0.1 * std::log(d.factor) + 1.0 : 1.0;
+  p->magnitude = d.magnitude > 0.0 ? d.magnitude : own;
   const double base = d.scaling == PA_ROPE_BASE ? d.base * std::pow(d.factor, static_cast<double>(r) / (r - 2)) : d.base;
   // PA_ROPE_RAMP: the pair index at which a pair turns t times over the original positions
   auto index_of = [&](double t) { return r * std::log(d.original_positions / (kTwoPi * t)) / (2.0 * std::log(d.base)); };
