@@ -262,7 +262,7 @@ typedef struct {
     double factor;               /* > 0 (ignored by PA_ROPE_NONE) */
     int32_t original_positions;  /* > 0 (PA_ROPE_RAMP and PA_ROPE_BANDS) */
     double low, high;            /* 0 < low < high (the same two) */
-    double magnitude;            /* 0: 1, or PA_ROPE_RAMP's; otherwise > 0 */
+    double magnitude;            /* 0: 1, or PA_ROPE_RAMP's; otherwise > 0 in binary32 */
 } pa_rope_desc;
 typedef struct pa_rope pa_rope; /* opaque host object, unchanged after its creation */
 

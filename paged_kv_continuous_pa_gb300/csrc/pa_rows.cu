@@ -23,6 +23,7 @@
 // 256 elements, two thirds of the issue slots, and 31 us to read them back as f32 (151 MB: 22 us), whose warps wait for
 // their row's page and then its codes.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <new>
 
@@ -580,8 +581,9 @@ pa_status pa_rope_create(const pa_rope_desc* desc, pa_rope** out) {
   if (ranged && (d.original_positions <= 0 || !(std::isfinite(d.high) && d.low > 0.0 && d.high > d.low)))
     return fail(PA_ERR_INVALID_ARG, "rope ranges need original_positions > 0 and 0 < low < high");
   if (d.scaling == PA_ROPE_BASE && r == 2) return fail(PA_ERR_INVALID_ARG, "a changed base needs rotary_dim > 2");
-  if (!(std::isfinite(d.magnitude) && d.magnitude >= 0.0))
-    return fail(PA_ERR_INVALID_ARG, "rope magnitude %g must not be negative", d.magnitude);
+  // (the kernels hold it in binary32)
+  if (!(d.magnitude == 0.0 || (d.magnitude > 0.0 && d.magnitude <= FLT_MAX && static_cast<float>(d.magnitude) > 0.0f)))
+    return fail(PA_ERR_INVALID_ARG, "rope magnitude %g must be 0 or a positive binary32 number", d.magnitude);
   pa_rope* p = new (std::nothrow) pa_rope;
   if (p == nullptr) return fail(PA_ERR_INVALID_ARG, "out of host memory");
   p->desc = d;

@@ -30,3 +30,16 @@ def test_ramps_that_stretch(factor):
 
 def test_a_given_magnitude_stays():
     assert ramp(1e-5, magnitude=0.25).frequencies()[1] == 0.25 and ramp(8.0, magnitude=1.0).frequencies()[1] == 1.0
+
+
+@pytest.mark.parametrize("magnitude", [1e39, 1e300, 1e-46, 5e-324])
+def test_magnitudes_beyond_fp32_are_refused(magnitude):
+    """The kernels hold it in FP32, where these are infinite or 0."""
+    with pytest.raises(pa.PaError) as e:
+        pa.Rope(64, magnitude=magnitude)
+    assert e.value.status == pa.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("magnitude", [3e38, 1e-44, 1.0])
+def test_magnitudes_of_fp32(magnitude):
+    assert pa.Rope(64, magnitude=magnitude).frequencies()[1] == magnitude
