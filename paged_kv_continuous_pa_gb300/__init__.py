@@ -6,7 +6,8 @@ ctypes.  PyTorch supplies device memory and streams.  There is no fallback:
 if the shared library is missing or a CUDA device is absent the calls raise.
 The calls of a serving step first try pa_bind, an extension module that looks at plain
 arguments and calls the library in one step; it answers None where an argument is of
-another kind, and the checks here then raise or make the call through ctypes.
+another kind, and the checks here then raise or make the call through ctypes.  It is loaded by the
+first such call; without it every call goes through ctypes, and the library needs no PyTorch.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ from typing import Optional, Sequence, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_lib", "libpa_gb300.so")
+BIND_PATH = os.path.join(HERE, "_lib", "pa_bind.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "pa.h")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_OUT_OF_RANGE, PA_ERR_TIMEOUT, PA_ERR_CUDA, PA_ERR_NO_PAGES = range(7)
@@ -28,7 +30,6 @@ ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 PA_ORDER_AUTO, PA_ORDER_CALL, PA_ORDER_LONGEST_FIRST = 0, 1, 2
 
 _lib = None
-_bind = None  # the module pa_bind, once the library is loaded
 _lock = threading.Lock()
 
 
@@ -181,26 +182,49 @@ def load(path: str = LIB_PATH):
         L.pa_kernel_launches.restype = ctypes.c_uint64
         L.pa_version.argtypes = []
         L.pa_version.restype = ctypes.c_char_p
-        _load_bind(L)
         _lib = L
         return L
 
 
-def _load_bind(L):
-    global _bind
-    import importlib.machinery
-    import importlib.util
+class _LongWay:
+    """In pa_bind's place where it cannot be loaded: no argument is of the plain kind."""
 
-    import torch  # noqa: F401  (its libraries come first)
-    path = os.path.join(HERE, "_lib", "pa_bind.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"pa_bind.so not built at {path}; run paged_kv_continuous_pa_gb300.build.build()")
-    loader = importlib.machinery.ExtensionFileLoader("pa_bind", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_bind", loader))
-    loader.exec_module(module)
-    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        L.pa_append_kv, L.pa_attention, L.pa_tables_grow, L.pa_rope_append, L.pa_prompt_attention, L.pa_read_kv)))
-    _bind = module
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+class _FirstCall:
+    """In pa_bind's place until a call comes that it takes and the library is loaded."""
+
+    def __getattr__(self, name):
+        return getattr(_load_bind() if _lib is not None else _LongWay(), name)
+
+
+_bind = _FirstCall()
+
+
+def _load_bind():
+    global _bind
+    with _lock:
+        if not isinstance(_bind, _FirstCall):
+            return _bind
+        import importlib.machinery
+        import importlib.util
+        import warnings
+
+        import torch  # noqa: F401  (its libraries come first)
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("pa_bind", BIND_PATH)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_bind", loader))
+            loader.exec_module(module)
+            module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                _lib.pa_append_kv, _lib.pa_attention, _lib.pa_tables_grow, _lib.pa_rope_append, _lib.pa_prompt_attention,
+                _lib.pa_read_kv)))
+            _bind = module
+        except ImportError as e:  # not built, or built against another torch
+            warnings.warn(f"{BIND_PATH} is not loaded: calls take the longer way through ctypes ({e})", RuntimeWarning)
+            _bind = _LongWay()
+        return _bind
 
 
 def _status(status: int):
@@ -804,7 +828,7 @@ def prompt_attention(q, k, v, row_starts, out, lse=None, softmax_scale: float = 
     [n, Hkv, D] bf16 (parts of a packed projection allowed), sequence s in rows
     row_starts[s] .. row_starts[s + 1] - 1 (int32, on the device), into out [n, Hq, D] and,
     if given, lse f32 [n, Hq]."""
-    if stream is None and _bind is not None:
+    if stream is None:
         st = _bind.prompt_attention(q, k, v, row_starts, out, lse, softmax_scale, workspace, status)
         if st is not None:
             return _status(st)
@@ -834,7 +858,7 @@ def tables_grow(seq_ids, lengths, new_tokens, free_pages, free_count, free_left,
     more tokens of each request, and the rows of the step: seq ids, positions and
     (optional, int64) token places in the pool.  All int32 on the device.  Entries of rows that no
     request gets stay as they were: fill row_seqs with -1 first where the step takes the whole array."""
-    if stream is None and _bind is not None:
+    if stream is None:
         st = _bind.tables_grow(seq_ids, lengths, new_tokens, free_pages, free_count, free_left, page_size, block_tables,
                                row_starts, page_starts, row_seqs, row_positions, row_slots, status)
         if st is not None:

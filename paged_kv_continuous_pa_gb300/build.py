@@ -3,16 +3,19 @@
 Each .cu under csrc/ compiles to an object in parallel, then one nvcc link
 produces ``_lib/libpa_gb300.so``.  Rebuilds only what changed (object newer
 than its source and every header).  Beside it ``_lib/pa_bind.so``, the binding's
-short way into the library, is compiled with g++ against the installed torch.
+short way into the library, is compiled with g++ against the installed torch; the library
+needs neither, and is built without it where there is no torch.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -101,11 +104,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
             sys.stderr.write(r.stdout + r.stderr)
         os.replace(tmp, o)
 
+    def bind_beside():
+        if variant or importlib.util.find_spec("torch") is None:
+            return
+        try:
+            build_bind(force)
+        except Exception as e:  # the calls go through ctypes without it
+            if os.path.exists(BIND_PATH):  # one of older sources
+                os.remove(BIND_PATH)
+            warnings.warn(f"pa_bind was not built: {e}", RuntimeWarning)
+
     with cf.ThreadPoolExecutor(max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
-        bind = ex.submit(build_bind, force) if not variant else None
+        bind = ex.submit(bind_beside)
         list(ex.map(compile_one, jobs))
-        if bind is not None:
-            bind.result()
+        bind.result()
     if force or jobs or _stale(lib_path, objs):
         tmp = lib_path + f".tmp{os.getpid()}"
         cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xcompiler", "-fPIC"]
