@@ -250,8 +250,9 @@ pa_status pa_step(const pa_pool *pool, int32_t n_rows, const void *q, pa_dtype q
  *                   and for 1 where factor is 1 or less
  *   PA_ROPE_BANDS   the same ends, with t_i = original_positions f_i / (2 pi) turns and the weight
  *                   (t_i - low) / (high - low), clamped to 0..1, on f_i
- * Angles are exact for every int32 position: f_i / 2 pi is held as a 64-bit fraction of a turn,
- * and p * f_i is taken modulo whole turns in integers.  Sines, cosines and products are FP32. */
+ * f_i is a binary64 number, f_i / 2 pi is held as a 64-bit fraction of a turn (off by 2^-64 of a turn
+ * for f_i up to 10^12), and p * f_i is taken modulo whole turns in integers: at any int32 position the
+ * angle is off by 2^-33 of a turn at most before it is rounded.  Sines, cosines and products are FP32. */
 typedef enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
 typedef enum { PA_ROPE_NONE = 0, PA_ROPE_LINEAR = 1, PA_ROPE_BASE = 2, PA_ROPE_RAMP = 3, PA_ROPE_BANDS = 4 } pa_rope_scaling;
 typedef struct {

@@ -5,8 +5,8 @@
 // A pair (a, b) at position p turns by the angle p f_i:
 //   (a, b) -> m (a cos - b sin, a sin + b cos)
 // The angle is taken in turns: f_i / 2 pi is a 64-bit fraction of a turn, so p f_i modulo
-// whole turns is one wrapping integer product, exact at any position (an FP32 product
-// is off by 0.06 rad at position 10^6); sincospi gets its upper 32 bits.  A row's
+// whole turns is one wrapping integer product, off by 2^-33 of a turn at any position (an
+// FP32 product is off by 0.06 rad at position 10^6); sincospi gets its upper 32 bits.  A row's
 // sines and cosines are the same for all of its heads, so a CTA computes them once
 // for its rows into shared memory.
 //
@@ -540,6 +540,17 @@ struct pa_rope {
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr double kTwoPiRest = 2.4492935982947064e-16;  // 2 pi - kTwoPi
+
+// f / 2 pi modulo whole turns, in 2^-64 of a turn.  A quotient in binary64 alone is off by 2^-54 of itself, which the
+// position multiplies (2^-22 rad at 2^31 for f of 1, 0.01 for 10^5): what it leaves of f is divided, too.
+uint64_t turns_of(double f) {
+  const double q = f / kTwoPi;
+  const double rest = (std::fma(-q, kTwoPi, f) - q * kTwoPiRest) / kTwoPi;
+  const double high = std::ldexp(std::fmod(q, 1.0), 32), whole = std::floor(high);
+  return (static_cast<uint64_t>(whole) << 32) + static_cast<uint64_t>(std::llrint(std::ldexp(high - whole, 32))) +
+         static_cast<uint64_t>(std::llrint(std::ldexp(std::fmod(rest, 1.0), 63))) * 2;  // (either sign: sums wrap)
+}
 
 // rows of `elements` elements, `stride` apart, as the kernels read them
 pa_status check_stride(const char* name, const void* base, int64_t stride, int64_t elements, pa_dtype dtype) {
@@ -611,8 +622,7 @@ pa_status pa_rope_create(const pa_rope_desc* desc, pa_rope** out) {
       return fail(PA_ERR_INVALID_ARG, "rope base %g and factor %g give no finite frequencies", d.base, d.factor);
     }
     p->frequencies[i] = g;
-    const double turn = std::fmod(g / kTwoPi, 1.0);
-    p->turns[i] = static_cast<uint64_t>(std::ldexp(turn, 63)) * 2;  // (2^64 itself would not fit)
+    p->turns[i] = turns_of(g);
   }
   *out = p;
   return PA_OK;
