@@ -323,7 +323,10 @@ pa_status pa_rope_append(const pa_pool *pool, const pa_rope *rope, int32_t n_row
  *   softmax_scale <= 0 selects 1 / sqrt(head_dim)
  *   workspace    pa_prompt_workspace_bytes(...) bytes, 256-byte aligned; scratch that each call
  *                writes before it reads it.  Calls that share one must not overlap on the GPU
- * Scores, sums and accumulators are FP32; a softmax weight enters its product with V as bf16.
+ * Scores, sums and accumulators are FP32; a softmax weight enters its product with V as bf16, off by
+ * 2^-8 of itself at most.  (The chunk tiles of pa_attention and pa_step take a weight in two parts, 2^-16:
+ * the same causal attention of a prompt is the more exact one there.  Against 64 bits the results of this
+ * call are off by 2.0e-3 of their norm, of which the output's rounding alone makes 1.6e-3.)
  * What masked keys and values hold (infinities and NaN too, other sequences' rows too) has no
  * influence.  An infinite value that a row attends to gives that element +-infinity, or NaN.
  * A row's bits depend on its own sequence alone.  One launch for few units of work (tiles of 128

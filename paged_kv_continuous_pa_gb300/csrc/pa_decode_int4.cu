@@ -22,7 +22,9 @@
 // f32 rows take c - 8 as a normal number, one operation more for two codes, for K too (its offset is low + 8 step
 // then): the tensor cores' sums were cut off at 2^-18 or so of their largest product with subnormal operands, and sums of c
 // are 15 to 20 times as large as the results of 53 keys: 1.5e-5 of the results' norm so, 5e-6 with c - 8 as a subnormal
-// number, 3e-7 now. bf16 rows' outputs are rounded at 2^-8.
+// number, 3e-7 now.  bf16 rows' outputs are rounded at 2^-8, beside which 2^-18 does not show, not in scores whose two
+// terms are large and opposite either: with queries of size 1 beside a common offset of 256 results are off by
+// what their rounding makes, to within half a percent.
 // (m16n8k32 on e4m3 bytes, where c is c 2^-9 as well, would need fewer operations, but ran as two f16
 // products and the conversions, 963 warp instructions for a stage.)
 //
